@@ -87,7 +87,9 @@ typedef struct {
   int32_t use_bias;    /* 1: select on logits + route_bias (§6.3) */
   int32_t n_shared;    /* 0 or 1 shared expert (§5) */
   int32_t d_ff_shared; /* Fs */
-  int32_t precision;   /* 0: bf16; 1: MXFP8 expert GEMM operands; 2: FP8 weights (bf16 activations); fp32 accumulation */
+  int32_t precision;   /* 0: bf16; 1: MXFP8 expert GEMM operands; 2: FP8 weights (bf16 activations);
+                          4: FP8 operands with one fp32 scale per block of 128 (3 is not assigned);
+                          fp32 accumulation */
 } moe_desc_t;
 
 /* Expert weights (all bf16, nn.Linear layout, see above).  ws1/ws3/ws2 are
@@ -486,6 +488,126 @@ MOE_API moe_status_t moe_grouped_ffn_fp8w(const moe_desc_t* d, const void* x_per
 MOE_API moe_status_t moe_backward_fp8w(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_mx_t* wq,
                                        const moe_fwd_state_t* s, const void* dy, const moe_grads_t* g, void* ws,
                                        size_t ws_bytes, void* stream);
+
+/* --------------------------------------------- FP8 blocks of 128 --
+ * FP8 x FP8 expert products with fp32 scales of fine blocks ("LLM
+ * Infrastructure Engineering 08: MoE Training Engineering" §13.6: fine-grained
+ * scaling, FP32 accumulation): E4M3 operands on the tensor cores, activations
+ * with one scale per 128 consecutive elements of a row (1 x 128), weights with
+ * one per 128 x 128 tile (moe_quantize_fp8_tile; the same codes and scales
+ * serve the forward and the data gradients).  Block scale s = amax / 448 (1
+ * where that is zero); code = E4M3 of the exact quotient x / s, rounded once to
+ * nearest even.  A NaN element has the code NaN; a block with an infinity has
+ * an infinite scale, so its row's products are NaN.  The products of each
+ * block of 128 are summed unscaled in fp32, multiplied by both scales and
+ * added in fp32 in the order of the blocks.
+ * Scales of an activation matrix [rows, cols]: fp32, block b of row r at
+ * scales[r * scale_ld + b], scale_ld = MOE_FP8_SCALE_LD(cols) in the layer's
+ * calls.  d->precision is 4 ("fp8b"). */
+#define MOE_FP8_SCALE_LD(cols) (((((cols) + 127) / 128 + 3) / 4) * 4)
+
+/* Quantise bf16 rows src [rows, cols]: codes [rows, cols] (uint8 E4M3) and
+ * scales [rows][scale_ld] (the first ceil(cols / 128) of each row are
+ * written).  cols must be a multiple of 16; the last block may be short. */
+MOE_API moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_t cols, void* codes, float* scales,
+                                           int64_t scale_ld, void* stream);
+
+/* Matrix products grouped by expert with ragged sizes on those operands:
+ *   out[r, j] = sum_i a[r, i] * B_g[j, i]   for the rows r in
+ *               [offsets[g], offsets[g+1]) of every group g,
+ * a [rows, k] codes with scales [rows][a_scale_ld]; out [rows, n] bf16.
+ * b_mn 0: b [n_groups, n, k] codes, b_scale [n_groups, ceil(n/128), ceil(k/128)]
+ * (forward); b_mn 1: b [n_groups, k, n], b_scale [n_groups, ceil(k/128),
+ * ceil(n/128)] (the data gradient through weights stored [k, n]).
+ * offsets [n_groups + 1] is read on the device and must not decrease; an entry
+ * outside [0, rows] is cut to that range and sets MOE_DEV_BAD_OFFSETS, and
+ * rows of no group are not written.  n and k must be multiples of 16;
+ * n_groups <= 1024.  ws: moe_grouped_gemm_fp8_workspace_size() bytes, status
+ * words first (moe_workspace_init before the first use; a layer workspace of
+ * at least that size serves too). */
+MOE_API moe_status_t moe_grouped_gemm_fp8_workspace_size(int64_t n_groups, int64_t rows, int64_t n, int64_t k,
+                                                         size_t* bytes);
+MOE_API moe_status_t moe_grouped_gemm_fp8(int64_t n_groups, int64_t rows, int64_t n, int64_t k, const void* a,
+                                          const float* a_scale, int64_t a_scale_ld, const int32_t* offsets,
+                                          const void* b, const float* b_scale, int32_t b_mn, void* out, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* moe_permute with the rows quantised: the same maps; codes xq_perm [R,D]
+ * and scales xs_perm [R][MOE_FP8_SCALE_LD(D)] of the permuted rows (each token
+ * row read and quantised once), optionally (non-NULL) x_perm [R,D] bf16 as
+ * moe_permute writes it (the weight gradients read it) and the token rows
+ * xq_tok [N,D], xs_tok [N][MOE_FP8_SCALE_LD(D)] for the shared expert.  Needs
+ * the forward workspace. */
+MOE_API moe_status_t moe_permute_fp8b(const moe_desc_t* d, const void* x, const int32_t* topk_idx,
+                                      const int32_t* offsets, int32_t* row_of_copy, int32_t* copy_of_row,
+                                      void* x_perm, void* xq_perm, float* xs_perm, void* xq_tok, float* xs_tok,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* moe_grouped_ffn on FP8 operands: GEMM1 from xq_perm / xs_perm and w1, w3;
+ * its epilogue computes h = silu(a1) * a3 in fp32 and quantises it per 1 x 128
+ * (kept in the workspace); GEMM2 with w2 into y_perm [R,D] bf16.  The
+ * shared expert does the same from xq_tok / xs_tok into y_shared.  wq: codes
+ * and fp32 tile scales from moe_quantize_fp8_tile.  `saved` receives bf16 a1,
+ * a3, h (a1s, a3s, hs) for the backward, or holds NULL pointers. */
+MOE_API moe_status_t moe_grouped_ffn_fp8b(const moe_desc_t* d, const void* xq_perm, const float* xs_perm,
+                                          const int32_t* offsets, const void* xq_tok, const float* xs_tok,
+                                          const moe_expert_weights_mx_t* wq, const moe_ffn_saved_t* saved,
+                                          void* y_perm, void* y_shared, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_backward of the FP8 layer: both data gradients run on FP8 operands
+ * (dYw quantised along D against w2; da1, da3 along F against w1, w3, from the
+ * bf16 tensors the layer stores); the weight gradients, which contract over
+ * the tokens, stay bf16 products with fp32 output.  Reads s->x_perm. */
+MOE_API moe_status_t moe_backward_fp8b(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_mx_t* wq,
+                                       const moe_fwd_state_t* s, const void* dy, const moe_grads_t* g, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------- the pre-norm block --
+ * What stands around the layer in a pre-norm transformer block,
+ * out = x + dropout(MoE(layernorm(x))) (no counterpart in the pages, which
+ * leave the residual path outside the layer, §6.4). */
+
+/* Layer norm over each row of x [N,D] (bf16, or fp32 with x_f32 = 1, the
+ * residual stream): y = (x - mean) * rstd * gamma + beta, bf16 [N,D];
+ * mean, rstd [N] fp32 (nullable), rstd = 1 / sqrt(var + eps) with the biased
+ * variance, summed in fp32 about the mean.  gamma, beta [D] fp32, beta
+ * nullable (zero).  eps > 0.  D <= 32768 (MOE_ERR_UNSUPPORTED above). */
+MOE_API moe_status_t moe_layernorm(const moe_desc_t* d, const void* x, int32_t x_f32, const float* gamma,
+                                   const float* beta, double eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Its backward for dy [N,D] (bf16): with g = dy * gamma, xhat = (x - mean) * rstd,
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dres  (type of x),
+ *   dgamma = sum_t dy * xhat, dbeta = sum_t dy  (fp32 [D], overwritten).
+ * dres (nullable, type of x) is the gradient that reaches x past the norm (the
+ * residual path's).  dbeta is nullable.  Sums have a fixed order: the same
+ * inputs give the same bits.  Needs the backward workspace. */
+MOE_API moe_status_t moe_layernorm_backward(const moe_desc_t* d, const void* dy, const void* x, int32_t x_f32,
+                                            const float* gamma, const float* mean, const float* rstd,
+                                            const void* dres, void* dx, float* dgamma, float* dbeta, void* ws,
+                                            size_t ws_bytes, void* stream);
+
+/* moe_combine with dropout and the residual sum:
+ *   out = resid + keep / (1 - p) * (sum_k topk_w y_perm[row_of_copy] + y_shared),
+ * fp32 throughout, stored in the residual's type (bf16, or fp32 with
+ * resid_f32 = 1); resid is nullable (zero).  0 <= p < 1.  Which elements are
+ * kept is a function of rng [2] (int64 on the device: seed, offset) and the
+ * position alone, so no mask is stored: element i = t * D + c is kept when
+ * word i % 4 of Philox-4x32 (ten rounds, Salmon et al. 2011) with key `seed`
+ * and counter offset + i / 4 (both as unsigned 64-bit numbers, the upper half
+ * of the counter zero) is at least round(p * 2^32).  A call uses
+ * ceil(N * D / 4) counters: the next call's offset must be at least that much
+ * further.  rng is read when the kernel runs, so a captured graph draws anew
+ * after the program has moved the offset.  Dropped copies (row -1) as in
+ * moe_combine. */
+MOE_API moe_status_t moe_combine_dropout(const moe_desc_t* d, const void* y_perm, const int32_t* row_of_copy,
+                                         const float* topk_w, const void* y_shared, const void* resid,
+                                         int32_t resid_f32, const int64_t* rng, double p, void* out, void* stream);
+
+/* Its backward towards the layer: dy = bf16(keep / (1 - p) * dout) for dout
+ * [N,D] (bf16, or fp32 with dout_f32 = 1) and the rng values of the forward;
+ * dy is moe_backward's upstream gradient.  The residual's gradient is dout. */
+MOE_API moe_status_t moe_dropout_backward(const moe_desc_t* d, const void* dout, int32_t dout_f32,
+                                          const int64_t* rng, double p, void* dy, void* stream);
 
 /* moe_permute without a workspace (no counterpart in the pages; an addition
  * of this library for callers that cannot allocate).  Same inputs, outputs

@@ -9,3 +9,4 @@ package.
 """
 from .moe_oracle import *  # noqa: F401,F403
 from .mxfp8 import *  # noqa: F401,F403
+from .fp8_block import *  # noqa: F401,F403

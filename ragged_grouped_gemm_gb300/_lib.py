@@ -94,6 +94,25 @@ SIGNATURES = {
     "moe_backward_mxfp8": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, ctypes.POINTER(MoeExpertWeightsMx),
                                    ctypes.POINTER(MoeFwdState), c_vp, ctypes.POINTER(MoeGrads), c_vp,
                                    ctypes.c_size_t, c_vp]),
+    "moe_quantize_fp8_rows": (c_i32, [c_vp, ctypes.c_int64, ctypes.c_int64, c_vp, c_vp, ctypes.c_int64, c_vp]),
+    "moe_grouped_gemm_fp8_workspace_size": (c_i32, [ctypes.c_int64] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_grouped_gemm_fp8": (c_i32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, c_vp, c_vp,
+                                     ctypes.c_int64, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_permute_fp8b": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                 c_vp, ctypes.c_size_t, c_vp]),
+    "moe_grouped_ffn_fp8b": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     ctypes.POINTER(MoeExpertWeightsMx), ctypes.POINTER(MoeFfnSaved), c_vp, c_vp,
+                                     c_vp, ctypes.c_size_t, c_vp]),
+    "moe_backward_fp8b": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, ctypes.POINTER(MoeExpertWeightsMx),
+                                  ctypes.POINTER(MoeFwdState), c_vp, ctypes.POINTER(MoeGrads), c_vp,
+                                  ctypes.c_size_t, c_vp]),
+    "moe_layernorm": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_i32, c_vp, c_vp, ctypes.c_double, c_vp, c_vp, c_vp,
+                              c_vp]),
+    "moe_layernorm_backward": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                       c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_combine_dropout": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                    ctypes.c_double, c_vp, c_vp]),
+    "moe_dropout_backward": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_i32, c_vp, ctypes.c_double, c_vp, c_vp]),
     "moe_timing_enable": (c_i32, [c_i32]),
     "moe_timing_read": (c_i32, [c_i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(ctypes.c_int64)]),

@@ -56,7 +56,7 @@ def make_desc(cfg: MoEConfig) -> _lib.MoeDesc:
     return _lib.MoeDesc(cfg.n_tok, cfg.d_model, cfg.d_ff, cfg.n_exp, cfg.top_k,
                         1 if cfg.gate == "sigmoid" else 0, 1 if cfg.use_bias else 0,
                         cfg.n_shared, cfg.d_ff_shared if cfg.n_shared else 0,
-                        {"bf16": 0, "mxfp8": 1, "fp8w": 2}[cfg.precision])
+                        {"bf16": 0, "mxfp8": 1, "fp8w": 2, "fp8b": 4}[cfg.precision])
 
 
 # --------------------------------------------------------------- entry points
@@ -459,6 +459,147 @@ def moe_grouped_ffn_mxfp8(desc, xq_perm, xs_perm, offsets, xq_tok, xs_tok, wq: d
         _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
 
 
+# --------------------------------------------------- FP8 with blocks of 128
+def fp8_scale_ld(cols: int) -> int:
+    """Floats per row of an activation's 1 x 128 block scales (MOE_FP8_SCALE_LD)."""
+    return ((cols + 127) // 128 + 3) // 4 * 4
+
+
+def moe_quantize_fp8_rows(src, codes, scales, stream=None):
+    """src bf16 [rows, cols] -> codes uint8 [rows, cols], scales fp32 [rows, ld]
+    (one per 128 columns; ld >= ceil(cols / 128), see :func:`fp8_scale_ld`)."""
+    rows, cols = src.shape
+    _check("moe_quantize_fp8_rows", _lib.load().moe_quantize_fp8_rows(
+        _p(src, BF16, name="src"), rows, cols, _p(codes, U8, (rows, cols), "codes"),
+        _p(scales, F32, (rows, scales.shape[-1]), "scales"), scales.shape[-1], _s(stream)))
+
+
+def moe_grouped_gemm_fp8_workspace_size(n_groups: int, rows: int, n: int, k: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_grouped_gemm_fp8_workspace_size", _lib.load().moe_grouped_gemm_fp8_workspace_size(
+        n_groups, rows, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def moe_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, out, ws, b_mn: bool = False, stream=None):
+    """out[r] = a[r] B_g^T for the rows of every group: a [rows, k] codes with
+    a_scale [rows, ld]; b [G, n, k] codes (``b_mn``: [G, k, n]) with one scale
+    per 128 x 128 tile; out bf16 [rows, n]."""
+    if b.dim() != 3:
+        raise ValueError(f"b must have three dimensions, got {tuple(b.shape)}")
+    rows, k = a.shape
+    g, n = b.shape[0], b.shape[2] if b_mn else b.shape[1]
+    tiles = (g,) + tuple((v + 127) // 128 for v in b.shape[1:])
+    _check("moe_grouped_gemm_fp8", _lib.load().moe_grouped_gemm_fp8(
+        g, rows, n, k, _p(a, U8, name="a"), _p(a_scale, F32, (rows, a_scale.shape[-1]), "a_scale"),
+        a_scale.shape[-1], _p(offsets, I32, (g + 1,), "offsets"), _p(b, U8, (g, k, n) if b_mn else (g, n, k), "b"),
+        _p(b_scale, F32, tiles, "b_scale"), 1 if b_mn else 0, _p(out, BF16, (rows, n), "out"), _p(ws, name="ws"),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_permute_fp8b(desc, x, topk_idx, offsets, row_of_copy, copy_of_row, x_perm, xq_perm, xs_perm, xq_tok, xs_tok,
+                     ws, stream=None):
+    """``x_perm`` (bf16 rows) and ``xq_tok``, ``xs_tok`` (token rows) may be None."""
+    n, d, e, k = desc.n_tok, desc.d_model, desc.n_exp, desc.top_k
+    r, ld = n * k, fp8_scale_ld(desc.d_model)
+    _check("moe_permute_fp8b", _lib.load().moe_permute_fp8b(
+        ctypes.byref(desc), _p(x, BF16, (n, d), "x"), _p(topk_idx, I32, (n, k), "topk_idx"),
+        _p(offsets, I32, (e + 1,), "offsets"), _p(row_of_copy, I32, (r,), "row_of_copy"),
+        _p(copy_of_row, I32, (r,), "copy_of_row"), _p(x_perm, BF16, (r, d), "x_perm"),
+        _p(xq_perm, U8, (r, d), "xq_perm"), _p(xs_perm, F32, (r, ld), "xs_perm"), _p(xq_tok, U8, (n, d), "xq_tok"),
+        _p(xs_tok, F32, (n, ld), "xs_tok"), _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def _fp8_struct(desc, wq):
+    d, f, e, fs = desc.d_model, desc.d_ff, desc.n_exp, desc.d_ff_shared
+    shapes = {"w1": (e, f, d), "w3": (e, f, d), "w2": (e, d, f)}
+    if desc.n_shared:
+        shapes.update(ws1=(fs, d), ws3=(fs, d), ws2=(d, fs))
+    ptr = []
+    for key in ("w1", "w3", "w2", "ws1", "ws3", "ws2"):
+        shape = shapes.get(key)
+        if shape is None:
+            ptr += [None, None]
+            continue
+        tiles = shape[:-2] + tuple((v + 127) // 128 for v in shape[-2:])
+        ptr += [_p(wq[key], U8, shape, key), _p(wq[key + "_scale"], F32, tiles, key + "_scale")]
+    return _lib.MoeExpertWeightsMx(*ptr)
+
+
+def moe_grouped_ffn_fp8b(desc, xq_perm, xs_perm, offsets, xq_tok, xs_tok, wq: dict, saved: dict, y_perm, y_shared,
+                         ws, stream=None):
+    """``wq``: output of :func:`quantize_weights_fp8_tile`; ``saved``: optional
+    bf16 a1, a3, h, a1s, a3s, hs for the backward (missing keys = not saved)."""
+    n, d, f, e, k = desc.n_tok, desc.d_model, desc.d_ff, desc.n_exp, desc.top_k
+    r, fs, sh, ld = n * k, desc.d_ff_shared, desc.n_shared, fp8_scale_ld(desc.d_model)
+    w = _fp8_struct(desc, wq)
+    sv = _lib.MoeFfnSaved(*[_p(saved.get(key), BF16, (n, fs) if key.endswith("s") else (r, f), key)
+                            for key in ("a1", "a3", "h", "a1s", "a3s", "hs")])
+    _check("moe_grouped_ffn_fp8b", _lib.load().moe_grouped_ffn_fp8b(
+        ctypes.byref(desc), _p(xq_perm, U8, (r, d), "xq_perm"), _p(xs_perm, F32, (r, ld), "xs_perm"),
+        _p(offsets, I32, (e + 1,), "offsets"), _p(xq_tok, U8, (n, d), "xq_tok") if sh else None,
+        _p(xs_tok, F32, (n, ld), "xs_tok") if sh else None, ctypes.byref(w), ctypes.byref(sv),
+        _p(y_perm, BF16, (r, d), "y_perm"), _p(y_shared, BF16, (n, d), "y_shared") if sh else None,
+        _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_backward_fp8b(desc, w_gate, wq: dict, state: dict, dy, grads: dict, ws, stream=None):
+    n, d, e = desc.n_tok, desc.d_model, desc.n_exp
+    w = _fp8_struct(desc, wq)
+    st, gr = _bwd_structs(desc, state, grads)
+    _check("moe_backward_fp8b", _lib.load().moe_backward_fp8b(
+        ctypes.byref(desc), _p(w_gate, BF16, (e, d), "w_gate"), ctypes.byref(w), ctypes.byref(st),
+        _p(dy, BF16, (n, d), "dy"), ctypes.byref(gr), _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+# --------------------------------------------------------- the pre-norm block
+def _stream_type(t, name: str) -> int:
+    """0 for a bf16 residual stream, 1 for an fp32 one."""
+    if t.dtype not in (BF16, F32):
+        raise ValueError(f"{name} must be {BF16} or {F32}, got {t.dtype}")
+    return int(t.dtype == F32)
+
+
+def moe_layernorm(desc, x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """x [N, D] bf16 or fp32 -> y bf16; gamma, beta fp32 [D] (beta may be None);
+    mean, rstd fp32 [N] for the backward (None in inference)."""
+    n, d = desc.n_tok, desc.d_model
+    _check("moe_layernorm", _lib.load().moe_layernorm(
+        ctypes.byref(desc), _p(x, None, (n, d), "x"), _stream_type(x, "x"), _p(gamma, F32, (d,), "gamma"),
+        _p(beta, F32, (d,), "beta"), float(eps), _p(y, BF16, (n, d), "y"), _p(mean, F32, (n,), "mean"),
+        _p(rstd, F32, (n,), "rstd"), _s(stream)))
+
+
+def moe_layernorm_backward(desc, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    """``dres`` (None: zero) is the gradient that reaches x past the norm and is
+    added to dx; both have x's type.  ``dbeta`` may be None."""
+    n, d = desc.n_tok, desc.d_model
+    _check("moe_layernorm_backward", _lib.load().moe_layernorm_backward(
+        ctypes.byref(desc), _p(dy, BF16, (n, d), "dy"), _p(x, None, (n, d), "x"), _stream_type(x, "x"),
+        _p(gamma, F32, (d,), "gamma"), _p(mean, F32, (n,), "mean"), _p(rstd, F32, (n,), "rstd"),
+        _p(dres, x.dtype, (n, d), "dres"), _p(dx, x.dtype, (n, d), "dx"), _p(dgamma, F32, (d,), "dgamma"),
+        _p(dbeta, F32, (d,), "dbeta"), _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_combine_dropout(desc, y_perm, row_of_copy, topk_w, y_shared, resid, rng, p: float, out, stream=None):
+    """moe_combine, dropout and the residual sum; ``resid`` (None: zero) and
+    ``out`` bf16 or fp32; ``rng``: int64 device tensor [2] = seed, offset."""
+    n, d, k = desc.n_tok, desc.d_model, desc.top_k
+    _check("moe_combine_dropout", _lib.load().moe_combine_dropout(
+        ctypes.byref(desc), _p(y_perm, BF16, (n * k, d), "y_perm"), _p(row_of_copy, I32, (n * k,), "row_of_copy"),
+        _p(topk_w, F32, (n, k), "topk_w"), _p(y_shared, BF16, (n, d), "y_shared"),
+        _p(resid, out.dtype, (n, d), "resid"), _stream_type(out, "out"), _p(rng, torch.int64, (2,), "rng"), float(p),
+        _p(out, None, (n, d), "out"), _s(stream)))
+
+
+def moe_dropout_backward(desc, dout, rng, p: float, dy, stream=None):
+    """dy (bf16) = mask / (1 - p) * dout with the mask of moe_combine_dropout for the same ``rng``."""
+    n, d = desc.n_tok, desc.d_model
+    _check("moe_dropout_backward", _lib.load().moe_dropout_backward(
+        ctypes.byref(desc), _p(dout, None, (n, d), "dout"), _stream_type(dout, "dout"),
+        _p(rng, torch.int64, (2,), "rng"), float(p), _p(dy, BF16, (n, d), "dy"), _s(stream)))
+
+
 # --------------------------------------------------------------- layer runner
 class MoELayer:
     """Buffers of one layer plus the forward / backward call sequences.
@@ -492,10 +633,11 @@ class MoELayer:
         else:
             self.buf.update(hs=None, y_shared=None, a1s=None, a3s=None)
         self.w8 = cfg.precision == "fp8w"
-        self.w8q = quantize_weights_fp8_tile(params) if self.w8 else None
+        self.f8 = cfg.precision == "fp8b"
+        self.w8q = quantize_weights_fp8_tile(params) if self.w8 or self.f8 else None
         self.cap = cfg.capacity_factor > 0
         if self.cap:
-            if cfg.precision == "mxfp8":
+            if cfg.precision in ("mxfp8", "fp8b"):
                 raise ValueError("the capacity-factor mode runs with bf16 operands")
             # routing writes the dropless offsets here; b["offsets"] holds the kept ones
             self.buf.update(offsets_full=z(e + 1, dt=I32), row_of_copy_full=z(r, dt=I32),
@@ -503,7 +645,15 @@ class MoELayer:
         self.mx = cfg.precision == "mxfp8"
         # E <= 32, bf16 rows, dropless, permuted copy: routing and dispatch in
         # one launch (moe_route_permute); fused_dispatch=False keeps two calls
-        self.fused_dispatch = (fused_dispatch and e <= 32 and not self.mx and not self.cap and not self.gather)
+        self.fused_dispatch = (fused_dispatch and e <= 32 and not self.mx and not self.f8 and not self.cap
+                               and not self.gather)
+        if self.f8:
+            if not train:   # the weight gradients alone read the bf16 rows
+                self.buf.update(x_perm=None, h=None, hs=None)
+            ld = fp8_scale_ld(d)
+            sh = cfg.n_shared
+            self.buf.update(xq_perm=z(r, d, dt=U8), xs_perm=z(r, ld, dt=F32), xq_tok=z(n, d, dt=U8) if sh else None,
+                            xs_tok=z(n, ld, dt=F32) if sh else None)
         if self.mx:
             self.wq = quantize_weights_mxfp8(params)
             self.wqt = quantize_weights_mxfp8_t(params) if train else None
@@ -524,6 +674,14 @@ class MoELayer:
         self.x = None
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
+        b = self.buf
+        self.experts(x, stream)
+        moe_combine(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], b["out"], stream)
+        return b["out"]
+
+    def experts(self, x: torch.Tensor, stream=None):
+        """Everything of the forward but the combine: ``buf`` then holds y_perm,
+        row_of_copy, topk_w and y_shared."""
         b, p = self.buf, self.p
         self.x = x
         if self.fused_dispatch:
@@ -531,11 +689,13 @@ class MoELayer:
             moe_route_permute(self.desc, x, p["w_gate"], p.get("bias"), b["logits"], b["topk_idx"], b["topk_w"],
                               b["counts"], b["offsets"], b["row_of_copy"], b["copy_of_row"], b["x_perm"], self.ws,
                               stream)
-            return self._ffn_combine(x, stream)
+            return self._ffn(x, stream)
         moe_route(self.desc, x, p["w_gate"], p.get("bias"), b["logits"], b["topk_idx"], b["topk_w"], b["counts"],
                   b["offsets_full"] if self.cap else b["offsets"], self.ws, stream)
         if self.mx:
             return self._forward_mx(x, stream)
+        if self.f8:
+            return self._forward_fp8b(x, stream)
         if self.gather:
             b = self.buf
             moe_permute_maps(self.desc, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"], self.ws,
@@ -543,10 +703,9 @@ class MoELayer:
             moe_grouped_ffn_gather(self.desc, x, b["copy_of_row"], b["offsets"], p["w1"], p["w3"], p["w2"],
                                    p.get("ws1"), p.get("ws3"), p.get("ws2"), None, None, b["h"], None, None,
                                    b["hs"], b["y_perm"], b["y_shared"], self.ws, stream)
-            moe_combine(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], b["out"], stream)
-            return b["out"]
+            return
         self._permute(x, stream)
-        return self._ffn_combine(x, stream)
+        self._ffn(x, stream)
 
     def _permute(self, x, stream=None):
         b = self.buf
@@ -558,7 +717,7 @@ class MoELayer:
             moe_permute(self.desc, x, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"], b["x_perm"],
                         self.ws, stream)
 
-    def _ffn_combine(self, x, stream=None):
+    def _ffn(self, x, stream=None):
         b, p = self.buf, self.p
         if self.w8:
             saved = {key: b[key] for key in ("a1", "a3", "h", "a1s", "a3s", "hs") if b.get(key) is not None}
@@ -568,8 +727,6 @@ class MoELayer:
             moe_grouped_ffn(self.desc, b["x_perm"], b["offsets"], x, p["w1"], p["w3"], p["w2"], p.get("ws1"),
                             p.get("ws3"), p.get("ws2"), b["a1"], b["a3"], b["h"], b["a1s"], b["a3s"], b["hs"],
                             b["y_perm"], b["y_shared"], self.ws, stream)
-        moe_combine(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], b["out"], stream)
-        return b["out"]
 
     def _forward_mx(self, x, stream=None):
         b = self.buf
@@ -579,8 +736,15 @@ class MoELayer:
                  if self.train else {})
         moe_grouped_ffn_mxfp8(self.desc, b["xq_perm"], b["xs_perm"], b["offsets"], b["xq_tok"], b["xs_tok"], self.wq,
                               saved, b["y_perm"], b["y_shared"], self.ws, stream)
-        moe_combine(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], b["out"], stream)
-        return b["out"]
+
+    def _forward_fp8b(self, x, stream=None):
+        b = self.buf
+        moe_permute_fp8b(self.desc, x, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"], b["x_perm"],
+                         b["xq_perm"], b["xs_perm"], b["xq_tok"], b["xs_tok"], self.ws, stream)
+        saved = ({key: b[key] for key in ("a1", "a3", "h", "a1s", "a3s", "hs") if b.get(key) is not None}
+                 if self.train else {})
+        moe_grouped_ffn_fp8b(self.desc, b["xq_perm"], b["xs_perm"], b["offsets"], b["xq_tok"], b["xs_tok"], self.w8q,
+                             saved, b["y_perm"], b["y_shared"], self.ws, stream)
 
     def backward(self, dy: torch.Tensor, stream=None) -> dict:
         b = self.buf
@@ -595,7 +759,9 @@ class MoELayer:
         state["x"] = self.x
         if self.cap:
             state.update(offsets_full=b["offsets_full"], copy_of_row_full=b["copy_of_row_full"])
-        if self.w8:
+        if self.f8:
+            moe_backward_fp8b(self.desc, self.p["w_gate"], self.w8q, state, dy, self.grads, self.ws, stream)
+        elif self.w8:
             moe_backward_fp8w(self.desc, self.p["w_gate"], self.w8q, state, dy, self.grads, self.ws, stream)
         else:
             moe_backward(self.desc, self.p["w_gate"], self.p, state, dy, self.grads, self.ws, stream)
@@ -612,3 +778,60 @@ class MoELayer:
 
     def device_status(self) -> tuple[int, int]:
         return moe_get_device_status(self.ws)
+
+
+class MoEBlock:
+    """A pre-norm block around one layer: out = x + dropout(MoE(layernorm(x))).
+
+    ``gamma``, ``beta``: fp32 [D] (beta may be None).  The residual stream x is
+    bf16 or fp32 (``stream_dtype``).  ``rng`` (seed, offset) lives on the
+    device; every training forward that drops moves the offset past the counters it used, as an
+    ordinary tensor operation on the same stream, so a captured step draws anew
+    at each replay.  ``backward`` uses the offset of the last forward.
+    """
+
+    def __init__(self, cfg: MoEConfig, params: dict, gamma, beta=None, p: float = 0.0, seed: int = 0,
+                 eps: float = 1e-5, train: bool = True, stream_dtype=BF16, device="cuda"):
+        if not 0.0 <= p < 1.0:
+            raise ValueError(f"p must be in [0, 1), got {p}")
+        self.layer = MoELayer(cfg, params, train=train, device=device)
+        self.desc, self.train, self.p, self.eps = self.layer.desc, train, float(p), float(eps)
+        self.gamma, self.beta = gamma, beta
+        n, d = cfg.n_tok, cfg.d_model
+        z = lambda *s, dt=BF16: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        self.normed, self.out = z(n, d), z(n, d, dt=stream_dtype)
+        self.rng = torch.tensor([seed, 0], dtype=torch.int64, device=device)
+        self.used = torch.zeros(2, dtype=torch.int64, device=device)
+        self.step = torch.tensor([0, (n * d + 3) // 4], dtype=torch.int64, device=device)
+        self.mean = self.rstd = self.grads = None
+        if train:
+            self.mean, self.rstd, self.dmoe = z(n, dt=F32), z(n, dt=F32), z(n, d)
+            self.grads = {"dx": z(n, d, dt=stream_dtype), "dgamma": z(d, dt=F32),
+                          "dbeta": z(d, dt=F32) if beta is not None else None}
+        self.x = None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        b = self.layer.buf
+        p = self.p if self.train else 0.0
+        self.x = x
+        moe_layernorm(self.desc, x, self.gamma, self.beta, self.normed, self.mean, self.rstd, self.eps)
+        self.layer.experts(self.normed)
+        if p > 0.0:
+            self.used.copy_(self.rng)
+            self.rng.add_(self.step)
+        moe_combine_dropout(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], x, self.used, p,
+                            self.out)
+        return self.out
+
+    def backward(self, dout: torch.Tensor) -> dict:
+        """``dout`` of the residual stream's type; returns dx, dgamma, dbeta and,
+        under "layer", the gradients of :meth:`MoELayer.backward`."""
+        g = self.grads
+        moe_dropout_backward(self.desc, dout, self.used, self.p, self.dmoe)
+        inner = self.layer.backward(self.dmoe)
+        moe_layernorm_backward(self.desc, inner["dx"], self.x, self.gamma, self.mean, self.rstd, dout, g["dx"],
+                               g["dgamma"], g["dbeta"], self.layer.ws)
+        return {**g, "layer": inner}
+
+    def device_status(self) -> tuple[int, int]:
+        return self.layer.device_status()

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 SOURCES = ["grouped_gemm.cu", "moe_kernels.cu", "moe_api.cu", "mxfp8.cu", "permute_noalloc.cu", "balance.cu",
-           "timing.cu", "selftest.cu"]
+           "timing.cu", "selftest.cu", "fp8_block.cu", "block.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

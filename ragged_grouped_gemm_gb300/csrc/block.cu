@@ -1,0 +1,459 @@
+// Layer norm (forward, backward with the reduction of the weight gradients)
+// and the residual dropout of a pre-norm MoE block.
+#include "block.cuh"
+#include "grouped_gemm.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Eight consecutive elements of a bf16 or fp32 row, kept packed as loaded.
+template <bool F32>
+struct Vec8;
+template <>
+struct Vec8<false> {
+  uint4 a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) { a = __ldg(static_cast<const uint4*>(p) + i); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t w = (j >> 1) == 0 ? a.x : (j >> 1) == 1 ? a.y : (j >> 1) == 2 ? a.z : a.w;
+    return (j & 1) ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+  }
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float (&f)[8]) {
+    static_cast<uint4*>(p)[i] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec8<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldg(static_cast<const float4*>(p) + 2 * i);
+    b = __ldg(static_cast<const float4*>(p) + 2 * i + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float get(int j) const {
+    return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
+  }
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float (&f)[8]) {
+    static_cast<float4*>(p)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+    static_cast<float4*>(p)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// Sum over the T threads of a row.  T > 32: the whole block shares the row; s
+// holds one value per warp, and a caller alternates between two of them, so
+// that one barrier a sum is enough.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (T == 32) return v;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) t += s[w];
+  return t;
+}
+template <int T>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if (T == 32) return v;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) {
+    t.x += s[w].x;
+    t.y += s[w].y;
+  }
+  return t;
+}
+
+// T threads a row, V vectors of eight columns a thread.  The mean and then the
+// squared deviations from it are summed over the registers that hold the row,
+// so the variance loses nothing to a large mean.
+template <bool F32, int T, int V>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t rows, int d8, const void* __restrict__ x,
+                                                                      const float* __restrict__ gamma,
+                                                                      const float* __restrict__ beta, float eps,
+                                                                      void* __restrict__ y, float* __restrict__ mean,
+                                                                      float* __restrict__ rstd) {
+  __shared__ float s_red[2][T == 32 ? 1 : T / 32];
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  const int tid = threadIdx.x % T;
+  const float inv_d = 1.0f / static_cast<float>(d8 * 8);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / T; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * RPB) {
+    Vec8<F32> v[V];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) v[i].load(x, r * d8 + c);
+      else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += v[i].get(j);
+    const float mu = row_sum<T>(sum, s_red[0]) * inv_d;
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (tid + i * T < d8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = v[i].get(j) - mu;
+          sq = fmaf(e, e, sq);
+        }
+      }
+    const float rs = 1.0f / sqrtf(row_sum<T>(sq, s_red[1]) * inv_d + eps);
+    if (tid == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        Vec8<true> g, b;
+        g.load(gamma, c);
+        if (beta) b.load(beta, c);
+        else b.zero();
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf((v[i].get(j) - mu) * rs, g.get(j), b.get(j));
+        Vec8<false>::store(y, r * d8 + c, o);
+      }
+    }
+  }
+}
+
+// Blocks of the backward, each of which leaves one partial sum of dgamma and
+// dbeta: two per SM.
+constexpr int kNormBlocks = 304;
+
+template <bool F32, int T, int V>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
+    int64_t rows, int d8, const uint4* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ gamma,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ dres,
+    void* __restrict__ dx, float* __restrict__ part) {
+  __shared__ float2 s_red[2][T == 32 ? 1 : T / 32];
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  const int tid = threadIdx.x % T;
+  const float inv_d = 1.0f / static_cast<float>(d8 * 8);
+  float dg[V][8], db[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
+  int flip = 0;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / T; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * RPB, flip ^= 1) {
+    Vec8<F32> xv[V];
+    Vec8<false> dv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        xv[i].load(x, r * d8 + c);
+        dv[i].load(dy, r * d8 + c);
+      } else {
+        xv[i].zero();
+        dv[i].zero();
+      }
+    }
+    const float mu = __ldg(mean + r), rs = __ldg(rstd + r);
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        Vec8<true> g;
+        g.load(gamma, c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xh = (xv[i].get(j) - mu) * rs, e = dv[i].get(j);
+          const float ge = g.get(j) * e;
+          sum.x += ge;
+          sum.y = fmaf(ge, xh, sum.y);
+          dg[i][j] = fmaf(e, xh, dg[i][j]);
+          db[i][j] += e;
+        }
+      }
+    }
+    sum = row_sum2<T>(sum, s_red[flip]);
+    const float m1 = sum.x * inv_d, m2 = sum.y * inv_d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        Vec8<true> g;
+        g.load(gamma, c);
+        Vec8<F32> res;
+        if (dres) res.load(dres, r * d8 + c);
+        else res.zero();
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xh = (xv[i].get(j) - mu) * rs;
+          o[j] = fmaf(rs, g.get(j) * dv[i].get(j) - m1 - xh * m2, res.get(j));
+        }
+        Vec8<F32>::store(dx, r * d8 + c, o);
+      }
+    }
+  }
+  // this block's partial sums [2][d]; rows of a block are added in order
+  const int d = d8 * 8;
+  float* p = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        Vec8<true>::store(p, c, dg[i]);
+        Vec8<true>::store(p + d, c, db[i]);
+      }
+    }
+  } else {
+    __shared__ float s_part[RPB][T * V * 8];
+    const int w = threadIdx.x / T;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_part[w][(tid + i * T) * 8 + j] = which ? db[i][j] : dg[i][j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += blockDim.x) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < RPB; ++k) t += s_part[k][c];
+        p[which * d + c] = t;
+      }
+    }
+  }
+}
+
+// dgamma, dbeta = the blocks' partial sums [blocks][2][d] added: 32 columns a
+// block, eight threads a column, joined in order.
+__global__ void __launch_bounds__(256) layernorm_reduce_kernel(int blocks, int d, const float* __restrict__ part,
+                                                               float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float s[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+  const int k = threadIdx.x >> 5;
+  float t = 0.0f;
+  if (c < 2 * d)
+    for (int b = k; b < blocks; b += 8) t += __ldg(part + static_cast<int64_t>(b) * 2 * d + c);
+  s[k][threadIdx.x & 31] = t;
+  __syncthreads();
+  if (k == 0 && c < 2 * d) {
+    t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += s[j][threadIdx.x];
+    if (c < d) dgamma[c] = t;
+    else if (dbeta) dbeta[c - d] = t;
+  }
+}
+
+// Four random words of counter `ctr`: Philox-4x32 with ten rounds (J. Salmon,
+// M. Moraes, R. Dror, D. Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// 2011): each round multiplies two words by constants and mixes the high
+// halves with the others and the key, which steps by constants of its own.
+__device__ __forceinline__ uint4 random_words(uint64_t key, uint64_t ctr) {
+  uint32_t k0 = static_cast<uint32_t>(key), k1 = static_cast<uint32_t>(key >> 32);
+  uint4 c = make_uint4(static_cast<uint32_t>(ctr), static_cast<uint32_t>(ctr >> 32), 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
+    const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
+    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
+                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+// Whether elements 8 i .. 8 i + 7 are kept, one bit each.
+__device__ __forceinline__ uint32_t keep8(uint64_t key, uint64_t first, int64_t i, uint32_t threshold) {
+  const uint4 a = random_words(key, first + 2 * static_cast<uint64_t>(i));
+  const uint4 b = random_words(key, first + 2 * static_cast<uint64_t>(i) + 1);
+  return (a.x >= threshold ? 1u : 0u) | (a.y >= threshold ? 2u : 0u) | (a.z >= threshold ? 4u : 0u) |
+         (a.w >= threshold ? 8u : 0u) | (b.x >= threshold ? 16u : 0u) | (b.y >= threshold ? 32u : 0u) |
+         (b.z >= threshold ? 64u : 0u) | (b.w >= threshold ? 128u : 0u);
+}
+
+// A thread takes eight columns of a token: KB copies' loads in flight.
+template <bool F32, int KB>
+__global__ void __launch_bounds__(256) combine_dropout_kernel(
+    int64_t items, int d8, int K, const uint4* __restrict__ y_perm, const int32_t* __restrict__ row_of_copy,
+    const float* __restrict__ topk_w, const uint4* __restrict__ y_shared, const void* __restrict__ resid,
+    const int64_t* __restrict__ rng, uint32_t threshold, float scale, void* __restrict__ out) {
+  uint64_t key = 0, first = 0;
+  if (threshold) {
+    key = static_cast<uint64_t>(__ldg(rng));
+    first = static_cast<uint64_t>(__ldg(rng + 1));
+  }
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items;
+       it += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t t = it / d8;
+    const int c = static_cast<int>(it - t * d8);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Vec8<F32> res;
+    if (resid) res.load(resid, it);
+    else res.zero();
+    Vec8<false> sh;
+    if (y_shared) sh.load(y_shared, it);
+    else sh.zero();
+    for (int k0 = 0; k0 < K; k0 += KB) {
+      Vec8<false> v[KB];
+      float w[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int64_t r = k0 + j < K ? __ldg(row_of_copy + t * K + k0 + j) : -1;   // -1: a dropped copy
+        w[j] = r >= 0 ? __ldg(topk_w + t * K + k0 + j) : 0.0f;
+        if (r >= 0) v[j].load(y_perm, r * d8 + c);
+        else v[j].zero();
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[j].get(e), acc[e]);
+    }
+    const uint32_t keep = threshold ? keep8(key, first, it, threshold) : 0xFFu;
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float m = acc[e] + sh.get(e);
+      o[e] = (keep >> e) & 1u ? fmaf(scale, m, res.get(e)) : res.get(e);
+    }
+    Vec8<F32>::store(out, it, o);
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) dropout_bwd_kernel(int64_t items, const void* __restrict__ dout,
+                                                          const int64_t* __restrict__ rng, uint32_t threshold,
+                                                          float scale, void* __restrict__ dy) {
+  uint64_t key = 0, first = 0;
+  if (threshold) {
+    key = static_cast<uint64_t>(__ldg(rng));
+    first = static_cast<uint64_t>(__ldg(rng + 1));
+  }
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items;
+       it += static_cast<int64_t>(gridDim.x) * 256) {
+    Vec8<F32> v;
+    v.load(dout, it);
+    const uint32_t keep = threshold ? keep8(key, first, it, threshold) : 0xFFu;
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (keep >> e) & 1u ? scale * v.get(e) : 0.0f;
+    Vec8<false>::store(dy, it, o);
+  }
+}
+
+// Calls f(threads-per-row, vectors-per-thread) with the row shape of d.
+template <class F>
+cudaError_t with_row_shape(int d, F&& f) {
+  const int d8 = d / 8;
+  auto pick = [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    switch ((d8 + T - 1) / T) {
+      case 1: return f(t, std::integral_constant<int, 1>());
+      case 2: return f(t, std::integral_constant<int, 2>());
+      case 3: return f(t, std::integral_constant<int, 3>());
+      default: return f(t, std::integral_constant<int, 4>());
+    }
+  };
+  if (d8 <= 128) return pick(std::integral_constant<int, 32>());
+  if (d8 <= 1024) return pick(std::integral_constant<int, 256>());
+  return pick(std::integral_constant<int, 1024>());
+}
+
+}  // namespace
+
+cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, const float* gamma, const float* beta,
+                             float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
+  if (rows <= 0) return cudaSuccess;
+  if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
+  return with_row_shape(d, [&](auto t, auto v) {
+    constexpr int T = decltype(t)::value, V = decltype(v)::value;
+    constexpr int RPB = T < 256 ? 256 / T : 1;
+    const int grid = static_cast<int>(std::min<int64_t>((rows + RPB - 1) / RPB, 1 << 20));
+    if (x_f32)
+      layernorm_kernel<true, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
+    else
+      layernorm_kernel<false, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
+    return cudaGetLastError();
+  });
+}
+
+size_t layernorm_bwd_floats(int64_t rows, int d) {
+  return static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(rows, 1), kNormBlocks)) * 2 * d;
+}
+
+cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void* x, bool x_f32, const float* gamma,
+                                 const float* mean, const float* rstd, const void* dres, void* dx, float* dgamma,
+                                 float* dbeta, float* scratch, cudaStream_t st) {
+  if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
+  int grid = 0;
+  if (rows > 0) {
+    const cudaError_t e = with_row_shape(d, [&](auto t, auto v) {
+      constexpr int T = decltype(t)::value, V = decltype(v)::value;
+      constexpr int RPB = T < 256 ? 256 / T : 1;
+      grid = static_cast<int>(std::min<int64_t>((rows + RPB - 1) / RPB, kNormBlocks));
+      if (x_f32)
+        layernorm_bwd_kernel<true, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x, gamma,
+                                                                   mean, rstd, dres, dx, scratch);
+      else
+        layernorm_bwd_kernel<false, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x,
+                                                                    gamma, mean, rstd, dres, dx, scratch);
+      return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return e;
+  }
+  layernorm_reduce_kernel<<<(2 * d + 31) / 32, 256, 0, st>>>(grid, d, scratch, dgamma, dbeta);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_dropout(int n_tok, int d, int top_k, const void* y_perm, const int32_t* row_of_copy,
+                                   const float* topk_w, const void* y_shared, const void* resid, bool f32,
+                                   const int64_t* rng, uint32_t threshold, float scale, void* out, cudaStream_t st) {
+  const int64_t items = static_cast<int64_t>(n_tok) * (d / 8);
+  if (items <= 0) return cudaSuccess;
+  const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, 1 << 20));
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, st>>>(items, d / 8, top_k, static_cast<const uint4*>(y_perm), row_of_copy, topk_w,
+                               static_cast<const uint4*>(y_shared), resid, rng, threshold, scale, out);
+    return cudaGetLastError();
+  };
+  if (top_k <= 1) return f32 ? run(combine_dropout_kernel<true, 1>) : run(combine_dropout_kernel<false, 1>);
+  if (top_k <= 2) return f32 ? run(combine_dropout_kernel<true, 2>) : run(combine_dropout_kernel<false, 2>);
+  return f32 ? run(combine_dropout_kernel<true, 4>) : run(combine_dropout_kernel<false, 4>);
+}
+
+cudaError_t launch_dropout_bwd(int64_t n, const void* dout, bool f32, const int64_t* rng, uint32_t threshold,
+                               float scale, void* dy, cudaStream_t st) {
+  const int64_t items = n / 8;
+  if (items <= 0) return cudaSuccess;
+  const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, 1 << 20));
+  if (f32) dropout_bwd_kernel<true><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
+  else dropout_bwd_kernel<false><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,696 @@
+// FP8 row quantisers and the grouped GEMM on E4M3 codes with one fp32 scale
+// per 1 x 128 block of A and per 128 x 128 tile of B.
+//
+// The scales are arbitrary fp32 numbers, so the tensor cores cannot apply
+// them: each k-block of 128 gives an unscaled fp32 partial product in tensor
+// memory (four K = 32 MMAs, kind::f8f6f4), and the epilogue warps add
+// a_scale * b_scale times it to fp32 accumulators they keep in registers.
+// Partial products alternate between the buffers that the 512 columns of
+// tensor memory hold, so the MMAs of one k-block run while the previous one is
+// being added.
+#include "fp8_block.cuh"
+#include "grouped_gemm.cuh"
+#include "sm100_ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <mutex>
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------ quantisation
+// Float whose E4M3 rounding is that of the exact quotient x / s: the quotient
+// truncated to fp32 with its last bit set where it is inexact (rounding to
+// odd), so that the conversion rounds once.
+__device__ __noinline__ float fp8_exact_quotient(float x, float s) {
+  const double q = static_cast<double>(x) / static_cast<double>(s);
+  const float f = __double2float_rz(q);
+  return static_cast<double>(f) == q ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// x / s for an E4M3 conversion.  x * inv (inv = 1 / s rounded) is within 2 ulp
+// of the quotient, and an fp32 number further than that from every border
+// between two codes has the quotient's code.  Borders of normal codes have the
+// low 20 mantissa bits 0x80000; below 2^-6 (subnormal codes, borders at
+// multiples of 2^-10) the quotient is computed.
+__device__ __forceinline__ float fp8_quotient(float x, float s, float inv, bool small_scale) {
+  const float q = x * inv;
+  const uint32_t u = __float_as_uint(q) & 0x7FFFFFFFu;
+  const bool near = ((u & 0xFFFFFu) - 0x7FFF8u) <= 0x10u;
+  const bool low = u - 0x3A000000u < 0x02800000u;   // [2^-11, 2^-6)
+  return (near || low || small_scale) ? fp8_exact_quotient(x, s) : q;
+}
+
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+struct BlockScale {
+  float s, inv;
+  bool small;   // 1 / s is not a normal number: divide
+};
+__device__ __forceinline__ BlockScale block_scale(float amax) {
+  BlockScale b;
+  const float s = amax / 448.0f;
+  b.s = s > 0.0f ? s : 1.0f;
+  b.inv = 1.0f / b.s;
+  b.small = b.s < 1e-37f;
+  return b;
+}
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Sixteen elements of a 128-element block per lane, eight lanes a block: the
+// block's scale and this lane's sixteen codes.
+__device__ __forceinline__ uint4 quant16(const uint4 v0, const uint4 v1, float& scale) {
+  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(lo16(w[i])), fabsf(hi16(w[i]))));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const BlockScale b = block_scale(m);
+  scale = b.s;
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = fp8_pack4(fp8_quotient(lo16(w[2 * i]), b.s, b.inv, b.small),
+                     fp8_quotient(hi16(w[2 * i]), b.s, b.inv, b.small),
+                     fp8_quotient(lo16(w[2 * i + 1]), b.s, b.inv, b.small),
+                     fp8_quotient(hi16(w[2 * i + 1]), b.s, b.inv, b.small));
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// A warp takes four blocks of a row at a time.
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint4* __restrict__ src, int64_t rows, int c16,
+                                                             uint4* __restrict__ codes, float* __restrict__ scales,
+                                                             int64_t ld) {
+  const int lane = threadIdx.x & 31;
+  const int segs = (c16 + 31) / 32;
+  const int64_t items = rows * segs;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += stride) {
+    const int64_t r = it / segs;
+    const int c = static_cast<int>(it - r * segs) * 32 + lane;
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (c < c16) {
+      v0 = __ldg(src + (r * c16 + c) * 2);
+      v1 = __ldg(src + (r * c16 + c) * 2 + 1);
+    }
+    float s;
+    const uint4 q = quant16(v0, v1, s);
+    if (c < c16) {
+      codes[r * c16 + c] = q;
+      if ((lane & 7) == 0) scales[r * ld + (c >> 3)] = s;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __restrict__ x, int n_tok, int c16,
+                                                                int top_k, const int32_t* __restrict__ row_of_copy,
+                                                                uint4* __restrict__ codes, float* __restrict__ scales,
+                                                                int64_t ld, uint4* __restrict__ tok_codes,
+                                                                float* __restrict__ tok_scales) {
+  const int lane = threadIdx.x & 31;
+  const int segs = (c16 + 31) / 32;
+  const int64_t items = static_cast<int64_t>(n_tok) * segs;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += stride) {
+    const int64_t t = it / segs;
+    const int c = static_cast<int>(it - t * segs) * 32 + lane;
+    const int my_row = lane < top_k ? __ldg(row_of_copy + t * top_k + lane) : -1;
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (c < c16) {
+      v0 = __ldg(x + (t * c16 + c) * 2);
+      v1 = __ldg(x + (t * c16 + c) * 2 + 1);
+    }
+    float s;
+    const uint4 q = quant16(v0, v1, s);
+    for (int k = 0; k < top_k; ++k) {
+      const int64_t r = __shfl_sync(0xffffffffu, my_row, k);
+      if (r >= 0 && c < c16) {
+        codes[r * c16 + c] = q;
+        if ((lane & 7) == 0) scales[r * ld + (c >> 3)] = s;
+      }
+    }
+    if (tok_codes && c < c16) {
+      tok_codes[t * c16 + c] = q;
+      if ((lane & 7) == 0) tok_scales[t * ld + (c >> 3)] = s;
+    }
+  }
+}
+
+// -------------------------------------------------------------------- GEMM
+constexpr int BM = 128;
+constexpr int BK = 128;              // contraction elements (bytes) of a k-block
+constexpr int kAuxThreads = 128;     // producer, MMA issuer, two idle warps
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = kAuxThreads + kEpiWarps * 32;
+// A block launches with 384 x 168 = 64512 registers; the split hands 112 of
+// them a thread from the first warpgroup to the two that accumulate:
+// 128 x 56 + 256 x 224 = 64512.
+constexpr int kAuxRegs = 56, kEpiRegs = 224;
+constexpr int kMaxGroups = 1024;
+constexpr int kTileBytes = BM * BK;  // 128 rows of A or 128 columns of B of a stage
+
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool b_mn) {
+  // D format fp32 (bits 4-5 = 1), A and B E4M3 (7-9, 10-12 = 0), B major (16), N >> 3 (17-22), M >> 4 (24-28)
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+struct Fp8Params {
+  CUtensorMap tmA[2];
+  CUtensorMap tmB[2];
+  const float* a_scale[2];
+  const float* b_scale[2];
+  int64_t a_scale_ld;
+  const int32_t* offsets;
+  int32_t groups;
+  int32_t rows;
+  int32_t n;
+  int32_t ntiles;      // column tiles
+  int32_t kb;          // k-blocks of one source
+  int32_t sources;
+  int32_t n128;        // 128-column tiles of a weight matrix's N
+  void* out0;
+  void* out1;
+  void* out2;
+  void* out3;
+  float* hs;
+  int64_t hs_ld;
+  const void* in0;
+  const void* in1;
+  int32_t* status;
+};
+
+template <int BN>
+struct Cfg {
+  static constexpr int kStageBytes = kTileBytes + BN * BK;
+  static constexpr int kStages = 196608 / kStageBytes;
+  static constexpr int kBufs = 512 / BN;                  // partial products in tensor memory
+  static constexpr int kEpiOff = kStages * kStageBytes;   // 2 KB of output staging a warp
+  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 2048;   // row maxima [2][2][128]
+  static constexpr int kBarOff = kMaxOff + 2048;
+  static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
+  static constexpr int kMiscOff = kBarOff + kBars * 8;
+  static constexpr int kTabOff = kMiscOff + 16;
+  static constexpr size_t smem_bytes(int groups) { return 1024 + kTabOff + 2 * 4 * (groups + 1); }
+  static_assert(smem_bytes(kMaxGroups) <= 232448, "shared memory above 227 KB");
+};
+
+struct Tile {
+  int g, nt, row0, valid;
+};
+
+__device__ __forceinline__ Tile find_tile(int tile, const int* s_off, const int* s_pre, int groups) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_pre[mid] <= tile) lo = mid; else hi = mid;
+  }
+  // M tiles innermost: the CTAs that run at once share an expert's weight blocks
+  const int mtiles = (s_off[lo + 1] - s_off[lo] + BM - 1) / BM;
+  const int rem = tile - s_pre[lo];
+  Tile t;
+  t.g = lo;
+  t.nt = rem / mtiles;
+  t.row0 = s_off[lo] + (rem - t.nt * mtiles) * BM;
+  t.valid = min(BM, s_off[lo + 1] - t.row0);
+  return t;
+}
+
+// One 32-row x 64-byte box of a warp: lane l holds row l in w[0..15]; written
+// to global memory as whole 64-byte row segments through 2 KB of shared memory.
+// dst: row 0 of the box; chunks: 16-byte chunks inside the output's columns.
+__device__ __forceinline__ void store_box(uint32_t stg, int lane, const uint32_t (&w)[16], uint8_t* dst,
+                                          int64_t ld_bytes, int rows, int chunks) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
+                 w[4 * j + 3]);
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    uint4 v;
+    ld_shared_v4(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+    if (r < rows && c < chunks) *reinterpret_cast<uint4*>(dst + r * ld_bytes + c * 16) = v;
+  }
+}
+// 32 fp32 columns of each lane's row as bf16.
+template <class F>
+__device__ __forceinline__ void store_bf16_32(uint32_t stg, int lane, F&& value, void* out, int64_t ld, int64_t row,
+                                              int col, int n, int rows) {
+  if (col >= n) return;
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = bf2(value(2 * j), value(2 * j + 1));
+  store_box(stg, lane, w, reinterpret_cast<uint8_t*>(out) + (row * ld + col) * 2, ld * 2, rows, (n - col) / 8);
+}
+
+template <int BN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages, NBUF = C::kBufs;
+  constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
+  constexpr int SEGS = BN / 128;      // 64-column segments an epilogue warp accumulates
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + NBUF;
+  uint64_t* xbar = tempty + NBUF;     // the two warps of a lane quarter exchanging row maxima
+  uint64_t* mma_done = xbar + 4;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  int* s_off = reinterpret_cast<int*>(smem + C::kTabOff);
+  int* s_pre = s_off + (p.groups + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = p.groups;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kEpiWarps);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], 2);
+    mbar_init(mma_done, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmA[0]);
+    tma_prefetch_desc(&p.tmB[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  // offsets cut to the rows there are, so that no tile reaches outside them
+  for (int i = threadIdx.x; i <= G; i += kThreads) {
+    const int v = p.offsets[i];
+    const int c = min(max(v, 0), p.rows);
+    if (c != v && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+    s_off[i] = c;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (G + 31) / 32;
+    const int lo = min(G, lane * per), hi = min(G, lo + per);
+    int sum = 0;
+    for (int g = lo; g < hi; ++g) sum += max(0, s_off[g + 1] - s_off[g] + BM - 1) / BM * p.ntiles;
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    int run = incl - sum;
+    for (int g = lo; g < hi; ++g) {
+      s_pre[g] = run;
+      run += max(0, s_off[g + 1] - s_off[g] + BM - 1) / BM * p.ntiles;
+    }
+    if (lane == 31) s_pre[G] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const int total = s_pre[G];
+  const int nkb = p.kb * p.sources;
+
+  if (warp < kAuxThreads / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = find_tile(tile, s_off, s_pre, G);
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % S;
+          if (!mbar_wait_bounded(&empty[s], ((it / S) & 1u) ^ 1u, s_abort, p.status, 800 + s)) { ok = false; break; }
+          uint8_t* sA = smem + s * C::kStageBytes;
+          uint8_t* sB = sA + kTileBytes;
+          const int src = kb < p.kb ? 0 : 1;
+          const int k0 = (kb - src * p.kb) * BK;
+          mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+          tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
+#pragma unroll
+          for (int a = 0; a < BN / 128; ++a) {
+            const CUtensorMap* m = &p.tmB[DUAL ? a : src];
+            const int n0 = DUAL ? t.nt * 128 : t.nt * BN + a * 128;
+            if (B_MN) tma_load_3d(sB + a * kTileBytes, m, &full[s], n0, k0, t.g);
+            else tma_load_3d(sB + a * kTileBytes, m, &full[s], k0, n0, t.g);
+          }
+        }
+      }
+      // no copy may still be landing when the CTA exits
+      for (int s = 0; s < S; ++s) {
+        if (it > static_cast<uint32_t>(s)) {
+          const uint32_t last = s + S * ((it - 1 - s) / S);
+          mbar_wait_drain(&full[s], (last / S) & 1u);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN, B_MN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % S, buf = it % NBUF;
+          if (!mbar_wait_bounded(&tempty[buf], ((it / NBUF) & 1u) ^ 1u, s_abort, p.status, 820 + buf) ||
+              !mbar_wait_bounded(&full[s], (it / S) & 1u, s_abort, p.status, 840 + s)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + s * C::kStageBytes);
+          const uint32_t b_base = a_base + kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: 128 columns a row of
+            // 128 bytes, 32 rows on, the next 128 columns a whole region further
+            const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 4096, kTileBytes, 1024)
+                                     : smem_desc_sw128(b_base + kk * 32, 16, 1024);
+            tc_mma_e4m3(tmem_base + buf * BN, ad, bd, idesc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&empty[s]);
+          tc_commit(&tfull[buf]);
+        }
+      }
+      tc_commit(mma_done);   // every MMA has completed before tensor memory is released
+      mbar_wait_drain(mma_done, 0);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - kAuxThreads / 32;
+    const int q = warp & 3;           // lane quarter of tensor memory this warp may read
+    const int hf = ew >> 2;           // column half
+    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 2048);
+    float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
+    // column of the tile at which segment j starts
+    auto seg_col = [&](int j) { return DUAL ? j * 128 + hf * 64 : hf * (BN / 2) + j * 64; };
+    uint32_t it = 0, tcount = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++tcount) {
+      const Tile t = find_tile(tile, s_off, s_pre, G);
+      const int r = q * 32 + lane;
+      const int64_t grow = min(t.row0 + r, p.rows - 1);
+      float acc[SEGS][64];
+#pragma unroll
+      for (int j = 0; j < SEGS; ++j)
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[j][i] = 0.0f;
+      // scale addresses: A by row, B by 128-column tile of each segment
+      const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
+      const int64_t bstep = B_MN ? p.n128 : 1;
+      int64_t boff[SEGS];
+#pragma unroll
+      for (int j = 0; j < SEGS; ++j) {
+        const int nb = DUAL ? t.nt : min((t.nt * BN + seg_col(j)) / 128, p.n128 - 1);
+        boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
+      }
+      auto load_scale = [&](int kb, float (&sc)[SEGS]) {
+        const int src = kb < p.kb ? 0 : 1;
+        const int k = kb - src * p.kb;
+        const float a = __ldg(p.a_scale[src] + grow * p.a_scale_ld + k);
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) sc[j] = a * __ldg(p.b_scale[DUAL ? j : src] + boff[j] + k * bstep);
+      };
+      float sc[SEGS];
+      load_scale(0, sc);
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int buf = it % NBUF;
+        float next[SEGS];
+        if (kb + 1 < nkb) load_scale(kb + 1, next);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[buf], (it / NBUF) & 1u, s_abort, p.status, 860 + buf));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(tb + seg_col(0), v[0]);
+#pragma unroll
+        for (int c = 0; c < 2 * SEGS; ++c) {
+          tmem_wait_ld(v[c & 1]);
+          if (c + 1 < 2 * SEGS) tmem_ld_32x32b_x32(tb + seg_col((c + 1) >> 1) + ((c + 1) & 1) * 32, v[(c + 1) & 1]);
+          else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            acc[c >> 1][(c & 1) * 32 + i] = fmaf(sc[c >> 1], __uint_as_float(v[c & 1][i]), acc[c >> 1][(c & 1) * 32 + i]);
+        }
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) sc[j] = next[j];
+      }
+      if (!ok) break;
+
+      const int rows = t.valid - q * 32;    // valid rows of this warp's box
+      const int64_t row = t.row0 + q * 32;
+      if constexpr (EPI == FP8_EPI_BF16) {
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            store_bf16_32(stg, lane, [&](int i) { return acc[j][c * 32 + i]; }, p.out0, p.n, row,
+                          t.nt * BN + seg_col(j) + c * 32, p.n, rows);
+      } else if constexpr (EPI == FP8_EPI_SWIGLU_FWD) {
+        const int f0 = t.nt * 128 + hf * 64;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (p.out1)
+            store_bf16_32(stg, lane, [&](int i) { return acc[0][c * 32 + i]; }, p.out1, p.n, row, f0 + c * 32, p.n, rows);
+          if (p.out2)
+            store_bf16_32(stg, lane, [&](int i) { return acc[1][c * 32 + i]; }, p.out2, p.n, row, f0 + c * 32, p.n, rows);
+        }
+        // columns past F hold zero (their weights are read as zero)
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const float a = acc[0][i];
+          acc[0][i] = a / (1.0f + __expf(-a)) * acc[1][i];
+          m = fmaxf(m, fabsf(acc[0][i]));
+        }
+        if (p.out3) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            store_bf16_32(stg, lane, [&](int i) { return acc[0][c * 32 + i]; }, p.out3, p.n, row, f0 + c * 32, p.n, rows);
+        }
+        // the other column half's maximum of the same rows; two buffers, since a
+        // warp is at most one exchange ahead of its partner
+        float* mx = s_max + (tcount & 1u) * 256;
+        mx[hf * 128 + r] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xbar[q]);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[q], tcount & 1u, s_abort, p.status, 880 + q));
+        if (!ok) break;
+        const BlockScale b = block_scale(fmaxf(m, mx[(hf ^ 1) * 128 + r]));
+        if (hf == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = fp8_pack4(fp8_quotient(acc[0][4 * i], b.s, b.inv, b.small),
+                           fp8_quotient(acc[0][4 * i + 1], b.s, b.inv, b.small),
+                           fp8_quotient(acc[0][4 * i + 2], b.s, b.inv, b.small),
+                           fp8_quotient(acc[0][4 * i + 3], b.s, b.inv, b.small));
+        if (f0 < p.n)
+          store_box(stg, lane, w, reinterpret_cast<uint8_t*>(p.out0) + row * p.n + f0, p.n, rows, (p.n - f0) / 16);
+      } else {
+        // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1)
+        const int64_t base = grow * p.n;
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = t.nt * BN + seg_col(j) + c * 32;
+            if (col >= p.n) continue;      // n is a multiple of 64: a box is inside or outside
+            uint32_t w1[16], w3[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in0) + base + col) + i);
+              const uint4 x3 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in1) + base + col) + i);
+              const uint32_t u1[4] = {x1.x, x1.y, x1.z, x1.w}, u3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float d1[2], d3[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float dh = acc[j][c * 32 + i * 8 + e * 2 + z];
+                  const float a = z ? hi16(u1[e]) : lo16(u1[e]);
+                  const float b = z ? hi16(u3[e]) : lo16(u3[e]);
+                  const float sg = 1.0f / (1.0f + __expf(-a));
+                  d1[z] = dh * b * sg * (1.0f + a * (1.0f - sg));
+                  d3[z] = dh * a * sg;
+                }
+                w1[i * 4 + e] = bf2(d1[0], d1[1]);
+                w3[i * 4 + e] = bf2(d3[0], d3[1]);
+              }
+            }
+            store_box(stg, lane, w1, static_cast<uint8_t*>(p.out0) + (row * p.n + col) * 2, p.n * 2, rows, 4);
+            store_box(stg, lane, w3, static_cast<uint8_t*>(p.out1) + (row * p.n + col) * 2, p.n * 2, rows, 4);
+          }
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+// -------------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(ptr);
+  });
+  return fn;
+}
+
+// Codes {inner, rows, groups} (2-D without groups) in boxes of 128 x 128
+// bytes, 128-byte swizzle, zero outside.
+bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups) {
+  EncodeFn enc = encode_fn();
+  if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15u) || inner % 16) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(groups > 0 ? groups : 1)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(inner * rows)};
+  cuuint32_t box[3] = {128, 128, 1};
+  cuuint32_t one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool B_MN, int EPI>
+cudaError_t launch_form(const Fp8Params& p, int64_t tiles, cudaStream_t st) {
+  auto kern = fp8_gemm_kernel<BN, B_MN, EPI>;
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(Cfg<BN>::smem_bytes(kMaxGroups)));
+  });
+  if (err != cudaSuccess) return err;
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
+  kern<<<grid, kThreads, Cfg<BN>::smem_bytes(p.groups), st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quant_rows(const void* src, int64_t rows, int64_t cols, uint8_t* codes, float* scales,
+                                  int64_t ld, cudaStream_t st) {
+  if (rows <= 0) return cudaSuccess;
+  const int64_t warps = rows * ((cols / 16 + 31) / 32);
+  const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
+  fp8_quant_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const uint4*>(src), rows, static_cast<int>(cols / 16),
+                                              reinterpret_cast<uint4*>(codes), scales, ld);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_quant_scatter(const void* x, int n_tok, int d, int top_k, const int32_t* row_of_copy,
+                                     uint8_t* codes, float* scales, int64_t ld, uint8_t* tok_codes,
+                                     float* tok_scales, cudaStream_t st) {
+  if (n_tok <= 0) return cudaSuccess;
+  const int64_t warps = static_cast<int64_t>(n_tok) * ((d / 16 + 31) / 32);
+  const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
+  fp8_quant_scatter_kernel<<<grid, 256, 0, st>>>(static_cast<const uint4*>(x), n_tok, d / 16, top_k, row_of_copy,
+                                                 reinterpret_cast<uint4*>(codes), scales, ld,
+                                                 reinterpret_cast<uint4*>(tok_codes), tok_scales);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
+  if (a.rows <= 0 || a.n <= 0 || a.groups <= 0) return cudaSuccess;
+  if (a.groups > kMaxGroups || a.k <= 0 || a.k % 16 || a.n % 16 || a.sources < 1 || a.sources > 2 ||
+      a.rows > 0x7fffff00LL || a.n > 0x3fffffffLL || a.k > 0x3fffffffLL)
+    return cudaErrorInvalidValue;
+  Fp8Params p{};
+  for (int s = 0; s < 2; ++s) {
+    const int sa = s < a.sources ? s : 0;
+    const int sb = (s < a.sources || a.dual) ? s : 0;
+    if (!code_map(&p.tmA[s], a.a[sa], a.k, a.rows, 0)) return cudaErrorInvalidValue;
+    if (!(a.b_mn ? code_map(&p.tmB[s], a.b[sb], a.n, a.k, a.groups) : code_map(&p.tmB[s], a.b[sb], a.k, a.n, a.groups)))
+      return cudaErrorInvalidValue;
+    p.a_scale[s] = a.a_scale[sa];
+    p.b_scale[s] = a.b_scale[sb];
+  }
+  p.a_scale_ld = a.a_scale_ld;
+  p.offsets = a.offsets;
+  p.groups = a.groups;
+  p.rows = static_cast<int32_t>(a.rows);
+  p.n = static_cast<int32_t>(a.n);
+  p.kb = static_cast<int32_t>((a.k + BK - 1) / BK);
+  p.sources = a.sources;
+  p.n128 = static_cast<int32_t>((a.n + 127) / 128);
+  p.out0 = a.out0;
+  p.out1 = a.out1;
+  p.out2 = a.out2;
+  p.out3 = a.out3;
+  p.hs = a.hs;
+  p.hs_ld = a.hs_ld;
+  p.in0 = a.in0;
+  p.in1 = a.in1;
+  p.status = a.status;
+  const int64_t mt = a.rows / BM + std::min<int64_t>(a.groups, a.rows);   // most M tiles of any split into groups
+  if (a.epi == FP8_EPI_SWIGLU_FWD) {
+    p.ntiles = p.n128;
+    return launch_form<256, false, FP8_EPI_SWIGLU_FWD>(p, mt * p.ntiles, st);
+  }
+  if (a.epi == FP8_EPI_SWIGLU_BWD) {
+    p.ntiles = (p.n + 255) / 256;
+    return launch_form<256, true, FP8_EPI_SWIGLU_BWD>(p, mt * p.ntiles, st);
+  }
+  p.ntiles = (p.n + 255) / 256;
+  return a.b_mn ? launch_form<256, true, FP8_EPI_BF16>(p, mt * p.ntiles, st)
+                : launch_form<256, false, FP8_EPI_BF16>(p, mt * p.ntiles, st);
+}
+
+}  // namespace moe

@@ -9,6 +9,8 @@
 #include <cstdint>
 
 #include "balance.cuh"
+#include "block.cuh"
+#include "fp8_block.cuh"
 #include "grouped_gemm.cuh"
 #include "moe_kernels.cuh"
 #include "mxfp8.cuh"
@@ -40,12 +42,14 @@ constexpr size_t kRouteAccWords = 1024;
 // The router logits GEMM has one 128-token tile per CTA; with few tiles its
 // contraction is cut into up to this many slices (summed in order after).
 constexpr int kGateSlices = 4;
+// moe_desc_t.precision of the FP8 layer with one scale per block of 128
+constexpr int kFp8b = 4;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct WsLayout {
   size_t status = 0, dense_off = 0, blk_counts = 0, blk_base = 0, look = 0, racc = 0, aux = 0, gpart = 0,
          rp_hist = 0, fwd_end = 0;
-  size_t hq = 0, hs = 0, hq_sh = 0, hs_sh = 0;   // MXFP8 h between GEMM1 and GEMM2
+  size_t hq = 0, hs = 0, hq_sh = 0, hs_sh = 0;   // MXFP8 / FP8 h between GEMM1 and GEMM2
   size_t dl = 0, dg = 0, dyw = 0, da1 = 0, da3 = 0, da1s = 0, da3s = 0, dxs = 0, dwg = 0, gmaps = 0, total = 0;
   // MXFP8 backward: row-wise codes/scales of dYw, da1, da3 (dgrad operands),
   // padded group starts, and four transposed token-blocked code matrices
@@ -53,6 +57,7 @@ struct WsLayout {
   size_t q_dy = 0, q_dys = 0, q_da1 = 0, q_da1s = 0, q_da3 = 0, q_da3s = 0, pad = 0, pad_sh = 0;
   size_t t_d0 = 0, t_d0s = 0, t_d1 = 0, t_d1s = 0, t_f0 = 0, t_f0s = 0, t_f1 = 0, t_f1s = 0;
   int64_t rp = 0;   // leading dimension of the transposed code matrices
+  size_t norm = 0;  // partial sums of the layer norm's weight gradients
 };
 
 int64_t ld16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -81,6 +86,12 @@ WsLayout layout(const moe_desc_t& d) {
     L.hs = o; o = align_up(o + F / 32 * moe::mx_scale_ld(R));
     L.hq_sh = o; o = align_up(o + N * Fs);
     L.hs_sh = o; o = align_up(o + Fs / 32 * moe::mx_scale_ld(N));
+  }
+  if (d.precision == kFp8b) {
+    L.hq = o; o = align_up(o + R * F);
+    L.hs = o; o = align_up(o + R * moe::fp8_scale_ld(F) * 4);
+    L.hq_sh = o; o = align_up(o + N * Fs);
+    L.hs_sh = o; o = align_up(o + N * moe::fp8_scale_ld(Fs) * 4);
   }
   L.fwd_end = o;
   L.dl = o; o = align_up(o + R * 4);
@@ -117,6 +128,16 @@ WsLayout layout(const moe_desc_t& d) {
     L.t_f1 = o; o = align_up(o + Fm * rp);
     L.t_f1s = o; o = align_up(o + rp / 32 * ld16(Fm));
   }
+  if (d.precision == kFp8b) {   // codes and scales of dYw, da1, da3
+    const size_t Fm = F > Fs ? F : Fs;
+    L.q_dy = o; o = align_up(o + R * D);
+    L.q_dys = o; o = align_up(o + R * moe::fp8_scale_ld(D) * 4);
+    L.q_da1 = o; o = align_up(o + R * Fm);
+    L.q_da1s = o; o = align_up(o + R * moe::fp8_scale_ld(Fm) * 4);
+    L.q_da3 = o; o = align_up(o + R * Fm);
+    L.q_da3s = o; o = align_up(o + R * moe::fp8_scale_ld(Fm) * 4);
+  }
+  L.norm = o; o = align_up(o + moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
   L.total = o;
   return L;
 }
@@ -142,7 +163,7 @@ moe_status_t check_desc(const moe_desc_t* d) {
   if (d->use_bias != 0 && d->use_bias != 1) return MOE_ERR_INVALID_ARG;
   if (d->n_shared != 0 && d->n_shared != 1) return d->n_shared > 1 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   if (d->n_shared && (d->d_ff_shared <= 0 || d->d_ff_shared % 64)) return MOE_ERR_INVALID_ARG;
-  if (d->precision < 0 || d->precision > 2) return MOE_ERR_UNSUPPORTED;
+  if (d->precision < 0 || d->precision > kFp8b || d->precision == 3) return MOE_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->n_tok) * d->top_k >= (int64_t{1} << 31)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -254,14 +275,75 @@ moe_status_t ffn_pair(const void* a_in, int64_t rows, int D, int F, int groups, 
   return MOE_OK;
 }
 
+// FP8 forms of one expert set (precision 4): codes and scales of its operands.
+struct Fp8Ffn {
+  const void *w1, *w3, *w2;
+  const void *w1s, *w3s, *w2s;
+};
+struct Fp8Scratch {
+  uint8_t *dy, *da1, *da3;
+  float *dys, *da1s, *da3s;
+};
+
+cudaError_t fp8_gemm(int kind, const moe::Fp8GemmArgs& a, cudaStream_t st) {
+  return moe::timed(kind, st, [&] { return moe::launch_fp8_gemm(a, st); });
+}
+
+// GEMM1 (w1 | w3, SwiGLU, h quantised along F) and GEMM2 over the FP8 rows
+// aq / as [rows, D].
+moe_status_t ffn_pair_fp8(const void* aq, const void* as, int64_t rows, int D, int F, int groups,
+                          const int32_t* offsets, const Fp8Ffn& w, uint8_t* hq, float* hs, void* h, void* a1,
+                          void* a3, void* y, int32_t* status, cudaStream_t st) {
+  moe::Fp8GemmArgs g1;
+  g1.epi = moe::FP8_EPI_SWIGLU_FWD;
+  g1.dual = true;
+  g1.a[0] = static_cast<const uint8_t*>(aq);
+  g1.a_scale[0] = static_cast<const float*>(as);
+  g1.a_scale_ld = moe::fp8_scale_ld(D);
+  g1.b[0] = static_cast<const uint8_t*>(w.w1);
+  g1.b[1] = static_cast<const uint8_t*>(w.w3);
+  g1.b_scale[0] = static_cast<const float*>(w.w1s);
+  g1.b_scale[1] = static_cast<const float*>(w.w3s);
+  g1.k = D;
+  g1.n = F;
+  g1.offsets = offsets;
+  g1.groups = groups;
+  g1.rows = rows;
+  g1.out0 = hq;
+  g1.hs = hs;
+  g1.hs_ld = moe::fp8_scale_ld(F);
+  g1.out1 = a1;
+  g1.out2 = a3;
+  g1.out3 = h;
+  g1.status = status;
+  MOE_CUDA(fp8_gemm(moe::TIMING_FFN_FWD, g1, st));
+  moe::Fp8GemmArgs g2;
+  g2.a[0] = hq;
+  g2.a_scale[0] = hs;
+  g2.a_scale_ld = moe::fp8_scale_ld(F);
+  g2.b[0] = static_cast<const uint8_t*>(w.w2);
+  g2.b_scale[0] = static_cast<const float*>(w.w2s);
+  g2.k = F;
+  g2.n = D;
+  g2.offsets = offsets;
+  g2.groups = groups;
+  g2.rows = rows;
+  g2.out0 = y;
+  g2.status = status;
+  MOE_CUDA(fp8_gemm(moe::TIMING_FFN_FWD, g2, st));
+  return MOE_OK;
+}
+
 // Backward of one expert set: dgrad through w2 with the SwiGLU derivative,
 // weight gradient of w2, dgrad through w1|w3, weight gradients of w1, w3.
 moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, const void* a3, const void* h,
                           int64_t rows, int D, int F, int groups, const int32_t* offsets, const void* w1,
                           const void* w3, const void* w2, void* da1, void* da3, void* dx_rows, float* dw1,
                           float* dw3, float* dw2, int32_t* status, cudaStream_t st, void* map_ws,
-                          const float* s1 = nullptr, const float* s3 = nullptr, const float* s2 = nullptr) {
-  const bool w8 = s1 != nullptr;   // FP8 weights in the data gradients; weight gradients stay bf16
+                          const float* s1 = nullptr, const float* s3 = nullptr, const float* s2 = nullptr,
+                          const Fp8Scratch* f8 = nullptr) {
+  // FP8 weights (w8) or FP8 operands (f8) in the data gradients; weight gradients stay bf16
+  const bool w8 = s1 != nullptr && !f8;
   GemmArgs g;
   g.w8 = w8;
   g.w8_scale[0] = s2;
@@ -280,7 +362,30 @@ moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, con
   g.out1 = da3;
   g.ld_out = F;
   g.status = status;
-  MOE_CUDA(gemm(moe::TIMING_DGRAD, g, st));
+  if (f8) {
+    MOE_CUDA(moe::launch_fp8_quant_rows(dyw, rows, D, f8->dy, f8->dys, moe::fp8_scale_ld(D), st));
+    moe::Fp8GemmArgs q;
+    q.epi = moe::FP8_EPI_SWIGLU_BWD;
+    q.b_mn = true;   // w2 [D, F]: contraction over D, f contiguous
+    q.a[0] = f8->dy;
+    q.a_scale[0] = f8->dys;
+    q.a_scale_ld = moe::fp8_scale_ld(D);
+    q.b[0] = static_cast<const uint8_t*>(w2);
+    q.b_scale[0] = s2;
+    q.k = D;
+    q.n = F;
+    q.offsets = offsets;
+    q.groups = groups;
+    q.rows = rows;
+    q.in0 = a1;
+    q.in1 = a3;
+    q.out0 = da1;
+    q.out1 = da3;
+    q.status = status;
+    MOE_CUDA(fp8_gemm(moe::TIMING_DGRAD, q, st));
+  } else {
+    MOE_CUDA(gemm(moe::TIMING_DGRAD, g, st));
+  }
 
   GemmArgs w;
   w.epi = moe::EPI_F32;
@@ -320,7 +425,33 @@ moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, con
   d.out0 = dx_rows;
   d.ld_out = D;
   d.status = status;
-  MOE_CUDA(gemm(moe::TIMING_DGRAD, d, st));
+  if (f8) {
+    const int64_t ld = moe::fp8_scale_ld(F);
+    MOE_CUDA(moe::launch_fp8_quant_rows(da1, rows, F, f8->da1, f8->da1s, ld, st));
+    MOE_CUDA(moe::launch_fp8_quant_rows(da3, rows, F, f8->da3, f8->da3s, ld, st));
+    moe::Fp8GemmArgs q;
+    q.b_mn = true;   // w1, w3 [F, D]: contraction over F, d contiguous
+    q.sources = 2;
+    q.a[0] = f8->da1;
+    q.a[1] = f8->da3;
+    q.a_scale[0] = f8->da1s;
+    q.a_scale[1] = f8->da3s;
+    q.a_scale_ld = ld;
+    q.b[0] = static_cast<const uint8_t*>(w1);
+    q.b[1] = static_cast<const uint8_t*>(w3);
+    q.b_scale[0] = s1;
+    q.b_scale[1] = s3;
+    q.k = F;
+    q.n = D;
+    q.offsets = offsets;
+    q.groups = groups;
+    q.rows = rows;
+    q.out0 = dx_rows;
+    q.status = status;
+    MOE_CUDA(fp8_gemm(moe::TIMING_DGRAD, q, st));
+  } else {
+    MOE_CUDA(gemm(moe::TIMING_DGRAD, d, st));
+  }
 
   // dW1_e [F,D] = da1_e^T x_e, dW3_e = da3_e^T x_e
   w.a[0] = act(da1, rows, F);
@@ -637,11 +768,14 @@ moe_status_t backward_impl(const moe_desc_t* d, const void* w_gate, const moe_ex
 
   MOE_CUDA(moe::launch_combine_bwd(N, D, K, d->gate, dy, s->y_perm, s->row_of_copy, s->topk_w, s->logits, E,
                                    s->topk_idx, dyw, dg, dl, st));
+  const Fp8Scratch f8{at<uint8_t>(ws, L.q_dy),  at<uint8_t>(ws, L.q_da1), at<uint8_t>(ws, L.q_da3),
+                      at<float>(ws, L.q_dys), at<float>(ws, L.q_da1s),  at<float>(ws, L.q_da3s)};
+  const Fp8Scratch* pf8 = d->precision == kFp8b ? &f8 : nullptr;
   // routed experts; dx_perm overwrites dYw once its last reader is done
   auto sc = [&](const void* p_) { return q ? static_cast<const float*>(p_) : nullptr; };
   MOE_TRY(ffn_pair_bwd(dyw, s->x_perm, s->a1, s->a3, s->h, R, D, F, E, s->offsets, w->w1, w->w3, w->w2, da1, da3,
                        dyw, g->dw1, g->dw3, g->dw2, status, st, map_scratch(ws, L), sc(q ? q->w1_scale : nullptr),
-                       sc(q ? q->w3_scale : nullptr), sc(q ? q->w2_scale : nullptr)));
+                       sc(q ? q->w3_scale : nullptr), sc(q ? q->w2_scale : nullptr), pf8));
   void* dxs = nullptr;
   if (d->n_shared) {
     int32_t* dense = at<int32_t>(ws, L.dense_off);
@@ -650,7 +784,7 @@ moe_status_t backward_impl(const moe_desc_t* d, const void* w_gate, const moe_ex
     MOE_TRY(ffn_pair_bwd(dy, s->x, s->a1s, s->a3s, s->hs, N, D, d->d_ff_shared, 1, dense, w->ws1, w->ws3, w->ws2,
                          at<void>(ws, L.da1s), at<void>(ws, L.da3s), dxs, g->dws1, g->dws3, g->dws2, status, st,
                          map_scratch(ws, L), sc(q ? q->ws1_scale : nullptr), sc(q ? q->ws3_scale : nullptr),
-                         sc(q ? q->ws2_scale : nullptr)));
+                         sc(q ? q->ws2_scale : nullptr), pf8));
   }
   if (s->offsets_full && s->copy_of_row_full)   // capacity mode: every copy, x gathered in dropless order
     MOE_CUDA(moe::launch_dwgate(N, K, E, D, s->offsets_full, s->copy_of_row_full, dl, s->x, K,
@@ -1091,6 +1225,192 @@ moe_status_t moe_update_bias(const moe_desc_t* d, const int32_t* counts, float* 
   if (!counts || !bias || (mode != 0 && mode != 1)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       moe::launch_update_bias(counts, d->n_exp, bias, gamma, mode, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_t cols, void* codes, float* scales,
+                                   int64_t scale_ld, void* stream) {
+  MOE_RANGE("moe_quantize_fp8_rows");
+  if (rows < 0 || cols <= 0 || cols % 16 || cols > (int64_t{1} << 30) || scale_ld < (cols + 127) / 128)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!all16({src, codes}) || !scales || (reinterpret_cast<uintptr_t>(scales) & 3u)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_fp8_quant_rows(src, rows, cols, static_cast<uint8_t*>(codes), scales, scale_ld,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_fp8_workspace_size(int64_t n_groups, int64_t rows, int64_t n, int64_t k,
+                                                 size_t* bytes) {
+  if (!bytes || n_groups < 1 || n_groups > 1024 || rows < 0 || n <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+  *bytes = kAlign;
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_gemm_fp8(int64_t n_groups, int64_t rows, int64_t n, int64_t k, const void* a,
+                                  const float* a_scale, int64_t a_scale_ld, const int32_t* offsets, const void* b,
+                                  const float* b_scale, int32_t b_mn, void* out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  MOE_RANGE("moe_grouped_gemm_fp8");
+  size_t need = 0;
+  MOE_TRY(moe_grouped_gemm_fp8_workspace_size(n_groups, rows, n, k, &need));
+  if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (n % 16 || k % 16 || n > (int64_t{1} << 29) || k > (int64_t{1} << 29) || rows >= (int64_t{1} << 31) - 256 ||
+      a_scale_ld < (k + 127) / 128 || (b_mn != 0 && b_mn != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!all16({a, b, out}) || !a_scale || !b_scale || !offsets) return MOE_ERR_INVALID_ARG;
+  moe::Fp8GemmArgs g;
+  g.b_mn = b_mn != 0;
+  g.a[0] = static_cast<const uint8_t*>(a);
+  g.a_scale[0] = a_scale;
+  g.a_scale_ld = a_scale_ld;
+  g.b[0] = static_cast<const uint8_t*>(b);
+  g.b_scale[0] = b_scale;
+  g.k = k;
+  g.n = n;
+  g.offsets = offsets;
+  g.groups = static_cast<int>(n_groups);
+  g.rows = rows;
+  g.out0 = out;
+  g.status = static_cast<int32_t*>(ws);
+  return cuda_status(fp8_gemm(b_mn ? moe::TIMING_DGRAD : moe::TIMING_FFN_FWD, g, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_permute_fp8b(const moe_desc_t* d, const void* x, const int32_t* topk_idx, const int32_t* offsets,
+                              int32_t* row_of_copy, int32_t* copy_of_row, void* x_perm, void* xq_perm, float* xs_perm,
+                              void* xq_tok, float* xs_tok, void* ws, size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_permute_fp8b");
+  MOE_TRY(check_desc(d));
+  if (d->precision != kFp8b) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(*d, ws, ws_bytes, false));
+  if (!all16({x, xq_perm, xs_perm}) || !topk_idx || !offsets || !row_of_copy || !copy_of_row)
+    return MOE_ERR_INVALID_ARG;
+  if (x_perm && !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
+  if (xq_tok && !all16({xq_tok, xs_tok})) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return MOE_OK;
+  if (x_perm)
+    MOE_TRY(moe_permute(d, x, topk_idx, offsets, row_of_copy, copy_of_row, x_perm, ws, ws_bytes, stream));
+  else
+    MOE_TRY(moe_permute_maps(d, topk_idx, offsets, row_of_copy, copy_of_row, ws, ws_bytes, stream));
+  return cuda_status(moe::launch_fp8_quant_scatter(
+      x, d->n_tok, d->d_model, d->top_k, row_of_copy, static_cast<uint8_t*>(xq_perm), xs_perm,
+      moe::fp8_scale_ld(d->d_model), static_cast<uint8_t*>(xq_tok), xs_tok, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_ffn_fp8b(const moe_desc_t* d, const void* xq_perm, const float* xs_perm,
+                                  const int32_t* offsets, const void* xq_tok, const float* xs_tok,
+                                  const moe_expert_weights_mx_t* w, const moe_ffn_saved_t* saved, void* y_perm,
+                                  void* y_shared, void* ws, size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_grouped_ffn_fp8b");
+  MOE_TRY(check_desc(d));
+  if (d->precision != kFp8b) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(*d, ws, ws_bytes, false));
+  if (!w || !offsets || !all16({xq_perm, xs_perm, w->w1, w->w3, w->w2, y_perm}) || !w->w1_scale || !w->w3_scale ||
+      !w->w2_scale)
+    return MOE_ERR_INVALID_ARG;
+  moe_ffn_saved_t sv{};
+  if (saved) sv = *saved;
+  for (const void* q : {sv.a1, sv.a3, sv.h, sv.a1s, sv.a3s, sv.hs})
+    if (q && !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (d->n_shared && (!all16({xq_tok, xs_tok, w->ws1, w->ws3, w->ws2, y_shared}) || !w->ws1_scale ||
+                      !w->ws3_scale || !w->ws2_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return MOE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WsLayout L = layout(*d);
+  int32_t* status = at<int32_t>(ws, L.status);
+  const int64_t R = static_cast<int64_t>(d->n_tok) * d->top_k;
+  MOE_TRY(ffn_pair_fp8(xq_perm, xs_perm, R, d->d_model, d->d_ff, d->n_exp, offsets,
+                       Fp8Ffn{w->w1, w->w3, w->w2, w->w1_scale, w->w3_scale, w->w2_scale}, at<uint8_t>(ws, L.hq),
+                       at<float>(ws, L.hs), sv.h, sv.a1, sv.a3, y_perm, status, st));
+  if (d->n_shared) {
+    int32_t* dense = at<int32_t>(ws, L.dense_off);
+    MOE_CUDA(moe::launch_dense_offsets(dense, d->n_tok, st));
+    MOE_TRY(ffn_pair_fp8(xq_tok, xs_tok, d->n_tok, d->d_model, d->d_ff_shared, 1, dense,
+                         Fp8Ffn{w->ws1, w->ws3, w->ws2, w->ws1_scale, w->ws3_scale, w->ws2_scale},
+                         at<uint8_t>(ws, L.hq_sh), at<float>(ws, L.hs_sh), sv.hs, sv.a1s, sv.a3s, y_shared, status,
+                         st));
+  }
+  return MOE_OK;
+}
+
+moe_status_t moe_backward_fp8b(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_mx_t* wq,
+                               const moe_fwd_state_t* s, const void* dy, const moe_grads_t* g, void* ws,
+                               size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_backward_fp8b");
+  MOE_TRY(check_desc(d));
+  if (d->precision != kFp8b || !wq) return MOE_ERR_INVALID_ARG;
+  if (!wq->w1_scale || !wq->w3_scale || !wq->w2_scale) return MOE_ERR_INVALID_ARG;
+  if (d->n_shared && (!wq->ws1_scale || !wq->ws3_scale || !wq->ws2_scale)) return MOE_ERR_INVALID_ARG;
+  const moe_expert_weights_t w{wq->w1, wq->w3, wq->w2, wq->ws1, wq->ws3, wq->ws2};
+  return backward_impl(d, w_gate, &w, wq, s, dy, g, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_layernorm(const moe_desc_t* d, const void* x, int32_t x_f32, const float* gamma, const float* beta,
+                           double eps, void* y, float* mean, float* rstd, void* stream) {
+  MOE_RANGE("moe_layernorm");
+  MOE_TRY(check_desc(d));
+  if (d->d_model > moe::kNormMaxCols) return MOE_ERR_UNSUPPORTED;
+  if ((x_f32 != 0 && x_f32 != 1) || !(eps > 0.0) || !(eps < 1e30) || !(static_cast<float>(eps) > 0.0f))
+    return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return MOE_OK;
+  if (!all16({x, gamma, y}) || (beta && !aligned16(beta))) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_layernorm(d->n_tok, d->d_model, x, x_f32 != 0, gamma, beta, static_cast<float>(eps),
+                                           y, mean, rstd, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_layernorm_backward(const moe_desc_t* d, const void* dy, const void* x, int32_t x_f32,
+                                    const float* gamma, const float* mean, const float* rstd, const void* dres,
+                                    void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_layernorm_backward");
+  MOE_TRY(check_desc(d));
+  if (d->d_model > moe::kNormMaxCols) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_ws(*d, ws, ws_bytes, true));
+  if ((x_f32 != 0 && x_f32 != 1) || !dgamma) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok > 0 && (!all16({dy, x, gamma, dx}) || !mean || !rstd)) return MOE_ERR_INVALID_ARG;
+  if (dres && !aligned16(dres)) return MOE_ERR_INVALID_ARG;
+  const WsLayout L = layout(*d);
+  return cuda_status(moe::launch_layernorm_bwd(d->n_tok, d->d_model, dy, x, x_f32 != 0, gamma, mean, rstd, dres, dx,
+                                               dgamma, dbeta, at<float>(ws, L.norm),
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+// Threshold and factor of a dropout probability in [0, 1).
+static bool dropout_params(double p, uint32_t* threshold, float* scale) {
+  if (!(p >= 0.0) || !(p < 1.0)) return false;
+  const double t = std::floor(p * 4294967296.0 + 0.5);
+  *threshold = t >= 4294967295.0 ? 4294967295u : static_cast<uint32_t>(t);
+  *scale = static_cast<float>(1.0 / (1.0 - p));
+  return true;
+}
+
+moe_status_t moe_combine_dropout(const moe_desc_t* d, const void* y_perm, const int32_t* row_of_copy,
+                                 const float* topk_w, const void* y_shared, const void* resid, int32_t resid_f32,
+                                 const int64_t* rng, double p, void* out, void* stream) {
+  MOE_RANGE("moe_combine_dropout");
+  MOE_TRY(check_desc(d));
+  uint32_t threshold = 0;
+  float scale = 1.0f;
+  if (!dropout_params(p, &threshold, &scale) || (resid_f32 != 0 && resid_f32 != 1)) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return MOE_OK;
+  if (!all16({y_perm, out}) || !row_of_copy || !topk_w || !rng) return MOE_ERR_INVALID_ARG;
+  if ((y_shared && !aligned16(y_shared)) || (resid && !aligned16(resid)) || (reinterpret_cast<uintptr_t>(rng) & 7u))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_combine_dropout(d->n_tok, d->d_model, d->top_k, y_perm, row_of_copy, topk_w,
+                                                 y_shared, resid, resid_f32 != 0, rng, threshold, scale, out,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_dropout_backward(const moe_desc_t* d, const void* dout, int32_t dout_f32, const int64_t* rng,
+                                  double p, void* dy, void* stream) {
+  MOE_RANGE("moe_dropout_backward");
+  MOE_TRY(check_desc(d));
+  uint32_t threshold = 0;
+  float scale = 1.0f;
+  if (!dropout_params(p, &threshold, &scale) || (dout_f32 != 0 && dout_f32 != 1)) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return MOE_OK;
+  if (!all16({dout, dy}) || !rng || (reinterpret_cast<uintptr_t>(rng) & 7u)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_dropout_bwd(static_cast<int64_t>(d->n_tok) * d->d_model, dout, dout_f32 != 0, rng,
+                                             threshold, scale, dy, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
