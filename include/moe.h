@@ -495,9 +495,11 @@ MOE_API moe_status_t moe_backward_fp8w(const moe_desc_t* d, const void* w_gate, 
  * scaling, FP32 accumulation): E4M3 operands on the tensor cores, activations
  * with one scale per 128 consecutive elements of a row (1 x 128), weights with
  * one per 128 x 128 tile (moe_quantize_fp8_tile; the same codes and scales
- * serve the forward and the data gradients).  Block scale s = amax / 448 (1
+ * serve the forward and the data gradients).  Block scale of an activation s =
+ * amax * (1 / 448), an fp32 product with the fp32 number nearest to 1 / 448 (1
  * where that is zero); code = E4M3 of the exact quotient x / s, rounded once to
- * nearest even.  A NaN element has the code NaN; a block with an infinity has
+ * nearest even.  bf16 elements often fall on the border between two codes, so
+ * the last bit of s decides codes.  A NaN element has the code NaN; a block with an infinity has
  * an infinite scale, so its row's products are NaN.  The products of each
  * block of 128 are summed unscaled in fp32, multiplied by both scales and
  * added in fp32 in the order of the blocks.

@@ -4,8 +4,8 @@ in fewer.
 
 FP8 ("LLM Infrastructure Engineering 08: MoE Training Engineering" §13.6):
 activations have one scale per 128 consecutive elements of a row, weights one
-per 128 x 128 tile; scale = amax / 448 (1 for an all-zero block), code =
-E4M3(x / scale).  Products are exact sums of the values the codes stand for.
+per 128 x 128 tile.  A row block's scale is the fp32 product amax * (1 / 448) (1
+for an all-zero block), a weight tile's amax / 448; code = E4M3(x / scale).  Products are exact sums of the values the codes stand for.
 """
 from __future__ import annotations
 
@@ -26,7 +26,7 @@ def fp8_rows_quantize(x: np.ndarray):
     for b in range(nb):
         blk = x[:, b * BLOCK:(b + 1) * BLOCK].astype(np.float64)
         amax = np.abs(blk).max(axis=1).astype(np.float32)
-        s = (amax / np.float32(448.0)).astype(np.float32)
+        s = (amax * (np.float32(1.0) / np.float32(448.0))).astype(np.float32)
         scales[:, b] = np.where(s > 0, s, np.float32(1.0))
         codes[:, b * BLOCK:(b + 1) * BLOCK] = e4m3_encode(blk / scales[:, b:b + 1].astype(np.float64))
     return codes, scales

@@ -56,7 +56,7 @@ struct BlockScale {
 };
 __device__ __forceinline__ BlockScale block_scale(float amax) {
   BlockScale b;
-  const float s = amax / 448.0f;
+  const float s = amax * (1.0f / 448.0f);
   b.s = s > 0.0f ? s : 1.0f;
   b.inv = 1.0f / b.s;
   b.small = b.s < 1e-37f;

@@ -2,8 +2,9 @@
 // quantisers and of the grouped GEMM on E4M3 codes.
 //
 // A block of 128 consecutive elements of an activation row (the contraction
-// dimension) has the scale s = amax / 448 (1 where that is zero) and the codes
-// E4M3(x / s), the exact quotient rounded once to nearest even.  Weights have
+// dimension) has the scale s = amax * (1 / 448), an fp32 product (1 where that is
+// zero), and the codes E4M3(x / s), the exact quotient rounded once to nearest
+// even.  Weights have
 // one scale per 128 x 128 tile (launch_fp8_tile_quant).
 #pragma once
 #include <cstddef>
