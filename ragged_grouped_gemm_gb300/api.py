@@ -33,6 +33,9 @@ def _check(fn: str, code: int):
 def _p(t: torch.Tensor | None, dtype=None, shape=None, name="tensor"):
     if t is None:
         return None
+    if (t.is_cuda and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -41,15 +44,22 @@ def _p(t: torch.Tensor | None, dtype=None, shape=None, name="tensor"):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    return t.data_ptr()   # a shape given as another kind of sequence
+
+
+# The handle of the current stream without building a Stream object for it,
+# which took 3 of the 11 us that one norm's enqueue did.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _s(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(stream)
+        return stream.cuda_stream
+    return stream
 
 
 def make_desc(cfg: MoEConfig) -> _lib.MoeDesc:
