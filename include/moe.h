@@ -517,7 +517,8 @@ MOE_API moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_
 /* Matrix products grouped by expert with ragged sizes on those operands:
  *   out[r, j] = sum_i a[r, i] * B_g[j, i]   for the rows r in
  *               [offsets[g], offsets[g+1]) of every group g,
- * a [rows, k] codes with scales [rows][a_scale_ld]; out [rows, n] bf16.
+ * a [rows, k] codes with scales [rows][a_scale_ld] (16-byte aligned, a_scale_ld
+ * a multiple of 4); out [rows, n] bf16.
  * b_mn 0: b [n_groups, n, k] codes, b_scale [n_groups, ceil(n/128), ceil(k/128)]
  * (forward); b_mn 1: b [n_groups, k, n], b_scale [n_groups, ceil(k/128),
  * ceil(n/128)] (the data gradient through weights stored [k, n]).

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 // -------------------------------------------------------------------- GEMM
 constexpr int BM = 128;
 constexpr int BK = 128;              // contraction elements (bytes) of a k-block
-constexpr int kAuxThreads = 128;     // producer, MMA issuer, two idle warps
+constexpr int kAuxThreads = 128;     // producer, MMA issuer, two scale warps
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = kAuxThreads + kEpiWarps * 32;
 // A block launches with 384 x 168 = 64512 registers; the split hands 112 of
@@ -176,8 +176,46 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// acc += s * v.  Volatile, which keeps it behind the wait for the tensor-memory
+// load whose register it reads; naming the registers in the wait costs a copy
+// of each.  (Two products in one instruction need their pair copied together,
+// so they are no fewer instructions.)
+__device__ __forceinline__ void fma_after_wait(float& acc, float s, uint32_t v) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(s), "f"(__uint_as_float(v)));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[16]) { tmem_ld_32x32b_x16(addr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(addr, v); }
+
+// mbar_wait_bounded for a whole warp, with the same answer in every lane and
+// little code: the limit and the abort flag are looked at now and then.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                          int site) {
+  uint64_t t0 = 0;
+  uint32_t n = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if ((++n & 63u) == 0) {
+      if (__any_sync(0xffffffffu, *abort_flag)) return false;
+      const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kSpinTimeoutNs) {
+        if ((threadIdx.x & 31) == 0) {
+          *abort_flag = 1;
+          if (status) {
+            atomicOr(status, DEV_TIMEOUT);
+            atomicExch(status + 1, site);
+          }
+        }
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 struct Fp8Params {
   CUtensorMap tmA[2];
+  CUtensorMap tmA32[2];   // boxes of 32 rows
   CUtensorMap tmB[2];
   const float* a_scale[2];
   const float* b_scale[2];
@@ -208,11 +246,12 @@ struct Cfg {
   static constexpr int kBufs = 512 / BN;                  // partial products in tensor memory
   static constexpr int kEpiOff = kStages * kStageBytes;   // 2 KB of output staging a warp
   static constexpr int kMaxOff = kEpiOff + kEpiWarps * 2048;   // row maxima [2][2][128]
-  static constexpr int kBarOff = kMaxOff + 2048;
-  static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
+  static constexpr int kScaleOff = kMaxOff + 2048;             // scale products [2][4 k-blocks][2][128]
+  static constexpr int kBarOff = kScaleOff + 8192;
+  static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 4 + 1;
   static constexpr int kMiscOff = kBarOff + kBars * 8;
   static constexpr int kTabOff = kMiscOff + 16;
-  static constexpr size_t smem_bytes(int groups) { return 1024 + kTabOff + 2 * 4 * (groups + 1); }
+  static constexpr size_t smem_bytes(int groups) { return 1024 + kTabOff + 4 * (groups + 1); }
   static_assert(smem_bytes(kMaxGroups) <= 232448, "shared memory above 227 KB");
 };
 
@@ -220,20 +259,26 @@ struct Tile {
   int g, nt, row0, valid;
 };
 
-__device__ __forceinline__ Tile find_tile(int tile, const int* s_off, const int* s_pre, int groups) {
-  int lo = 0, hi = groups;
+// An offset cut to the rows there are, so that no tile reaches outside them.
+__device__ __forceinline__ int cut_offset(const Fp8Params& p, int i) {
+  return min(max(__ldg(p.offsets + i), 0), p.rows);
+}
+
+__device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const int* s_pre) {
+  int lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (s_pre[mid] <= tile) lo = mid; else hi = mid;
   }
   // M tiles innermost: the CTAs that run at once share an expert's weight blocks
-  const int mtiles = (s_off[lo + 1] - s_off[lo] + BM - 1) / BM;
+  const int first = cut_offset(p, lo), last = cut_offset(p, lo + 1);
+  const int mtiles = (last - first + BM - 1) / BM;
   const int rem = tile - s_pre[lo];
   Tile t;
   t.g = lo;
   t.nt = rem / mtiles;
-  t.row0 = s_off[lo] + (rem - t.nt * mtiles) * BM;
-  t.valid = min(BM, s_off[lo + 1] - t.row0);
+  t.row0 = first + (rem - t.nt * mtiles) * BM;
+  t.valid = min(BM, last - t.row0);
   return t;
 }
 
@@ -273,6 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   using C = Cfg<BN>;
   constexpr int S = C::kStages, NBUF = C::kBufs;
   constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
+#ifndef CHV
+#define CHV 32
+#endif
+  constexpr int CH = CHV;
   constexpr int SEGS = BN / 128;      // 64-column segments an epilogue warp accumulates
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -281,13 +330,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + NBUF;
   uint64_t* xbar = tempty + NBUF;     // the two warps of a lane quarter exchanging row maxima
-  uint64_t* mma_done = xbar + 4;
+  uint64_t* sfull = xbar + 4;         // scale products of four k-blocks written
+  uint64_t* sempty = sfull + 2;
+  uint64_t* mma_done = sempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-  int* s_off = reinterpret_cast<int*>(smem + C::kTabOff);
-  int* s_pre = s_off + (p.groups + 1);
+  int* s_pre = reinterpret_cast<int*>(smem + C::kTabOff);
+  float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
 
-  const int warp = threadIdx.x >> 5;
+  // the same in every lane, which lets tensor-memory and barrier addresses stay in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int G = p.groups;
 
@@ -301,6 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(&tempty[b], kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], 2);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sfull[b], 2);
+      mbar_init(&sempty[b], kEpiWarps);
+    }
     mbar_init(mma_done, 1);
     *s_abort = 0;
     fence_mbar_init();
@@ -311,19 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
-  // offsets cut to the rows there are, so that no tile reaches outside them
-  for (int i = threadIdx.x; i <= G; i += kThreads) {
-    const int v = p.offsets[i];
-    const int c = min(max(v, 0), p.rows);
-    if (c != v && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
-    s_off[i] = c;
-  }
-  __syncthreads();
+  for (int i = threadIdx.x; i <= G; i += kThreads)
+    if (cut_offset(p, i) != __ldg(p.offsets + i) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
   if (warp == 0) {
+    auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + BM - 1) / BM * p.ntiles; };
     const int per = (G + 31) / 32;
     const int lo = min(G, lane * per), hi = min(G, lo + per);
     int sum = 0;
-    for (int g = lo; g < hi; ++g) sum += max(0, s_off[g + 1] - s_off[g] + BM - 1) / BM * p.ntiles;
+    for (int g = lo; g < hi; ++g) sum += tiles_of(g);
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -333,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     int run = incl - sum;
     for (int g = lo; g < hi; ++g) {
       s_pre[g] = run;
-      run += max(0, s_off[g + 1] - s_off[g] + BM - 1) / BM * p.ntiles;
+      run += tiles_of(g);
     }
     if (lane == 31) s_pre[G] = incl;
   }
@@ -351,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = find_tile(tile, s_off, s_pre, G);
+        const Tile t = find_tile(tile, p, s_pre);
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % S;
           if (!mbar_wait_bounded(&empty[s], ((it / S) & 1u) ^ 1u, s_abort, p.status, 800 + s)) { ok = false; break; }
@@ -359,8 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           uint8_t* sB = sA + kTileBytes;
           const int src = kb < p.kb ? 0 : 1;
           const int k0 = (kb - src * p.kb) * BK;
-          mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-          tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
+          // a tile of at most 32 rows loads no others: what the rest of its stage
+          // holds reaches accumulator rows that nothing reads
+          const bool few = t.valid <= 32;
+          mbar_arrive_expect_tx(&full[s], few ? C::kStageBytes - kTileBytes * 3 / 4 : C::kStageBytes);
+          tma_load_2d(sA, few ? &p.tmA32[src] : &p.tmA[src], &full[s], k0, t.row0);
 #pragma unroll
           for (int a = 0; a < BN / 128; ++a) {
             const CUtensorMap* m = &p.tmB[DUAL ? a : src];
@@ -408,6 +462,54 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
       tc_commit(mma_done);   // every MMA has completed before tensor memory is released
       mbar_wait_drain(mma_done, 0);
+    } else if (warp >= 2) {
+      // -------------------------------------------------------- scales
+      // The products a_scale[r, k-block] * b_scale[n / 128, k-block] of a tile's
+      // rows and its two 128-column blocks, four k-blocks at a time, up to eight
+      // ahead of the epilogue, which then reads one number per row.
+      const int at = static_cast<int>(threadIdx.x) - 64;    // rows at and at + 64
+      const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
+      const int64_t bstep = B_MN ? p.n128 : 1;
+      uint32_t gi = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = find_tile(tile, p, s_pre);
+        int64_t boff[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int nb = DUAL ? t.nt : min(t.nt * (BN / 128) + (BN > 128 ? j : 0), p.n128 - 1);
+          boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
+        }
+        for (int src = 0; ok && src < p.sources; ++src) {
+          for (int k4 = 0; k4 < p.kb; k4 += 4, ++gi) {
+            float4 a[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              a[h] = __ldg(reinterpret_cast<const float4*>(
+                  p.a_scale[src] + static_cast<int64_t>(min(t.row0 + at + 64 * h, p.rows - 1)) * p.a_scale_ld + k4));
+            float b[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff[j] + min(k4 + u, p.kb - 1) * bstep);
+            ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
+            if (!ok) break;
+            float* dst = s_scale + (gi & 1u) * 1024 + at;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                dst[j * 128 + h * 64] = a[h].x * b[j][0];
+                dst[256 + j * 128 + h * 64] = a[h].y * b[j][1];
+                dst[512 + j * 128 + h * 64] = a[h].z * b[j][2];
+                dst[768 + j * 128 + h * 64] = a[h].w * b[j][3];
+              }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfull[gi & 1u]);
+          }
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -420,60 +522,62 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
     // column of the tile at which segment j starts
     auto seg_col = [&](int j) { return DUAL ? j * 128 + hf * 64 : hf * (BN / 2) + j * 64; };
-    uint32_t it = 0, tcount = 0;
+    // this warp has read a partial product
+    auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+    };
+    uint32_t it = 0, gi = 0, tcount = 0;
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++tcount) {
-      const Tile t = find_tile(tile, s_off, s_pre, G);
+      const Tile t = find_tile(tile, p, s_pre);
       const int r = q * 32 + lane;
-      const int64_t grow = min(t.row0 + r, p.rows - 1);
+      const bool mine = q * 32 < t.valid;    // whether this warp has rows of the tile
       float acc[SEGS][64];
 #pragma unroll
       for (int j = 0; j < SEGS; ++j)
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[j][i] = 0.0f;
-      // scale addresses: A by row, B by 128-column tile of each segment
-      const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
-      const int64_t bstep = B_MN ? p.n128 : 1;
-      int64_t boff[SEGS];
+      for (int src = 0; ok && src < p.sources; ++src) {
+        for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
+          ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
+          const float* ps = s_scale + (gi & 1u) * 1024 + r;
 #pragma unroll
-      for (int j = 0; j < SEGS; ++j) {
-        const int nb = DUAL ? t.nt : min((t.nt * BN + seg_col(j)) / 128, p.n128 - 1);
-        boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
-      }
-      auto load_scale = [&](int kb, float (&sc)[SEGS]) {
-        const int src = kb < p.kb ? 0 : 1;
-        const int k = kb - src * p.kb;
-        const float a = __ldg(p.a_scale[src] + grow * p.a_scale_ld + k);
+          for (int u = 0; u < 4; ++u) {
+            if (ok && k4 + u < p.kb) {
+              float sc[SEGS];
 #pragma unroll
-        for (int j = 0; j < SEGS; ++j) sc[j] = a * __ldg(p.b_scale[DUAL ? j : src] + boff[j] + k * bstep);
-      };
-      float sc[SEGS];
-      load_scale(0, sc);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int buf = it % NBUF;
-        float next[SEGS];
-        if (kb + 1 < nkb) load_scale(kb + 1, next);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[buf], (it / NBUF) & 1u, s_abort, p.status, 860 + buf));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(tb + seg_col(0), v[0]);
+              for (int j = 0; j < SEGS; ++j) sc[j] = ps[u * 256 + (DUAL ? j : BN > 128 ? hf : 0) * 128];
+              const int buf = it % NBUF;
+              ok = warp_wait(&tfull[buf], (it / NBUF) & 1u, s_abort, p.status, 860);
+              if (ok) {
+                if (mine) {
+                  tc_fence_after();
+                  const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+                  uint32_t v[2][CH];
+                  tmem_ld(tb + seg_col(0), v[0]);
+                  constexpr int PS = 64 / CH;   // loads of a segment
 #pragma unroll
-        for (int c = 0; c < 2 * SEGS; ++c) {
-          tmem_wait_ld(v[c & 1]);
-          if (c + 1 < 2 * SEGS) tmem_ld_32x32b_x32(tb + seg_col((c + 1) >> 1) + ((c + 1) & 1) * 32, v[(c + 1) & 1]);
-          else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[buf]);
+                  for (int c = 0; c < PS * SEGS; ++c) {
+                    tmem_wait_ld();
+                    if (c + 1 < PS * SEGS)
+                      tmem_ld(tb + seg_col((c + 1) / PS) + ((c + 1) % PS) * CH, v[(c + 1) & 1]);
+                    else
+                      release(buf);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) fma_after_wait(acc[c / PS][(c % PS) * CH + i], sc[c / PS], v[c & 1][i]);
+                  }
+                } else {
+                  release(buf);
+                }
+                ++it;
+              }
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            acc[c >> 1][(c & 1) * 32 + i] = fmaf(sc[c >> 1], __uint_as_float(v[c & 1][i]), acc[c >> 1][(c & 1) * 32 + i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
         }
-#pragma unroll
-        for (int j = 0; j < SEGS; ++j) sc[j] = next[j];
       }
       if (!ok) break;
 
@@ -514,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         mx[hf * 128 + r] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(&xbar[q]);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&xbar[q], tcount & 1u, s_abort, p.status, 880 + q));
+        ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
         if (!ok) break;
         const BlockScale b = block_scale(fmaxf(m, mx[(hf ^ 1) * 128 + r]));
         if (hf == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
@@ -526,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           store_box(stg, lane, w, reinterpret_cast<uint8_t*>(p.out0) + row * p.n + f0, p.n, rows, (p.n - f0) / 16);
       } else {
         // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1)
-        const int64_t base = grow * p.n;
+        const int64_t base = static_cast<int64_t>(min(t.row0 + r, p.rows - 1)) * p.n;
 #pragma unroll
         for (int j = 0; j < SEGS; ++j)
 #pragma unroll
@@ -588,15 +692,15 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Codes {inner, rows, groups} (2-D without groups) in boxes of 128 x 128
-// bytes, 128-byte swizzle, zero outside.
-bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups) {
+// Codes {inner, rows, groups} (2-D without groups) in boxes of 128
+// bytes x 128 rows, 128-byte swizzle, zero outside.
+bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups, uint32_t box_rows = 128) {
   EncodeFn enc = encode_fn();
   if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15u) || inner % 16) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(groups > 0 ? groups : 1)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(inner * rows)};
-  cuuint32_t box[3] = {128, 128, 1};
+  cuuint32_t box[3] = {128, box_rows, 1};
   cuuint32_t one[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -649,7 +753,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   Fp8Params p{};
   for (int s = 0; s < a.sources; ++s) {
-    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0)) return cudaErrorInvalidValue;
+    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0) || !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 32))
+      return cudaErrorInvalidValue;
     p.a_scale[s] = a.a_scale[s];
   }
   for (int s = 0; s < (a.dual ? 2 : a.sources); ++s) {

@@ -1254,10 +1254,10 @@ moe_status_t moe_grouped_gemm_fp8(int64_t n_groups, int64_t rows, int64_t n, int
   MOE_TRY(moe_grouped_gemm_fp8_workspace_size(n_groups, rows, n, k, &need));
   if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (n % 16 || k % 16 || n > (int64_t{1} << 29) || k > (int64_t{1} << 29) || rows >= (int64_t{1} << 31) - 256 ||
-      a_scale_ld < (k + 127) / 128 || (b_mn != 0 && b_mn != 1))
+      a_scale_ld < (k + 127) / 128 || a_scale_ld % 4 || (b_mn != 0 && b_mn != 1))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!all16({a, b, out}) || !a_scale || !b_scale || !offsets) return MOE_ERR_INVALID_ARG;
+  if (!all16({a, a_scale, b, out}) || !b_scale || !offsets) return MOE_ERR_INVALID_ARG;
   moe::Fp8GemmArgs g;
   g.b_mn = b_mn != 0;
   g.a[0] = static_cast<const uint8_t*>(a);

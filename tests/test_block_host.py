@@ -50,7 +50,7 @@ def test_grouped_gemm_refusals(lib):
     def call(g=4, rows=8, n=64, k=128, a=P, sa=P, ld=4, off=P, b=P, sb=P, mn=0, out=P, ws=P, wsb=1 << 20):
         return lib.moe_grouped_gemm_fp8(g, rows, n, k, a, sa, ld, off, b, sb, mn, out, ws, wsb, None)
     for bad in (dict(g=0), dict(g=1025), dict(rows=-1), dict(n=0), dict(k=0), dict(n=72), dict(k=72),
-                dict(ld=0), dict(k=144, ld=1), dict(mn=2), dict(a=None), dict(a=P + 8), dict(b=P + 4),
+                dict(ld=0), dict(k=144, ld=1), dict(ld=5), dict(sa=P + 8), dict(mn=2), dict(a=None), dict(a=P + 8), dict(b=P + 4),
                 dict(out=P + 2), dict(sa=None), dict(sb=None), dict(off=None), dict(rows=1 << 31),
                 dict(n=1 << 30), dict(k=1 << 30)):
         assert call(**bad) == INVALID, bad
