@@ -5,9 +5,8 @@
 // them: each k-block of 128 gives an unscaled fp32 partial product in tensor
 // memory (four K = 32 MMAs, kind::f8f6f4), and the epilogue warps add
 // a_scale * b_scale times it to fp32 accumulators they keep in registers.
-// Partial products alternate between the buffers that the 512 columns of
-// tensor memory hold, so the MMAs of one k-block run while the previous one is
-// being added.
+// The partial products rotate through four buffers in tensor memory, so the
+// MMAs run while earlier ones are being added.
 #include "fp8_block.cuh"
 #include "grouped_gemm.cuh"
 #include "sm100_ptx.cuh"
@@ -16,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <mutex>
 
 namespace moe {
@@ -149,42 +149,77 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 }
 
 // -------------------------------------------------------------------- GEMM
-constexpr int BM = 128;
+// Roles (640 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer,
+// warps 2-3 scale products, warps 4-19 epilogue (warp w reads tensor-memory
+// lanes 32 (w % 4) .. + 31, a quarter of the columns each).  A CTA's tile is 128
+// rows x 128 columns, so a thread accumulates 32 numbers and four partial products fit
+// tensor memory: the sixteen warps work on different k-blocks at once, which
+// hides the latency of the tensor-memory loads.  (128 x 256 tiles on eight warps
+// with 128 accumulators a thread, two partial products: 8192 x 4096 x 14336
+// rows x columns x contraction took 460 us, the MMAs and loads alone 362.)
+//
+// CTA pair (PAIR): two CTAs share a 256 x 128 tile, M = 256, each with its own
+// 128 rows of A and half of B's columns: 24 KB a k-block per SM instead of 32.
+// Rank 0 issues the MMAs; both CTAs' loads complete on its barriers and its
+// commits arrive on both CTAs'.
+//
+// GEMM1 (SwiGLU): a unit of work is 128 columns of h, in two sub-tiles of 64
+// columns of w1 next to the same 64 of w3; the first half of h waits in
+// registers, since the block's scale needs all 128 columns.
+constexpr int BM = 128, BN = 128;
 constexpr int BK = 128;              // contraction elements (bytes) of a k-block
-constexpr int kAuxThreads = 128;     // producer, MMA issuer, two scale warps
-constexpr int kEpiWarps = 8;
+constexpr int kAuxThreads = 128;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = kAuxThreads + kEpiWarps * 32;
-// A block launches with 384 x 168 = 64512 registers; the split hands 112 of
-// them a thread from the first warpgroup to the two that accumulate:
-// 128 x 56 + 256 x 224 = 64512.
-constexpr int kAuxRegs = 56, kEpiRegs = 224;
+// A block launches with 640 x 96 = 61440 registers; the split hands 32 of them a
+// thread from the first warpgroup to the other four: 128 x 64 + 512 x 104 = 61440.
+constexpr int kAuxRegs = 64, kEpiRegs = 104;
 constexpr int kMaxGroups = 1024;
-constexpr int kTileBytes = BM * BK;  // 128 rows of A or 128 columns of B of a stage
+constexpr int kABytes = BM * BK;     // A of a stage
+constexpr int kBufs = 4;             // partial products in tensor memory
 
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool b_mn) {
   // D format fp32 (bits 4-5 = 1), A and B E4M3 (7-9, 10-12 = 0), B major (16), N >> 3 (17-22), M >> 4 (24-28)
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// MN-major operand of 64 columns (64-byte rows, 64-byte swizzle: layout 4): 8-row
+// groups 512 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw64_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 4ull << 61;
+  return d;
 }
 
 // acc += s * v.  Volatile, which keeps it behind the wait for the tensor-memory
 // load whose register it reads; naming the registers in the wait costs a copy
-// of each.  (Two products in one instruction need their pair copied together,
+// of each.  (Two products in one instruction need a copy to make their pair,
 // so they are no fewer instructions.)
 __device__ __forceinline__ void fma_after_wait(float& acc, float s, uint32_t v) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(s), "f"(__uint_as_float(v)));
 }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[16]) { tmem_ld_32x32b_x16(addr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(addr, v); }
 
 // mbar_wait_bounded for a whole warp, with the same answer in every lane and
 // little code: the limit and the abort flag are looked at now and then.
@@ -224,10 +259,9 @@ struct Fp8Params {
   int32_t groups;
   int32_t rows;
   int32_t n;
-  int32_t ntiles;      // column tiles
+  int32_t ntiles;      // 128-column tiles of the output, and of a weight matrix's N
   int32_t kb;          // k-blocks of one source
   int32_t sources;
-  int32_t n128;        // 128-column tiles of a weight matrix's N
   void* out0;
   void* out1;
   void* out2;
@@ -239,14 +273,14 @@ struct Fp8Params {
   int32_t* status;
 };
 
-template <int BN>
+template <bool PAIR>
 struct Cfg {
-  static constexpr int kStageBytes = kTileBytes + BN * BK;
+  static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * BK;
+  static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;
-  static constexpr int kBufs = 512 / BN;                  // partial products in tensor memory
-  static constexpr int kEpiOff = kStages * kStageBytes;   // 2 KB of output staging a warp
-  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 2048;   // row maxima [2][2][128]
-  static constexpr int kScaleOff = kMaxOff + 2048;             // scale products [2][4 k-blocks][2][128]
+  static constexpr int kEpiOff = kStages * kStageBytes;        // 1 KB of output staging a warp
+  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 1024;   // row maxima [2][4][128]
+  static constexpr int kScaleOff = kMaxOff + 4096;             // scale products [2][4 k-blocks][2][128]
   static constexpr int kBarOff = kScaleOff + 8192;
   static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 4 + 1;
   static constexpr int kMiscOff = kBarOff + kBars * 8;
@@ -256,7 +290,7 @@ struct Cfg {
 };
 
 struct Tile {
-  int g, nt, row0, valid;
+  int g, nt, row0, valid;   // valid: rows of this CTA's 128 (at most 0 where a pair's second half is empty)
 };
 
 // An offset cut to the rows there are, so that no tile reaches outside them.
@@ -264,7 +298,9 @@ __device__ __forceinline__ int cut_offset(const Fp8Params& p, int i) {
   return min(max(__ldg(p.offsets + i), 0), p.rows);
 }
 
-__device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const int* s_pre) {
+template <bool PAIR>
+__device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const int* s_pre, int rank) {
+  constexpr int UR = PAIR ? 2 * BM : BM;
   int lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -272,64 +308,61 @@ __device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const in
   }
   // M tiles innermost: the CTAs that run at once share an expert's weight blocks
   const int first = cut_offset(p, lo), last = cut_offset(p, lo + 1);
-  const int mtiles = (last - first + BM - 1) / BM;
+  const int mtiles = (last - first + UR - 1) / UR;
   const int rem = tile - s_pre[lo];
   Tile t;
   t.g = lo;
   t.nt = rem / mtiles;
-  t.row0 = first + (rem - t.nt * mtiles) * BM;
+  t.row0 = first + (rem - t.nt * mtiles) * UR + rank * BM;
   t.valid = min(BM, last - t.row0);
   return t;
 }
 
-// One 32-row x 64-byte box of a warp: lane l holds row l in w[0..15]; written
-// to global memory as whole 64-byte row segments through 2 KB of shared memory.
-// dst: row 0 of the box; chunks: 16-byte chunks inside the output's columns.
-__device__ __forceinline__ void store_box(uint32_t stg, int lane, const uint32_t (&w)[16], uint8_t* dst,
-                                          int64_t ld_bytes, int rows, int chunks) {
-  __syncwarp();
+// Sixteen 32-bit words of each lane's row (64 bytes) written to global memory
+// as 32-byte row segments, through 1 KB of shared memory, half at a time.
+// dst: row 0 of the warp's 32; chunks: 16-byte chunks inside the output's columns.
+__device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint32_t (&w)[16], uint8_t* dst,
+                                             int64_t ld_bytes, int rows, int chunks) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
-                 w[4 * j + 3]);
-  __syncwarp();
-  const int c = lane & 3;
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    uint4 v;
-    ld_shared_v4(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
-    if (r < rows && c < chunks) *reinterpret_cast<uint4*>(dst + r * ld_bytes + c * 16) = v;
+    for (int j = 0; j < 2; ++j)   // chunk j of row l at j ^ ((l >> 2) & 1): four rows span the banks
+      st_shared_v4(stg + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4), w[8 * h + 4 * j], w[8 * h + 4 * j + 1],
+                   w[8 * h + 4 * j + 2], w[8 * h + 4 * j + 3]);
+    __syncwarp();
+    const int c = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + (lane >> 1);
+      uint4 v;
+      ld_shared_v4(stg + r * 32 + ((c ^ ((r >> 2) & 1)) << 4), v.x, v.y, v.z, v.w);
+      if (r < rows && 2 * h + c < chunks) *reinterpret_cast<uint4*>(dst + r * ld_bytes + (2 * h + c) * 16) = v;
+    }
   }
 }
-// 32 fp32 columns of each lane's row as bf16.
-template <class F>
-__device__ __forceinline__ void store_bf16_32(uint32_t stg, int lane, F&& value, void* out, int64_t ld, int64_t row,
-                                              int col, int n, int rows) {
-  if (col >= n) return;
-  uint32_t w[16];
+// Sixteen numbers of this lane's row as bf16, 32 bytes.
+__device__ __forceinline__ void store_bf16_16(const float* f, __nv_bfloat16* dst) {
+  uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = bf2(value(2 * j), value(2 * j + 1));
-  store_box(stg, lane, w, reinterpret_cast<uint8_t*>(out) + (row * ld + col) * 2, ld * 2, rows, (n - col) / 8);
+  for (int j = 0; j < 8; ++j) w[j] = bf2(f[2 * j], f[2 * j + 1]);
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-template <int BN, bool B_MN, int EPI>
+template <bool B_MN, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
-  using C = Cfg<BN>;
-  constexpr int S = C::kStages, NBUF = C::kBufs;
+  using C = Cfg<PAIR>;
+  constexpr int S = C::kStages;
   constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
-#ifndef CHV
-#define CHV 32
-#endif
-  constexpr int CH = CHV;
-  constexpr int SEGS = BN / 128;      // 64-column segments an epilogue warp accumulates
+  constexpr int SUBS = DUAL ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
-  uint64_t* tempty = tfull + NBUF;
-  uint64_t* xbar = tempty + NBUF;     // the two warps of a lane quarter exchanging row maxima
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* xbar = tempty + kBufs;    // the four warps of a lane quarter exchanging row maxima
   uint64_t* sfull = xbar + 4;         // scale products of four k-blocks written
   uint64_t* sempty = sfull + 2;
   uint64_t* mma_done = sempty + 2;
@@ -338,21 +371,23 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   int* s_pre = reinterpret_cast<int*>(smem + C::kTabOff);
   float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
 
-  // the same in every lane, which lets tensor-memory and barrier addresses stay in uniform registers
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int G = p.groups;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit0 = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int ustride = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < NBUF; ++b) {
+    for (int b = 0; b < kBufs; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kEpiWarps);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], 2);
+    for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], 4);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sfull[b], 2);
       mbar_init(&sempty[b], kEpiWarps);
@@ -364,13 +399,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     tma_prefetch_desc(&p.tmB[0]);
   }
   if (warp == 1) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(s_tmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    }
   }
   for (int i = threadIdx.x; i <= G; i += kThreads)
     if (cut_offset(p, i) != __ldg(p.offsets + i) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
   if (warp == 0) {
-    auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + BM - 1) / BM * p.ntiles; };
+    constexpr int UR = PAIR ? 2 * BM : BM;
+    auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + UR - 1) / UR * p.ntiles; };
     const int per = (G + 31) / 32;
     const int lo = min(G, lane * per), hi = min(G, lo + per);
     int sum = 0;
@@ -390,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();   // the peer's barriers are initialised and its tensor memory allocated
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
   const int total = s_pre[G];
@@ -401,105 +443,124 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       // ---------------------------------------------------------- producer
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = find_tile(tile, p, s_pre);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % S;
-          if (!mbar_wait_bounded(&empty[s], ((it / S) & 1u) ^ 1u, s_abort, p.status, 800 + s)) { ok = false; break; }
-          uint8_t* sA = smem + s * C::kStageBytes;
-          uint8_t* sB = sA + kTileBytes;
-          const int src = kb < p.kb ? 0 : 1;
-          const int k0 = (kb - src * p.kb) * BK;
-          // a tile of at most 32 rows loads no others: what the rest of its stage
-          // holds reaches accumulator rows that nothing reads
-          const bool few = t.valid <= 32;
-          mbar_arrive_expect_tx(&full[s], few ? C::kStageBytes - kTileBytes * 3 / 4 : C::kStageBytes);
-          tma_load_2d(sA, few ? &p.tmA32[src] : &p.tmA[src], &full[s], k0, t.row0);
-#pragma unroll
-          for (int a = 0; a < BN / 128; ++a) {
-            const CUtensorMap* m = &p.tmB[DUAL ? a : src];
-            const int n0 = DUAL ? t.nt * 128 : t.nt * BN + a * 128;
-            if (B_MN) tma_load_3d(sB + a * kTileBytes, m, &full[s], n0, k0, t.g);
-            else tma_load_3d(sB + a * kTileBytes, m, &full[s], k0, n0, t.g);
+      for (int tile = unit0; ok && tile < total; tile += ustride) {
+        const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
+        // a tile of at most 32 rows loads no others: what the rest of its stage
+        // holds reaches accumulator rows that nothing reads
+        const bool few = !PAIR && t.valid <= 32;
+        for (int sub = 0; ok && sub < SUBS; ++sub) {
+          for (int kb = 0; kb < nkb; ++kb, ++it) {
+            const int s = it % S;
+            if (!mbar_wait_bounded(&empty[s], ((it / S) & 1u) ^ 1u, s_abort, p.status, 800 + s)) { ok = false; break; }
+            uint8_t* sA = smem + s * C::kStageBytes;
+            uint8_t* sB = sA + kABytes;
+            const int src = kb < p.kb ? 0 : 1;
+            const int k0 = (kb - src * p.kb) * BK;
+            const int n0 = t.nt * 128;
+            if (PAIR) {
+              // both CTAs' loads complete on rank 0's barrier, which rank 0 arms
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+              const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+              tma_load_2d_pair(sA, &p.tmA[src], bar, k0, t.row0);
+              if (DUAL) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, n0 + sub * 64, t.g);
+              else if (B_MN) tma_load_3d_pair(sB, &p.tmB[src], bar, n0 + rank * 64, k0, t.g);
+              else tma_load_3d_pair(sB, &p.tmB[src], bar, k0, n0 + rank * 64, t.g);
+            } else {
+              mbar_arrive_expect_tx(&full[s], few ? C::kStageBytes - kABytes * 3 / 4 : C::kStageBytes);
+              tma_load_2d(sA, few ? &p.tmA32[src] : &p.tmA[src], &full[s], k0, t.row0);
+              if (B_MN) {
+                tma_load_3d(sB, &p.tmB[src], &full[s], n0, k0, t.g);
+              } else if (DUAL) {
+                tma_load_3d(sB, &p.tmB[0], &full[s], k0, n0 + sub * 64, t.g);
+                tma_load_3d(sB + 8192, &p.tmB[1], &full[s], k0, n0 + sub * 64, t.g);
+              } else {
+                tma_load_3d(sB, &p.tmB[src], &full[s], k0, n0, t.g);
+                tma_load_3d(sB + 8192, &p.tmB[src], &full[s], k0, n0 + 64, t.g);
+              }
+            }
           }
         }
       }
-      // no copy may still be landing when the CTA exits
-      for (int s = 0; s < S; ++s) {
+      // no copy may still be landing when the CTA exits (rank 0's barriers count both CTAs' copies)
+      for (int s = 0; s < S && rank == 0; ++s) {
         if (it > static_cast<uint32_t>(s)) {
           const uint32_t last = s + S * ((it - 1 - s) / S);
           mbar_wait_drain(&full[s], (last / S) & 1u);
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
       // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN, B_MN);
+      constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN, B_MN);
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % S, buf = it % NBUF;
-          if (!mbar_wait_bounded(&tempty[buf], ((it / NBUF) & 1u) ^ 1u, s_abort, p.status, 820 + buf) ||
+      for (int tile = unit0; ok && tile < total; tile += ustride) {
+        for (int kb = 0; kb < nkb * SUBS; ++kb, ++it) {
+          const int s = it % S, buf = it % kBufs;
+          if (!mbar_wait_bounded(&tempty[buf], ((it / kBufs) & 1u) ^ 1u, s_abort, p.status, 820 + buf) ||
               !mbar_wait_bounded(&full[s], (it / S) & 1u, s_abort, p.status, 840 + s)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t a_base = smem_u32(smem + s * C::kStageBytes);
-          const uint32_t b_base = a_base + kTileBytes;
+          const uint32_t b_base = a_base + kABytes;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: 128 columns a row of
-            // 128 bytes, 32 rows on, the next 128 columns a whole region further
+            // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: rows of 128
+            // (pair: 64) columns, 32 rows on
             const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 4096, kTileBytes, 1024)
-                                     : smem_desc_sw128(b_base + kk * 32, 16, 1024);
-            tc_mma_e4m3(tmem_base + buf * BN, ad, bd, idesc, kk > 0 ? 1u : 0u);
+            const uint64_t bd = !B_MN ? smem_desc_sw128(b_base + kk * 32, 16, 1024)
+                                : PAIR ? smem_desc_sw64_mn(b_base + kk * 2048)
+                                       : smem_desc_sw128(b_base + kk * 4096, 16384, 1024);
+            tc_mma_e4m3<PAIR>(tmem_base + buf * BN, ad, bd, idesc, kk > 0 ? 1u : 0u);
           }
-          tc_commit(&empty[s]);
-          tc_commit(&tfull[buf]);
+          if (PAIR) {
+            tc_commit_pair_mc(&empty[s], 3);
+            tc_commit_pair_mc(&tfull[buf], 3);
+          } else {
+            tc_commit(&empty[s]);
+            tc_commit(&tfull[buf]);
+          }
         }
       }
-      tc_commit(mma_done);   // every MMA has completed before tensor memory is released
+      // every MMA has completed before tensor memory is released
+      if (PAIR) tc_commit_pair_mc(mma_done, 1);
+      else tc_commit(mma_done);
       mbar_wait_drain(mma_done, 0);
     } else if (warp >= 2) {
       // -------------------------------------------------------- scales
       // The products a_scale[r, k-block] * b_scale[n / 128, k-block] of a tile's
-      // rows and its two 128-column blocks, four k-blocks at a time, up to eight
-      // ahead of the epilogue, which then reads one number per row.
+      // rows (two for w1 and w3), four k-blocks at a time, up to eight ahead of
+      // the epilogue, which then reads one number per row.
       const int at = static_cast<int>(threadIdx.x) - 64;    // rows at and at + 64
-      const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
-      const int64_t bstep = B_MN ? p.n128 : 1;
+      const int64_t wtiles = static_cast<int64_t>(p.ntiles) * p.kb;
+      const int64_t bstep = B_MN ? p.ntiles : 1;
       uint32_t gi = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = find_tile(tile, p, s_pre);
-        int64_t boff[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int nb = DUAL ? t.nt : min(t.nt * (BN / 128) + (BN > 128 ? j : 0), p.n128 - 1);
-          boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
-        }
-        for (int src = 0; ok && src < p.sources; ++src) {
+      for (int tile = unit0; ok && tile < total; tile += ustride) {
+        const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
+        const int64_t boff = t.g * wtiles + (B_MN ? t.nt : static_cast<int64_t>(t.nt) * p.kb);
+        for (int ss = 0; ok && ss < SUBS * p.sources; ++ss) {
+          const int src = DUAL ? 0 : ss;
           for (int k4 = 0; k4 < p.kb; k4 += 4, ++gi) {
             float4 a[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               a[h] = __ldg(reinterpret_cast<const float4*>(
                   p.a_scale[src] + static_cast<int64_t>(min(t.row0 + at + 64 * h, p.rows - 1)) * p.a_scale_ld + k4));
-            float b[2][4];
+            float b[SUBS][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < SUBS; ++j)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff[j] + min(k4 + u, p.kb - 1) * bstep);
+                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff + min(k4 + u, p.kb - 1) * bstep);
             ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
             if (!ok) break;
             float* dst = s_scale + (gi & 1u) * 1024 + at;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < SUBS; ++j) {
                 dst[j * 128 + h * 64] = a[h].x * b[j][0];
                 dst[256 + j * 128 + h * 64] = a[h].y * b[j][1];
                 dst[512 + j * 128 + h * 64] = a[h].z * b[j][2];
@@ -517,138 +578,103 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // -------------------------------------------------------------- epilogue
     const int ew = warp - kAuxThreads / 32;
     const int q = warp & 3;           // lane quarter of tensor memory this warp may read
-    const int hf = ew >> 2;           // column half
-    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 2048);
+    const int cg = ew >> 2;           // column quarter
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cg * (DUAL ? 16 : 32);
+    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 1024);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
-    // column of the tile at which segment j starts
-    auto seg_col = [&](int j) { return DUAL ? j * 128 + hf * 64 : hf * (BN / 2) + j * 64; };
+    const uint32_t tempty_addr = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
+    const int r = q * 32 + lane;
     // this warp has read a partial product
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_remote(tempty_addr + buf * 8);
+        else mbar_arrive(&tempty[buf]);
+      }
     };
     uint32_t it = 0, gi = 0, tcount = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++tcount) {
-      const Tile t = find_tile(tile, p, s_pre);
-      const int r = q * 32 + lane;
-      const bool mine = q * 32 < t.valid;    // whether this warp has rows of the tile
-      float acc[SEGS][64];
+    for (int tile = unit0; ok && tile < total; tile += ustride, ++tcount) {
+      const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
+      const bool mine = q * 32 < t.valid;   // whether this warp has rows of the tile
+      const int rows = t.valid - q * 32;
+      const int64_t row = t.row0 + q * 32;
+      float h0[DUAL ? 16 : 1];              // the first 64 columns' part of h
 #pragma unroll
-      for (int j = 0; j < SEGS; ++j)
+      for (int sub = 0; sub < SUBS; ++sub) {
+        float acc[32];                      // DUAL: 16 columns of a1, the same 16 of a3
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[j][i] = 0.0f;
-      for (int src = 0; ok && src < p.sources; ++src) {
-        for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
-          ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
-          const float* ps = s_scale + (gi & 1u) * 1024 + r;
+        for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
+        for (int src = 0; ok && src < p.sources; ++src) {
+          for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
+            ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
+            const float* ps = s_scale + (gi & 1u) * 1024 + r;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (ok && k4 + u < p.kb) {
-              float sc[SEGS];
-#pragma unroll
-              for (int j = 0; j < SEGS; ++j) sc[j] = ps[u * 256 + (DUAL ? j : BN > 128 ? hf : 0) * 128];
-              const int buf = it % NBUF;
-              ok = warp_wait(&tfull[buf], (it / NBUF) & 1u, s_abort, p.status, 860);
-              if (ok) {
-                if (mine) {
+            for (int u = 0; u < 4; ++u) {
+              if (ok && k4 + u < p.kb) {
+                const float sa = ps[u * 256], sb = DUAL ? ps[u * 256 + 128] : sa;
+                const int buf = it % kBufs;
+                ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
+                if (ok && mine) {
                   tc_fence_after();
-                  const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
-                  uint32_t v[2][CH];
-                  tmem_ld(tb + seg_col(0), v[0]);
-                  constexpr int PS = 64 / CH;   // loads of a segment
-#pragma unroll
-                  for (int c = 0; c < PS * SEGS; ++c) {
+                  if (DUAL) {
+                    uint32_t v[16], w[16];
+                    tmem_ld_32x32b_x16(lane_base + buf * BN, v);
+                    tmem_ld_32x32b_x16(lane_base + buf * BN + 64, w);
                     tmem_wait_ld();
-                    if (c + 1 < PS * SEGS)
-                      tmem_ld(tb + seg_col((c + 1) / PS) + ((c + 1) % PS) * CH, v[(c + 1) & 1]);
-                    else
-                      release(buf);
+                    release(buf);
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) fma_after_wait(acc[c / PS][(c % PS) * CH + i], sc[c / PS], v[c & 1][i]);
+                    for (int i = 0; i < 16; ++i) {
+                      fma_after_wait(acc[i], sa, v[i]);
+                      fma_after_wait(acc[16 + i], sb, w[i]);
+                    }
+                  } else {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(lane_base + buf * BN, v);
+                    tmem_wait_ld();
+                    release(buf);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) fma_after_wait(acc[i], sa, v[i]);
                   }
-                } else {
+                } else if (ok) {
                   release(buf);
                 }
                 ++it;
               }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
         }
-      }
-      if (!ok) break;
-
-      const int rows = t.valid - q * 32;    // valid rows of this warp's box
-      const int64_t row = t.row0 + q * 32;
-      if constexpr (EPI == FP8_EPI_BF16) {
-#pragma unroll
-        for (int j = 0; j < SEGS; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            store_bf16_32(stg, lane, [&](int i) { return acc[j][c * 32 + i]; }, p.out0, p.n, row,
-                          t.nt * BN + seg_col(j) + c * 32, p.n, rows);
-      } else if constexpr (EPI == FP8_EPI_SWIGLU_FWD) {
-        const int f0 = t.nt * 128 + hf * 64;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (p.out1)
-            store_bf16_32(stg, lane, [&](int i) { return acc[0][c * 32 + i]; }, p.out1, p.n, row, f0 + c * 32, p.n, rows);
-          if (p.out2)
-            store_bf16_32(stg, lane, [&](int i) { return acc[1][c * 32 + i]; }, p.out2, p.n, row, f0 + c * 32, p.n, rows);
-        }
-        // columns past F hold zero (their weights are read as zero)
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const float a = acc[0][i];
-          acc[0][i] = a / (1.0f + __expf(-a)) * acc[1][i];
-          m = fmaxf(m, fabsf(acc[0][i]));
-        }
-        if (p.out3) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            store_bf16_32(stg, lane, [&](int i) { return acc[0][c * 32 + i]; }, p.out3, p.n, row, f0 + c * 32, p.n, rows);
-        }
-        // the other column half's maximum of the same rows; two buffers, since a
-        // warp is at most one exchange ahead of its partner
-        float* mx = s_max + (tcount & 1u) * 256;
-        mx[hf * 128 + r] = m;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&xbar[q]);
-        ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
         if (!ok) break;
-        const BlockScale b = block_scale(fmaxf(m, mx[(hf ^ 1) * 128 + r]));
-        if (hf == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
-        uint32_t w[16];
+
+        if constexpr (EPI == FP8_EPI_BF16) {
+          const int col = t.nt * BN + cg * 32;
+          if (mine && col < p.n) {
+            uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = fp8_encode4(acc[0][4 * i], acc[0][4 * i + 1], acc[0][4 * i + 2], acc[0][4 * i + 3], b);
-        if (f0 < p.n)
-          store_box(stg, lane, w, reinterpret_cast<uint8_t*>(p.out0) + row * p.n + f0, p.n, rows, (p.n - f0) / 16);
-      } else {
-        // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1)
-        const int64_t base = static_cast<int64_t>(min(t.row0 + r, p.rows - 1)) * p.n;
-#pragma unroll
-        for (int j = 0; j < SEGS; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = t.nt * BN + seg_col(j) + c * 32;
-            if (col >= p.n) continue;      // n is a multiple of 64: a box is inside or outside
+            for (int j = 0; j < 16; ++j) w[j] = bf2(acc[2 * j], acc[2 * j + 1]);
+            store_rows64(stg, lane, w, static_cast<uint8_t*>(p.out0) + (row * p.n + col) * 2,
+                         static_cast<int64_t>(p.n) * 2, rows, (p.n - col) / 8);
+          }
+        } else if constexpr (EPI == FP8_EPI_SWIGLU_BWD) {
+          // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1); n is a multiple of 64
+          const int col = t.nt * BN + cg * 32;
+          if (mine && col < p.n) {
+            const int64_t base = static_cast<int64_t>(min(t.row0 + r, p.rows - 1)) * p.n + col;
             uint32_t w1[16], w3[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in0) + base + col) + i);
-              const uint4 x3 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in1) + base + col) + i);
+              const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in0) + base) + i);
+              const uint4 x3 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in1) + base) + i);
               const uint32_t u1[4] = {x1.x, x1.y, x1.z, x1.w}, u3[4] = {x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float d1[2], d3[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                  const float dh = acc[j][c * 32 + i * 8 + e * 2 + z];
+                  const float dh = acc[i * 8 + e * 2 + z];
                   const float a = z ? hi16(u1[e]) : lo16(u1[e]);
                   const float b = z ? hi16(u3[e]) : lo16(u3[e]);
                   const float sg = 1.0f / (1.0f + __expf(-a));
@@ -659,18 +685,65 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 w3[i * 4 + e] = bf2(d3[0], d3[1]);
               }
             }
-            store_box(stg, lane, w1, static_cast<uint8_t*>(p.out0) + (row * p.n + col) * 2, p.n * 2, rows, 4);
-            store_box(stg, lane, w3, static_cast<uint8_t*>(p.out1) + (row * p.n + col) * 2, p.n * 2, rows, 4);
+            const int64_t off = (row * p.n + col) * 2;
+            store_rows64(stg, lane, w1, static_cast<uint8_t*>(p.out0) + off, static_cast<int64_t>(p.n) * 2, rows, 4);
+            store_rows64(stg, lane, w3, static_cast<uint8_t*>(p.out1) + off, static_cast<int64_t>(p.n) * 2, rows, 4);
           }
+        } else {
+          // columns past F hold zero (their weights are read as zero)
+          const int f = t.nt * 128 + sub * 64 + cg * 16;
+          const bool inside = r < t.valid && f < p.n;
+          const int64_t off = (row + lane) * p.n + f;
+          if (p.out1 && inside) store_bf16_16(acc, static_cast<__nv_bfloat16*>(p.out1) + off);
+          if (p.out2 && inside) store_bf16_16(acc + 16, static_cast<__nv_bfloat16*>(p.out2) + off);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i] = acc[i] / (1.0f + __expf(-acc[i])) * acc[16 + i];
+          if (p.out3 && inside) store_bf16_16(acc, static_cast<__nv_bfloat16*>(p.out3) + off);
+          if (sub == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h0[i] = acc[i];
+          } else {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, fmaxf(fabsf(h0[i]), fabsf(acc[i])));
+            // the other column quarters' maxima of the same rows; two buffers, since
+            // a warp is at most one exchange ahead of the others
+            float* mx = s_max + (tcount & 1u) * 512 + r;
+            mx[cg * 128] = m;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&xbar[q]);
+            ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
+            if (!ok) break;
+            m = fmaxf(fmaxf(mx[0], mx[128]), fmaxf(mx[256], mx[384]));
+            const BlockScale b = block_scale(m);
+            if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
+            uint8_t* dst = static_cast<uint8_t*>(p.out0) + off - 64;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = half ? fp8_encode4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3], b)
+                            : fp8_encode4(h0[4 * i], h0[4 * i + 1], h0[4 * i + 2], h0[4 * i + 3], b);
+              if (r < t.valid && f - 64 + 64 * half < p.n)
+                *reinterpret_cast<uint4*>(dst + 64 * half) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
       }
+      if (!ok) break;
     }
     __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();   // rank 0's MMAs into the peer's tensor memory and all arrivals across are done
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, 512);
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tmem_base, 512);
+    else tmem_dealloc(tmem_base, 512);
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -692,34 +765,61 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Codes {inner, rows, groups} (2-D without groups) in boxes of 128
-// bytes x 128 rows, 128-byte swizzle, zero outside.
-bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups, uint32_t box_rows = 128) {
+// Codes {inner, rows, groups} (2-D without groups) in boxes of box_cols (64 or
+// 128) bytes x box_rows, swizzled over the box's row length, zero outside.
+bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups, uint32_t box_cols,
+              uint32_t box_rows) {
   EncodeFn enc = encode_fn();
   if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15u) || inner % 16) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(groups > 0 ? groups : 1)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(inner * rows)};
-  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t one[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool B_MN, int EPI>
-cudaError_t launch_form(const Fp8Params& p, int64_t tiles, cudaStream_t st) {
-  auto kern = fp8_gemm_kernel<BN, B_MN, EPI>;
+template <bool B_MN, int EPI, bool PAIR>
+cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
+  using C = Cfg<PAIR>;
+  auto kern = fp8_gemm_kernel<B_MN, EPI, PAIR>;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = PAIR ? 2 : 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
+  static int resident = 0;   // CTAs, or CTA pairs, that run at once
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(Cfg<BN>::smem_bytes(kMaxGroups)));
+                               static_cast<int>(C::smem_bytes(kMaxGroups)));
+    resident = PAIR ? num_sms() / 2 : num_sms();
+    if (err == cudaSuccess && PAIR) {
+      cfg.gridDim = dim3(2 * resident);
+      cfg.dynamicSmemBytes = C::smem_bytes(kMaxGroups);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) resident = n;
+      cudaGetLastError();
+    }
   });
   if (err != cudaSuccess) return err;
-  const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
-  kern<<<grid, kThreads, Cfg<BN>::smem_bytes(p.groups), st>>>(p);
-  return cudaGetLastError();
+  const int u = static_cast<int>(std::min<int64_t>(units, resident));
+  cfg.gridDim = dim3(PAIR ? 2 * u : u);
+  cfg.dynamicSmemBytes = C::smem_bytes(p.groups);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool B_MN, int EPI>
+cudaError_t launch_pick(const Fp8Params& p, bool pair, int64_t units, cudaStream_t st) {
+  return pair ? launch_form<B_MN, EPI, true>(p, units, st) : launch_form<B_MN, EPI, false>(p, units, st);
 }
 
 }  // namespace
@@ -751,14 +851,18 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.groups > kMaxGroups || a.k <= 0 || a.k % 16 || a.n % 16 || a.sources < 1 || a.sources > 2 ||
       a.rows > 0x7fffff00LL || a.n > 0x3fffffffLL || a.k > 0x3fffffffLL)
     return cudaErrorInvalidValue;
+  // A pair's tile spans 256 rows: worth it where groups fill them.
+  const char* force = std::getenv("MOE_GEMM_CTA_PAIR");
+  const bool pair = force && (force[0] == '0' || force[0] == '1') ? force[0] == '1' : a.rows >= 512LL * a.groups;
   Fp8Params p{};
   for (int s = 0; s < a.sources; ++s) {
-    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0) || !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 32))
-      return cudaErrorInvalidValue;
+    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0, 128, 128)) return cudaErrorInvalidValue;
+    if (!pair && !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 128, 32)) return cudaErrorInvalidValue;
     p.a_scale[s] = a.a_scale[s];
   }
   for (int s = 0; s < (a.dual ? 2 : a.sources); ++s) {
-    if (!(a.b_mn ? code_map(&p.tmB[s], a.b[s], a.n, a.k, a.groups) : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups)))
+    if (!(a.b_mn ? code_map(&p.tmB[s], a.b[s], a.n, a.k, a.groups, pair ? 64 : 128, 128)
+                 : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups, 128, 64)))
       return cudaErrorInvalidValue;
     p.b_scale[s] = a.b_scale[s];
   }
@@ -769,7 +873,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.n = static_cast<int32_t>(a.n);
   p.kb = static_cast<int32_t>((a.k + BK - 1) / BK);
   p.sources = a.sources;
-  p.n128 = static_cast<int32_t>((a.n + 127) / 128);
+  p.ntiles = static_cast<int32_t>((a.n + 127) / 128);
   p.out0 = a.out0;
   p.out1 = a.out1;
   p.out2 = a.out2;
@@ -779,18 +883,12 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.in0 = a.in0;
   p.in1 = a.in1;
   p.status = a.status;
-  const int64_t mt = a.rows / BM + std::min<int64_t>(a.groups, a.rows);   // most M tiles of any split into groups
-  if (a.epi == FP8_EPI_SWIGLU_FWD) {
-    p.ntiles = p.n128;
-    return launch_form<256, false, FP8_EPI_SWIGLU_FWD>(p, mt * p.ntiles, st);
-  }
-  if (a.epi == FP8_EPI_SWIGLU_BWD) {
-    p.ntiles = (p.n + 255) / 256;
-    return launch_form<256, true, FP8_EPI_SWIGLU_BWD>(p, mt * p.ntiles, st);
-  }
-  p.ntiles = (p.n + 255) / 256;
-  return a.b_mn ? launch_form<256, true, FP8_EPI_BF16>(p, mt * p.ntiles, st)
-                : launch_form<256, false, FP8_EPI_BF16>(p, mt * p.ntiles, st);
+  // most M tiles of any split of the rows into groups
+  const int64_t units = (a.rows / (pair ? 2 * BM : BM) + std::min<int64_t>(a.groups, a.rows)) * p.ntiles;
+  if (a.epi == FP8_EPI_SWIGLU_FWD) return launch_pick<false, FP8_EPI_SWIGLU_FWD>(p, pair, units, st);
+  if (a.epi == FP8_EPI_SWIGLU_BWD) return launch_pick<true, FP8_EPI_SWIGLU_BWD>(p, pair, units, st);
+  return a.b_mn ? launch_pick<true, FP8_EPI_BF16>(p, pair, units, st)
+                : launch_pick<false, FP8_EPI_BF16>(p, pair, units, st);
 }
 
 }  // namespace moe
