@@ -5,8 +5,8 @@
 // them: each k-block of 128 gives an unscaled fp32 partial product in tensor
 // memory (four K = 32 MMAs, kind::f8f6f4), and the epilogue warps add
 // a_scale * b_scale times it to fp32 accumulators they keep in registers.
-// The partial products rotate through four buffers in tensor memory, so the
-// MMAs run while earlier ones are being added.
+// The partial products take turns in the 512 columns of tensor memory, so the
+// MMAs of one k-block run while the previous one is being added.
 #include "fp8_block.cuh"
 #include "grouped_gemm.cuh"
 #include "sm100_ptx.cuh"
@@ -151,32 +151,28 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 // -------------------------------------------------------------------- GEMM
 // Roles (640 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer,
 // warps 2-3 scale products, warps 4-19 epilogue (warp w reads tensor-memory
-// lanes 32 (w % 4) .. + 31, a quarter of the columns each).  A CTA's tile is 128
-// rows x 128 columns, so a thread accumulates 32 numbers and four partial products fit
-// tensor memory: the sixteen warps work on different k-blocks at once, which
-// hides the latency of the tensor-memory loads.  (128 x 256 tiles on eight warps
-// with 128 accumulators a thread, two partial products: 8192 x 4096 x 14336
-// rows x columns x contraction took 460 us, the MMAs and loads alone 362.)
+// lanes 32 (w % 4) .. + 31 and a quarter of the columns: 64 accumulators a thread).
+// Tiles of 128 rows x BN columns per CTA, 512 / BN partial products in tensor
+// memory.  Sixteen warps, because a warp's tensor-memory loads, waits and
+// multiply-adds follow each other: four warps a scheduler cover each other's.
 //
-// CTA pair (PAIR): two CTAs share a 256 x 128 tile, M = 256, each with its own
-// 128 rows of A and half of B's columns: 24 KB a k-block per SM instead of 32.
+// CTA pair (PAIR): two CTAs share a 256 x 256 tile, M = 256, each with its own
+// 128 rows of A and half of B's columns: 32 KB a k-block per SM instead of 48.
 // Rank 0 issues the MMAs; both CTAs' loads complete on its barriers and its
 // commits arrive on both CTAs'.
 //
-// GEMM1 (SwiGLU): a unit of work is 128 columns of h, in two sub-tiles of 64
-// columns of w1 next to the same 64 of w3; the first half of h waits in
-// registers, since the block's scale needs all 128 columns.
-constexpr int BM = 128, BN = 128;
+// GEMM1 (SwiGLU): a tile holds 128 columns of w1 and the same 128 of w3, which
+// is one scale block of h.
+constexpr int BM = 128;
 constexpr int BK = 128;              // contraction elements (bytes) of a k-block
 constexpr int kAuxThreads = 128;
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = kAuxThreads + kEpiWarps * 32;
-// A block launches with 640 x 96 = 61440 registers; the split hands 32 of them a
-// thread from the first warpgroup to the other four: 128 x 64 + 512 x 104 = 61440.
-constexpr int kAuxRegs = 64, kEpiRegs = 104;
 constexpr int kMaxGroups = 1024;
 constexpr int kABytes = BM * BK;     // A of a stage
-constexpr int kBufs = 4;             // partial products in tensor memory
+// A block launches with 640 x 96 = 61440 registers; the split hands 32 of them a
+// thread from the first warpgroup to the other four: 128 x 64 + 512 x 104 = 61440.
+constexpr int kAuxRegs = 96, kEpiRegs = 96;
 
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool b_mn) {
   // D format fp32 (bits 4-5 = 1), A and B E4M3 (7-9, 10-12 = 0), B major (16), N >> 3 (17-22), M >> 4 (24-28)
@@ -201,24 +197,25 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// MN-major operand of 64 columns (64-byte rows, 64-byte swizzle: layout 4): 8-row
-// groups 512 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_sw64_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;
-  d |= static_cast<uint64_t>(512 >> 4) << 32;
-  d |= 1ull << 46;
-  d |= 4ull << 61;
-  return d;
-}
-
 // acc += s * v.  Volatile, which keeps it behind the wait for the tensor-memory
 // load whose register it reads; naming the registers in the wait costs a copy
 // of each.  (Two products in one instruction need a copy to make their pair,
 // so they are no fewer instructions.)
 __device__ __forceinline__ void fma_after_wait(float& acc, float s, uint32_t v) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(s), "f"(__uint_as_float(v)));
+}
+
+// One lane of a converged warp.  The compiler knows this form: operands of the
+// TMA and tcgen05 instructions behind it go to uniform registers at once, where a
+// `lane == 0` branch makes each a loop over the lanes (four MMAs 250 clocks).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // mbar_wait_bounded for a whole warp, with the same answer in every lane and
@@ -259,7 +256,8 @@ struct Fp8Params {
   int32_t groups;
   int32_t rows;
   int32_t n;
-  int32_t ntiles;      // 128-column tiles of the output, and of a weight matrix's N
+  int32_t ntiles;      // column tiles of the output
+  int32_t n128;        // 128-column tiles of a weight matrix's N
   int32_t kb;          // k-blocks of one source
   int32_t sources;
   void* out0;
@@ -273,8 +271,9 @@ struct Fp8Params {
   int32_t* status;
 };
 
-template <bool PAIR>
+template <int BN, bool PAIR>
 struct Cfg {
+  static constexpr int kBufs = 512 / BN;             // partial products in tensor memory
   static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;
@@ -341,21 +340,15 @@ __device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint3
     }
   }
 }
-// Sixteen numbers of this lane's row as bf16, 32 bytes.
-__device__ __forceinline__ void store_bf16_16(const float* f, __nv_bfloat16* dst) {
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = bf2(f[2 * j], f[2 * j + 1]);
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-template <bool B_MN, int EPI, bool PAIR>
+template <int BN, bool B_MN, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
-  using C = Cfg<PAIR>;
-  constexpr int S = C::kStages;
+  using C = Cfg<BN, PAIR>;
+  constexpr int S = C::kStages, kBufs = C::kBufs;
   constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
-  constexpr int SUBS = DUAL ? 2 : 1;
+  constexpr int NS = BN / 128;        // scale products a row and k-block: 128-column blocks, or w1 and w3
+  constexpr int COLS = BN / 4;        // columns of an epilogue warp
+  static_assert(!DUAL || BN == 256, "w1 and w3 halves of a 256-column tile");
+  static_assert(!PAIR || BN == 256, "pairs share 256 columns");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -439,81 +432,82 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
   if (warp < kAuxThreads / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------- producer
-      uint32_t it = 0;
+      uint32_t it = 0, s = 0, ph = 1;
       bool ok = true;
+      const uint32_t lead_full = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
       for (int tile = unit0; ok && tile < total; tile += ustride) {
         const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
         // a tile of at most 32 rows loads no others: what the rest of its stage
         // holds reaches accumulator rows that nothing reads
         const bool few = !PAIR && t.valid <= 32;
-        for (int sub = 0; ok && sub < SUBS; ++sub) {
-          for (int kb = 0; kb < nkb; ++kb, ++it) {
-            const int s = it % S;
-            if (!mbar_wait_bounded(&empty[s], ((it / S) & 1u) ^ 1u, s_abort, p.status, 800 + s)) { ok = false; break; }
+        const uint32_t bytes = few ? C::kStageBytes - kABytes * 3 / 4 : C::kStageBytes;
+        for (int src = 0; ok && src < p.sources; ++src) {
+          const CUtensorMap* ma = few ? &p.tmA32[src] : &p.tmA[src];
+          const CUtensorMap* mb = &p.tmB[DUAL && PAIR ? rank : src];
+          const int n0 = DUAL ? t.nt * 128 : t.nt * BN + (PAIR ? rank * 128 : 0);
+          for (int k0 = 0; k0 < p.kb * BK; k0 += BK, ++it) {
+            ok = warp_wait(&empty[s], ph, s_abort, p.status, 800);
+            if (!ok) break;
             uint8_t* sA = smem + s * C::kStageBytes;
             uint8_t* sB = sA + kABytes;
-            const int src = kb < p.kb ? 0 : 1;
-            const int k0 = (kb - src * p.kb) * BK;
-            const int n0 = t.nt * 128;
-            if (PAIR) {
-              // both CTAs' loads complete on rank 0's barrier, which rank 0 arms
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-              const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-              tma_load_2d_pair(sA, &p.tmA[src], bar, k0, t.row0);
-              if (DUAL) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, n0 + sub * 64, t.g);
-              else if (B_MN) tma_load_3d_pair(sB, &p.tmB[src], bar, n0 + rank * 64, k0, t.g);
-              else tma_load_3d_pair(sB, &p.tmB[src], bar, k0, n0 + rank * 64, t.g);
-            } else {
-              mbar_arrive_expect_tx(&full[s], few ? C::kStageBytes - kABytes * 3 / 4 : C::kStageBytes);
-              tma_load_2d(sA, few ? &p.tmA32[src] : &p.tmA[src], &full[s], k0, t.row0);
-              if (B_MN) {
-                tma_load_3d(sB, &p.tmB[src], &full[s], n0, k0, t.g);
-              } else if (DUAL) {
-                tma_load_3d(sB, &p.tmB[0], &full[s], k0, n0 + sub * 64, t.g);
-                tma_load_3d(sB + 8192, &p.tmB[1], &full[s], k0, n0 + sub * 64, t.g);
+            if (elect_one()) {
+              if (PAIR) {
+                // both CTAs' loads complete on rank 0's barrier, which rank 0 arms
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+                const uint32_t bar = lead_full + s * 8;
+                tma_load_2d_pair(sA, ma, bar, k0, t.row0);
+                if (B_MN) tma_load_3d_pair(sB, mb, bar, n0, k0, t.g);
+                else tma_load_3d_pair(sB, mb, bar, k0, n0, t.g);
               } else {
-                tma_load_3d(sB, &p.tmB[src], &full[s], k0, n0, t.g);
-                tma_load_3d(sB + 8192, &p.tmB[src], &full[s], k0, n0 + 64, t.g);
+                mbar_arrive_expect_tx(&full[s], bytes);
+                tma_load_2d(sA, ma, &full[s], k0, t.row0);
+                if (B_MN) {
+                  tma_load_3d(sB, mb, &full[s], n0, k0, t.g);
+                  if (BN == 256) tma_load_3d(sB + 16384, mb, &full[s], n0 + 128, k0, t.g);
+                } else {
+                  tma_load_3d(sB, mb, &full[s], k0, n0, t.g);
+                  if (DUAL) tma_load_3d(sB + 16384, &p.tmB[1], &full[s], k0, n0, t.g);
+                }
               }
+            }
+            __syncwarp();
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
             }
           }
         }
       }
       // no copy may still be landing when the CTA exits (rank 0's barriers count both CTAs' copies)
-      for (int s = 0; s < S && rank == 0; ++s) {
-        if (it > static_cast<uint32_t>(s)) {
-          const uint32_t last = s + S * ((it - 1 - s) / S);
-          mbar_wait_drain(&full[s], (last / S) & 1u);
+      for (uint32_t i = 0; i < S && rank == 0; ++i) {
+        if (it > i) {
+          const uint32_t last = i + S * ((it - 1 - i) / S);
+          mbar_wait_drain(&full[i], (last / S) & 1u);
         }
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+      __syncwarp();
+    } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN, B_MN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total; tile += ustride) {
-        for (int kb = 0; kb < nkb * SUBS; ++kb, ++it) {
-          const int s = it % S, buf = it % kBufs;
-          if (!mbar_wait_bounded(&tempty[buf], ((it / kBufs) & 1u) ^ 1u, s_abort, p.status, 820 + buf) ||
-              !mbar_wait_bounded(&full[s], (it / S) & 1u, s_abort, p.status, 840 + s)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * C::kStageBytes);
-          const uint32_t b_base = a_base + kABytes;
+      int64_t left = 0;   // k-blocks of this CTA's (pair's) tiles
+      for (int tile = unit0; tile < total; tile += ustride) left += nkb;
+      // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: 128 columns a row of
+      // 128 bytes, 32 rows on, the next 128 columns a whole region further
+      constexpr uint32_t kAdvB = (B_MN ? 4096 : 32) >> 4;
+      const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + kABytes, B_MN ? 16384 : 16, 1024);
+      uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+      for (; left > 0; --left) {
+        if (!warp_wait(&tempty[buf], bph, s_abort, p.status, 820) || !warp_wait(&full[s], ph, s_abort, p.status, 840))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ad = ad0 + s * (C::kStageBytes >> 4), bd = bd0 + s * (C::kStageBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: rows of 128
-            // (pair: 64) columns, 32 rows on
-            const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = !B_MN ? smem_desc_sw128(b_base + kk * 32, 16, 1024)
-                                : PAIR ? smem_desc_sw64_mn(b_base + kk * 2048)
-                                       : smem_desc_sw128(b_base + kk * 4096, 16384, 1024);
-            tc_mma_e4m3<PAIR>(tmem_base + buf * BN, ad, bd, idesc, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_e4m3<PAIR>(tmem_base + buf * BN, ad + kk * 2, bd + kk * kAdvB, idesc, kk > 0 ? 1u : 0u);
           if (PAIR) {
             tc_commit_pair_mc(&empty[s], 3);
             tc_commit_pair_mc(&tfull[buf], 3);
@@ -522,45 +516,60 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             tc_commit(&tfull[buf]);
           }
         }
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if (++buf == kBufs) {
+          buf = 0;
+          bph ^= 1u;
+        }
       }
       // every MMA has completed before tensor memory is released
-      if (PAIR) tc_commit_pair_mc(mma_done, 1);
-      else tc_commit(mma_done);
-      mbar_wait_drain(mma_done, 0);
+      if (elect_one()) {
+        if (PAIR) tc_commit_pair_mc(mma_done, 1);
+        else tc_commit(mma_done);
+        mbar_wait_drain(mma_done, 0);
+      }
     } else if (warp >= 2) {
       // -------------------------------------------------------- scales
       // The products a_scale[r, k-block] * b_scale[n / 128, k-block] of a tile's
-      // rows (two for w1 and w3), four k-blocks at a time, up to eight ahead of
-      // the epilogue, which then reads one number per row.
+      // rows and its 128-column blocks (or w1 and w3), four k-blocks at a time, up to
+      // eight ahead of the epilogue, which then reads one number per row and block.
       const int at = static_cast<int>(threadIdx.x) - 64;    // rows at and at + 64
-      const int64_t wtiles = static_cast<int64_t>(p.ntiles) * p.kb;
-      const int64_t bstep = B_MN ? p.ntiles : 1;
+      const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
+      const int64_t bstep = B_MN ? p.n128 : 1;
       uint32_t gi = 0;
       bool ok = true;
       for (int tile = unit0; ok && tile < total; tile += ustride) {
         const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
-        const int64_t boff = t.g * wtiles + (B_MN ? t.nt : static_cast<int64_t>(t.nt) * p.kb);
-        for (int ss = 0; ok && ss < SUBS * p.sources; ++ss) {
-          const int src = DUAL ? 0 : ss;
+        int64_t boff[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int nb = DUAL ? t.nt : min(t.nt * NS + j, p.n128 - 1);
+          boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
+        }
+        for (int src = 0; ok && src < p.sources; ++src) {
           for (int k4 = 0; k4 < p.kb; k4 += 4, ++gi) {
             float4 a[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               a[h] = __ldg(reinterpret_cast<const float4*>(
                   p.a_scale[src] + static_cast<int64_t>(min(t.row0 + at + 64 * h, p.rows - 1)) * p.a_scale_ld + k4));
-            float b[SUBS][4];
+            float b[NS][4];
 #pragma unroll
-            for (int j = 0; j < SUBS; ++j)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff + min(k4 + u, p.kb - 1) * bstep);
+                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff[j] + min(k4 + u, p.kb - 1) * bstep);
             ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
             if (!ok) break;
             float* dst = s_scale + (gi & 1u) * 1024 + at;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int j = 0; j < SUBS; ++j) {
+              for (int j = 0; j < NS; ++j) {
                 dst[j * 128 + h * 64] = a[h].x * b[j][0];
                 dst[256 + j * 128 + h * 64] = a[h].y * b[j][1];
                 dst[512 + j * 128 + h * 64] = a[h].z * b[j][2];
@@ -579,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int ew = warp - kAuxThreads / 32;
     const int q = warp & 3;           // lane quarter of tensor memory this warp may read
     const int cg = ew >> 2;           // column quarter
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cg * (DUAL ? 16 : 32);
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    // tile column of this warp's 16-column chunk c (w1 | w3: half of the chunks each)
+    auto chunk_col = [&](int c) { return DUAL ? (c >> 1) * 128 + cg * 32 + (c & 1) * 16 : cg * COLS + c * 16; };
     const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 1024);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
     const uint32_t tempty_addr = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
@@ -600,138 +611,117 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const bool mine = q * 32 < t.valid;   // whether this warp has rows of the tile
       const int rows = t.valid - q * 32;
       const int64_t row = t.row0 + q * 32;
-      float h0[DUAL ? 16 : 1];              // the first 64 columns' part of h
+      float acc[COLS];                      // DUAL: 32 columns of a1, the same 32 of a3
 #pragma unroll
-      for (int sub = 0; sub < SUBS; ++sub) {
-        float acc[32];                      // DUAL: 16 columns of a1, the same 16 of a3
+      for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+      for (int src = 0; ok && src < p.sources; ++src) {
+        for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
+          ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
+          const float* ps = s_scale + (gi & 1u) * 1024 + (DUAL || BN == 128 ? 0 : (cg >> 1) * 128) + r;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
-        for (int src = 0; ok && src < p.sources; ++src) {
-          for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
-            ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
-            const float* ps = s_scale + (gi & 1u) * 1024 + r;
+          for (int u = 0; u < 4; ++u) {
+            if (ok && k4 + u < p.kb) {
+              const float sa = ps[u * 256], sb = DUAL ? ps[u * 256 + 128] : sa;
+              const int buf = it % kBufs;
+              ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
+              if (ok && mine) {
+                tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              if (ok && k4 + u < p.kb) {
-                const float sa = ps[u * 256], sb = DUAL ? ps[u * 256 + 128] : sa;
-                const int buf = it % kBufs;
-                ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
-                if (ok && mine) {
-                  tc_fence_after();
-                  if (DUAL) {
-                    uint32_t v[16], w[16];
-                    tmem_ld_32x32b_x16(lane_base + buf * BN, v);
-                    tmem_ld_32x32b_x16(lane_base + buf * BN + 64, w);
-                    tmem_wait_ld();
-                    release(buf);
+                for (int c = 0; c < COLS / 16; ++c) {
+                  uint32_t v[16];
+                  tmem_ld_32x32b_x16(lane_base + buf * BN + chunk_col(c), v);
+                  tmem_wait_ld();
+                  if (c + 1 == COLS / 16) release(buf);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                      fma_after_wait(acc[i], sa, v[i]);
-                      fma_after_wait(acc[16 + i], sb, w[i]);
-                    }
-                  } else {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(lane_base + buf * BN, v);
-                    tmem_wait_ld();
-                    release(buf);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) fma_after_wait(acc[i], sa, v[i]);
-                  }
-                } else if (ok) {
-                  release(buf);
+                  for (int i = 0; i < 16; ++i) fma_after_wait(acc[c * 16 + i], DUAL && c >= 2 ? sb : sa, v[i]);
                 }
-                ++it;
+              } else if (ok) {
+                release(buf);
               }
+              ++it;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
         }
-        if (!ok) break;
+      }
+      if (!ok) break;
 
-        if constexpr (EPI == FP8_EPI_BF16) {
-          const int col = t.nt * BN + cg * 32;
-          if (mine && col < p.n) {
-            uint32_t w[16];
+      auto rows_bf16 = [&](const float* f, void* out, int col) {   // 32 columns of the warp's rows
+        uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = bf2(acc[2 * j], acc[2 * j + 1]);
-            store_rows64(stg, lane, w, static_cast<uint8_t*>(p.out0) + (row * p.n + col) * 2,
-                         static_cast<int64_t>(p.n) * 2, rows, (p.n - col) / 8);
-          }
-        } else if constexpr (EPI == FP8_EPI_SWIGLU_BWD) {
-          // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1); n is a multiple of 64
-          const int col = t.nt * BN + cg * 32;
+        for (int j = 0; j < 16; ++j) w[j] = bf2(f[2 * j], f[2 * j + 1]);
+        if (mine && col < p.n)
+          store_rows64(stg, lane, w, static_cast<uint8_t*>(out) + (row * p.n + col) * 2, static_cast<int64_t>(p.n) * 2,
+                       rows, (p.n - col) / 8);
+      };
+      if constexpr (EPI == FP8_EPI_BF16) {
+#pragma unroll
+        for (int c = 0; c < COLS / 32; ++c) rows_bf16(acc + 32 * c, p.out0, t.nt * BN + cg * COLS + c * 32);
+      } else if constexpr (EPI == FP8_EPI_SWIGLU_BWD) {
+        // dh -> da1 = dh a3 silu'(a1), da3 = dh silu(a1); n is a multiple of 64
+#pragma unroll
+        for (int c = 0; c < COLS / 32; ++c) {
+          const int col = t.nt * BN + cg * COLS + c * 32;
           if (mine && col < p.n) {
             const int64_t base = static_cast<int64_t>(min(t.row0 + r, p.rows - 1)) * p.n + col;
-            uint32_t w1[16], w3[16];
+            float d1[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in0) + base) + i);
               const uint4 x3 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.in1) + base) + i);
               const uint32_t u1[4] = {x1.x, x1.y, x1.z, x1.w}, u3[4] = {x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float d1[2], d3[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const float dh = acc[i * 8 + e * 2 + z];
-                  const float a = z ? hi16(u1[e]) : lo16(u1[e]);
-                  const float b = z ? hi16(u3[e]) : lo16(u3[e]);
-                  const float sg = 1.0f / (1.0f + __expf(-a));
-                  d1[z] = dh * b * sg * (1.0f + a * (1.0f - sg));
-                  d3[z] = dh * a * sg;
-                }
-                w1[i * 4 + e] = bf2(d1[0], d1[1]);
-                w3[i * 4 + e] = bf2(d3[0], d3[1]);
+              for (int e = 0; e < 8; ++e) {
+                const float dh = acc[c * 32 + i * 8 + e];
+                const float a = (e & 1) ? hi16(u1[e >> 1]) : lo16(u1[e >> 1]);
+                const float b = (e & 1) ? hi16(u3[e >> 1]) : lo16(u3[e >> 1]);
+                const float sg = 1.0f / (1.0f + __expf(-a));
+                d1[i * 8 + e] = dh * b * sg * (1.0f + a * (1.0f - sg));
+                acc[c * 32 + i * 8 + e] = dh * a * sg;
               }
             }
-            const int64_t off = (row * p.n + col) * 2;
-            store_rows64(stg, lane, w1, static_cast<uint8_t*>(p.out0) + off, static_cast<int64_t>(p.n) * 2, rows, 4);
-            store_rows64(stg, lane, w3, static_cast<uint8_t*>(p.out1) + off, static_cast<int64_t>(p.n) * 2, rows, 4);
+            rows_bf16(d1, p.out0, col);
+            rows_bf16(acc + 32 * c, p.out1, col);
           }
-        } else {
-          // columns past F hold zero (their weights are read as zero)
-          const int f = t.nt * 128 + sub * 64 + cg * 16;
-          const bool inside = r < t.valid && f < p.n;
-          const int64_t off = (row + lane) * p.n + f;
-          if (p.out1 && inside) store_bf16_16(acc, static_cast<__nv_bfloat16*>(p.out1) + off);
-          if (p.out2 && inside) store_bf16_16(acc + 16, static_cast<__nv_bfloat16*>(p.out2) + off);
+        }
+      } else {
+        // columns past F hold zero (their weights are read as zero)
+        const int f = t.nt * 128 + cg * 32;
+        if (p.out1) rows_bf16(acc, p.out1, f);
+        if (p.out2) rows_bf16(acc + 32, p.out2, f);
+        float m = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[i] = acc[i] / (1.0f + __expf(-acc[i])) * acc[16 + i];
-          if (p.out3 && inside) store_bf16_16(acc, static_cast<__nv_bfloat16*>(p.out3) + off);
-          if (sub == 0) {
+        for (int i = 0; i < 32; ++i) {
+          acc[i] = acc[i] / (1.0f + __expf(-acc[i])) * acc[32 + i];
+          m = fmaxf(m, fabsf(acc[i]));
+        }
+        if (p.out3) rows_bf16(acc, p.out3, f);
+        // the other column quarters' maxima of the same rows; two buffers, since a
+        // warp is at most one exchange ahead of the others
+        float* mx = s_max + (tcount & 1u) * 512 + r;
+        mx[cg * 128] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xbar[q]);
+        ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
+        if (!ok) break;
+        m = fmaxf(fmaxf(mx[0], mx[128]), fmaxf(mx[256], mx[384]));
+        const BlockScale b = block_scale(m);
+        if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
+        if (r < t.valid && f < p.n) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out0) + (row + lane) * p.n + f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) h0[i] = acc[i];
-          } else {
-            float m = 0.0f;
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, fmaxf(fabsf(h0[i]), fabsf(acc[i])));
-            // the other column quarters' maxima of the same rows; two buffers, since
-            // a warp is at most one exchange ahead of the others
-            float* mx = s_max + (tcount & 1u) * 512 + r;
-            mx[cg * 128] = m;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&xbar[q]);
-            ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
-            if (!ok) break;
-            m = fmaxf(fmaxf(mx[0], mx[128]), fmaxf(mx[256], mx[384]));
-            const BlockScale b = block_scale(m);
-            if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
-            uint8_t* dst = static_cast<uint8_t*>(p.out0) + off - 64;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = half ? fp8_encode4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3], b)
-                            : fp8_encode4(h0[4 * i], h0[4 * i + 1], h0[4 * i + 2], h0[4 * i + 3], b);
-              if (r < t.valid && f - 64 + 64 * half < p.n)
-                *reinterpret_cast<uint4*>(dst + 64 * half) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) {
+              const float* h = acc + half * 16 + 4 * i;
+              w[i] = fp8_encode4(h[0], h[1], h[2], h[3], b);
             }
+            dst[half] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
-      if (!ok) break;
     }
     __syncwarp();
   }
@@ -765,26 +755,25 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Codes {inner, rows, groups} (2-D without groups) in boxes of box_cols (64 or
-// 128) bytes x box_rows, swizzled over the box's row length, zero outside.
-bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups, uint32_t box_cols,
-              uint32_t box_rows) {
+// Codes {inner, rows, groups} (2-D without groups) in boxes of 128 bytes x
+// box_rows, 128-byte swizzle, zero outside.
+bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups, uint32_t box_rows) {
   EncodeFn enc = encode_fn();
   if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15u) || inner % 16) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(groups > 0 ? groups : 1)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(inner * rows)};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t box[3] = {128, box_rows, 1};
   cuuint32_t one[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool B_MN, int EPI, bool PAIR>
+template <int BN, bool B_MN, int EPI, bool PAIR>
 cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
-  using C = Cfg<PAIR>;
-  auto kern = fp8_gemm_kernel<B_MN, EPI, PAIR>;
+  using C = Cfg<BN, PAIR>;
+  auto kern = fp8_gemm_kernel<BN, B_MN, EPI, PAIR>;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -818,8 +807,11 @@ cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
 }
 
 template <bool B_MN, int EPI>
-cudaError_t launch_pick(const Fp8Params& p, bool pair, int64_t units, cudaStream_t st) {
-  return pair ? launch_form<B_MN, EPI, true>(p, units, st) : launch_form<B_MN, EPI, false>(p, units, st);
+cudaError_t launch_pick(const Fp8Params& p, bool pair, int bn, int64_t units, cudaStream_t st) {
+  if (pair) return launch_form<256, B_MN, EPI, true>(p, units, st);
+  if constexpr (EPI == FP8_EPI_BF16)
+    if (bn == 128) return launch_form<128, B_MN, EPI, false>(p, units, st);
+  return launch_form<256, B_MN, EPI, false>(p, units, st);
 }
 
 }  // namespace
@@ -854,15 +846,19 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   // A pair's tile spans 256 rows: worth it where groups fill them.
   const char* force = std::getenv("MOE_GEMM_CTA_PAIR");
   const bool pair = force && (force[0] == '0' || force[0] == '1') ? force[0] == '1' : a.rows >= 512LL * a.groups;
+  // most M tiles of any split of the rows into groups
+  const int64_t mtiles = a.rows / (pair ? 2 * BM : BM) + std::min<int64_t>(a.groups, a.rows);
+  // 128 columns a tile where 256 leave SMs without one
+  const int bn = a.epi == FP8_EPI_BF16 && !pair && mtiles * ((a.n + 255) / 256) < num_sms() ? 128 : 256;
   Fp8Params p{};
   for (int s = 0; s < a.sources; ++s) {
-    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0, 128, 128)) return cudaErrorInvalidValue;
-    if (!pair && !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 128, 32)) return cudaErrorInvalidValue;
+    if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0, 128)) return cudaErrorInvalidValue;
+    if (!pair && !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 32)) return cudaErrorInvalidValue;
     p.a_scale[s] = a.a_scale[s];
   }
   for (int s = 0; s < (a.dual ? 2 : a.sources); ++s) {
-    if (!(a.b_mn ? code_map(&p.tmB[s], a.b[s], a.n, a.k, a.groups, pair ? 64 : 128, 128)
-                 : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups, 128, 64)))
+    if (!(a.b_mn ? code_map(&p.tmB[s], a.b[s], a.n, a.k, a.groups, 128)
+                 : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups, pair || a.dual ? 128 : bn)))
       return cudaErrorInvalidValue;
     p.b_scale[s] = a.b_scale[s];
   }
@@ -873,7 +869,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.n = static_cast<int32_t>(a.n);
   p.kb = static_cast<int32_t>((a.k + BK - 1) / BK);
   p.sources = a.sources;
-  p.ntiles = static_cast<int32_t>((a.n + 127) / 128);
+  p.n128 = static_cast<int32_t>((a.n + 127) / 128);
+  p.ntiles = a.dual ? p.n128 : static_cast<int32_t>((a.n + bn - 1) / bn);
   p.out0 = a.out0;
   p.out1 = a.out1;
   p.out2 = a.out2;
@@ -883,12 +880,11 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.in0 = a.in0;
   p.in1 = a.in1;
   p.status = a.status;
-  // most M tiles of any split of the rows into groups
-  const int64_t units = (a.rows / (pair ? 2 * BM : BM) + std::min<int64_t>(a.groups, a.rows)) * p.ntiles;
-  if (a.epi == FP8_EPI_SWIGLU_FWD) return launch_pick<false, FP8_EPI_SWIGLU_FWD>(p, pair, units, st);
-  if (a.epi == FP8_EPI_SWIGLU_BWD) return launch_pick<true, FP8_EPI_SWIGLU_BWD>(p, pair, units, st);
-  return a.b_mn ? launch_pick<true, FP8_EPI_BF16>(p, pair, units, st)
-                : launch_pick<false, FP8_EPI_BF16>(p, pair, units, st);
+  const int64_t units = mtiles * p.ntiles;
+  if (a.epi == FP8_EPI_SWIGLU_FWD) return launch_pick<false, FP8_EPI_SWIGLU_FWD>(p, pair, bn, units, st);
+  if (a.epi == FP8_EPI_SWIGLU_BWD) return launch_pick<true, FP8_EPI_SWIGLU_BWD>(p, pair, bn, units, st);
+  return a.b_mn ? launch_pick<true, FP8_EPI_BF16>(p, pair, bn, units, st)
+                : launch_pick<false, FP8_EPI_BF16>(p, pair, bn, units, st);
 }
 
 }  // namespace moe
