@@ -218,28 +218,37 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// mbar_wait_bounded for a whole warp, with the same answer in every lane and
-// little code: the limit and the abort flag are looked at now and then.
+// try_wait that may suspend the warp for 100 us: without the hint it comes back
+// every few hundred clocks, and the polls of sixteen warps took a third of the
+// issue slots.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait_bounded for a whole warp, with the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
                                           int site) {
-  uint64_t t0 = 0;
-  uint32_t n = 0;
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    if ((++n & 63u) == 0) {
-      if (__any_sync(0xffffffffu, *abort_flag)) return false;
-      const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kSpinTimeoutNs) {
-        if ((threadIdx.x & 31) == 0) {
-          *abort_flag = 1;
-          if (status) {
-            atomicOr(status, DEV_TIMEOUT);
-            atomicExch(status + 1, site);
-          }
+  if (__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) return true;
+  const uint64_t t0 = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    if (__shfl_sync(0xffffffffu, globaltimer_ns(), 0) - t0 > kSpinTimeoutNs) {
+      if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        if (status) {
+          atomicOr(status, DEV_TIMEOUT);
+          atomicExch(status + 1, site);
         }
-        return false;
       }
+      return false;
     }
   }
   return true;
@@ -540,45 +549,64 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const int at = static_cast<int>(threadIdx.x) - 64;    // rows at and at + 64
       const int64_t wtiles = static_cast<int64_t>(p.n128) * p.kb;
       const int64_t bstep = B_MN ? p.n128 : 1;
-      uint32_t gi = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total; tile += ustride) {
-        const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
-        int64_t boff[NS];
+      float4 a[2];
+      float b[NS][4];
+      // the factors of k-blocks k4 .. k4 + 3 of a tile
+      auto load = [&](const Tile& t, int src, int k4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          a[h] = __ldg(reinterpret_cast<const float4*>(
+              p.a_scale[src] + static_cast<int64_t>(min(t.row0 + at + 64 * h, p.rows - 1)) * p.a_scale_ld + k4));
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           const int nb = DUAL ? t.nt : min(t.nt * NS + j, p.n128 - 1);
-          boff[j] = t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
+          const float* pb = p.b_scale[DUAL ? j : src] + t.g * wtiles + (B_MN ? nb : static_cast<int64_t>(nb) * p.kb);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) b[j][u] = __ldg(pb + min(k4 + u, p.kb - 1) * bstep);
         }
-        for (int src = 0; ok && src < p.sources; ++src) {
-          for (int k4 = 0; k4 < p.kb; k4 += 4, ++gi) {
-            float4 a[2];
+      };
+      uint32_t gi = 0;
+      bool ok = true;
+      int tile = unit0, src = 0, k4 = 0;
+      Tile t{};
+      if (tile < total) {
+        t = find_tile<PAIR>(tile, p, s_pre, rank);
+        load(t, 0, 0);
+      }
+      while (tile < total) {
+        float prod[2][NS][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              a[h] = __ldg(reinterpret_cast<const float4*>(
-                  p.a_scale[src] + static_cast<int64_t>(min(t.row0 + at + 64 * h, p.rows - 1)) * p.a_scale_ld + k4));
-            float b[NS][4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                b[j][u] = __ldg(p.b_scale[DUAL ? j : src] + boff[j] + min(k4 + u, p.kb - 1) * bstep);
-            ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
-            if (!ok) break;
-            float* dst = s_scale + (gi & 1u) * 1024 + at;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < NS; ++j) {
-                dst[j * 128 + h * 64] = a[h].x * b[j][0];
-                dst[256 + j * 128 + h * 64] = a[h].y * b[j][1];
-                dst[512 + j * 128 + h * 64] = a[h].z * b[j][2];
-                dst[768 + j * 128 + h * 64] = a[h].w * b[j][3];
-              }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull[gi & 1u]);
+          for (int j = 0; j < NS; ++j) {
+            prod[h][j][0] = a[h].x * b[j][0];
+            prod[h][j][1] = a[h].y * b[j][1];
+            prod[h][j][2] = a[h].z * b[j][2];
+            prod[h][j][3] = a[h].w * b[j][3];
+          }
+        // the next four's factors are on their way while these are handed over
+        k4 += 4;
+        if (k4 >= p.kb) {
+          k4 = 0;
+          if (++src == p.sources) {
+            src = 0;
+            tile += ustride;
+            if (tile < total) t = find_tile<PAIR>(tile, p, s_pre, rank);
           }
         }
+        if (tile < total) load(t, src, k4);
+        ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
+        if (!ok) break;
+        float* dst = s_scale + (gi & 1u) * 1024 + at;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dst[u * 256 + j * 128 + h * 64] = prod[h][j][u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[gi & 1u]);
+        ++gi;
       }
     }
     __syncwarp();
@@ -599,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
+      if (elect_one()) {
         if (PAIR) mbar_arrive_remote(tempty_addr + buf * 8);
         else mbar_arrive(&tempty[buf]);
       }
