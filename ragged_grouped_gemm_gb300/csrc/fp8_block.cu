@@ -149,12 +149,20 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 }
 
 // -------------------------------------------------------------------- GEMM
-// Roles (640 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer,
-// warps 2-3 scale products, warps 4-19 epilogue (warp w reads tensor-memory
-// lanes 32 (w % 4) .. + 31 and a quarter of the columns: 64 accumulators a thread).
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer,
+// warps 2-3 scale products, warps 4-11 epilogue (warp w reads tensor-memory
+// lanes 32 (w % 4) .. + 31 and half of the columns: 128 accumulators a thread).
 // Tiles of 128 rows x BN columns per CTA, 512 / BN partial products in tensor
-// memory.  Sixteen warps, because a warp's tensor-memory loads, waits and
-// multiply-adds follow each other: four warps a scheduler cover each other's.
+// memory.
+//
+// What bounds it is the chain from one k-block to the next: the MMAs' completion
+// seen through a barrier, 128 tensor-memory words added by each epilogue thread
+// (256 issue slots a scheduler and k-block), the buffer's release seen by the
+// MMA warp.  8192 rows x 4096 columns x 14336: 358 us on CTA pairs (2.69
+// PFLOP/s), 368 alone; 16 epilogue warps of 64 columns 413; the two-product
+// multiply-add 448; loads of 32 columns 438; 128-column tiles with four partial
+// products in flight 622, since the issue of a k-block (four MMAs, two commits,
+// two waits) takes 400 clocks whatever its size.
 //
 // CTA pair (PAIR): two CTAs share a 256 x 256 tile, M = 256, each with its own
 // 128 rows of A and half of B's columns: 32 KB a k-block per SM instead of 48.
@@ -166,13 +174,13 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 constexpr int BM = 128;
 constexpr int BK = 128;              // contraction elements (bytes) of a k-block
 constexpr int kAuxThreads = 128;
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = kAuxThreads + kEpiWarps * 32;
 constexpr int kMaxGroups = 1024;
 constexpr int kABytes = BM * BK;     // A of a stage
-// A block launches with 640 x 96 = 61440 registers; the split hands 32 of them a
-// thread from the first warpgroup to the other four: 128 x 64 + 512 x 104 = 61440.
-constexpr int kAuxRegs = 96, kEpiRegs = 96;
+// A block launches with 384 x 168 = 64512 registers; the split hands 96 of them a
+// thread from the first warpgroup to the two that accumulate: 128 x 72 + 256 x 216 = 64512.
+constexpr int kAuxRegs = 72, kEpiRegs = 216;
 
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool b_mn) {
   // D format fp32 (bits 4-5 = 1), A and B E4M3 (7-9, 10-12 = 0), B major (16), N >> 3 (17-22), M >> 4 (24-28)
@@ -199,10 +207,17 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
 }
 // acc += s * v.  Volatile, which keeps it behind the wait for the tensor-memory
 // load whose register it reads; naming the registers in the wait costs a copy
-// of each.  (Two products in one instruction need a copy to make their pair,
-// so they are no fewer instructions.)
+// of each.  (The instruction for two products runs at half the rate.)
 __device__ __forceinline__ void fma_after_wait(float& acc, float s, uint32_t v) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(s), "f"(__uint_as_float(v)));
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
 // One lane of a converged warp.  The compiler knows this form: operands of the
@@ -218,29 +233,24 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// try_wait that may suspend the warp for 100 us: without the hint it comes back
-// every few hundred clocks, and the polls of sixteen warps took a third of the
-// issue slots.
-__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait_bounded for a whole warp, with the same answer in every lane.
+// mbar_wait_bounded for a whole warp, with the same answer in every lane.  The
+// abort flag and the limit are looked at now and then: the polls of the
+// waiting warps take issue slots from the others.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
                                           int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) return true;
-  const uint64_t t0 = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  uint64_t t0 = 0;
+  uint32_t n = 0;
 #pragma unroll 1
-  while (!__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) {
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *abort_flag)) return false;
-    if (__shfl_sync(0xffffffffu, globaltimer_ns(), 0) - t0 > kSpinTimeoutNs) {
+    const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+    if (n++ == 0) {
+      t0 = now;
+    } else if (now - t0 > kSpinTimeoutNs) {
       if ((threadIdx.x & 31) == 0) {
         *abort_flag = 1;
         if (status) {
@@ -251,7 +261,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
       return false;
     }
   }
-  return true;
 }
 
 struct Fp8Params {
@@ -286,8 +295,8 @@ struct Cfg {
   static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;
-  static constexpr int kEpiOff = kStages * kStageBytes;        // 1 KB of output staging a warp
-  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 1024;   // row maxima [2][4][128]
+  static constexpr int kEpiOff = kStages * kStageBytes;        // 512 bytes of output staging a warp
+  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 512;   // row maxima [2][4][128]
   static constexpr int kScaleOff = kMaxOff + 4096;             // scale products [2][4 k-blocks][2][128]
   static constexpr int kBarOff = kScaleOff + 8192;
   static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 4 + 1;
@@ -327,35 +336,40 @@ __device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const in
 }
 
 // Sixteen 32-bit words of each lane's row (64 bytes) written to global memory
-// as 32-byte row segments, through 1 KB of shared memory, half at a time.
+// as 32-byte row segments, through 512 bytes of shared memory, sixteen rows and
+// half a row at a time.
 // dst: row 0 of the warp's 32; chunks: 16-byte chunks inside the output's columns.
 __device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint32_t (&w)[16], uint8_t* dst,
                                              int64_t ld_bytes, int rows, int chunks) {
+  const int l = lane & 15, c = lane & 1;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    __syncwarp();
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)   // chunk j of row l at j ^ ((l >> 2) & 1): four rows span the banks
-      st_shared_v4(stg + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4), w[8 * h + 4 * j], w[8 * h + 4 * j + 1],
-                   w[8 * h + 4 * j + 2], w[8 * h + 4 * j + 3]);
-    __syncwarp();
-    const int c = lane & 1;
+    for (int g = 0; g < 2; ++g) {
+      __syncwarp();
+      if ((lane >> 4) == g) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = i * 16 + (lane >> 1);
+        for (int j = 0; j < 2; ++j)   // chunk j of row l at j ^ ((l >> 2) & 1): four rows span the banks
+          st_shared_v4(stg + l * 32 + ((j ^ ((l >> 2) & 1)) << 4), w[8 * h + 4 * j], w[8 * h + 4 * j + 1],
+                       w[8 * h + 4 * j + 2], w[8 * h + 4 * j + 3]);
+      }
+      __syncwarp();
+      const int s = lane >> 1, r = g * 16 + s;
       uint4 v;
-      ld_shared_v4(stg + r * 32 + ((c ^ ((r >> 2) & 1)) << 4), v.x, v.y, v.z, v.w);
+      ld_shared_v4(stg + s * 32 + ((c ^ ((s >> 2) & 1)) << 4), v.x, v.y, v.z, v.w);
       if (r < rows && 2 * h + c < chunks) *reinterpret_cast<uint4*>(dst + r * ld_bytes + (2 * h + c) * 16) = v;
     }
-  }
 }
+
 template <int BN, bool B_MN, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
   using C = Cfg<BN, PAIR>;
   constexpr int S = C::kStages, kBufs = C::kBufs;
   constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
   constexpr int NS = BN / 128;        // scale products a row and k-block: 128-column blocks, or w1 and w3
-  constexpr int COLS = BN / 4;        // columns of an epilogue warp
+  constexpr int CG = kEpiWarps / 4;   // column groups of the epilogue warps
+  constexpr int COLS = BN / CG;       // columns of an epilogue warp
+  constexpr int CW = 16;              // columns of a tensor-memory load
   static_assert(!DUAL || BN == 256, "w1 and w3 halves of a 256-column tile");
   static_assert(!PAIR || BN == 256, "pairs share 256 columns");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -371,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
   int* s_pre = reinterpret_cast<int*>(smem + C::kTabOff);
-  float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
+  const uint32_t s_scale = smem_u32(smem + C::kScaleOff);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], 4);
+    for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], CG);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sfull[b], 2);
       mbar_init(&sempty[b], kEpiWarps);
@@ -509,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + kABytes, B_MN ? 16384 : 16, 1024);
       uint32_t s = 0, ph = 0, buf = 0, bph = 1;
       for (; left > 0; --left) {
-        if (!warp_wait(&tempty[buf], bph, s_abort, p.status, 820) || !warp_wait(&full[s], ph, s_abort, p.status, 840))
+        // the operands are there long before the buffer is
+        if (!warp_wait(&full[s], ph, s_abort, p.status, 840) || !warp_wait(&tempty[buf], bph, s_abort, p.status, 820))
           break;
         tc_fence_after();
         if (elect_one()) {
@@ -597,13 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (tile < total) load(t, src, k4);
         ok = warp_wait(&sempty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, s_abort, p.status, 870);
         if (!ok) break;
-        float* dst = s_scale + (gi & 1u) * 1024 + at;
+        const uint32_t dst = s_scale + ((gi & 1u) * 1024 + at) * 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) dst[u * 256 + j * 128 + h * 64] = prod[h][j][u];
+            for (int u = 0; u < 4; ++u) st_shared_f32(dst + (u * 256 + j * 128 + h * 64) * 4, prod[h][j][u]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[gi & 1u]);
         ++gi;
@@ -615,11 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // -------------------------------------------------------------- epilogue
     const int ew = warp - kAuxThreads / 32;
     const int q = warp & 3;           // lane quarter of tensor memory this warp may read
-    const int cg = ew >> 2;           // column quarter
+    const int cg = ew >> 2;           // column group
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    // tile column of this warp's 16-column chunk c (w1 | w3: half of the chunks each)
-    auto chunk_col = [&](int c) { return DUAL ? (c >> 1) * 128 + cg * 32 + (c & 1) * 16 : cg * COLS + c * 16; };
-    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 1024);
+    // tile column of this warp's chunk c (w1 | w3: half of the chunks each)
+    auto chunk_col = [&](int c) { constexpr int H = COLS / 32;
+      return DUAL ? (c / H) * 128 + cg * (COLS / 2) + (c % H) * 16 : cg * COLS + c * 16; };
+    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 512);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
     const uint32_t tempty_addr = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
     const int r = q * 32 + lane;
@@ -639,38 +655,39 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const bool mine = q * 32 < t.valid;   // whether this warp has rows of the tile
       const int rows = t.valid - q * 32;
       const int64_t row = t.row0 + q * 32;
-      float acc[COLS];                      // DUAL: 32 columns of a1, the same 32 of a3
+      float acc[COLS];                      // DUAL: half of them a1, the same columns of a3 the rest
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
       for (int src = 0; ok && src < p.sources; ++src) {
         for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
           ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
-          const float* ps = s_scale + (gi & 1u) * 1024 + (DUAL || BN == 128 ? 0 : (cg >> 1) * 128) + r;
-#pragma unroll
+          const uint32_t ps = s_scale + ((gi & 1u) * 1024 + (DUAL ? 0 : cg * COLS / 128 * 128) + r) * 4;
+          const int n4 = min(4, p.kb - k4);
+#pragma unroll 1   // four copies of the body miss the instruction cache: 410 us against 358
           for (int u = 0; u < 4; ++u) {
-            if (ok && k4 + u < p.kb) {
-              const float sa = ps[u * 256], sb = DUAL ? ps[u * 256 + 128] : sa;
-              const int buf = it % kBufs;
-              ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
-              if (ok && mine) {
-                tc_fence_after();
+            if (!ok || u >= n4) break;
+            const float sa = ld_shared_f32(ps + u * 1024), sb = DUAL ? ld_shared_f32(ps + u * 1024 + 512) : sa;
+            const uint32_t buf = it % kBufs;
+            ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
+            if (!ok) break;
+            if (mine) {
+              tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < COLS / 16; ++c) {
-                  uint32_t v[16];
-                  tmem_ld_32x32b_x16(lane_base + buf * BN + chunk_col(c), v);
-                  tmem_wait_ld();
-                  if (c + 1 == COLS / 16) release(buf);
+              for (int c = 0; c < COLS / CW; ++c) {
+                uint32_t v[CW];
+                tmem_ld_32x32b_x16(lane_base + buf * BN + chunk_col(c), v);
+                tmem_wait_ld();
+                if (c + 1 == COLS / CW) release(buf);
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) fma_after_wait(acc[c * 16 + i], DUAL && c >= 2 ? sb : sa, v[i]);
-                }
-              } else if (ok) {
-                release(buf);
+                for (int i = 0; i < CW; ++i) fma_after_wait(acc[c * CW + i], DUAL && c >= COLS / CW / 2 ? sb : sa, v[i]);
               }
-              ++it;
+            } else {
+              release(buf);
             }
+            ++it;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[gi & 1u]);
+          if (elect_one()) mbar_arrive(&sempty[gi & 1u]);
         }
       }
       if (!ok) break;
@@ -715,17 +732,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
       } else {
         // columns past F hold zero (their weights are read as zero)
-        const int f = t.nt * 128 + cg * 32;
-        if (p.out1) rows_bf16(acc, p.out1, f);
-        if (p.out2) rows_bf16(acc + 32, p.out2, f);
+        constexpr int HC = COLS / 2;
+        const int f = t.nt * 128 + cg * HC;
+#pragma unroll
+        for (int c = 0; c < HC / 32; ++c) {
+          if (p.out1) rows_bf16(acc + 32 * c, p.out1, f + 32 * c);
+          if (p.out2) rows_bf16(acc + HC + 32 * c, p.out2, f + 32 * c);
+        }
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          acc[i] = acc[i] / (1.0f + __expf(-acc[i])) * acc[32 + i];
+        for (int i = 0; i < HC; ++i) {
+          acc[i] = acc[i] / (1.0f + __expf(-acc[i])) * acc[HC + i];
           m = fmaxf(m, fabsf(acc[i]));
         }
-        if (p.out3) rows_bf16(acc, p.out3, f);
-        // the other column quarters' maxima of the same rows; two buffers, since a
+        if (p.out3) {
+#pragma unroll
+          for (int c = 0; c < HC / 32; ++c) rows_bf16(acc + 32 * c, p.out3, f + 32 * c);
+        }
+        // the other column groups' maxima of the same rows; two buffers, since a
         // warp is at most one exchange ahead of the others
         float* mx = s_max + (tcount & 1u) * 512 + r;
         mx[cg * 128] = m;
@@ -733,21 +757,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(&xbar[q]);
         ok = warp_wait(&xbar[q], tcount & 1u, s_abort, p.status, 890 + q);
         if (!ok) break;
-        m = fmaxf(fmaxf(mx[0], mx[128]), fmaxf(mx[256], mx[384]));
+#pragma unroll
+        for (int g = 0; g < CG; ++g) m = fmaxf(m, mx[g * 128]);
         const BlockScale b = block_scale(m);
         if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = b.s;
-        if (r < t.valid && f < p.n) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out0) + (row + lane) * p.n + f);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out0) + (row + lane) * p.n + f);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[4];
+        for (int k = 0; k < HC / 16; ++k) {
+          uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* h = acc + half * 16 + 4 * i;
-              w[i] = fp8_encode4(h[0], h[1], h[2], h[3], b);
-            }
-            dst[half] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) {
+            const float* h = acc + k * 16 + 4 * i;
+            w[i] = fp8_encode4(h[0], h[1], h[2], h[3], b);
           }
+          if (r < t.valid && f + k * 16 < p.n) dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
