@@ -548,7 +548,8 @@ MOE_API moe_status_t moe_permute_fp8b(const moe_desc_t* d, const void* x, const 
 
 /* moe_grouped_ffn on FP8 operands: GEMM1 from xq_perm / xs_perm and w1, w3;
  * its epilogue computes h = silu(a1) * a3 in fp32 and quantises it per 1 x 128
- * (kept in the workspace); GEMM2 with w2 into y_perm [R,D] bf16.  The
+ * (codes of h times the fp32 reciprocal of the block's scale; kept in the
+ * workspace); GEMM2 with w2 into y_perm [R,D] bf16.  The
  * shared expert does the same from xq_tok / xs_tok into y_shared.  wq: codes
  * and fp32 tile scales from moe_quantize_fp8_tile.  `saved` receives bf16 a1,
  * a3, h (a1s, a3s, hs) for the backward, or holds NULL pointers. */
