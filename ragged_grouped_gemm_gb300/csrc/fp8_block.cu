@@ -9,6 +9,7 @@
 // MMAs of one k-block run while the previous one is being added.
 #include "fp8_block.cuh"
 #include "grouped_gemm.cuh"
+#include "pdl.cuh"
 #include "sm100_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -93,6 +94,8 @@ __device__ __forceinline__ uint4 quant16(const uint4 v0, const uint4 v1, float& 
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint4* __restrict__ src, int64_t rows, int c16,
                                                              uint4* __restrict__ codes, float* __restrict__ scales,
                                                              int64_t ld) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int segs = (c16 + 31) / 32;
   const int64_t items = rows * segs;
@@ -119,6 +122,8 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
                                                                 uint4* __restrict__ codes, float* __restrict__ scales,
                                                                 int64_t ld, uint4* __restrict__ tok_codes,
                                                                 float* __restrict__ tok_scales) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int segs = (c16 + 31) / 32;
   const int64_t items = static_cast<int64_t>(n_tok) * segs;
@@ -423,6 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       tmem_relinquish();
     }
   }
+  // all of the above needs nothing of the kernels before this one
+  pdl_trigger();
+  pdl_wait();
   for (int i = threadIdx.x; i <= G; i += kThreads)
     if (cut_offset(p, i) != __ldg(p.offsets + i) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
   if (warp == 0) {
@@ -829,15 +837,6 @@ template <int BN, bool B_MN, int EPI, bool PAIR>
 cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
   using C = Cfg<BN, PAIR>;
   auto kern = fp8_gemm_kernel<BN, B_MN, EPI, PAIR>;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = PAIR ? 2 : 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   static int resident = 0;   // CTAs, or CTA pairs, that run at once
@@ -846,8 +845,17 @@ cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
                                static_cast<int>(C::smem_bytes(kMaxGroups)));
     resident = PAIR ? num_sms() / 2 : num_sms();
     if (err == cudaSuccess && PAIR) {
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 2;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(2 * resident);
+      cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = C::smem_bytes(kMaxGroups);
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) resident = n;
       cudaGetLastError();
@@ -855,10 +863,7 @@ cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
   });
   if (err != cudaSuccess) return err;
   const int u = static_cast<int>(std::min<int64_t>(units, resident));
-  cfg.gridDim = dim3(PAIR ? 2 * u : u);
-  cfg.dynamicSmemBytes = C::smem_bytes(p.groups);
-  cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_pdl(kern, PAIR ? 2 * u : u, kThreads, C::smem_bytes(p.groups), st, PAIR ? 2 : 1, p);
 }
 
 template <bool B_MN, int EPI>
@@ -876,9 +881,8 @@ cudaError_t launch_fp8_quant_rows(const void* src, int64_t rows, int64_t cols, u
   if (rows <= 0) return cudaSuccess;
   const int64_t warps = rows * ((cols / 16 + 31) / 32);
   const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
-  fp8_quant_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const uint4*>(src), rows, static_cast<int>(cols / 16),
-                                              reinterpret_cast<uint4*>(codes), scales, ld);
-  return cudaGetLastError();
+  return launch_pdl(fp8_quant_rows_kernel, grid, 256, 0, st, 1, static_cast<const uint4*>(src), rows,
+                    static_cast<int>(cols / 16), reinterpret_cast<uint4*>(codes), scales, ld);
 }
 
 cudaError_t launch_fp8_quant_scatter(const void* x, int n_tok, int d, int top_k, const int32_t* row_of_copy,
@@ -887,10 +891,9 @@ cudaError_t launch_fp8_quant_scatter(const void* x, int n_tok, int d, int top_k,
   if (n_tok <= 0) return cudaSuccess;
   const int64_t warps = static_cast<int64_t>(n_tok) * ((d / 16 + 31) / 32);
   const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
-  fp8_quant_scatter_kernel<<<grid, 256, 0, st>>>(static_cast<const uint4*>(x), n_tok, d / 16, top_k, row_of_copy,
-                                                 reinterpret_cast<uint4*>(codes), scales, ld,
-                                                 reinterpret_cast<uint4*>(tok_codes), tok_scales);
-  return cudaGetLastError();
+  return launch_pdl(fp8_quant_scatter_kernel, grid, 256, 0, st, 1, static_cast<const uint4*>(x), n_tok, d / 16, top_k,
+                    row_of_copy, reinterpret_cast<uint4*>(codes), scales, ld, reinterpret_cast<uint4*>(tok_codes),
+                    tok_scales);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
