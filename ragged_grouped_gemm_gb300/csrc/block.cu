@@ -2,6 +2,8 @@
 // and the residual dropout of a pre-norm MoE block.
 #include "block.cuh"
 #include "grouped_gemm.cuh"
+#include "pdl.cuh"
+#include "sm100_ptx.cuh"
 
 #include <cuda_bf16.h>
 
@@ -142,6 +144,251 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
   }
 }
 
+// ---- rows through shared memory
+// For rows of 1024 to 8192 elements the inputs arrive by bulk copies in a ring
+// of row buffers, so that the loads of the next rows run under the arithmetic
+// and the block sums of this one; gamma, beta and the gradients' sums stay in
+// registers.  One block's warps would otherwise wait for memory once a row:
+// 4096 rows of 7168 bf16 numbers, straight from global memory on two blocks an
+// SM, took 32 us forward and 67 us backward.
+constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its blocks
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <bool F32>
+__device__ __forceinline__ void smem_vec8(const uint8_t* row, int c, float (&f)[8]) {
+  if (F32) {
+    const float4 a = reinterpret_cast<const float4*>(row)[2 * c], b = reinterpret_cast<const float4*>(row)[2 * c + 1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    Vec8<false> v;
+    v.a = reinterpret_cast<const uint4*>(row)[c];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = v.get(j);
+  }
+}
+__device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8]) {
+  Vec8<true> v;
+  v.load(p, c);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = v.get(j);
+}
+
+// T threads share a row, V vectors of eight columns each; `stages` row buffers.
+template <bool F32, int T, int V>
+__global__ void __launch_bounds__(T, 512 / T) layernorm_ring_kernel(
+    int64_t rows, int d8, int stages, const uint8_t* __restrict__ x, const float* __restrict__ gamma,
+    const float* __restrict__ beta, float eps, void* __restrict__ y, float* __restrict__ mean,
+    float* __restrict__ rstd) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[8];
+  __shared__ float2 s_red[2][T / 32];
+  const int tid = threadIdx.x;
+  const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16);
+  const float inv_d = 1.0f / static_cast<float>(d8 * 8);
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  float g[V][8], b[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = min(tid + i * T, d8 - 1);
+    load_f32x8(gamma, c, g[i]);
+    if (beta) load_f32x8(beta, c, b[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
+  }
+  __syncthreads();
+  auto fetch = [&](int s, int64_t r) {
+    mbar_arrive_expect_tx(&full[s], xb);
+    bulk_load(ring + static_cast<size_t>(s) * xb, x + r * xb, xb, &full[s]);
+  };
+  if (tid == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t r = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (r < rows) fetch(s, r);
+    }
+  // One block sum a row: the squared deviations of this row together with the
+  // plain sum of the next, which is in its buffer by then.
+  float v[V][8], w[V][8];
+  auto take = [&](int s, uint32_t ph, float (&f)[V][8]) {   // a row into registers; its sum
+    mbar_wait_drain(&full[s], ph);
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        smem_vec8<F32>(ring + static_cast<size_t>(s) * xb, c, f[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t += f[i][j];
+    }
+    return t;
+  };
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  int64_t r = blockIdx.x;
+  if (r >= rows) return;
+  float mu = row_sum2<T>(make_float2(take(0, 0, v), 0.0f), s_red[1]).x * inv_d;
+  for (; r < rows; r += gridDim.x, flip ^= 1) {
+    const int s0 = s;
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+    const bool more = r + gridDim.x < rows;
+    float2 sum = make_float2(0.0f, more ? take(s, ph, w) : 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (tid + i * T < d8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = v[i][j] - mu;
+          sum.x = fmaf(e, e, sum.x);
+        }
+      }
+    sum = row_sum2<T>(sum, s_red[flip]);
+    // every thread has taken this row: its buffer is free
+    const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
+    if (tid == 0 && next < rows) fetch(s0, next);
+    const float rs = 1.0f / sqrtf(sum.x * inv_d + eps);
+    if (tid == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf((v[i][j] - mu) * rs, g[i][j], b[i][j]);
+        Vec8<false>::store(y, r * d8 + c, o);
+      }
+    }
+    mu = sum.y * inv_d;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = w[i][j];
+  }
+}
+
+template <bool F32, int T, int V>
+__global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
+    int64_t rows, int d8, int stages, const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
+    const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const uint8_t* __restrict__ dres, void* __restrict__ dx, float* __restrict__ part) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[8];
+  __shared__ float2 s_red[2][T / 32];
+  const int tid = threadIdx.x;
+  const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16), yb = static_cast<uint32_t>(d8) * 16;
+  const float inv_d = 1.0f / static_cast<float>(d8 * 8);
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  float g[V][8], dg[V][8], db[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    load_f32x8(gamma, min(tid + i * T, d8 - 1), g[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
+  }
+  __syncthreads();
+  const uint32_t sb = xb + yb + (dres ? xb : 0);   // a row's x, dy and dres
+  auto fetch = [&](int s, int64_t r) {
+    uint8_t* dst = ring + static_cast<size_t>(s) * sb;
+    mbar_arrive_expect_tx(&full[s], sb);
+    bulk_load(dst, x + r * xb, xb, &full[s]);
+    bulk_load(dst + xb, dy + r * yb, yb, &full[s]);
+    if (dres) bulk_load(dst + xb + yb, dres + r * xb, xb, &full[s]);
+  };
+  if (tid == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t r = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (r < rows) fetch(s, r);
+    }
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+    const float mu = __ldg(mean + r), rs = __ldg(rstd + r);
+    mbar_wait_drain(&full[s], ph);
+    const uint8_t* row = ring + static_cast<size_t>(s) * sb;
+    float res[V][8];
+    float2 sum = make_float2(0.0f, 0.0f);
+    float xh[V][8], ge[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        float e[8];
+        smem_vec8<F32>(row, c, xh[i]);
+        smem_vec8<false>(row + xb, c, e);
+        if (dres) {
+          smem_vec8<F32>(row + xb + yb, c, res[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) res[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          xh[i][j] = (xh[i][j] - mu) * rs;
+          ge[i][j] = g[i][j] * e[j];
+          sum.x += ge[i][j];
+          sum.y = fmaf(ge[i][j], xh[i][j], sum.y);
+          dg[i][j] = fmaf(e[j], xh[i][j], dg[i][j]);
+          db[i][j] += e[j];
+        }
+      }
+    }
+    sum = row_sum2<T>(sum, s_red[flip]);
+    // every thread has read the buffer
+    const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
+    if (tid == 0 && next < rows) fetch(s, next);
+    const float m1 = sum.x * inv_d, m2 = sum.y * inv_d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < d8) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf(rs, ge[i][j] - m1 - xh[i][j] * m2, res[i][j]);
+        Vec8<F32>::store(dx, r * d8 + c, o);
+      }
+    }
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  float* p = part + static_cast<int64_t>(blockIdx.x) * 16 * d8;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * T;
+    if (c < d8) {
+      Vec8<true>::store(p, c, dg[i]);
+      Vec8<true>::store(p + 8 * d8, c, db[i]);
+    }
+  }
+}
+
 // Blocks of the backward, each of which leaves one partial sum of dgamma and
 // dbeta: two per SM.
 constexpr int kNormBlocks = 304;
@@ -254,6 +501,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
 __global__ void __launch_bounds__(256) layernorm_reduce_kernel(int blocks, int d, const float* __restrict__ part,
                                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
   __shared__ float s[8][32];
+  pdl_trigger();
+  pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31);
   const int k = threadIdx.x >> 5;
   float t = 0.0f;
@@ -366,6 +615,26 @@ __global__ void __launch_bounds__(256) dropout_bwd_kernel(int64_t items, const v
   }
 }
 
+// Row buffers of a ring kernel with `blocks` blocks an SM and buffers of
+// `bytes`, at most 8 and no more than there are rows for; 0: rows too wide.
+int ring_stages(int64_t bytes, int blocks) {
+  const int64_t n = std::min<int64_t>(8, kRingBytes / blocks / bytes);
+  return n < 2 ? 0 : static_cast<int>(n);
+}
+template <auto K, class... A>
+cudaError_t launch_ring(unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  // a ring's dynamic shared memory, allowed once a kernel
+  static const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  return e != cudaSuccess ? e : launch_pdl(K, grid, block, smem, st, 1, args...);
+}
+// Calls f(threads, vectors) with the ring kernels' shape of a row of 1024 < d <= 8192.
+template <class F>
+cudaError_t with_ring_shape(int d, F&& f) {
+  if (d <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
+  if (d <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+}
+
 // Calls f(threads-per-row, vectors-per-thread) with the row shape of d.
 template <class F>
 cudaError_t with_row_shape(int d, F&& f) {
@@ -390,6 +659,20 @@ cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, con
                              float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
+  // one row a block leaves nothing to overlap: the direct kernel starts sooner
+  if (d > 1024 && d <= 8192 && rows > 2 * num_sms())
+    return with_ring_shape(d, [&](auto t, auto v) {
+      constexpr int T = decltype(t)::value, V = decltype(v)::value;
+      constexpr int per_sm = 512 / T;
+      const int64_t bytes = static_cast<int64_t>(d) * (x_f32 ? 4 : 2);
+      const int stages = ring_stages(bytes, per_sm);
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * per_sm));
+      const auto* px = static_cast<const uint8_t*>(x);
+      return x_f32 ? launch_ring<layernorm_ring_kernel<true, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages, px,
+                                                                    gamma, beta, eps, y, mean, rstd)
+                   : launch_ring<layernorm_ring_kernel<false, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages,
+                                                                     px, gamma, beta, eps, y, mean, rstd);
+    });
   return with_row_shape(d, [&](auto t, auto v) {
     constexpr int T = decltype(t)::value, V = decltype(v)::value;
     constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -411,7 +694,24 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
                                  float* dbeta, float* scratch, cudaStream_t st) {
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
   int grid = 0;
-  if (rows > 0) {
+  if (d > 1024 && d <= 8192 && rows > 2 * num_sms()) {
+    const cudaError_t e = with_ring_shape(d, [&](auto t, auto v) {
+      constexpr int T = decltype(t)::value, V = decltype(v)::value;
+      constexpr int per_sm = 512 / T;
+      const int64_t bytes = static_cast<int64_t>(d) * ((x_f32 ? 4 : 2) * (dres ? 2 : 1) + 2);
+      const int stages = ring_stages(bytes, per_sm);
+      grid = static_cast<int>(std::min<int64_t>(kNormBlocks, static_cast<int64_t>(num_sms()) * per_sm));
+      const auto* px = static_cast<const uint8_t*>(x);
+      const auto* pd = static_cast<const uint8_t*>(dy);
+      const auto* pr = static_cast<const uint8_t*>(dres);
+      return x_f32 ? launch_ring<layernorm_bwd_ring_kernel<true, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages,
+                                                                        pd, px, gamma, mean, rstd, pr, dx, scratch)
+                   : launch_ring<layernorm_bwd_ring_kernel<false, T, V>>(grid, T, stages * bytes, st, rows, d / 8,
+                                                                         stages, pd, px, gamma, mean, rstd, pr, dx,
+                                                                         scratch);
+    });
+    if (e != cudaSuccess) return e;
+  } else if (rows > 0) {
     const cudaError_t e = with_row_shape(d, [&](auto t, auto v) {
       constexpr int T = decltype(t)::value, V = decltype(v)::value;
       constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -426,8 +726,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
     });
     if (e != cudaSuccess) return e;
   }
-  layernorm_reduce_kernel<<<(2 * d + 31) / 32, 256, 0, st>>>(grid, d, scratch, dgamma, dbeta);
-  return cudaGetLastError();
+  return launch_pdl(layernorm_reduce_kernel, (2 * d + 31) / 32, 256, 0, st, 1, grid, d, scratch, dgamma, dbeta);
 }
 
 cudaError_t launch_combine_dropout(int n_tok, int d, int top_k, const void* y_perm, const int32_t* row_of_copy,
