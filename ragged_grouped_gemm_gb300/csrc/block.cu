@@ -497,25 +497,30 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
 }
 
 // dgamma, dbeta = the blocks' partial sums [blocks][2][d] added: 32 columns a
-// block, eight threads a column, joined in order.
-__global__ void __launch_bounds__(256) layernorm_reduce_kernel(int blocks, int d, const float* __restrict__ part,
-                                                               float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float s[8][32];
+// block, 32 threads a column (a handful of loads in a row each), joined in order.
+__global__ void __launch_bounds__(1024) layernorm_reduce_kernel(int blocks, int d, const float* __restrict__ part,
+                                                                float* __restrict__ dgamma,
+                                                                float* __restrict__ dbeta) {
+  __shared__ float s[32][33];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
-  const int k = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float t = 0.0f;
-  if (c < 2 * d)
-    for (int b = k; b < blocks; b += 8) t += __ldg(part + static_cast<int64_t>(b) * 2 * d + c);
-  s[k][threadIdx.x & 31] = t;
+  if (c < 2 * d) {
+#pragma unroll 4
+    for (int b = k; b < blocks; b += 32) t += __ldg(part + static_cast<int64_t>(b) * 2 * d + c);
+  }
+  s[k][lane] = t;
   __syncthreads();
-  if (k == 0 && c < 2 * d) {
-    t = 0.0f;
+  // warp k adds column k of the 32 by a shuffle tree
+  t = s[lane][k];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t += s[j][threadIdx.x];
-    if (c < d) dgamma[c] = t;
-    else if (dbeta) dbeta[c - d] = t;
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int ck = blockIdx.x * 32 + k;
+  if (lane == 0 && ck < 2 * d) {
+    if (ck < d) dgamma[ck] = t;
+    else if (dbeta) dbeta[ck - d] = t;
   }
 }
 
@@ -603,15 +608,23 @@ __global__ void __launch_bounds__(256) dropout_bwd_kernel(int64_t items, const v
     key = static_cast<uint64_t>(__ldg(rng));
     first = static_cast<uint64_t>(__ldg(rng + 1));
   }
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items;
-       it += static_cast<int64_t>(gridDim.x) * 256) {
-    Vec8<F32> v;
-    v.load(dout, it);
-    const uint32_t keep = threshold ? keep8(key, first, it, threshold) : 0xFFu;
-    float o[8];
+  // the loads of a turn's items are in flight together, under the random words of the last
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items; it += 2 * stride) {
+    Vec8<F32> v[2];
+    const bool two = it + stride < items;
+    v[0].load(dout, it);
+    if (two) v[1].load(dout, it + stride);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = (keep >> e) & 1u ? scale * v.get(e) : 0.0f;
-    Vec8<false>::store(dy, it, o);
+    for (int h = 0; h < 2; ++h) {
+      if (h && !two) break;
+      const int64_t i = it + h * stride;
+      const uint32_t keep = threshold ? keep8(key, first, i, threshold) : 0xFFu;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (keep >> e) & 1u ? scale * v[h].get(e) : 0.0f;
+      Vec8<false>::store(dy, i, o);
+    }
   }
 }
 
@@ -726,7 +739,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(layernorm_reduce_kernel, (2 * d + 31) / 32, 256, 0, st, 1, grid, d, scratch, dgamma, dbeta);
+  return launch_pdl(layernorm_reduce_kernel, (2 * d + 31) / 32, 1024, 0, st, 1, grid, d, scratch, dgamma, dbeta);
 }
 
 cudaError_t launch_combine_dropout(int n_tok, int d, int top_k, const void* y_perm, const int32_t* row_of_copy,
@@ -749,7 +762,7 @@ cudaError_t launch_dropout_bwd(int64_t n, const void* dout, bool f32, const int6
                                float scale, void* dy, cudaStream_t st) {
   const int64_t items = n / 8;
   if (items <= 0) return cudaSuccess;
-  const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, 1 << 20));
+  const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(num_sms()) * 8));
   if (f32) dropout_bwd_kernel<true><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
   else dropout_bwd_kernel<false><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
   return cudaGetLastError();
