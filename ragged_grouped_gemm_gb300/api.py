@@ -684,8 +684,11 @@ class MoELayer:
         self.x = None
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
-        b = self.buf
         self.experts(x, stream)
+        return self._combine(stream)
+
+    def _combine(self, stream=None):
+        b = self.buf
         moe_combine(self.desc, b["y_perm"], b["row_of_copy"], b["topk_w"], b["y_shared"], b["out"], stream)
         return b["out"]
 
@@ -703,9 +706,9 @@ class MoELayer:
         moe_route(self.desc, x, p["w_gate"], p.get("bias"), b["logits"], b["topk_idx"], b["topk_w"], b["counts"],
                   b["offsets_full"] if self.cap else b["offsets"], self.ws, stream)
         if self.mx:
-            return self._forward_mx(x, stream)
+            return self._experts_mx(x, stream)
         if self.f8:
-            return self._forward_fp8b(x, stream)
+            return self._experts_fp8b(x, stream)
         if self.gather:
             b = self.buf
             moe_permute_maps(self.desc, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"], self.ws,
@@ -738,7 +741,15 @@ class MoELayer:
                             p.get("ws3"), p.get("ws2"), b["a1"], b["a3"], b["h"], b["a1s"], b["a3s"], b["hs"],
                             b["y_perm"], b["y_shared"], self.ws, stream)
 
+    def _ffn_combine(self, x, stream=None):
+        self._ffn(x, stream)
+        return self._combine(stream)
+
     def _forward_mx(self, x, stream=None):
+        self._experts_mx(x, stream)
+        return self._combine(stream)
+
+    def _experts_mx(self, x, stream=None):
         b = self.buf
         moe_permute_mxfp8(self.desc, x, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"],
                           b["xq_perm"], b["xs_perm"], b["xq_tok"], b["xs_tok"], self.ws, stream)
@@ -747,7 +758,7 @@ class MoELayer:
         moe_grouped_ffn_mxfp8(self.desc, b["xq_perm"], b["xs_perm"], b["offsets"], b["xq_tok"], b["xs_tok"], self.wq,
                               saved, b["y_perm"], b["y_shared"], self.ws, stream)
 
-    def _forward_fp8b(self, x, stream=None):
+    def _experts_fp8b(self, x, stream=None):
         b = self.buf
         moe_permute_fp8b(self.desc, x, b["topk_idx"], b["offsets"], b["row_of_copy"], b["copy_of_row"], b["x_perm"],
                          b["xq_perm"], b["xs_perm"], b["xq_tok"], b["xs_tok"], self.ws, stream)
