@@ -718,7 +718,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
       constexpr int per_sm = 512 / T;
       const int64_t bytes = static_cast<int64_t>(d) * ((x_f32 ? 4 : 2) * (dres ? 2 : 1) + 2);
       const int stages = ring_stages(bytes, per_sm);
-      grid = static_cast<int>(std::min<int64_t>(kNormBlocks, static_cast<int64_t>(num_sms()) * per_sm));
+      grid = static_cast<int>(std::min<int64_t>({rows, kNormBlocks, static_cast<int64_t>(num_sms()) * per_sm}));
       const auto* px = static_cast<const uint8_t*>(x);
       const auto* pd = static_cast<const uint8_t*>(dy);
       const auto* pr = static_cast<const uint8_t*>(dres);
