@@ -148,9 +148,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
 // For rows of 1024 to 8192 elements the inputs arrive by bulk copies in a ring
 // of row buffers, so that the loads of the next rows run under the arithmetic
 // and the block sums of this one; gamma, beta and the gradients' sums stay in
-// registers.  One block's warps would otherwise wait for memory once a row:
-// 4096 rows of 7168 bf16 numbers, straight from global memory on two blocks an
-// SM, took 32 us forward and 67 us backward.
+// registers.  4096 rows of 7168 bf16 numbers: 25.8 us forward, 46.1 us backward with
+// its sums (17.3 and 34.6 at the rate of a plain copy); straight from global
+// memory, two blocks of 256 threads an SM, 27.2 and 66; one row 2.5 against 2.9.
+// What bounds it is a row's way through a block: two (backward: one) block sums
+// and 16 elements a thread, about 1.7 us.  One sum a row by taking the next row's
+// mean along needs twice the registers, one block an SM: 31.9 us.
 constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its blocks
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -182,13 +185,13 @@ __device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8])
 
 // T threads share a row, V vectors of eight columns each; `stages` row buffers.
 template <bool F32, int T, int V>
-__global__ void __launch_bounds__(T, 512 / T) layernorm_ring_kernel(
+__global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ beta, float eps, void* __restrict__ y, float* __restrict__ mean,
     float* __restrict__ rstd) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
-  __shared__ float2 s_red[2][T / 32];
+  __shared__ float s_red[2][T / 32];
   const int tid = threadIdx.x;
   const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16);
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
@@ -218,53 +221,40 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_ring_kernel(
       const int64_t r = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
       if (r < rows) fetch(s, r);
     }
-  // One block sum a row: the squared deviations of this row together with the
-  // plain sum of the next, which is in its buffer by then.
-  float v[V][8], w[V][8];
-  auto take = [&](int s, uint32_t ph, float (&f)[V][8]) {   // a row into registers; its sum
+  int s = 0;
+  uint32_t ph = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     mbar_wait_drain(&full[s], ph);
-    float t = 0.0f;
+    const uint8_t* row = ring + static_cast<size_t>(s) * xb;
+    float v[V][8];
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * T;
       if (c < d8) {
-        smem_vec8<F32>(ring + static_cast<size_t>(s) * xb, c, f[i]);
+        smem_vec8<F32>(row, c, v[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t += f[i][j];
+      for (int j = 0; j < 8; ++j) sum += v[i][j];
     }
-    return t;
-  };
-  int s = 0, flip = 0;
-  uint32_t ph = 0;
-  int64_t r = blockIdx.x;
-  if (r >= rows) return;
-  float mu = row_sum2<T>(make_float2(take(0, 0, v), 0.0f), s_red[1]).x * inv_d;
-  for (; r < rows; r += gridDim.x, flip ^= 1) {
-    const int s0 = s;
-    if (++s == stages) {
-      s = 0;
-      ph ^= 1u;
-    }
-    const bool more = r + gridDim.x < rows;
-    float2 sum = make_float2(0.0f, more ? take(s, ph, w) : 0.0f);
+    const float mu = row_sum<T>(sum, s_red[0]) * inv_d;
+    // every thread has read the buffer: the row after next `stages` may land in it
+    const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
+    if (tid == 0 && next < rows) fetch(s, next);
+    float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (tid + i * T < d8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float e = v[i][j] - mu;
-          sum.x = fmaf(e, e, sum.x);
+          sq = fmaf(e, e, sq);
         }
       }
-    sum = row_sum2<T>(sum, s_red[flip]);
-    // every thread has taken this row: its buffer is free
-    const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
-    if (tid == 0 && next < rows) fetch(s0, next);
-    const float rs = 1.0f / sqrtf(sum.x * inv_d + eps);
+    const float rs = 1.0f / sqrtf(row_sum<T>(sq, s_red[1]) * inv_d + eps);
     if (tid == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
@@ -279,11 +269,10 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_ring_kernel(
         Vec8<false>::store(y, r * d8 + c, o);
       }
     }
-    mu = sum.y * inv_d;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = w[i][j];
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
   }
 }
 
@@ -653,7 +642,8 @@ cudaError_t with_ring_shape(int d, F&& f) {
   return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
 }
 
-// Calls f(threads-per-row, vectors-per-thread) with the row shape of d.
+// Calls f(threads-per-row, vectors-per-thread) with the direct kernels' shape of d: a
+// warp a row up to 1024 elements, a block of 1024 threads a row above 8192.
 template <class F>
 cudaError_t with_row_shape(int d, F&& f) {
   const int d8 = d / 8;
@@ -667,7 +657,6 @@ cudaError_t with_row_shape(int d, F&& f) {
     }
   };
   if (d8 <= 128) return pick(std::integral_constant<int, 32>());
-  if (d8 <= 1024) return pick(std::integral_constant<int, 256>());
   return pick(std::integral_constant<int, 1024>());
 }
 
@@ -677,11 +666,10 @@ cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, con
                              float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
-  // one row a block leaves nothing to overlap: the direct kernel starts sooner
-  if (d > 1024 && d <= 8192 && rows > 2 * num_sms())
+  if (d > 1024 && d <= 8192)
     return with_ring_shape(d, [&](auto t, auto v) {
       constexpr int T = decltype(t)::value, V = decltype(v)::value;
-      constexpr int per_sm = 512 / T;
+      constexpr int per_sm = 1024 / T;
       const int64_t bytes = static_cast<int64_t>(d) * (x_f32 ? 4 : 2);
       const int stages = ring_stages(bytes, per_sm);
       const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * per_sm));
@@ -712,7 +700,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
                                  float* dbeta, float* scratch, cudaStream_t st) {
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
   int grid = 0;
-  if (d > 1024 && d <= 8192 && rows > 2 * num_sms()) {
+  if (rows > 0 && d > 1024 && d <= 8192) {
     const cudaError_t e = with_ring_shape(d, [&](auto t, auto v) {
       constexpr int T = decltype(t)::value, V = decltype(v)::value;
       constexpr int per_sm = 512 / T;

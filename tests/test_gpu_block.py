@@ -246,3 +246,41 @@ def test_block_captured_step_draws_anew_at_each_replay():
         np.testing.assert_array_equal(np32(block.out)[~keep], np32(x)[~keep])
         assert (np32(block.dmoe)[keep] == 2 * np32(dout)[keep]).all()
     assert block.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("n,d", [(305, 1088), (611, 2048), (400, 2560), (1000, 4096), (307, 7168), (330, 8192)])
+def test_layernorm_many_rows(n, d, kind):
+    """More rows than blocks: every block takes several, through all its row buffers."""
+    g = torch.Generator().manual_seed(n + d + 1)
+    x = (torch.randn(n, d, generator=g) * 2 - 0.5).to(kind).cuda()
+    dres = torch.randn(n, d, generator=g).to(kind).cuda()
+    dy = torch.randn(n, d, generator=g).to(BF16).cuda()
+    gamma, beta = torch.randn(d, generator=g).cuda(), torch.randn(d, generator=g).cuda()
+    a = _norm(x, dy, gamma, beta, dres)
+    _check_norm(x, dy, gamma, beta, dres, a)
+    for u, v in zip(a, _norm(x, dy, gamma, beta, dres)):
+        assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    _check_norm(x, dy, gamma, None, None, _norm(x, dy, gamma, None, None))
+
+
+def test_layernorm_gradient_against_differences():
+    """The loss sum(y t) in 64 bits along a direction against the kernel's gradients: a central
+    difference of step 2^-10 is off by step^2 times the third derivative (order one), and
+    the gradients by the roundings of the checks above."""
+    g = torch.Generator().manual_seed(11)
+    n, d = 4, 1536
+    x, v = torch.randn(n, d, generator=g), torch.randn(n, d, generator=g)
+    t = torch.randn(n, d, generator=g).to(BF16)
+    gamma, beta, vg = (torch.randn(d, generator=g) for _ in range(3))
+    _, _, _, dx, dgamma, dbeta = _norm(x.cuda(), t.cuda(), gamma.cuda(), beta.cuda(), None)
+    x64, g64, b64, t64 = (np32(w).astype(np.float64) for w in (x, gamma, beta, t))
+    loss = lambda xx, gg: (O.layernorm(xx, gg, b64, 1e-5)[0] * t64).sum()  # noqa: E731
+    h = 2.0 ** -10
+    vx, vgn = np32(v).astype(np.float64), np32(vg).astype(np.float64)
+    num_x = (loss(x64 + h * vx, g64) - loss(x64 - h * vx, g64)) / (2 * h)
+    num_g = (loss(x64, g64 + h * vgn) - loss(x64, g64 - h * vgn)) / (2 * h)
+    scale = np.sqrt(n * d)
+    assert abs(num_x - (np32(dx).astype(np.float64) * vx).sum()) <= 1e-4 * scale
+    assert abs(num_g - (np32(dgamma).astype(np.float64) * vgn).sum()) <= 1e-4 * scale
+    assert abs(np32(dbeta).astype(np.float64) - t64.sum(0)).max() <= 4 * 2.0 ** -24 * np.abs(t64).sum(0).max()

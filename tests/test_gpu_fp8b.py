@@ -215,3 +215,49 @@ def test_permute_fp8b_rows():
         rc, rs = O.fp8_rows_quantize(np32(x))
         np.testing.assert_array_equal(b[codes].cpu().numpy(), rc)
         np.testing.assert_array_equal(b[scales][:, :rs.shape[1]].cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("form", ["0", "1"])
+@pytest.mark.parametrize("mn", [False, True])
+@pytest.mark.parametrize("sizes,n,k", [([700], 528, 400), ([300, 0, 900, 5], 256, 656), ([1, 40, 33], 2064, 144),
+                                       ([512, 513], 272, 1296)])
+def test_grouped_product_forms(sizes, n, k, mn, form, monkeypatch):
+    """Tiles alone and on CTA pairs, few and many rows a group, many column tiles."""
+    monkeypatch.setenv("MOE_GEMM_CTA_PAIR", form)
+    g = torch.Generator().manual_seed(sum(sizes) + n + k)
+    rows = sum(sizes)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    codes, scales = _quantise(torch.randn(rows, k, generator=g).to(torch.bfloat16))
+    w, ws = _weights(g, len(sizes), *((k, n) if mn else (n, k)))
+    out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(api.moe_grouped_gemm_fp8_workspace_size(len(sizes), rows, n, k), dtype=torch.uint8,
+                       device="cuda")
+    api.moe_workspace_init(work)
+    api.moe_grouped_gemm_fp8(codes, scales, torch.from_numpy(off).cuda(), w, ws, out, work, b_mn=mn)
+    assert api.moe_get_device_status(work) == (0, 0)
+    ref, mag = _product_ref(codes, scales, off, w, ws, mn)
+    assert (np.abs(np32(out) - ref) <= _product_tol(ref, mag, k)).all()
+
+
+def test_grouped_product_forms_are_adjoint():
+    """<a W^T, g> = <a, g W>: the forward and the data gradient of the same weights, on operands that
+    are their own quantised values; each output element is off by the product's tolerance."""
+    r = torch.Generator().manual_seed(5)
+    rows, n, k = 200, 384, 640
+    off = torch.tensor([0, 60, 200], dtype=torch.int32, device="cuda")
+    w, ws = _weights(r, 2, n, k)
+    work = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    val = lambda c, s, m: O.fp8_rows_dequantize(c.cpu().numpy(), s[:, :m // 128].cpu().numpy())  # noqa: E731
+    a, sa = _quantise(torch.randn(rows, k, generator=r).to(torch.bfloat16))
+    g, sg = _quantise(torch.randn(rows, n, generator=r).to(torch.bfloat16))
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    dx = torch.empty(rows, k, dtype=torch.bfloat16, device="cuda")
+    api.moe_grouped_gemm_fp8(a, sa, off, w, ws, y, work)
+    api.moe_grouped_gemm_fp8(g, sg, off, w, ws, dx, work, b_mn=True)
+    av, gv = val(a, sa, k), val(g, sg, n)
+    left, right = np32(y).astype(np.float64) * gv, np32(dx).astype(np.float64) * av
+    slack = lambda m: (2.0 ** -8 + 2.0 ** -12) * np.abs(m).sum()  # noqa: E731
+    assert abs(left.sum() - right.sum()) <= slack(left) + slack(right)
+    # and much closer, since the roundings are as often up as down: eight standard deviations
+    dev = 2.0 ** -8 / np.sqrt(3) * np.sqrt((left ** 2).sum() + (right ** 2).sum())
+    assert abs(left.sum() - right.sum()) <= 8 * dev + 2.0 ** -12 * (np.abs(left).sum() + np.abs(right).sum())
