@@ -268,6 +268,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Whether the phase has completed, for a whole warp.
+__device__ __forceinline__ bool try_wait_all(uint32_t addr, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred q, p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return r != 0;
+}
+
 struct Fp8Params {
   CUtensorMap tmA[2];
   CUtensorMap tmA32[2];   // boxes of 32 rows
@@ -645,10 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       return DUAL ? (c / H) * 128 + cg * (COLS / 2) + (c % H) * 16 : cg * COLS + c * 16; };
     const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 512);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
+    const uint32_t tfull_addr = smem_u32(tfull);
     const uint32_t tempty_addr = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
     const int r = q * 32 + lane;
     // this warp has read a partial product
-    auto release = [&](int buf) {
+    auto release = [&](uint32_t buf) {
       tc_fence_before();
       __syncwarp();
       if (elect_one()) {
@@ -656,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         else mbar_arrive(&tempty[buf]);
       }
     };
-    uint32_t it = 0, gi = 0, tcount = 0;
+    uint32_t buf = 0, bph = 0, gi = 0, tcount = 0;
     bool ok = true;
     for (int tile = unit0; ok && tile < total; tile += ustride, ++tcount) {
       const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
@@ -669,21 +684,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       for (int src = 0; ok && src < p.sources; ++src) {
         for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
           ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
-          const uint32_t ps = s_scale + ((gi & 1u) * 1024 + (DUAL ? 0 : cg * COLS / 128 * 128) + r) * 4;
-          const int n4 = min(4, p.kb - k4);
+          uint32_t ps = s_scale + ((gi & 1u) * 1024 + (DUAL ? 0 : cg * COLS / 128 * 128) + r) * 4;
+          const uint32_t pe = ps + min(4, p.kb - k4) * 1024;
 #pragma unroll 1   // four copies of the body miss the instruction cache: 410 us against 358
-          for (int u = 0; u < 4; ++u) {
-            if (!ok || u >= n4) break;
-            const float sa = ld_shared_f32(ps + u * 1024), sb = DUAL ? ld_shared_f32(ps + u * 1024 + 512) : sa;
-            const uint32_t buf = it % kBufs;
-            ok = warp_wait(&tfull[buf], (it / kBufs) & 1u, s_abort, p.status, 860);
-            if (!ok) break;
+          for (; ok && ps != pe; ps += 1024) {
+            const float sa = ld_shared_f32(ps), sb = DUAL ? ld_shared_f32(ps + 512) : sa;
+            if (!try_wait_all(tfull_addr + buf * 8, bph)) {
+              ok = warp_wait(&tfull[buf], bph, s_abort, p.status, 860);
+              if (!ok) break;
+            }
             if (mine) {
               tc_fence_after();
+              const uint32_t tb = lane_base + buf * BN;
 #pragma unroll
               for (int c = 0; c < COLS / CW; ++c) {
                 uint32_t v[CW];
-                tmem_ld_32x32b_x16(lane_base + buf * BN + chunk_col(c), v);
+                tmem_ld_32x32b_x16(tb + chunk_col(c), v);
                 tmem_wait_ld();
                 if (c + 1 == COLS / CW) release(buf);
 #pragma unroll
@@ -692,7 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             } else {
               release(buf);
             }
-            ++it;
+            if (++buf == kBufs) {
+              buf = 0;
+              bph ^= 1u;
+            }
           }
           __syncwarp();
           if (elect_one()) mbar_arrive(&sempty[gi & 1u]);
