@@ -632,7 +632,7 @@ template <auto K, class... A>
 cudaError_t launch_ring(unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
   // a ring's dynamic shared memory, allowed once a kernel
   static const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  return e != cudaSuccess ? e : launch_pdl(K, grid, block, smem, st, 1, args...);
+  return e != cudaSuccess ? e : launch_pdl(K, grid, block, smem, st, args...);
 }
 // Calls f(threads, vectors) with the ring kernels' shape of a row of 1024 < d <= 8192.
 template <class F>
@@ -732,7 +732,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(layernorm_reduce_kernel, (2 * d + 31) / 32, 1024, 0, st, 1, grid, d, scratch, dgamma, dbeta);
+  return launch_pdl(layernorm_reduce_kernel, (2 * d + 31) / 32, 1024, 0, st, grid, d, scratch, dgamma, dbeta);
 }
 
 cudaError_t launch_combine_dropout(int n_tok, int d, int top_k, const void* y_perm, const int32_t* row_of_copy,

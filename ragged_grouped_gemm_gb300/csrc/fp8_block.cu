@@ -16,7 +16,6 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <mutex>
 
 namespace moe {
@@ -160,19 +159,17 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 // Tiles of 128 rows x BN columns per CTA, 512 / BN partial products in tensor
 // memory.
 //
-// What bounds it is the chain from one k-block to the next: the MMAs' completion
-// seen through a barrier, 128 tensor-memory words added by each epilogue thread
-// (256 issue slots a scheduler and k-block), the buffer's release seen by the
-// MMA warp.  8192 rows x 4096 columns x 14336: 358 us on CTA pairs (2.69
-// PFLOP/s), 368 alone; 16 epilogue warps of 64 columns 413; the two-product
-// multiply-add 448; loads of 32 columns 438; 128-column tiles with four partial
-// products in flight 622, since the issue of a k-block (four MMAs, two commits,
-// two waits) takes 400 clocks whatever its size.
-//
-// CTA pair (PAIR): two CTAs share a 256 x 256 tile, M = 256, each with its own
-// 128 rows of A and half of B's columns: 32 KB a k-block per SM instead of 48.
-// Rank 0 issues the MMAs; both CTAs' loads complete on its barriers and its
-// commits arrive on both CTAs'.
+// What bounds it: a k-block's operands are written to shared memory once and
+// read once by the MMAs (96 KB, about 750 clocks), and the chain from one k-block
+// to the next (the MMAs' completion seen through a barrier, 128 tensor-memory
+// words added by each epilogue thread, the buffer's release seen by the MMA
+// warp) takes about 850.  8192 rows x 4096 columns x 14336: 357 us (2.70 PFLOP/s).
+// Measured against it on that shape: 16 epilogue warps of 64 columns 413; the
+// two-product multiply-add 448; tensor-memory loads of 32 columns 438, of the next
+// 16 columns ahead of the multiply-adds 400; 128-column tiles with four
+// partial products 622, since the issue of a k-block (four MMAs, two commits,
+// two waits) takes 400 clocks whatever its size; CTA pairs sharing 256 x 256
+// tiles 352, and no faster than this within an expert layer (1.42 ms both).
 //
 // GEMM1 (SwiGLU): a tile holds 128 columns of w1 and the same 128 of w3, which
 // is one scale block of h.
@@ -192,24 +189,16 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
-template <bool PAIR>
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
-  if (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
+
 // acc += s * v.  Volatile, which keeps it behind the wait for the tensor-memory
 // load whose register it reads; naming the registers in the wait costs a copy
 // of each.  (The instruction for two products runs at half the rate.)
@@ -308,10 +297,10 @@ struct Fp8Params {
   int32_t* status;
 };
 
-template <int BN, bool PAIR>
+template <int BN>
 struct Cfg {
   static constexpr int kBufs = 512 / BN;             // partial products in tensor memory
-  static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * BK;
+  static constexpr int kBBytes = BN * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;
   static constexpr int kEpiOff = kStages * kStageBytes;        // 512 bytes of output staging a warp
@@ -326,7 +315,7 @@ struct Cfg {
 };
 
 struct Tile {
-  int g, nt, row0, valid;   // valid: rows of this CTA's 128 (at most 0 where a pair's second half is empty)
+  int g, nt, row0, valid;   // valid: rows of the 128
 };
 
 // An offset cut to the rows there are, so that no tile reaches outside them.
@@ -334,9 +323,7 @@ __device__ __forceinline__ int cut_offset(const Fp8Params& p, int i) {
   return min(max(__ldg(p.offsets + i), 0), p.rows);
 }
 
-template <bool PAIR>
-__device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const int* s_pre, int rank) {
-  constexpr int UR = PAIR ? 2 * BM : BM;
+__device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const int* s_pre) {
   int lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -344,12 +331,12 @@ __device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const in
   }
   // M tiles innermost: the CTAs that run at once share an expert's weight blocks
   const int first = cut_offset(p, lo), last = cut_offset(p, lo + 1);
-  const int mtiles = (last - first + UR - 1) / UR;
+  const int mtiles = (last - first + BM - 1) / BM;
   const int rem = tile - s_pre[lo];
   Tile t;
   t.g = lo;
   t.nt = rem / mtiles;
-  t.row0 = first + (rem - t.nt * mtiles) * UR + rank * BM;
+  t.row0 = first + (rem - t.nt * mtiles) * BM;
   t.valid = min(BM, last - t.row0);
   return t;
 }
@@ -380,9 +367,9 @@ __device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint3
     }
 }
 
-template <int BN, bool B_MN, int EPI, bool PAIR>
+template <int BN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN>;
   constexpr int S = C::kStages, kBufs = C::kBufs;
   constexpr bool DUAL = EPI == FP8_EPI_SWIGLU_FWD;
   constexpr int NS = BN / 128;        // scale products a row and k-block: 128-column blocks, or w1 and w3
@@ -390,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   constexpr int COLS = BN / CG;       // columns of an epilogue warp
   constexpr int CW = 16;              // columns of a tensor-memory load
   static_assert(!DUAL || BN == 256, "w1 and w3 halves of a 256-column tile");
-  static_assert(!PAIR || BN == 256, "pairs share 256 columns");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -409,9 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int G = p.groups;
-  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int unit0 = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int ustride = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int unit0 = blockIdx.x, ustride = gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -420,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
+      mbar_init(&tempty[b], kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&xbar[q], CG);
     for (int b = 0; b < 2; ++b) {
@@ -434,13 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     tma_prefetch_desc(&p.tmB[0]);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(s_tmem, 512);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(s_tmem, 512);
-      tmem_relinquish();
-    }
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
   }
   // all of the above needs nothing of the kernels before this one
   pdl_trigger();
@@ -448,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   for (int i = threadIdx.x; i <= G; i += kThreads)
     if (cut_offset(p, i) != __ldg(p.offsets + i) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
   if (warp == 0) {
-    constexpr int UR = PAIR ? 2 * BM : BM;
-    auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + UR - 1) / UR * p.ntiles; };
+    auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + BM - 1) / BM * p.ntiles; };
     const int per = (G + 31) / 32;
     const int lo = min(G, lane * per), hi = min(G, lo + per);
     int sum = 0;
@@ -469,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();   // the peer's barriers are initialised and its tensor memory allocated
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
   const int total = s_pre[G];
@@ -481,40 +458,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       // ---------------------------------------------------------- producer
       uint32_t it = 0, s = 0, ph = 1;
       bool ok = true;
-      const uint32_t lead_full = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
       for (int tile = unit0; ok && tile < total; tile += ustride) {
-        const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
-        // a tile of at most 32 rows loads no others: what the rest of its stage
-        // holds reaches accumulator rows that nothing reads
-        const bool few = !PAIR && t.valid <= 32;
+        const Tile t = find_tile(tile, p, s_pre);
+        // a tile of at most 32 rows loads no others (47.8 -> 40.4 us for 2 rows of 16 groups
+        // of 7168 x 2048): what the rest of its stage holds reaches accumulator rows that
+        // nothing reads
+        const bool few = t.valid <= 32;
         const uint32_t bytes = few ? C::kStageBytes - kABytes * 3 / 4 : C::kStageBytes;
         for (int src = 0; ok && src < p.sources; ++src) {
           const CUtensorMap* ma = few ? &p.tmA32[src] : &p.tmA[src];
-          const CUtensorMap* mb = &p.tmB[DUAL && PAIR ? rank : src];
-          const int n0 = DUAL ? t.nt * 128 : t.nt * BN + (PAIR ? rank * 128 : 0);
+          const CUtensorMap* mb = &p.tmB[src];
+          const int n0 = DUAL ? t.nt * 128 : t.nt * BN;
           for (int k0 = 0; k0 < p.kb * BK; k0 += BK, ++it) {
             ok = warp_wait(&empty[s], ph, s_abort, p.status, 800);
             if (!ok) break;
             uint8_t* sA = smem + s * C::kStageBytes;
             uint8_t* sB = sA + kABytes;
             if (elect_one()) {
-              if (PAIR) {
-                // both CTAs' loads complete on rank 0's barrier, which rank 0 arms
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-                const uint32_t bar = lead_full + s * 8;
-                tma_load_2d_pair(sA, ma, bar, k0, t.row0);
-                if (B_MN) tma_load_3d_pair(sB, mb, bar, n0, k0, t.g);
-                else tma_load_3d_pair(sB, mb, bar, k0, n0, t.g);
+              mbar_arrive_expect_tx(&full[s], bytes);
+              tma_load_2d(sA, ma, &full[s], k0, t.row0);
+              if (B_MN) {
+                tma_load_3d(sB, mb, &full[s], n0, k0, t.g);
+                if (BN == 256) tma_load_3d(sB + 16384, mb, &full[s], n0 + 128, k0, t.g);
               } else {
-                mbar_arrive_expect_tx(&full[s], bytes);
-                tma_load_2d(sA, ma, &full[s], k0, t.row0);
-                if (B_MN) {
-                  tma_load_3d(sB, mb, &full[s], n0, k0, t.g);
-                  if (BN == 256) tma_load_3d(sB + 16384, mb, &full[s], n0 + 128, k0, t.g);
-                } else {
-                  tma_load_3d(sB, mb, &full[s], k0, n0, t.g);
-                  if (DUAL) tma_load_3d(sB + 16384, &p.tmB[1], &full[s], k0, n0, t.g);
-                }
+                tma_load_3d(sB, mb, &full[s], k0, n0, t.g);
+                if (DUAL) tma_load_3d(sB + 16384, &p.tmB[1], &full[s], k0, n0, t.g);
               }
             }
             __syncwarp();
@@ -525,18 +493,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           }
         }
       }
-      // no copy may still be landing when the CTA exits (rank 0's barriers count both CTAs' copies)
-      for (uint32_t i = 0; i < S && rank == 0; ++i) {
+      // no copy and no stage release may still be under way when the CTA exits
+      for (uint32_t i = 0; i < S; ++i) {
         if (it > i) {
-          const uint32_t last = i + S * ((it - 1 - i) / S);
-          mbar_wait_drain(&full[i], (last / S) & 1u);
+          const uint32_t uses = (it - 1 - i) / S + 1;   // of stage i
+          mbar_wait_drain(&full[i], (uses - 1) & 1u);
+          if (ok) mbar_wait_drain(&empty[i], (uses - 1) & 1u);
         }
       }
       __syncwarp();
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN, B_MN);
-      int64_t left = 0;   // k-blocks of this CTA's (pair's) tiles
+      constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN, B_MN);
+      int64_t left = 0;   // k-blocks of this CTA's tiles
       for (int tile = unit0; tile < total; tile += ustride) left += nkb;
       // K-major: rows of 128 bytes, 32 bytes on per K = 32; MN-major: 128 columns a row of
       // 128 bytes, 32 rows on, the next 128 columns a whole region further
@@ -553,14 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           const uint64_t ad = ad0 + s * (C::kStageBytes >> 4), bd = bd0 + s * (C::kStageBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_e4m3<PAIR>(tmem_base + buf * BN, ad + kk * 2, bd + kk * kAdvB, idesc, kk > 0 ? 1u : 0u);
-          if (PAIR) {
-            tc_commit_pair_mc(&empty[s], 3);
-            tc_commit_pair_mc(&tfull[buf], 3);
-          } else {
-            tc_commit(&empty[s]);
-            tc_commit(&tfull[buf]);
-          }
+            tc_mma_e4m3(tmem_base + buf * BN, ad + kk * 2, bd + kk * kAdvB, idesc, kk > 0 ? 1u : 0u);
+          tc_commit(&empty[s]);
+          tc_commit(&tfull[buf]);
         }
         __syncwarp();
         if (++s == S) {
@@ -574,8 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
       // every MMA has completed before tensor memory is released
       if (elect_one()) {
-        if (PAIR) tc_commit_pair_mc(mma_done, 1);
-        else tc_commit(mma_done);
+        tc_commit(mma_done);
         mbar_wait_drain(mma_done, 0);
       }
     } else if (warp >= 2) {
@@ -607,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       int tile = unit0, src = 0, k4 = 0;
       Tile t{};
       if (tile < total) {
-        t = find_tile<PAIR>(tile, p, s_pre, rank);
+        t = find_tile(tile, p, s_pre);
         load(t, 0, 0);
       }
       while (tile < total) {
@@ -628,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           if (++src == p.sources) {
             src = 0;
             tile += ustride;
-            if (tile < total) t = find_tile<PAIR>(tile, p, s_pre, rank);
+            if (tile < total) t = find_tile(tile, p, s_pre);
           }
         }
         if (tile < total) load(t, src, k4);
@@ -660,21 +623,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 512);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
     const uint32_t tfull_addr = smem_u32(tfull);
-    const uint32_t tempty_addr = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
     const int r = q * 32 + lane;
     // this warp has read a partial product
     auto release = [&](uint32_t buf) {
       tc_fence_before();
       __syncwarp();
-      if (elect_one()) {
-        if (PAIR) mbar_arrive_remote(tempty_addr + buf * 8);
-        else mbar_arrive(&tempty[buf]);
-      }
+      if (elect_one()) mbar_arrive(&tempty[buf]);
     };
     uint32_t buf = 0, bph = 0, gi = 0, tcount = 0;
     bool ok = true;
     for (int tile = unit0; ok && tile < total; tile += ustride, ++tcount) {
-      const Tile t = find_tile<PAIR>(tile, p, s_pre, rank);
+      const Tile t = find_tile(tile, p, s_pre);
       const bool mine = q * 32 < t.valid;   // whether this warp has rows of the tile
       const int rows = t.valid - q * 32;
       const int64_t row = t.row0 + q * 32;
@@ -810,12 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();   // rank 0's MMAs into the peer's tensor memory and all arrivals across are done
   tc_fence_after();
-  if (warp == 1) {
-    if (PAIR) tmem_dealloc_pair(tmem_base, 512);
-    else tmem_dealloc(tmem_base, 512);
-  }
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
 }
 
 // -------------------------------------------------------------------- host
@@ -852,45 +807,26 @@ bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool B_MN, int EPI, bool PAIR>
+template <int BN, bool B_MN, int EPI>
 cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
-  using C = Cfg<BN, PAIR>;
-  auto kern = fp8_gemm_kernel<BN, B_MN, EPI, PAIR>;
+  using C = Cfg<BN>;
+  auto kern = fp8_gemm_kernel<BN, B_MN, EPI>;
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
-  static int resident = 0;   // CTAs, or CTA pairs, that run at once
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(C::smem_bytes(kMaxGroups)));
-    resident = PAIR ? num_sms() / 2 : num_sms();
-    if (err == cudaSuccess && PAIR) {
-      cudaLaunchConfig_t cfg{};
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2;
-      at[0].val.clusterDim.y = 1;
-      at[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2 * resident);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = C::smem_bytes(kMaxGroups);
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) resident = n;
-      cudaGetLastError();
-    }
   });
   if (err != cudaSuccess) return err;
-  const int u = static_cast<int>(std::min<int64_t>(units, resident));
-  return launch_pdl(kern, PAIR ? 2 * u : u, kThreads, C::smem_bytes(p.groups), st, PAIR ? 2 : 1, p);
+  return launch_pdl(kern, static_cast<unsigned>(std::min<int64_t>(units, num_sms())), kThreads,
+                    C::smem_bytes(p.groups), st, p);
 }
 
 template <bool B_MN, int EPI>
-cudaError_t launch_pick(const Fp8Params& p, bool pair, int bn, int64_t units, cudaStream_t st) {
-  if (pair) return launch_form<256, B_MN, EPI, true>(p, units, st);
+cudaError_t launch_pick(const Fp8Params& p, int bn, int64_t units, cudaStream_t st) {
   if constexpr (EPI == FP8_EPI_BF16)
-    if (bn == 128) return launch_form<128, B_MN, EPI, false>(p, units, st);
-  return launch_form<256, B_MN, EPI, false>(p, units, st);
+    if (bn == 128) return launch_form<128, B_MN, EPI>(p, units, st);
+  return launch_form<256, B_MN, EPI>(p, units, st);
 }
 
 }  // namespace
@@ -900,7 +836,7 @@ cudaError_t launch_fp8_quant_rows(const void* src, int64_t rows, int64_t cols, u
   if (rows <= 0) return cudaSuccess;
   const int64_t warps = rows * ((cols / 16 + 31) / 32);
   const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
-  return launch_pdl(fp8_quant_rows_kernel, grid, 256, 0, st, 1, static_cast<const uint4*>(src), rows,
+  return launch_pdl(fp8_quant_rows_kernel, grid, 256, 0, st, static_cast<const uint4*>(src), rows,
                     static_cast<int>(cols / 16), reinterpret_cast<uint4*>(codes), scales, ld);
 }
 
@@ -910,7 +846,7 @@ cudaError_t launch_fp8_quant_scatter(const void* x, int n_tok, int d, int top_k,
   if (n_tok <= 0) return cudaSuccess;
   const int64_t warps = static_cast<int64_t>(n_tok) * ((d / 16 + 31) / 32);
   const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(num_sms()) * 32));
-  return launch_pdl(fp8_quant_scatter_kernel, grid, 256, 0, st, 1, static_cast<const uint4*>(x), n_tok, d / 16, top_k,
+  return launch_pdl(fp8_quant_scatter_kernel, grid, 256, 0, st, static_cast<const uint4*>(x), n_tok, d / 16, top_k,
                     row_of_copy, reinterpret_cast<uint4*>(codes), scales, ld, reinterpret_cast<uint4*>(tok_codes),
                     tok_scales);
 }
@@ -920,22 +856,22 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.groups > kMaxGroups || a.k <= 0 || a.k % 16 || a.n % 16 || a.sources < 1 || a.sources > 2 ||
       a.rows > 0x7fffff00LL || a.n > 0x3fffffffLL || a.k > 0x3fffffffLL)
     return cudaErrorInvalidValue;
-  // A pair's tile spans 256 rows: worth it where groups fill them.
-  const char* force = std::getenv("MOE_GEMM_CTA_PAIR");
-  const bool pair = force && (force[0] == '0' || force[0] == '1') ? force[0] == '1' : a.rows >= 512LL * a.groups;
   // most M tiles of any split of the rows into groups
-  const int64_t mtiles = a.rows / (pair ? 2 * BM : BM) + std::min<int64_t>(a.groups, a.rows);
-  // 128 columns a tile where 256 leave SMs without one
-  const int bn = a.epi == FP8_EPI_BF16 && !pair && mtiles * ((a.n + 255) / 256) < num_sms() ? 128 : 256;
+  const int64_t mtiles = a.rows / BM + std::min<int64_t>(a.groups, a.rows);
+  // 128 columns a tile where 256 would leave SMs without one: a row for each of 8
+  // groups of 2048 x 7168 24.7 us (256: 28.8), 8 rows of one group 20.7 (26.8); with
+  // tiles enough 256: 64 groups of 128 rows of 7168 x 2048 164 us (128: 174), 8 of 1024
+  // rows of 4096 x 4096 116 (172)
+  const int bn = a.epi == FP8_EPI_BF16 && mtiles * ((a.n + 255) / 256) < num_sms() ? 128 : 256;
   Fp8Params p{};
   for (int s = 0; s < a.sources; ++s) {
     if (!code_map(&p.tmA[s], a.a[s], a.k, a.rows, 0, 128)) return cudaErrorInvalidValue;
-    if (!pair && !code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 32)) return cudaErrorInvalidValue;
+    if (!code_map(&p.tmA32[s], a.a[s], a.k, a.rows, 0, 32)) return cudaErrorInvalidValue;
     p.a_scale[s] = a.a_scale[s];
   }
   for (int s = 0; s < (a.dual ? 2 : a.sources); ++s) {
     if (!(a.b_mn ? code_map(&p.tmB[s], a.b[s], a.n, a.k, a.groups, 128)
-                 : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups, pair || a.dual ? 128 : bn)))
+                 : code_map(&p.tmB[s], a.b[s], a.k, a.n, a.groups, a.dual ? 128 : bn)))
       return cudaErrorInvalidValue;
     p.b_scale[s] = a.b_scale[s];
   }
@@ -958,10 +894,10 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.in1 = a.in1;
   p.status = a.status;
   const int64_t units = mtiles * p.ntiles;
-  if (a.epi == FP8_EPI_SWIGLU_FWD) return launch_pick<false, FP8_EPI_SWIGLU_FWD>(p, pair, bn, units, st);
-  if (a.epi == FP8_EPI_SWIGLU_BWD) return launch_pick<true, FP8_EPI_SWIGLU_BWD>(p, pair, bn, units, st);
-  return a.b_mn ? launch_pick<true, FP8_EPI_BF16>(p, pair, bn, units, st)
-                : launch_pick<false, FP8_EPI_BF16>(p, pair, bn, units, st);
+  if (a.epi == FP8_EPI_SWIGLU_FWD) return launch_pick<false, FP8_EPI_SWIGLU_FWD>(p, bn, units, st);
+  if (a.epi == FP8_EPI_SWIGLU_BWD) return launch_pick<true, FP8_EPI_SWIGLU_BWD>(p, bn, units, st);
+  return a.b_mn ? launch_pick<true, FP8_EPI_BF16>(p, bn, units, st)
+                : launch_pick<false, FP8_EPI_BF16>(p, bn, units, st);
 }
 
 }  // namespace moe

@@ -217,13 +217,11 @@ def test_permute_fp8b_rows():
         np.testing.assert_array_equal(b[scales][:, :rs.shape[1]].cpu().numpy(), rs)
 
 
-@pytest.mark.parametrize("form", ["0", "1"])
 @pytest.mark.parametrize("mn", [False, True])
 @pytest.mark.parametrize("sizes,n,k", [([700], 528, 400), ([300, 0, 900, 5], 256, 656), ([1, 40, 33], 2064, 144),
-                                       ([512, 513], 272, 1296)])
-def test_grouped_product_forms(sizes, n, k, mn, form, monkeypatch):
-    """Tiles alone and on CTA pairs, few and many rows a group, many column tiles."""
-    monkeypatch.setenv("MOE_GEMM_CTA_PAIR", form)
+                                       ([512, 513], 272, 1296), ([1300, 900], 2320, 256)])
+def test_grouped_product_tiles(sizes, n, k, mn):
+    """Both tile widths, few and many rows a group, many column tiles."""
     g = torch.Generator().manual_seed(sum(sizes) + n + k)
     rows = sum(sizes)
     off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
@@ -239,7 +237,7 @@ def test_grouped_product_forms(sizes, n, k, mn, form, monkeypatch):
     assert (np.abs(np32(out) - ref) <= _product_tol(ref, mag, k)).all()
 
 
-def test_grouped_product_forms_are_adjoint():
+def test_grouped_product_and_data_gradient_are_adjoint():
     """<a W^T, g> = <a, g W>: the forward and the data gradient of the same weights, on operands that
     are their own quantised values; each output element is off by the product's tolerance."""
     r = torch.Generator().manual_seed(5)
