@@ -303,8 +303,8 @@ struct Cfg {
   static constexpr int kBBytes = BN * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;
-  static constexpr int kEpiOff = kStages * kStageBytes;        // 512 bytes of output staging a warp
-  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 512;   // row maxima [2][4][128]
+  static constexpr int kEpiOff = kStages * kStageBytes;        // 2 KB of output staging a warp
+  static constexpr int kMaxOff = kEpiOff + kEpiWarps * 2048;   // row maxima [2][4][128]
   static constexpr int kScaleOff = kMaxOff + 4096;             // scale products [2][4 k-blocks][2][128]
   static constexpr int kBarOff = kScaleOff + 8192;
   static constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 4 + 1;
@@ -342,29 +342,26 @@ __device__ __forceinline__ Tile find_tile(int tile, const Fp8Params& p, const in
 }
 
 // Sixteen 32-bit words of each lane's row (64 bytes) written to global memory
-// as 32-byte row segments, through 512 bytes of shared memory, sixteen rows and
-// half a row at a time.
+// as whole 64-byte row segments, through 2 KB of shared memory.
 // dst: row 0 of the warp's 32; chunks: 16-byte chunks inside the output's columns.
 __device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint32_t (&w)[16], uint8_t* dst,
                                              int64_t ld_bytes, int rows, int chunks) {
-  const int l = lane & 15, c = lane & 1;
+  __syncwarp();
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int j = 0; j < 4; ++j)   // chunk j of row l at j ^ ((l >> 1) & 3): eight rows span the banks twice
+    st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
+                 w[4 * j + 3]);
+  __syncwarp();
+  const int c = lane & 3, r0 = lane >> 2;
+  uint8_t* p = dst + r0 * ld_bytes + c * 16;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      __syncwarp();
-      if ((lane >> 4) == g) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)   // chunk j of row l at j ^ ((l >> 2) & 1): four rows span the banks
-          st_shared_v4(stg + l * 32 + ((j ^ ((l >> 2) & 1)) << 4), w[8 * h + 4 * j], w[8 * h + 4 * j + 1],
-                       w[8 * h + 4 * j + 2], w[8 * h + 4 * j + 3]);
-      }
-      __syncwarp();
-      const int s = lane >> 1, r = g * 16 + s;
-      uint4 v;
-      ld_shared_v4(stg + s * 32 + ((c ^ ((s >> 2) & 1)) << 4), v.x, v.y, v.z, v.w);
-      if (r < rows && 2 * h + c < chunks) *reinterpret_cast<uint4*>(dst + r * ld_bytes + (2 * h + c) * 16) = v;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + r0;
+    uint4 v;
+    ld_shared_v4(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+    if (r < rows && c < chunks) *reinterpret_cast<uint4*>(p) = v;
+    p += 8 * ld_bytes;
+  }
 }
 
 template <int BN, bool B_MN, int EPI>
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // tile column of this warp's chunk c (w1 | w3: half of the chunks each)
     auto chunk_col = [&](int c) { constexpr int H = COLS / 32;
       return DUAL ? (c / H) * 128 + cg * (COLS / 2) + (c % H) * 16 : cg * COLS + c * 16; };
-    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 512);
+    const uint32_t stg = smem_u32(smem + C::kEpiOff + ew * 2048);
     float* s_max = reinterpret_cast<float*>(smem + C::kMaxOff);
     const uint32_t tfull_addr = smem_u32(tfull);
     const int r = q * 32 + lane;
