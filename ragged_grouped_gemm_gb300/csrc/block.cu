@@ -84,6 +84,40 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* s) {
   return t;
 }
 
+// N sums (2 or 4) over the T threads of a block at once.  While two lanes have more
+// than one sum between them, each passes the half that the other goes on with; the
+// warps' sums are joined the same way: 5 + 6 and 7 + 12 shuffles with 16 warps.
+template <int T, int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[N]) {
+  const int lane = threadIdx.x & 31;
+  float a;
+  if constexpr (N == 4) {
+    const bool up = lane & 16;
+    const float k0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+    const float k1 = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+    const bool up2 = lane & 8;
+    a = (up2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, 8);
+  } else {
+    const bool up = lane & 16;
+    a = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (lane % (32 / N) == 0) s[threadIdx.x >> 5][lane / (32 / N)] = a;
+  __syncthreads();
+  // the warps' sums: lane l takes Q of warp l % W's
+  constexpr int W = T / 32, P = 32 / W, Q = N > P ? N / P : 1;
+  float q[Q];
+#pragma unroll
+  for (int j = 0; j < Q; ++j) {
+    q[j] = s[lane % W][lane / W % (N / Q) * Q + j];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) q[j] += __shfl_xor_sync(0xffffffffu, q[j], o);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = N == Q ? q[j] : __shfl_sync(0xffffffffu, q[j % Q], j / Q * W);
+}
+
 // T threads a row, V vectors of eight columns a thread.  The mean and then the
 // squared deviations from it are summed over the registers that hold the row,
 // so the variance loses nothing to a large mean.
@@ -148,12 +182,13 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
 // For rows of 1024 to 8192 elements the inputs arrive by bulk copies in a ring
 // of row buffers, so that the loads of the next rows run under the arithmetic
 // and the block sums of this one; gamma, beta and the gradients' sums stay in
-// registers.  4096 rows of 7168 bf16 numbers: 25.8 us forward, 46.1 us backward with
+// registers.  4096 rows of 7168 bf16 numbers: 25.8 us forward, 41 us backward with
 // its sums (17.3 and 34.6 at the rate of a plain copy); straight from global
 // memory, two blocks of 256 threads an SM, 27.2 and 66; one row 2.5 against 2.9.
 // What bounds it is a row's way through a block: two (backward: one) block sums
-// and 16 elements a thread, about 1.7 us.  One sum a row by taking the next row's
-// mean along needs twice the registers, one block an SM: 31.9 us.
+// and 16 elements a thread, about 1.7 us.  Forward, one sum a row by taking the next
+// row's mean along needs twice the registers, one block an SM: 31.9 us; two rows
+// together spill at two blocks an SM: 40.8.
 constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its blocks
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -163,18 +198,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Vector c of a row in shared memory, packed.
 template <bool F32>
-__device__ __forceinline__ void smem_vec8(const uint8_t* row, int c, float (&f)[8]) {
-  if (F32) {
-    const float4 a = reinterpret_cast<const float4*>(row)[2 * c], b = reinterpret_cast<const float4*>(row)[2 * c + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ Vec8<F32> smem_vec8(const uint8_t* row, int c) {
+  Vec8<F32> v;
+  if constexpr (F32) {
+    v.a = reinterpret_cast<const float4*>(row)[2 * c];
+    v.b = reinterpret_cast<const float4*>(row)[2 * c + 1];
   } else {
-    Vec8<false> v;
     v.a = reinterpret_cast<const uint4*>(row)[c];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = v.get(j);
   }
+  return v;
 }
 __device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8]) {
   Vec8<true> v;
@@ -232,7 +266,9 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * T;
       if (c < d8) {
-        smem_vec8<F32>(row, c, v[i]);
+        const Vec8<F32> p = smem_vec8<F32>(row, c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = p.get(j);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
@@ -276,14 +312,16 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
   }
 }
 
-template <bool F32, int T, int V>
+// R rows (blockIdx.x + i gridDim.x) pass through a block together, packed: two bf16 rows
+// share the block sum, 41 us against 46; fp32 rows have no registers for it.
+template <bool F32, int T, int V, int R>
 __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
     const uint8_t* __restrict__ dres, void* __restrict__ dx, float* __restrict__ part) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
-  __shared__ float2 s_red[2][T / 32];
+  __shared__ __align__(16) float s_red[2][T / 32][2 * R];
   const int tid = threadIdx.x;
   const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16), yb = static_cast<uint32_t>(d8) * 16;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
@@ -316,55 +354,76 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
     }
   int s = 0, flip = 0;
   uint32_t ph = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
-    const float mu = __ldg(mean + r), rs = __ldg(rstd + r);
-    mbar_wait_drain(&full[s], ph);
-    const uint8_t* row = ring + static_cast<size_t>(s) * sb;
-    float res[V][8];
-    float2 sum = make_float2(0.0f, 0.0f);
-    float xh[V][8], ge[V][8];
+  const int64_t step = gridDim.x;
+  for (int64_t r = blockIdx.x; r < rows; r += R * step, flip ^= 1) {
+    Vec8<F32> xv[R][V], res[R][V];
+    Vec8<false> ev[R][V];
+    float mu[R], rs[R], sum[2 * R];   // of g dy and of g dy x^, row by row
+    int freed[R];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
-      if (c < d8) {
-        float e[8];
-        smem_vec8<F32>(row, c, xh[i]);
-        smem_vec8<false>(row + xb, c, e);
-        if (dres) {
-          smem_vec8<F32>(row + xb + yb, c, res[i]);
-        } else {
+    for (int h = 0; h < R; ++h) {
+      const int64_t at = min(r + h * step, rows - 1);
+      mu[h] = __ldg(mean + at);
+      rs[h] = __ldg(rstd + at);
+    }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) res[i][j] = 0.0f;
-        }
+    for (int h = 0; h < R; ++h) {
+      const bool have = h == 0 || r + h * step < rows;
+      const uint8_t* row = ring + static_cast<size_t>(s) * sb;
+      sum[2 * h] = sum[2 * h + 1] = 0.0f;
+      if (have) {
+        mbar_wait_drain(&full[s], ph);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          xh[i][j] = (xh[i][j] - mu) * rs;
-          ge[i][j] = g[i][j] * e[j];
-          sum.x += ge[i][j];
-          sum.y = fmaf(ge[i][j], xh[i][j], sum.y);
-          dg[i][j] = fmaf(e[j], xh[i][j], dg[i][j]);
-          db[i][j] += e[j];
+        for (int i = 0; i < V; ++i) {
+          const int c = tid + i * T;
+          if (c < d8) {
+            xv[h][i] = smem_vec8<F32>(row, c);
+            ev[h][i] = smem_vec8<false>(row + xb, c);
+            if (dres) res[h][i] = smem_vec8<F32>(row + xb + yb, c);
+            else res[h][i].zero();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float e = ev[h][i].get(j), xh = (xv[h][i].get(j) - mu[h]) * rs[h], ge = g[i][j] * e;
+              sum[2 * h] += ge;
+              sum[2 * h + 1] = fmaf(ge, xh, sum[2 * h + 1]);
+              dg[i][j] = fmaf(e, xh, dg[i][j]);
+              db[i][j] += e;
+            }
+          }
         }
       }
-    }
-    sum = row_sum2<T>(sum, s_red[flip]);
-    // every thread has read the buffer
-    const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
-    if (tid == 0 && next < rows) fetch(s, next);
-    const float m1 = sum.x * inv_d, m2 = sum.y * inv_d;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
-      if (c < d8) {
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fmaf(rs, ge[i][j] - m1 - xh[i][j] * m2, res[i][j]);
-        Vec8<F32>::store(dx, r * d8 + c, o);
+      freed[h] = s;
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1u;
       }
     }
-    if (++s == stages) {
-      s = 0;
-      ph ^= 1u;
+    block_sums<T, 2 * R>(sum, s_red[flip]);
+    // every thread has read the buffers
+    if (tid == 0)
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const int64_t next = r + (h + stages) * step;
+        if (next < rows) fetch(freed[h], next);
+      }
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const int64_t row = r + h * step;
+      if (h > 0 && row >= rows) break;
+      const float m1 = sum[2 * h] * inv_d, m2 = sum[2 * h + 1] * inv_d;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * T;
+        if (c < d8) {
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float xh = (xv[h][i].get(j) - mu[h]) * rs[h];
+            o[j] = fmaf(rs[h], g[i][j] * ev[h][i].get(j) - m1 - xh * m2, res[h][i].get(j));
+          }
+          Vec8<F32>::store(dx, row * d8 + c, o);
+        }
+      }
     }
   }
   float* p = part + static_cast<int64_t>(blockIdx.x) * 16 * d8;
@@ -710,9 +769,9 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
       const auto* px = static_cast<const uint8_t*>(x);
       const auto* pd = static_cast<const uint8_t*>(dy);
       const auto* pr = static_cast<const uint8_t*>(dres);
-      return x_f32 ? launch_ring<layernorm_bwd_ring_kernel<true, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages,
+      return x_f32 ? launch_ring<layernorm_bwd_ring_kernel<true, T, V, 1>>(grid, T, stages * bytes, st, rows, d / 8, stages,
                                                                         pd, px, gamma, mean, rstd, pr, dx, scratch)
-                   : launch_ring<layernorm_bwd_ring_kernel<false, T, V>>(grid, T, stages * bytes, st, rows, d / 8,
+                   : launch_ring<layernorm_bwd_ring_kernel<false, T, V, 2>>(grid, T, stages * bytes, st, rows, d / 8,
                                                                          stages, pd, px, gamma, mean, rstd, pr, dx,
                                                                          scratch);
     });
