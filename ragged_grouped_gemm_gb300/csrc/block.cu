@@ -50,14 +50,16 @@ struct Vec8<true> {
   }
 };
 
-// Sum over the T threads of a row.  T > 32: the whole block shares the row; s
-// holds one value per warp, and a caller alternates between two of them, so
-// that one barrier a sum is enough.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* s) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (T == 32) return v;
+  return v;
+}
+// Sum over the T threads of a block; s holds one value per warp, and a caller
+// alternates between two of them, so that one barrier a sum is enough.
+template <int T>
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = 0.0f;
@@ -65,30 +67,38 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
   for (int w = 0; w < T / 32; ++w) t += s[w];
   return t;
 }
-template <int T>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* s) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if (T == 32) return v;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int w = 0; w < T / 32; ++w) {
-    t.x += s[w].x;
-    t.y += s[w].y;
-  }
-  return t;
+
+// ---- clusters: C blocks of a cluster hold the columns of a row between them
+template <int C>
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r = 0;
+  if constexpr (C > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster arrives; shared memory written before is visible after.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(const void* at, uint32_t rank, float v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32x2(const void* at, uint32_t rank, float v, float w) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v), "f"(w) : "memory");
 }
 
-// N sums (2 or 4) over the T threads of a block at once.  While two lanes have more
-// than one sum between them, each passes the half that the other goes on with; the
-// warps' sums are joined the same way: 5 + 6 and 7 + 12 shuffles with 16 warps.
-template <int T, int N>
+// N sums (2 or 4) over the T threads of each of C blocks at once.  While two lanes
+// have more than one sum between them, each passes the half that the other goes on
+// with; in one block the warps' sums are joined the same way (16 warps: 5 + 6 shuffles for
+// two sums, 7 + 12 for four).  In a cluster each warp leaves its sums with every block.  s
+// holds N values a warp of the cluster, and a caller alternates between two of them.
+template <int T, int N, int C>
 __device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[N]) {
+  constexpr int W = T / 32;
   const int lane = threadIdx.x & 31;
   float a;
   if constexpr (N == 4) {
@@ -103,41 +113,58 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[N]) {
   }
 #pragma unroll
   for (int o = 16 / N; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (lane % (32 / N) == 0) s[threadIdx.x >> 5][lane / (32 / N)] = a;
-  __syncthreads();
-  // the warps' sums: lane l takes Q of warp l % W's
-  constexpr int W = T / 32, P = 32 / W, Q = N > P ? N / P : 1;
-  float q[Q];
+  const int warp = threadIdx.x >> 5, which = lane / (32 / N);
+  const bool mine = lane % (32 / N) == 0;
+  if constexpr (C > 1) {
+    static_assert(C * W % 32 == 0);
+    const uint32_t me = cluster_rank<C>();
+    if (mine)
 #pragma unroll
-  for (int j = 0; j < Q; ++j) {
-    q[j] = s[lane % W][lane / W % (N / Q) * Q + j];
+      for (int c = 0; c < C; ++c) st_cluster_f32(&s[me * W + warp][which], c, a);
+    cluster_sync();
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) q[j] += __shfl_xor_sync(0xffffffffu, q[j], o);
+    for (int j = 0; j < N; ++j) {
+      v[j] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < C * W; w += 32) v[j] += s[w + lane][j];
+      v[j] = warp_sum(v[j]);
+    }
+  } else {
+    if (mine) s[warp][which] = a;
+    __syncthreads();
+    // lane l takes Q sums of warp l % W
+    constexpr int P = 32 / W, Q = N > P ? N / P : 1;
+    float q[Q];
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      q[j] = s[lane % W][lane / W % (N / Q) * Q + j];
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) q[j] += __shfl_xor_sync(0xffffffffu, q[j], o);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = N == Q ? q[j] : __shfl_sync(0xffffffffu, q[j % Q], j / Q * W);
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = N == Q ? q[j] : __shfl_sync(0xffffffffu, q[j % Q], j / Q * W);
 }
 
-// T threads a row, V vectors of eight columns a thread.  The mean and then the
-// squared deviations from it are summed over the registers that hold the row,
-// so the variance loses nothing to a large mean.
-template <bool F32, int T, int V>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t rows, int d8, const void* __restrict__ x,
-                                                                      const float* __restrict__ gamma,
-                                                                      const float* __restrict__ beta, float eps,
-                                                                      void* __restrict__ y, float* __restrict__ mean,
-                                                                      float* __restrict__ rstd) {
-  __shared__ float s_red[2][T == 32 ? 1 : T / 32];
-  constexpr int RPB = T < 256 ? 256 / T : 1;
-  const int tid = threadIdx.x % T;
+// A warp a row of at most 1024 elements, V vectors of eight columns a lane.  The mean
+// and then the squared deviations from it are summed over the registers that hold the
+// row, so the variance loses nothing to a large mean.
+constexpr int kRowWarps = 8;   // rows of a block
+template <bool F32, int V>
+__global__ void __launch_bounds__(kRowWarps * 32) layernorm_kernel(int64_t rows, int d8, const void* __restrict__ x,
+                                                                   const float* __restrict__ gamma,
+                                                                   const float* __restrict__ beta, float eps,
+                                                                   void* __restrict__ y, float* __restrict__ mean,
+                                                                   float* __restrict__ rstd) {
+  const int lane = threadIdx.x & 31;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / T; r < rows;
-       r += static_cast<int64_t>(gridDim.x) * RPB) {
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * kRowWarps) {
     Vec8<F32> v[V];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
+      const int c = lane + i * 32;
       if (c < d8) v[i].load(x, r * d8 + c);
       else v[i].zero();
     }
@@ -145,25 +172,25 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += v[i].get(j);
-    const float mu = row_sum<T>(sum, s_red[0]) * inv_d;
+    const float mu = warp_sum(sum) * inv_d;
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (tid + i * T < d8) {
+      if (lane + i * 32 < d8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float e = v[i].get(j) - mu;
           sq = fmaf(e, e, sq);
         }
       }
-    const float rs = 1.0f / sqrtf(row_sum<T>(sq, s_red[1]) * inv_d + eps);
-    if (tid == 0) {
+    const float rs = 1.0f / sqrtf(warp_sum(sq) * inv_d + eps);
+    if (lane == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
+      const int c = lane + i * 32;
       if (c < d8) {
         Vec8<true> g, b;
         g.load(gamma, c);
@@ -179,7 +206,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
 }
 
 // ---- rows through shared memory
-// For rows of 1024 to 8192 elements the inputs arrive by bulk copies in a ring
+// For rows of more than 1024 elements the inputs arrive by bulk copies in a ring
 // of row buffers, so that the loads of the next rows run under the arithmetic
 // and the block sums of this one; gamma, beta and the gradients' sums stay in
 // registers.  4096 rows of 7168 bf16 numbers: 25.8 us forward, 41 us backward with
@@ -189,6 +216,11 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(int64_t ro
 // and 16 elements a thread, about 1.7 us.  Forward, one sum a row by taking the next
 // row's mean along needs twice the registers, one block an SM: 31.9 us; two rows
 // together spill at two blocks an SM: 40.8.
+// Above 8192 elements a cluster of two blocks, above 16384 one of four, shares the row,
+// each with a ring of its own columns.  2730 rows of 12288 bf16 numbers: 40 us forward,
+// 64 backward; 1024 of 32768 40 and 68 (all 19.8 and 39.6 at the rate of a plain copy).
+// From global memory with 1024 threads a row they were 64, 88, 47 and 147: no loads under
+// the sums, and the backward's sums did not fit the registers.
 constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its blocks
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -215,6 +247,27 @@ __device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8])
   v.load(p, c);
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = v.get(j);
+}
+
+// A block's share of the rows: vectors first .. first + n8 - 1 of rows row0, row0 + step, ...
+struct Part {
+  int first, n8;
+  int64_t row0, step;
+};
+template <int C>
+__device__ __forceinline__ Part part_of(int d8) {
+  if constexpr (C == 1) return {0, d8, blockIdx.x, gridDim.x};
+  const int per = (d8 + C - 1) / C, first = per * static_cast<int>(cluster_rank<C>());
+  return {first, min(per, d8 - first), blockIdx.x / C, gridDim.x / C};
+}
+// Columns of a row that warp w of block `rank` holds.
+template <int T, int V, int C>
+__device__ __forceinline__ float warp_columns(int d8, int rank, int w) {
+  const int per = (d8 + C - 1) / C, n8 = min(per, d8 - per * rank);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) n += max(0, min(32, n8 - i * T - w * 32));
+  return static_cast<float>(8 * n);
 }
 
 // T threads share a row, V vectors of eight columns each; `stages` row buffers.
@@ -276,7 +329,7 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += v[i][j];
     }
-    const float mu = row_sum<T>(sum, s_red[0]) * inv_d;
+    const float mu = block_sum<T>(sum, s_red[0]) * inv_d;
     // every thread has read the buffer: the row after next `stages` may land in it
     const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
     if (tid == 0 && next < rows) fetch(s, next);
@@ -290,7 +343,7 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
           sq = fmaf(e, e, sq);
         }
       }
-    const float rs = 1.0f / sqrtf(row_sum<T>(sq, s_red[1]) * inv_d + eps);
+    const float rs = 1.0f / sqrtf(block_sum<T>(sq, s_red[1]) * inv_d + eps);
     if (tid == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
@@ -312,18 +365,165 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
   }
 }
 
-// R rows (blockIdx.x + i gridDim.x) pass through a block together, packed: two bf16 rows
+// T threads of C blocks share a row, V vectors of eight columns each; `stages` row
+// buffers.  R rows an exchange between the blocks, which costs about 0.6 us: every warp
+// takes its columns' mean m_w and the squares about it, q_w, and mean = sum n_w m_w / n,
+// variance = sum (q_w + n_w (m_w - mean)^2) / n, which like two passes over the row loses
+// nothing to a large mean.  Two exchanges of one row each, two blocks an SM: 2730 x 12288
+// 54.7 us, one 43.7; four bf16 (two fp32) rows an exchange, one block an SM, 40.2.
+template <bool F32, int T, int V, int R, int C>
+__global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
+    int64_t rows, int d8, int stages, const uint8_t* __restrict__ x, const float* __restrict__ gamma,
+    const float* __restrict__ beta, float eps, void* __restrict__ y, float* __restrict__ mean,
+    float* __restrict__ rstd) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[8];
+  constexpr int W = C * T / 32, K = W / 32;   // warps of a row; a lane joins K of them
+  static_assert(W % 32 == 0);
+  __shared__ float2 s_red[2][W][R];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const Part part = part_of<C>(d8);
+  const int n8 = part.n8;
+  const uint32_t xb = static_cast<uint32_t>(n8) * (F32 ? 32 : 16);
+  const float inv_d = 1.0f / static_cast<float>(d8 * 8);
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  float g[V][8], b[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = part.first + min(tid + i * T, n8 - 1);
+    load_f32x8(gamma, c, g[i]);
+    if (beta) load_f32x8(beta, c, b[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
+  }
+  cluster_sync();   // every block of the cluster has started
+  const int me = static_cast<int>(cluster_rank<C>()) * (T / 32) + (tid >> 5);
+  const float own_n = warp_columns<T, V, C>(d8, me / (T / 32), me % (T / 32)), own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
+  float wn[K], winv[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int w = lane + 32 * k;
+    wn[k] = warp_columns<T, V, C>(d8, w / (T / 32), w % (T / 32));
+    winv[k] = wn[k] > 0.0f ? 1.0f / wn[k] : 0.0f;
+  }
+  auto fetch = [&](int s, int64_t r) {
+    mbar_arrive_expect_tx(&full[s], xb);
+    bulk_load(ring + static_cast<size_t>(s) * xb, x + (r * d8 + part.first) * (F32 ? 32 : 16), xb, &full[s]);
+  };
+  if (tid == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t r = part.row0 + static_cast<int64_t>(s) * part.step;
+      if (r < rows) fetch(s, r);
+    }
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  for (int64_t r = part.row0; r < rows; r += R * part.step, flip ^= 1) {
+    Vec8<F32> v[R][V];
+    float sum[R], sq[R];
+    int freed[R];
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const bool have = h == 0 || r + h * part.step < rows;
+      const uint8_t* row = ring + static_cast<size_t>(s) * xb;
+      sum[h] = sq[h] = 0.0f;
+      if (have) mbar_wait_drain(&full[s], ph);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * T;
+        if (have && c < n8) v[h][i] = smem_vec8<F32>(row, c);
+        else v[h][i].zero();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[h] += v[h][i].get(j);
+      }
+      freed[h] = s;
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      sum[h] = warp_sum(sum[h]);
+      const float wmean = sum[h] * own_inv;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (tid + i * T < n8) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float e = v[h][i].get(j) - wmean;
+            sq[h] = fmaf(e, e, sq[h]);
+          }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      sq[h] = warp_sum(sq[h]);
+      if (lane < C) st_cluster_f32x2(&s_red[flip][me][h], lane, sum[h], sq[h]);
+    }
+    cluster_sync();
+    // every thread has read the buffers: later rows may land in them
+    if (tid == 0)
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const int64_t next = r + (h + stages) * part.step;
+        if (next < rows) fetch(freed[h], next);
+      }
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const int64_t row = r + h * part.step;
+      if (h > 0 && row >= rows) break;
+      float2 p[K];
+      float mu = 0.0f, var = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        p[k] = s_red[flip][lane + 32 * k][h];
+        mu += p[k].x;
+      }
+      mu = warp_sum(mu) * inv_d;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float e = fmaf(p[k].x, winv[k], -mu);
+        var += fmaf(wn[k] * e, e, p[k].y);
+      }
+      const float rs = 1.0f / sqrtf(warp_sum(var) * inv_d + eps);
+      if (tid == 0 && part.first == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = rs;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * T;
+        if (c < n8) {
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fmaf((v[h][i].get(j) - mu) * rs, g[i][j], b[i][j]);
+          Vec8<false>::store(y, row * d8 + part.first + c, o);
+        }
+      }
+    }
+  }
+}
+
+// R rows pass through a block together, packed: two bf16 rows
 // share the block sum, 41 us against 46; fp32 rows have no registers for it.
-template <bool F32, int T, int V, int R>
+template <bool F32, int T, int V, int R, int C>
 __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
     const uint8_t* __restrict__ dres, void* __restrict__ dx, float* __restrict__ part) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
-  __shared__ __align__(16) float s_red[2][T / 32][2 * R];
+  __shared__ __align__(16) float s_red[2][C * T / 32][2 * R];
   const int tid = threadIdx.x;
-  const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16), yb = static_cast<uint32_t>(d8) * 16;
+  const Part own = part_of<C>(d8);
+  const int n8 = own.n8;
+  const uint32_t xb = static_cast<uint32_t>(n8) * (F32 ? 32 : 16), yb = static_cast<uint32_t>(n8) * 16;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -334,28 +534,30 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
   float g[V][8], dg[V][8], db[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    load_f32x8(gamma, min(tid + i * T, d8 - 1), g[i]);
+    load_f32x8(gamma, own.first + min(tid + i * T, n8 - 1), g[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
   }
-  __syncthreads();
+  if constexpr (C > 1) cluster_sync();   // every block of the cluster has started
+  else __syncthreads();
   const uint32_t sb = xb + yb + (dres ? xb : 0);   // a row's x, dy and dres
   auto fetch = [&](int s, int64_t r) {
     uint8_t* dst = ring + static_cast<size_t>(s) * sb;
     mbar_arrive_expect_tx(&full[s], sb);
-    bulk_load(dst, x + r * xb, xb, &full[s]);
-    bulk_load(dst + xb, dy + r * yb, yb, &full[s]);
-    if (dres) bulk_load(dst + xb + yb, dres + r * xb, xb, &full[s]);
+    const int64_t at = r * d8 + own.first;
+    bulk_load(dst, x + at * (F32 ? 32 : 16), xb, &full[s]);
+    bulk_load(dst + xb, dy + at * 16, yb, &full[s]);
+    if (dres) bulk_load(dst + xb + yb, dres + at * (F32 ? 32 : 16), xb, &full[s]);
   };
   if (tid == 0)
     for (int s = 0; s < stages; ++s) {
-      const int64_t r = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      const int64_t r = own.row0 + static_cast<int64_t>(s) * own.step;
       if (r < rows) fetch(s, r);
     }
   int s = 0, flip = 0;
   uint32_t ph = 0;
-  const int64_t step = gridDim.x;
-  for (int64_t r = blockIdx.x; r < rows; r += R * step, flip ^= 1) {
+  const int64_t step = own.step;
+  for (int64_t r = own.row0; r < rows; r += R * step, flip ^= 1) {
     Vec8<F32> xv[R][V], res[R][V];
     Vec8<false> ev[R][V];
     float mu[R], rs[R], sum[2 * R];   // of g dy and of g dy x^, row by row
@@ -376,7 +578,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int c = tid + i * T;
-          if (c < d8) {
+          if (c < n8) {
             xv[h][i] = smem_vec8<F32>(row, c);
             ev[h][i] = smem_vec8<false>(row + xb, c);
             if (dres) res[h][i] = smem_vec8<F32>(row + xb + yb, c);
@@ -398,7 +600,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
         ph ^= 1u;
       }
     }
-    block_sums<T, 2 * R>(sum, s_red[flip]);
+    block_sums<T, 2 * R, C>(sum, s_red[flip]);
     // every thread has read the buffers
     if (tid == 0)
 #pragma unroll
@@ -414,23 +616,23 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = tid + i * T;
-        if (c < d8) {
+        if (c < n8) {
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float xh = (xv[h][i].get(j) - mu[h]) * rs[h];
             o[j] = fmaf(rs[h], g[i][j] * ev[h][i].get(j) - m1 - xh * m2, res[h][i].get(j));
           }
-          Vec8<F32>::store(dx, row * d8 + c, o);
+          Vec8<F32>::store(dx, row * d8 + own.first + c, o);
         }
       }
     }
   }
-  float* p = part + static_cast<int64_t>(blockIdx.x) * 16 * d8;
+  float* p = part + (own.row0 * 2 * d8 + own.first) * 8;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = tid + i * T;
-    if (c < d8) {
+    if (c < n8) {
       Vec8<true>::store(p, c, dg[i]);
       Vec8<true>::store(p + 8 * d8, c, db[i]);
     }
@@ -441,28 +643,26 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
 // dbeta: two per SM.
 constexpr int kNormBlocks = 304;
 
-template <bool F32, int T, int V>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
+template <bool F32, int V>
+__global__ void __launch_bounds__(kRowWarps * 32) layernorm_bwd_kernel(
     int64_t rows, int d8, const uint4* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ dres,
     void* __restrict__ dx, float* __restrict__ part) {
-  __shared__ float2 s_red[2][T == 32 ? 1 : T / 32];
-  constexpr int RPB = T < 256 ? 256 / T : 1;
-  const int tid = threadIdx.x % T;
+  __shared__ float s_part[kRowWarps][V * 256];
+  const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   float dg[V][8], db[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
-  int flip = 0;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / T; r < rows;
-       r += static_cast<int64_t>(gridDim.x) * RPB, flip ^= 1) {
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + w; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * kRowWarps) {
     Vec8<F32> xv[V];
     Vec8<false> dv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
+      const int c = lane + i * 32;
       if (c < d8) {
         xv[i].load(x, r * d8 + c);
         dv[i].load(dy, r * d8 + c);
@@ -475,7 +675,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
+      const int c = lane + i * 32;
       if (c < d8) {
         Vec8<true> g;
         g.load(gamma, c);
@@ -490,11 +690,10 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
         }
       }
     }
-    sum = row_sum2<T>(sum, s_red[flip]);
-    const float m1 = sum.x * inv_d, m2 = sum.y * inv_d;
+    const float m1 = warp_sum(sum.x) * inv_d, m2 = warp_sum(sum.y) * inv_d;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
+      const int c = lane + i * 32;
       if (c < d8) {
         Vec8<true> g;
         g.load(gamma, c);
@@ -514,32 +713,19 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_bwd_kernel(
   // this block's partial sums [2][d]; rows of a block are added in order
   const int d = d8 * 8;
   float* p = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
-  if constexpr (RPB == 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * T;
-      if (c < d8) {
-        Vec8<true>::store(p, c, dg[i]);
-        Vec8<true>::store(p + d, c, db[i]);
-      }
-    }
-  } else {
-    __shared__ float s_part[RPB][T * V * 8];
-    const int w = threadIdx.x / T;
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      __syncthreads();
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int j = 0; j < 8; ++j) s_part[w][(lane + i * 32) * 8 + j] = which ? db[i][j] : dg[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += kRowWarps * 32) {
+      float t = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s_part[w][(tid + i * T) * 8 + j] = which ? db[i][j] : dg[i][j];
-      __syncthreads();
-      for (int c = threadIdx.x; c < d; c += blockDim.x) {
-        float t = 0.0f;
-#pragma unroll
-        for (int k = 0; k < RPB; ++k) t += s_part[k][c];
-        p[which * d + c] = t;
-      }
+      for (int k = 0; k < kRowWarps; ++k) t += s_part[k][c];
+      p[which * d + c] = t;
     }
   }
 }
@@ -687,36 +873,63 @@ int ring_stages(int64_t bytes, int blocks) {
   const int64_t n = std::min<int64_t>(8, kRingBytes / blocks / bytes);
   return n < 2 ? 0 : static_cast<int>(n);
 }
-template <auto K, class... A>
-cudaError_t launch_ring(unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+// Launches K on `clusters` clusters of C blocks.
+template <auto K, int C, class... A>
+cudaError_t launch_ring(int64_t clusters, unsigned block, size_t smem, cudaStream_t st, A... args) {
   // a ring's dynamic shared memory, allowed once a kernel
   static const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  return e != cudaSuccess ? e : launch_pdl(K, grid, block, smem, st, args...);
+  return e != cudaSuccess ? e : launch_pdl<C>(K, static_cast<unsigned>(clusters * C), block, smem, st, args...);
 }
-// Calls f(threads, vectors) with the ring kernels' shape of a row of 1024 < d <= 8192.
+// How many clusters of C blocks of K run at once, with `blocks` an SM.
+template <auto K, int C>
+int resident(int block, int blocks) {
+  if (C == 1) return num_sms() * blocks;
+  static const int n = [&] {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {C, 1, 1};
+    cfg.gridDim = dim3(C * num_sms());
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = kRingBytes / blocks;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, K, &cfg) != cudaSuccess || clusters < 1) {
+      cudaGetLastError();
+      return 1;
+    }
+    return clusters;
+  }();
+  return n;
+}
+template <bool F32, int T, int V, int C>
+constexpr auto forward_kernel() {
+  if constexpr (C > 1) return layernorm_cluster_kernel<F32, T, V, F32 ? 2 : 4, C>;
+  else return layernorm_ring_kernel<F32, T, V>;
+}
+// Calls f(threads, vectors, blocks) with the ring kernels' shape of a row of more than
+// 1024 elements: a cluster of 2 or 4 blocks shares a row of more than 8192 or 16384.
 template <class F>
 cudaError_t with_ring_shape(int d, F&& f) {
-  if (d <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-  if (d <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-  return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  using std::integral_constant;
+  if (d <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 1>(), integral_constant<int, 1>());
+  if (d <= 4096) return f(integral_constant<int, 256>(), integral_constant<int, 2>(), integral_constant<int, 1>());
+  if (d <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), integral_constant<int, 1>());
+  if (d <= 16384) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), integral_constant<int, 2>());
+  return f(integral_constant<int, 512>(), integral_constant<int, 2>(), integral_constant<int, 4>());
 }
 
-// Calls f(threads-per-row, vectors-per-thread) with the direct kernels' shape of d: a
-// warp a row up to 1024 elements, a block of 1024 threads a row above 8192.
+// Calls f(vectors) with the warp kernels' shape of a row of at most 1024 elements.
 template <class F>
 cudaError_t with_row_shape(int d, F&& f) {
-  const int d8 = d / 8;
-  auto pick = [&](auto t) {
-    constexpr int T = decltype(t)::value;
-    switch ((d8 + T - 1) / T) {
-      case 1: return f(t, std::integral_constant<int, 1>());
-      case 2: return f(t, std::integral_constant<int, 2>());
-      case 3: return f(t, std::integral_constant<int, 3>());
-      default: return f(t, std::integral_constant<int, 4>());
-    }
-  };
-  if (d8 <= 128) return pick(std::integral_constant<int, 32>());
-  return pick(std::integral_constant<int, 1024>());
+  switch ((d / 8 + 31) / 32) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    default: return f(std::integral_constant<int, 4>());
+  }
 }
 
 }  // namespace
@@ -725,27 +938,26 @@ cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, con
                              float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
-  if (d > 1024 && d <= 8192)
-    return with_ring_shape(d, [&](auto t, auto v) {
-      constexpr int T = decltype(t)::value, V = decltype(v)::value;
-      constexpr int per_sm = 1024 / T;
-      const int64_t bytes = static_cast<int64_t>(d) * (x_f32 ? 4 : 2);
+  if (d > 1024)
+    return with_ring_shape(d, [&](auto t, auto v, auto c) {
+      constexpr int T = decltype(t)::value, V = decltype(v)::value, C = decltype(c)::value;
+      constexpr int per_sm = C > 1 ? 1 : 1024 / T;
+      const int64_t bytes = static_cast<int64_t>((d / 8 + C - 1) / C) * (x_f32 ? 32 : 16);
       const int stages = ring_stages(bytes, per_sm);
-      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * per_sm));
       const auto* px = static_cast<const uint8_t*>(x);
-      return x_f32 ? launch_ring<layernorm_ring_kernel<true, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages, px,
-                                                                    gamma, beta, eps, y, mean, rstd)
-                   : launch_ring<layernorm_ring_kernel<false, T, V>>(grid, T, stages * bytes, st, rows, d / 8, stages,
-                                                                     px, gamma, beta, eps, y, mean, rstd);
+      auto run = [&](auto f32) {
+        constexpr bool F = decltype(f32)::value;
+        constexpr auto K = forward_kernel<F, T, V, C>();
+        return launch_ring<K, C>(std::min<int64_t>(rows, resident<K, C>(T, per_sm)), T, stages * bytes, st, rows, d / 8,
+                                 stages, px, gamma, beta, eps, y, mean, rstd);
+      };
+      return x_f32 ? run(std::true_type()) : run(std::false_type());
     });
-  return with_row_shape(d, [&](auto t, auto v) {
-    constexpr int T = decltype(t)::value, V = decltype(v)::value;
-    constexpr int RPB = T < 256 ? 256 / T : 1;
-    const int grid = static_cast<int>(std::min<int64_t>((rows + RPB - 1) / RPB, 1 << 20));
-    if (x_f32)
-      layernorm_kernel<true, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
-    else
-      layernorm_kernel<false, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
+  return with_row_shape(d, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    const int grid = static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 1 << 20));
+    const auto kern = x_f32 ? layernorm_kernel<true, V> : layernorm_kernel<false, V>;
+    kern<<<grid, kRowWarps * 32, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
     return cudaGetLastError();
   });
 }
@@ -759,34 +971,29 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
                                  float* dbeta, float* scratch, cudaStream_t st) {
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
   int grid = 0;
-  if (rows > 0 && d > 1024 && d <= 8192) {
-    const cudaError_t e = with_ring_shape(d, [&](auto t, auto v) {
-      constexpr int T = decltype(t)::value, V = decltype(v)::value;
+  if (rows > 0 && d > 1024) {
+    const cudaError_t e = with_ring_shape(d, [&](auto t, auto v, auto c) {
+      constexpr int T = decltype(t)::value, V = decltype(v)::value, C = decltype(c)::value;
       constexpr int per_sm = 512 / T;
-      const int64_t bytes = static_cast<int64_t>(d) * ((x_f32 ? 4 : 2) * (dres ? 2 : 1) + 2);
+      const int64_t bytes = static_cast<int64_t>((d / 8 + C - 1) / C) * 8 * ((x_f32 ? 4 : 2) * (dres ? 2 : 1) + 2);
       const int stages = ring_stages(bytes, per_sm);
-      grid = static_cast<int>(std::min<int64_t>({rows, kNormBlocks, static_cast<int64_t>(num_sms()) * per_sm}));
-      const auto* px = static_cast<const uint8_t*>(x);
-      const auto* pd = static_cast<const uint8_t*>(dy);
-      const auto* pr = static_cast<const uint8_t*>(dres);
-      return x_f32 ? launch_ring<layernorm_bwd_ring_kernel<true, T, V, 1>>(grid, T, stages * bytes, st, rows, d / 8, stages,
-                                                                        pd, px, gamma, mean, rstd, pr, dx, scratch)
-                   : launch_ring<layernorm_bwd_ring_kernel<false, T, V, 2>>(grid, T, stages * bytes, st, rows, d / 8,
-                                                                         stages, pd, px, gamma, mean, rstd, pr, dx,
-                                                                         scratch);
+      auto run = [&](auto f32) {
+        constexpr auto K = layernorm_bwd_ring_kernel<decltype(f32)::value, T, V, decltype(f32)::value ? 1 : 2, C>;
+        grid = static_cast<int>(std::min<int64_t>({rows, kNormBlocks, resident<K, C>(T, per_sm)}));
+        return launch_ring<K, C>(grid, T, stages * bytes, st, rows, d / 8, stages, static_cast<const uint8_t*>(dy),
+                                 static_cast<const uint8_t*>(x), gamma, mean, rstd, static_cast<const uint8_t*>(dres),
+                                 dx, scratch);
+      };
+      return x_f32 ? run(std::true_type()) : run(std::false_type());
     });
     if (e != cudaSuccess) return e;
   } else if (rows > 0) {
-    const cudaError_t e = with_row_shape(d, [&](auto t, auto v) {
-      constexpr int T = decltype(t)::value, V = decltype(v)::value;
-      constexpr int RPB = T < 256 ? 256 / T : 1;
-      grid = static_cast<int>(std::min<int64_t>((rows + RPB - 1) / RPB, kNormBlocks));
-      if (x_f32)
-        layernorm_bwd_kernel<true, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x, gamma,
-                                                                   mean, rstd, dres, dx, scratch);
-      else
-        layernorm_bwd_kernel<false, T, V><<<grid, T * RPB, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x,
-                                                                    gamma, mean, rstd, dres, dx, scratch);
+    const cudaError_t e = with_row_shape(d, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      grid = static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, kNormBlocks));
+      const auto kern = x_f32 ? layernorm_bwd_kernel<true, V> : layernorm_bwd_kernel<false, V>;
+      kern<<<grid, kRowWarps * 32, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x, gamma, mean, rstd, dres, dx,
+                                            scratch);
       return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + kBufs;
-  uint64_t* xbar = tempty + kBufs;    // the four warps of a lane quarter exchanging row maxima
+  uint64_t* xbar = tempty + kBufs;    // the warps of a lane quarter exchanging row maxima
   uint64_t* sfull = xbar + 4;         // scale products of four k-blocks written
   uint64_t* sempty = sfull + 2;
   uint64_t* mma_done = sempty + 2;

@@ -99,6 +99,26 @@ def test_layernorm_large_mean_constant_rows_and_not_finite():
     assert torch.isnan(y[4:]).all() and torch.isfinite(y[:4]).all() and torch.isfinite(dx[:4]).all()
 
 
+@pytest.mark.parametrize("n,d", [(320, 2048), (330, 8192), (310, 8256), (160, 16448)])
+def test_layernorm_large_mean_and_not_finite_beside_other_rows(n, d):
+    """Rows that pass through a block together keep to themselves."""
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, d, generator=g) + 1000.0
+    dy = torch.randn(n, d, generator=g).to(BF16).cuda()
+    gamma = torch.ones(d, device="cuda")
+    x = x.cuda()
+    _check_norm(x, dy, gamma, None, None, _norm(x, dy, gamma, None, None))
+    for kind in (F32, BF16):
+        z = (x - 1000.0).to(kind)
+        clean = _norm(z, dy, gamma, None, None)
+        z[1, d - 1], z[n - 1, 0] = float("inf"), float("nan")
+        y, mean, rstd, dx, _, _ = _norm(z, dy, gamma, None, None)
+        bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+        bad[1] = bad[n - 1] = True
+        assert torch.isnan(y[bad]).all()
+        assert torch.equal(y[~bad], clean[0][~bad]) and torch.equal(dx[~bad], clean[3][~bad])
+
+
 def test_layernorm_without_tokens_clears_the_weight_gradients():
     desc, ws = _desc(1, 128)
     desc.n_tok = 0
@@ -253,6 +273,22 @@ def test_block_captured_step_draws_anew_at_each_replay():
 def test_layernorm_many_rows(n, d, kind):
     """More rows than blocks: every block takes several, through all its row buffers."""
     g = torch.Generator().manual_seed(n + d + 1)
+    x = (torch.randn(n, d, generator=g) * 2 - 0.5).to(kind).cuda()
+    dres = torch.randn(n, d, generator=g).to(kind).cuda()
+    dy = torch.randn(n, d, generator=g).to(BF16).cuda()
+    gamma, beta = torch.randn(d, generator=g).cuda(), torch.randn(d, generator=g).cuda()
+    a = _norm(x, dy, gamma, beta, dres)
+    _check_norm(x, dy, gamma, beta, dres, a)
+    for u, v in zip(a, _norm(x, dy, gamma, beta, dres)):
+        assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    _check_norm(x, dy, gamma, None, None, _norm(x, dy, gamma, None, None))
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("n,d", [(153, 8256), (400, 9024), (311, 12288), (160, 16384), (77, 16448), (154, 24576), (80, 32768)])
+def test_layernorm_wide_rows(n, d, kind):
+    """Rows that two or four blocks share, several a cluster; the last block's share may be smaller."""
+    g = torch.Generator().manual_seed(n + d + 2)
     x = (torch.randn(n, d, generator=g) * 2 - 0.5).to(kind).cuda()
     dres = torch.randn(n, d, generator=g).to(kind).cuda()
     dy = torch.randn(n, d, generator=g).to(BF16).cuda()
