@@ -71,24 +71,19 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
 // ---- clusters: C blocks of a cluster hold the columns of a row between them
 template <int C>
 __device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r = 0;
-  if constexpr (C > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
+  return C > 1 ? cluster_ctarank() : 0u;
 }
 // Every thread of the cluster arrives; shared memory written before is visible after.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_sync_all();
 }
 __device__ __forceinline__ void st_cluster_f32(const void* at, uint32_t rank, float v) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(at), rank)), "f"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f32x2(const void* at, uint32_t rank, float v, float w) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v), "f"(w) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(at), rank)), "f"(v), "f"(w)
+               : "memory");
 }
 
 // N sums (2 or 4) over the T threads of each of C blocks at once.  While two lanes

@@ -214,6 +214,20 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float x) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // One lane of a converged warp.  The compiler knows this form: operands of the
 // TMA and tcgen05 instructions behind it go to uniform registers at once, where a
 // `lane == 0` branch makes each a loop over the lanes (four MMAs 250 clocks).
@@ -364,7 +378,7 @@ __device__ __forceinline__ void store_rows64(uint32_t stg, int lane, const uint3
   }
 }
 
-template <int BN, bool B_MN, int EPI>
+template <int BN, bool B_MN, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
   using C = Cfg<BN>;
   constexpr int S = C::kStages, kBufs = C::kBufs;
@@ -374,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   constexpr int COLS = BN / CG;       // columns of an epilogue warp
   constexpr int CW = 16;              // columns of a tensor-memory load
   static_assert(!DUAL || BN == 256, "w1 and w3 halves of a 256-column tile");
+  static_assert(!SPLIT || (EPI == FP8_EPI_BF16 && BN == 128), "128-column tiles of partial sums");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -392,7 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int G = p.groups;
-  const int unit0 = blockIdx.x, ustride = gridDim.x;
+  // SPLIT: a cluster has one tile (or none) and each CTA a share of its k-blocks, in fours
+  const int ranks = SPLIT ? static_cast<int>(cluster_nctarank()) : 1;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit0 = blockIdx.x / ranks, ustride = gridDim.x / ranks;
+  const int fours = (p.kb + 3) / 4;
+  const int kbeg = SPLIT ? fours * rank / ranks * 4 : 0;
+  const int kend = SPLIT ? min(p.kb, fours * (rank + 1) / ranks * 4) : p.kb;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -446,8 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  const int total = s_pre[G];
-  const int nkb = p.kb * p.sources;
+  // tiles; descending offsets can give a split launch more than it has clusters for
+  const int total = SPLIT ? min(s_pre[G], ustride) : s_pre[G];
+  if (SPLIT && threadIdx.x == 0 && s_pre[G] > ustride && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+  const int nkb = (kend - kbeg) * p.sources;
 
   if (warp < kAuxThreads / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
@@ -466,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           const CUtensorMap* ma = few ? &p.tmA32[src] : &p.tmA[src];
           const CUtensorMap* mb = &p.tmB[src];
           const int n0 = DUAL ? t.nt * 128 : t.nt * BN;
-          for (int k0 = 0; k0 < p.kb * BK; k0 += BK, ++it) {
+          for (int k0 = kbeg * BK; k0 < kend * BK; k0 += BK, ++it) {
             ok = warp_wait(&empty[s], ph, s_abort, p.status, 800);
             if (!ok) break;
             uint8_t* sA = smem + s * C::kStageBytes;
@@ -564,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       };
       uint32_t gi = 0;
       bool ok = true;
-      int tile = unit0, src = 0, k4 = 0;
+      int tile = unit0, src = 0, k4 = kbeg;
       Tile t{};
       if (tile < total) {
         t = find_tile(tile, p, s_pre);
-        load(t, 0, 0);
+        load(t, 0, kbeg);
       }
       while (tile < total) {
         float prod[2][NS][4];
@@ -583,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           }
         // the next four's factors are on their way while these are handed over
         k4 += 4;
-        if (k4 >= p.kb) {
-          k4 = 0;
+        if (k4 >= kend) {
+          k4 = kbeg;
           if (++src == p.sources) {
             src = 0;
             tile += ustride;
@@ -607,6 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
     }
     __syncwarp();
+    if constexpr (SPLIT) {
+      cluster_sync_all();
+      cluster_sync_all();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // -------------------------------------------------------------- epilogue
@@ -638,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
       for (int src = 0; ok && src < p.sources; ++src) {
-        for (int k4 = 0; ok && k4 < p.kb; k4 += 4, ++gi) {
+        for (int k4 = kbeg; ok && k4 < kend; k4 += 4, ++gi) {
           ok = warp_wait(&sfull[gi & 1u], (gi >> 1) & 1u, s_abort, p.status, 880);
           uint32_t ps = s_scale + ((gi & 1u) * 1024 + (DUAL ? 0 : cg * COLS / 128 * 128) + r) * 4;
-          const uint32_t pe = ps + min(4, p.kb - k4) * 1024;
+          const uint32_t pe = ps + min(4, kend - k4) * 1024;
 #pragma unroll 1   // four copies of the body miss the instruction cache: 410 us against 358
           for (; ok && ps != pe; ps += 1024) {
             const float sa = ld_shared_f32(ps), sb = DUAL ? ld_shared_f32(ps + 512) : sa;
@@ -683,7 +710,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           store_rows64(stg, lane, w, static_cast<uint8_t*>(out) + (row * p.n + col) * 2, static_cast<int64_t>(p.n) * 2,
                        rows, (p.n - col) / 8);
       };
-      if constexpr (EPI == FP8_EPI_BF16) {
+      if constexpr (SPLIT) {
+        // this CTA's sums, 512 bytes a row, over the operands' stages, which no load and no
+        // MMA uses any more; 16-byte chunk c of row r at c ^ (r & 31)
+        if (r < t.valid) {
+#pragma unroll
+          for (int i = 0; i < COLS / 4; ++i)
+            st_shared_v4(smem_u32(smem) + r * 512 + (((cg * (COLS / 4) + i) ^ (r & 31)) << 4),
+                         __float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]), __float_as_uint(acc[4 * i + 2]),
+                         __float_as_uint(acc[4 * i + 3]));
+        }
+      } else if constexpr (EPI == FP8_EPI_BF16) {
 #pragma unroll
         for (int c = 0; c < COLS / 32; ++c) rows_bf16(acc + 32 * c, p.out0, t.nt * BN + cg * COLS + c * 32);
       } else if constexpr (EPI == FP8_EPI_SWIGLU_BWD) {
@@ -762,6 +799,29 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
     }
     __syncwarp();
+    if constexpr (SPLIT) {
+      cluster_sync_all();
+      // a warp a row: the CTAs' sums added in the order of their k-blocks
+      if (unit0 < total) {
+        const Tile t = find_tile(unit0, p, s_pre);
+        const int col = t.nt * BN + lane * 4;
+        for (int r = rank * kEpiWarps + ew; r < t.valid; r += ranks * kEpiWarps) {
+          const uint32_t at = smem_u32(smem) + r * 512 + ((lane ^ (r & 31)) << 4);
+          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int c = 0; c < ranks; ++c) {
+            const float4 v = ld_cluster_f32x4(mapa_shared(at, c));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+          }
+          if (col < p.n)
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out0) + ((t.row0 + r) * static_cast<int64_t>(p.n) + col) * 2) =
+                make_uint2(bf2(sum.x, sum.y), bf2(sum.z, sum.w));
+        }
+      }
+      cluster_sync_all();   // no CTA's sums go away while another reads them
+    }
   }
 
   tc_fence_before();
@@ -804,25 +864,68 @@ bool code_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Allows the kernel its shared memory, once.
+template <auto K, int BN>
+cudaError_t prepare() {
+  static const cudaError_t err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      static_cast<int>(Cfg<BN>::smem_bytes(kMaxGroups)));
+  return err;
+}
+
 template <int BN, bool B_MN, int EPI>
 cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
-  using C = Cfg<BN>;
-  auto kern = fp8_gemm_kernel<BN, B_MN, EPI>;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(C::smem_bytes(kMaxGroups)));
-  });
+  constexpr auto K = fp8_gemm_kernel<BN, B_MN, EPI, false>;
+  const cudaError_t err = prepare<K, BN>();
   if (err != cudaSuccess) return err;
-  return launch_pdl(kern, static_cast<unsigned>(std::min<int64_t>(units, num_sms())), kThreads,
-                    C::smem_bytes(p.groups), st, p);
+  return launch_pdl(K, static_cast<unsigned>(std::min<int64_t>(units, num_sms())), kThreads,
+                    Cfg<BN>::smem_bytes(p.groups), st, p);
+}
+
+// Clusters of S CTAs of the split kernel that run at once.
+template <auto K, int S>
+int resident_clusters() {
+  static const int n = [] {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {S, 1, 1};
+    cfg.gridDim = dim3(S * num_sms());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<128>::smem_bytes(kMaxGroups);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (prepare<K, 128>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&clusters, K, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    return clusters;
+  }();
+  return n;
+}
+// Launches `units` tiles on clusters of S, or of fewer where they would not all run at
+// once or a CTA would have fewer than eight k-blocks; false: not split.
+template <bool B_MN, int S>
+bool launch_split(const Fp8Params& p, int64_t units, cudaStream_t st, cudaError_t* err) {
+  if constexpr (S == 1) {
+    return false;
+  } else {
+    constexpr auto K = fp8_gemm_kernel<128, B_MN, FP8_EPI_BF16, true>;
+    if (p.kb < 8 * S || units * S > num_sms() || units > resident_clusters<K, S>())
+      return launch_split<B_MN, S / 2>(p, units, st, err);
+    *err = launch_pdl<S>(K, static_cast<unsigned>(units * S), kThreads, Cfg<128>::smem_bytes(p.groups), st, p);
+    return true;
+  }
 }
 
 template <bool B_MN, int EPI>
 cudaError_t launch_pick(const Fp8Params& p, int bn, int64_t units, cudaStream_t st) {
   if constexpr (EPI == FP8_EPI_BF16)
-    if (bn == 128) return launch_form<128, B_MN, EPI>(p, units, st);
+    if (bn == 128) {
+      cudaError_t err;
+      if (p.sources == 1 && launch_split<B_MN, 8>(p, units, st, &err)) return err;
+      return launch_form<128, B_MN, EPI>(p, units, st);
+    }
   return launch_form<256, B_MN, EPI>(p, units, st);
 }
 

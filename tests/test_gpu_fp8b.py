@@ -114,6 +114,30 @@ def test_grouped_product(n, k, mn):
         assert (err <= _product_tol(ref, mag, k)).all(), (sizes, float((err - _product_tol(ref, mag, k)).max()))
 
 
+@pytest.mark.parametrize("mn", [False, True])
+@pytest.mark.parametrize("sizes,n,k", [([8], 144, 2048), ([1, 0, 130], 512, 2064), ([3, 40], 1040, 4112),
+                                       ([300], 272, 8208), ([1], 4112, 1168), ([0, 129, 0], 16, 16400)])
+def test_grouped_product_split_along_the_contraction(sizes, n, k, mn):
+    """Few tiles: clusters of CTAs share each.  At most nb / ranks + ranks <= nb additions a sum."""
+    g = torch.Generator().manual_seed(n + k)
+    rows = sum(sizes)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    x = torch.randn(rows, k, generator=g).to(torch.bfloat16)
+    w, ws = _weights(g, len(sizes), *((k, n) if mn else (n, k)))
+    codes, scales = _quantise(x)
+    work = torch.empty(api.moe_grouped_gemm_fp8_workspace_size(len(sizes), rows, n, k), dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(work)
+    outs = []
+    for _ in range(3):
+        out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        api.moe_grouped_gemm_fp8(codes, scales, torch.from_numpy(off).cuda(), w, ws, out, work, b_mn=mn)
+        outs.append(out)
+    assert api.moe_get_device_status(work) == (0, 0)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])   # the same order every time
+    ref, mag = _product_ref(codes, scales, off, w, ws, mn)
+    assert (np.abs(np32(outs[0]) - ref) <= _product_tol(ref, mag, k)).all()
+
+
 def test_grouped_product_rows_of_no_group_and_offsets_past_the_rows():
     g = torch.Generator().manual_seed(1)
     x = torch.randn(40, 128, generator=g).to(torch.bfloat16)
