@@ -173,6 +173,13 @@ __global__ void __launch_bounds__(256) fp8_quant_scatter_kernel(const uint4* __r
 //
 // GEMM1 (SwiGLU): a tile holds 128 columns of w1 and the same 128 of w3, which
 // is one scale block of h.
+//
+// Few tiles: one CTA takes about 0.35 us a k-block of a long contraction while other SMs
+// idle.  Where 2, 4 or 8 CTAs a tile still all run at once and have eight k-blocks
+// each, a cluster shares the tile; the CTAs leave their sums in shared memory and add each
+// other's, row by row, in the order of the k-blocks.  8 rows of 2048 x 7168: 11.1 us
+// (one CTA a tile 20.5), a row of 7168 x 7168 15.1 (21.1), two groups of one row of
+// 4096 x 14336 25.8 (36.8); a token through one expert of 7168 x 2048, whole layer, 35.9 (50.7).
 constexpr int BM = 128;
 constexpr int BK = 128;              // contraction elements (bytes) of a k-block
 constexpr int kAuxThreads = 128;
@@ -226,6 +233,13 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ float swiglu(float a1, float a3) { return __fdividef(a1, 1.0f + __expf(-a1)) * a3; }
+// The scale of a block of h with the largest magnitude m: h below 448e-37 is zero here.
+__device__ __forceinline__ float scale_of_h(float m) {
+  const float s = m * (1.0f / 448.0f);
+  return s > 1e-37f ? s : 1.0f;
 }
 
 // One lane of a converged warp.  The compiler knows this form: operands of the
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   constexpr int COLS = BN / CG;       // columns of an epilogue warp
   constexpr int CW = 16;              // columns of a tensor-memory load
   static_assert(!DUAL || BN == 256, "w1 and w3 halves of a 256-column tile");
-  static_assert(!SPLIT || (EPI == FP8_EPI_BF16 && BN == 128), "128-column tiles of partial sums");
+  static_assert(!SPLIT || EPI == FP8_EPI_SWIGLU_FWD || (EPI == FP8_EPI_BF16 && BN == 128), "forms of partial sums");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -711,14 +725,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                        rows, (p.n - col) / 8);
       };
       if constexpr (SPLIT) {
-        // this CTA's sums, 512 bytes a row, over the operands' stages, which no load and no
-        // MMA uses any more; 16-byte chunk c of row r at c ^ (r & 31)
+        // this CTA's sums over the operands' stages, which no load and no MMA uses any
+        // more; 16-byte chunk c of row r at c ^ (r & 31)
         if (r < t.valid) {
 #pragma unroll
-          for (int i = 0; i < COLS / 4; ++i)
-            st_shared_v4(smem_u32(smem) + r * 512 + (((cg * (COLS / 4) + i) ^ (r & 31)) << 4),
-                         __float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]), __float_as_uint(acc[4 * i + 2]),
+          for (int i = 0; i < COLS / 4; ++i) {
+            const int c = chunk_col(i / 4) / 4 + i % 4;
+            st_shared_v4(smem_u32(smem) + r * (BN * 4) + ((c ^ (r & 31)) << 4), __float_as_uint(acc[4 * i]),
+                         __float_as_uint(acc[4 * i + 1]), __float_as_uint(acc[4 * i + 2]),
                          __float_as_uint(acc[4 * i + 3]));
+          }
         }
       } else if constexpr (EPI == FP8_EPI_BF16) {
 #pragma unroll
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          acc[i] = __fdividef(acc[i], 1.0f + __expf(-acc[i])) * acc[HC + i];
+          acc[i] = swiglu(acc[i], acc[HC + i]);
           m = fmaxf(m, fabsf(acc[i]));
         }
         if (p.out3) {
@@ -779,9 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (!ok) break;
 #pragma unroll
         for (int g = 0; g < CG; ++g) m = fmaxf(m, mx[g * 128]);
-        const float s8 = m * (1.0f / 448.0f);
-        const float hscale = s8 > 1e-37f ? s8 : 1.0f;   // h below 448e-37 is zero here
-        const float rs = 1.0f / hscale;
+        const float hscale = scale_of_h(m), rs = 1.0f / hscale;
         if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = hscale;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out0) + (row + lane) * p.n + f);
 #pragma unroll
@@ -804,20 +818,45 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       // a warp a row: the CTAs' sums added in the order of their k-blocks
       if (unit0 < total) {
         const Tile t = find_tile(unit0, p, s_pre);
-        const int col = t.nt * BN + lane * 4;
+        const int col = t.nt * 128 + lane * 4;
         for (int r = rank * kEpiWarps + ew; r < t.valid; r += ranks * kEpiWarps) {
-          const uint32_t at = smem_u32(smem) + r * 512 + ((lane ^ (r & 31)) << 4);
-          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = 0; c < ranks; ++c) {
-            const float4 v = ld_cluster_f32x4(mapa_shared(at, c));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
+          const uint32_t at = smem_u32(smem) + r * (BN * 4) + ((lane ^ (r & 31)) << 4);
+          float a[NS][4] = {};
+          for (int c = 0; c < ranks; ++c)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              const float4 v = ld_cluster_f32x4(mapa_shared(at + j * 512, c));
+              a[j][0] += v.x;
+              a[j][1] += v.y;
+              a[j][2] += v.z;
+              a[j][3] += v.w;
+            }
+          const int64_t row = t.row0 + r;
+          auto row_bf16 = [&](const float* f, void* out) {
+            if (out && col < p.n)
+              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + (row * p.n + col) * 2) =
+                  make_uint2(bf2(f[0], f[1]), bf2(f[2], f[3]));
+          };
+          if constexpr (DUAL) {
+            row_bf16(a[0], p.out1);
+            row_bf16(a[1], p.out2);
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[0][i] = swiglu(a[0][i], a[1][i]);
+              m = fmaxf(m, fabsf(a[0][i]));
+            }
+            row_bf16(a[0], p.out3);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float hscale = scale_of_h(m), rs = 1.0f / hscale;
+            if (lane == 0) p.hs[row * p.hs_ld + t.nt] = hscale;
+            if (col < p.n)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out0) + row * p.n + col) =
+                  fp8_pack4(a[0][0] * rs, a[0][1] * rs, a[0][2] * rs, a[0][3] * rs);
+          } else {
+            row_bf16(a[0], p.out0);
           }
-          if (col < p.n)
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out0) + ((t.row0 + r) * static_cast<int64_t>(p.n) + col) * 2) =
-                make_uint2(bf2(sum.x, sum.y), bf2(sum.z, sum.w));
         }
       }
       cluster_sync_all();   // no CTA's sums go away while another reads them
@@ -881,8 +920,8 @@ cudaError_t launch_form(const Fp8Params& p, int64_t units, cudaStream_t st) {
                     Cfg<BN>::smem_bytes(p.groups), st, p);
 }
 
-// Clusters of S CTAs of the split kernel that run at once.
-template <auto K, int S>
+// Clusters of S CTAs of a split kernel that run at once.
+template <auto K, int BN, int S>
 int resident_clusters() {
   static const int n = [] {
     cudaLaunchConfig_t cfg{};
@@ -891,11 +930,11 @@ int resident_clusters() {
     at[0].val.clusterDim = {S, 1, 1};
     cfg.gridDim = dim3(S * num_sms());
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<128>::smem_bytes(kMaxGroups);
+    cfg.dynamicSmemBytes = Cfg<BN>::smem_bytes(kMaxGroups);
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (prepare<K, 128>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&clusters, K, &cfg) != cudaSuccess) {
+    if (prepare<K, BN>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&clusters, K, &cfg) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -905,27 +944,27 @@ int resident_clusters() {
 }
 // Launches `units` tiles on clusters of S, or of fewer where they would not all run at
 // once or a CTA would have fewer than eight k-blocks; false: not split.
-template <bool B_MN, int S>
+template <int BN, bool B_MN, int EPI, int S>
 bool launch_split(const Fp8Params& p, int64_t units, cudaStream_t st, cudaError_t* err) {
   if constexpr (S == 1) {
     return false;
   } else {
-    constexpr auto K = fp8_gemm_kernel<128, B_MN, FP8_EPI_BF16, true>;
-    if (p.kb < 8 * S || units * S > num_sms() || units > resident_clusters<K, S>())
-      return launch_split<B_MN, S / 2>(p, units, st, err);
-    *err = launch_pdl<S>(K, static_cast<unsigned>(units * S), kThreads, Cfg<128>::smem_bytes(p.groups), st, p);
+    constexpr auto K = fp8_gemm_kernel<BN, B_MN, EPI, true>;
+    if (p.sources > 1 || p.kb < 8 * S || units * S > num_sms() || units > resident_clusters<K, BN, S>())
+      return launch_split<BN, B_MN, EPI, S / 2>(p, units, st, err);
+    *err = launch_pdl<S>(K, static_cast<unsigned>(units * S), kThreads, Cfg<BN>::smem_bytes(p.groups), st, p);
     return true;
   }
 }
 
 template <bool B_MN, int EPI>
 cudaError_t launch_pick(const Fp8Params& p, int bn, int64_t units, cudaStream_t st) {
+  cudaError_t err;
   if constexpr (EPI == FP8_EPI_BF16)
-    if (bn == 128) {
-      cudaError_t err;
-      if (p.sources == 1 && launch_split<B_MN, 8>(p, units, st, &err)) return err;
-      return launch_form<128, B_MN, EPI>(p, units, st);
-    }
+    if (bn == 128)
+      return launch_split<128, B_MN, EPI, 8>(p, units, st, &err) ? err : launch_form<128, B_MN, EPI>(p, units, st);
+  if constexpr (EPI == FP8_EPI_SWIGLU_FWD)
+    if (launch_split<256, B_MN, EPI, 8>(p, units, st, &err)) return err;
   return launch_form<256, B_MN, EPI>(p, units, st);
 }
 

@@ -8,7 +8,7 @@ import torch
 import oracle as O
 from parity_util import BF16_TOL, host_params, np32, rel, routing_agreement, to_dev
 from ragged_grouped_gemm_gb300 import api
-from ragged_grouped_gemm_gb300.inputs import CONFIGS, make_dy, make_layer
+from ragged_grouped_gemm_gb300.inputs import CONFIGS, MoEConfig, make_dy, make_layer
 
 pytestmark = pytest.mark.gpu
 BAD_OFFSETS = 4
@@ -191,12 +191,7 @@ def test_grouped_product_many_groups_on_another_stream():
     assert (np.abs(np32(out) - ref) <= _product_tol(ref, mag, 64)).all()
 
 
-@pytest.mark.parametrize("name,tokens", [("tiny", None), ("small_softmax", None), ("small_sigmoid", None),
-                                         ("small_fine", None), ("small_sigmoid", 1)])
-def test_fp8b_layer_forward_backward(name, tokens):
-    cfg = CONFIGS[name].replace(precision="fp8b")
-    if tokens:
-        cfg = cfg.replace(n_tok=tokens)
+def _check_layer(cfg):
     p_cpu = make_layer(cfg, "cpu")
     p, h = to_dev(p_cpu), host_params(p_cpu)
     dy = make_dy(cfg, "cpu")
@@ -225,6 +220,21 @@ def test_fp8b_layer_forward_backward(name, tokens):
     infer = api.MoELayer(cfg, p, train=False)
     assert torch.equal(infer.forward(p["x"]).view(torch.int16), out.view(torch.int16))
     assert torch.equal(layer.forward(p["x"]).view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("name,tokens", [("tiny", None), ("small_softmax", None), ("small_sigmoid", None),
+                                         ("small_fine", None), ("small_sigmoid", 1)])
+def test_fp8b_layer_forward_backward(name, tokens):
+    cfg = CONFIGS[name].replace(precision="fp8b")
+    if tokens:
+        cfg = cfg.replace(n_tok=tokens)
+    _check_layer(cfg)
+
+
+@pytest.mark.parametrize("tokens,d,f,e,k", [(1, 2048, 256, 4, 2), (3, 4096, 2048, 4, 1), (2, 7168, 320, 8, 4), (130, 2112, 192, 2, 1)])
+def test_fp8b_layer_few_tokens(tokens, d, f, e, k):
+    """Products of few tiles, split along the contraction."""
+    _check_layer(MoEConfig("few", tokens, d, f, e, k, precision="fp8b"))
 
 
 def test_permute_fp8b_rows():
