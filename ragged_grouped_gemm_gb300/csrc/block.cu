@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) layernorm_kernel(int64_t rows,
                                                                    const float* __restrict__ beta, float eps,
                                                                    void* __restrict__ y, float* __restrict__ mean,
                                                                    float* __restrict__ rstd) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows;
@@ -644,6 +646,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) layernorm_bwd_kernel(
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ dres,
     void* __restrict__ dx, float* __restrict__ part) {
   __shared__ float s_part[kRowWarps][V * 256];
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   float dg[V][8], db[V][8];
@@ -788,6 +792,8 @@ __global__ void __launch_bounds__(256) combine_dropout_kernel(
     int64_t items, int d8, int K, const uint4* __restrict__ y_perm, const int32_t* __restrict__ row_of_copy,
     const float* __restrict__ topk_w, const uint4* __restrict__ y_shared, const void* __restrict__ resid,
     const int64_t* __restrict__ rng, uint32_t threshold, float scale, void* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
   uint64_t key = 0, first = 0;
   if (threshold) {
     key = static_cast<uint64_t>(__ldg(rng));
@@ -837,6 +843,8 @@ template <bool F32>
 __global__ void __launch_bounds__(256) dropout_bwd_kernel(int64_t items, const void* __restrict__ dout,
                                                           const int64_t* __restrict__ rng, uint32_t threshold,
                                                           float scale, void* __restrict__ dy) {
+  pdl_trigger();
+  pdl_wait();
   uint64_t key = 0, first = 0;
   if (threshold) {
     key = static_cast<uint64_t>(__ldg(rng));
@@ -952,8 +960,7 @@ cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, con
     constexpr int V = decltype(v)::value;
     const int grid = static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 1 << 20));
     const auto kern = x_f32 ? layernorm_kernel<true, V> : layernorm_kernel<false, V>;
-    kern<<<grid, kRowWarps * 32, 0, st>>>(rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
-    return cudaGetLastError();
+    return launch_pdl(kern, grid, kRowWarps * 32, 0, st, rows, d / 8, x, gamma, beta, eps, y, mean, rstd);
   });
 }
 
@@ -987,9 +994,8 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
       constexpr int V = decltype(v)::value;
       grid = static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, kNormBlocks));
       const auto kern = x_f32 ? layernorm_bwd_kernel<true, V> : layernorm_bwd_kernel<false, V>;
-      kern<<<grid, kRowWarps * 32, 0, st>>>(rows, d / 8, static_cast<const uint4*>(dy), x, gamma, mean, rstd, dres, dx,
-                                            scratch);
-      return cudaGetLastError();
+      return launch_pdl(kern, grid, kRowWarps * 32, 0, st, rows, d / 8, static_cast<const uint4*>(dy), x, gamma, mean,
+                        rstd, dres, dx, scratch);
     });
     if (e != cudaSuccess) return e;
   }
@@ -1004,9 +1010,8 @@ cudaError_t launch_combine_dropout(int n_tok, int d, int top_k, const void* y_pe
   // eight blocks an SM, each thread several items: 105 us at 4096 x 7168, K = 8, a block per 256 items 117
   const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(num_sms()) * 8));
   auto run = [&](auto kern) {
-    kern<<<grid, 256, 0, st>>>(items, d / 8, top_k, static_cast<const uint4*>(y_perm), row_of_copy, topk_w,
-                               static_cast<const uint4*>(y_shared), resid, rng, threshold, scale, out);
-    return cudaGetLastError();
+    return launch_pdl(kern, grid, 256, 0, st, items, d / 8, top_k, static_cast<const uint4*>(y_perm), row_of_copy,
+                      topk_w, static_cast<const uint4*>(y_shared), resid, rng, threshold, scale, out);
   };
   if (top_k <= 1) return f32 ? run(combine_dropout_kernel<true, 1>) : run(combine_dropout_kernel<false, 1>);
   if (top_k <= 2) return f32 ? run(combine_dropout_kernel<true, 2>) : run(combine_dropout_kernel<false, 2>);
@@ -1018,9 +1023,8 @@ cudaError_t launch_dropout_bwd(int64_t n, const void* dout, bool f32, const int6
   const int64_t items = n / 8;
   if (items <= 0) return cudaSuccess;
   const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(num_sms()) * 8));
-  if (f32) dropout_bwd_kernel<true><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
-  else dropout_bwd_kernel<false><<<grid, 256, 0, st>>>(items, dout, rng, threshold, scale, dy);
-  return cudaGetLastError();
+  return launch_pdl(f32 ? dropout_bwd_kernel<true> : dropout_bwd_kernel<false>, grid, 256, 0, st, items, dout, rng,
+                    threshold, scale, dy);
 }
 
 }  // namespace moe
