@@ -50,12 +50,13 @@ def _p(t: torch.Tensor | None, dtype=None, shape=None, name="tensor"):
 # The handle of the current stream without building a Stream object for it,
 # which took 3 of the 11 us that one norm's enqueue did.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _s(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
