@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
   }
   cluster_sync();   // every block of the cluster has started
   const int me = static_cast<int>(cluster_rank<C>()) * (T / 32) + (tid >> 5);
-  const float own_n = warp_columns<T, V, C>(d8, me / (T / 32), me % (T / 32)), own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
+  const float own_n = warp_columns<T, V, C>(d8, me / (T / 32), me % (T / 32));
+  const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
   float wn[K], winv[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {

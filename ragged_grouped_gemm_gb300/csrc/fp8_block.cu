@@ -483,7 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   const uint32_t tmem_base = *s_tmem;
   // tiles; descending offsets can give a split launch more than it has clusters for
   const int total = SPLIT ? min(s_pre[G], ustride) : s_pre[G];
-  if (SPLIT && threadIdx.x == 0 && s_pre[G] > ustride && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+  if constexpr (SPLIT) {
+    if (threadIdx.x == 0 && s_pre[G] > ustride && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+    __syncwarp();
+  }
   const int nkb = (kend - kbeg) * p.sources;
 
   if (warp < kAuxThreads / 32) {

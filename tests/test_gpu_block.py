@@ -285,7 +285,8 @@ def test_layernorm_many_rows(n, d, kind):
 
 
 @pytest.mark.parametrize("kind", [BF16, F32])
-@pytest.mark.parametrize("n,d", [(153, 8256), (400, 9024), (311, 12288), (160, 16384), (77, 16448), (154, 24576), (80, 32768)])
+@pytest.mark.parametrize("n,d", [(153, 8256), (400, 9024), (311, 12288), (160, 16384), (77, 16448), (154, 24576),
+                                 (80, 32768)])
 def test_layernorm_wide_rows(n, d, kind):
     """Rows that two or four blocks share, several a cluster; the last block's share may be smaller."""
     g = torch.Generator().manual_seed(n + d + 2)

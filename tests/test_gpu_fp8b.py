@@ -157,6 +157,20 @@ def test_grouped_product_rows_of_no_group_and_offsets_past_the_rows():
         assert (np.abs(np32(out) - ref) <= _product_tol(ref, mag, 128))[inside].all()
 
 
+def test_split_product_descending_offsets_are_flagged():
+    """More tiles than ascending offsets over these rows could have: those past the launch's clusters are left out."""
+    g = torch.Generator().manual_seed(5)
+    n, k = 144, 2048
+    codes, scales = _quantise(torch.randn(300, k, generator=g).to(torch.bfloat16))
+    w, ws = _weights(g, 5, n, k)
+    out = torch.empty(300, n, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(api.moe_grouped_gemm_fp8_workspace_size(5, 300, n, k), dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(work)
+    off = torch.tensor([0, 300, 0, 300, 0, 300], dtype=torch.int32, device="cuda")
+    api.moe_grouped_gemm_fp8(codes, scales, off, w, ws, out, work)
+    assert api.moe_get_device_status(work)[0] == BAD_OFFSETS
+
+
 def test_grouped_product_not_finite_rows_stay_apart():
     g = torch.Generator().manual_seed(2)
     x = torch.randn(9, 256, generator=g).to(torch.bfloat16)
@@ -231,7 +245,8 @@ def test_fp8b_layer_forward_backward(name, tokens):
     _check_layer(cfg)
 
 
-@pytest.mark.parametrize("tokens,d,f,e,k", [(1, 2048, 256, 4, 2), (3, 4096, 2048, 4, 1), (2, 7168, 320, 8, 4), (130, 2112, 192, 2, 1)])
+@pytest.mark.parametrize("tokens,d,f,e,k", [(1, 2048, 256, 4, 2), (3, 4096, 2048, 4, 1), (2, 7168, 320, 8, 4),
+                                            (130, 2112, 192, 2, 1)])
 def test_fp8b_layer_few_tokens(tokens, d, f, e, k):
     """Products of few tiles, split along the contraction."""
     _check_layer(MoEConfig("few", tokens, d, f, e, k, precision="fp8b"))
