@@ -26,14 +26,15 @@ namespace {
 // (inv = 1 / s rounded) is within 2 ulp of the quotient, which is enough to find
 // the border b between the two codes around it: low 20 mantissa bits 0x80000, or,
 // below 2^-6 where the codes are subnormal and as far apart as in [2^-6, 2^-5),
-// the same after adding 2^-6.  The sign of |x| - b s, exact in one FMA, says on
+// the same after adding 2^-6 (truncated: a sum rounded up to 2^-5 would give a border of
+// the next binade).  The sign of |x| - b s, exact in one FMA, says on
 // which side of b the quotient lies: quotients of bf16 numbers do fall on borders,
 // where a rounded one would round a second time.  All in fp32: with 64-bit
 // divisions near the borders 8192 x 4096 took 125 us instead of 30.
 __device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
   const float q = fabsf(x) * inv;
   const float up = q < 0.015625f ? 0.015625f : 0.0f;
-  const float b = __uint_as_float((__float_as_uint(q + up) & 0xFFF00000u) | 0x80000u) - up;
+  const float b = __uint_as_float((__float_as_uint(__fadd_rz(q, up)) & 0xFFF00000u) | 0x80000u) - up;
   const float r = fmaf(-b, s, fabsf(x));
   const uint32_t u = __float_as_uint(b) + (r > 0.0f ? 1u : 0u) - (r < 0.0f ? 1u : 0u);
   return __uint_as_float(u | (__float_as_uint(x) & 0x80000000u));
