@@ -73,11 +73,6 @@ template <int C>
 __device__ __forceinline__ uint32_t cluster_rank() {
   return C > 1 ? cluster_ctarank() : 0u;
 }
-// Every thread of the cluster arrives; shared memory written before is visible after.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  cluster_sync_all();
-}
 __device__ __forceinline__ void st_cluster_f32(const void* at, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(at), rank)), "f"(v) : "memory");
 }
@@ -116,7 +111,7 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[N]) {
     if (mine)
 #pragma unroll
       for (int c = 0; c < C; ++c) st_cluster_f32(&s[me * W + warp][which], c, a);
-    cluster_sync();
+    cluster_sync_all();
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       v[j] = 0.0f;
@@ -399,7 +394,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
   }
-  cluster_sync();   // every block of the cluster has started
+  cluster_sync_all();   // every block of the cluster has started
   const int me = static_cast<int>(cluster_rank<C>()) * (T / 32) + (tid >> 5);
   const float own_n = warp_columns<T, V, C>(d8, me / (T / 32), me % (T / 32));
   const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
@@ -464,7 +459,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
       sq[h] = warp_sum(sq[h]);
       if (lane < C) st_cluster_f32x2(&s_red[flip][me][h], lane, sum[h], sq[h]);
     }
-    cluster_sync();
+    cluster_sync_all();
     // every thread has read the buffers: later rows may land in them
     if (tid == 0)
 #pragma unroll
@@ -536,7 +531,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
   }
-  if constexpr (C > 1) cluster_sync();   // every block of the cluster has started
+  if constexpr (C > 1) cluster_sync_all();   // every block of the cluster has started
   else __syncthreads();
   const uint32_t sb = xb + yb + (dres ? xb : 0);   // a row's x, dy and dres
   auto fetch = [&](int s, int64_t r) {
