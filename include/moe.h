@@ -524,7 +524,9 @@ MOE_API moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_
  * ceil(n/128)] (the data gradient through weights stored [k, n]).
  * offsets [n_groups + 1] is read on the device and must not decrease; an entry
  * outside [0, rows] is cut to that range and sets MOE_DEV_BAD_OFFSETS, and
- * rows of no group are not written.  n and k must be multiples of 16;
+ * rows of no group are not written.  Offsets that decrease all the same set
+ * MOE_DEV_BAD_OFFSETS, and no row is written (their groups would overlap); the
+ * layer's products below treat theirs alike.  n and k must be multiples of 16;
  * n_groups <= 1024.  ws: moe_grouped_gemm_fp8_workspace_size() bytes, status
  * words first (moe_workspace_init before the first use; a layer workspace of
  * at least that size serves too). */

@@ -457,8 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   // all of the above needs nothing of the kernels before this one
   pdl_trigger();
   pdl_wait();
-  for (int i = threadIdx.x; i <= G; i += kThreads)
-    if (cut_offset(p, i) != __ldg(p.offsets + i) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+  bool descend = false;
+  for (int i = threadIdx.x; i <= G; i += kThreads) {
+    const int o = cut_offset(p, i);
+    const bool less = i < G && cut_offset(p, i + 1) < o;
+    descend |= less;
+    if ((less || o != __ldg(p.offsets + i)) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+  }
   if (warp == 0) {
     auto tiles_of = [&](int g) { return max(0, cut_offset(p, g + 1) - cut_offset(p, g) + BM - 1) / BM * p.ntiles; };
     const int per = (G + 31) / 32;
@@ -479,15 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     if (lane == 31) s_pre[G] = incl;
   }
   tc_fence_before();
-  __syncthreads();
+  descend = __syncthreads_or(descend);
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  // tiles; descending offsets can give a split launch more than it has clusters for
-  const int total = SPLIT ? min(s_pre[G], ustride) : s_pre[G];
-  if constexpr (SPLIT) {
-    if (threadIdx.x == 0 && s_pre[G] > ustride && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
-    __syncwarp();
-  }
+  // groups of descending offsets overlap, and two tiles would write the same rows: then none is written
+  const int total = descend ? 0 : s_pre[G];
   const int nkb = (kend - kbeg) * p.sources;
 
   if (warp < kAuxThreads / 32) {

@@ -1,13 +1,16 @@
 """GPU parity of the FP8 blocks of 128 where their numbers end: every border
-between two codes under every mantissa of a block's scale."""
+between two codes under every mantissa of a block's scale, and offsets that
+decrease."""
 import numpy as np
 import pytest
 import torch
 
 import oracle as O
 from ragged_grouped_gemm_gb300 import api
+from ragged_grouped_gemm_gb300.inputs import MoEConfig
 
 pytestmark = pytest.mark.gpu
+BAD_OFFSETS = 4
 
 
 def _quantise(x):
@@ -41,3 +44,49 @@ def test_quantise_rows_every_mantissa_of_the_scale(exponent):
     r, c = np.nonzero(wrong)
     assert not wrong.any(), (int(wrong.sum()), [(float(x[i, 0]), float(x[i, j]), int(codes[i, j]), int(rc[i, j]))
                                                 for i, j in zip(r[:4], c[:4])])
+
+
+def _tiles(g, e, r, c):
+    w = (torch.randn(e, r, c, generator=g) * 0.05).to(torch.bfloat16).cuda()
+    q = api.quantize_weights_fp8_tile({"w1": w})
+    return q["w1"], q["w1_scale"]
+
+
+@pytest.mark.parametrize("mn", [False, True])
+@pytest.mark.parametrize("n,k", [(144, 128), (400, 1168), (144, 2048), (1040, 4112)])
+@pytest.mark.parametrize("off", [[0, 300, 0, 300], [0, 300, 299, 300], [300, 0, 0, 300], [0, 10, 5, 5], [0, 400, 20, 300]])
+def test_product_descending_offsets_are_flagged_and_write_nothing(off, n, k, mn):
+    """In both the split (k from 2048) and the plain launch, whatever number of tiles they give."""
+    g = torch.Generator().manual_seed(n + k)
+    codes, scales = _quantise(torch.randn(300, k, generator=g).to(torch.bfloat16))
+    w, ws = _tiles(g, 3, *((k, n) if mn else (n, k)))
+    out = torch.full((300, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(api.moe_grouped_gemm_fp8_workspace_size(3, 300, n, k), dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(work)
+    api.moe_grouped_gemm_fp8(codes, scales, torch.tensor(off, dtype=torch.int32, device="cuda"), w, ws, out, work,
+                             b_mn=mn)
+    assert api.moe_get_device_status(work)[0] == BAD_OFFSETS
+    assert (out == 7.0).all()
+    # the same workspace and buffers go on with offsets that ascend
+    api.moe_workspace_init(work)
+    api.moe_grouped_gemm_fp8(codes, scales, torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda"), w, ws,
+                             out, work, b_mn=mn)
+    assert api.moe_get_device_status(work) == (0, 0)
+    assert (out != 7.0).any(1).all()
+
+
+def test_layer_products_descending_offsets_are_flagged():
+    cfg = MoEConfig("descend", 64, 256, 192, 4, 2, precision="fp8b")
+    g = torch.Generator().manual_seed(2)
+    desc = api.make_desc(cfg)
+    ws = torch.empty(api.moe_workspace_size(desc)[0], dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(ws)
+    codes, scales = _quantise(torch.randn(128, 256, generator=g).to(torch.bfloat16))
+    wq = {}
+    for key, r, c in (("w1", 192, 256), ("w3", 192, 256), ("w2", 256, 192)):
+        wq[key], wq[key + "_scale"] = _tiles(g, 4, r, c)
+    y = torch.full((128, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 128, 0, 128, 128], dtype=torch.int32, device="cuda")
+    api.moe_grouped_ffn_fp8b(desc, codes, scales, off, None, None, wq, {}, y, None, ws)
+    assert api.moe_get_device_status(ws)[0] == BAD_OFFSETS
+    assert (y == 7.0).all()
