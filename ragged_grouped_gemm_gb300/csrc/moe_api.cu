@@ -205,6 +205,14 @@ bool all16(std::initializer_list<const void*> ps) {
   return true;
 }
 
+// The same of arrays whose 32-bit numbers are read one by one.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool all4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p || !aligned4(p)) return false;
+  return true;
+}
+
 // A K-major activation [rows, cols] (row-major, ld = cols).
 Operand act(const void* p, int64_t rows, int64_t cols) {
   Operand o;
@@ -1233,7 +1241,7 @@ moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_t cols, 
   if (rows < 0 || cols <= 0 || cols % 16 || cols > (int64_t{1} << 30) || scale_ld < (cols + 127) / 128)
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!all16({src, codes}) || !scales || (reinterpret_cast<uintptr_t>(scales) & 3u)) return MOE_ERR_INVALID_ARG;
+  if (!all16({src, codes}) || !all4({scales})) return MOE_ERR_INVALID_ARG;
   return cuda_status(moe::launch_fp8_quant_rows(src, rows, cols, static_cast<uint8_t*>(codes), scales, scale_ld,
                                                 static_cast<cudaStream_t>(stream)));
 }
@@ -1257,7 +1265,7 @@ moe_status_t moe_grouped_gemm_fp8(int64_t n_groups, int64_t rows, int64_t n, int
       a_scale_ld < (k + 127) / 128 || a_scale_ld % 4 || (b_mn != 0 && b_mn != 1))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!all16({a, a_scale, b, out}) || !b_scale || !offsets) return MOE_ERR_INVALID_ARG;
+  if (!all16({a, a_scale, b, out}) || !all4({b_scale, offsets})) return MOE_ERR_INVALID_ARG;
   moe::Fp8GemmArgs g;
   g.b_mn = b_mn != 0;
   g.a[0] = static_cast<const uint8_t*>(a);
@@ -1282,7 +1290,7 @@ moe_status_t moe_permute_fp8b(const moe_desc_t* d, const void* x, const int32_t*
   MOE_TRY(check_desc(d));
   if (d->precision != kFp8b) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(*d, ws, ws_bytes, false));
-  if (!all16({x, xq_perm, xs_perm}) || !topk_idx || !offsets || !row_of_copy || !copy_of_row)
+  if (!all16({x, xq_perm, xs_perm}) || !all4({topk_idx, offsets, row_of_copy, copy_of_row}))
     return MOE_ERR_INVALID_ARG;
   if (x_perm && !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
   if (xq_tok && !all16({xq_tok, xs_tok})) return MOE_ERR_INVALID_ARG;
@@ -1304,15 +1312,15 @@ moe_status_t moe_grouped_ffn_fp8b(const moe_desc_t* d, const void* xq_perm, cons
   MOE_TRY(check_desc(d));
   if (d->precision != kFp8b) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(*d, ws, ws_bytes, false));
-  if (!w || !offsets || !all16({xq_perm, xs_perm, w->w1, w->w3, w->w2, y_perm}) || !w->w1_scale || !w->w3_scale ||
-      !w->w2_scale)
+  if (!w || !all16({xq_perm, xs_perm, w->w1, w->w3, w->w2, y_perm}) ||
+      !all4({offsets, w->w1_scale, w->w3_scale, w->w2_scale}))
     return MOE_ERR_INVALID_ARG;
   moe_ffn_saved_t sv{};
   if (saved) sv = *saved;
   for (const void* q : {sv.a1, sv.a3, sv.h, sv.a1s, sv.a3s, sv.hs})
     if (q && !aligned16(q)) return MOE_ERR_INVALID_ARG;
-  if (d->n_shared && (!all16({xq_tok, xs_tok, w->ws1, w->ws3, w->ws2, y_shared}) || !w->ws1_scale ||
-                      !w->ws3_scale || !w->ws2_scale))
+  if (d->n_shared && (!all16({xq_tok, xs_tok, w->ws1, w->ws3, w->ws2, y_shared}) ||
+                      !all4({w->ws1_scale, w->ws3_scale, w->ws2_scale})))
     return MOE_ERR_INVALID_ARG;
   if (d->n_tok == 0) return MOE_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1339,8 +1347,8 @@ moe_status_t moe_backward_fp8b(const moe_desc_t* d, const void* w_gate, const mo
   MOE_RANGE("moe_backward_fp8b");
   MOE_TRY(check_desc(d));
   if (d->precision != kFp8b || !wq) return MOE_ERR_INVALID_ARG;
-  if (!wq->w1_scale || !wq->w3_scale || !wq->w2_scale) return MOE_ERR_INVALID_ARG;
-  if (d->n_shared && (!wq->ws1_scale || !wq->ws3_scale || !wq->ws2_scale)) return MOE_ERR_INVALID_ARG;
+  if (!all4({wq->w1_scale, wq->w3_scale, wq->w2_scale})) return MOE_ERR_INVALID_ARG;
+  if (d->n_shared && !all4({wq->ws1_scale, wq->ws3_scale, wq->ws2_scale})) return MOE_ERR_INVALID_ARG;
   const moe_expert_weights_t w{wq->w1, wq->w3, wq->w2, wq->ws1, wq->ws3, wq->ws2};
   return backward_impl(d, w_gate, &w, wq, s, dy, g, ws, ws_bytes, stream);
 }
@@ -1353,7 +1361,8 @@ moe_status_t moe_layernorm(const moe_desc_t* d, const void* x, int32_t x_f32, co
   if ((x_f32 != 0 && x_f32 != 1) || !(eps > 0.0) || !(eps < 1e30) || !(static_cast<float>(eps) > 0.0f))
     return MOE_ERR_INVALID_ARG;
   if (d->n_tok == 0) return MOE_OK;
-  if (!all16({x, gamma, y}) || (beta && !aligned16(beta))) return MOE_ERR_INVALID_ARG;
+  if (!all16({x, gamma, y}) || (beta && !aligned16(beta)) || !aligned4(mean) || !aligned4(rstd))
+    return MOE_ERR_INVALID_ARG;
   return cuda_status(moe::launch_layernorm(d->n_tok, d->d_model, x, x_f32 != 0, gamma, beta, static_cast<float>(eps),
                                            y, mean, rstd, static_cast<cudaStream_t>(stream)));
 }
@@ -1365,8 +1374,8 @@ moe_status_t moe_layernorm_backward(const moe_desc_t* d, const void* dy, const v
   MOE_TRY(check_desc(d));
   if (d->d_model > moe::kNormMaxCols) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_ws(*d, ws, ws_bytes, true));
-  if ((x_f32 != 0 && x_f32 != 1) || !dgamma) return MOE_ERR_INVALID_ARG;
-  if (d->n_tok > 0 && (!all16({dy, x, gamma, dx}) || !mean || !rstd)) return MOE_ERR_INVALID_ARG;
+  if ((x_f32 != 0 && x_f32 != 1) || !all4({dgamma}) || !aligned4(dbeta)) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok > 0 && (!all16({dy, x, gamma, dx}) || !all4({mean, rstd}))) return MOE_ERR_INVALID_ARG;
   if (dres && !aligned16(dres)) return MOE_ERR_INVALID_ARG;
   const WsLayout L = layout(*d);
   return cuda_status(moe::launch_layernorm_bwd(d->n_tok, d->d_model, dy, x, x_f32 != 0, gamma, mean, rstd, dres, dx,
@@ -1392,7 +1401,7 @@ moe_status_t moe_combine_dropout(const moe_desc_t* d, const void* y_perm, const 
   float scale = 1.0f;
   if (!dropout_params(p, &threshold, &scale) || (resid_f32 != 0 && resid_f32 != 1)) return MOE_ERR_INVALID_ARG;
   if (d->n_tok == 0) return MOE_OK;
-  if (!all16({y_perm, out}) || !row_of_copy || !topk_w || !rng) return MOE_ERR_INVALID_ARG;
+  if (!all16({y_perm, out}) || !all4({row_of_copy, topk_w}) || !rng) return MOE_ERR_INVALID_ARG;
   if ((y_shared && !aligned16(y_shared)) || (resid && !aligned16(resid)) || (reinterpret_cast<uintptr_t>(rng) & 7u))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(moe::launch_combine_dropout(d->n_tok, d->d_model, d->top_k, y_perm, row_of_copy, topk_w,

@@ -1,9 +1,36 @@
-"""Limits of the block's entry points and kernels that hold on the CPU."""
+"""Limits of the block's entry points and kernels that hold on the CPU.  Every call
+here is refused before anything is enqueued (the addresses are never read)."""
+import ctypes
 import glob
 import os
 import re
 
-from ragged_grouped_gemm_gb300 import build
+import pytest
+
+from ragged_grouped_gemm_gb300 import _lib, api, build
+from ragged_grouped_gemm_gb300.inputs import CONFIGS
+
+INVALID = 1
+P = 1 << 20          # an aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def _desc(**kw):
+    d = api.make_desc(CONFIGS["tiny"])
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def _ws(lib, d):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.moe_workspace_size(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b)) == 0
+    return f.value, b.value
 
 
 def _sources():
@@ -21,3 +48,35 @@ def test_every_aligned_cluster_barrier_converges_its_warp_first():
             found.append(name)
             assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", body), (name, body)
     assert found == ["sm100_ptx.cuh"]
+
+
+@pytest.mark.parametrize("odd", [1, 2, 3])
+def test_misaligned_arrays_of_32_bit_numbers_are_refused(lib, odd):
+    """The kernels read them word by word: an address between two words would fault on the device."""
+    q = P + odd
+    for off, sb in ((q, P), (P, q)):
+        assert lib.moe_grouped_gemm_fp8(4, 8, 64, 128, P, P, 4, off, P, sb, 0, P, P, 1 << 20, None) == INVALID
+    d = _desc(precision=4, n_shared=1, d_ff_shared=64)
+    f, b = _ws(lib, d)
+    ref = ctypes.byref(d)
+    for i in range(4):
+        maps = [q if i == j else P for j in range(4)]
+        assert lib.moe_permute_fp8b(ref, P, maps[0], maps[1], maps[2], maps[3], None, P, P, None, None, P, f,
+                                    None) == INVALID
+    saved = ctypes.byref(_lib.MoeFfnSaved(*[P] * 6))
+    state, grads = ctypes.byref(_lib.MoeFwdState(*[P] * 17)), ctypes.byref(_lib.MoeGrads(*[P] * 10))
+    plain = ctypes.byref(_lib.MoeExpertWeightsMx(*[P] * 12))
+    assert lib.moe_grouped_ffn_fp8b(ref, P, P, q, P, P, plain, saved, P, P, P, f, None) == INVALID
+    for i in range(6):
+        w = ctypes.byref(_lib.MoeExpertWeightsMx(*[q if j == 2 * i + 1 else P for j in range(12)]))
+        assert lib.moe_grouped_ffn_fp8b(ref, P, P, P, P, P, w, saved, P, P, P, f, None) == INVALID
+        assert lib.moe_backward_fp8b(ref, P, w, state, P, grads, P, b, None) == INVALID
+    t = _desc()
+    ref, b = ctypes.byref(t), _ws(lib, t)[1]
+    for mean, rstd in ((q, None), (None, q)):
+        assert lib.moe_layernorm(ref, P, 0, P, None, 1e-5, P, mean, rstd, None) == INVALID
+    for i in range(4):
+        mean, rstd, dgamma, dbeta = (q if i == j else P for j in range(4))
+        assert lib.moe_layernorm_backward(ref, P, P, 0, P, mean, rstd, None, P, dgamma, dbeta, P, b, None) == INVALID
+    for rows, w in ((q, P), (P, q)):
+        assert lib.moe_combine_dropout(ref, P, rows, w, None, None, 0, P, 0.1, P, None) == INVALID
