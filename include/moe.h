@@ -577,7 +577,9 @@ MOE_API moe_status_t moe_backward_fp8b(const moe_desc_t* d, const void* w_gate, 
  * residual stream): y = (x - mean) * rstd * gamma + beta, bf16 [N,D];
  * mean, rstd [N] fp32 (nullable), rstd = 1 / sqrt(var + eps) with the biased
  * variance, summed in fp32 about the mean.  gamma, beta [D] fp32, beta
- * nullable (zero).  eps > 0.  D <= 32768 (MOE_ERR_UNSUPPORTED above). */
+ * nullable (zero).  eps > 0.  D <= 32768 (MOE_ERR_UNSUPPORTED above).  There
+ * is no status word here: a bounded wait that ran out leaves NaN in its row
+ * and in the later rows of the same blocks (y, mean, rstd). */
 MOE_API moe_status_t moe_layernorm(const moe_desc_t* d, const void* x, int32_t x_f32, const float* gamma,
                                    const float* beta, double eps, void* y, float* mean, float* rstd, void* stream);
 
@@ -586,7 +588,9 @@ MOE_API moe_status_t moe_layernorm(const moe_desc_t* d, const void* x, int32_t x
  *   dgamma = sum_t dy * xhat, dbeta = sum_t dy  (fp32 [D], overwritten).
  * dres (nullable, type of x) is the gradient that reaches x past the norm (the
  * residual path's).  dbeta is nullable.  Sums have a fixed order: the same
- * inputs give the same bits.  Needs the backward workspace. */
+ * inputs give the same bits.  A bounded wait that ran out sets MOE_DEV_TIMEOUT
+ * and leaves NaN in those rows of dx and in dgamma and dbeta.  Needs the
+ * backward workspace. */
 MOE_API moe_status_t moe_layernorm_backward(const moe_desc_t* d, const void* dy, const void* x, int32_t x_f32,
                                             const float* gamma, const float* mean, const float* rstd,
                                             const void* dres, void* dx, float* dgamma, float* dbeta, void* ws,
@@ -652,6 +656,18 @@ MOE_API moe_status_t moe_permute_noalloc(const moe_desc_t* d, const void* x, con
  * moe_workspace_init first and read the result with moe_get_device_status. */
 MOE_API moe_status_t moe_selftest_wait_timeout(void* ws, size_t ws_bytes, uint64_t limit_ns, int32_t site,
                                                void* stream);
+
+/* The same of the layer norm, whose rows of more than 1024 elements arrive
+ * under bounded waits: the norm (dy NULL: x, gamma -> y, mean, rstd, no bias,
+ * eps 1e-5) or its backward (dy, x, gamma, mean, rstd -> dx, dgamma, dbeta)
+ * with row `row` never asked for, so that the wait for it has the limit
+ * `limit_ns` (1 ns .. 1 s) and runs out.  The rest as a wait that runs out in
+ * moe_layernorm and moe_layernorm_backward.  D > 1024 (MOE_ERR_UNSUPPORTED
+ * otherwise); needs the backward workspace. */
+MOE_API moe_status_t moe_selftest_layernorm_timeout(const moe_desc_t* d, const void* dy, const void* x, int32_t x_f32,
+                                                    const float* gamma, void* y, float* mean, float* rstd, void* dx,
+                                                    float* dgamma, float* dbeta, int64_t row, uint64_t limit_ns,
+                                                    void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------- kernel timing --
  * Per-kernel timing of the grouped GEMMs (no counterpart in the pages; a

@@ -304,6 +304,19 @@ def moe_selftest_wait_timeout(ws, limit_ns: int, site: int, stream=None):
         _p(ws, name="ws"), ws.numel() * ws.element_size(), int(limit_ns), int(site), _s(stream)))
 
 
+def moe_selftest_layernorm_timeout(desc, x, gamma, mean, rstd, row: int, limit_ns: int, ws, y=None, dy=None, dx=None,
+                                   dgamma=None, dbeta=None, stream=None):
+    """The layer norm (``y``) or its backward (``dy`` and its outputs) in which the
+    wait for row ``row`` runs out after ``limit_ns`` (see moe.h)."""
+    n, d = desc.n_tok, desc.d_model
+    _check("moe_selftest_layernorm_timeout", _lib.load().moe_selftest_layernorm_timeout(
+        ctypes.byref(desc), _p(dy, BF16, (n, d), "dy"), _p(x, None, (n, d), "x"), _stream_type(x, "x"),
+        _p(gamma, F32, (d,), "gamma"), _p(y, BF16, (n, d), "y"), _p(mean, F32, (n,), "mean"),
+        _p(rstd, F32, (n,), "rstd"), _p(dx, x.dtype, (n, d), "dx"), _p(dgamma, F32, (d,), "dgamma"),
+        _p(dbeta, F32, (d,), "dbeta"), int(row), int(limit_ns), _p(ws, name="ws"), ws.numel() * ws.element_size(),
+        _s(stream)))
+
+
 def moe_update_bias(desc, counts, bias, gamma: float, mode: int = 0, stream=None):
     _check("moe_update_bias", _lib.load().moe_update_bias(
         ctypes.byref(desc), _p(counts, I32, (desc.n_exp,), "counts"), _p(bias, F32, (desc.n_exp,), "bias"),

@@ -241,6 +241,38 @@ __device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8])
   for (int j = 0; j < 8; ++j) f[j] = v.get(j);
 }
 
+// Waits for a row.  A wait that runs out raises `stop` in every block of the cluster, where
+// the others' waits end at it; a caller looks at it behind the row's next barrier, which
+// no thread passes before the row's waits, and takes turns between two of them where there is one
+// barrier a turn, so that all threads find the same.  It leaves at the turn's end, so that nothing
+// waits for the look, and what the turn stored is overwritten.
+constexpr int kRowWaitSite = 900;
+template <int C>
+__device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, int* stop, const RowWait& w) {
+  if (mbar_wait_bounded(bar, parity, stop, w.status, kRowWaitSite, w.limit_ns)) return;
+  if constexpr (C > 1)
+    for (int c = 0; c < C; ++c)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(stop), c)), "r"(1) : "memory");
+}
+__device__ __forceinline__ bool stopped(const int* stop) { return *static_cast<const volatile int*>(stop) != 0; }
+// One thread's wait, with a limit too, for the copies of rows from r on that are under way when
+// a block gives up: those of `stages` rows.
+__device__ __noinline__ void drain_rows(uint64_t* full, int stages, int64_t r, int64_t row0, int64_t step, int64_t rows,
+                                        uint64_t limit_ns) {
+  int64_t j = (r - row0) / step;
+  for (int k = 0; k < stages && r < rows; ++k, ++j, r += step)
+    mbar_wait_drain(&full[j % stages], static_cast<uint32_t>(j / stages) & 1u, limit_ns / 8);
+}
+__device__ __forceinline__ float not_a_number() { return __uint_as_float(0x7FC00000u); }
+// Vectors first .. first + n8 - 1 of row r: not a number.
+template <bool F32>
+__device__ __forceinline__ void fill_nan(void* out, int64_t r, int d8, int first, int n8) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = not_a_number();
+  for (int c = threadIdx.x; c < n8; c += blockDim.x) Vec8<F32>::store(out, r * d8 + first + c, f);
+}
+
 // A block's share of the rows: vectors first .. first + n8 - 1 of rows row0, row0 + step, ...
 struct Part {
   int first, n8;
@@ -267,15 +299,17 @@ template <bool F32, int T, int V>
 __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ beta, float eps, void* __restrict__ y, float* __restrict__ mean,
-    float* __restrict__ rstd) {
+    float* __restrict__ rstd, const RowWait wait) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
+  __shared__ int stop;
   __shared__ float s_red[2][T / 32];
   const int tid = threadIdx.x;
   const uint32_t xb = static_cast<uint32_t>(d8) * (F32 ? 32 : 16);
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    stop = 0;
     fence_mbar_init();
   }
   pdl_trigger();
@@ -292,6 +326,7 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
   }
   __syncthreads();
   auto fetch = [&](int s, int64_t r) {
+    if (r == wait.withheld) return;
     mbar_arrive_expect_tx(&full[s], xb);
     bulk_load(ring + static_cast<size_t>(s) * xb, x + r * xb, xb, &full[s]);
   };
@@ -302,8 +337,9 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
     }
   int s = 0;
   uint32_t ph = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    mbar_wait_drain(&full[s], ph);
+  int64_t r = blockIdx.x;
+  for (; r < rows; r += gridDim.x) {
+    wait_row<1>(&full[s], ph, &stop, wait);
     const uint8_t* row = ring + static_cast<size_t>(s) * xb;
     float v[V][8];
     float sum = 0.0f;
@@ -322,9 +358,10 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
       for (int j = 0; j < 8; ++j) sum += v[i][j];
     }
     const float mu = block_sum<T>(sum, s_red[0]) * inv_d;
+    const bool halt = stopped(&stop);
     // every thread has read the buffer: the row after next `stages` may land in it
     const int64_t next = r + static_cast<int64_t>(stages) * gridDim.x;
-    if (tid == 0 && next < rows) fetch(s, next);
+    if (tid == 0 && !halt && next < rows) fetch(s, next);
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -350,9 +387,18 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
         Vec8<false>::store(y, r * d8 + c, o);
       }
     }
+    if (halt) break;
     if (++s == stages) {
       s = 0;
       ph ^= 1u;
+    }
+  }
+  if (r < rows && tid == 0) drain_rows(full, stages, r, blockIdx.x, gridDim.x, rows, wait.limit_ns);
+  for (; r < rows; r += gridDim.x) {
+    fill_nan<false>(y, r, d8, 0, d8);
+    if (tid == 0) {
+      if (mean) mean[r] = not_a_number();
+      if (rstd) rstd[r] = not_a_number();
     }
   }
 }
@@ -367,9 +413,10 @@ template <bool F32, int T, int V, int R, int C>
 __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ x, const float* __restrict__ gamma,
     const float* __restrict__ beta, float eps, void* __restrict__ y, float* __restrict__ mean,
-    float* __restrict__ rstd) {
+    float* __restrict__ rstd, const RowWait wait) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
+  __shared__ int stop[2];
   constexpr int W = C * T / 32, K = W / 32;   // warps of a row; a lane joins K of them
   static_assert(W % 32 == 0);
   __shared__ float2 s_red[2][W][R];
@@ -380,6 +427,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    stop[0] = stop[1] = 0;
     fence_mbar_init();
   }
   pdl_trigger();
@@ -406,6 +454,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
     winv[k] = wn[k] > 0.0f ? 1.0f / wn[k] : 0.0f;
   }
   auto fetch = [&](int s, int64_t r) {
+    if (r == wait.withheld) return;
     mbar_arrive_expect_tx(&full[s], xb);
     bulk_load(ring + static_cast<size_t>(s) * xb, x + (r * d8 + part.first) * (F32 ? 32 : 16), xb, &full[s]);
   };
@@ -416,7 +465,8 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
     }
   int s = 0, flip = 0;
   uint32_t ph = 0;
-  for (int64_t r = part.row0; r < rows; r += R * part.step, flip ^= 1) {
+  int64_t r = part.row0;
+  for (; r < rows; r += R * part.step, flip ^= 1) {
     Vec8<F32> v[R][V];
     float sum[R], sq[R];
     int freed[R];
@@ -425,7 +475,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
       const bool have = h == 0 || r + h * part.step < rows;
       const uint8_t* row = ring + static_cast<size_t>(s) * xb;
       sum[h] = sq[h] = 0.0f;
-      if (have) mbar_wait_drain(&full[s], ph);
+      if (have) wait_row<C>(&full[s], ph, &stop[flip], wait);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = tid + i * T;
@@ -460,8 +510,9 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
       if (lane < C) st_cluster_f32x2(&s_red[flip][me][h], lane, sum[h], sq[h]);
     }
     cluster_sync_all();
+    const bool halt = stopped(&stop[flip]);
     // every thread has read the buffers: later rows may land in them
-    if (tid == 0)
+    if (tid == 0 && !halt)
 #pragma unroll
       for (int h = 0; h < R; ++h) {
         const int64_t next = r + (h + stages) * part.step;
@@ -500,6 +551,15 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
         }
       }
     }
+    if (halt) break;
+  }
+  if (r < rows && tid == 0) drain_rows(full, stages, r, part.row0, part.step, rows, wait.limit_ns);
+  for (; r < rows; r += part.step) {
+    fill_nan<false>(y, r, d8, part.first, n8);
+    if (tid == 0 && part.first == 0) {
+      if (mean) mean[r] = not_a_number();
+      if (rstd) rstd[r] = not_a_number();
+    }
   }
 }
 
@@ -509,9 +569,10 @@ template <bool F32, int T, int V, int R, int C>
 __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
     int64_t rows, int d8, int stages, const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
-    const uint8_t* __restrict__ dres, void* __restrict__ dx, float* __restrict__ part) {
+    const uint8_t* __restrict__ dres, void* __restrict__ dx, float* __restrict__ part, const RowWait wait) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8];
+  __shared__ int stop[2];
   __shared__ __align__(16) float s_red[2][C * T / 32][2 * R];
   const int tid = threadIdx.x;
   const Part own = part_of<C>(d8);
@@ -520,6 +581,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
   const float inv_d = 1.0f / static_cast<float>(d8 * 8);
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    stop[0] = stop[1] = 0;
     fence_mbar_init();
   }
   pdl_trigger();
@@ -536,6 +598,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
   const uint32_t sb = xb + yb + (dres ? xb : 0);   // a row's x, dy and dres
   auto fetch = [&](int s, int64_t r) {
     uint8_t* dst = ring + static_cast<size_t>(s) * sb;
+    if (r == wait.withheld) return;
     mbar_arrive_expect_tx(&full[s], sb);
     const int64_t at = r * d8 + own.first;
     bulk_load(dst, x + at * (F32 ? 32 : 16), xb, &full[s]);
@@ -550,7 +613,8 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
   int s = 0, flip = 0;
   uint32_t ph = 0;
   const int64_t step = own.step;
-  for (int64_t r = own.row0; r < rows; r += R * step, flip ^= 1) {
+  int64_t r = own.row0;
+  for (; r < rows; r += R * step, flip ^= 1) {
     Vec8<F32> xv[R][V], res[R][V];
     Vec8<false> ev[R][V];
     float mu[R], rs[R], sum[2 * R];   // of g dy and of g dy x^, row by row
@@ -567,7 +631,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
       const uint8_t* row = ring + static_cast<size_t>(s) * sb;
       sum[2 * h] = sum[2 * h + 1] = 0.0f;
       if (have) {
-        mbar_wait_drain(&full[s], ph);
+        wait_row<C>(&full[s], ph, &stop[flip], wait);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int c = tid + i * T;
@@ -594,8 +658,9 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
       }
     }
     block_sums<T, 2 * R, C>(sum, s_red[flip]);
+    const bool halt = stopped(&stop[flip]);
     // every thread has read the buffers
-    if (tid == 0)
+    if (tid == 0 && !halt)
 #pragma unroll
       for (int h = 0; h < R; ++h) {
         const int64_t next = r + (h + stages) * step;
@@ -620,6 +685,15 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
         }
       }
     }
+    if (halt) break;
+  }
+  if (r < rows) {
+    if (tid == 0) drain_rows(full, stages, r, own.row0, step, rows, wait.limit_ns);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = not_a_number();
+    for (; r < rows; r += step) fill_nan<F32>(dx, r, d8, own.first, n8);
   }
   float* p = part + (own.row0 * 2 * d8 + own.first) * 8;
 #pragma unroll
@@ -934,7 +1008,7 @@ cudaError_t with_row_shape(int d, F&& f) {
 }  // namespace
 
 cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, const float* gamma, const float* beta,
-                             float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
+                             float eps, void* y, float* mean, float* rstd, cudaStream_t st, const RowWait& wait) {
   if (rows <= 0) return cudaSuccess;
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
   if (d > 1024)
@@ -948,7 +1022,7 @@ cudaError_t launch_layernorm(int64_t rows, int d, const void* x, bool x_f32, con
         constexpr bool F = decltype(f32)::value;
         constexpr auto K = forward_kernel<F, T, V, C>();
         return launch_ring<K, C>(std::min<int64_t>(rows, resident<K, C>(T, per_sm)), T, stages * bytes, st, rows, d / 8,
-                                 stages, px, gamma, beta, eps, y, mean, rstd);
+                                 stages, px, gamma, beta, eps, y, mean, rstd, wait);
       };
       return x_f32 ? run(std::true_type()) : run(std::false_type());
     });
@@ -966,7 +1040,7 @@ size_t layernorm_bwd_floats(int64_t rows, int d) {
 
 cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void* x, bool x_f32, const float* gamma,
                                  const float* mean, const float* rstd, const void* dres, void* dx, float* dgamma,
-                                 float* dbeta, float* scratch, cudaStream_t st) {
+                                 float* dbeta, float* scratch, cudaStream_t st, const RowWait& wait) {
   if (d <= 0 || d % 8 || d > kNormMaxCols) return cudaErrorInvalidValue;
   int grid = 0;
   if (rows > 0 && d > 1024) {
@@ -980,7 +1054,7 @@ cudaError_t launch_layernorm_bwd(int64_t rows, int d, const void* dy, const void
         grid = static_cast<int>(std::min<int64_t>({rows, kNormBlocks, resident<K, C>(T, per_sm)}));
         return launch_ring<K, C>(grid, T, stages * bytes, st, rows, d / 8, stages, static_cast<const uint8_t*>(dy),
                                  static_cast<const uint8_t*>(x), gamma, mean, rstd, static_cast<const uint8_t*>(dres),
-                                 dx, scratch);
+                                 dx, scratch, wait);
       };
       return x_f32 ? run(std::true_type()) : run(std::false_type());
     });

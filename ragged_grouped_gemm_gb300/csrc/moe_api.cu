@@ -1378,9 +1378,36 @@ moe_status_t moe_layernorm_backward(const moe_desc_t* d, const void* dy, const v
   if (d->n_tok > 0 && (!all16({dy, x, gamma, dx}) || !all4({mean, rstd}))) return MOE_ERR_INVALID_ARG;
   if (dres && !aligned16(dres)) return MOE_ERR_INVALID_ARG;
   const WsLayout L = layout(*d);
+  moe::RowWait wait;
+  wait.status = at<int32_t>(ws, L.status);
   return cuda_status(moe::launch_layernorm_bwd(d->n_tok, d->d_model, dy, x, x_f32 != 0, gamma, mean, rstd, dres, dx,
                                                dgamma, dbeta, at<float>(ws, L.norm),
-                                               static_cast<cudaStream_t>(stream)));
+                                               static_cast<cudaStream_t>(stream), wait));
+}
+
+moe_status_t moe_selftest_layernorm_timeout(const moe_desc_t* d, const void* dy, const void* x, int32_t x_f32,
+                                            const float* gamma, void* y, float* mean, float* rstd, void* dx,
+                                            float* dgamma, float* dbeta, int64_t row, uint64_t limit_ns, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_selftest_layernorm_timeout");
+  MOE_TRY(check_desc(d));
+  if (d->d_model > moe::kNormMaxCols || d->d_model <= 1024) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_ws(*d, ws, ws_bytes, true));
+  if ((x_f32 != 0 && x_f32 != 1) || row < 0 || row >= d->n_tok || limit_ns == 0 || limit_ns > 1000000000ull)
+    return MOE_ERR_INVALID_ARG;
+  if (!all16({x, gamma, dy ? dx : y}) || !all4({mean, rstd}) || (dy && (!aligned16(dy) || !all4({dgamma, dbeta}))))
+    return MOE_ERR_INVALID_ARG;
+  const WsLayout L = layout(*d);
+  moe::RowWait wait;
+  wait.limit_ns = limit_ns;
+  wait.withheld = row;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!dy)
+    return cuda_status(moe::launch_layernorm(d->n_tok, d->d_model, x, x_f32 != 0, gamma, nullptr, 1e-5f, y, mean, rstd,
+                                             st, wait));
+  wait.status = at<int32_t>(ws, L.status);
+  return cuda_status(moe::launch_layernorm_bwd(d->n_tok, d->d_model, dy, x, x_f32 != 0, gamma, mean, rstd, nullptr, dx,
+                                               dgamma, dbeta, at<float>(ws, L.norm), st, wait));
 }
 
 // Threshold and factor of a dropout probability in [0, 1).

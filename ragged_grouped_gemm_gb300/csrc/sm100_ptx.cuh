@@ -83,12 +83,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 // Drain wait used on the way out of a kernel: waits (bounded, ignoring the
 // abort flag) for this CTA's own asynchronous copies or MMAs, which complete
 // without help from any other role.
-__device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity,
+                                                uint64_t limit_ns = kSpinTimeoutNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   uint32_t n = 0;
   while (!mbar_try_wait(bar, parity)) {
-    if ((++n & 63u) == 0 && globaltimer_ns() - t0 > kSpinTimeoutNs) return false;
+    if ((++n & 63u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
   }
   return true;
 }

@@ -80,3 +80,19 @@ def test_misaligned_arrays_of_32_bit_numbers_are_refused(lib, odd):
         assert lib.moe_layernorm_backward(ref, P, P, 0, P, mean, rstd, None, P, dgamma, dbeta, P, b, None) == INVALID
     for rows, w in ((q, P), (P, q)):
         assert lib.moe_combine_dropout(ref, P, rows, w, None, None, 0, P, 0.1, P, None) == INVALID
+
+
+def test_layernorm_timeout_selftest_refusals(lib):
+    d = _desc(d_model=2048)
+    b = _ws(lib, d)[1]
+
+    def call(desc=d, dy=None, x=P, f32=0, y=P, mean=P, dx=P, dgamma=P, row=0, limit=50_000, ws=P, n=b):
+        return lib.moe_selftest_layernorm_timeout(ctypes.byref(desc), dy, x, f32, P, y, mean, P, dx, dgamma, P, row,
+                                                  limit, ws, n, None)
+    for bad in (dict(x=None), dict(f32=2), dict(y=None), dict(y=P + 8), dict(mean=None), dict(row=-1),
+                dict(row=d.n_tok), dict(limit=0), dict(limit=1_000_000_001), dict(dy=P + 8), dict(dy=P, dx=None),
+                dict(dy=P, dgamma=None), dict(dy=P, dgamma=P + 2)):
+        assert call(**bad) == INVALID, bad
+    assert call(ws=None) == 3 and call(n=b - 1) == 3
+    for wide in (1024, 32768 + 64):                       # rows that no wait holds up, rows that are too wide
+        assert call(desc=_desc(d_model=wide)) == 2
