@@ -237,10 +237,14 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 }
 
 __device__ __forceinline__ float swiglu(float a1, float a3) { return __fdividef(a1, 1.0f + __expf(-a1)) * a3; }
-// The scale of a block of h with the largest magnitude m: h below 448e-37 is zero here.
+// What a block of h with the scale s is multiplied by before the scale's reciprocal, which
+// is beyond fp32's range for the smallest scales: the reciprocal is that of h_factor(s) * s.
+__device__ __forceinline__ float h_factor(float s) {
+  return s < 5.421010862427522e-20f ? 18446744073709551616.0f : 1.0f;   // 2^-64, 2^64
+}
 __device__ __forceinline__ float scale_of_h(float m) {
   const float s = m * (1.0f / 448.0f);
-  return s > 1e-37f ? s : 1.0f;
+  return s > 0.0f ? s : 1.0f;
 }
 
 // One lane of a converged warp.  The compiler knows this form: operands of the
@@ -800,7 +804,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (!ok) break;
 #pragma unroll
         for (int g = 0; g < CG; ++g) m = fmaxf(m, mx[g * 128]);
-        const float hscale = scale_of_h(m), rs = 1.0f / hscale;
+        const float hscale = scale_of_h(m), hf = h_factor(hscale), rs = 1.0f / (hscale * hf);
+        if (hf != 1.0f) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i) acc[i] *= hf;
+        }
         if (cg == 0 && r < t.valid) p.hs[(row + lane) * p.hs_ld + t.nt] = hscale;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out0) + (row + lane) * p.n + f);
 #pragma unroll
@@ -854,11 +862,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             row_bf16(a[0], p.out3);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float hscale = scale_of_h(m), rs = 1.0f / hscale;
+            const float hscale = scale_of_h(m), hf = h_factor(hscale), rs = 1.0f / (hscale * hf);
             if (lane == 0) p.hs[row * p.hs_ld + t.nt] = hscale;
             if (col < p.n)
               *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out0) + row * p.n + col) =
-                  fp8_pack4(a[0][0] * rs, a[0][1] * rs, a[0][2] * rs, a[0][3] * rs);
+                  fp8_pack4(a[0][0] * hf * rs, a[0][1] * hf * rs, a[0][2] * hf * rs, a[0][3] * hf * rs);
           } else {
             row_bf16(a[0], p.out0);
           }

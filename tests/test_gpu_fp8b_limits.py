@@ -1,11 +1,12 @@
 """GPU parity of the FP8 blocks of 128 where their numbers end: every border
-between two codes under every mantissa of a block's scale, and offsets that
-decrease."""
+between two codes under every mantissa of a block's scale, blocks of h near the
+end of fp32's range, and offsets that decrease."""
 import numpy as np
 import pytest
 import torch
 
 import oracle as O
+from parity_util import BF16_TOL, np32, rel
 from ragged_grouped_gemm_gb300 import api
 from ragged_grouped_gemm_gb300.inputs import MoEConfig
 
@@ -90,3 +91,35 @@ def test_layer_products_descending_offsets_are_flagged():
     api.moe_grouped_ffn_fp8b(desc, codes, scales, off, None, None, wq, {}, y, None, ws)
     assert api.moe_get_device_status(ws)[0] == BAD_OFFSETS
     assert (y == 7.0).all()
+
+
+@pytest.mark.parametrize("down", [0, -90, -113, -118])
+@pytest.mark.parametrize("sizes,d,f", [([40, 0, 90], 256, 192), ([1, 2], 2048, 128)])
+def test_layer_products_of_small_h(sizes, d, f, down):
+    """h = silu(a1) a3 with a3 scaled down by 2^down and w2 up by as much: the largest magnitude of a
+    block of h is then about 2^down, 2^-118 below 448e-37, and y stays of order one.  The scale
+    products of a3 are about 2^-20 of it; the smallest keep 2^-149 / 2^-138 = 2^-11 of their
+    value, half of that off (2^-12), a part of the tolerance of 5e-3."""
+    g = torch.Generator().manual_seed(d - down)
+    rows, e = sum(sizes), len(sizes)
+    cfg = MoEConfig("small h", rows, d, f, e, 1, precision="fp8b")
+    desc = api.make_desc(cfg)
+    ws = torch.empty(api.moe_workspace_size(desc)[0], dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(ws)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    codes, scales = _quantise(torch.randn(rows, d, generator=g).to(torch.bfloat16))
+    wq = {}
+    for key, r, c in (("w1", f, d), ("w3", f, d), ("w2", d, f)):
+        wq[key], wq[key + "_scale"] = _tiles(g, e, r, c)
+    wq["w3_scale"] *= 2.0 ** down
+    wq["w2_scale"] *= 2.0 ** -down
+    y = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+    api.moe_grouped_ffn_fp8b(desc, codes, scales, torch.from_numpy(off).cuda(), None, None, wq, {}, y, None, ws)
+    assert api.moe_get_device_status(ws) == (0, 0)
+    x = O.fp8_rows_dequantize(codes.cpu().numpy(), scales[:, :-(-d // 128)].cpu().numpy())
+    v = {k: O.fp8_tile_value(wq[k].cpu().numpy(), wq[k + "_scale"].cpu().numpy()) for k in ("w1", "w3", "w2")}
+    want = np.zeros((rows, d))
+    for i, (lo, hi) in enumerate(zip(off, off[1:])):
+        if lo < hi:
+            want[lo:hi] = O.swiglu_expert_fp8b(x[lo:hi], v["w1"][i], v["w3"][i], v["w2"][i])[0]
+    assert rel(np32(y), want) < BF16_TOL
