@@ -73,7 +73,8 @@ typedef enum {
 #define MOE_DEV_TIMEOUT 1      /* a bounded wait inside a kernel ran out */
 #define MOE_DEV_BAD_INDEX 2    /* an expert index outside [0, E) */
 #define MOE_DEV_BAD_OFFSETS 4  /* the histogram did not sum to N*K, or (permute)
-                                  offsets inconsistent with the expert indices */
+                                  offsets inconsistent with the expert indices,
+                                  or (FP8 products) outside the rows or decreasing */
 
 /* Layer description; the pages' MoELayer(d_model, d_ff, n_experts, top_k,
  * n_shared, use_bias_balance) constructor (§9). */
@@ -501,8 +502,14 @@ MOE_API moe_status_t moe_backward_fp8w(const moe_desc_t* d, const void* w_gate, 
  * nearest even.  bf16 elements often fall on the border between two codes, so
  * the last bit of s decides codes.  A NaN element has the code NaN; a block with an infinity has
  * an infinite scale, so its row's products are NaN.  The products of each
- * block of 128 are summed unscaled in fp32, multiplied by both scales and
- * added in fp32 in the order of the blocks.
+ * block of 128 are summed unscaled in fp32, multiplied by the fp32 product of
+ * both scales (below 2^-126 that product loses bits, and above fp32's range it
+ * is infinite) and added in fp32 in the order of the blocks.  A call with few
+ * tiles may share each between 2, 4 or 8 thread blocks: each then adds its
+ * own run of consecutive blocks in that order, and the runs' sums are added in
+ * order.  Whether it does depends on rows, n_groups, n, k and the device alone:
+ * a call repeated gives the same bits, but a row's last bits may differ between
+ * calls of different shapes.
  * Scales of an activation matrix [rows, cols]: fp32, block b of row r at
  * scales[r * scale_ld + b], scale_ld = MOE_FP8_SCALE_LD(cols) in the layer's
  * calls.  d->precision is 4 ("fp8b"). */
@@ -551,7 +558,9 @@ MOE_API moe_status_t moe_permute_fp8b(const moe_desc_t* d, const void* x, const 
 /* moe_grouped_ffn on FP8 operands: GEMM1 from xq_perm / xs_perm and w1, w3;
  * its epilogue computes h = silu(a1) * a3 in fp32 and quantises it per 1 x 128
  * (codes of h times the fp32 reciprocal of the block's scale; kept in the
- * workspace); GEMM2 with w2 into y_perm [R,D] bf16.  The
+ * workspace); GEMM2 with w2 into y_perm [R,D] bf16, the layer's buffer in
+ * every precision: an expert's output is rounded to bf16 before the combine
+ * weighs it, and the combine's sum once more.  The
  * shared expert does the same from xq_tok / xs_tok into y_shared.  wq: codes
  * and fp32 tile scales from moe_quantize_fp8_tile.  `saved` receives bf16 a1,
  * a3, h (a1s, a3s, hs) for the backward, or holds NULL pointers. */

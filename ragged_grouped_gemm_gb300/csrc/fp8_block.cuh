@@ -37,7 +37,9 @@ enum Fp8Epi : int {
 // For every group g and its rows r in [offsets[g], offsets[g + 1]):
 //   acc[r, n] = sum over k-blocks b of a_scale[r, b] * b_scale[g, n / 128, b] * sum_{k in b} a[r, k] b[g, n, k]
 // over the contraction sources (b[1] is instead the second half of the N tile
-// with `dual`).  B is stored [N, K] per group, or [K, N] with b_mn.
+// with `dual`), in the order of the k-blocks, or, where a cluster of 2, 4 or 8 CTAs shares a
+// tile, each CTA's run of them in that order and then the runs' sums in order.  B is stored
+// [N, K] per group, or [K, N] with b_mn.  Offsets that decrease: no row is written.
 struct Fp8GemmArgs {
   Fp8Epi epi = FP8_EPI_BF16;
   bool b_mn = false;
@@ -51,7 +53,7 @@ struct Fp8GemmArgs {
   int64_t a_scale_ld = 0;
   const int32_t* offsets = nullptr;   // device, [groups + 1]
   int groups = 1;
-  int64_t rows = 0;            // rows of A; offsets past it are cut to it (DEV_BAD_OFFSETS)
+  int64_t rows = 0;            // rows of A; offsets outside 0 .. rows are cut to it (DEV_BAD_OFFSETS)
   void* out0 = nullptr;
   void* out1 = nullptr;
   void* out2 = nullptr;

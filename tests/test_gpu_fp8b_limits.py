@@ -123,3 +123,47 @@ def test_layer_products_of_small_h(sizes, d, f, down):
         if lo < hi:
             want[lo:hi] = O.swiglu_expert_fp8b(x[lo:hi], v["w1"][i], v["w3"][i], v["w2"][i])[0]
     assert rel(np32(y), want) < BF16_TOL
+
+
+def test_layer_rounds_its_expert_outputs_and_their_sum_and_nothing_else():
+    """Against the formula with bf16 expert outputs the layer's output is off by what moves a value over
+    a border: fp32 sums of 2048 products, about 2^-21 of their magnitude, change a share of 2^-13
+    of the bf16 roundings by a step of 2^-8 (2^-14 in the norm), and a share of 2^-17 of h's codes (128
+    a binade pair of 2^-4) by 2^-3, which is 2^-11.5 of the norm of h and so of y.  2^-10 in all, a third of the 2.7e-3
+    that leaving out the first rounding makes.  A second run gives the same bits."""
+    cfg = MoEConfig("rounds", 96, 2048, 512, 8, 4, precision="fp8b")
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(96, 2048, generator=g).to(torch.bfloat16)
+    idx = torch.stack([torch.randperm(8, generator=g)[:4] for _ in range(96)]).to(torch.int32)
+    w = torch.softmax(torch.randn(96, 4, generator=g), 1)
+    off = np.concatenate([[0], np.cumsum(np.bincount(idx.numpy().ravel(), minlength=8))]).astype(np.int32)
+    desc = api.make_desc(cfg)
+    ws = torch.empty(api.moe_workspace_size(desc)[0], dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(ws)
+    wq = {}
+    for key, r, c in (("w1", 512, 2048), ("w3", 512, 2048), ("w2", 2048, 512)):
+        wq[key], wq[key + "_scale"] = _tiles(g, 8, r, c)
+    rows, copies = (torch.empty(384, dtype=torch.int32, device="cuda") for _ in range(2))
+    xq = torch.empty(384, 2048, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(384, api.fp8_scale_ld(2048), device="cuda")
+    y = torch.empty(384, 2048, dtype=torch.bfloat16, device="cuda")
+    outs = []
+    for _ in range(2):
+        out = torch.empty(96, 2048, dtype=torch.bfloat16, device="cuda")
+        o = torch.from_numpy(off).cuda()
+        api.moe_permute_fp8b(desc, x.cuda(), idx.cuda(), o, rows, copies, None, xq, xs, None, None, ws)
+        api.moe_grouped_ffn_fp8b(desc, xq, xs, o, None, None, wq, {}, y, None, ws)
+        api.moe_combine(desc, y, rows, w.cuda(), None, out)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1])
+    v = {k: O.fp8_tile_value(wq[k].cpu().numpy(), wq[k + "_scale"].cpu().numpy()) for k in ("w1", "w3", "w2")}
+    xv, once, twice = O.fp8_rows_value(x.float().numpy()), np.zeros((96, 2048)), np.zeros((96, 2048))
+    for e in range(8):
+        tok, kk = np.nonzero(idx.numpy() == e)
+        ye = O.swiglu_expert_fp8b(xv[tok], v["w1"][e], v["w3"][e], v["w2"][e])[0]
+        gw = w.numpy()[tok, kk].astype(np.float64)[:, None]
+        np.add.at(once, tok, ye * gw)
+        np.add.at(twice, tok, O.bf16_round(ye.astype(np.float32)).astype(np.float64) * gw)
+    stored = O.bf16_round(twice.astype(np.float32))
+    assert rel(np32(outs[0]), stored) < 2.0 ** -10
+    assert rel(np32(outs[0]), once) < (2.0 ** -8 / np.sqrt(3)) * np.sqrt(2)    # two evenly spread roundings at most
