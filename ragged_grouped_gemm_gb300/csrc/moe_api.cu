@@ -57,7 +57,7 @@ struct WsLayout {
   size_t q_dy = 0, q_dys = 0, q_da1 = 0, q_da1s = 0, q_da3 = 0, q_da3s = 0, pad = 0, pad_sh = 0;
   size_t t_d0 = 0, t_d0s = 0, t_d1 = 0, t_d1s = 0, t_f0 = 0, t_f0s = 0, t_f1 = 0, t_f1s = 0;
   int64_t rp = 0;   // leading dimension of the transposed code matrices
-  size_t norm = 0;  // partial sums of the layer norm's weight gradients
+  size_t norm = 0;  // partial sums of the layer norm's weight gradients (over others' scratch)
 };
 
 int64_t ld16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -137,7 +137,11 @@ WsLayout layout(const moe_desc_t& d) {
     L.q_da3 = o; o = align_up(o + R * Fm);
     L.q_da3s = o; o = align_up(o + R * moe::fp8_scale_ld(Fm) * 4);
   }
-  L.norm = o; o = align_up(o + moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
+  // the norm's backward is a call of its own: its sums lie over the layer backward's
+  // gradients (dl .. dwg, which that writes before it reads) where they fit
+  const size_t norm = align_up(moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
+  L.norm = norm <= L.gmaps - L.dl ? L.dl : o;
+  if (L.norm == o) o += norm;
   L.total = o;
   return L;
 }

@@ -96,3 +96,43 @@ def test_layernorm_timeout_selftest_refusals(lib):
     assert call(ws=None) == 3 and call(n=b - 1) == 3
     for wide in (1024, 32768 + 64):                       # rows that no wait holds up, rows that are too wide
         assert call(desc=_desc(d_model=wide)) == 2
+
+
+# bytes of the backward workspace of the layer alone
+LAYER_BACKWARD_BYTES = [
+    ("tiny", "bf16", 1751808),
+    ("tiny", "mxfp8", 2597120),
+    ("tiny", "fp8w", 1751808),
+    ("mixtral", "bf16", 541083136),
+    ("mixtral", "mxfp8", 1289373696),
+    ("mixtral", "fp8w", 541083136),
+    ("dsv3", "bf16", 870979584),
+    ("dsv3", "mxfp8", 2575179264),
+    ("dsv3", "fp8w", 870979584),
+    ("mixtral_quarter", "bf16", 188761600),
+    ("mixtral_quarter", "mxfp8", 460179456),
+    ("mixtral_quarter", "fp8w", 188761600),
+    ("dsv3_e16", "bf16", 49044736),
+    ("dsv3_e16", "mxfp8", 155016960),
+    ("dsv3_e16", "fp8w", 49044736),
+    ("small_softmax", "bf16", 5666304),
+    ("small_softmax", "mxfp8", 12626176),
+    ("small_softmax", "fp8w", 5666304),
+    ("small_sigmoid", "bf16", 9567488),
+    ("small_sigmoid", "mxfp8", 22138368),
+    ("small_sigmoid", "fp8w", 9567488),
+    ("small_fine", "bf16", 8250112),
+    ("small_fine", "mxfp8", 29110272),
+    ("small_fine", "fp8w", 8250112)]
+
+
+@pytest.mark.parametrize("name,precision,layer", LAYER_BACKWARD_BYTES)
+def test_norm_adds_nothing_to_the_layers_workspace(lib, name, precision, layer):
+    """Its partial sums lie over the layer backward's own scratch."""
+    assert _ws(lib, api.make_desc(CONFIGS[name].replace(precision=precision)))[1] == layer
+
+
+def test_norm_workspace_where_the_layers_is_smaller(lib):
+    n, d = 16, 32768
+    f, b = _ws(lib, _desc(n_tok=n, d_model=d, d_ff=64, n_exp=8, top_k=1))
+    assert b - f >= n * 2 * d * 4                     # a partial sum of each gradient for every row
