@@ -860,7 +860,11 @@ class MoEBlock:
 
     def backward(self, dout: torch.Tensor) -> dict:
         """``dout`` of the residual stream's type; returns dx, dgamma, dbeta and,
-        under "layer", the gradients of :meth:`MoELayer.backward`."""
+        under "layer", the gradients of :meth:`MoELayer.backward`.  Needs ``train`` and a forward."""
+        if not self.train:
+            raise ValueError("a block built with train=False has no backward")
+        if self.x is None:
+            raise ValueError("backward needs the forward that it belongs to")
         g = self.grads
         moe_dropout_backward(self.desc, dout, self.used, self.p, self.dmoe)
         inner = self.layer.backward(self.dmoe)

@@ -136,3 +136,13 @@ def test_norm_workspace_where_the_layers_is_smaller(lib):
     n, d = 16, 32768
     f, b = _ws(lib, _desc(n_tok=n, d_model=d, d_ff=64, n_exp=8, top_k=1))
     assert b - f >= n * 2 * d * 4                     # a partial sum of each gradient for every row
+
+
+def test_block_backward_without_training_or_forward_is_refused():
+    block = api.MoEBlock.__new__(api.MoEBlock)
+    block.train, block.x = False, object()
+    with pytest.raises(ValueError, match="train=False"):
+        block.backward(None)
+    block.train, block.x = True, None
+    with pytest.raises(ValueError, match="forward"):
+        block.backward(None)
