@@ -48,7 +48,8 @@ def _p(t: torch.Tensor | None, dtype=None, shape=None, name="tensor"):
 
 
 # The handle of the current stream without building a Stream object for it,
-# which took 3 of the 11 us that one norm's enqueue did.
+# which took 3 of the 11 us that one norm's enqueue did.  Neither looks whether CUDA is
+# initialised: every call passes a CUDA tensor first.  Without them, the public calls.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
