@@ -241,36 +241,48 @@ __device__ __forceinline__ void load_f32x8(const float* p, int c, float (&f)[8])
   for (int j = 0; j < 8; ++j) f[j] = v.get(j);
 }
 
-// Waits for a row.  A wait that runs out raises `stop` in every block of the cluster, where
-// the others' waits end at it; a caller looks at it behind the row's next barrier, which
+// Waits for a row.  A wait that runs out raises `stop` in every block of the cluster, at which
+// no later wait of the turn begins; a caller looks at it behind the row's next barrier, which
 // no thread passes before the row's waits, and takes turns between two of them where there is one
 // barrier a turn, so that all threads find the same.  It leaves at the turn's end, so that nothing
 // waits for the look, and what the turn stored is overwritten.
 constexpr int kRowWaitSite = 900;
+__device__ __forceinline__ bool stopped(const int* stop) { return *static_cast<const volatile int*>(stop) != 0; }
 template <int C>
 __device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, int* stop, const RowWait& w) {
-  if (mbar_wait_bounded(bar, parity, stop, w.status, kRowWaitSite, w.limit_ns)) return;
+  if (mbar_try_wait(bar, parity)) return;
+  if (!stopped(stop) && mbar_wait_drain(bar, parity, w.limit_ns)) return;
+  *static_cast<volatile int*>(stop) = 1;
+  if (w.status) {
+    atomicOr(w.status, DEV_TIMEOUT);
+    atomicExch(w.status + 1, kRowWaitSite);
+  }
   if constexpr (C > 1)
     for (int c = 0; c < C; ++c)
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(stop), c)), "r"(1) : "memory");
 }
-__device__ __forceinline__ bool stopped(const int* stop) { return *static_cast<const volatile int*>(stop) != 0; }
-// One thread's wait, with a limit too, for the copies of rows from r on that are under way when
-// a block gives up: those of `stages` rows.
-__device__ __noinline__ void drain_rows(uint64_t* full, int stages, int64_t r, int64_t row0, int64_t step, int64_t rows,
-                                        uint64_t limit_ns) {
-  int64_t j = (r - row0) / step;
-  for (int k = 0; k < stages && r < rows; ++k, ++j, r += step)
-    mbar_wait_drain(&full[j % stages], static_cast<uint32_t>(j / stages) & 1u, limit_ns / 8);
-}
 __device__ __forceinline__ float not_a_number() { return __uint_as_float(0x7FC00000u); }
-// Vectors first .. first + n8 - 1 of row r: not a number.
+// What a block does that gives up at row r: one thread waits, with a limit too, for the copies
+// under way, those of `stages` rows; vectors first .. first + n8 - 1 of the rows left are not a number.
 template <bool F32>
-__device__ __forceinline__ void fill_nan(void* out, int64_t r, int d8, int first, int n8) {
+__device__ __noinline__ void give_up(uint64_t* full, int stages, int64_t r, int64_t row0, int64_t step, int64_t rows,
+                                     int d8, int first, int n8, void* out, float* mean, float* rstd,
+                                     uint64_t limit_ns) {
+  if (threadIdx.x == 0) {
+    int64_t j = (r - row0) / step, at = r;
+    for (int k = 0; k < stages && at < rows; ++k, ++j, at += step)
+      mbar_wait_drain(&full[j % stages], static_cast<uint32_t>(j / stages) & 1u, limit_ns / 8);
+  }
   float f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = not_a_number();
-  for (int c = threadIdx.x; c < n8; c += blockDim.x) Vec8<F32>::store(out, r * d8 + first + c, f);
+  for (; r < rows; r += step) {
+    for (int c = threadIdx.x; c < n8; c += blockDim.x) Vec8<F32>::store(out, r * d8 + first + c, f);
+    if (threadIdx.x == 0 && first == 0) {
+      if (mean) mean[r] = not_a_number();
+      if (rstd) rstd[r] = not_a_number();
+    }
+  }
 }
 
 // A block's share of the rows: vectors first .. first + n8 - 1 of rows row0, row0 + step, ...
@@ -393,14 +405,8 @@ __global__ void __launch_bounds__(T, 1024 / T) layernorm_ring_kernel(
       ph ^= 1u;
     }
   }
-  if (r < rows && tid == 0) drain_rows(full, stages, r, blockIdx.x, gridDim.x, rows, wait.limit_ns);
-  for (; r < rows; r += gridDim.x) {
-    fill_nan<false>(y, r, d8, 0, d8);
-    if (tid == 0) {
-      if (mean) mean[r] = not_a_number();
-      if (rstd) rstd[r] = not_a_number();
-    }
-  }
+  if (r < rows)
+    give_up<false>(full, stages, r, blockIdx.x, gridDim.x, rows, d8, 0, d8, y, mean, rstd, wait.limit_ns);
 }
 
 // T threads of C blocks share a row, V vectors of eight columns each; `stages` row
@@ -553,14 +559,8 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_cluster_kernel(
     }
     if (halt) break;
   }
-  if (r < rows && tid == 0) drain_rows(full, stages, r, part.row0, part.step, rows, wait.limit_ns);
-  for (; r < rows; r += part.step) {
-    fill_nan<false>(y, r, d8, part.first, n8);
-    if (tid == 0 && part.first == 0) {
-      if (mean) mean[r] = not_a_number();
-      if (rstd) rstd[r] = not_a_number();
-    }
-  }
+  if (r < rows)
+    give_up<false>(full, stages, r, part.row0, part.step, rows, d8, part.first, n8, y, mean, rstd, wait.limit_ns);
 }
 
 // R rows pass through a block together, packed: two bf16 rows
@@ -688,12 +688,11 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_ring_kernel(
     if (halt) break;
   }
   if (r < rows) {
-    if (tid == 0) drain_rows(full, stages, r, own.row0, step, rows, wait.limit_ns);
+    give_up<F32>(full, stages, r, own.row0, step, rows, d8, own.first, n8, dx, nullptr, nullptr, wait.limit_ns);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = not_a_number();
-    for (; r < rows; r += step) fill_nan<F32>(dx, r, d8, own.first, n8);
   }
   float* p = part + (own.row0 * 2 * d8 + own.first) * 8;
 #pragma unroll

@@ -236,6 +236,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// Zero below a1 = -87, where 1 + e^-a1 is past 2^126 and silu smaller than 2^-119.
 __device__ __forceinline__ float swiglu(float a1, float a3) { return __fdividef(a1, 1.0f + __expf(-a1)) * a3; }
 // What a block of h with the scale s is multiplied by before the scale's reciprocal, which
 // is beyond fp32's range for the smallest scales: the reciprocal is that of h_factor(s) * s.
