@@ -628,6 +628,147 @@ MOE_API moe_status_t moe_combine_dropout(const moe_desc_t* d, const void* y_perm
 MOE_API moe_status_t moe_dropout_backward(const moe_desc_t* d, const void* dout, int32_t dout_f32,
                                           const int64_t* rng, double p, void* dy, void* stream);
 
+/* ---------------------------------------- balance over sequences --
+ * The load-balancing loss of a batch of ragged sequences with the router's
+ * z-loss, and the way of their gradient to x and W_g.  ("LLM Infrastructure
+ * Engineering 08: MoE Training Engineering" §6.2 gives the loss over one batch,
+ * moe_aux_loss; the sequences, the z-loss and the products behind the gradient
+ * are additions of this library.) */
+
+/* Sequence s holds the tokens [seq_offsets[s], seq_offsets[s+1]), T_s of them;
+ * tokens of no sequence (before the first, behind the last) are padding and
+ * count nowhere.  With S' sequences that are not empty, T = sum T_s,
+ * f_si = counts_si / T_s and q_t the gate's distribution over all experts as in
+ * moe_aux_loss:
+ *   counts[s,i] (int32 [n_seq,E], out) = copies of sequence s routed to expert i,
+ *   loss[0] = coef * E / S' * sum_s sum_i f_si * mean over s of q_ti,
+ *   loss[1] = z_coef / T * sum_t (log sum_i exp(logits_ti))^2,
+ *   dlogits [N,E] (fp32, NULL: not computed) = dloss[0] * d(loss[0] + loss[1]) / d logits
+ * with f held fixed; padding rows are zero.  dloss is one float on the device
+ * (NULL: 1), the upstream gradient or a loss scale.  One sequence over all tokens
+ * and z_coef = 0 give moe_aux_loss.  A logit of -inf (a masked expert) has
+ * probability 0; a row of nothing else has no probabilities, no z-loss and a zero
+ * gradient, its copies still count.  A NaN or +inf logit makes its row and the
+ * losses NaN.  logits [N,E], topk_idx [N,K] from moe_route.  An entry of
+ * seq_offsets outside [0, N] is cut to that range and sets MOE_DEV_BAD_OFFSETS;
+ * entries that decrease set it too, and every output is zero then.  An index
+ * outside [0, E) is not counted (MOE_DEV_BAD_INDEX).  Sums in a fixed order:
+ * equal calls give equal bits.  n_seq >= 1.  Needs the forward workspace. */
+MOE_API moe_status_t moe_balance_loss(const moe_desc_t* d, const float* logits, const int32_t* topk_idx,
+                                      const int32_t* seq_offsets, int64_t n_seq, float coef, float z_coef,
+                                      const float* dloss, int32_t* counts, float* loss, float* dlogits, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* The dense router gradient behind dlogits [N,E] (fp32, for instance from
+ * moe_balance_loss; moe_backward's own covers the selected experts alone):
+ *   dx [N,D] (bf16)        = dx_in + dlogits * W_g,
+ *   dw_gate [E,D] (fp32)   = dw_in + dlogits^T * x.
+ * dx_in and dw_in are nullable (zero) and may be the outputs themselves: after
+ * moe_backward, passing its dx and dw_gate on both sides adds the loss's
+ * gradient to them.  dlogits enters the tensor cores as a sum of bf16 numbers:
+ * two for dx (2^-17 of an entry is lost, dx itself is rounded at 2^-9), three for dw_gate
+ * (2^-24).  Needs the backward workspace. */
+MOE_API moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, const void* x, const void* w_gate,
+                                         const void* dx_in, void* dx, const float* dw_in, float* dw_gate, void* ws,
+                                         size_t ws_bytes, void* stream);
+
+/* --------------------------------------- 8-bit activation checkpoints --
+ * What a training forward keeps for its backward, in 8 bits (an addition of
+ * this library).  The bf16 layer keeps x_perm, a1, a3, h and y_perm, 6 R F + 4 R D
+ * bytes; here the layer keeps a1, a3 [R,F] and its input x [N,D] (not permuted)
+ * as MXFP8 rows, 1/32 more than 2 R F + N D bytes.  The codes and scales are
+ * those of moe_quantize_mxfp8 with one group: E4M3, one power-of-two scale per 32
+ * elements of a row, scales [cols/32][MOE_MX_SCALE_LD(rows)].  Every kept value is
+ * a bf16 number, so the backward's bf16 products on them round nothing more.
+ * The forward's results are those of moe_grouped_ffn: only the backward sees the
+ * kept values, and its gradients are those of a layer whose a1, a3 and x have
+ * them.  h is formed again from a1 and a3, and the gate gradient
+ * <dY, y> is formed as <dY W2, h>, so that no y is kept.  bf16 layers
+ * (precision 0), dropless. */
+typedef struct {
+  void* a1;         /* [R,F] codes */
+  void* a1_scale;   /* [F/32][MOE_MX_SCALE_LD(R)] */
+  void* a3;
+  void* a3_scale;
+  void* a1s;        /* [N,Fs] codes of the shared expert (ignored when n_shared == 0) */
+  void* a1s_scale;  /* [Fs/32][MOE_MX_SCALE_LD(N)] */
+  void* a3s;
+  void* a3s_scale;
+} moe_ckpt_t;
+
+/* What moe_backward_ckpt reads of the forward. */
+typedef struct {
+  const void* x;               /* [N,D] codes: moe_quantize_mxfp8 of the layer's input */
+  const void* x_scale;         /* [D/32][MOE_MX_SCALE_LD(N)] */
+  const float* logits;         /* as in moe_fwd_state_t */
+  const int32_t* topk_idx;
+  const float* topk_w;
+  const int32_t* offsets;
+  const int32_t* row_of_copy;
+  const int32_t* copy_of_row;
+  moe_ckpt_t kept;             /* from moe_grouped_ffn_ckpt */
+} moe_ckpt_state_t;
+
+/* Bytes of workspace of moe_grouped_ffn_ckpt and moe_backward_ckpt (more than
+ * moe_workspace_size gives; such a workspace serves every other call too).
+ * Layers that run one after another on one stream can share it. */
+MOE_API moe_status_t moe_ckpt_workspace_size(const moe_desc_t* d, size_t* bytes);
+
+/* moe_grouped_ffn that keeps a1 and a3 in 8 bits (encoded from the fp32
+ * accumulators by the first product's epilogue) and nothing else: y_perm and
+ * y_shared have the bits of moe_grouped_ffn. */
+MOE_API moe_status_t moe_grouped_ffn_ckpt(const moe_desc_t* d, const void* x_perm, const int32_t* offsets,
+                                          const void* x, const moe_expert_weights_t* w, const moe_ckpt_t* kept,
+                                          void* y_perm, void* y_shared, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_backward from the kept values; every output as there. */
+MOE_API moe_status_t moe_backward_ckpt(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_t* w,
+                                       const moe_ckpt_state_t* s, const void* dy, const moe_grads_t* g, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Its first product, for given groups: for the rows r in [offsets[e], offsets[e+1])
+ * of every expert e, with g = row_w[r] (row_w NULL: 1), dh = dy[r] W2_e and
+ * s = sigmoid(a1):
+ *   da1 = g dh a3 s (1 + a1 (1 - s)),  da3 = g dh a1 s,  h = g a1 s a3   (bf16 [rows,f]),
+ *   dg[r] = <dh, a1 s a3>  (fp32, nullable): the gradient of row_w.
+ * h carries the weight, so that dW2_e = dy^T h over the expert's rows.
+ * dy [rows,d] bf16; w2 [n_groups,d,f]; a1, a3 [rows,f] kept codes with scales
+ * [f/32][scale_ld], scale_ld >= rows and a multiple of 16; d and f multiples of
+ * 64; n_groups <= 1024.  offsets as in moe_grouped_gemm_fp8: cut to [0, rows] and
+ * flagged, nothing written where they decrease; rows of no group are not
+ * written.  ws: moe_swiglu_backward_ckpt_workspace_size() bytes, status words
+ * first (moe_workspace_init before the first use). */
+MOE_API moe_status_t moe_swiglu_backward_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t d, int64_t f,
+                                                             size_t* bytes);
+MOE_API moe_status_t moe_swiglu_backward_ckpt(int64_t n_groups, int64_t rows, int64_t d, int64_t f, const void* dy,
+                                              const int32_t* offsets, const void* w2, const float* row_w,
+                                              const void* a1, const void* a1_scale, const void* a3,
+                                              const void* a3_scale, int64_t scale_ld, void* da1, void* da3, void* h,
+                                              float* dg, void* ws, size_t ws_bytes, void* stream);
+
+/* Weight gradients from kept rows: for every group e
+ *   dw[e] [m,k] (fp32) = sum over the rows r of e of dy[r]^T x[row_map[r] / row_div],
+ * zero for an empty group.  dy [rows,m] bf16; x [x_rows,k] kept codes with scales
+ * [k/32][scale_ld], scale_ld >= x_rows and a multiple of 16.  row_map [rows]
+ * (copy_of_row with row_div = top_k reads token rows in expert order; NULL: row r,
+ * x_rows = rows); an index outside [0, x_rows) stands for a zero row and sets
+ * MOE_DEV_BAD_INDEX.  m and k multiples of 64; n_groups <= 1024; offsets as above,
+ * every gradient zero where they decrease.  ws:
+ * moe_grouped_wgrad_ckpt_workspace_size() bytes, status words first. */
+MOE_API moe_status_t moe_grouped_wgrad_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t m, int64_t k,
+                                                           size_t* bytes);
+MOE_API moe_status_t moe_grouped_wgrad_ckpt(int64_t n_groups, int64_t rows, int64_t m, int64_t k, const void* dy,
+                                            const void* x, const void* x_scale, int64_t x_rows, int64_t scale_ld,
+                                            const int32_t* row_map, int32_t row_div, const int32_t* offsets,
+                                            float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* The values of MXFP8 rows as bf16 (the inverse of moe_quantize_mxfp8 with one
+ * group): codes [rows,cols], scales [cols/32][scale_ld] -> out [rows,cols].  Exact
+ * wherever bf16 reaches: a block whose largest element is below 2^-116 may round.
+ * cols must be a multiple of 32. */
+MOE_API moe_status_t moe_dequantize_mxfp8(const void* codes, const void* scales, int64_t rows, int64_t cols,
+                                          int64_t scale_ld, void* out, void* stream);
+
 /* moe_permute without a workspace (no counterpart in the pages; an addition
  * of this library for callers that cannot allocate).  Same inputs, outputs
  * and results as moe_permute, for callers that cannot give the library any

@@ -10,3 +10,4 @@ package.
 from .moe_oracle import *  # noqa: F401,F403
 from .mxfp8 import *  # noqa: F401,F403
 from .fp8_block import *  # noqa: F401,F403
+from .train_step import *  # noqa: F401,F403

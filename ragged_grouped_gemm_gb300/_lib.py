@@ -42,6 +42,15 @@ class MoeGrads(ctypes.Structure):
                 ("dws3", c_vp), ("dws2", c_vp), ("dg", c_vp), ("dlogits", c_vp)]
 
 
+class MoeCkpt(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("a1", "a1_scale", "a3", "a3_scale", "a1s", "a1s_scale", "a3s", "a3s_scale")]
+
+
+class MoeCkptState(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("x_scale", c_vp), ("logits", c_vp), ("topk_idx", c_vp), ("topk_w", c_vp),
+                ("offsets", c_vp), ("row_of_copy", c_vp), ("copy_of_row", c_vp), ("kept", MoeCkpt)]
+
+
 class MoeExpertWeightsMx(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in ("w1", "w1_scale", "w3", "w3_scale", "w2", "w2_scale",
                                     "ws1", "ws1_scale", "ws3", "ws3_scale", "ws2", "ws2_scale")]
@@ -113,6 +122,22 @@ SIGNATURES = {
     "moe_combine_dropout": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
                                     ctypes.c_double, c_vp, c_vp]),
     "moe_dropout_backward": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_i32, c_vp, ctypes.c_double, c_vp, c_vp]),
+    "moe_balance_loss": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, ctypes.c_int64, ctypes.c_float,
+                                 ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_router_backward": (c_i32, [ctypes.POINTER(MoeDesc)] + [c_vp] * 8 + [ctypes.c_size_t, c_vp]),
+    "moe_ckpt_workspace_size": (c_i32, [ctypes.POINTER(MoeDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_grouped_ffn_ckpt": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, c_vp, c_vp, ctypes.POINTER(MoeExpertWeights),
+                                     ctypes.POINTER(MoeCkpt), c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_backward_ckpt": (c_i32, [ctypes.POINTER(MoeDesc), c_vp, ctypes.POINTER(MoeExpertWeights),
+                                  ctypes.POINTER(MoeCkptState), c_vp, ctypes.POINTER(MoeGrads), c_vp,
+                                  ctypes.c_size_t, c_vp]),
+    "moe_swiglu_backward_ckpt_workspace_size": (c_i32, [ctypes.c_int64] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_swiglu_backward_ckpt": (c_i32, [ctypes.c_int64] * 4 + [c_vp] * 8 + [ctypes.c_int64] + [c_vp] * 5
+                                 + [ctypes.c_size_t, c_vp]),
+    "moe_grouped_wgrad_ckpt_workspace_size": (c_i32, [ctypes.c_int64] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_grouped_wgrad_ckpt": (c_i32, [ctypes.c_int64] * 4 + [c_vp] * 3 + [ctypes.c_int64] * 2
+                               + [c_vp, c_i32, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_dequantize_mxfp8": (c_i32, [c_vp, c_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, c_vp, c_vp]),
     "moe_timing_enable": (c_i32, [c_i32]),
     "moe_timing_read": (c_i32, [c_i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(ctypes.c_int64)]),

@@ -217,26 +217,35 @@ def _bwd_structs(desc, state: dict, grads: dict, need_x_perm: bool = True):
         _p(S.get("hs"), BF16, (n, fs), "hs") if sh else None,
         _p(S.get("offsets_full"), I32, (e + 1,), "offsets_full"),
         _p(S.get("copy_of_row_full"), I32, (r,), "copy_of_row_full"))
-    G = grads
-    gr = _lib.MoeGrads(
+    return st, _grads_struct(desc, grads)
+
+
+def _grads_struct(desc, grads: dict):
+    n, d, f, e, k = desc.n_tok, desc.d_model, desc.d_ff, desc.n_exp, desc.top_k
+    fs, sh, G = desc.d_ff_shared, desc.n_shared, grads
+    return _lib.MoeGrads(
         _p(G["dx"], BF16, (n, d), "dx"), _p(G["dw_gate"], F32, (e, d), "dw_gate"), _p(G["dw1"], F32, (e, f, d), "dw1"),
         _p(G["dw3"], F32, (e, f, d), "dw3"), _p(G["dw2"], F32, (e, d, f), "dw2"),
         _p(G.get("dws1"), F32, (fs, d), "dws1") if sh else None, _p(G.get("dws3"), F32, (fs, d), "dws3") if sh else None,
         _p(G.get("dws2"), F32, (d, fs), "dws2") if sh else None,
         _p(G.get("dg"), F32, (n, k), "dg"), _p(G.get("dlogits"), F32, (n, k), "dlogits"))
-    return st, gr
+
+
+def _weights_struct(desc, weights: dict):
+    d, f, e = desc.d_model, desc.d_ff, desc.n_exp
+    fs, sh = desc.d_ff_shared, desc.n_shared
+    return _lib.MoeExpertWeights(_p(weights["w1"], BF16, (e, f, d), "w1"), _p(weights["w3"], BF16, (e, f, d), "w3"),
+                                 _p(weights["w2"], BF16, (e, d, f), "w2"),
+                                 _p(weights.get("ws1"), BF16, (fs, d), "ws1") if sh else None,
+                                 _p(weights.get("ws3"), BF16, (fs, d), "ws3") if sh else None,
+                                 _p(weights.get("ws2"), BF16, (d, fs), "ws2") if sh else None)
 
 
 def moe_backward(desc, w_gate, weights: dict, state: dict, dy, grads: dict, ws, stream=None):
     """``weights``: w1, w3, w2 (+ ws1, ws3, ws2); ``state``: the fields of
     moe_fwd_state_t; ``grads``: the fields of moe_grads_t (dg, dlogits optional)."""
-    n, d, f, e = desc.n_tok, desc.d_model, desc.d_ff, desc.n_exp
-    fs, sh = desc.d_ff_shared, desc.n_shared
-    w = _lib.MoeExpertWeights(_p(weights["w1"], BF16, (e, f, d), "w1"), _p(weights["w3"], BF16, (e, f, d), "w3"),
-                              _p(weights["w2"], BF16, (e, d, f), "w2"),
-                              _p(weights.get("ws1"), BF16, (fs, d), "ws1") if sh else None,
-                              _p(weights.get("ws3"), BF16, (fs, d), "ws3") if sh else None,
-                              _p(weights.get("ws2"), BF16, (d, fs), "ws2") if sh else None)
+    n, d, e = desc.n_tok, desc.d_model, desc.n_exp
+    w = _weights_struct(desc, weights)
     st, gr = _bwd_structs(desc, state, grads)
     _check("moe_backward", _lib.load().moe_backward(
         ctypes.byref(desc), _p(w_gate, BF16, (e, d), "w_gate"), ctypes.byref(w), ctypes.byref(st),
@@ -625,16 +634,179 @@ def moe_dropout_backward(desc, dout, rng, p: float, dy, stream=None):
         _p(rng, torch.int64, (2,), "rng"), float(p), _p(dy, BF16, (n, d), "dy"), _s(stream)))
 
 
+# ------------------------------------------------------ balance over sequences
+def moe_balance_loss(desc, logits, topk_idx, seq_offsets, counts, loss, dlogits=None, ws=None, coef: float = 1.0,
+                     z_coef: float = 0.0, dloss=None, stream=None):
+    """Balance loss over ragged sequences and the router's z-loss: ``seq_offsets``
+    int32 [S + 1] (tokens of no sequence are padding); ``counts`` int32 [S, E],
+    ``loss`` fp32 [2] = balance, z; ``dlogits`` fp32 [N, E] their gradient times
+    ``dloss`` (one float on the device, None: 1)."""
+    n, e, k = desc.n_tok, desc.n_exp, desc.top_k
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        raise ValueError(f"seq_offsets must have one dimension and two entries at least, got {tuple(seq_offsets.shape)}")
+    s = seq_offsets.shape[0] - 1
+    _check("moe_balance_loss", _lib.load().moe_balance_loss(
+        ctypes.byref(desc), _p(logits, F32, (n, e), "logits"), _p(topk_idx, I32, (n, k), "topk_idx"),
+        _p(seq_offsets, I32, (s + 1,), "seq_offsets"), s, float(coef), float(z_coef), _p(dloss, F32, (1,), "dloss"),
+        _p(counts, I32, (s, e), "counts"), _p(loss, F32, (2,), "loss"), _p(dlogits, F32, (n, e), "dlogits"),
+        _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_router_backward(desc, dlogits, x, w_gate, dx_in, dx, dw_in, dw_gate, ws, stream=None):
+    """dx (bf16) = dx_in + dlogits W_g and dw_gate (fp32) = dw_in + dlogits^T x for
+    a dense ``dlogits`` fp32 [N, E]; ``dx_in``, ``dw_in`` may be None or the outputs."""
+    n, d, e = desc.n_tok, desc.d_model, desc.n_exp
+    _check("moe_router_backward", _lib.load().moe_router_backward(
+        ctypes.byref(desc), _p(dlogits, F32, (n, e), "dlogits"), _p(x, BF16, (n, d), "x"),
+        _p(w_gate, BF16, (e, d), "w_gate"), _p(dx_in, BF16, (n, d), "dx_in"), _p(dx, BF16, (n, d), "dx"),
+        _p(dw_in, F32, (e, d), "dw_in"), _p(dw_gate, F32, (e, d), "dw_gate"), _p(ws, name="ws"),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+# ------------------------------------------------- 8-bit activation checkpoints
+def moe_ckpt_workspace_size(desc) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_ckpt_workspace_size", _lib.load().moe_ckpt_workspace_size(ctypes.byref(desc), ctypes.byref(b)))
+    return b.value
+
+
+def ckpt_buffers(desc, device="cuda") -> dict:
+    """What one layer keeps for :func:`moe_backward_ckpt` in 8 bits: codes and
+    scales of a1, a3 (a1s, a3s with a shared expert) and of the input x."""
+    n, d, f = desc.n_tok, desc.d_model, desc.d_ff
+    shapes = {"x": (n, d), "a1": (n * desc.top_k, f), "a3": (n * desc.top_k, f)}
+    if desc.n_shared:
+        shapes.update(a1s=(n, desc.d_ff_shared), a3s=(n, desc.d_ff_shared))
+    out = {}
+    for key, (rows, cols) in shapes.items():
+        out[key] = torch.empty(rows, cols, dtype=U8, device=device)
+        out[key + "_scale"] = torch.empty(cols // 32, mx_scale_ld(rows), dtype=U8, device=device)
+    return out
+
+
+def _ckpt_struct(desc, kept: dict):
+    ptr = []
+    for key in ("a1", "a3", "a1s", "a3s"):
+        shared = key.endswith("s")
+        if shared and not desc.n_shared:
+            ptr += [None, None]
+            continue
+        rows, cols = (desc.n_tok, desc.d_ff_shared) if shared else (desc.n_tok * desc.top_k, desc.d_ff)
+        ptr += [_p(kept[key], U8, (rows, cols), key),
+                _p(kept[key + "_scale"], U8, (cols // 32, mx_scale_ld(rows)), key + "_scale")]
+    return _lib.MoeCkpt(*ptr)
+
+
+def moe_grouped_ffn_ckpt(desc, x_perm, offsets, x, weights: dict, kept: dict, y_perm, y_shared, ws, stream=None):
+    """:func:`moe_grouped_ffn` that keeps a1 and a3 in 8 bits (``kept``:
+    :func:`ckpt_buffers`) and no other activation."""
+    n, d, f, e, k = desc.n_tok, desc.d_model, desc.d_ff, desc.n_exp, desc.top_k
+    r, fs, sh = n * k, desc.d_ff_shared, desc.n_shared
+    w = _weights_struct(desc, weights)
+    _check("moe_grouped_ffn_ckpt", _lib.load().moe_grouped_ffn_ckpt(
+        ctypes.byref(desc), _p(x_perm, BF16, (r, d), "x_perm"), _p(offsets, I32, (e + 1,), "offsets"),
+        _p(x, BF16, (n, d), "x") if sh else None, ctypes.byref(w), ctypes.byref(_ckpt_struct(desc, kept)),
+        _p(y_perm, BF16, (r, d), "y_perm"), _p(y_shared, BF16, (n, d), "y_shared") if sh else None,
+        _p(ws, name="ws"), ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_backward_ckpt(desc, w_gate, weights: dict, state: dict, dy, grads: dict, ws, stream=None):
+    """:func:`moe_backward` from 8-bit checkpoints.  ``state``: the codes and scales of
+    :func:`ckpt_buffers` (x from :func:`moe_quantize_mxfp8`) and logits, topk_idx, topk_w, offsets,
+    row_of_copy, copy_of_row of the forward."""
+    n, d, e, k = desc.n_tok, desc.d_model, desc.n_exp, desc.top_k
+    S = state
+    st = _lib.MoeCkptState(
+        _p(S["x"], U8, (n, d), "x"), _p(S["x_scale"], U8, (d // 32, mx_scale_ld(n)), "x_scale"),
+        _p(S["logits"], F32, (n, e), "logits"), _p(S["topk_idx"], I32, (n, k), "topk_idx"),
+        _p(S["topk_w"], F32, (n, k), "topk_w"), _p(S["offsets"], I32, (e + 1,), "offsets"),
+        _p(S["row_of_copy"], I32, (n * k,), "row_of_copy"), _p(S["copy_of_row"], I32, (n * k,), "copy_of_row"),
+        _ckpt_struct(desc, S))
+    _check("moe_backward_ckpt", _lib.load().moe_backward_ckpt(
+        ctypes.byref(desc), _p(w_gate, BF16, (e, d), "w_gate"), ctypes.byref(_weights_struct(desc, weights)),
+        ctypes.byref(st), _p(dy, BF16, (n, d), "dy"), ctypes.byref(_grads_struct(desc, grads)), _p(ws, name="ws"),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_swiglu_backward_ckpt_workspace_size(n_groups: int, rows: int, d: int, f: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_swiglu_backward_ckpt_workspace_size", _lib.load().moe_swiglu_backward_ckpt_workspace_size(
+        n_groups, rows, d, f, ctypes.byref(b)))
+    return b.value
+
+
+def moe_swiglu_backward_ckpt(dy, offsets, w2, row_w, a1, a1_scale, a3, a3_scale, da1, da3, h, dg, ws, stream=None):
+    """The backward through w2 [G, d, f] and the SwiGLU from kept a1, a3 (codes uint8
+    [rows, f], scales uint8 [f / 32, ld]) for dy bf16 [rows, d]: da1, da3 and the weighted h, bf16
+    [rows, f], and dg fp32 [rows] (or None), the gradient of ``row_w`` (fp32 [rows], None: 1)."""
+    if w2.dim() != 3 or a1_scale.dim() != 2:
+        raise ValueError(f"w2 must have three dimensions and a1_scale two, got {tuple(w2.shape)}, "
+                         f"{tuple(a1_scale.shape)}")
+    g, d, f = w2.shape
+    rows, ld = dy.shape[0], a1_scale.shape[-1]
+    _check("moe_swiglu_backward_ckpt", _lib.load().moe_swiglu_backward_ckpt(
+        g, rows, d, f, _p(dy, BF16, (rows, d), "dy"), _p(offsets, I32, (g + 1,), "offsets"),
+        _p(w2, BF16, (g, d, f), "w2"), _p(row_w, F32, (rows,), "row_w"), _p(a1, U8, (rows, f), "a1"),
+        _p(a1_scale, U8, (f // 32, ld), "a1_scale"), _p(a3, U8, (rows, f), "a3"),
+        _p(a3_scale, U8, (f // 32, ld), "a3_scale"), ld, _p(da1, BF16, (rows, f), "da1"),
+        _p(da3, BF16, (rows, f), "da3"), _p(h, BF16, (rows, f), "h"), _p(dg, F32, (rows,), "dg"), _p(ws, name="ws"),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_grouped_wgrad_ckpt_workspace_size(n_groups: int, rows: int, m: int, k: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_grouped_wgrad_ckpt_workspace_size", _lib.load().moe_grouped_wgrad_ckpt_workspace_size(
+        n_groups, rows, m, k, ctypes.byref(b)))
+    return b.value
+
+
+def moe_grouped_wgrad_ckpt(dy, x, x_scale, offsets, row_map, row_div: int, dw, ws, stream=None):
+    """dw fp32 [G, m, k]: per group the sum over its rows of dy[r]^T x[row_map[r] // row_div] for dy
+    bf16 [rows, m] and kept rows x (codes uint8 [x_rows, k], scales uint8 [k / 32, ld]).  ``row_map``
+    None (with row_div 1): row r."""
+    if dw.dim() != 3 or x_scale.dim() != 2:
+        raise ValueError(f"dw must have three dimensions and x_scale two, got {tuple(dw.shape)}, "
+                         f"{tuple(x_scale.shape)}")
+    g, m, k = dw.shape
+    rows, x_rows, ld = dy.shape[0], x.shape[0], x_scale.shape[-1]
+    _check("moe_grouped_wgrad_ckpt", _lib.load().moe_grouped_wgrad_ckpt(
+        g, rows, m, k, _p(dy, BF16, (rows, m), "dy"), _p(x, U8, (x_rows, k), "x"),
+        _p(x_scale, U8, (k // 32, ld), "x_scale"), x_rows, ld, _p(row_map, I32, (rows,), "row_map"), int(row_div),
+        _p(offsets, I32, (g + 1,), "offsets"), _p(dw, F32, (g, m, k), "dw"), _p(ws, name="ws"),
+        ws.numel() * ws.element_size(), _s(stream)))
+
+
+def moe_dequantize_mxfp8(codes, scales, out, stream=None):
+    """The values of MXFP8 rows (codes uint8 [rows, cols], scales uint8 [cols / 32, ld]) in bf16."""
+    rows, cols = codes.shape
+    _check("moe_dequantize_mxfp8", _lib.load().moe_dequantize_mxfp8(
+        _p(codes, U8, name="codes"), _p(scales, U8, (cols // 32, scales.shape[-1]), "scales"), rows, cols,
+        scales.shape[-1], _p(out, BF16, (rows, cols), "out"), _s(stream)))
+
+
 # --------------------------------------------------------------- layer runner
 class MoELayer:
     """Buffers of one layer plus the forward / backward call sequences.
 
     ``params``: x-independent tensors from :func:`inputs.make_layer` on the GPU
     (w_gate, w1, w3, w2, bias, and ws1, ws3, ws2 with a shared expert).
+
+    ``checkpoint``: the forward keeps a1, a3 and x for the backward in 8 bits
+    (``ckpt``, about 2 R F + N D bytes) instead of 6 R F + 4 R D bytes of bf16
+    activations, and x itself is not read again.  ``share``: another
+    checkpointing layer of the same shapes, whose workspace and buffers in
+    passing (permuted rows, expert outputs) this layer uses as well; layers that
+    share run one after another on one stream, and a layer's ``experts`` and its
+    combine come one after the other.
     """
 
     def __init__(self, cfg: MoEConfig, params: dict, train: bool = True, device="cuda", gather: bool = False,
-                 fused_dispatch: bool = True):
+                 fused_dispatch: bool = True, checkpoint: bool = False, share: "MoELayer | None" = None):
+        if checkpoint and (not train or cfg.precision != "bf16" or cfg.capacity_factor > 0):
+            raise ValueError("8-bit checkpoints are kept by bf16 layers in training, without a capacity")
+        if share is not None and not (checkpoint and share.ckpt is not None
+                                      and bytes(make_desc(cfg)) == bytes(share.desc)):
+            raise ValueError("a layer shares buffers with a checkpointing layer of the same shapes only")
         self.cfg = cfg
         self.desc = make_desc(cfg)
         self.p = params
@@ -645,16 +817,19 @@ class MoELayer:
         # gather=True (inference, bf16 experts, no capacity): GEMM1 reads its rows
         # straight from x (moe_permute_maps + moe_grouped_ffn_gather), no x_perm
         self.gather = gather and (not train) and cfg.precision == "bf16" and cfg.capacity_factor <= 0
+        self.checkpoint = checkpoint
+        mine = share is None          # buffers in passing are this layer's own
+        keep = train and not checkpoint
         self.buf = {
             "logits": z(n, e, dt=F32), "topk_idx": z(n, k, dt=I32), "topk_w": z(n, k, dt=F32),
             "counts": z(e, dt=I32), "offsets": z(e + 1, dt=I32), "row_of_copy": z(r, dt=I32),
-            "copy_of_row": z(r, dt=I32), "x_perm": None if self.gather else z(r, d), "h": z(r, f),
-            "y_perm": z(r, d), "out": z(n, d),
-            "a1": z(r, f) if train else None, "a3": z(r, f) if train else None,
+            "copy_of_row": z(r, dt=I32), "x_perm": None if self.gather or not mine else z(r, d),
+            "h": None if checkpoint else z(r, f), "y_perm": z(r, d) if mine else None, "out": z(n, d),
+            "a1": z(r, f) if keep else None, "a3": z(r, f) if keep else None,
         }
         if cfg.n_shared:
-            self.buf.update(hs=z(n, fs), y_shared=z(n, d), a1s=z(n, fs) if train else None,
-                            a3s=z(n, fs) if train else None)
+            self.buf.update(hs=None if checkpoint else z(n, fs), y_shared=z(n, d) if mine else None,
+                            a1s=z(n, fs) if keep else None, a3s=z(n, fs) if keep else None)
         else:
             self.buf.update(hs=None, y_shared=None, a1s=None, a3s=None)
         self.w8 = cfg.precision == "fp8w"
@@ -686,9 +861,16 @@ class MoELayer:
                             xq_tok=z(n, d, dt=U8) if cfg.n_shared else None,
                             xs_tok=(torch.zeros(d // 32, mx_scale_ld(n), dtype=U8, device=device)
                                     if cfg.n_shared else None))
-        fwd_b, bwd_b = moe_workspace_size(self.desc)
-        self.ws = torch.empty((bwd_b if train else fwd_b) + 256, dtype=torch.uint8, device=device)
-        moe_workspace_init(self.ws)
+        self.ckpt = ckpt_buffers(self.desc, device) if checkpoint else None
+        if share is not None:
+            self.buf.update({key: share.buf[key] for key in ("x_perm", "y_perm", "y_shared")})
+            self.ws = share.ws
+        else:
+            fwd_b, bwd_b = moe_workspace_size(self.desc)
+            need = moe_ckpt_workspace_size(self.desc) if checkpoint else bwd_b if train else fwd_b
+            self.ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+            moe_workspace_init(self.ws)
+        self.balance = None
         self.grads = None
         if train:
             self.grads = {"dx": z(n, d), "dw_gate": z(e, d, dt=F32), "dw1": z(e, f, d, dt=F32),
@@ -711,7 +893,9 @@ class MoELayer:
         """Everything of the forward but the combine: ``buf`` then holds y_perm,
         row_of_copy, topk_w and y_shared."""
         b, p = self.buf, self.p
-        self.x = x
+        self.x = None if self.checkpoint else x
+        if self.balance is not None:
+            self.balance.pop("pending", None)   # a loss of the forward before, never taken back
         if self.fused_dispatch:
             # routing and the permuted copy of the tokens in one launch (E <= 32)
             moe_route_permute(self.desc, x, p["w_gate"], p.get("bias"), b["logits"], b["topk_idx"], b["topk_w"],
@@ -747,7 +931,11 @@ class MoELayer:
 
     def _ffn(self, x, stream=None):
         b, p = self.buf, self.p
-        if self.w8:
+        if self.checkpoint:
+            moe_quantize_mxfp8(x, self.ckpt["x"], self.ckpt["x_scale"], stream)
+            moe_grouped_ffn_ckpt(self.desc, b["x_perm"], b["offsets"], x, p, self.ckpt, b["y_perm"], b["y_shared"],
+                                 self.ws, stream)
+        elif self.w8:
             saved = {key: b[key] for key in ("a1", "a3", "h", "a1s", "a3s", "hs") if b.get(key) is not None}
             moe_grouped_ffn_fp8w(self.desc, b["x_perm"], b["offsets"], x, self.w8q, saved, b["y_perm"],
                                  b["y_shared"], self.ws, stream)
@@ -782,8 +970,49 @@ class MoELayer:
         moe_grouped_ffn_fp8b(self.desc, b["xq_perm"], b["xs_perm"], b["offsets"], b["xq_tok"], b["xs_tok"], self.w8q,
                              saved, b["y_perm"], b["y_shared"], self.ws, stream)
 
+    def balance_loss(self, seq_offsets: torch.Tensor, coef: float, z_coef: float = 0.0, dloss=None,
+                     stream=None) -> torch.Tensor:
+        """The balance and z losses (fp32 [2]) of the last forward's routing over the sequences
+        ``seq_offsets`` (int32 [S + 1]); the next backward adds their gradient, times ``dloss``, to dx and
+        dw_gate.  ``balance["counts"]`` holds the copies per sequence and expert."""
+        if not self.train:
+            raise ValueError("a layer built with train=False has no backward")
+        if self.cap:
+            raise ValueError("the balance over sequences is of the dropless layer")
+        b, e = self.buf, self.cfg.n_exp
+        s = seq_offsets.shape[0] - 1
+        if self.balance is None or self.balance["counts"].shape[0] != s:
+            z = lambda *shape, dt: torch.empty(shape, dtype=dt, device=b["logits"].device)  # noqa: E731
+            self.balance = {"counts": z(s, e, dt=I32), "loss": z(2, dt=F32),
+                            "dlogits": z(self.cfg.n_tok, e, dt=F32)}
+            if self.checkpoint:
+                self.balance["x"] = z(self.cfg.n_tok, self.cfg.d_model, dt=BF16)
+        q = self.balance
+        moe_balance_loss(self.desc, b["logits"], b["topk_idx"], seq_offsets, q["counts"], q["loss"], q["dlogits"],
+                         self.ws, coef, z_coef, dloss, stream)
+        q["pending"] = True
+        return q["loss"]
+
     def backward(self, dy: torch.Tensor, stream=None) -> dict:
+        self._backward(dy, stream)
+        q, g = self.balance, self.grads
+        if q is not None and q.pop("pending", False):
+            x = self.x
+            if self.checkpoint:
+                x = q["x"]
+                moe_dequantize_mxfp8(self.ckpt["x"], self.ckpt["x_scale"], x, stream)
+            moe_router_backward(self.desc, q["dlogits"], x, self.p["w_gate"], g["dx"], g["dx"], g["dw_gate"],
+                                g["dw_gate"], self.ws, stream)
+        return g
+
+    def _backward(self, dy: torch.Tensor, stream=None) -> dict:
         b = self.buf
+        if self.checkpoint:
+            state = {key: b[key] for key in ("logits", "topk_idx", "topk_w", "offsets", "row_of_copy",
+                                             "copy_of_row")}
+            moe_backward_ckpt(self.desc, self.p["w_gate"], self.p, {**state, **self.ckpt}, dy, self.grads, self.ws,
+                              stream)
+            return self.grads
         if self.mx:
             state = {key: b[key] for key in ("logits", "topk_idx", "topk_w", "offsets", "row_of_copy",
                                              "copy_of_row", "a1", "a3", "h", "y_perm", "a1s", "a3s", "hs")}
@@ -824,13 +1053,14 @@ class MoEBlock:
     device; every training forward that drops moves the offset past the counters it used, as an
     ordinary tensor operation on the same stream, so a captured step draws anew
     at each replay.  ``backward`` uses the offset of the last forward.
+    ``checkpoint``: the layer keeps its activations in 8 bits (:class:`MoELayer`).
     """
 
     def __init__(self, cfg: MoEConfig, params: dict, gamma, beta=None, p: float = 0.0, seed: int = 0,
-                 eps: float = 1e-5, train: bool = True, stream_dtype=BF16, device="cuda"):
+                 eps: float = 1e-5, train: bool = True, stream_dtype=BF16, device="cuda", checkpoint: bool = False):
         if not 0.0 <= p < 1.0:
             raise ValueError(f"p must be in [0, 1), got {p}")
-        self.layer = MoELayer(cfg, params, train=train, device=device)
+        self.layer = MoELayer(cfg, params, train=train, device=device, checkpoint=checkpoint)
         self.desc, self.train, self.p, self.eps = self.layer.desc, train, float(p), float(eps)
         self.gamma, self.beta = gamma, beta
         n, d = cfg.n_tok, cfg.d_model

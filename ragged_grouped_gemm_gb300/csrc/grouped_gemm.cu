@@ -98,6 +98,12 @@ struct KParams {
   int64_t s_ld;
   const void* in0;
   const void* in1;
+  const void* in2;
+  const void* in3;
+  const float* row_w;
+  const int32_t* w_map;
+  float* row_dot;
+  int64_t dot_ld;
   int64_t ld_out;
   int64_t group_stride_out;
   int32_t* status;
@@ -322,6 +328,48 @@ __device__ __forceinline__ int mx_exponent_of(float amax) {
   const int ex = static_cast<int>(b >> 23);
   const int fl = ex ? ex - 127 : -149 + (31 - __clz(static_cast<int>(b)));
   return max(-127, min(127, fl - 8));
+}
+
+// 32 fp32 values of a row -> their 32 E4M3 codes and E8M0 scale byte (MXFP8,
+// the rule of mx_quant_block32 applied to the unrounded values).
+__device__ __forceinline__ uint8_t mx_encode32(const uint32_t (&lo)[16], const uint32_t (&hi)[16], uint4& c0,
+                                               uint4& c1) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(lo[j])), fabsf(__uint_as_float(hi[j]))));
+  const int e = mx_exponent_of(amax);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  uint32_t cw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t* v = i < 4 ? &lo[4 * i] : &hi[4 * (i - 4)];
+    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
+        make_float2(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
+        make_float2(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv), __NV_SATFINITE, __NV_E4M3);
+    cw[i] = static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+  }
+  c0 = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+  c1 = make_uint4(cw[4], cw[5], cw[6], cw[7]);
+  return static_cast<uint8_t>(e + 127);
+}
+
+// 2^(byte - 127), the value of an E8M0 scale (byte 0: the subnormal 2^-127).
+__device__ __forceinline__ float mx_scale_value(uint8_t b) {
+  return __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x00400000u);
+}
+
+// Four E4M3 codes (little-endian in a word) -> four fp32 values (exact).
+__device__ __forceinline__ void e4m3x4_decode(uint32_t w, float (&f)[4]) {
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * hh)), __NV_E4M3);
+    __half2 h2;
+    *reinterpret_cast<__half2_raw*>(&h2) = hr;
+    const float2 v = __half22float2(h2);
+    f[2 * hh] = v.x;
+    f[2 * hh + 1] = v.y;
+  }
 }
 
 // GATHER (ragged M, bf16, one contraction source): A rows are gathered from
@@ -975,7 +1023,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
       const bool row_ok = r < t.rows_valid;
-      if (EPI == EPI_BF16 || EPI == EPI_F32) {
+      if (EPI == EPI_BF16 || EPI == EPI_F32 || EPI == EPI_BF16_ADD) {
         int64_t grow;
         char* obase = static_cast<char*>(p.out0);
         if (!RAGGED_K) {
@@ -1205,6 +1253,22 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               } else {
                 __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(obase) + grow * p.ld_out + col;
                 uint32_t w[8];
+                if (EPI == EPI_BF16_ADD && p.in0) {
+                  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.in0) + grow * p.ld_out + col;
+                  if (nvalid == 16) {
+                    const uint4 s0 = reinterpret_cast<const uint4*>(src)[0], s1 = reinterpret_cast<const uint4*>(src)[1];
+                    const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                      v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) + bf16lo(sw[j]));
+                      v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) + bf16hi(sw[j]));
+                    }
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                      if (j < nvalid) v[j] = __float_as_uint(__uint_as_float(v[j]) + __bfloat162float(src[j]));
+                  }
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
                 if (nvalid == 16) {
@@ -1332,6 +1396,128 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
             }
           }
         }
+      } else if (EPI == EPI_SWIGLU_FWD_C) {
+        // h = silu(a1) * a3 in bf16, and a1, a3 kept in 8 bits for the backward: blocks of 32
+        // columns of one row, which one thread owns, so a block's largest value needs no exchange.
+        // The codes come from the fp32 accumulators: one rounding.  65 bytes leave a row for 16
+        // columns of h, a1 and a3 where the bf16 form writes 96.
+        const int64_t grow = t.row0 + r;
+        const int f0 = t.nt * (BN / 2);
+#pragma unroll 1
+        for (int c = hf * (BN / 4); c < (hf + 1) * (BN / 4); c += 32) {
+          uint32_t u0[16], u1[16], v0[16], v1[16];
+          tmem_ld_32x32b_x16(tb + c, u0);
+          tmem_ld_32x32b_x16(tb + c + 16, u1);
+          tmem_ld_32x32b_x16(tb + BN / 2 + c, v0);
+          tmem_ld_32x32b_x16(tb + BN / 2 + c + 16, v1);
+          tmem_wait_ld(u0);
+          reg_fence(u1);
+          reg_fence(v0);
+          reg_fence(v1);
+          const int col = f0 + c;
+          if (row_ok && col < p.n_size) {   // n_size is a multiple of 32
+            const int64_t off = grow * p.ld_out + col;
+            uint4* h = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out0) + off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* a = i < 2 ? &u0[8 * i] : &u1[8 * (i - 2)];
+              const uint32_t* b = i < 2 ? &v0[8 * i] : &v1[8 * (i - 2)];
+              uint32_t hw[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x0 = __uint_as_float(a[2 * j]), x1 = __uint_as_float(a[2 * j + 1]);
+                hw[j] = pack_bf16x2(x0 * sigmoidf_fast(x0) * __uint_as_float(b[2 * j]),
+                                    x1 * sigmoidf_fast(x1) * __uint_as_float(b[2 * j + 1]));
+              }
+              h[i] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            }
+            const int64_t so = static_cast<int64_t>(col / 32) * p.s_ld + grow;
+            uint4 c0, c1;
+            static_cast<uint8_t*>(p.out2)[so] = mx_encode32(u0, u1, c0, c1);
+            uint4* d1 = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out1) + off);
+            d1[0] = c0;
+            d1[1] = c1;
+            static_cast<uint8_t*>(p.out4)[so] = mx_encode32(v0, v1, c0, c1);
+            uint4* d3 = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out3) + off);
+            d3[0] = c0;
+            d3[1] = c1;
+          }
+        }
+      } else if (EPI == EPI_SWIGLU_BWD_C) {
+        // With a1, a3 from their 8 bits, s = sigmoid(a1), silu = a1 s and the row's weight g:
+        //   da3 = g dh silu,  da1 = g dh a3 (s + silu (1 - s)),  h = g silu a3,  dot += dh silu a3.
+        // The weight comes after the product, so dY enters it as it is and <dh, h> is the weight's
+        // own gradient.  Each thread owns a row: its sum over this tile's half of the columns
+        // leaves as one number of a slice, and the slices are added in order later.
+        const int64_t grow = t.row0 + r;
+        float g = 1.0f, dot = 0.0f;
+        if (row_ok && p.row_w) g = p.row_w[p.w_map ? p.w_map[grow] : grow];
+#pragma unroll 1
+        for (int c = hf * (BN / 2); c < (hf + 1) * (BN / 2); c += 32) {
+          uint32_t d0[16], d1[16];
+          tmem_ld_32x32b_x16(tb + c, d0);
+          tmem_ld_32x32b_x16(tb + c + 16, d1);
+          const int col = t.nt * BN + c;
+          const bool ok = row_ok && col < p.n_size;   // n_size is a multiple of 32
+          const int64_t off = grow * p.ld_out + col;
+          const int64_t so = static_cast<int64_t>(col / 32) * p.s_ld + grow;
+          uint4 ca[2], cb[2];
+          uint8_t ea = 0, eb = 0;
+          if (ok) {
+            const uint4* pa = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in0) + off);
+            const uint4* pb = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in2) + off);
+            ca[0] = pa[0];
+            ca[1] = pa[1];
+            cb[0] = pb[0];
+            cb[1] = pb[1];
+            ea = static_cast<const uint8_t*>(p.in1)[so];
+            eb = static_cast<const uint8_t*>(p.in3)[so];
+          }
+          tmem_wait_ld(d0);
+          reg_fence(d1);
+          if (ok) {
+            const float sa = mx_scale_value(ea), sb = mx_scale_value(eb);
+            const uint32_t aw[8] = {ca[0].x, ca[0].y, ca[0].z, ca[0].w, ca[1].x, ca[1].y, ca[1].z, ca[1].w};
+            const uint32_t bw[8] = {cb[0].x, cb[0].y, cb[0].z, cb[0].w, cb[1].x, cb[1].y, cb[1].z, cb[1].w};
+            uint4* q1 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out0) + off);
+            uint4* q3 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out1) + off);
+            uint4* qh = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out2) + off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {   // 8 columns a turn
+              uint32_t w1[4], w3[4], wh[4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float a1[4], a3[4], o1[4], o3[4], oh[4];
+                e4m3x4_decode(aw[2 * i + k], a1);
+                e4m3x4_decode(bw[2 * i + k], a3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int n = 8 * i + 4 * k + j;
+                  const float dh = __uint_as_float(n < 16 ? d0[n & 15] : d1[n & 15]);
+                  const float x = a1[j] * sa, y = a3[j] * sb;
+                  const float sg = sigmoidf_fast(x);
+                  const float silu = x * sg;
+                  const float hv = silu * y;
+                  const float gd = g * dh;
+                  dot = fmaf(dh, hv, dot);
+                  oh[j] = g * hv;
+                  o3[j] = gd * silu;
+                  o1[j] = gd * y * fmaf(silu, 1.0f - sg, sg);
+                }
+                w1[2 * k] = pack_bf16x2(o1[0], o1[1]);
+                w1[2 * k + 1] = pack_bf16x2(o1[2], o1[3]);
+                w3[2 * k] = pack_bf16x2(o3[0], o3[1]);
+                w3[2 * k + 1] = pack_bf16x2(o3[2], o3[3]);
+                wh[2 * k] = pack_bf16x2(oh[0], oh[1]);
+                wh[2 * k + 1] = pack_bf16x2(oh[2], oh[3]);
+              }
+              q1[i] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+              q3[i] = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+              qh[i] = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            }
+          }
+        }
+        if (p.row_dot && row_ok) p.row_dot[static_cast<int64_t>(2 * t.nt + hf) * p.dot_ld + grow] = dot;
       } else {  // EPI_SWIGLU_BWD
         const int64_t grow = t.row0 + r;
 #pragma unroll 1
@@ -1581,6 +1767,12 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   kp.s_ld = a.s_ld;
   kp.in0 = a.in0;
   kp.in1 = a.in1;
+  kp.in2 = a.in2;
+  kp.in3 = a.in3;
+  kp.row_w = a.row_w;
+  kp.w_map = a.w_map;
+  kp.row_dot = a.row_dot;
+  kp.dot_ld = a.dot_ld;
   kp.ld_out = a.ld_out;
   kp.group_stride_out = a.group_stride_out;
   kp.status = a.status;
@@ -1759,9 +1951,10 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
                 : launch_impl<256, false, false, EPI_BF16, false, false, false, true>(kp, u, stream);
   }
   // CTA pairs: each CTA loads its own 128 rows of A and half of the B tile
-  const bool pair = BN == 256 && use_cta_pair(a.max_rows, a.num_groups) &&
+  const bool pair = BN == 256 && !a.one_sm && use_cta_pair(a.max_rows, a.num_groups) &&
                     (a.ragged_k ? a.epi == EPI_F32
-                                : (a.epi == EPI_BF16 || a.epi == EPI_SWIGLU_FWD || a.epi == EPI_SWIGLU_BWD));
+                                : (a.epi == EPI_BF16 || a.epi == EPI_SWIGLU_FWD || a.epi == EPI_SWIGLU_BWD ||
+                                   a.epi == EPI_SWIGLU_FWD_C || a.epi == EPI_SWIGLU_BWD_C));
   kp.kblk = BK;
   if (!a.ragged_k) {
     if (a.max_rows <= 0) return cudaSuccess;
@@ -1841,6 +2034,9 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
       case EPI_SWIGLU_FWD:
         return pair ? launch_impl<256, false, false, EPI_SWIGLU_FWD, false, true>(kp, u, stream)
                     : launch_impl<256, false, false, EPI_SWIGLU_FWD>(kp, u, stream);
+      case EPI_SWIGLU_FWD_C:
+        return pair ? launch_impl<256, false, false, EPI_SWIGLU_FWD_C, false, true>(kp, u, stream)
+                    : launch_impl<256, false, false, EPI_SWIGLU_FWD_C>(kp, u, stream);
       default: return cudaErrorInvalidValue;
     }
   }
@@ -1852,6 +2048,10 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
       case EPI_SWIGLU_BWD:
         return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD, false, true>(kp, u, stream)
                     : launch_impl<256, false, true, EPI_SWIGLU_BWD>(kp, u, stream);
+      case EPI_SWIGLU_BWD_C:
+        return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD_C, false, true>(kp, u, stream)
+                    : launch_impl<256, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream);
+      case EPI_BF16_ADD: return launch_impl<256, false, true, EPI_BF16_ADD>(kp, u, stream);
       default: return cudaErrorInvalidValue;
     }
   }

@@ -24,7 +24,15 @@ enum EpiKind : int {
   EPI_SWIGLU_BWD = 3,  // acc = dh; in0 = a1, in1 = a3 -> out0 = da1, out1 = da3 (bf16)
   EPI_SWIGLU_FWD_Q = 4,  // acc = [a1 | a3] -> h quantised to MXFP8 along F: out0 = codes [rows, n],
                          // out1 = scales [n/32, s_ld]; optional bf16 out2 = h, out3 = a1, out4 = a3
+  EPI_SWIGLU_FWD_C = 5,  // acc = [a1 | a3] -> out0 = h (bf16); a1 and a3 kept as MXFP8 along F: out1, out3 = codes
+                         // [rows, n], out2, out4 = their scales [n/32, s_ld]
+  EPI_SWIGLU_BWD_C = 6,  // acc = dh; in0, in2 = kept codes of a1, a3, in1, in3 = their scales [n/32, s_ld], g = row
+                         // weight -> out0 = da1, out1 = da3, out2 = g h (bf16), row_dot = partial sums of dh h
+  EPI_BF16_ADD = 7,      // out0[row, col] = bf16(acc + in0[row, col])  (in0 null: zero)
 };
+
+// Column slices of GemmArgs::row_dot: two per 256-column tile.
+inline int64_t gemm_row_dot_slices(int64_t n) { return 2 * ((n + 255) / 256); }
 
 // MXFP8 operand: E4M3 codes [groups][rows, cols] and E8M0 scales
 // [groups][cols/32, scale_ld] (see mxfp8.cuh), cols = contraction dimension.
@@ -55,6 +63,7 @@ struct GemmArgs {
   bool b_mn = false;          // B stored MN-major (data gradients)
   bool ragged_k = false;      // contraction over the group's rows
   int block_n = 256;          // 256, or 32 for narrow N (router logits)
+  bool one_sm = false;        // bf16: no CTA pairs (weight gradients of few output rows)
   int ksplit = 1;             // one group, fp32 out: the contraction in ksplit slices, out0 =
                               // [ksplit][rows][ld_out] partial products (summed by the caller)
   EpiKind epi = EPI_BF16;
@@ -76,9 +85,17 @@ struct GemmArgs {
   void* out2 = nullptr;
   void* out3 = nullptr;
   void* out4 = nullptr;
-  int64_t s_ld = 0;           // EPI_SWIGLU_FWD_Q: leading dimension of the h scales
+  int64_t s_ld = 0;           // EPI_SWIGLU_FWD_Q, _FWD_C, _BWD_C: leading dimension of the scales
   const void* in0 = nullptr;
   const void* in1 = nullptr;
+  const void* in2 = nullptr;
+  const void* in3 = nullptr;
+  // EPI_SWIGLU_BWD_C: weight of row r is row_w[w_map ? w_map[r] : r] (null: 1); row_dot (nullable)
+  // [gemm_row_dot_slices(n_size)][dot_ld] receives every row's sum of dh * silu(a1) * a3 over each slice
+  const float* row_w = nullptr;
+  const int32_t* w_map = nullptr;
+  float* row_dot = nullptr;
+  int64_t dot_ld = 0;
   int64_t ld_out = 0;
   int64_t group_stride_out = 0;
   int32_t* status = nullptr;  // device status words

@@ -10,10 +10,12 @@
 
 #include "balance.cuh"
 #include "block.cuh"
+#include "ckpt.cuh"
 #include "fp8_block.cuh"
 #include "grouped_gemm.cuh"
 #include "moe_kernels.cuh"
 #include "mxfp8.cuh"
+#include "seq_balance.cuh"
 #include "timing.cuh"
 
 #include <nvtx3/nvToolsExt.h>
@@ -33,6 +35,8 @@ constexpr int kRouterAccWord = 16;
 // words 48..50: the single-pass permute's chunk ticket, done counter and
 // generation (it leaves the first two zero and advances the third)
 constexpr int kPermuteCtlWord = 48;
+// word 52: the balance loss's block counter (left zero)
+constexpr int kBalanceTicketWord = 52;
 // Look-back words of the single-pass permute (1 MiB): ceil(N/16) * E of them
 // per call; larger problems take the two-kernel permute.
 constexpr size_t kLookWords = 131072;
@@ -58,7 +62,19 @@ struct WsLayout {
   size_t t_d0 = 0, t_d0s = 0, t_d1 = 0, t_d1s = 0, t_f0 = 0, t_f0s = 0, t_f1 = 0, t_f1s = 0;
   int64_t rp = 0;   // leading dimension of the transposed code matrices
   size_t norm = 0;  // partial sums of the layer norm's weight gradients (over others' scratch)
+  size_t rterms = 0, rend = 0;  // the dense router gradient's terms and partial products (over others' scratch)
 };
+
+// Bytes of the dense router gradient's scratch with `slices` runs of tokens: the bf16 terms of
+// dlogits, {0, N} and the runs' starts, the partial weight gradients.
+size_t router_terms_bytes(const moe_desc_t& d) {
+  return align_up(static_cast<size_t>(d.n_tok) * 3 * moe::router_term_cols(d.n_exp) * 2);
+}
+constexpr int kRouterSlices = 16;
+size_t router_bytes(const moe_desc_t& d, int slices) {
+  return router_terms_bytes(d) + kAlign +
+         align_up(static_cast<size_t>(slices) * 3 * moe::router_term_cols(d.n_exp) * d.d_model * 4);
+}
 
 int64_t ld16(int64_t v) { return (v + 15) / 16 * 16; }
 
@@ -142,6 +158,33 @@ WsLayout layout(const moe_desc_t& d) {
   const size_t norm = align_up(moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
   L.norm = norm <= L.gmaps - L.dl ? L.dl : o;
   if (L.norm == o) o += norm;
+  // the dense router gradient too, over the same scratch where one run of tokens fits
+  const size_t router = router_bytes(d, 1);
+  const bool over = router <= L.gmaps - L.dl;
+  L.rterms = over ? L.dl : o;
+  if (!over) o += router;
+  L.rend = over ? L.gmaps : o;
+  L.total = o;
+  return L;
+}
+
+// The workspace of a layer with 8-bit checkpoints: the layer's own, then what the forward and
+// the backward hold in passing (h of either, the decoded x, partial sums of the gate gradient).
+struct CkptLayout {
+  WsLayout base;
+  size_t h = 0, hs = 0, xp = 0, xt = 0, dot = 0, dgr = 0, total = 0;
+};
+CkptLayout ckpt_layout(const moe_desc_t& d) {
+  CkptLayout L;
+  L.base = layout(d);
+  const size_t N = d.n_tok, D = d.d_model, F = d.d_ff, R = N * d.top_k, Fs = d.n_shared ? d.d_ff_shared : 0;
+  size_t o = align_up(L.base.total);
+  L.h = o; o = align_up(o + R * F * 2);
+  L.hs = o; o = align_up(o + N * Fs * 2);
+  L.xp = o; o = align_up(o + R * D * 2);
+  L.xt = o; o = align_up(o + (Fs ? N * D * 2 : 0));
+  L.dot = o; o = align_up(o + static_cast<size_t>(moe::gemm_row_dot_slices(d.d_ff)) * R * 4);
+  L.dgr = o; o = align_up(o + R * 4);
   L.total = o;
   return L;
 }
@@ -236,16 +279,23 @@ Operand wstack(const void* p, int64_t groups, int64_t rows, int64_t cols) {
   return o;
 }
 
+// a1 and a3 of one expert set kept as MXFP8 rows: codes, scales and the scales' leading dimension.
+struct KeptRows {
+  const void *a1, *a1s, *a3, *a3s;
+  int64_t ld;
+};
+
 // SwiGLU FFN of one "expert set": GEMM1 (fused w1|w3 with SwiGLU epilogue)
 // then GEMM2, over `groups` ragged row groups of `a_in` [rows, D].
 // (w8: w1, w3, w2 are E4M3 codes with fp32 tile scales s1, s3, s2)
 // (gather: GEMM1's row r is row gather[r] / gather_k of a_in [n_src, D], read
 // by TMA gathers instead of a permuted copy)
+// (kept: GEMM1 keeps a1 and a3 in 8 bits, and a1, a3 are not used)
 moe_status_t ffn_pair(const void* a_in, int64_t rows, int D, int F, int groups, const int32_t* offsets,
                       const void* w1, const void* w3, const void* w2, void* h, void* a1, void* a3, void* y,
                       int32_t* status, cudaStream_t st, const float* s1 = nullptr, const float* s3 = nullptr,
                       const float* s2 = nullptr, const int32_t* gather = nullptr, int gather_k = 0,
-                      int64_t n_src = 0) {
+                      int64_t n_src = 0, const KeptRows* kept = nullptr) {
   const bool w8 = s1 != nullptr;
   GemmArgs g1;
   g1.w8 = w8;
@@ -266,6 +316,14 @@ moe_status_t ffn_pair(const void* a_in, int64_t rows, int D, int F, int groups, 
   g1.out0 = h;
   g1.out1 = a1;
   g1.out2 = a3;
+  if (kept) {
+    g1.epi = moe::EPI_SWIGLU_FWD_C;
+    g1.out1 = const_cast<void*>(kept->a1);
+    g1.out2 = const_cast<void*>(kept->a1s);
+    g1.out3 = const_cast<void*>(kept->a3);
+    g1.out4 = const_cast<void*>(kept->a3s);
+    g1.s_ld = kept->ld;
+  }
   g1.ld_out = F;
   g1.status = status;
   MOE_CUDA(gemm(moe::TIMING_FFN_FWD, g1, st));
@@ -349,6 +407,29 @@ moe_status_t ffn_pair_fp8(const void* aq, const void* as, int64_t rows, int D, i
   return MOE_OK;
 }
 
+// The first product of the backward from kept rows: dY as it is, the row weights in the
+// epilogue, h (with the weight) formed again, and the weights' gradient in slices.
+struct KeptBackward {
+  KeptRows rows;
+  void* h;                // [rows, F] bf16, written here and read by dW2
+  const float* row_w;     // weight of row r: row_w[w_map ? w_map[r] : r]; null: 1
+  const int32_t* w_map;
+  float* dot;             // [gemm_row_dot_slices(F)][rows], nullable
+};
+void kept_dgrad(GemmArgs& g, const KeptBackward& k, int64_t rows) {
+  g.epi = moe::EPI_SWIGLU_BWD_C;
+  g.in0 = k.rows.a1;
+  g.in1 = k.rows.a1s;
+  g.in2 = k.rows.a3;
+  g.in3 = k.rows.a3s;
+  g.s_ld = k.rows.ld;
+  g.out2 = k.h;
+  g.row_w = k.row_w;
+  g.w_map = k.w_map;
+  g.row_dot = k.dot;
+  g.dot_ld = rows;
+}
+
 // Backward of one expert set: dgrad through w2 with the SwiGLU derivative,
 // weight gradient of w2, dgrad through w1|w3, weight gradients of w1, w3.
 moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, const void* a3, const void* h,
@@ -356,7 +437,7 @@ moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, con
                           const void* w3, const void* w2, void* da1, void* da3, void* dx_rows, float* dw1,
                           float* dw3, float* dw2, int32_t* status, cudaStream_t st, void* map_ws,
                           const float* s1 = nullptr, const float* s3 = nullptr, const float* s2 = nullptr,
-                          const Fp8Scratch* f8 = nullptr) {
+                          const Fp8Scratch* f8 = nullptr, const KeptBackward* kept = nullptr) {
   // FP8 weights (w8) or FP8 operands (f8) in the data gradients; weight gradients stay bf16
   const bool w8 = s1 != nullptr && !f8;
   GemmArgs g;
@@ -377,6 +458,10 @@ moe_status_t ffn_pair_bwd(const void* dyw, const void* a_in, const void* a1, con
   g.out1 = da3;
   g.ld_out = F;
   g.status = status;
+  if (kept) {
+    kept_dgrad(g, *kept, rows);
+    h = kept->h;
+  }
   if (f8) {
     MOE_CUDA(moe::launch_fp8_quant_rows(dyw, rows, D, f8->dy, f8->dys, moe::fp8_scale_ld(D), st));
     moe::Fp8GemmArgs q;
@@ -743,6 +828,22 @@ moe_status_t moe_combine(const moe_desc_t* d, const void* y_perm, const int32_t*
 }  // extern "C"
 
 namespace {
+// The gradients of a layer without tokens.
+moe_status_t zero_weight_grads(const moe_desc_t& d, const moe_grads_t& g, cudaStream_t st) {
+  const size_t D = d.d_model, F = d.d_ff, E = d.n_exp;
+  MOE_CUDA(cudaMemsetAsync(g.dw_gate, 0, sizeof(float) * E * D, st));
+  MOE_CUDA(cudaMemsetAsync(g.dw1, 0, sizeof(float) * E * F * D, st));
+  MOE_CUDA(cudaMemsetAsync(g.dw3, 0, sizeof(float) * E * F * D, st));
+  MOE_CUDA(cudaMemsetAsync(g.dw2, 0, sizeof(float) * E * F * D, st));
+  if (d.n_shared) {
+    const size_t fs = d.d_ff_shared;
+    MOE_CUDA(cudaMemsetAsync(g.dws1, 0, sizeof(float) * fs * D, st));
+    MOE_CUDA(cudaMemsetAsync(g.dws3, 0, sizeof(float) * fs * D, st));
+    MOE_CUDA(cudaMemsetAsync(g.dws2, 0, sizeof(float) * fs * D, st));
+  }
+  return MOE_OK;
+}
+
 // The layer backward (moe_backward); with FP8 weights (q non-NULL) the data
 // gradients read the E4M3 weight codes w1, w3, w2 with their tile scales.
 moe_status_t backward_impl(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_t* w,
@@ -761,19 +862,7 @@ moe_status_t backward_impl(const moe_desc_t* d, const void* w_gate, const moe_ex
   const WsLayout L = layout(*d);
   const int N = d->n_tok, D = d->d_model, F = d->d_ff, E = d->n_exp, K = d->top_k;
   const int64_t R = static_cast<int64_t>(N) * K;
-  if (N == 0) {
-    MOE_CUDA(cudaMemsetAsync(g->dw_gate, 0, sizeof(float) * E * D, st));
-    MOE_CUDA(cudaMemsetAsync(g->dw1, 0, sizeof(float) * E * F * D, st));
-    MOE_CUDA(cudaMemsetAsync(g->dw3, 0, sizeof(float) * E * F * D, st));
-    MOE_CUDA(cudaMemsetAsync(g->dw2, 0, sizeof(float) * E * F * D, st));
-    if (d->n_shared) {
-      const size_t fs = d->d_ff_shared;
-      MOE_CUDA(cudaMemsetAsync(g->dws1, 0, sizeof(float) * fs * D, st));
-      MOE_CUDA(cudaMemsetAsync(g->dws3, 0, sizeof(float) * fs * D, st));
-      MOE_CUDA(cudaMemsetAsync(g->dws2, 0, sizeof(float) * fs * D, st));
-    }
-    return MOE_OK;
-  }
+  if (N == 0) return zero_weight_grads(*d, *g, st);
   int32_t* status = at<int32_t>(ws, L.status);
   float* dl = g->dlogits ? g->dlogits : at<float>(ws, L.dl);
   float* dg = g->dg ? g->dg : at<float>(ws, L.dg);
@@ -1240,6 +1329,334 @@ moe_status_t moe_update_bias(const moe_desc_t* d, const int32_t* counts, float* 
   if (!counts || !bias || (mode != 0 && mode != 1)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       moe::launch_update_bias(counts, d->n_exp, bias, gamma, mode, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- balance over sequences
+moe_status_t moe_balance_loss(const moe_desc_t* d, const float* logits, const int32_t* topk_idx,
+                              const int32_t* seq_offsets, int64_t n_seq, float coef, float z_coef,
+                              const float* dloss, int32_t* counts, float* loss, float* dlogits, void* ws,
+                              size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_balance_loss");
+  MOE_TRY(check_desc(d));
+  MOE_TRY(check_ws(*d, ws, ws_bytes, false));
+  if (n_seq < 1 || n_seq > (int64_t{1} << 24) || !std::isfinite(coef) || !std::isfinite(z_coef))
+    return MOE_ERR_INVALID_ARG;
+  if (!all4({counts, loss})) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok > 0 && (!all4({logits, topk_idx, seq_offsets}) || !aligned4(dloss) || !aligned4(dlogits)))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->n_tok == 0) {   // empty arrays have no address
+    MOE_CUDA(cudaMemsetAsync(counts, 0, sizeof(int32_t) * n_seq * d->n_exp, st));
+    return cuda_status(cudaMemsetAsync(loss, 0, 2 * sizeof(float), st));
+  }
+  const WsLayout L = layout(*d);
+  moe::SeqBalanceArgs a;
+  a.n_tok = d->n_tok;
+  a.n_exp = d->n_exp;
+  a.top_k = d->top_k;
+  a.gate = d->gate;
+  a.n_seq = static_cast<int>(n_seq);
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.seq_offsets = seq_offsets;
+  a.coef = coef;
+  a.z_coef = z_coef;
+  a.dloss = dloss;
+  a.counts = counts;
+  a.loss = loss;
+  a.dlogits = dlogits;
+  a.part = at<double>(ws, L.gpart);   // at most N pairs; the region holds 16 N E bytes
+  a.head = at<int32_t>(ws, L.aux);
+  a.status = at<int32_t>(ws, L.status);
+  a.ticket = a.status + kBalanceTicketWord;
+  return cuda_status(moe::launch_seq_balance(a, st));
+}
+
+moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, const void* x, const void* w_gate,
+                                 const void* dx_in, void* dx, const float* dw_in, float* dw_gate, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_router_backward");
+  MOE_TRY(check_desc(d));
+  MOE_TRY(check_ws(*d, ws, ws_bytes, true));
+  if (!all16({w_gate, dw_gate}) || !aligned16(dw_in)) return MOE_ERR_INVALID_ARG;
+  if (d->n_tok > 0 && (!all16({dlogits, x, dx}) || !aligned16(dx_in))) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int N = d->n_tok, D = d->d_model, E = d->n_exp;
+  if (N == 0) {
+    if (!dw_in) return cuda_status(cudaMemsetAsync(dw_gate, 0, sizeof(float) * E * D, st));
+    if (dw_in != dw_gate)
+      MOE_CUDA(cudaMemcpyAsync(dw_gate, dw_in, sizeof(float) * E * D, cudaMemcpyDeviceToDevice, st));
+    return MOE_OK;
+  }
+  const WsLayout L = layout(*d);
+  const int e8 = moe::router_term_cols(E), m = 3 * e8;
+  // The weight gradient contracts over the tokens: their runs are the groups of one ragged
+  // product, as many as fill the SMs and the scratch holds, 256 tokens at least.
+  const int64_t tiles = static_cast<int64_t>((m + 127) / 128) * ((D + 255) / 256);
+  int slices = static_cast<int>(std::min<int64_t>(
+      {kRouterSlices, std::max<int64_t>(1, 2 * moe::num_sms() / tiles), (static_cast<int64_t>(N) + 255) / 256}));
+  while (slices > 1 && router_bytes(*d, slices) > L.rend - L.rterms) --slices;
+  const int per = static_cast<int>(((static_cast<int64_t>(N) + slices - 1) / slices + 63) / 64 * 64);
+  slices = (N + per - 1) / per;
+  char* terms = at<char>(ws, L.rterms);
+  int32_t* dense = reinterpret_cast<int32_t*>(terms + router_terms_bytes(*d));
+  int32_t* starts = dense + 4;
+  float* part = reinterpret_cast<float*>(terms + router_terms_bytes(*d) + kAlign);
+  int32_t* status = at<int32_t>(ws, L.status);
+  MOE_CUDA(moe::launch_router_terms(dlogits, N, E, terms, dense, starts, slices, per, st));
+  GemmArgs w;
+  w.epi = moe::EPI_F32;
+  w.a_mn = w.b_mn = w.ragged_k = true;
+  w.one_sm = true;
+  w.map_ws = map_scratch(ws, L);
+  w.offsets = starts;
+  w.num_groups = slices;
+  w.max_rows = N;
+  w.status = status;
+  w.a[0] = act(terms, N, m);
+  w.b[0] = act(x, N, D);
+  w.m_size = m;
+  w.n_size = D;
+  w.out0 = part;
+  w.ld_out = D;
+  w.group_stride_out = static_cast<int64_t>(m) * D;
+  MOE_CUDA(gemm(moe::TIMING_WGRAD, w, st));
+  MOE_CUDA(moe::launch_router_dw(part, slices, E, D, dw_in, dw_gate, st));
+  // dx: the first two terms against W_g, one contraction source each
+  GemmArgs g;
+  g.epi = moe::EPI_BF16_ADD;
+  g.b_mn = true;
+  for (int i = 0; i < 2; ++i) {
+    g.a[i] = act(terms + static_cast<size_t>(i) * e8 * 2, N, e8);
+    g.a[i].ld = m;
+    g.b[i] = wstack(w_gate, 1, E, D);
+  }
+  g.k0 = g.k1 = e8;
+  g.offsets = dense;
+  g.num_groups = 1;
+  g.max_rows = N;
+  g.n_size = D;
+  g.in0 = dx_in;
+  g.out0 = dx;
+  g.ld_out = D;
+  g.status = status;
+  return cuda_status(gemm(moe::TIMING_DGRAD, g, st));
+}
+
+// ------------------------------------------------- 8-bit activation checkpoints
+moe_status_t moe_ckpt_workspace_size(const moe_desc_t* d, size_t* bytes) {
+  MOE_TRY(check_desc(d));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (d->precision != 0) return MOE_ERR_UNSUPPORTED;
+  *bytes = ckpt_layout(*d).total;
+  return MOE_OK;
+}
+
+static moe_status_t check_ckpt(const moe_desc_t* d, const void* ws, size_t ws_bytes) {
+  MOE_TRY(check_desc(d));
+  if (d->precision != 0) return MOE_ERR_UNSUPPORTED;
+  if (!ws || !aligned16(ws) || ws_bytes < ckpt_layout(*d).total) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_ffn_ckpt(const moe_desc_t* d, const void* x_perm, const int32_t* offsets, const void* x,
+                                  const moe_expert_weights_t* w, const moe_ckpt_t* kept, void* y_perm, void* y_shared,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_grouped_ffn_ckpt");
+  MOE_TRY(check_ckpt(d, ws, ws_bytes));
+  if (d->n_tok == 0) return MOE_OK;
+  if (!w || !kept || !all16({x_perm, w->w1, w->w3, w->w2, kept->a1, kept->a1_scale, kept->a3, kept->a3_scale, y_perm}) ||
+      !all4({offsets}))
+    return MOE_ERR_INVALID_ARG;
+  if (d->n_shared && !all16({x, w->ws1, w->ws3, w->ws2, kept->a1s, kept->a1s_scale, kept->a3s, kept->a3s_scale,
+                             y_shared}))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const CkptLayout L = ckpt_layout(*d);
+  int32_t* status = at<int32_t>(ws, L.base.status);
+  const int64_t R = static_cast<int64_t>(d->n_tok) * d->top_k;
+  const KeptRows rows{kept->a1, kept->a1_scale, kept->a3, kept->a3_scale, moe::mx_scale_ld(R)};
+  MOE_TRY(ffn_pair(x_perm, R, d->d_model, d->d_ff, d->n_exp, offsets, w->w1, w->w3, w->w2, at<void>(ws, L.h), nullptr,
+                   nullptr, y_perm, status, st, nullptr, nullptr, nullptr, nullptr, 0, 0, &rows));
+  if (d->n_shared) {
+    int32_t* dense = at<int32_t>(ws, L.base.dense_off);
+    MOE_CUDA(moe::launch_dense_offsets(dense, d->n_tok, st));
+    const KeptRows srows{kept->a1s, kept->a1s_scale, kept->a3s, kept->a3s_scale, moe::mx_scale_ld(d->n_tok)};
+    MOE_TRY(ffn_pair(x, d->n_tok, d->d_model, d->d_ff_shared, 1, dense, w->ws1, w->ws3, w->ws2, at<void>(ws, L.hs),
+                     nullptr, nullptr, y_shared, status, st, nullptr, nullptr, nullptr, nullptr, 0, 0, &srows));
+  }
+  return MOE_OK;
+}
+
+moe_status_t moe_backward_ckpt(const moe_desc_t* d, const void* w_gate, const moe_expert_weights_t* w,
+                               const moe_ckpt_state_t* s, const void* dy, const moe_grads_t* g, void* ws,
+                               size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_backward_ckpt");
+  MOE_TRY(check_ckpt(d, ws, ws_bytes));
+  if (!w || !s || !g) return MOE_ERR_INVALID_ARG;
+  const moe_ckpt_t& k = s->kept;
+  if (!all16({g->dw_gate, g->dw1, g->dw3, g->dw2}) || (d->n_shared && !all16({g->dws1, g->dws3, g->dws2})))
+    return MOE_ERR_INVALID_ARG;
+  if (d->n_tok == 0) return zero_weight_grads(*d, *g, static_cast<cudaStream_t>(stream));
+  if (!all16({w_gate, w->w1, w->w3, w->w2, s->x, s->x_scale, k.a1, k.a1_scale, k.a3, k.a3_scale, dy, g->dx}))
+    return MOE_ERR_INVALID_ARG;
+  if (!all4({s->logits, s->topk_idx, s->topk_w, s->offsets, s->row_of_copy, s->copy_of_row}) || !aligned4(g->dg) ||
+      !aligned4(g->dlogits))
+    return MOE_ERR_INVALID_ARG;
+  if (d->n_shared && !all16({w->ws1, w->ws3, w->ws2, k.a1s, k.a1s_scale, k.a3s, k.a3s_scale}))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const CkptLayout C = ckpt_layout(*d);
+  const WsLayout& L = C.base;
+  const int N = d->n_tok, D = d->d_model, F = d->d_ff, E = d->n_exp, K = d->top_k;
+  const int64_t R = static_cast<int64_t>(N) * K;
+  int32_t* status = at<int32_t>(ws, L.status);
+  float* dl = g->dlogits ? g->dlogits : at<float>(ws, L.dl);
+  float* dg = g->dg ? g->dg : at<float>(ws, L.dg);
+  void* rows = at<void>(ws, L.dyw);   // dY per row, then dx per row
+  void* xp = at<void>(ws, C.xp);
+  MOE_CUDA(moe::launch_permute_rows(N, D, K, dy, s->row_of_copy, rows, st));
+  MOE_CUDA(moe::launch_mx_dequant_rows(static_cast<const uint8_t*>(s->x), static_cast<const uint8_t*>(s->x_scale), N, D,
+                                       moe::mx_scale_ld(N), s->copy_of_row, K, R, xp, status, st));
+  KeptBackward kb{{k.a1, k.a1_scale, k.a3, k.a3_scale, moe::mx_scale_ld(R)}, at<void>(ws, C.h), s->topk_w,
+                  s->copy_of_row, at<float>(ws, C.dot)};
+  MOE_TRY(ffn_pair_bwd(rows, xp, nullptr, nullptr, nullptr, R, D, F, E, s->offsets, w->w1, w->w3, w->w2,
+                       at<void>(ws, L.da1), at<void>(ws, L.da3), rows, g->dw1, g->dw3, g->dw2, status, st,
+                       map_scratch(ws, L), nullptr, nullptr, nullptr, nullptr, &kb));
+  float* dgr = at<float>(ws, C.dgr);
+  MOE_CUDA(moe::launch_row_dot_sum(kb.dot, moe::gemm_row_dot_slices(F), R, s->offsets, E, R, dgr, st));
+  MOE_CUDA(moe::launch_gate_bwd(N, K, d->gate, dgr, s->row_of_copy, s->topk_w, s->logits, E, s->topk_idx, dg, dl, st));
+  void* dxs = nullptr;
+  if (d->n_shared) {
+    int32_t* dense = at<int32_t>(ws, L.dense_off);
+    MOE_CUDA(moe::launch_dense_offsets(dense, N, st));
+    dxs = at<void>(ws, L.dxs);
+    void* xt = at<void>(ws, C.xt);
+    MOE_CUDA(moe::launch_mx_dequant_rows(static_cast<const uint8_t*>(s->x), static_cast<const uint8_t*>(s->x_scale), N,
+                                         D, moe::mx_scale_ld(N), nullptr, 1, N, xt, status, st));
+    KeptBackward ks{{k.a1s, k.a1s_scale, k.a3s, k.a3s_scale, moe::mx_scale_ld(N)}, at<void>(ws, C.hs), nullptr, nullptr,
+                    nullptr};
+    MOE_TRY(ffn_pair_bwd(dy, xt, nullptr, nullptr, nullptr, N, D, d->d_ff_shared, 1, dense, w->ws1, w->ws3, w->ws2,
+                         at<void>(ws, L.da1s), at<void>(ws, L.da3s), dxs, g->dws1, g->dws3, g->dws2, status, st,
+                         map_scratch(ws, L), nullptr, nullptr, nullptr, nullptr, &ks));
+  }
+  MOE_CUDA(moe::launch_dwgate(N, K, E, D, s->offsets, s->copy_of_row, dl, xp, 0, at<float>(ws, L.dwg), g->dw_gate, st));
+  MOE_CUDA(moe::launch_unpermute_dx(N, D, K, rows, s->row_of_copy, dl, s->topk_idx, w_gate, dxs, g->dx, st));
+  return MOE_OK;
+}
+
+// Sizes of a product on kept rows outside the layer: a and b are its two matrix sizes.
+static bool ckpt_sizes_ok(int64_t n_groups, int64_t rows, int64_t a, int64_t b) {
+  return n_groups >= 1 && n_groups <= 1024 && rows >= 0 && rows < (int64_t{1} << 31) - 256 && a > 0 && a % 64 == 0 &&
+         a <= (int64_t{1} << 24) && b > 0 && b % 64 == 0 && b <= (int64_t{1} << 24);
+}
+
+moe_status_t moe_swiglu_backward_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t d, int64_t f,
+                                                     size_t* bytes) {
+  if (!bytes || !ckpt_sizes_ok(n_groups, rows, d, f)) return MOE_ERR_INVALID_ARG;
+  *bytes = kAlign + align_up((n_groups + 1) * 4) + align_up(static_cast<size_t>(moe::gemm_row_dot_slices(f)) * rows * 4);
+  return MOE_OK;
+}
+
+moe_status_t moe_swiglu_backward_ckpt(int64_t n_groups, int64_t rows, int64_t d, int64_t f, const void* dy,
+                                      const int32_t* offsets, const void* w2, const float* row_w, const void* a1,
+                                      const void* a1_scale, const void* a3, const void* a3_scale, int64_t scale_ld,
+                                      void* da1, void* da3, void* h, float* dg, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  MOE_RANGE("moe_swiglu_backward_ckpt");
+  size_t need = 0;
+  MOE_TRY(moe_swiglu_backward_ckpt_workspace_size(n_groups, rows, d, f, &need));
+  if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (scale_ld < rows || scale_ld % 16) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!all16({dy, w2, a1, a1_scale, a3, a3_scale, da1, da3, h}) || !all4({offsets}) || !aligned4(row_w) ||
+      !aligned4(dg))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t* status = static_cast<int32_t*>(ws);
+  int32_t* off = at<int32_t>(ws, kAlign);
+  const int groups = static_cast<int>(n_groups);
+  MOE_CUDA(moe::launch_check_offsets(offsets, groups, rows, off, status, st));
+  GemmArgs g;
+  g.b_mn = true;
+  g.a[0] = act(dy, rows, d);
+  g.b[0] = wstack(w2, groups, d, f);
+  g.k0 = static_cast<int>(d);
+  g.offsets = off;
+  g.num_groups = groups;
+  g.max_rows = rows;
+  g.n_size = static_cast<int>(f);
+  g.out0 = da1;
+  g.out1 = da3;
+  g.ld_out = f;
+  g.status = status;
+  float* dot = dg ? at<float>(ws, kAlign + align_up((n_groups + 1) * 4)) : nullptr;
+  kept_dgrad(g, KeptBackward{{a1, a1_scale, a3, a3_scale, scale_ld}, h, row_w, nullptr, dot}, rows);
+  MOE_CUDA(gemm(moe::TIMING_DGRAD, g, st));
+  if (!dg) return MOE_OK;
+  return cuda_status(moe::launch_row_dot_sum(dot, moe::gemm_row_dot_slices(f), rows, off, groups, rows, dg, st));
+}
+
+moe_status_t moe_grouped_wgrad_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t m, int64_t k,
+                                                   size_t* bytes) {
+  if (!bytes || !ckpt_sizes_ok(n_groups, rows, m, k)) return MOE_ERR_INVALID_ARG;
+  *bytes = kAlign + align_up((n_groups + 1) * 4) + align_up(moe::kGemmMapScratchBytes + 128) +
+           align_up(static_cast<size_t>(rows) * k * 2);
+  return MOE_OK;
+}
+
+moe_status_t moe_grouped_wgrad_ckpt(int64_t n_groups, int64_t rows, int64_t m, int64_t k, const void* dy,
+                                    const void* x, const void* x_scale, int64_t x_rows, int64_t scale_ld,
+                                    const int32_t* row_map, int32_t row_div, const int32_t* offsets, float* dw,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  MOE_RANGE("moe_grouped_wgrad_ckpt");
+  size_t need = 0;
+  MOE_TRY(moe_grouped_wgrad_ckpt_workspace_size(n_groups, rows, m, k, &need));
+  if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (x_rows < 0 || x_rows >= (int64_t{1} << 31) || scale_ld < x_rows || scale_ld % 16 || row_div < 1 ||
+      (!row_map && (x_rows != rows || row_div != 1)))
+    return MOE_ERR_INVALID_ARG;
+  if (!all16({dw}) || !all4({offsets}) || !aligned4(row_map)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, sizeof(float) * n_groups * m * k, st));
+  if (!all16({dy}) || (x_rows > 0 && !all16({x, x_scale}))) return MOE_ERR_INVALID_ARG;
+  int32_t* status = static_cast<int32_t*>(ws);
+  int32_t* off = at<int32_t>(ws, kAlign);
+  const size_t maps = kAlign + align_up((n_groups + 1) * 4);
+  void* xp = at<void>(ws, maps + align_up(moe::kGemmMapScratchBytes + 128));
+  const int groups = static_cast<int>(n_groups);
+  MOE_CUDA(moe::launch_check_offsets(offsets, groups, rows, off, status, st));
+  MOE_CUDA(moe::launch_mx_dequant_rows(static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(x_scale), x_rows,
+                                       static_cast<int>(k), scale_ld, row_map, row_div, rows, xp, status, st));
+  GemmArgs w;
+  w.epi = moe::EPI_F32;
+  w.a_mn = w.b_mn = w.ragged_k = true;
+  w.map_ws = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(at<char>(ws, maps)) + 127) & ~uintptr_t(127));
+  w.offsets = off;
+  w.num_groups = groups;
+  w.max_rows = rows;
+  w.status = status;
+  w.a[0] = act(dy, rows, m);
+  w.b[0] = act(xp, rows, k);
+  w.m_size = static_cast<int>(m);
+  w.n_size = static_cast<int>(k);
+  w.out0 = dw;
+  w.ld_out = k;
+  w.group_stride_out = m * k;
+  return cuda_status(gemm(moe::TIMING_WGRAD, w, st));
+}
+
+moe_status_t moe_dequantize_mxfp8(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t scale_ld,
+                                  void* out, void* stream) {
+  MOE_RANGE("moe_dequantize_mxfp8");
+  if (rows < 0 || cols <= 0 || cols % 32 || cols > (int64_t{1} << 30) || scale_ld < rows || scale_ld % 16)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!all16({codes, scales, out})) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_mx_dequant_rows(static_cast<const uint8_t*>(codes),
+                                                 static_cast<const uint8_t*>(scales), rows, static_cast<int>(cols),
+                                                 scale_ld, nullptr, 1, rows, out, nullptr,
+                                                 static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_quantize_fp8_rows(const void* src, int64_t rows, int64_t cols, void* codes, float* scales,

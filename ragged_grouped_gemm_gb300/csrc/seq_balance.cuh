@@ -1,0 +1,40 @@
+// The router's balance loss over ragged sequences, with its z-loss, and the
+// dense router gradient (see seq_balance.cu).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+struct SeqBalanceArgs {
+  int n_tok, n_exp, top_k, gate;
+  int n_seq;
+  const float* logits;         // [N, E]
+  const int32_t* topk_idx;     // [N, K]
+  const int32_t* seq_offsets;  // [S + 1]
+  float coef, z_coef;
+  const float* dloss;          // one float (nullable: 1)
+  int32_t* counts;             // [S, E]
+  float* loss;                 // [2]
+  float* dlogits;              // [N, E], nullable
+  double* part;                // seq_balance_partials(n_tok) pairs
+  int32_t* head;               // 4 int32: sequences that are not empty, their tokens, offsets that decrease
+  int32_t* ticket;             // zero before the launch, left zero
+  int32_t* status;
+};
+// Pairs of doubles of scratch (never more than the tokens).
+int64_t seq_balance_partials(int n_tok);
+cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st);
+
+// dlogits [N, E] fp32 as a sum of three bf16 terms [N, 3 * E8], E8 = E rounded up to 8, term i in the columns
+// from i * E8 (zero past E): what remains of a number after its terms is below 2^-24 of it.  Also
+// offsets = {0, N} and the starts of `slices` runs of `slice_rows` tokens.
+inline int router_term_cols(int n_exp) { return (n_exp + 7) / 8 * 8; }
+cudaError_t launch_router_terms(const float* dl, int n_tok, int n_exp, void* terms, int32_t* dense, int32_t* slices,
+                                int n_slices, int slice_rows, cudaStream_t st);
+// dw[e, :] = dw_in[e, :] + the sum over the slices and the three terms of part[slice][term * E8 + e][d].
+cudaError_t launch_router_dw(const float* part, int n_slices, int n_exp, int d, const float* dw_in, float* dw,
+                             cudaStream_t st);
+
+}  // namespace moe
