@@ -1,5 +1,5 @@
-// Activation checkpoints in 8 bits (MXFP8 rows) on the backward's side: decoding rows, the
-// row weights' gradient, and offsets that come from outside the layer (see ckpt.cu).
+// Activation checkpoints in 8 bits (MXFP8 rows) on the backward's side: decoding rows and the
+// row weights' gradient (see ckpt.cu).
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -12,10 +12,7 @@ namespace moe {
 cudaError_t launch_mx_dequant_rows(const uint8_t* codes, const uint8_t* scales, int64_t src_rows, int cols, int64_t ld,
                                    const int32_t* row_map, int row_div, int64_t rows, void* out, int32_t* status,
                                    cudaStream_t st);
-// dst [groups + 1] = offsets cut to [0, rows]; all zero where they decrease.  Either sets DEV_BAD_OFFSETS.
-cudaError_t launch_check_offsets(const int32_t* offsets, int groups, int64_t rows, int32_t* dst, int32_t* status,
-                                 cudaStream_t st);
-// dg[r] = sum over the slices, in order, of part[slice][ld] for the rows of [offsets[0], offsets[groups]).
+// dg[r] = sum over the slices, in a fixed order, of part[slice][ld] for the rows of [offsets[0], offsets[groups]).
 cudaError_t launch_row_dot_sum(const float* part, int64_t slices, int64_t ld, const int32_t* offsets, int groups,
                                int64_t rows, float* dg, cudaStream_t st);
 // Per token: dg[t, k] = dg_row[row_of_copy[t K + k]] (0 for a row of -1) and the router's logit gradient dl[t, k],

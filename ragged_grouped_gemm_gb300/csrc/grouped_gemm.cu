@@ -48,6 +48,7 @@
 //             descriptor LBO = kb x 128 (next MN atom), SBO = 1024 (next 8
 //             K-rows), advance 2048 B per K=16 step.
 #include "grouped_gemm.cuh"
+#include "pdl.cuh"
 #include "sm100_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -122,6 +123,18 @@ struct KParams {
   // written by build_group_maps_kernel before the launch; null with one group
   // (the whole-tensor maps end at the group's end already)
   const CUtensorMap* gmaps;
+  // Ragged K: A holds this many terms of a matrix side by side, term i in the
+  // columns from i * a_term_cols; every group's contraction runs over all of
+  // them against the same rows of B (0: one term).  Groups start at multiples
+  // of the k-block, so the whole-tensor maps serve them all.
+  int32_t a_terms;
+  int32_t a_term_cols;
+  int32_t out_wide;      // out0, out1, out2 (EPI_BF16_ADD: in0 too) start on 32 bytes
+  // Ragged M: offsets from outside the layer are cut to 0 .. check_rows and may
+  // not decrease (DEV_BAD_OFFSETS; no tile then); range_out receives the first
+  // and the last one as used.  0: not checked
+  int32_t check_rows;
+  int32_t* range_out;
 };
 
 // The per-group maps of a ragged-K launch: thread g writes group g's copy of
@@ -139,6 +152,34 @@ __global__ void build_group_maps_kernel(CUtensorMap* out, const __grid_constant_
                         rows);
   tensormap_rebase_rows(out + G + g, &tb, reinterpret_cast<uint64_t>(b_ptr + static_cast<int64_t>(r0) * b_ld_bytes),
                         rows);
+}
+
+// The same for offsets from outside the layer, in one block: each is cut to
+// 0 .. rows into `checked`, all of them to zero where they decrease
+// (DEV_BAD_OFFSETS either way).
+__global__ void __launch_bounds__(1024) checked_group_maps_kernel(
+    CUtensorMap* out, const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+    const int32_t* __restrict__ offsets, int G, int rows, int32_t* __restrict__ checked, int32_t* status,
+    const char* a_ptr, int64_t a_ld_bytes, const char* b_ptr, int64_t b_ld_bytes) {
+  const int g = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  int o0 = 0, o1 = 0;
+  if (g < G) {
+    o0 = offsets[g];
+    o1 = offsets[g + 1];
+  }
+  const int out_of = __syncthreads_or(g < G && (o0 < 0 || o0 > rows || o1 < 0 || o1 > rows));
+  const int less = __syncthreads_or(o1 < o0);
+  if (g >= G) return;
+  o0 = less ? 0 : min(max(o0, 0), rows);
+  o1 = less ? 0 : min(max(o1, 0), rows);
+  checked[g] = o0;
+  if (g == G - 1) checked[G] = o1;
+  if (g == 0 && (less || out_of) && status) atomicOr(status, DEV_BAD_OFFSETS);
+  const uint32_t n = static_cast<uint32_t>(max(o1 - o0, 1));   // an empty group is never loaded
+  tensormap_rebase_rows(out + g, &ta, reinterpret_cast<uint64_t>(a_ptr + static_cast<int64_t>(o0) * a_ld_bytes), n);
+  tensormap_rebase_rows(out + G + g, &tb, reinterpret_cast<uint64_t>(b_ptr + static_cast<int64_t>(o0) * b_ld_bytes), n);
 }
 
 // STG: the kernel stages fp32 output blocks for TMA stores (weight gradients)
@@ -246,6 +287,7 @@ __device__ __forceinline__ Tile decode_tile_rk(int tile, const KParams& p, int o
   t.k_rows = off1 - off0;
   t.rows_valid = min(BM, p.m_size - t.m0);
   t.num_kb = (t.k_rows + p.kblk - 1) / p.kblk;
+  if (p.a_terms > 1) t.num_kb *= p.a_terms;
   return t;
 }
 
@@ -372,6 +414,51 @@ __device__ __forceinline__ void e4m3x4_decode(uint32_t w, float (&f)[4]) {
   }
 }
 
+// One 32-byte sector a thread, in one store where the outputs start on 32 bytes (16 are asked for).
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8], bool wide) {
+  if (!wide) {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void ld_global_32b(const void* p, uint32_t (&w)[8], bool wide) {
+  if (!wide) {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    return;
+  }
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// The kept codes of 32 columns of a1 and a3 of one row, and their scale bytes.
+struct KeptBlock {
+  uint32_t a[8], b[8];
+  uint8_t ea, eb;
+  __device__ __forceinline__ void load(const KParams& p, bool row_ok, int64_t row, int col) {
+    if (!row_ok || col >= p.n_size) return;
+    const int64_t off = row * p.ld_out + col;
+    const int64_t so = static_cast<int64_t>(col / 32) * p.s_ld + row;
+    const uint4* pa = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in0) + off);
+    const uint4* pb = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in2) + off);
+    const uint4 a0 = __ldg(pa), a1 = __ldg(pa + 1), b0 = __ldg(pb), b1 = __ldg(pb + 1);
+    ea = __ldg(static_cast<const uint8_t*>(p.in1) + so);
+    eb = __ldg(static_cast<const uint8_t*>(p.in3) + so);
+    a[0] = a0.x; a[1] = a0.y; a[2] = a0.z; a[3] = a0.w;
+    a[4] = a1.x; a[5] = a1.y; a[6] = a1.z; a[7] = a1.w;
+    b[0] = b0.x; b[1] = b0.y; b[2] = b0.z; b[3] = b0.w;
+    b[4] = b1.x; b[5] = b1.y; b[6] = b1.z; b[7] = b1.w;
+  }
+};
+
 // GATHER (ragged M, bf16, one contraction source): A rows are gathered from
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
 // instruction, every lane of the producer warp taking four of the tile's
@@ -452,10 +539,33 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
       tmem_relinquish();
     }
   }
+  // Launched behind its predecessor (GemmArgs::pdl) or not: what came before used none of its results
+  pdl_wait();
   // group offsets and (ragged M) the prefix of per-group tile counts
   // (128-row M tiles times N tiles)
   if (C::kMaxG > 0)
     for (int i = threadIdx.x; i <= G; i += blockDim.x) s_tab[i] = p.offsets[i];
+  if (C::kMaxG > 0 && p.check_rows > 0) {
+    int less = 0, out = 0;
+    for (int i = threadIdx.x; i <= G; i += blockDim.x) {
+      const int o = s_tab[i];
+      less |= i > 0 && o < p.offsets[i - 1];
+      out |= o < 0 || o > p.check_rows;
+      s_tab[i] = min(max(o, 0), p.check_rows);
+    }
+    less = __syncthreads_or(less);
+    out = __syncthreads_or(out);
+    if (less)   // groups would overlap: none has a row
+      for (int i = threadIdx.x; i <= G; i += blockDim.x) s_tab[i] = 0;
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      if ((less || out) && p.status) atomicOr(p.status, DEV_BAD_OFFSETS);
+      if (p.range_out) {
+        p.range_out[0] = s_tab[0];
+        p.range_out[1] = s_tab[G];
+      }
+    }
+  }
   __syncthreads();
   if (!RAGGED_K && warp == 0) {
     const int ntiles = (p.n_size + p.tile_n - 1) / p.tile_n;
@@ -492,6 +602,10 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
     const int mtiles = (p.m_size + UR - 1) / UR;
     total_tiles = G * mtiles * ((p.n_size + BN - 1) / BN);
   }
+
+  // One tile a CTA: the next kernel may come in beside it.  With more, blocks that only wait would hold
+  // registers and slots for long (weight gradients of 64 x 2048 x 7168: 652 us so, 627 without).
+  if (total_tiles <= ustride) pdl_trigger();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -667,20 +781,26 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               tensormap_acquire(mB);
               map_g = t.g;
             }
-            const int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
+            int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
+            int m0 = t.m0;
+            if (p.a_terms > 1) {
+              const int per = t.num_kb / p.a_terms, term = kb / per;
+              r -= term * per * C::kKb;
+              m0 += term * p.a_term_cols;
+            }
             if (PAIR) {
               // both CTAs' loads complete on the leader's barrier, armed by the leader
               const int n0 = t.nt * BN + (rank & 1) * (BN / 2);
               if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
               const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-              tma_load_2d_pair(sA, mA, bar, t.m0, r);
-              tma_load_2d_pair(sA + C::kKb * 128, mA, bar, t.m0 + 64, r);
+              tma_load_2d_pair(sA, mA, bar, m0, r);
+              tma_load_2d_pair(sA + C::kKb * 128, mA, bar, m0 + 64, r);
 #pragma unroll
               for (int a = 0; a < BN / 128; ++a) tma_load_2d_pair(sB + a * C::kKb * 128, mB, bar, n0 + 64 * a, r);
             } else {
               mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-              tma_load_2d(sA, mA, &full[s], t.m0, r);
-              tma_load_2d(sA + 8192, mA, &full[s], t.m0 + 64, r);
+              tma_load_2d(sA, mA, &full[s], m0, r);
+              tma_load_2d(sA + 8192, mA, &full[s], m0 + 64, r);
 #pragma unroll
               for (int a = 0; a < BN / 64; ++a) tma_load_2d(sB + a * 8192, mB, &full[s], t.nt * BN + 64 * a, r);
             }
@@ -847,7 +967,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         // group's rows are skipped.
         constexpr int KB = RAGGED_K ? C::kKb : BK;
         const int rv = t.k_rows - kb * KB;
-        const int nkk = (RAGGED_K && rv < KB) ? (rv + 15) / 16 : KB / 16;
+        const int nkk = (RAGGED_K && rv < KB && p.a_terms <= 1) ? (rv + 15) / 16 : KB / 16;
         if (lane == 0) {
           const uint32_t a_base = smem_u32(sA);
           const uint32_t b_base = smem_u32(sB);
@@ -1015,6 +1135,23 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
     const int r = q * 32 + lane;
     uint32_t tcount = 0;
     uint32_t nstore = 0;   // TMA stores this warp has issued (fp32 staging)
+    // EPI_BF16_ADD: the addend's 128 columns of this thread's row of the tile at hand, 32 bytes a
+    // load; each is asked for as soon as the one of the tile before has been used
+    uint32_t add[EPI == EPI_BF16_ADD ? BN / 32 : 1][8];
+    auto load_add = [&](uint32_t (&v)[8], const Tile& t, int i) {
+      const int col = t.nt * BN + hf * (BN / 2) + 16 * i;
+      if (p.in0 && r < t.rows_valid && col < p.n_size)
+        ld_global_32b(static_cast<const __nv_bfloat16*>(p.in0) + static_cast<int64_t>(t.row0 + r) * p.ld_out + col, v,
+                      p.out_wide != 0);
+    };
+    if (EPI == EPI_BF16_ADD) {
+#pragma unroll
+      for (int i = 0; i < (EPI == EPI_BF16_ADD ? BN / 32 : 1); ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add[i][j] = 0u;
+        if (unit0 < total_tiles) load_add(add[i], decode_tile<RAGGED_K, BN, PAIR>(unit0, p, s_off, s_pre, rank), i);
+      }
+    }
     for (int tile = unit0; tile < total_tiles; tile += ustride, ++tcount) {
       const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
       const uint32_t buf = tcount & 1u;
@@ -1023,7 +1160,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
       const bool row_ok = r < t.rows_valid;
-      if (EPI == EPI_BF16 || EPI == EPI_F32 || EPI == EPI_BF16_ADD) {
+      if (EPI == EPI_BF16 || EPI == EPI_F32) {
         int64_t grow;
         char* obase = static_cast<char*>(p.out0);
         if (!RAGGED_K) {
@@ -1253,22 +1390,6 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               } else {
                 __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(obase) + grow * p.ld_out + col;
                 uint32_t w[8];
-                if (EPI == EPI_BF16_ADD && p.in0) {
-                  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.in0) + grow * p.ld_out + col;
-                  if (nvalid == 16) {
-                    const uint4 s0 = reinterpret_cast<const uint4*>(src)[0], s1 = reinterpret_cast<const uint4*>(src)[1];
-                    const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                      v[2 * j] = __float_as_uint(__uint_as_float(v[2 * j]) + bf16lo(sw[j]));
-                      v[2 * j + 1] = __float_as_uint(__uint_as_float(v[2 * j + 1]) + bf16hi(sw[j]));
-                    }
-                  } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                      if (j < nvalid) v[j] = __float_as_uint(__uint_as_float(v[j]) + __bfloat162float(src[j]));
-                  }
-                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
                 if (nvalid == 16) {
@@ -1396,6 +1517,28 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
             }
           }
         }
+      } else if (EPI == EPI_BF16_ADD) {
+        // out = bf16(acc + addend).  The addend came in ahead: a load in each 16-column turn cost its
+        // whole latency (4096 x 7168, E = 256: 56 us; all of a tile's loads before its wait: 37).
+        const int64_t grow = t.row0 + r;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out0) + grow * p.ld_out;
+        const bool more = tile + ustride < total_tiles;
+        const Tile next = decode_tile<RAGGED_K, BN, PAIR>(more ? tile + ustride : tile, p, s_off, s_pre, rank);
+#pragma unroll
+        for (int i = 0; i < (EPI == EPI_BF16_ADD ? BN / 32 : 1); ++i) {
+          const int c = hf * (BN / 2) + 16 * i;
+          const int col = t.nt * BN + c;
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tb + c, v);
+          tmem_wait_ld(v);
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            w[j] = pack_bf16x2(__uint_as_float(v[2 * j]) + bf16lo(add[i][j]),
+                               __uint_as_float(v[2 * j + 1]) + bf16hi(add[i][j]));
+          if (row_ok && col < p.n_size) st_global_32b(dst + col, w, p.out_wide != 0);   // n_size: a multiple of 16
+          if (more) load_add(add[i], next, i);
+        }
       } else if (EPI == EPI_SWIGLU_FWD_C) {
         // h = silu(a1) * a3 in bf16, and a1, a3 kept in 8 bits for the backward: blocks of 32
         // columns of one row, which one thread owns, so a block's largest value needs no exchange.
@@ -1452,6 +1595,9 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         const int64_t grow = t.row0 + r;
         float g = 1.0f, dot = 0.0f;
         if (row_ok && p.row_w) g = p.row_w[p.w_map ? p.w_map[grow] : grow];
+        // the codes of the next 32 columns are asked for while these are worked on
+        KeptBlock kb;
+        kb.load(p, row_ok, grow, t.nt * BN + hf * (BN / 2));
 #pragma unroll 1
         for (int c = hf * (BN / 2); c < (hf + 1) * (BN / 2); c += 32) {
           uint32_t d0[16], d1[16];
@@ -1460,42 +1606,28 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
           const int col = t.nt * BN + c;
           const bool ok = row_ok && col < p.n_size;   // n_size is a multiple of 32
           const int64_t off = grow * p.ld_out + col;
-          const int64_t so = static_cast<int64_t>(col / 32) * p.s_ld + grow;
-          uint4 ca[2], cb[2];
-          uint8_t ea = 0, eb = 0;
-          if (ok) {
-            const uint4* pa = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in0) + off);
-            const uint4* pb = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.in2) + off);
-            ca[0] = pa[0];
-            ca[1] = pa[1];
-            cb[0] = pb[0];
-            cb[1] = pb[1];
-            ea = static_cast<const uint8_t*>(p.in1)[so];
-            eb = static_cast<const uint8_t*>(p.in3)[so];
-          }
+          const KeptBlock cur = kb;
+          if (c + 32 < (hf + 1) * (BN / 2)) kb.load(p, row_ok, grow, col + 32);
           tmem_wait_ld(d0);
           reg_fence(d1);
           if (ok) {
-            const float sa = mx_scale_value(ea), sb = mx_scale_value(eb);
-            const uint32_t aw[8] = {ca[0].x, ca[0].y, ca[0].z, ca[0].w, ca[1].x, ca[1].y, ca[1].z, ca[1].w};
-            const uint32_t bw[8] = {cb[0].x, cb[0].y, cb[0].z, cb[0].w, cb[1].x, cb[1].y, cb[1].z, cb[1].w};
-            uint4* q1 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out0) + off);
-            uint4* q3 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out1) + off);
-            uint4* qh = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out2) + off);
+            const float sa = mx_scale_value(cur.ea), sb = mx_scale_value(cur.eb);
+            __nv_bfloat16* q1 = static_cast<__nv_bfloat16*>(p.out0) + off;
+            __nv_bfloat16* q3 = static_cast<__nv_bfloat16*>(p.out1) + off;
+            __nv_bfloat16* qh = static_cast<__nv_bfloat16*>(p.out2) + off;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {   // 8 columns a turn
-              uint32_t w1[4], w3[4], wh[4];
+            for (int i = 0; i < 2; ++i) {   // 16 columns a turn: 32 bytes of each output
+              uint32_t w1[8], w3[8], wh[8];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
+              for (int k = 0; k < 4; ++k) {
                 float a1[4], a3[4], o1[4], o3[4], oh[4];
-                e4m3x4_decode(aw[2 * i + k], a1);
-                e4m3x4_decode(bw[2 * i + k], a3);
+                e4m3x4_decode(cur.a[4 * i + k], a1);
+                e4m3x4_decode(cur.b[4 * i + k], a3);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const int n = 8 * i + 4 * k + j;
-                  const float dh = __uint_as_float(n < 16 ? d0[n & 15] : d1[n & 15]);
+                  const float dh = __uint_as_float(i == 0 ? d0[4 * k + j] : d1[4 * k + j]);
                   const float x = a1[j] * sa, y = a3[j] * sb;
-                  const float sg = sigmoidf_fast(x);
+                  const float sg = __fdividef(1.0f, 1.0f + __expf(-x));
                   const float silu = x * sg;
                   const float hv = silu * y;
                   const float gd = g * dh;
@@ -1511,9 +1643,9 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
                 wh[2 * k] = pack_bf16x2(oh[0], oh[1]);
                 wh[2 * k + 1] = pack_bf16x2(oh[2], oh[3]);
               }
-              q1[i] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-              q3[i] = make_uint4(w3[0], w3[1], w3[2], w3[3]);
-              qh[i] = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+              st_global_32b(q1 + 16 * i, w1, p.out_wide != 0);
+              st_global_32b(q3 + 16 * i, w3, p.out_wide != 0);
+              st_global_32b(qh + 16 * i, wh, p.out_wide != 0);
             }
           }
         }
@@ -1661,7 +1793,7 @@ bool make_map_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* d
 
 template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT = false, bool PAIR = false, bool W8 = false,
           bool GATHER = false>
-cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream) {
+cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream, bool pdl = false) {
   using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8>;
   constexpr int CN = 2;   // CTAs per cluster (PAIR)
   const size_t smem = C::smem_bytes(kp.num_groups);
@@ -1692,22 +1824,26 @@ cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream
   });
   if (attr_err != cudaSuccess) return attr_err;
   const int units = static_cast<int>(units_ub < max_units ? units_ub : max_units);
-  if (!PAIR) {
-    kern<<<units, QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads), smem, stream>>>(kp);
+  const int threads = QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads);
+  if (units_ub > max_units) pdl = false;   // several tiles a CTA: the start is not what counts
+  if (!PAIR && !pdl) {
+    kern<<<units, threads, smem, stream>>>(kp);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CN;
+  at[0].val.clusterDim.x = PAIR ? CN : 1;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(CN * units);
-  cfg.blockDim = dim3(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads));
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((PAIR ? CN : 1) * units);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.attrs = PAIR ? at : at + 1;
+  cfg.numAttrs = PAIR && pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, kp);
 }
 
@@ -1724,6 +1860,13 @@ bool use_cta_pair(int64_t rows, int groups) {
 }
 
 }  // namespace
+
+int gemm_narrow_n(int64_t rows, int groups, int64_t n) {
+  const int64_t tiles = (rows + BM - 1) / BM + std::min<int64_t>(groups, rows) / 2;   // a group's last tile is partial
+  const int64_t sms = num_sms();
+  if (tiles * ((n + 63) / 64) <= sms) return 64;
+  return tiles * ((n + 127) / 128) <= sms ? 128 : 256;
+}
 
 int gemm_ksplit(int64_t k, int requested) {
   const int64_t kb = (k + BK - 1) / BK;
@@ -1747,7 +1890,9 @@ int num_sms() {
 cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   if (a.num_groups < 1 || a.num_groups > kMaxGroups || !a.offsets || !a.out0 || a.n_size <= 0)
     return cudaErrorInvalidValue;
-  if (a.block_n != 256 && !(a.block_n == 32 && !a.b_mn && !a.a_mn && a.epi == EPI_F32))
+  const bool narrow = (a.block_n == 64 || a.block_n == 128) && !a.quant && !a.w8 && !a.a_gather && a.b_mn && !a.a_mn &&
+                      (a.epi == EPI_SWIGLU_BWD_C || a.epi == EPI_BF16_ADD);
+  if (a.block_n != 256 && !narrow && !(a.block_n == 32 && !a.b_mn && !a.a_mn && a.epi == EPI_F32))
     return cudaErrorInvalidValue;
   // bf16: ragged K comes with MN-major A (the two forms this kernel implements)
   if (!a.quant && a.ragged_k != a.a_mn) return cudaErrorInvalidValue;
@@ -1765,6 +1910,9 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   kp.out3 = a.out3;
   kp.out4 = a.out4;
   kp.s_ld = a.s_ld;
+  kp.out_wide = ((reinterpret_cast<uintptr_t>(a.out0) | reinterpret_cast<uintptr_t>(a.out1) |
+                  reinterpret_cast<uintptr_t>(a.out2) | (a.epi == EPI_BF16_ADD ? reinterpret_cast<uintptr_t>(a.in0) : 0)) &
+                 31u) == 0;
   kp.in0 = a.in0;
   kp.in1 = a.in1;
   kp.in2 = a.in2;
@@ -1772,6 +1920,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   kp.row_w = a.row_w;
   kp.w_map = a.w_map;
   kp.row_dot = a.row_dot;
+  kp.check_rows = a.check_offsets ? static_cast<int32_t>(a.max_rows) : 0;
+  kp.range_out = a.range_out;
   kp.dot_ld = a.dot_ld;
   kp.ld_out = a.ld_out;
   kp.group_stride_out = a.group_stride_out;
@@ -1951,10 +2101,10 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
                 : launch_impl<256, false, false, EPI_BF16, false, false, false, true>(kp, u, stream);
   }
   // CTA pairs: each CTA loads its own 128 rows of A and half of the B tile
-  const bool pair = BN == 256 && !a.one_sm && use_cta_pair(a.max_rows, a.num_groups) &&
+  const bool pair = BN == 256 && (a.cta_pair < 0 ? use_cta_pair(a.max_rows, a.num_groups) : a.cta_pair == 1) &&
                     (a.ragged_k ? a.epi == EPI_F32
                                 : (a.epi == EPI_BF16 || a.epi == EPI_SWIGLU_FWD || a.epi == EPI_SWIGLU_BWD ||
-                                   a.epi == EPI_SWIGLU_FWD_C || a.epi == EPI_SWIGLU_BWD_C));
+                                   a.epi == EPI_SWIGLU_FWD_C || a.epi == EPI_SWIGLU_BWD_C || a.epi == EPI_BF16_ADD));
   kp.kblk = BK;
   if (!a.ragged_k) {
     if (a.max_rows <= 0) return cudaSuccess;
@@ -1995,7 +2145,20 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
       return cudaErrorInvalidValue;
     kp.tmA[1] = kp.tmA[0];
     kp.tmB[1] = kp.tmB[0];
-    if (a.num_groups > 1) {
+    kp.a_terms = a.a_terms;
+    kp.a_term_cols = a.a_term_cols;
+    if (a.checked) {
+      if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 || a.aligned_groups)
+        return cudaErrorInvalidValue;
+      CUtensorMap* maps = static_cast<CUtensorMap*>(a.map_ws);
+      const cudaError_t e = launch_pdl(checked_group_maps_kernel, 1, (a.num_groups + 31) / 32 * 32, 0, stream, maps,
+                                       kp.tmA[0], kp.tmB[0], a.offsets, a.num_groups, static_cast<int>(a.max_rows),
+                                       a.checked, a.status, static_cast<const char*>(a.a[0].ptr), a.a[0].ld * 2,
+                                       static_cast<const char*>(a.b[0].ptr), a.b[0].ld * 2);
+      if (e != cudaSuccess) return e;
+      kp.gmaps = maps;
+      kp.offsets = a.checked;
+    } else if (a.num_groups > 1 && !a.aligned_groups) {
       // every group's own maps (copies of these two, rebased), written just before the GEMM
       if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 ||
           2 * static_cast<size_t>(a.num_groups) * sizeof(CUtensorMap) > kGemmMapScratchBytes)
@@ -2035,8 +2198,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
         return pair ? launch_impl<256, false, false, EPI_SWIGLU_FWD, false, true>(kp, u, stream)
                     : launch_impl<256, false, false, EPI_SWIGLU_FWD>(kp, u, stream);
       case EPI_SWIGLU_FWD_C:
-        return pair ? launch_impl<256, false, false, EPI_SWIGLU_FWD_C, false, true>(kp, u, stream)
-                    : launch_impl<256, false, false, EPI_SWIGLU_FWD_C>(kp, u, stream);
+        return pair ? launch_impl<256, false, false, EPI_SWIGLU_FWD_C, false, true>(kp, u, stream, a.pdl)
+                    : launch_impl<256, false, false, EPI_SWIGLU_FWD_C>(kp, u, stream, a.pdl);
       default: return cudaErrorInvalidValue;
     }
   }
@@ -2049,15 +2212,21 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
         return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD, false, true>(kp, u, stream)
                     : launch_impl<256, false, true, EPI_SWIGLU_BWD>(kp, u, stream);
       case EPI_SWIGLU_BWD_C:
-        return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD_C, false, true>(kp, u, stream)
-                    : launch_impl<256, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream);
-      case EPI_BF16_ADD: return launch_impl<256, false, true, EPI_BF16_ADD>(kp, u, stream);
+        if (BN == 64) return launch_impl<64, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream, a.pdl);
+        if (BN == 128) return launch_impl<128, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream, a.pdl);
+        return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD_C, false, true>(kp, u, stream, a.pdl)
+                    : launch_impl<256, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream, a.pdl);
+      case EPI_BF16_ADD:
+        if (BN == 64) return launch_impl<64, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
+        if (BN == 128) return launch_impl<128, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
+        return pair ? launch_impl<256, false, true, EPI_BF16_ADD, false, true>(kp, u, stream, a.pdl)
+                    : launch_impl<256, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
       default: return cudaErrorInvalidValue;
     }
   }
   if (a.a_mn && a.b_mn && a.epi == EPI_F32) {
-    return pair ? launch_impl<256, true, true, EPI_F32, false, true>(kp, u, stream)
-                : launch_impl<256, true, true, EPI_F32>(kp, u, stream);
+    return pair ? launch_impl<256, true, true, EPI_F32, false, true>(kp, u, stream, a.pdl)
+                : launch_impl<256, true, true, EPI_F32>(kp, u, stream, a.pdl);
   }
   return cudaErrorInvalidValue;
 }

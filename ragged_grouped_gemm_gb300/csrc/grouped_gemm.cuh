@@ -31,8 +31,8 @@ enum EpiKind : int {
   EPI_BF16_ADD = 7,      // out0[row, col] = bf16(acc + in0[row, col])  (in0 null: zero)
 };
 
-// Column slices of GemmArgs::row_dot: two per 256-column tile.
-inline int64_t gemm_row_dot_slices(int64_t n) { return 2 * ((n + 255) / 256); }
+// Column slices of GemmArgs::row_dot: two per tile of block_n columns.
+inline int64_t gemm_row_dot_slices(int64_t n, int block_n) { return 2 * ((n + block_n - 1) / block_n); }
 
 // MXFP8 operand: E4M3 codes [groups][rows, cols] and E8M0 scales
 // [groups][cols/32, scale_ld] (see mxfp8.cuh), cols = contraction dimension.
@@ -62,8 +62,9 @@ struct GemmArgs {
   bool a_mn = false;          // A stored MN-major (weight gradients)
   bool b_mn = false;          // B stored MN-major (data gradients)
   bool ragged_k = false;      // contraction over the group's rows
-  int block_n = 256;          // 256, or 32 for narrow N (router logits)
-  bool one_sm = false;        // bf16: no CTA pairs (weight gradients of few output rows)
+  int block_n = 256;          // 256, or 32 for narrow N (router logits); EPI_SWIGLU_BWD_C, EPI_BF16_ADD: 64, 128 too
+  bool pdl = false;           // bf16: may start while the kernel before it runs (its results are waited for)
+  int cta_pair = -1;          // bf16: 0 one SM a tile, 1 a CTA pair, -1 by the rows per group
   int ksplit = 1;             // one group, fp32 out: the contraction in ksplit slices, out0 =
                               // [ksplit][rows][ld_out] partial products (summed by the caller)
   EpiKind epi = EPI_BF16;
@@ -110,6 +111,21 @@ struct GemmArgs {
   // loaded by TMA tile::gather4 instead of a permuted copy
   const int32_t* a_gather = nullptr;
   int gather_k = 0;
+  // Ragged K (bf16): A holds a_terms terms of a matrix side by side (a_term_cols
+  // columns each), all contracted with the same rows of B.  aligned_groups: every
+  // group starts at a multiple of 128 rows and the last ends with the rows, so no
+  // per-group maps are needed (required with terms)
+  int a_terms = 0;
+  int a_term_cols = 0;
+  bool aligned_groups = false;
+  // Offsets from outside the layer: cut to 0 .. max_rows and refused where they
+  // decrease (DEV_BAD_OFFSETS, no row of any group then).  Ragged M (not W8, not
+  // MXFP8): check_offsets, and range_out (nullable) receives the first and the last
+  // as used.  Ragged K: checked, scratch of num_groups + 1 entries (map_ws is
+  // needed for one group too)
+  bool check_offsets = false;
+  int32_t* range_out = nullptr;
+  int32_t* checked = nullptr;
   // Ragged K (bf16) with several groups: global scratch of
   // kGemmMapScratchBytes, 128-byte aligned, for the per-group tensor maps a
   // small kernel writes before the GEMM (same stream)
@@ -125,6 +141,10 @@ constexpr size_t kGemmMapScratchBytes = 2 * 1024 * 128;
 cudaError_t launch_grouped_gemm(const GemmArgs& args, cudaStream_t stream);
 
 int num_sms();
+// block_n for EPI_SWIGLU_BWD_C and EPI_BF16_ADD: 64 or 128 where so many tiles still run at once (each tile's end
+// is a chain of loads, sums and stores that narrower tiles shorten: 3108 rows in 16 groups, 256 columns of
+// 512 17.3 us on 256 columns a tile), else 256.
+int gemm_narrow_n(int64_t rows, int groups, int64_t n);
 // Contraction slices a launch with GemmArgs::ksplit = requested over k
 // elements actually uses (slices of whole 64-element k-blocks, none empty).
 int gemm_ksplit(int64_t k, int requested);

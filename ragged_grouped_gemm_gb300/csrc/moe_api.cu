@@ -65,15 +65,56 @@ struct WsLayout {
   size_t rterms = 0, rend = 0;  // the dense router gradient's terms and partial products (over others' scratch)
 };
 
-// Bytes of the dense router gradient's scratch with `slices` runs of tokens: the bf16 terms of
-// dlogits, {0, N} and the runs' starts, the partial weight gradients.
+// The dense router gradient's weight product contracts over the tokens, dlogits being three bf16
+// terms of E8 columns.  Up to 128 columns in all the terms are the rows of one tile (MMA time does
+// not matter there, x is read once); more: one tile of E8 rows whose contraction runs over the three
+// terms in turn, so that a partial product is a third as large and no tile mixes terms.  The tokens
+// are cut into runs, the groups of one ragged launch, to fill the SMs: what counts is full waves
+// against the traffic of the partial products.
+struct RouterPlan {
+  int e8, m;        // columns of a term, rows of a partial product
+  bool packed, pair;
+  int slices, per;  // runs and the tokens of each but the last (a multiple of 128)
+};
+constexpr int kRouterSlices = 16;
 size_t router_terms_bytes(const moe_desc_t& d) {
   return align_up(static_cast<size_t>(d.n_tok) * 3 * moe::router_term_cols(d.n_exp) * 2);
 }
-constexpr int kRouterSlices = 16;
-size_t router_bytes(const moe_desc_t& d, int slices) {
-  return router_terms_bytes(d) + kAlign +
-         align_up(static_cast<size_t>(slices) * 3 * moe::router_term_cols(d.n_exp) * d.d_model * 4);
+// Bytes of scratch: the terms, {0, N} and the runs' starts, the partial products.
+size_t router_bytes(const moe_desc_t& d, int m, int slices) {
+  return router_terms_bytes(d) + kAlign + align_up(static_cast<size_t>(slices) * m * d.d_model * 4);
+}
+int router_rows(const moe_desc_t& d) {
+  const int e8 = moe::router_term_cols(d.n_exp);
+  return 3 * e8 <= 128 ? 3 * e8 : e8;
+}
+RouterPlan router_plan(const moe_desc_t& d, size_t scratch) {
+  RouterPlan p;
+  p.e8 = moe::router_term_cols(d.n_exp);
+  p.m = router_rows(d);
+  p.packed = p.m != p.e8;
+  p.pair = p.m > 128;
+  const int64_t N = d.n_tok, D = d.d_model;
+  const int64_t units = ((p.m + (p.pair ? 255 : 127)) / (p.pair ? 256 : 128)) * ((D + 255) / 256);
+  const int64_t at_once = std::max(1, moe::num_sms() / (p.pair ? 2 : 1));
+  // a wave of whole contractions: 64 tokens take four MMAs of about 0.085 us a term; partial
+  // products are read again at about 5 TB/s (they are written while the MMAs run)
+  const double work = static_cast<double>(N) / 64 * 4 * 0.085 * (p.packed ? 1 : 3);
+  const double traffic = 4.0 * p.m * D / 5e6;
+  double best = 0;
+  p.slices = 0;
+  for (int s = 1; s <= kRouterSlices && (s == 1 || (N + s - 1) / s >= 128); ++s) {
+    if (s > 1 && router_bytes(d, p.m, s) > scratch) break;
+    const double waves = static_cast<double>((units * s + at_once - 1) / at_once);
+    const double t = waves * work / s + s * traffic;
+    if (!p.slices || t < best) {
+      best = t;
+      p.slices = s;
+    }
+  }
+  p.per = static_cast<int>(((N + p.slices - 1) / p.slices + 127) / 128 * 128);
+  p.slices = static_cast<int>((N + p.per - 1) / p.per);
+  return p;
 }
 
 int64_t ld16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -159,7 +200,7 @@ WsLayout layout(const moe_desc_t& d) {
   L.norm = norm <= L.gmaps - L.dl ? L.dl : o;
   if (L.norm == o) o += norm;
   // the dense router gradient too, over the same scratch where one run of tokens fits
-  const size_t router = router_bytes(d, 1);
+  const size_t router = router_bytes(d, router_rows(d), 1);
   const bool over = router <= L.gmaps - L.dl;
   L.rterms = over ? L.dl : o;
   if (!over) o += router;
@@ -167,6 +208,9 @@ WsLayout layout(const moe_desc_t& d) {
   L.total = o;
   return L;
 }
+
+// Columns a tile of the first product of the backward from kept rows.
+int dot_block_n(int64_t rows, int groups, int64_t f) { return moe::gemm_narrow_n(rows, groups, f); }
 
 // The workspace of a layer with 8-bit checkpoints: the layer's own, then what the forward and
 // the backward hold in passing (h of either, the decoded x, partial sums of the gate gradient).
@@ -183,7 +227,7 @@ CkptLayout ckpt_layout(const moe_desc_t& d) {
   L.hs = o; o = align_up(o + N * Fs * 2);
   L.xp = o; o = align_up(o + R * D * 2);
   L.xt = o; o = align_up(o + (Fs ? N * D * 2 : 0));
-  L.dot = o; o = align_up(o + static_cast<size_t>(moe::gemm_row_dot_slices(d.d_ff)) * R * 4);
+  L.dot = o; o = align_up(o + static_cast<size_t>(moe::gemm_row_dot_slices(d.d_ff, dot_block_n(R, d.n_exp, d.d_ff))) * R * 4);
   L.dgr = o; o = align_up(o + R * 4);
   L.total = o;
   return L;
@@ -428,6 +472,8 @@ void kept_dgrad(GemmArgs& g, const KeptBackward& k, int64_t rows) {
   g.w_map = k.w_map;
   g.row_dot = k.dot;
   g.dot_ld = rows;
+  g.block_n = dot_block_n(rows, g.num_groups, g.n_size);
+  g.pdl = true;
 }
 
 // Backward of one expert set: dgrad through w2 with the SwiGLU derivative,
@@ -1389,46 +1435,44 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
     return MOE_OK;
   }
   const WsLayout L = layout(*d);
-  const int e8 = moe::router_term_cols(E), m = 3 * e8;
-  // The weight gradient contracts over the tokens: their runs are the groups of one ragged
-  // product, as many as fill the SMs and the scratch holds, 256 tokens at least.
-  const int64_t tiles = static_cast<int64_t>((m + 127) / 128) * ((D + 255) / 256);
-  int slices = static_cast<int>(std::min<int64_t>(
-      {kRouterSlices, std::max<int64_t>(1, 2 * moe::num_sms() / tiles), (static_cast<int64_t>(N) + 255) / 256}));
-  while (slices > 1 && router_bytes(*d, slices) > L.rend - L.rterms) --slices;
-  const int per = static_cast<int>(((static_cast<int64_t>(N) + slices - 1) / slices + 63) / 64 * 64);
-  slices = (N + per - 1) / per;
+  const RouterPlan plan = router_plan(*d, L.rend - L.rterms);
+  const int e8 = plan.e8;
   char* terms = at<char>(ws, L.rterms);
   int32_t* dense = reinterpret_cast<int32_t*>(terms + router_terms_bytes(*d));
   int32_t* starts = dense + 4;
   float* part = reinterpret_cast<float*>(terms + router_terms_bytes(*d) + kAlign);
   int32_t* status = at<int32_t>(ws, L.status);
-  MOE_CUDA(moe::launch_router_terms(dlogits, N, E, terms, dense, starts, slices, per, st));
+  MOE_CUDA(moe::launch_router_terms(dlogits, N, E, terms, dense, starts, plan.slices, plan.per, st));
   GemmArgs w;
   w.epi = moe::EPI_F32;
   w.a_mn = w.b_mn = w.ragged_k = true;
-  w.one_sm = true;
-  w.map_ws = map_scratch(ws, L);
+  w.cta_pair = plan.pair ? 1 : 0;
+  w.pdl = true;
+  w.aligned_groups = true;
   w.offsets = starts;
-  w.num_groups = slices;
+  w.num_groups = plan.slices;
   w.max_rows = N;
   w.status = status;
-  w.a[0] = act(terms, N, m);
+  w.a[0] = act(terms, N, 3 * e8);
   w.b[0] = act(x, N, D);
-  w.m_size = m;
+  if (!plan.packed) {
+    w.a_terms = 3;
+    w.a_term_cols = e8;
+  }
+  w.m_size = plan.m;
   w.n_size = D;
   w.out0 = part;
   w.ld_out = D;
-  w.group_stride_out = static_cast<int64_t>(m) * D;
+  w.group_stride_out = static_cast<int64_t>(plan.m) * D;
   MOE_CUDA(gemm(moe::TIMING_WGRAD, w, st));
-  MOE_CUDA(moe::launch_router_dw(part, slices, E, D, dw_in, dw_gate, st));
+  MOE_CUDA(moe::launch_router_dw(part, plan.slices, plan.packed ? 3 : 1, E, D, dw_in, dw_gate, st));
   // dx: the first two terms against W_g, one contraction source each
   GemmArgs g;
   g.epi = moe::EPI_BF16_ADD;
   g.b_mn = true;
   for (int i = 0; i < 2; ++i) {
     g.a[i] = act(terms + static_cast<size_t>(i) * e8 * 2, N, e8);
-    g.a[i].ld = m;
+    g.a[i].ld = 3 * e8;
     g.b[i] = wstack(w_gate, 1, E, D);
   }
   g.k0 = g.k1 = e8;
@@ -1438,6 +1482,10 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
   g.n_size = D;
   g.in0 = dx_in;
   g.out0 = dx;
+  g.block_n = moe::gemm_narrow_n(N, 1, D);
+  // a pair shares W_g's tiles: with few experts there is little of it to share
+  g.cta_pair = g.block_n == 256 && E > 64 && N >= 512 ? 1 : 0;
+  g.pdl = true;
   g.ld_out = D;
   g.status = status;
   return cuda_status(gemm(moe::TIMING_DGRAD, g, st));
@@ -1524,7 +1572,7 @@ moe_status_t moe_backward_ckpt(const moe_desc_t* d, const void* w_gate, const mo
                        at<void>(ws, L.da1), at<void>(ws, L.da3), rows, g->dw1, g->dw3, g->dw2, status, st,
                        map_scratch(ws, L), nullptr, nullptr, nullptr, nullptr, &kb));
   float* dgr = at<float>(ws, C.dgr);
-  MOE_CUDA(moe::launch_row_dot_sum(kb.dot, moe::gemm_row_dot_slices(F), R, s->offsets, E, R, dgr, st));
+  MOE_CUDA(moe::launch_row_dot_sum(kb.dot, moe::gemm_row_dot_slices(F, dot_block_n(R, E, F)), R, s->offsets, E, R, dgr, st));
   MOE_CUDA(moe::launch_gate_bwd(N, K, d->gate, dgr, s->row_of_copy, s->topk_w, s->logits, E, s->topk_idx, dg, dl, st));
   void* dxs = nullptr;
   if (d->n_shared) {
@@ -1554,7 +1602,7 @@ static bool ckpt_sizes_ok(int64_t n_groups, int64_t rows, int64_t a, int64_t b) 
 moe_status_t moe_swiglu_backward_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t d, int64_t f,
                                                      size_t* bytes) {
   if (!bytes || !ckpt_sizes_ok(n_groups, rows, d, f)) return MOE_ERR_INVALID_ARG;
-  *bytes = kAlign + align_up((n_groups + 1) * 4) + align_up(static_cast<size_t>(moe::gemm_row_dot_slices(f)) * rows * 4);
+  *bytes = 2 * kAlign + align_up(static_cast<size_t>(moe::gemm_row_dot_slices(f, dot_block_n(rows, static_cast<int>(n_groups), f))) * rows * 4);
   return MOE_OK;
 }
 
@@ -1574,15 +1622,16 @@ moe_status_t moe_swiglu_backward_ckpt(int64_t n_groups, int64_t rows, int64_t d,
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* status = static_cast<int32_t*>(ws);
-  int32_t* off = at<int32_t>(ws, kAlign);
+  int32_t* range = at<int32_t>(ws, kAlign);
   const int groups = static_cast<int>(n_groups);
-  MOE_CUDA(moe::launch_check_offsets(offsets, groups, rows, off, status, st));
   GemmArgs g;
   g.b_mn = true;
   g.a[0] = act(dy, rows, d);
   g.b[0] = wstack(w2, groups, d, f);
   g.k0 = static_cast<int>(d);
-  g.offsets = off;
+  g.offsets = offsets;
+  g.check_offsets = true;
+  g.range_out = range;
   g.num_groups = groups;
   g.max_rows = rows;
   g.n_size = static_cast<int>(f);
@@ -1590,11 +1639,11 @@ moe_status_t moe_swiglu_backward_ckpt(int64_t n_groups, int64_t rows, int64_t d,
   g.out1 = da3;
   g.ld_out = f;
   g.status = status;
-  float* dot = dg ? at<float>(ws, kAlign + align_up((n_groups + 1) * 4)) : nullptr;
+  float* dot = dg ? at<float>(ws, 2 * kAlign) : nullptr;
   kept_dgrad(g, KeptBackward{{a1, a1_scale, a3, a3_scale, scale_ld}, h, row_w, nullptr, dot}, rows);
   MOE_CUDA(gemm(moe::TIMING_DGRAD, g, st));
   if (!dg) return MOE_OK;
-  return cuda_status(moe::launch_row_dot_sum(dot, moe::gemm_row_dot_slices(f), rows, off, groups, rows, dg, st));
+  return cuda_status(moe::launch_row_dot_sum(dot, moe::gemm_row_dot_slices(f, g.block_n), rows, range, 1, rows, dg, st));
 }
 
 moe_status_t moe_grouped_wgrad_ckpt_workspace_size(int64_t n_groups, int64_t rows, int64_t m, int64_t k,
@@ -1625,14 +1674,15 @@ moe_status_t moe_grouped_wgrad_ckpt(int64_t n_groups, int64_t rows, int64_t m, i
   const size_t maps = kAlign + align_up((n_groups + 1) * 4);
   void* xp = at<void>(ws, maps + align_up(moe::kGemmMapScratchBytes + 128));
   const int groups = static_cast<int>(n_groups);
-  MOE_CUDA(moe::launch_check_offsets(offsets, groups, rows, off, status, st));
   MOE_CUDA(moe::launch_mx_dequant_rows(static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(x_scale), x_rows,
                                        static_cast<int>(k), scale_ld, row_map, row_div, rows, xp, status, st));
   GemmArgs w;
   w.epi = moe::EPI_F32;
   w.a_mn = w.b_mn = w.ragged_k = true;
   w.map_ws = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(at<char>(ws, maps)) + 127) & ~uintptr_t(127));
-  w.offsets = off;
+  w.offsets = offsets;
+  w.checked = off;
+  w.pdl = true;
   w.num_groups = groups;
   w.max_rows = rows;
   w.status = status;

@@ -89,12 +89,12 @@ __global__ void __launch_bounds__(kThreads) seq_counts_kernel(int n_tok, int E, 
   const int64_t a = lo + min(n, per * rank), b = lo + min(n, per * (rank + 1));
   int* mine = s_hist + warp * E;
   bool bad = false;
-  for (int64_t i = a + threadIdx.x; i < b; i += 4 * kThreads) {
-    int e[4];
+  for (int64_t i = a + threadIdx.x; i < b; i += 8 * kThreads) {
+    int e[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = i + j * kThreads < b ? __ldg(idx + i + j * kThreads) : E;
+    for (int j = 0; j < 8; ++j) e[j] = i + j * kThreads < b ? __ldg(idx + i + j * kThreads) : E;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       if (e[j] >= 0 && e[j] < E) atomicAdd(mine + e[j], 1);
       else bad |= i + j * kThreads < b;
     }
@@ -156,8 +156,59 @@ struct RowsParams {
 // warp consecutive so that a sequence's f stays in registers from one to the
 // next.  Each block's sums leave as two doubles, and the last block to finish
 // adds them in a fixed order: equal calls give equal bits.
+// acc += v with what the addition lost kept in acc.y (a warp's tokens add up in 32 bits; 64-bit additions by every
+// warp took 4 of 12 us).
+__device__ __forceinline__ void add_kept(float2& acc, float v) {
+  const float s = acc.x + v;
+  const float b = s - acc.x;
+  acc.y += (acc.x - (s - b)) + (v - b);
+  acc.x = s;
+}
+
+// Resident blocks an SM by the registers a row takes: all blocks run at once, so that the look-up of a warp's
+// sequence and a block's end are paid once.
 template <int NPER>
-__global__ void __launch_bounds__(kThreads) seq_rows_kernel(const RowsParams p) {
+constexpr int kRowBlocks = NPER <= 4 ? 4 : NPER <= 8 ? 3 : NPER <= 16 ? 2 : 1;
+
+// Register j of a lane holds expert e_of(lane, j): VEC consecutive experts a lane, so that rows move in 16-byte
+// words where E and the arrays allow it.
+template <int VEC>
+__device__ __forceinline__ int e_of(int lane, int j) {
+  return VEC * lane + j % VEC + 32 * VEC * (j / VEC);
+}
+template <int NPER, int VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&v)[NPER]) {
+#pragma unroll
+  for (int j = 0; j < NPER; j += VEC) {
+    const int e = e_of<VEC>(lane, j);
+    if (VEC == 4) {
+      const float4 x = e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      v[j] = x.x;
+      v[j + 1 < NPER ? j + 1 : j] = x.y;
+      v[j + 2 < NPER ? j + 2 : j] = x.z;
+      v[j + 3 < NPER ? j + 3 : j] = x.w;
+    } else {
+      v[j] = e < E ? __ldg(row + e) : -INFINITY;
+    }
+  }
+}
+template <int NPER, int VEC>
+__device__ __forceinline__ void store_row(float* __restrict__ row, int E, int lane, const float (&v)[NPER]) {
+#pragma unroll
+  for (int j = 0; j < NPER; j += VEC) {
+    const int e = e_of<VEC>(lane, j);
+    if (e >= E) continue;
+    if (VEC == 4)
+      *reinterpret_cast<float4*>(row + e) = make_float4(v[j], v[j + 1 < NPER ? j + 1 : j], v[j + 2 < NPER ? j + 2 : j],
+                                                        v[j + 3 < NPER ? j + 3 : j]);
+    else
+      row[e] = v[j];
+  }
+}
+
+template <int NPER, int VEC>
+__global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(const RowsParams p) {
   __shared__ double s_red[2][kThreads];
   __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -166,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) seq_rows_kernel(const RowsParams p) 
   const int full = __ldg(p.head), used = __ldg(p.head + 1), wrong = __ldg(p.head + 2);
   const float up = p.dloss ? __ldg(p.dloss) : 1.0f;
   const float zf = used > 0 ? p.z_coef / static_cast<float>(used) : 0.0f;
-  double bal = 0.0, zz = 0.0;
+  float2 bal = make_float2(0.0f, 0.0f), zz = bal;
   const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.per;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(N), w0));
   const int t1 = static_cast<int>(min(static_cast<int64_t>(N), w0 + p.per));
@@ -179,15 +230,27 @@ __global__ void __launch_bounds__(kThreads) seq_rows_kernel(const RowsParams p) 
   int end = t0;         // the first token that the sequence at hand does not hold
   bool inside = false;
   float factor = 0.0f;
-  float f[NPER];
+  float f[NPER], nxt[NPER];
 #pragma unroll
   for (int j = 0; j < NPER; ++j) f[j] = 0.0f;
+  // the first row is on its way while its sequence is looked up, every later one while the one before is worked on
+  if (t0 < t1) load_row<NPER, VEC>(p.logits + static_cast<int64_t>(t0) * E, E, lane, nxt);
   for (int t = t0; t < t1; ++t) {
+    float l[NPER];
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) l[j] = nxt[j];
+    if (t + 1 < t1) load_row<NPER, VEC>(p.logits + static_cast<int64_t>(t + 1) * E, E, lane, nxt);
     if (t >= end) {
-      int lo = -1, hi = p.S;   // lo: the last sequence that starts at or before t (-1: none)
+      // the last sequence that starts at or before t (-1: none), 32 starts a look
+      int lo = -1, hi = p.S;   // start[lo] <= t < start[hi]
       while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (seq_at(p.off, mid, N) <= t) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + 1 + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, i < hi && seq_at(p.off, min(i, p.S), N) <= t);
+        const int c = __popc(le);   // starts do not decrease (or `wrong` is set): a run of lanes from the first
+        const int base = lo;
+        if (c > 0) lo = base + 1 + (c - 1) * step;
+        hi = min(hi, base + 1 + c * step);
       }
       const int a = lo < 0 ? 0 : seq_at(p.off, lo, N);
       const int b = seq_at(p.off, lo + 1, N);
@@ -198,84 +261,101 @@ __global__ void __launch_bounds__(kThreads) seq_rows_kernel(const RowsParams p) 
         factor = p.coef * static_cast<float>(E) / (static_cast<float>(full) * len);
         const int32_t* c = p.counts + static_cast<int64_t>(lo) * E;
 #pragma unroll
-        for (int j = 0; j < NPER; ++j)
-          f[j] = lane + 32 * j < E ? static_cast<float>(__ldg(c + lane + 32 * j)) / len : 0.0f;
+        for (int j = 0; j < NPER; ++j) {
+          const int e = e_of<VEC>(lane, j);
+          f[j] = e < E ? static_cast<float>(__ldg(c + e)) / len : 0.0f;
+        }
       }
     }
     const int64_t row = static_cast<int64_t>(t) * E;
     if (!inside) {
       if (p.dl) {
 #pragma unroll
-        for (int j = 0; j < NPER; ++j)
-          if (lane + 32 * j < E) p.dl[row + lane + 32 * j] = 0.0f;
+        for (int j = 0; j < NPER; ++j) l[j] = 0.0f;
+        store_row<NPER, VEC>(p.dl + row, E, lane, l);
       }
       continue;
     }
-    float l[NPER], q[NPER];
-#pragma unroll
-    for (int j = 0; j < NPER; ++j) l[j] = lane + 32 * j < E ? __ldg(p.logits + row + lane + 32 * j) : -INFINITY;
-    float m = l[0];
-    bool nan = false;   // fmaxf passes a NaN over
-#pragma unroll
-    for (int j = 0; j < NPER; ++j) {
-      m = fmaxf(m, l[j]);
-      nan |= l[j] != l[j];
-    }
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.0f;   // every expert masked: no probability, no z
-    if (__any_sync(0xffffffffu, nan)) m = NAN;
-    const bool soft = p.gate == 0 || p.z_coef != 0.0f;
-    float z = 0.0f;
+    float inner, lse = 0.0f;
+    // q: the softmax before its division by z; w: the slope of the gate's distribution before its own
+    float q[NPER], w[NPER];
+    float z = 0.0f, sum = 0.0f, fs = 0.0f;
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
-      q[j] = soft ? expf(l[j] - m) : 0.0f;
+      q[j] = expf(l[j]);
       z += q[j];
-    }
-    float lse = 0.0f, invz = 0.0f;
-    if (soft) {
-      z = warp_add(z);
-      if (z != 0.0f) {
-        lse = m + logf(z);
-        invz = 1.0f / z;
+      if (p.gate == 0) {
+        fs = fmaf(f[j], q[j], fs);
+      } else {
+        // sigmoid = v / (1 + v) and its slope v / (1 + v)^2 for v = e^l: the softmax's exponential serves both
+        const float r = __fdividef(1.0f, 1.0f + q[j]);
+        const float sg = q[j] * r;
+        sum += sg;
+        fs = fmaf(f[j], sg, fs);
+        w[j] = sg * r;
       }
     }
-    float inner = 0.0f, invs = 0.0f;
-    const float g2 = 2.0f * zf * lse * invz * up;
-    if (p.gate == 0) {
-#pragma unroll
-      for (int j = 0; j < NPER; ++j) inner = fmaf(f[j], q[j], inner);
-      inner = warp_add(inner) * invz;
-      if (p.dl) {
-        const float g1 = factor * invz * up;
-#pragma unroll
-        for (int j = 0; j < NPER; ++j)
-          if (lane + 32 * j < E) p.dl[row + lane + 32 * j] = q[j] * fmaf(g1, f[j] - inner, g2);
-      }
+    z = warp_add(z);
+    fs = warp_add(fs);
+    if (p.gate != 0) sum = warp_add(sum);
+    float invz, invq;
+    // Exponentials of the logits as they are, without the largest taken off: right while their sum is neither near the
+    // end of fp32's range (every logit is below 78 then, 1 + v is finite) nor so small that terms that matter were
+    // lost (the largest is above -28 then, what e^l loses below -87 is 1e-25 of it).  Else row by row the long way.
+    if (z < 1e34f && z > 1e-9f) {
+      invz = 1.0f / z;
+      lse = logf(z);
+      invq = p.gate == 0 ? invz : 1.0f / sum;
+      inner = fs * invq;
     } else {
-      float sum = 0.0f, sg[NPER];
+      float m = l[0];
+      bool nan = false;   // fmaxf passes a NaN over
 #pragma unroll
       for (int j = 0; j < NPER; ++j) {
-        sg[j] = 1.0f / (1.0f + expf(-l[j]));
-        sum += sg[j];
-        inner = fmaf(f[j], sg[j], inner);
+        m = fmaxf(m, l[j]);
+        nan |= l[j] != l[j];
       }
-      sum = warp_add(sum);
-      if (sum != 0.0f) invs = 1.0f / sum;
-      inner = warp_add(inner) * invs;
-      if (p.dl) {
-        const float g1 = factor * invs * up;
+      m = warp_max(m);
+      if (m == -INFINITY) m = 0.0f;   // every expert masked: no probability, no z
+      if (__any_sync(0xffffffffu, nan)) m = NAN;
+      z = sum = fs = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NPER; ++j)
-          if (lane + 32 * j < E)
-            p.dl[row + lane + 32 * j] = fmaf(g1 * (sg[j] * (1.0f - sg[j])), f[j] - inner, g2 * q[j]);
+      for (int j = 0; j < NPER; ++j) {
+        q[j] = expf(l[j] - m);
+        z += q[j];
+        float d = q[j];
+        if (p.gate != 0) {
+          const float v = expf(-fabsf(l[j]));   // sigmoid(|l|) = 1 / (1 + v), the other side v / (1 + v)
+          const float big = 1.0f / (1.0f + v), small = v * big;
+          d = l[j] > 0.0f ? big : small;
+          if (l[j] != l[j]) d = l[j];
+          w[j] = big * small;
+          if (l[j] == -INFINITY) d = w[j] = 0.0f;
+          sum += d;
+        }
+        fs = fmaf(f[j], d, fs);
       }
+      z = warp_add(z);
+      sum = warp_add(sum);
+      fs = warp_add(fs);
+      invz = z != 0.0f ? 1.0f / z : 0.0f;
+      lse = z != 0.0f ? m + logf(z) : 0.0f;
+      invq = p.gate == 0 ? invz : sum != 0.0f ? 1.0f / sum : 0.0f;
+      inner = fs * invq;
     }
-    bal += static_cast<double>(factor) * inner;
-    zz += static_cast<double>(lse) * lse;
+    if (p.dl) {
+      const float g1 = factor * invq * up, g2 = 2.0f * zf * lse * invz * up;
+#pragma unroll
+      for (int j = 0; j < NPER; ++j)
+        l[j] = p.gate == 0 ? q[j] * fmaf(g1, f[j] - inner, g2) : fmaf(g1 * w[j], f[j] - inner, g2 * q[j]);
+      store_row<NPER, VEC>(p.dl + row, E, lane, l);
+    }
+    add_kept(bal, factor * inner);
+    if (p.z_coef != 0.0f) add_kept(zz, lse * lse);   // a row of the type's lowest value is infinite here
   }
   if (lane == 0) {
-    s_red[0][warp] = bal;
-    s_red[1][warp] = zz;
+    s_red[0][warp] = static_cast<double>(bal.x) + (isfinite(bal.x) ? bal.y : 0.0f);
+    s_red[1][warp] = static_cast<double>(zz.x) + (isfinite(zz.x) ? zz.y : 0.0f);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -314,10 +394,18 @@ __global__ void __launch_bounds__(kThreads) seq_rows_kernel(const RowsParams p) 
   }
 }
 
-// Blocks of the rows kernel: a warp a token, at most eight blocks an SM.
-int rows_grid(int n_tok) {
+int row_blocks(int n_exp) {
+  return n_exp <= 128 ? kRowBlocks<4> : n_exp <= 256 ? kRowBlocks<8> : n_exp <= 512 ? kRowBlocks<16> : kRowBlocks<32>;
+}
+// Blocks of the rows kernel: a warp a token, no more than are resident.
+int rows_grid(int n_tok, int n_exp) {
   return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(n_tok) + kWarps - 1) / kWarps,
-                                            static_cast<int64_t>(num_sms()) * 8));
+                                            static_cast<int64_t>(num_sms()) * row_blocks(n_exp)));
+}
+
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float4 plus(const float4& a, const float4& b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 // 8 columns of a row a thread.
@@ -366,29 +454,27 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
   }
 }
 
-__global__ void __launch_bounds__(256) router_dw_kernel(const float4* __restrict__ part, int n_slices, int E, int e8,
-                                                        int d4, const float4* dw_in, float4* dw) {
+// V numbers a thread: four where that leaves every SM its threads, one where few experts would not.
+template <int TERMS, typename V>
+__global__ void __launch_bounds__(256) router_dw_kernel(const V* __restrict__ part, int n_slices, int64_t n,
+                                                        int64_t term, const V* dw_in, V* dw) {
+  pdl_trigger();
   pdl_wait();
-  const int e = blockIdx.x;
-  const int i = blockIdx.y * 256 + threadIdx.x;
-  if (i >= d4) return;
-  const int64_t o = static_cast<int64_t>(e) * d4 + i;
-  float4 acc = dw_in ? dw_in[o] : make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (o >= n) return;
+  V acc{};
+  if (dw_in) acc = dw_in[o];
+#pragma unroll 4
   for (int s = 0; s < n_slices; ++s) {
-    const float4* src = part + static_cast<int64_t>(s) * 3 * e8 * d4 + o;
-    const float4 h = __ldcg(src), m = __ldcg(src + static_cast<int64_t>(e8) * d4),
-                 l = __ldcg(src + 2 * static_cast<int64_t>(e8) * d4);
-    acc.x += h.x + (m.x + l.x);
-    acc.y += h.y + (m.y + l.y);
-    acc.z += h.z + (m.z + l.z);
-    acc.w += h.w + (m.w + l.w);
+    const V* src = part + s * TERMS * term + o;
+    V v = __ldcg(src);
+    if (TERMS == 3) v = plus(v, plus(__ldcg(src + term), __ldcg(src + 2 * term)));
+    acc = plus(acc, v);
   }
   dw[o] = acc;
 }
 
 }  // namespace
-
-int64_t seq_balance_partials(int n_tok) { return rows_grid(n_tok); }
 
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   if (a.n_tok < 1 || a.n_exp < 1 || a.n_exp > 1024 || a.n_seq < 1) return cudaErrorInvalidValue;
@@ -405,7 +491,7 @@ cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
     e = launch_pdl(seq_counts_kernel<1>, static_cast<unsigned>(a.n_seq + 1), kThreads, smem, st, a.n_tok, a.n_exp,
                    a.top_k, a.n_seq, a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
   if (e != cudaSuccess) return e;
-  const int grid = rows_grid(a.n_tok);
+  const int grid = rows_grid(a.n_tok, a.n_exp);
   RowsParams p;
   p.logits = a.logits;
   p.counts = a.counts;
@@ -425,11 +511,15 @@ cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   p.S = a.n_seq;
   p.per = static_cast<int>((static_cast<int64_t>(a.n_tok) + static_cast<int64_t>(grid) * kWarps - 1) /
                            (static_cast<int64_t>(grid) * kWarps));
-  auto kern = a.n_exp <= 32 ? seq_rows_kernel<1>
-              : a.n_exp <= 64 ? seq_rows_kernel<2>
-              : a.n_exp <= 128 ? seq_rows_kernel<4>
-              : a.n_exp <= 256 ? seq_rows_kernel<8>
-              : a.n_exp <= 512 ? seq_rows_kernel<16> : seq_rows_kernel<32>;
+  // 16-byte words above 64 experts (below, lanes would idle), where every row starts on one
+  const bool vec = a.n_exp > 64 && a.n_exp % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) |
+                                                        reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0;
+  auto kern = a.n_exp <= 32 ? seq_rows_kernel<1, 1>
+              : a.n_exp <= 64 ? seq_rows_kernel<2, 1>
+              : a.n_exp <= 128 ? (vec ? seq_rows_kernel<4, 4> : seq_rows_kernel<4, 1>)
+              : a.n_exp <= 256 ? (vec ? seq_rows_kernel<8, 4> : seq_rows_kernel<8, 1>)
+              : a.n_exp <= 512 ? (vec ? seq_rows_kernel<16, 4> : seq_rows_kernel<16, 1>)
+                               : (vec ? seq_rows_kernel<32, 4> : seq_rows_kernel<32, 1>);
   return launch_pdl(kern, static_cast<unsigned>(grid), kThreads, 0, st, p);
 }
 
@@ -441,13 +531,15 @@ cudaError_t launch_router_terms(const float* dl, int n_tok, int n_exp, void* ter
                     static_cast<uint4*>(terms), dense, slices, n_slices, slice_rows);
 }
 
-cudaError_t launch_router_dw(const float* part, int n_slices, int n_exp, int d, const float* dw_in, float* dw,
-                             cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(n_exp), static_cast<unsigned>((d / 4 + 255) / 256));
-  router_dw_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(part), n_slices, n_exp,
-                                         router_term_cols(n_exp), d / 4, reinterpret_cast<const float4*>(dw_in),
-                                         reinterpret_cast<float4*>(dw));
-  return cudaGetLastError();
+cudaError_t launch_router_dw(const float* part, int n_slices, int terms, int n_exp, int d, const float* dw_in,
+                             float* dw, cudaStream_t st) {
+  const int64_t n = static_cast<int64_t>(n_exp) * d, term = static_cast<int64_t>(router_term_cols(n_exp)) * d;
+  if (n / 4 >= static_cast<int64_t>(num_sms()) * 512)
+    return launch_pdl(terms == 3 ? router_dw_kernel<3, float4> : router_dw_kernel<1, float4>,
+                      static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, st, reinterpret_cast<const float4*>(part),
+                      n_slices, n / 4, term / 4, reinterpret_cast<const float4*>(dw_in), reinterpret_cast<float4*>(dw));
+  return launch_pdl(terms == 3 ? router_dw_kernel<3, float> : router_dw_kernel<1, float>,
+                    static_cast<unsigned>((n + 255) / 256), 256, 0, st, part, n_slices, n, term, dw_in, dw);
 }
 
 }  // namespace moe

@@ -18,13 +18,11 @@ struct SeqBalanceArgs {
   int32_t* counts;             // [S, E]
   float* loss;                 // [2]
   float* dlogits;              // [N, E], nullable
-  double* part;                // seq_balance_partials(n_tok) pairs
+  double* part;                // two a block of 8 tokens
   int32_t* head;               // 4 int32: sequences that are not empty, their tokens, offsets that decrease
   int32_t* ticket;             // zero before the launch, left zero
   int32_t* status;
 };
-// Pairs of doubles of scratch (never more than the tokens).
-int64_t seq_balance_partials(int n_tok);
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st);
 
 // dlogits [N, E] fp32 as a sum of three bf16 terms [N, 3 * E8], E8 = E rounded up to 8, term i in the columns
@@ -33,8 +31,8 @@ cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st);
 inline int router_term_cols(int n_exp) { return (n_exp + 7) / 8 * 8; }
 cudaError_t launch_router_terms(const float* dl, int n_tok, int n_exp, void* terms, int32_t* dense, int32_t* slices,
                                 int n_slices, int slice_rows, cudaStream_t st);
-// dw[e, :] = dw_in[e, :] + the sum over the slices and the three terms of part[slice][term * E8 + e][d].
-cudaError_t launch_router_dw(const float* part, int n_slices, int n_exp, int d, const float* dw_in, float* dw,
-                             cudaStream_t st);
+// dw[e, :] = dw_in[e, :] + the sum over the slices and terms (1 or 3) of part[slice][term * E8 + e][d].
+cudaError_t launch_router_dw(const float* part, int n_slices, int terms, int n_exp, int d, const float* dw_in,
+                             float* dw, cudaStream_t st);
 
 }  // namespace moe

@@ -265,7 +265,7 @@ def test_dequantize_every_code_and_scale():
 
 
 GROUPS = [  # groups, rows, offsets
-    (1, 1, [0, 1]), (3, 130, [0, 0, 129, 130]), (4, 300, [5, 5, 150, 151, 290]), (2, 257, [0, 128, 257]),
+    (1, 1, [0, 1]), (1, 200, [17, 150]), (3, 130, [0, 0, 129, 130]), (4, 300, [5, 5, 150, 151, 290]), (2, 257, [0, 128, 257]),
     (16, 777, None), (64, 500, None), (2, 1300, [0, 700, 1300])]
 
 
