@@ -123,13 +123,10 @@ struct KParams {
   // written by build_group_maps_kernel before the launch; null with one group
   // (the whole-tensor maps end at the group's end already)
   const CUtensorMap* gmaps;
-  // Ragged K: A holds this many terms of a matrix side by side, term i in the
-  // columns from i * a_term_cols; every group's contraction runs over all of
-  // them against the same rows of B (0: one term).  Groups start at multiples
-  // of the k-block, so the whole-tensor maps serve them all.
-  int32_t a_terms;
+  // TERMS > 1, ragged K: term i of A in its columns from i * a_term_cols (ragged M: behind tmA[i]).
+  // Groups start at multiples of the k-block, so the whole-tensor maps serve them all
   int32_t a_term_cols;
-  int32_t out_wide;      // out0, out1, out2 (EPI_BF16_ADD: in0 too) start on 32 bytes
+  int32_t out_wide;      // out0, out1, out2 start on 32 bytes
   // Ragged M: offsets from outside the layer are cut to 0 .. check_rows and may
   // not decrease (DEV_BAD_OFFSETS; no tile then); range_out receives the first
   // and the last one as used.  0: not checked
@@ -188,8 +185,10 @@ __global__ void __launch_bounds__(1024) checked_group_maps_kernel(
 // offsets from global memory), and the room goes to 4 KB of fp32 staging per
 // epilogue warp: two 2 KB TMA-store buffers (one-SM form) or one 32 x 32 box
 // for plain stores (CTA-pair form)
+// TERMS: A is a sum of that many matrices; a stage holds a tile of each beside one of B
+// ADD: 8 KB per epilogue warp, the addend's and then the output's 32 rows x 128 columns, and a barrier each
 template <int BN, bool QUANT = false, bool PAIR = false, bool W8 = false, bool STG = false, int MAXG = kMaxGroups,
-          int MAXS = 6>
+          int MAXS = 6, bool ADD = false, int TERMS = 1>
 struct Cfg {
   // FP8 weights (W8): the B codes of a k-block (BN x 64 bytes) land in a
   // two-slot staging ring; converters write the bf16 B tile into the stage
@@ -211,17 +210,18 @@ struct Cfg {
   // bf16: PAIR = this CTA holds half of the B tile (the pair shares a 256-row tile)
   // k-block length: 128 rows for the bf16 ragged-K form on CTA pairs (eight
   // K=16 MMAs per stage barrier instead of four), 64 elsewhere
-  static constexpr int kKb = (MAXG == 0 && PAIR && !QUANT && !W8) ? BKR : BK;
+  static constexpr int kKb = (MAXG == 0 && PAIR && !QUANT && !W8 && TERMS == 1) ? BKR : BK;
   static constexpr int kABytesC = BM * kKb * 2;   // A bytes of a bf16 stage
   static constexpr int kStageBytes =
-      QUANT ? (kQAtoms + 1536 + 1023) / 1024 * 1024 : (BM + (PAIR ? BN / 2 : BN)) * kKb * 2;
+      QUANT ? (kQAtoms + 1536 + 1023) / 1024 * 1024 : (TERMS * BM + (PAIR ? BN / 2 : BN)) * kKb * 2;
   // shared memory left for the stages: 227 KB less the alignment slack, the
   // staging buffers, the barriers (at most MAXS stages) and the group tables
   static constexpr bool kWideStaging = STG && MAXG == 0;
-  static constexpr int kEpiWarpBytes = kWideStaging ? 4096 : 2048;
-  static constexpr int kEpiBytes = STG ? 8 * kEpiWarpBytes : 0;
+  static constexpr int kEpiWarpBytes = ADD ? 8192 : kWideStaging ? 4096 : 2048;
+  static constexpr int kEpiBytes = STG || ADD ? 8 * kEpiWarpBytes : 0;
+  static constexpr int kAddBars = ADD ? 8 : 0;
   static constexpr int kTableBytes = MAXG > 0 ? 2 * 4 * (MAXG + 1) : 0;
-  static constexpr int kStageBudget = 232448 - 1024 - kEpiBytes - (3 * MAXS + 2 * 2 + 5) * 8 - 16 -
+  static constexpr int kStageBudget = 232448 - 1024 - kEpiBytes - (3 * MAXS + 2 * 2 + 5 + kAddBars) * 8 - 16 -
                                       kTableBytes - kW8Slots * kW8SlotBytes;
   static constexpr int kStagesRaw = kStageBudget / kStageBytes;
   static constexpr int kStages = kStagesRaw > MAXS ? MAXS : kStagesRaw;
@@ -233,7 +233,8 @@ struct Cfg {
   static constexpr int kW8Off = kStages * kStageBytes;
   static constexpr int kEpiOff = kW8Off + kW8Slots * kW8SlotBytes;
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
-  static constexpr int kMiscOff = kBarOff + ((QUANT ? 3 : 2) * kStages + 2 * kW8Slots + 5) * 8;
+  static constexpr int kAddBarOff = kBarOff + ((QUANT ? 3 : 2) * kStages + 2 * kW8Slots + 5) * 8;
+  static constexpr int kMiscOff = kAddBarOff + kAddBars * 8;
   static constexpr int kOffOff = kMiscOff + 16;
   static constexpr int kMaxG = MAXG;
   static constexpr size_t smem_bytes(int groups) {
@@ -246,8 +247,9 @@ struct Cfg {
 
 // The configuration of each kernel form: the bf16 ragged-K (weight-gradient)
 // form keeps no group tables and has 4 KB of fp32 staging per epilogue warp.
-template <int BN, bool A_MN, int EPI, bool QUANT, bool PAIR, bool W8>
-using KernelCfg = Cfg<BN, QUANT, PAIR, W8, EPI == EPI_F32, (A_MN && !QUANT && !W8) ? 0 : kMaxGroups>;
+template <int BN, bool A_MN, int EPI, bool QUANT, bool PAIR, bool W8, int TERMS = 1>
+using KernelCfg = Cfg<BN, QUANT, PAIR, W8, EPI == EPI_F32, (A_MN && !QUANT && !W8) ? 0 : kMaxGroups, 6,
+                      EPI == EPI_BF16_ADD, TERMS>;
 
 struct Tile {
   int g, mt, nt;
@@ -287,7 +289,6 @@ __device__ __forceinline__ Tile decode_tile_rk(int tile, const KParams& p, int o
   t.k_rows = off1 - off0;
   t.rows_valid = min(BM, p.m_size - t.m0);
   t.num_kb = (t.k_rows + p.kblk - 1) / p.kblk;
-  if (p.a_terms > 1) t.num_kb *= p.a_terms;
   return t;
 }
 
@@ -426,19 +427,6 @@ __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8], b
                : "memory");
 }
 
-__device__ __forceinline__ void ld_global_32b(const void* p, uint32_t (&w)[8], bool wide) {
-  if (!wide) {
-    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    return;
-  }
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
-}
-
 // The kept codes of 32 columns of a1 and a3 of one row, and their scale bytes.
 struct KeptBlock {
   uint32_t a[8], b[8];
@@ -463,11 +451,15 @@ struct KeptBlock {
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
 // instruction, every lane of the producer warp taking four of the tile's
 // 128 rows; no permuted copy of the tokens is read.
-template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT, bool PAIR, bool W8 = false, bool GATHER = false>
+// TERMS (bf16, at most 2 with ragged M): every k-block multiplies that many tiles of A by one of B
+// into the same accumulator.
+template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT, bool PAIR, bool W8 = false, bool GATHER = false,
+          int TERMS = 1>
 __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads), 1)
     grouped_gemm_kernel(const __grid_constant__ KParams p) {
   static_assert(!GATHER || (!A_MN && !B_MN && !QUANT && !W8), "GATHER: K-major bf16 ragged-M forms");
-  using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8>;
+  static_assert(TERMS == 1 || (B_MN && !QUANT && !W8 && !GATHER), "TERMS: bf16 forms with MN-major B");
+  using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8, TERMS>;
   // bf16: the MN-major-A form is the ragged-K (weight-gradient) form.  MXFP8
   // operands are always K-major; A_MN then only selects the ragged-K form.
   constexpr bool RAGGED_K = A_MN;
@@ -519,6 +511,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * (kEpiThreads / 32));   // one arrival per epilogue warp
     }
     mbar_init(mma_done, 1);
+    for (int w = 0; w < C::kAddBars; ++w) mbar_init(reinterpret_cast<uint64_t*>(smem + C::kAddBarOff) + w, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -738,7 +731,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
           const uint32_t ph = (it / S) & 1u;
           if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s)) { ok = false; break; }
           uint8_t* sA = smem + s * C::kStageBytes;
-          uint8_t* sB = sA + (RAGGED_K ? C::kABytesC : kABytes);
+          uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
           if (W8) {
             // FP8 weights: A (bf16) straight into the stage; the B codes of the
             // k-block into a staging slot for the converters
@@ -781,26 +774,28 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               tensormap_acquire(mB);
               map_g = t.g;
             }
-            int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
-            int m0 = t.m0;
-            if (p.a_terms > 1) {
-              const int per = t.num_kb / p.a_terms, term = kb / per;
-              r -= term * per * C::kKb;
-              m0 += term * p.a_term_cols;
-            }
+            const int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
             if (PAIR) {
               // both CTAs' loads complete on the leader's barrier, armed by the leader
               const int n0 = t.nt * BN + (rank & 1) * (BN / 2);
               if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
               const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-              tma_load_2d_pair(sA, mA, bar, m0, r);
-              tma_load_2d_pair(sA + C::kKb * 128, mA, bar, m0 + 64, r);
+#pragma unroll
+              for (int i = 0; i < TERMS; ++i) {
+                const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
+                tma_load_2d_pair(sA + i * C::kABytesC, mA, bar, m0, r);
+                tma_load_2d_pair(sA + i * C::kABytesC + C::kKb * 128, mA, bar, m0 + 64, r);
+              }
 #pragma unroll
               for (int a = 0; a < BN / 128; ++a) tma_load_2d_pair(sB + a * C::kKb * 128, mB, bar, n0 + 64 * a, r);
             } else {
               mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-              tma_load_2d(sA, mA, &full[s], m0, r);
-              tma_load_2d(sA + 8192, mA, &full[s], m0 + 64, r);
+#pragma unroll
+              for (int i = 0; i < TERMS; ++i) {
+                const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
+                tma_load_2d(sA + i * C::kABytesC, mA, &full[s], m0, r);
+                tma_load_2d(sA + i * C::kABytesC + 8192, mA, &full[s], m0 + 64, r);
+              }
 #pragma unroll
               for (int a = 0; a < BN / 64; ++a) tma_load_2d(sB + a * 8192, mB, &full[s], t.nt * BN + 64 * a, r);
             }
@@ -810,9 +805,10 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
             // both CTAs' loads complete on the leader's barrier, armed by the leader
             if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
             const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-            const int src = (kb < p.kb0) ? 0 : 1;
+            const int src = (TERMS > 1 || kb < p.kb0) ? 0 : 1;
             const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
             tma_load_2d_pair(sA, &p.tmA[src], bar, k0, t.row0);
+            if (TERMS > 1) tma_load_2d_pair(sA + kABytes, &p.tmA[1], bar, k0, t.row0);
             if (!B_MN) {
               if (p.b_dual_n) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, t.nt * (BN / 2), t.g);  // W1 | W3 half
               else tma_load_3d_pair(sB, &p.tmB[src], bar, k0, t.nt * BN + rank * (BN / 2), t.g);
@@ -826,9 +822,10 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
           mbar_arrive_expect_tx(&full[s], C::kStageBytes);
           if (!RAGGED_K) {
             const int kbg = t.kbeg + kb;   // k-block within the whole contraction
-            const int src = (kbg < p.kb0) ? 0 : 1;
+            const int src = (TERMS > 1 || kbg < p.kb0) ? 0 : 1;
             const int k0 = (src == 0 ? kbg : kbg - p.kb0) * BK;
             tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
+            if (TERMS > 1) tma_load_2d(sA + kABytes, &p.tmA[1], &full[s], k0, t.row0);
             // B maps of the ragged-M form are always 3-D: {cols, rows, group}
             if (!B_MN) {
               if (p.b_dual_n) {
@@ -961,23 +958,27 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 300 + s)) { ok = false; break; }
         tc_fence_after();
         uint8_t* sA = smem + s * C::kStageBytes;
-        uint8_t* sB = sA + (RAGGED_K ? C::kABytesC : kABytes);
+        uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
         // Ragged K: rows past the group's end arrive as zeros (the per-group
         // maps end at the group's last row); K=16 steps holding none of the
         // group's rows are skipped.
         constexpr int KB = RAGGED_K ? C::kKb : BK;
         const int rv = t.k_rows - kb * KB;
-        const int nkk = (RAGGED_K && rv < KB && p.a_terms <= 1) ? (rv + 15) / 16 : KB / 16;
+        const int nkk = (RAGGED_K && rv < KB) ? (rv + 15) / 16 : KB / 16;
         if (lane == 0) {
-          const uint32_t a_base = smem_u32(sA);
           const uint32_t b_base = smem_u32(sB);
-          for (int kk = 0; kk < nkk; ++kk) {
-            const uint64_t ad = A_MN ? smem_desc_sw128(a_base + kk * 2048, KB * 128, 1024)
-                                     : smem_desc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 2048, KB * 128, 1024)
-                                     : smem_desc_sw128(b_base + kk * 32, 16, 1024);
-            if (PAIR) tc_mma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-            else tc_mma_bf16(d_tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int i = 0; i < TERMS; ++i) {
+            const uint32_t a_base = smem_u32(sA) + i * (RAGGED_K ? C::kABytesC : kABytes);
+            for (int kk = 0; kk < nkk; ++kk) {
+              const uint64_t ad = A_MN ? smem_desc_sw128(a_base + kk * 2048, KB * 128, 1024)
+                                       : smem_desc_sw128(a_base + kk * 32, 16, 1024);
+              const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 2048, KB * 128, 1024)
+                                       : smem_desc_sw128(b_base + kk * 32, 16, 1024);
+              const uint32_t acc = (kb > 0 || kk > 0 || i > 0) ? 1u : 0u;
+              if (PAIR) tc_mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
+              else tc_mma_bf16(d_tmem, ad, bd, idesc, acc);
+            }
           }
           if (PAIR) tc_commit_pair_mc(&empty[s], 3);
           else tc_commit(&empty[s]);
@@ -1135,23 +1136,25 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
     const int r = q * 32 + lane;
     uint32_t tcount = 0;
     uint32_t nstore = 0;   // TMA stores this warp has issued (fp32 staging)
-    // EPI_BF16_ADD: the addend's 128 columns of this thread's row of the tile at hand, 32 bytes a
-    // load; each is asked for as soon as the one of the tile before has been used
-    uint32_t add[EPI == EPI_BF16_ADD ? BN / 32 : 1][8];
-    auto load_add = [&](uint32_t (&v)[8], const Tile& t, int i) {
-      const int col = t.nt * BN + hf * (BN / 2) + 16 * i;
-      if (p.in0 && r < t.rows_valid && col < p.n_size)
-        ld_global_32b(static_cast<const __nv_bfloat16*>(p.in0) + static_cast<int64_t>(t.row0 + r) * p.ld_out + col, v,
-                      p.out_wide != 0);
+    // EPI_BF16_ADD: this warp's 32 rows of the addend come into its own buffer by TMA in boxes of 64
+    // columns, those of the next tile as soon as the output has left the buffer again
+    uint8_t* abuf = smem + C::kEpiOff + (warp - 2) * C::kEpiWarpBytes;
+    uint64_t* abar = reinterpret_cast<uint64_t*>(smem + C::kAddBarOff) + (warp - 2);
+    uint32_t asked = 0, got = 0;
+    auto box_col = [&](const Tile& t) { return t.nt * BN + (BN == 64 ? 0 : hf * (BN / 2)); };
+    auto boxes = [&](const Tile& t) {   // none past the output's rows or columns
+      if ((BN == 64 && hf != 0) || t.row0 + q * 32 >= p.c_rows) return 0;
+      return max(0, min(BN >= 256 ? 2 : 1, (p.n_size - box_col(t) + 63) / 64));
     };
-    if (EPI == EPI_BF16_ADD) {
-#pragma unroll
-      for (int i = 0; i < (EPI == EPI_BF16_ADD ? BN / 32 : 1); ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) add[i][j] = 0u;
-        if (unit0 < total_tiles) load_add(add[i], decode_tile<RAGGED_K, BN, PAIR>(unit0, p, s_off, s_pre, rank), i);
-      }
-    }
+    auto ask = [&](const Tile& t) {
+      const int n = boxes(t);
+      if (!p.in0 || n == 0) return;
+      ++asked;
+      if (lane != 0) return;
+      mbar_arrive_expect_tx(abar, n * 4096);
+      for (int b = 0; b < n; ++b) tma_load_2d(abuf + b * 4096, &p.tmAs[0], abar, box_col(t) + 64 * b, t.row0 + q * 32);
+    };
+    if (EPI == EPI_BF16_ADD && unit0 < total_tiles) ask(decode_tile<RAGGED_K, BN, PAIR>(unit0, p, s_off, s_pre, rank));
     for (int tile = unit0; tile < total_tiles; tile += ustride, ++tcount) {
       const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
       const uint32_t buf = tcount & 1u;
@@ -1518,26 +1521,43 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
           }
         }
       } else if (EPI == EPI_BF16_ADD) {
-        // out = bf16(acc + addend).  The addend came in ahead: a load in each 16-column turn cost its
-        // whole latency (4096 x 7168, E = 256: 56 us; all of a tile's loads before its wait: 37).
-        const int64_t grow = t.row0 + r;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out0) + grow * p.ld_out;
-        const bool more = tile + ustride < total_tiles;
-        const Tile next = decode_tile<RAGGED_K, BN, PAIR>(more ? tile + ustride : tile, p, s_off, s_pre, rank);
+        // out = bf16(acc + addend), in the buffer the addend came into (128-byte rows, swizzled: 16-byte
+        // chunk j of row r at chunk j ^ (r & 7)), from where TMA stores take whole rows of 64 columns.
+        // 4096 x 7168, E = 256: a global load and store of 32 bytes a row and turn took 56 us,
+        // the loads asked for a tile ahead 38.
+        const int nb = boxes(t);
+        if (p.in0 && nb > 0) {
+          if (!mbar_wait_bounded(abar, got & 1u, s_abort, p.status, 480)) break;
+          ++got;
+        }
+        for (int b = 0; b < nb; ++b) {
+          const uint32_t row = smem_u32(abuf + b * 4096 + lane * 128);
 #pragma unroll
-        for (int i = 0; i < (EPI == EPI_BF16_ADD ? BN / 32 : 1); ++i) {
-          const int c = hf * (BN / 2) + 16 * i;
-          const int col = t.nt * BN + c;
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tb + c, v);
-          tmem_wait_ld(v);
-          uint32_t w[8];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tb + (BN == 64 ? 0 : hf * (BN / 2)) + 64 * b + 16 * i, v);
+            uint32_t s0[4] = {0u, 0u, 0u, 0u}, s1[4] = {0u, 0u, 0u, 0u};
+            const uint32_t c0 = row + (((2 * i) ^ (lane & 7)) << 4), c1 = row + (((2 * i + 1) ^ (lane & 7)) << 4);
+            if (p.in0) {
+              ld_shared_v4(c0, s0[0], s0[1], s0[2], s0[3]);
+              ld_shared_v4(c1, s1[0], s1[1], s1[2], s1[3]);
+            }
+            tmem_wait_ld(v);
+            uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            w[j] = pack_bf16x2(__uint_as_float(v[2 * j]) + bf16lo(add[i][j]),
-                               __uint_as_float(v[2 * j + 1]) + bf16hi(add[i][j]));
-          if (row_ok && col < p.n_size) st_global_32b(dst + col, w, p.out_wide != 0);   // n_size: a multiple of 16
-          if (more) load_add(add[i], next, i);
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t sw = j < 4 ? s0[j] : s1[j - 4];
+              w[j] = pack_bf16x2(__uint_as_float(v[2 * j]) + bf16lo(sw), __uint_as_float(v[2 * j + 1]) + bf16hi(sw));
+            }
+            st_shared_v4(c0, w[0], w[1], w[2], w[3]);
+            st_shared_v4(c1, w[4], w[5], w[6], w[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && nb > 0) {
+          for (int b = 0; b < nb; ++b) tma_store_3d(&p.tmC, abuf + b * 4096, box_col(t) + 64 * b, t.row0 + q * 32, 0);
+          bulk_commit_group();
         }
       } else if (EPI == EPI_SWIGLU_FWD_C) {
         // h = silu(a1) * a3 in bf16, and a1, a3 kept in 8 bits for the backward: blocks of 32
@@ -1696,8 +1716,14 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         if (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[buf]), lead));
         else mbar_arrive(&tempty[buf]);
       }
+      if (EPI == EPI_BF16_ADD) {
+        if (lane == 0) bulk_wait_group_read0();   // the buffer is free again
+        __syncwarp();
+        if (tile + ustride < total_tiles) ask(decode_tile<RAGGED_K, BN, PAIR>(tile + ustride, p, s_off, s_pre, rank));
+      }
     }
-    if (EPI == EPI_F32 && lane == 0) bulk_wait_group0();   // every TMA store of this warp has landed
+    if (EPI == EPI_BF16_ADD && asked != got) mbar_wait_drain(abar, got & 1u);   // after a wait that ran out
+    if ((EPI == EPI_F32 || EPI == EPI_BF16_ADD) && lane == 0) bulk_wait_group0();   // every TMA store has landed
     __syncwarp();
   }
 
@@ -1792,12 +1818,12 @@ bool make_map_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* d
 }
 
 template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT = false, bool PAIR = false, bool W8 = false,
-          bool GATHER = false>
+          bool GATHER = false, int TERMS = 1>
 cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream, bool pdl = false) {
-  using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8>;
+  using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8, TERMS>;
   constexpr int CN = 2;   // CTAs per cluster (PAIR)
   const size_t smem = C::smem_bytes(kp.num_groups);
-  auto kern = grouped_gemm_kernel<BN, A_MN, B_MN, EPI, QUANT, PAIR, W8, GATHER>;
+  auto kern = grouped_gemm_kernel<BN, A_MN, B_MN, EPI, QUANT, PAIR, W8, GATHER, TERMS>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int max_units = 0;   // co-resident CTAs (or CTA pairs)
@@ -1911,8 +1937,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   kp.out4 = a.out4;
   kp.s_ld = a.s_ld;
   kp.out_wide = ((reinterpret_cast<uintptr_t>(a.out0) | reinterpret_cast<uintptr_t>(a.out1) |
-                  reinterpret_cast<uintptr_t>(a.out2) | (a.epi == EPI_BF16_ADD ? reinterpret_cast<uintptr_t>(a.in0) : 0)) &
-                 31u) == 0;
+                  reinterpret_cast<uintptr_t>(a.out2)) & 31u) == 0;
   kp.in0 = a.in0;
   kp.in1 = a.in1;
   kp.in2 = a.in2;
@@ -2112,8 +2137,12 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     kp.kb1 = (a.k1 + BK - 1) / BK;
     if (kp.kb0 <= 0) return cudaErrorInvalidValue;
     const int nsrc = kp.kb1 > 0 ? 2 : 1;
+    // EPI_BF16_ADD: two terms of A against one B
+    if ((a.epi == EPI_BF16_ADD) != (a.a_terms == 2) || (a.a_terms == 2 && (nsrc != 1 || !a.b_mn)))
+      return cudaErrorInvalidValue;
     for (int s = 0; s < nsrc; ++s) {
       if (!make_map(&kp.tmA[s], a.a[s], 64, BM, false)) return cudaErrorInvalidValue;
+      if (a.a_terms == 2 && !make_map(&kp.tmA[1], a.a[1], 64, BM, false)) return cudaErrorInvalidValue;
       if (!a.b_mn) {
         const int box_rows = (a.b_dual_n || pair) ? BN / 2 : BN;
         if (!make_map(&kp.tmB[s], a.b[s], 64, box_rows, true)) return cudaErrorInvalidValue;
@@ -2125,7 +2154,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
       if (a.b_mn || nsrc != 1 || !make_map(&kp.tmB[1], a.b[1], 64, BN / 2, true)) return cudaErrorInvalidValue;
     }
     if (nsrc == 1) {
-      kp.tmA[1] = kp.tmA[0];
+      if (a.a_terms != 2) kp.tmA[1] = kp.tmA[0];
       if (!a.b_dual_n) kp.tmB[1] = kp.tmB[0];
     }
     const int64_t ntiles = (a.n_size + kp.tile_n - 1) / kp.tile_n;
@@ -2139,13 +2168,13 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   } else {
     if (a.m_size <= 0) return cudaSuccess;
     // k-blocks of BKR rows on CTA pairs (the kernel form's k-block length)
-    const int kbr = pair ? BKR : BK;
+    const int kbr = pair && a.a_terms <= 1 ? BKR : BK;
     kp.kblk = kbr;
     if (!make_map(&kp.tmA[0], a.a[0], 64, kbr, false) || !make_map(&kp.tmB[0], a.b[0], 64, kbr, false))
       return cudaErrorInvalidValue;
     kp.tmA[1] = kp.tmA[0];
     kp.tmB[1] = kp.tmB[0];
-    kp.a_terms = a.a_terms;
+    if (a.a_terms > 1 && (a.a_terms != 3 || !a.aligned_groups)) return cudaErrorInvalidValue;
     kp.a_term_cols = a.a_term_cols;
     if (a.checked) {
       if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 || a.aligned_groups)
@@ -2184,6 +2213,19 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
                                 a.ld_out, gs, (BN / 2) % 32 == 0) ? 1 : 0;
     kp.c_rows = static_cast<int32_t>(m);
   }
+  if (a.epi == EPI_BF16_ADD) {
+    // the addend's and the output's boxes: 32 rows of 64 columns
+    Operand o;
+    o.ptr = a.out0;
+    o.rows = a.max_rows;
+    o.cols = a.n_size;
+    o.ld = a.ld_out;
+    o.group_stride = o.rows * o.ld;
+    if (a.num_groups != 1 || a.n_size % 64 || !make_map(&kp.tmC, o, 64, 32, true)) return cudaErrorInvalidValue;
+    o.ptr = a.in0;
+    if (a.in0 && !make_map(&kp.tmAs[0], o, 64, 32, false)) return cudaErrorInvalidValue;
+    kp.c_rows = static_cast<int32_t>(a.max_rows);
+  }
   if (kp.ksplit > 1 && !kp.c_tma) return cudaErrorInvalidValue;   // partials leave through the TMA stores
   const int64_t u = tiles_ub;
 
@@ -2217,14 +2259,17 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
         return pair ? launch_impl<256, false, true, EPI_SWIGLU_BWD_C, false, true>(kp, u, stream, a.pdl)
                     : launch_impl<256, false, true, EPI_SWIGLU_BWD_C>(kp, u, stream, a.pdl);
       case EPI_BF16_ADD:
-        if (BN == 64) return launch_impl<64, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
-        if (BN == 128) return launch_impl<128, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
-        return pair ? launch_impl<256, false, true, EPI_BF16_ADD, false, true>(kp, u, stream, a.pdl)
-                    : launch_impl<256, false, true, EPI_BF16_ADD>(kp, u, stream, a.pdl);
+        if (BN == 64) return launch_impl<64, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
+        if (BN == 128) return launch_impl<128, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
+        return pair ? launch_impl<256, false, true, EPI_BF16_ADD, false, true, false, false, 2>(kp, u, stream, a.pdl)
+                    : launch_impl<256, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
       default: return cudaErrorInvalidValue;
     }
   }
   if (a.a_mn && a.b_mn && a.epi == EPI_F32) {
+    if (a.a_terms == 3)
+      return pair ? launch_impl<256, true, true, EPI_F32, false, true, false, false, 3>(kp, u, stream, a.pdl)
+                  : launch_impl<256, true, true, EPI_F32, false, false, false, false, 3>(kp, u, stream, a.pdl);
     return pair ? launch_impl<256, true, true, EPI_F32, false, true>(kp, u, stream, a.pdl)
                 : launch_impl<256, true, true, EPI_F32>(kp, u, stream, a.pdl);
   }

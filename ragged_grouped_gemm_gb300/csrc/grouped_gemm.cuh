@@ -28,7 +28,8 @@ enum EpiKind : int {
                          // [rows, n], out2, out4 = their scales [n/32, s_ld]
   EPI_SWIGLU_BWD_C = 6,  // acc = dh; in0, in2 = kept codes of a1, a3, in1, in3 = their scales [n/32, s_ld], g = row
                          // weight -> out0 = da1, out1 = da3, out2 = g h (bf16), row_dot = partial sums of dh h
-  EPI_BF16_ADD = 7,      // out0[row, col] = bf16(acc + in0[row, col])  (in0 null: zero)
+  EPI_BF16_ADD = 7,      // out0[row, col] = bf16(acc + in0[row, col])  (in0 null: zero); one group, n % 64 == 0, two
+                         // terms of A
 };
 
 // Column slices of GemmArgs::row_dot: two per tile of block_n columns.
@@ -111,11 +112,12 @@ struct GemmArgs {
   // loaded by TMA tile::gather4 instead of a permuted copy
   const int32_t* a_gather = nullptr;
   int gather_k = 0;
-  // Ragged K (bf16): A holds a_terms terms of a matrix side by side (a_term_cols
-  // columns each), all contracted with the same rows of B.  aligned_groups: every
-  // group starts at a multiple of 128 rows and the last ends with the rows, so no
-  // per-group maps are needed (required with terms)
-  int a_terms = 0;
+  // A as a sum of a_terms matrices, all multiplied by the same tiles of B.  3
+  // (ragged K, aligned_groups): side by side in a[0], a_term_cols columns each.  2
+  // (EPI_BF16_ADD): a[0] and a[1].  aligned_groups (ragged K, bf16): every group
+  // starts at a multiple of 128 rows and the last ends with the rows, so that no
+  // per-group maps are needed
+  int a_terms = 1;
   int a_term_cols = 0;
   bool aligned_groups = false;
   // Offsets from outside the layer: cut to 0 .. max_rows and refused where they

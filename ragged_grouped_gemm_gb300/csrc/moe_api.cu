@@ -67,8 +67,8 @@ struct WsLayout {
 
 // The dense router gradient's weight product contracts over the tokens, dlogits being three bf16
 // terms of E8 columns.  Up to 128 columns in all the terms are the rows of one tile (MMA time does
-// not matter there, x is read once); more: one tile of E8 rows whose contraction runs over the three
-// terms in turn, so that a partial product is a third as large and no tile mixes terms.  The tokens
+// not matter there, x is read once); more: one tile of E8 rows, every tile of x multiplied by the
+// three terms in turn, so that a partial product is a third as large and no tile mixes terms.  The tokens
 // are cut into runs, the groups of one ragged launch, to fill the SMs: what counts is full waves
 // against the traffic of the partial products.
 struct RouterPlan {
@@ -1411,7 +1411,7 @@ moe_status_t moe_balance_loss(const moe_desc_t* d, const float* logits, const in
   a.counts = counts;
   a.loss = loss;
   a.dlogits = dlogits;
-  a.part = at<double>(ws, L.gpart);   // at most N pairs; the region holds 16 N E bytes
+  a.part = at<float4>(ws, L.gpart);   // at most N; the region holds 16 N E bytes
   a.head = at<int32_t>(ws, L.aux);
   a.status = at<int32_t>(ws, L.status);
   a.ticket = a.status + kBalanceTicketWord;
@@ -1466,16 +1466,17 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
   w.group_stride_out = static_cast<int64_t>(plan.m) * D;
   MOE_CUDA(gemm(moe::TIMING_WGRAD, w, st));
   MOE_CUDA(moe::launch_router_dw(part, plan.slices, plan.packed ? 3 : 1, E, D, dw_in, dw_gate, st));
-  // dx: the first two terms against W_g, one contraction source each
+  // dx: the first two terms against W_g
   GemmArgs g;
   g.epi = moe::EPI_BF16_ADD;
   g.b_mn = true;
+  g.a_terms = 2;
   for (int i = 0; i < 2; ++i) {
     g.a[i] = act(terms + static_cast<size_t>(i) * e8 * 2, N, e8);
     g.a[i].ld = 3 * e8;
-    g.b[i] = wstack(w_gate, 1, E, D);
   }
-  g.k0 = g.k1 = e8;
+  g.b[0] = wstack(w_gate, 1, E, D);
+  g.k0 = e8;
   g.offsets = dense;
   g.num_groups = 1;
   g.max_rows = N;

@@ -40,25 +40,25 @@ __device__ __forceinline__ int seq_at(const int32_t* __restrict__ off, int i, in
   return min(max(__ldg(off + i), 0), n);
 }
 
-// counts[s][e] of one sequence by a cluster of C blocks: each counts its run of
-// the sequence's indices, one histogram a warp (few experts meet in one word
-// otherwise), and the blocks' sums are joined through the cluster's shared
-// memory, so no count is zeroed first or added by atomics in global memory.
-// The last cluster counts the sequences and their tokens instead.
-template <int C>
-__global__ void __launch_bounds__(kThreads) seq_counts_kernel(int n_tok, int E, int K, int S,
-                                                              const int32_t* __restrict__ idx,
-                                                              const int32_t* __restrict__ off,
-                                                              int32_t* __restrict__ counts, int32_t* __restrict__ head,
-                                                              int32_t* status) {
-  extern __shared__ int s_hist[];   // [kWarps][E]
+// counts[s][e] of one sequence by one block, or by a cluster of C: each counts its
+// run of the sequence's indices in nh histograms (its warps in turn; few experts
+// meet in one word otherwise), and the blocks' sums are joined through the
+// cluster's shared memory, so no count is zeroed first or added by atomics in
+// global memory.  The last block or cluster counts the sequences and their tokens.
+template <int C, int T>
+__global__ void __launch_bounds__(T) seq_counts_kernel(int n_tok, int E, int K, int S, int nh,
+                                                       const int32_t* __restrict__ idx,
+                                                       const int32_t* __restrict__ off,
+                                                       int32_t* __restrict__ counts, int32_t* __restrict__ head,
+                                                       int32_t* status) {
+  extern __shared__ int s_hist[];   // [nh][E]
   __shared__ int s_sum[3];
   __shared__ int s_bad;
   const int s = blockIdx.x / C, rank = blockIdx.x % C;
   const int warp = threadIdx.x >> 5;
   pdl_trigger();
   if (s < S)
-    for (int i = threadIdx.x; i < kWarps * E; i += kThreads) s_hist[i] = 0;
+    for (int i = threadIdx.x; i < nh * E; i += T) s_hist[i] = 0;
   if (threadIdx.x < 3) s_sum[threadIdx.x] = 0;
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) seq_counts_kernel(int n_tok, int E, 
   if (s == S) {
     if (rank != 0) return;   // nobody of this cluster meets at a barrier
     int full = 0, used = 0, less = 0, out = 0;
-    for (int i = threadIdx.x; i < S; i += kThreads) {
+    for (int i = threadIdx.x; i < S; i += T) {
       const int a = off[i], b = off[i + 1];
       const int len = seq_at(off, i + 1, n_tok) - seq_at(off, i, n_tok);
       full += len > 0;
@@ -87,37 +87,34 @@ __global__ void __launch_bounds__(kThreads) seq_counts_kernel(int n_tok, int E, 
   const int64_t n = max(static_cast<int64_t>(seq_at(off, s + 1, n_tok)) * K - lo, int64_t{0});
   const int64_t per = (n + C - 1) / C;
   const int64_t a = lo + min(n, per * rank), b = lo + min(n, per * (rank + 1));
-  int* mine = s_hist + warp * E;
+  int* mine = s_hist + (warp & (nh - 1)) * E;
   bool bad = false;
-  for (int64_t i = a + threadIdx.x; i < b; i += 8 * kThreads) {
+  for (int64_t i = a + threadIdx.x; i < b; i += 8 * T) {
     int e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = i + j * kThreads < b ? __ldg(idx + i + j * kThreads) : E;
+    for (int j = 0; j < 8; ++j) e[j] = i + j * T < b ? __ldg(idx + i + j * T) : E;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (e[j] >= 0 && e[j] < E) atomicAdd(mine + e[j], 1);
-      else bad |= i + j * kThreads < b;
+      else bad |= i + j * T < b;
     }
   }
   if (bad) s_bad = 1;
   __syncthreads();
   if (threadIdx.x == 0 && s_bad) atomicOr(status, DEV_BAD_INDEX);
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    int v = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_hist[w * E + e];
-    s_hist[e] = v;   // row 0, read above by this thread alone
-  }
   int32_t* dst = counts + static_cast<int64_t>(s) * E;
-  if (C == 1) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) dst[e] = s_hist[e];
-    return;
+  for (int e = threadIdx.x; e < E; e += T) {
+    int v = 0;
+#pragma unroll 8
+    for (int w = 0; w < nh; ++w) v += s_hist[w * E + e];
+    if (C == 1) dst[e] = v;
+    else s_hist[e] = v;   // row 0, read above by this thread alone
   }
+  if (C == 1) return;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
   const int eper = (E + C - 1) / C;
-  for (int e = rank * eper + threadIdx.x; e < min(E, (rank + 1) * eper); e += kThreads) {
+  for (int e = rank * eper + threadIdx.x; e < min(E, (rank + 1) * eper); e += T) {
     int v = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) v += cl.map_shared_rank(s_hist, r)[e];
@@ -145,24 +142,46 @@ struct RowsParams {
   const int32_t* head;
   float* dl;
   float* loss;
-  double* part;
+  float4* part;
   int32_t* ticket;
   int32_t* counts_out;
   float coef, z_coef;
-  int n_tok, E, gate, S, per;
+  int n_tok, E, S, per;
 };
 
 // A warp a token, its experts over the lanes (NPER registers), tokens of a
 // warp consecutive so that a sequence's f stays in registers from one to the
-// next.  Each block's sums leave as two doubles, and the last block to finish
-// adds them in a fixed order: equal calls give equal bits.
-// acc += v with what the addition lost kept in acc.y (a warp's tokens add up in 32 bits; 64-bit additions by every
-// warp took 4 of 12 us).
-__device__ __forceinline__ void add_kept(float2& acc, float v) {
+// next.  Each block's sums leave as two numbers with their rests, and the last
+// block to finish adds them in a fixed order: equal calls give equal bits.
+// acc += v with what the addition lost kept in acc.y: 48 bits from 32-bit additions (64-bit ones, by every warp and
+// then in a tree of the last block, took 9 of 21 us).  An infinite or NaN sum has no rest.
+__device__ __forceinline__ void add_kept(float2& acc, float v, float rest = 0.0f) {
   const float s = acc.x + v;
   const float b = s - acc.x;
-  acc.y += (acc.x - (s - b)) + (v - b);
+  const float e = (acc.x - (s - b)) + (v - b);
+  acc.y = isfinite(s) ? acc.y + rest + e : 0.0f;
   acc.x = s;
+}
+
+// The warps' sums (of lane 0) added in warp order by thread 0.
+__device__ __forceinline__ void block_sum(float2& bal, float2& zz, float4* s_red, int warp, int lane) {
+  __syncthreads();
+  if (lane == 0) s_red[warp] = make_float4(bal.x, bal.y, zz.x, zz.y);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 v = s_red[w];
+    add_kept(bal, v.x, v.y);
+    add_kept(zz, v.z, v.w);
+  }
+}
+
+// 1 / x to the unit's one ulp, for normal x and 1 / x.
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Resident blocks an SM by the registers a row takes: all blocks run at once, so that the look-up of a warp's
@@ -207,9 +226,9 @@ __device__ __forceinline__ void store_row(float* __restrict__ row, int E, int la
   }
 }
 
-template <int NPER, int VEC>
+template <int NPER, int VEC, int GATE>
 __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(const RowsParams p) {
-  __shared__ double s_red[2][kThreads];
+  __shared__ float4 s_red[kWarps];
   __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.E, N = p.n_tok;
@@ -284,11 +303,11 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
     for (int j = 0; j < NPER; ++j) {
       q[j] = expf(l[j]);
       z += q[j];
-      if (p.gate == 0) {
+      if (GATE == 0) {
         fs = fmaf(f[j], q[j], fs);
       } else {
         // sigmoid = v / (1 + v) and its slope v / (1 + v)^2 for v = e^l: the softmax's exponential serves both
-        const float r = __fdividef(1.0f, 1.0f + q[j]);
+        const float r = rcp_fast(1.0f + q[j]);
         const float sg = q[j] * r;
         sum += sg;
         fs = fmaf(f[j], sg, fs);
@@ -297,15 +316,15 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
     }
     z = warp_add(z);
     fs = warp_add(fs);
-    if (p.gate != 0) sum = warp_add(sum);
+    if (GATE != 0) sum = warp_add(sum);
     float invz, invq;
     // Exponentials of the logits as they are, without the largest taken off: right while their sum is neither near the
     // end of fp32's range (every logit is below 78 then, 1 + v is finite) nor so small that terms that matter were
     // lost (the largest is above -28 then, what e^l loses below -87 is 1e-25 of it).  Else row by row the long way.
     if (z < 1e34f && z > 1e-9f) {
-      invz = 1.0f / z;
+      invz = rcp_fast(z);
       lse = logf(z);
-      invq = p.gate == 0 ? invz : 1.0f / sum;
+      invq = GATE == 0 ? invz : rcp_fast(sum);
       inner = fs * invq;
     } else {
       float m = l[0];
@@ -324,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
         q[j] = expf(l[j] - m);
         z += q[j];
         float d = q[j];
-        if (p.gate != 0) {
+        if (GATE != 0) {
           const float v = expf(-fabsf(l[j]));   // sigmoid(|l|) = 1 / (1 + v), the other side v / (1 + v)
           const float big = 1.0f / (1.0f + v), small = v * big;
           d = l[j] > 0.0f ? big : small;
@@ -340,62 +359,60 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
       fs = warp_add(fs);
       invz = z != 0.0f ? 1.0f / z : 0.0f;
       lse = z != 0.0f ? m + logf(z) : 0.0f;
-      invq = p.gate == 0 ? invz : sum != 0.0f ? 1.0f / sum : 0.0f;
+      invq = GATE == 0 ? invz : sum != 0.0f ? 1.0f / sum : 0.0f;
       inner = fs * invq;
     }
     if (p.dl) {
       const float g1 = factor * invq * up, g2 = 2.0f * zf * lse * invz * up;
 #pragma unroll
       for (int j = 0; j < NPER; ++j)
-        l[j] = p.gate == 0 ? q[j] * fmaf(g1, f[j] - inner, g2) : fmaf(g1 * w[j], f[j] - inner, g2 * q[j]);
+        l[j] = GATE == 0 ? q[j] * fmaf(g1, f[j] - inner, g2) : fmaf(g1 * w[j], f[j] - inner, g2 * q[j]);
       store_row<NPER, VEC>(p.dl + row, E, lane, l);
     }
     add_kept(bal, factor * inner);
     if (p.z_coef != 0.0f) add_kept(zz, lse * lse);   // a row of the type's lowest value is infinite here
   }
-  if (lane == 0) {
-    s_red[0][warp] = static_cast<double>(bal.x) + (isfinite(bal.x) ? bal.y : 0.0f);
-    s_red[1][warp] = static_cast<double>(zz.x) + (isfinite(zz.x) ? zz.y : 0.0f);
-  }
-  __syncthreads();
+  block_sum(bal, zz, s_red, warp, lane);
   if (threadIdx.x == 0) {
-    double a = 0.0, b = 0.0;
-    for (int w = 0; w < kWarps; ++w) {
-      a += s_red[0][w];
-      b += s_red[1][w];
-    }
-    p.part[2 * blockIdx.x] = a;
-    p.part[2 * blockIdx.x + 1] = b;
+    p.part[blockIdx.x] = make_float4(bal.x, bal.y, zz.x, zz.y);
     __threadfence();
     s_last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  double a = 0.0, b = 0.0;
+  bal = zz = make_float2(0.0f, 0.0f);
   for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kThreads) {
-    a += __ldcg(p.part + 2 * i);
-    b += __ldcg(p.part + 2 * i + 1);
+    const float4 v = __ldcg(p.part + i);
+    add_kept(bal, v.x, v.y);
+    add_kept(zz, v.z, v.w);
   }
-  s_red[0][threadIdx.x] = a;
-  s_red[1][threadIdx.x] = b;
-  __syncthreads();
-  for (int n = kThreads / 2; n > 0; n >>= 1) {
-    if (threadIdx.x < n) {
-      s_red[0][threadIdx.x] += s_red[0][threadIdx.x + n];
-      s_red[1][threadIdx.x] += s_red[1][threadIdx.x + n];
-    }
-    __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, bal.x, o), __shfl_xor_sync(0xffffffffu, bal.y, o),
+                                 __shfl_xor_sync(0xffffffffu, zz.x, o), __shfl_xor_sync(0xffffffffu, zz.y, o));
+    add_kept(bal, v.x, v.y);
+    add_kept(zz, v.z, v.w);
   }
+  block_sum(bal, zz, s_red, warp, lane);
   if (threadIdx.x == 0) {
-    p.loss[0] = static_cast<float>(s_red[0][0]);
-    p.loss[1] = used > 0 ? static_cast<float>(s_red[1][0] * (static_cast<double>(p.z_coef) / used)) : 0.0f;
+    p.loss[0] = bal.x + bal.y;
+    p.loss[1] = p.z_coef != 0.0f ? (zz.x + zz.y) * zf : 0.0f;
     *p.ticket = 0;
   }
 }
 
 int row_blocks(int n_exp) {
   return n_exp <= 128 ? kRowBlocks<4> : n_exp <= 256 ? kRowBlocks<8> : n_exp <= 512 ? kRowBlocks<16> : kRowBlocks<32>;
+}
+template <int GATE>
+auto rows_kernel(int n_exp, bool vec) {
+  return n_exp <= 32 ? seq_rows_kernel<1, 1, GATE>
+         : n_exp <= 64 ? seq_rows_kernel<2, 1, GATE>
+         : n_exp <= 128 ? (vec ? seq_rows_kernel<4, 4, GATE> : seq_rows_kernel<4, 1, GATE>)
+         : n_exp <= 256 ? (vec ? seq_rows_kernel<8, 4, GATE> : seq_rows_kernel<8, 1, GATE>)
+         : n_exp <= 512 ? (vec ? seq_rows_kernel<16, 4, GATE> : seq_rows_kernel<16, 1, GATE>)
+                        : (vec ? seq_rows_kernel<32, 4, GATE> : seq_rows_kernel<32, 1, GATE>);
 }
 // Blocks of the rows kernel: a warp a token, no more than are resident.
 int rows_grid(int n_tok, int n_exp) {
@@ -478,18 +495,24 @@ __global__ void __launch_bounds__(256) router_dw_kernel(const V* __restrict__ pa
 
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   if (a.n_tok < 1 || a.n_exp < 1 || a.n_exp > 1024 || a.n_seq < 1) return cudaErrorInvalidValue;
-  // A cluster of eight blocks a sequence where one block's share of the indices would be long
-  // (16384 tokens, top 8, 8 sequences: 16384 indices a sequence), one block where they are few.
+  // One block counts a sequence of up to about 8192 indices in one turn of its 1024 threads; longer
+  // ones, on average, take a cluster of eight (16384 of them: 12 thousand cycles in one block, 9 in eight).
   const int64_t copies = static_cast<int64_t>(a.n_tok) * a.top_k;
-  const bool wide = copies >= 4096 && a.n_seq <= 4096;
-  const size_t smem = static_cast<size_t>(kWarps) * a.n_exp * sizeof(int);
   cudaError_t e;
-  if (wide)
-    e = launch_pdl<8>(seq_counts_kernel<8>, static_cast<unsigned>(a.n_seq + 1) * 8, kThreads, smem, st, a.n_tok,
-                      a.n_exp, a.top_k, a.n_seq, a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
-  else
-    e = launch_pdl(seq_counts_kernel<1>, static_cast<unsigned>(a.n_seq + 1), kThreads, smem, st, a.n_tok, a.n_exp,
-                   a.top_k, a.n_seq, a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  if (copies / a.n_seq > 8192) {
+    e = launch_pdl<8>(seq_counts_kernel<8, 256>, static_cast<unsigned>(a.n_seq + 1) * 8, 256,
+                      8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
+                      a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  } else if (copies / a.n_seq > 512 || copies > 32768) {   // lengths may be uneven: one sequence may hold most
+    const int nh = a.n_exp <= 256 ? 32 : 8;
+    e = launch_pdl(seq_counts_kernel<1, 1024>, static_cast<unsigned>(a.n_seq + 1), 1024,
+                   nh * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, nh,
+                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  } else {
+    e = launch_pdl(seq_counts_kernel<1, 256>, static_cast<unsigned>(a.n_seq + 1), 256,
+                   8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
+                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  }
   if (e != cudaSuccess) return e;
   const int grid = rows_grid(a.n_tok, a.n_exp);
   RowsParams p;
@@ -507,19 +530,13 @@ cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   p.z_coef = a.z_coef;
   p.n_tok = a.n_tok;
   p.E = a.n_exp;
-  p.gate = a.gate;
   p.S = a.n_seq;
   p.per = static_cast<int>((static_cast<int64_t>(a.n_tok) + static_cast<int64_t>(grid) * kWarps - 1) /
                            (static_cast<int64_t>(grid) * kWarps));
   // 16-byte words above 64 experts (below, lanes would idle), where every row starts on one
   const bool vec = a.n_exp > 64 && a.n_exp % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) |
                                                         reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0;
-  auto kern = a.n_exp <= 32 ? seq_rows_kernel<1, 1>
-              : a.n_exp <= 64 ? seq_rows_kernel<2, 1>
-              : a.n_exp <= 128 ? (vec ? seq_rows_kernel<4, 4> : seq_rows_kernel<4, 1>)
-              : a.n_exp <= 256 ? (vec ? seq_rows_kernel<8, 4> : seq_rows_kernel<8, 1>)
-              : a.n_exp <= 512 ? (vec ? seq_rows_kernel<16, 4> : seq_rows_kernel<16, 1>)
-                               : (vec ? seq_rows_kernel<32, 4> : seq_rows_kernel<32, 1>);
+  auto kern = a.gate == 0 ? rows_kernel<0>(a.n_exp, vec) : rows_kernel<1>(a.n_exp, vec);
   return launch_pdl(kern, static_cast<unsigned>(grid), kThreads, 0, st, p);
 }
 

@@ -18,7 +18,7 @@ struct SeqBalanceArgs {
   int32_t* counts;             // [S, E]
   float* loss;                 // [2]
   float* dlogits;              // [N, E], nullable
-  double* part;                // two a block of 8 tokens
+  float4* part;                // one a block of 8 tokens, 16-byte aligned
   int32_t* head;               // 4 int32: sequences that are not empty, their tokens, offsets that decrease
   int32_t* ticket;             // zero before the launch, left zero
   int32_t* status;
