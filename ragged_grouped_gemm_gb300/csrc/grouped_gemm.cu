@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(1024) checked_group_maps_kernel(
 // epilogue warp: two 2 KB TMA-store buffers (one-SM form) or one 32 x 32 box
 // for plain stores (CTA-pair form)
 // TERMS: A is a sum of that many matrices; a stage holds a tile of each beside one of B
-// ADD: 8 KB per epilogue warp, the addend's and then the output's 32 rows x 128 columns, and a barrier each
+// ADD: 8 KB per epilogue warp for the addend's and then the output's 32 rows of 128 columns (or two buffers of 64),
+// and a barrier a buffer
 template <int BN, bool QUANT = false, bool PAIR = false, bool W8 = false, bool STG = false, int MAXG = kMaxGroups,
           int MAXS = 6, bool ADD = false, int TERMS = 1>
 struct Cfg {
@@ -219,7 +220,8 @@ struct Cfg {
   static constexpr bool kWideStaging = STG && MAXG == 0;
   static constexpr int kEpiWarpBytes = ADD ? 8192 : kWideStaging ? 4096 : 2048;
   static constexpr int kEpiBytes = STG || ADD ? 8 * kEpiWarpBytes : 0;
-  static constexpr int kAddBars = ADD ? 8 : 0;
+  static constexpr int kAddBufs = ADD ? (BN >= 256 ? 1 : 2) : 0;   // buffers a warp
+  static constexpr int kAddBars = 8 * kAddBufs;
   static constexpr int kTableBytes = MAXG > 0 ? 2 * 4 * (MAXG + 1) : 0;
   static constexpr int kStageBudget = 232448 - 1024 - kEpiBytes - (3 * MAXS + 2 * 2 + 5 + kAddBars) * 8 - 16 -
                                       kTableBytes - kW8Slots * kW8SlotBytes;
@@ -1137,24 +1139,29 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
     uint32_t tcount = 0;
     uint32_t nstore = 0;   // TMA stores this warp has issued (fp32 staging)
     // EPI_BF16_ADD: this warp's 32 rows of the addend come into its own buffer by TMA in boxes of 64
-    // columns, those of the next tile as soon as the output has left the buffer again
+    // columns, those of the next tile as soon as an output has left a buffer again: with one buffer
+    // (256-column tiles, the warp's 128 columns) at the tile's end, with two at its start
+    constexpr int AB = C::kAddBufs == 2 ? 2 : 1;
     uint8_t* abuf = smem + C::kEpiOff + (warp - 2) * C::kEpiWarpBytes;
-    uint64_t* abar = reinterpret_cast<uint64_t*>(smem + C::kAddBarOff) + (warp - 2);
-    uint32_t asked = 0, got = 0;
+    uint64_t* abar = reinterpret_cast<uint64_t*>(smem + C::kAddBarOff) + (warp - 2) * AB;
+    uint32_t asked = 0, got = 0;   // loads asked for and met; load i is in buffer i % AB
     auto box_col = [&](const Tile& t) { return t.nt * BN + (BN == 64 ? 0 : hf * (BN / 2)); };
     auto boxes = [&](const Tile& t) {   // none past the output's rows or columns
       if ((BN == 64 && hf != 0) || t.row0 + q * 32 >= p.c_rows) return 0;
       return max(0, min(BN >= 256 ? 2 : 1, (p.n_size - box_col(t) + 63) / 64));
     };
-    auto ask = [&](const Tile& t) {
+    auto ask = [&](int tile) {
+      if (tile >= total_tiles) return;
+      const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
       const int n = boxes(t);
-      if (!p.in0 || n == 0) return;
-      ++asked;
-      if (lane != 0) return;
-      mbar_arrive_expect_tx(abar, n * 4096);
-      for (int b = 0; b < n; ++b) tma_load_2d(abuf + b * 4096, &p.tmAs[0], abar, box_col(t) + 64 * b, t.row0 + q * 32);
+      if (n == 0) return;
+      const uint32_t b = asked++ % AB;
+      if (lane != 0 || !p.in0) return;
+      mbar_arrive_expect_tx(abar + b, n * 4096);
+      for (int i = 0; i < n; ++i)
+        tma_load_2d(abuf + (AB * i + b) * 4096, &p.tmAs[0], abar + b, box_col(t) + 64 * i, t.row0 + q * 32);
     };
-    if (EPI == EPI_BF16_ADD && unit0 < total_tiles) ask(decode_tile<RAGGED_K, BN, PAIR>(unit0, p, s_off, s_pre, rank));
+    if (EPI == EPI_BF16_ADD) ask(unit0);
     for (int tile = unit0; tile < total_tiles; tile += ustride, ++tcount) {
       const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
       const uint32_t buf = tcount & 1u;
@@ -1526,12 +1533,18 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         // 4096 x 7168, E = 256: a global load and store of 32 bytes a row and turn took 56 us,
         // the loads asked for a tile ahead 38.
         const int nb = boxes(t);
-        if (p.in0 && nb > 0) {
-          if (!mbar_wait_bounded(abar, got & 1u, s_abort, p.status, 480)) break;
+        if (AB == 2) {   // the other buffer's output, of the tile before, has been read
+          if (lane == 0) bulk_wait_group_read0();
+          __syncwarp();
+          ask(tile + ustride);
+        }
+        uint8_t* mine = abuf + (got % AB) * 4096;
+        if (nb > 0) {
+          if (p.in0 && !mbar_wait_bounded(abar + got % AB, (got / AB) & 1u, s_abort, p.status, 480)) break;
           ++got;
         }
         for (int b = 0; b < nb; ++b) {
-          const uint32_t row = smem_u32(abuf + b * 4096 + lane * 128);
+          const uint32_t row = smem_u32(mine + b * 4096 + lane * 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t v[16];
@@ -1556,7 +1569,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && nb > 0) {
-          for (int b = 0; b < nb; ++b) tma_store_3d(&p.tmC, abuf + b * 4096, box_col(t) + 64 * b, t.row0 + q * 32, 0);
+          for (int b = 0; b < nb; ++b) tma_store_3d(&p.tmC, mine + b * 4096, box_col(t) + 64 * b, t.row0 + q * 32, 0);
           bulk_commit_group();
         }
       } else if (EPI == EPI_SWIGLU_FWD_C) {
@@ -1716,13 +1729,15 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         if (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[buf]), lead));
         else mbar_arrive(&tempty[buf]);
       }
-      if (EPI == EPI_BF16_ADD) {
+      if (EPI == EPI_BF16_ADD && AB == 1) {
         if (lane == 0) bulk_wait_group_read0();   // the buffer is free again
         __syncwarp();
-        if (tile + ustride < total_tiles) ask(decode_tile<RAGGED_K, BN, PAIR>(tile + ustride, p, s_off, s_pre, rank));
+        ask(tile + ustride);
       }
     }
-    if (EPI == EPI_BF16_ADD && asked != got) mbar_wait_drain(abar, got & 1u);   // after a wait that ran out
+    // after a wait that ran out: the loads asked for have landed before the block leaves
+    if (EPI == EPI_BF16_ADD && p.in0)
+      for (; got != asked; ++got) mbar_wait_drain(abar + got % AB, (got / AB) & 1u);
     if ((EPI == EPI_F32 || EPI == EPI_BF16_ADD) && lane == 0) bulk_wait_group0();   // every TMA store has landed
     __syncwarp();
   }
@@ -2262,7 +2277,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
         if (BN == 64) return launch_impl<64, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
         if (BN == 128) return launch_impl<128, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
         return pair ? launch_impl<256, false, true, EPI_BF16_ADD, false, true, false, false, 2>(kp, u, stream, a.pdl)
-                    : launch_impl<256, false, true, EPI_BF16_ADD, false, false, false, false, 2>(kp, u, stream, a.pdl);
+                    : cudaErrorInvalidValue;
       default: return cudaErrorInvalidValue;
     }
   }
