@@ -31,6 +31,11 @@
 // rank 0's accumulator-free barrier.  TMEM is allocated and freed by both
 // CTAs together, between cluster barriers.
 //
+// Backward from kept activations (EPI_SWIGLU_BWD_C): 384 threads, the epilogue in
+// warps 4..11 with registers from the first warpgroup.  A contraction is cut into
+// chunks of about 13 k-blocks, each an accumulator of its own that the epilogue
+// warps add to sums in their registers.
+//
 // fp32 outputs of the ragged-M forms leave through TMA tensor stores: each
 // epilogue warp stages 16 rows x 32 columns (whole 128-byte rows) at a time
 // in 2 KB of shared memory, or 32 x 16 when a tile's column halves are 16
@@ -67,7 +72,16 @@ constexpr int BKR = 128;   // k-block rows of the bf16 weight gradients on CTA p
 constexpr int kThreads = 320;        // producer, MMA, 8 epilogue warps
 constexpr int kThreadsQ = 448;       // + 4 scale-factor warps (MXFP8 operands)
 constexpr int kThreadsW8 = 576;      // + 8 converter warps (FP8 weights)
+constexpr int kThreadsC = 384;       // CHUNKED: three warpgroups, the epilogue in two of them
 constexpr int kConvWarps = 8;
+constexpr int kChunk = 13;           // k-blocks of 64 elements a chunk, about (CHUNKED)
+// CHUNKED on 256-column tiles: registers a thread at launch, of the first warpgroup and of the epilogue's
+constexpr int kRegsLaunch = 168, kRegsFirst = 40, kRegsEpi = 232;
+static_assert(128 * kRegsFirst + 256 * kRegsEpi <= kThreadsC * kRegsLaunch, "more registers than the block has");
+// Threads of a kernel form.
+constexpr int threads_of(int epi, bool quant, bool w8) {
+  return quant ? kThreadsQ : w8 ? kThreadsW8 : epi == EPI_SWIGLU_BWD_C ? kThreadsC : kThreads;
+}
 constexpr int kEpiThreads = 256;
 constexpr int kSfWarps = 4;
 
@@ -348,6 +362,14 @@ __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w <
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float sigmoidf_fast(float a) { return 1.0f / (1.0f + __expf(-a)); }
 
+// 1 / (1 + 2^(-x log2 e)) on the unit's exponential and reciprocal: 4 + |x| ulps; 0 and 1 at the ends.
+__device__ __forceinline__ float sigmoid_ftz(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
 // 16 E4M3 codes (little-endian in a uint4) times an fp32 tile scale ->
 // 8 bf16x2 words: each decoded value (exact in fp32) times the scale, the
 // fp32 product rounded to bf16 (round to nearest even).
@@ -453,13 +475,36 @@ struct KeptBlock {
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
 // instruction, every lane of the producer warp taking four of the tile's
 // 128 rows; no permuted copy of the tokens is read.
+// CHUNKED: the chunks of a contraction of n k-blocks, and the first k-block of chunk ch.  What the chains cut is in
+// proportion to the mean of the chunks' squared lengths over n (8e-7 of a sum where all are 13); the first two
+// are longer where there are several, because they run while the epilogue of the tile before keeps the warps
+// that would empty a third.
+__device__ __forceinline__ int num_chunks(int n) { return (n + kChunk - 1) / kChunk; }
+__device__ __forceinline__ int chunk_start(int ch, int n) {
+  const int nch = num_chunks(n);
+  if (nch < 4) return ch * n / max(nch, 1);
+  constexpr int kLong = kChunk + 5;
+  return ch <= 2 ? ch * kLong : 2 * kLong + (ch - 2) * (n - 2 * kLong) / (nch - 2);
+}
+
 // TERMS (bf16, at most 2 with ragged M): every k-block multiplies that many tiles of A by one of B
 // into the same accumulator.
 template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT, bool PAIR, bool W8 = false, bool GATHER = false,
           int TERMS = 1>
-__global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads), 1)
+__global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
     grouped_gemm_kernel(const __grid_constant__ KParams p) {
   static_assert(!GATHER || (!A_MN && !B_MN && !QUANT && !W8), "GATHER: K-major bf16 ragged-M forms");
+  // The tensor cores cut what an addition to the fp32 accumulator does not hold, so a long chain shrinks a sum by about
+  // 1.4e-8 an instruction (8e-6 over 7168 elements).  Where a 32-bit output hangs on it the chain is kept short.
+  // CHUNKED: every kChunk k-blocks start a new accumulator, and the epilogue warps add it to sums in their registers
+  // while the next one is filled (128 a thread on 256-column tiles, for which the first warpgroup hands them
+  // registers).  The sums in tensor memory instead had the MMAs wait at every chunk (8192 rows, 14336 x 4096: 842 us,
+  // these 716, one chain 660 with dg off by 4e-6 of its norm; what a chunk costs is its reading from tensor memory).
+  constexpr bool CHUNKED = EPI == EPI_SWIGLU_BWD_C && !QUANT && !W8;
+  constexpr int EW = CHUNKED ? 4 : 2;   // first epilogue warp
+  // SPLIT: the first term of A has one accumulator, the others, 2^-8 of it or less, the other: adding them to one would
+  // cut its last bits three times as often
+  constexpr bool SPLIT = TERMS == 3;
   static_assert(TERMS == 1 || (B_MN && !QUANT && !W8 && !GATHER), "TERMS: bf16 forms with MN-major B");
   using C = KernelCfg<BN, A_MN, EPI, QUANT, PAIR, W8, TERMS>;
   // bf16: the MN-major-A form is the ragged-K (weight-gradient) form.  MXFP8
@@ -602,542 +647,557 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
   // registers and slots for long (weight gradients of 64 x 2048 x 7168: 652 us so, 627 without).
   if (total_tiles <= ustride) pdl_trigger();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (QUANT && lane == 0) {
-      // MXFP8 operands: E4M3 codes (128-byte swizzled, straight to the MMA) and
-      // the raw scale rows of each 128-element k-block
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
-        const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (it / S) & 1u;
-          if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s)) { ok = false; break; }
-          uint8_t* st = smem + s * C::kStageBytes;
-          if (RAGGED_K) {
-            // weight gradient: A [M][tokens] and B [N][tokens] codes (tokens of
-            // each group padded to 128 with zero codes), scales [tokens/32][M or N]
-            mbar_arrive_expect_tx(&full[s], C::kQTxBytesK);
-            const int k0 = t.row0 + kb * 128;
-            tma_load_2d(st, &p.tmA[0], &full[s], k0, t.m0);
-            tma_load_2d(st + C::kQARaw, &p.tmAs[0], &full[s], t.m0, k0 / 32);
-            tma_load_2d(st + C::kQBCodes, &p.tmB[0], &full[s], k0, t.nt * BN);
-            tma_load_2d(st + C::kQBRaw, &p.tmBs[0], &full[s], t.nt * BN, k0 / 32);
-            continue;
-          }
-          mbar_arrive_expect_tx(&full[s], C::kQTxBytes);
-          const int src = (kb < p.kb0) ? 0 : 1;
-          const int k0 = (src == 0 ? kb : kb - p.kb0) * 128;
-          tma_load_2d(st, &p.tmA[src], &full[s], k0, t.row0);
-          tma_load_2d(st + C::kQARaw, &p.tmAs[src], &full[s], t.row0 & ~15, k0 / 32);   // 16-byte aligned x
-          // CTA pair: this CTA's half of the B codes (W1 or W3 for the dual-N
-          // tile), and every B scale row (each CTA's tensor memory needs them all)
-          if (p.b_dual_n) {
-            const int f0 = t.nt * (BN / 2);
-            if (PAIR) {
-              tma_load_3d(st + C::kQBCodes, &p.tmB[rank & 1], &full[s], k0, f0, t.g);
-            } else {
-              tma_load_3d(st + C::kQBCodes, &p.tmB[0], &full[s], k0, f0, t.g);
-              tma_load_3d(st + C::kQBCodes + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
+  const bool epilogue = CHUNKED ? warp >= EW : warp >= 2 && (!(QUANT || W8) || warp < 10);
+  if (!epilogue) {
+    // CHUNKED: two more warps beside the producer and the MMA issuer complete their warpgroup
+    if (CHUNKED && BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFirst));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (QUANT && lane == 0) {
+        // MXFP8 operands: E4M3 codes (128-byte swizzled, straight to the MMA) and
+        // the raw scale rows of each 128-element k-block
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
+          const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+          for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (it / S) & 1u;
+            if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s)) { ok = false; break; }
+            uint8_t* st = smem + s * C::kStageBytes;
+            if (RAGGED_K) {
+              // weight gradient: A [M][tokens] and B [N][tokens] codes (tokens of
+              // each group padded to 128 with zero codes), scales [tokens/32][M or N]
+              mbar_arrive_expect_tx(&full[s], C::kQTxBytesK);
+              const int k0 = t.row0 + kb * 128;
+              tma_load_2d(st, &p.tmA[0], &full[s], k0, t.m0);
+              tma_load_2d(st + C::kQARaw, &p.tmAs[0], &full[s], t.m0, k0 / 32);
+              tma_load_2d(st + C::kQBCodes, &p.tmB[0], &full[s], k0, t.nt * BN);
+              tma_load_2d(st + C::kQBRaw, &p.tmBs[0], &full[s], t.nt * BN, k0 / 32);
+              continue;
             }
-            tma_load_3d(st + C::kQBRaw, &p.tmBs[0], &full[s], f0, k0 / 32, t.g);
-            tma_load_3d(st + C::kQBRaw + 2 * BN, &p.tmBs[1], &full[s], f0, k0 / 32, t.g);
-          } else {
-            tma_load_3d(st + C::kQBCodes, &p.tmB[src], &full[s], k0, t.nt * BN + (PAIR ? (rank & 1) * (BN / 2) : 0),
-                        t.g);
-            tma_load_3d(st + C::kQBRaw, &p.tmBs[src], &full[s], t.nt * BN, k0 / 32, t.g);
-          }
-        }
-      }
-      for (int s = 0; s < S; ++s) {
-        if (it > static_cast<uint32_t>(s)) {
-          const uint32_t last = s + S * ((it - 1 - s) / S);
-          mbar_wait_drain(&full[s], (last / S) & 1u);
-        }
-      }
-    } else if (GATHER) {
-      // Gathered A: lane l loads the tile's rows 4l..4l+3 (token row
-      // a_gather[r] / gather_k; a row past the group's end loads token row 0,
-      // whose products the epilogue never stores) by one gather4 into its
-      // 512-byte quarter-atom of the stage; lane 0 waits for the stage, arms
-      // the barrier and loads B.
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
-        const Tile t = decode_tile<false, BN, PAIR>(tile, p, s_off, s_pre, rank);
-        const int gend = s_off[t.g + 1];
-        int rr[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = t.row0 + 4 * lane + j;
-          rr[j] = r < gend ? __ldg(p.a_gather + r) / p.gather_k : 0;
-        }
-        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (it / S) & 1u;
-          int okl = 1;
-          if (lane == 0) okl = mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, okl, 0)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sA = smem + s * C::kStageBytes;
-          uint8_t* sB = sA + (RAGGED_K ? C::kABytesC : kABytes);
-          const int k0 = kb * BK;
-          if (PAIR) {
-            if (leader && lane == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-            const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-            __syncwarp();
-            tma_gather4_pair(sA + lane * 512, &p.tmA[0], bar, k0, rr[0], rr[1], rr[2], rr[3]);
-            if (lane == 0) {
-              if (p.b_dual_n) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, t.nt * (BN / 2), t.g);
-              else tma_load_3d_pair(sB, &p.tmB[0], bar, k0, t.nt * BN + rank * (BN / 2), t.g);
-            }
-          } else {
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-            __syncwarp();
-            tma_gather4(sA + lane * 512, &p.tmA[0], &full[s], k0, rr[0], rr[1], rr[2], rr[3]);
-            if (lane == 0) {
-              if (p.b_dual_n) {
-                const int f0 = t.nt * (BN / 2);
-                tma_load_3d(sB, &p.tmB[0], &full[s], k0, f0, t.g);
-                tma_load_3d(sB + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
+            mbar_arrive_expect_tx(&full[s], C::kQTxBytes);
+            const int src = (kb < p.kb0) ? 0 : 1;
+            const int k0 = (src == 0 ? kb : kb - p.kb0) * 128;
+            tma_load_2d(st, &p.tmA[src], &full[s], k0, t.row0);
+            tma_load_2d(st + C::kQARaw, &p.tmAs[src], &full[s], t.row0 & ~15, k0 / 32);   // 16-byte aligned x
+            // CTA pair: this CTA's half of the B codes (W1 or W3 for the dual-N
+            // tile), and every B scale row (each CTA's tensor memory needs them all)
+            if (p.b_dual_n) {
+              const int f0 = t.nt * (BN / 2);
+              if (PAIR) {
+                tma_load_3d(st + C::kQBCodes, &p.tmB[rank & 1], &full[s], k0, f0, t.g);
               } else {
-                tma_load_3d(sB, &p.tmB[0], &full[s], k0, t.nt * BN, t.g);
+                tma_load_3d(st + C::kQBCodes, &p.tmB[0], &full[s], k0, f0, t.g);
+                tma_load_3d(st + C::kQBCodes + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
               }
+              tma_load_3d(st + C::kQBRaw, &p.tmBs[0], &full[s], f0, k0 / 32, t.g);
+              tma_load_3d(st + C::kQBRaw + 2 * BN, &p.tmBs[1], &full[s], f0, k0 / 32, t.g);
+            } else {
+              tma_load_3d(st + C::kQBCodes, &p.tmB[src], &full[s], k0, t.nt * BN + (PAIR ? (rank & 1) * (BN / 2) : 0),
+                          t.g);
+              tma_load_3d(st + C::kQBRaw, &p.tmBs[src], &full[s], t.nt * BN, k0 / 32, t.g);
             }
           }
         }
-      }
-      // every stage's last armed load has landed before the CTA exits (for a
-      // pair the leader's barriers count both CTAs' copies)
-      if (lane == 0 && (!PAIR || leader)) {
         for (int s = 0; s < S; ++s) {
           if (it > static_cast<uint32_t>(s)) {
             const uint32_t last = s + S * ((it - 1 - s) / S);
             mbar_wait_drain(&full[s], (last / S) & 1u);
           }
         }
-      }
-      __syncwarp();
-    } else if (!QUANT && lane == 0) {
-      uint32_t it = 0;
-      int map_g = -1;   // ragged K: the group whose maps this thread last acquired
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
-        const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (it / S) & 1u;
-          if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s)) { ok = false; break; }
-          uint8_t* sA = smem + s * C::kStageBytes;
-          uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
-          if (W8) {
-            // FP8 weights: A (bf16) straight into the stage; the B codes of the
-            // k-block into a staging slot for the converters
-            const int src = (kb < p.kb0) ? 0 : 1;
-            const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
-            mbar_arrive_expect_tx(&full[s], kABytes);
-            tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
-            const uint32_t wit = it;   // one code slot use per k-block
-            const int ws_ = wit % C::kW8Slots;
-            if (!mbar_wait_bounded(&wempty[ws_], ((wit / C::kW8Slots) & 1u) ^ 1u, s_abort, p.status, 130 + ws_)) {
+      } else if (GATHER) {
+        // Gathered A: lane l loads the tile's rows 4l..4l+3 (token row
+        // a_gather[r] / gather_k; a row past the group's end loads token row 0,
+        // whose products the epilogue never stores) by one gather4 into its
+        // 512-byte quarter-atom of the stage; lane 0 waits for the stage, arms
+        // the barrier and loads B.
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
+          const Tile t = decode_tile<false, BN, PAIR>(tile, p, s_off, s_pre, rank);
+          const int gend = s_off[t.g + 1];
+          int rr[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = t.row0 + 4 * lane + j;
+            rr[j] = r < gend ? __ldg(p.a_gather + r) / p.gather_k : 0;
+          }
+          for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (it / S) & 1u;
+            int okl = 1;
+            if (lane == 0) okl = mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s) ? 1 : 0;
+            if (!__shfl_sync(0xffffffffu, okl, 0)) {
               ok = false;
               break;
             }
-            uint8_t* q = smem + C::kW8Off + ws_ * C::kW8SlotBytes;
-            mbar_arrive_expect_tx(&wfull[ws_], C::kW8SlotBytes);
-            if (!B_MN) {
-              if (p.b_dual_n) {
-                const int f0 = t.nt * (BN / 2);
-                tma_load_3d(q, &p.tmB[0], &wfull[ws_], k0, f0, t.g);
-                tma_load_3d(q + (BN / 2) * 64, &p.tmB[1], &wfull[ws_], k0, f0, t.g);
-              } else {
-                tma_load_3d(q, &p.tmB[src], &wfull[ws_], k0, t.nt * BN, t.g);
+            uint8_t* sA = smem + s * C::kStageBytes;
+            uint8_t* sB = sA + (RAGGED_K ? C::kABytesC : kABytes);
+            const int k0 = kb * BK;
+            if (PAIR) {
+              if (leader && lane == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+              const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
+              __syncwarp();
+              tma_gather4_pair(sA + lane * 512, &p.tmA[0], bar, k0, rr[0], rr[1], rr[2], rr[3]);
+              if (lane == 0) {
+                if (p.b_dual_n) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, t.nt * (BN / 2), t.g);
+                else tma_load_3d_pair(sB, &p.tmB[0], bar, k0, t.nt * BN + rank * (BN / 2), t.g);
               }
             } else {
-#pragma unroll
-              for (int a = 0; a < BN / 64; ++a)
-                tma_load_3d(q + a * 4096, &p.tmB[src], &wfull[ws_], t.nt * BN + 64 * a, k0, t.g);
+              if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+              __syncwarp();
+              tma_gather4(sA + lane * 512, &p.tmA[0], &full[s], k0, rr[0], rr[1], rr[2], rr[3]);
+              if (lane == 0) {
+                if (p.b_dual_n) {
+                  const int f0 = t.nt * (BN / 2);
+                  tma_load_3d(sB, &p.tmB[0], &full[s], k0, f0, t.g);
+                  tma_load_3d(sB + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
+                } else {
+                  tma_load_3d(sB, &p.tmB[0], &full[s], k0, t.nt * BN, t.g);
+                }
+              }
             }
-            continue;
           }
-          if (RAGGED_K) {
-            // The group's own maps end at its last row, so its last k-block
-            // reads zeros past the group's end (TMA fill) instead of the next
-            // group's rows.  One group: the whole-tensor maps do the same.
-            const bool gm = p.gmaps != nullptr;
-            const CUtensorMap* mA = gm ? p.gmaps + t.g : &p.tmA[0];
-            const CUtensorMap* mB = gm ? p.gmaps + G + t.g : &p.tmB[0];
-            if (gm && t.g != map_g) {
-              tensormap_acquire(mA);
-              tensormap_acquire(mB);
-              map_g = t.g;
+        }
+        // every stage's last armed load has landed before the CTA exits (for a
+        // pair the leader's barriers count both CTAs' copies)
+        if (lane == 0 && (!PAIR || leader)) {
+          for (int s = 0; s < S; ++s) {
+            if (it > static_cast<uint32_t>(s)) {
+              const uint32_t last = s + S * ((it - 1 - s) / S);
+              mbar_wait_drain(&full[s], (last / S) & 1u);
             }
-            const int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
-            if (PAIR) {
+          }
+        }
+        __syncwarp();
+      } else if (!QUANT && lane == 0) {
+        uint32_t it = 0;
+        int map_g = -1;   // ragged K: the group whose maps this thread last acquired
+        bool ok = true;
+        for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
+          const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+          for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (it / S) & 1u;
+            if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 100 + s)) { ok = false; break; }
+            uint8_t* sA = smem + s * C::kStageBytes;
+            uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
+            if (W8) {
+              // FP8 weights: A (bf16) straight into the stage; the B codes of the
+              // k-block into a staging slot for the converters
+              const int src = (kb < p.kb0) ? 0 : 1;
+              const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
+              mbar_arrive_expect_tx(&full[s], kABytes);
+              tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
+              const uint32_t wit = it;   // one code slot use per k-block
+              const int ws_ = wit % C::kW8Slots;
+              if (!mbar_wait_bounded(&wempty[ws_], ((wit / C::kW8Slots) & 1u) ^ 1u, s_abort, p.status, 130 + ws_)) {
+                ok = false;
+                break;
+              }
+              uint8_t* q = smem + C::kW8Off + ws_ * C::kW8SlotBytes;
+              mbar_arrive_expect_tx(&wfull[ws_], C::kW8SlotBytes);
+              if (!B_MN) {
+                if (p.b_dual_n) {
+                  const int f0 = t.nt * (BN / 2);
+                  tma_load_3d(q, &p.tmB[0], &wfull[ws_], k0, f0, t.g);
+                  tma_load_3d(q + (BN / 2) * 64, &p.tmB[1], &wfull[ws_], k0, f0, t.g);
+                } else {
+                  tma_load_3d(q, &p.tmB[src], &wfull[ws_], k0, t.nt * BN, t.g);
+                }
+              } else {
+#pragma unroll
+                for (int a = 0; a < BN / 64; ++a)
+                  tma_load_3d(q + a * 4096, &p.tmB[src], &wfull[ws_], t.nt * BN + 64 * a, k0, t.g);
+              }
+              continue;
+            }
+            if (RAGGED_K) {
+              // The group's own maps end at its last row, so its last k-block
+              // reads zeros past the group's end (TMA fill) instead of the next
+              // group's rows.  One group: the whole-tensor maps do the same.
+              const bool gm = p.gmaps != nullptr;
+              const CUtensorMap* mA = gm ? p.gmaps + t.g : &p.tmA[0];
+              const CUtensorMap* mB = gm ? p.gmaps + G + t.g : &p.tmB[0];
+              if (gm && t.g != map_g) {
+                tensormap_acquire(mA);
+                tensormap_acquire(mB);
+                map_g = t.g;
+              }
+              const int r = gm ? kb * C::kKb : t.row0 + kb * C::kKb;   // rows of the group's map
+              if (PAIR) {
+                // both CTAs' loads complete on the leader's barrier, armed by the leader
+                const int n0 = t.nt * BN + (rank & 1) * (BN / 2);
+                if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+                const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) {
+                  const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
+                  tma_load_2d_pair(sA + i * C::kABytesC, mA, bar, m0, r);
+                  tma_load_2d_pair(sA + i * C::kABytesC + C::kKb * 128, mA, bar, m0 + 64, r);
+                }
+#pragma unroll
+                for (int a = 0; a < BN / 128; ++a) tma_load_2d_pair(sB + a * C::kKb * 128, mB, bar, n0 + 64 * a, r);
+              } else {
+                mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) {
+                  const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
+                  tma_load_2d(sA + i * C::kABytesC, mA, &full[s], m0, r);
+                  tma_load_2d(sA + i * C::kABytesC + 8192, mA, &full[s], m0 + 64, r);
+                }
+#pragma unroll
+                for (int a = 0; a < BN / 64; ++a) tma_load_2d(sB + a * 8192, mB, &full[s], t.nt * BN + 64 * a, r);
+              }
+              continue;
+            }
+            if (PAIR && !RAGGED_K) {
               // both CTAs' loads complete on the leader's barrier, armed by the leader
-              const int n0 = t.nt * BN + (rank & 1) * (BN / 2);
               if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
               const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-#pragma unroll
-              for (int i = 0; i < TERMS; ++i) {
-                const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
-                tma_load_2d_pair(sA + i * C::kABytesC, mA, bar, m0, r);
-                tma_load_2d_pair(sA + i * C::kABytesC + C::kKb * 128, mA, bar, m0 + 64, r);
-              }
-#pragma unroll
-              for (int a = 0; a < BN / 128; ++a) tma_load_2d_pair(sB + a * C::kKb * 128, mB, bar, n0 + 64 * a, r);
-            } else {
-              mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-#pragma unroll
-              for (int i = 0; i < TERMS; ++i) {
-                const int m0 = t.m0 + (TERMS > 1 ? i * p.a_term_cols : 0);
-                tma_load_2d(sA + i * C::kABytesC, mA, &full[s], m0, r);
-                tma_load_2d(sA + i * C::kABytesC + 8192, mA, &full[s], m0 + 64, r);
-              }
-#pragma unroll
-              for (int a = 0; a < BN / 64; ++a) tma_load_2d(sB + a * 8192, mB, &full[s], t.nt * BN + 64 * a, r);
-            }
-            continue;
-          }
-          if (PAIR && !RAGGED_K) {
-            // both CTAs' loads complete on the leader's barrier, armed by the leader
-            if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-            const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
-            const int src = (TERMS > 1 || kb < p.kb0) ? 0 : 1;
-            const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
-            tma_load_2d_pair(sA, &p.tmA[src], bar, k0, t.row0);
-            if (TERMS > 1) tma_load_2d_pair(sA + kABytes, &p.tmA[1], bar, k0, t.row0);
-            if (!B_MN) {
-              if (p.b_dual_n) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, t.nt * (BN / 2), t.g);  // W1 | W3 half
-              else tma_load_3d_pair(sB, &p.tmB[src], bar, k0, t.nt * BN + rank * (BN / 2), t.g);
-            } else {
-#pragma unroll
-              for (int a = 0; a < BN / 128; ++a)
-                tma_load_3d_pair(sB + a * 8192, &p.tmB[src], bar, t.nt * BN + rank * (BN / 2) + 64 * a, k0, t.g);
-            }
-            continue;
-          }
-          mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-          if (!RAGGED_K) {
-            const int kbg = t.kbeg + kb;   // k-block within the whole contraction
-            const int src = (TERMS > 1 || kbg < p.kb0) ? 0 : 1;
-            const int k0 = (src == 0 ? kbg : kbg - p.kb0) * BK;
-            tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
-            if (TERMS > 1) tma_load_2d(sA + kABytes, &p.tmA[1], &full[s], k0, t.row0);
-            // B maps of the ragged-M form are always 3-D: {cols, rows, group}
-            if (!B_MN) {
-              if (p.b_dual_n) {
-                const int f0 = t.nt * (BN / 2);
-                tma_load_3d(sB, &p.tmB[0], &full[s], k0, f0, t.g);
-                tma_load_3d(sB + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
+              const int src = (TERMS > 1 || kb < p.kb0) ? 0 : 1;
+              const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
+              tma_load_2d_pair(sA, &p.tmA[src], bar, k0, t.row0);
+              if (TERMS > 1) tma_load_2d_pair(sA + kABytes, &p.tmA[1], bar, k0, t.row0);
+              if (!B_MN) {
+                if (p.b_dual_n) tma_load_3d_pair(sB, &p.tmB[rank], bar, k0, t.nt * (BN / 2), t.g);  // W1 | W3 half
+                else tma_load_3d_pair(sB, &p.tmB[src], bar, k0, t.nt * BN + rank * (BN / 2), t.g);
               } else {
-                tma_load_3d(sB, &p.tmB[src], &full[s], k0, t.nt * BN, t.g);
-              }
-            } else {
 #pragma unroll
-              for (int a = 0; a < BN / 64; ++a)
-                tma_load_3d(sB + a * 8192, &p.tmB[src], &full[s], t.nt * BN + 64 * a, k0, t.g);
+                for (int a = 0; a < BN / 128; ++a)
+                  tma_load_3d_pair(sB + a * 8192, &p.tmB[src], bar, t.nt * BN + rank * (BN / 2) + 64 * a, k0, t.g);
+              }
+              continue;
+            }
+            mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+            if (!RAGGED_K) {
+              const int kbg = t.kbeg + kb;   // k-block within the whole contraction
+              const int src = (TERMS > 1 || kbg < p.kb0) ? 0 : 1;
+              const int k0 = (src == 0 ? kbg : kbg - p.kb0) * BK;
+              tma_load_2d(sA, &p.tmA[src], &full[s], k0, t.row0);
+              if (TERMS > 1) tma_load_2d(sA + kABytes, &p.tmA[1], &full[s], k0, t.row0);
+              // B maps of the ragged-M form are always 3-D: {cols, rows, group}
+              if (!B_MN) {
+                if (p.b_dual_n) {
+                  const int f0 = t.nt * (BN / 2);
+                  tma_load_3d(sB, &p.tmB[0], &full[s], k0, f0, t.g);
+                  tma_load_3d(sB + (BN / 2) * 128, &p.tmB[1], &full[s], k0, f0, t.g);
+                } else {
+                  tma_load_3d(sB, &p.tmB[src], &full[s], k0, t.nt * BN, t.g);
+                }
+              } else {
+#pragma unroll
+                for (int a = 0; a < BN / 64; ++a)
+                  tma_load_3d(sB + a * 8192, &p.tmB[src], &full[s], t.nt * BN + 64 * a, k0, t.g);
+              }
             }
           }
         }
-      }
-      // Wait (bounded) for every stage's last armed load so that no copy is
-      // still landing in shared memory when the CTA exits (for a pair the
-      // leader's barriers count both CTAs' copies).
-      for (int s = 0; s < S && (!PAIR || leader); ++s) {
-        if (it > static_cast<uint32_t>(s)) {
-          const uint32_t last = s + S * ((it - 1 - s) / S);
-          mbar_wait_drain(&full[s], (last / S) & 1u);
+        // Wait (bounded) for every stage's last armed load so that no copy is
+        // still landing in shared memory when the CTA exits (for a pair the
+        // leader's barriers count both CTAs' copies).
+        for (int s = 0; s < S && (!PAIR || leader); ++s) {
+          if (it > static_cast<uint32_t>(s)) {
+            const uint32_t last = s + S * ((it - 1 - s) / S);
+            mbar_wait_drain(&full[s], (last / S) & 1u);
+          }
+        }
+        for (int s = 0; s < C::kW8Slots; ++s) {
+          if (it > static_cast<uint32_t>(s)) {
+            const uint32_t last = s + C::kW8Slots * ((it - 1 - s) / C::kW8Slots);
+            mbar_wait_drain(&wfull[s], (last / C::kW8Slots) & 1u);
+          }
         }
       }
-      for (int s = 0; s < C::kW8Slots; ++s) {
-        if (it > static_cast<uint32_t>(s)) {
-          const uint32_t last = s + C::kW8Slots * ((it - 1 - s) / C::kW8Slots);
-          mbar_wait_drain(&wfull[s], (last / C::kW8Slots) & 1u);
-        }
-      }
-    }
-  } else if (PAIR && warp == 1 && !leader) {
-    // the leader CTA issues the pair's MMAs; this warp has nothing to do
-  } else if (warp == 1 && QUANT) {
-    // ------------------------------------------------------------ MMA issuer (MXFP8)
-    // Per k-block: the scale atoms go to tensor memory by tcgen05.cp, then four
-    // block-scaled MMAs (K = 32 each) select scale byte 0..3.  Both are issued
-    // by the same thread, so the copies are ordered before the MMAs.
-    uint32_t it = 0, tcount = 0;
-    bool ok = true;
-    for (int tile = unit0; ok && tile < total_tiles; tile += ustride, ++tcount) {
-      const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-      const uint32_t buf = tcount & 1u;
-      const uint32_t aph = (tcount >> 1) & 1u;
-      if (!mbar_wait_bounded(&tempty[buf], aph ^ 1u, s_abort, p.status, 200)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + buf * BN;
-      for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-        const int s = it % S;
-        const uint32_t ph = (it / S) & 1u;
-        if (!mbar_wait_bounded(&sready[s], ph, s_abort, p.status, 320 + s)) { ok = false; break; }
+    } else if (PAIR && warp == 1 && !leader) {
+      // the leader CTA issues the pair's MMAs; this warp has nothing to do
+    } else if (warp == 1 && QUANT) {
+      // ------------------------------------------------------------ MMA issuer (MXFP8)
+      // Per k-block: the scale atoms go to tensor memory by tcgen05.cp, then four
+      // block-scaled MMAs (K = 32 each) select scale byte 0..3.  Both are issued
+      // by the same thread, so the copies are ordered before the MMAs.
+      uint32_t it = 0, tcount = 0;
+      bool ok = true;
+      for (int tile = unit0; ok && tile < total_tiles; tile += ustride, ++tcount) {
+        const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+        const uint32_t buf = tcount & 1u;
+        const uint32_t aph = (tcount >> 1) & 1u;
+        if (!mbar_wait_bounded(&tempty[buf], aph ^ 1u, s_abort, p.status, 200)) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint8_t* st = smem + s * C::kStageBytes;
-          // one 16-column scale buffer per stage (A: +0..3, B: +4..11): a buffer is
-          // rewritten only after the MMAs that read it have completed (stage release)
-          const uint32_t sf = tmem_base + C::kSfCol + s * 16;
-          const uint32_t atoms = smem_u32(st + C::kQAtoms);
-          if (PAIR) {   // each CTA's atoms to its own tensor memory
-            tc_cp_32x128b_warpx4_pair(sf, atoms);
-            tc_cp_32x128b_warpx4_pair(sf + 4, atoms + 512);
-            if (BN > 128) tc_cp_32x128b_warpx4_pair(sf + 8, atoms + 1024);
-          } else {
-            tc_cp_32x128b_warpx4(sf, atoms);
-            tc_cp_32x128b_warpx4(sf + 4, atoms + 512);
-            if (BN > 128) tc_cp_32x128b_warpx4(sf + 8, atoms + 1024);
-          }
-          const uint32_t a_base = smem_u32(st);
-          const uint32_t b_base = smem_u32(st + C::kQBCodes);
+        const uint32_t d_tmem = tmem_base + buf * BN;
+        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (it / S) & 1u;
+          if (!mbar_wait_bounded(&sready[s], ph, s_abort, p.status, 320 + s)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint8_t* st = smem + s * C::kStageBytes;
+            // one 16-column scale buffer per stage (A: +0..3, B: +4..11): a buffer is
+            // rewritten only after the MMAs that read it have completed (stage release)
+            const uint32_t sf = tmem_base + C::kSfCol + s * 16;
+            const uint32_t atoms = smem_u32(st + C::kQAtoms);
+            if (PAIR) {   // each CTA's atoms to its own tensor memory
+              tc_cp_32x128b_warpx4_pair(sf, atoms);
+              tc_cp_32x128b_warpx4_pair(sf + 4, atoms + 512);
+              if (BN > 128) tc_cp_32x128b_warpx4_pair(sf + 8, atoms + 1024);
+            } else {
+              tc_cp_32x128b_warpx4(sf, atoms);
+              tc_cp_32x128b_warpx4(sf + 4, atoms + 512);
+              if (BN > 128) tc_cp_32x128b_warpx4(sf + 8, atoms + 1024);
+            }
+            const uint32_t a_base = smem_u32(st);
+            const uint32_t b_base = smem_u32(st + C::kQBCodes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = smem_desc_sw128(b_base + kk * 32, 16, 1024);
-            if (PAIR)
-              tc_mma_mxf8_pair(d_tmem, ad, bd, idesc_mxf8(2 * BM, BN, kk), sf, sf + 4, (kb > 0 || kk > 0) ? 1u : 0u);
-            else
-              tc_mma_mxf8(d_tmem, ad, bd, idesc_mxf8(BM, BN, kk), sf, sf + 4, (kb > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
+              const uint64_t bd = smem_desc_sw128(b_base + kk * 32, 16, 1024);
+              if (PAIR)
+                tc_mma_mxf8_pair(d_tmem, ad, bd, idesc_mxf8(2 * BM, BN, kk), sf, sf + 4, (kb > 0 || kk > 0) ? 1u : 0u);
+              else
+                tc_mma_mxf8(d_tmem, ad, bd, idesc_mxf8(BM, BN, kk), sf, sf + 4, (kb > 0 || kk > 0) ? 1u : 0u);
+            }
+            if (PAIR) tc_commit_pair_mc(&empty[s], 3);
+            else tc_commit(&empty[s]);
           }
-          if (PAIR) tc_commit_pair_mc(&empty[s], 3);
-          else tc_commit(&empty[s]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (PAIR) tc_commit_pair_mc(&tfull[buf], static_cast<uint16_t>(3u << lead));
+          else if (t.num_kb > 0) tc_commit(&tfull[buf]);
+          else mbar_arrive(&tfull[buf]);
         }
         __syncwarp();
       }
-      if (!ok) break;
       if (lane == 0) {
-        if (PAIR) tc_commit_pair_mc(&tfull[buf], static_cast<uint16_t>(3u << lead));
-        else if (t.num_kb > 0) tc_commit(&tfull[buf]);
-        else mbar_arrive(&tfull[buf]);
+        if (PAIR) tc_commit_pair_mc(mma_done, static_cast<uint16_t>(1u << lead));
+        else tc_commit(mma_done);
+        mbar_wait_drain(mma_done, 0);
       }
       __syncwarp();
-    }
-    if (lane == 0) {
-      if (PAIR) tc_commit_pair_mc(mma_done, static_cast<uint16_t>(1u << lead));
-      else tc_commit(mma_done);
-      mbar_wait_drain(mma_done, 0);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * BM : BM, BN, A_MN, B_MN);
-    uint32_t it = 0, tcount = 0;
-    bool ok = true;
-    // ragged K: the next tile's group offsets (global memory) are loaded
-    // before this tile's k-blocks are issued and used only after them, so
-    // their latency falls while the MMAs run instead of between tiles
-    int nx0 = 0, nx1 = 0;
-    if (RAGGED_K && unit0 < total_tiles) {
-      const int g = rk_group<BN, PAIR>(unit0, p);
-      nx0 = s_off[g];
-      nx1 = s_off[g + 1];
-    }
-    for (int tile = unit0; ok && tile < total_tiles; tile += ustride, ++tcount) {
-      const Tile t = RAGGED_K ? decode_tile_rk<BN, PAIR>(tile, p, nx0, nx1, rank)
-                              : decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-      if (RAGGED_K && tile + ustride < total_tiles) {
-        const int g = rk_group<BN, PAIR>(tile + ustride, p);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * BM : BM, BN, A_MN, B_MN);
+      uint32_t it = 0, tcount = 0;
+      uint32_t chunk = 0;   // CHUNKED: chunks so far
+      bool ok = true;
+      // ragged K: the next tile's group offsets (global memory) are loaded
+      // before this tile's k-blocks are issued and used only after them, so
+      // their latency falls while the MMAs run instead of between tiles
+      int nx0 = 0, nx1 = 0;
+      if (RAGGED_K && unit0 < total_tiles) {
+        const int g = rk_group<BN, PAIR>(unit0, p);
         nx0 = s_off[g];
         nx1 = s_off[g + 1];
       }
-      const uint32_t buf = tcount & 1u;
-      const uint32_t aph = (tcount >> 1) & 1u;
-      if (!mbar_wait_bounded(&tempty[buf], aph ^ 1u, s_abort, p.status, 200)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + buf * BN;
-      for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-        const int s = it % S;
-        const uint32_t ph = (it / S) & 1u;
-        if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 300 + s)) { ok = false; break; }
-        tc_fence_after();
-        uint8_t* sA = smem + s * C::kStageBytes;
-        uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
-        // Ragged K: rows past the group's end arrive as zeros (the per-group
-        // maps end at the group's last row); K=16 steps holding none of the
-        // group's rows are skipped.
-        constexpr int KB = RAGGED_K ? C::kKb : BK;
-        const int rv = t.k_rows - kb * KB;
-        const int nkk = (RAGGED_K && rv < KB) ? (rv + 15) / 16 : KB / 16;
-        if (lane == 0) {
-          const uint32_t b_base = smem_u32(sB);
-#pragma unroll
-          for (int i = 0; i < TERMS; ++i) {
-            const uint32_t a_base = smem_u32(sA) + i * (RAGGED_K ? C::kABytesC : kABytes);
-            for (int kk = 0; kk < nkk; ++kk) {
-              const uint64_t ad = A_MN ? smem_desc_sw128(a_base + kk * 2048, KB * 128, 1024)
-                                       : smem_desc_sw128(a_base + kk * 32, 16, 1024);
-              const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 2048, KB * 128, 1024)
-                                       : smem_desc_sw128(b_base + kk * 32, 16, 1024);
-              const uint32_t acc = (kb > 0 || kk > 0 || i > 0) ? 1u : 0u;
-              if (PAIR) tc_mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
-              else tc_mma_bf16(d_tmem, ad, bd, idesc, acc);
-            }
-          }
-          if (PAIR) tc_commit_pair_mc(&empty[s], 3);
-          else tc_commit(&empty[s]);
+      for (int tile = unit0; ok && tile < total_tiles; tile += ustride, ++tcount) {
+        const Tile t = RAGGED_K ? decode_tile_rk<BN, PAIR>(tile, p, nx0, nx1, rank)
+                                : decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+        if (RAGGED_K && tile + ustride < total_tiles) {
+          const int g = rk_group<BN, PAIR>(tile + ustride, p);
+          nx0 = s_off[g];
+          nx1 = s_off[g + 1];
         }
-        __syncwarp();
+        const int nch = CHUNKED ? num_chunks(t.num_kb) : 1;
+        for (int ch = 0; ch < nch; ++ch) {
+          const uint32_t use = CHUNKED ? chunk++ : tcount;   // accumulators filled before this one
+          const uint32_t buf = SPLIT ? 0u : use & 1u;
+          const uint32_t aph = (SPLIT ? use : use >> 1) & 1u;
+          if (!mbar_wait_bounded(&tempty[buf], aph ^ 1u, s_abort, p.status, 200)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + buf * BN;
+          const int kb0 = ch * kChunk;
+          for (int kb = kb0; kb < (CHUNKED ? min(t.num_kb, kb0 + kChunk) : t.num_kb); ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (it / S) & 1u;
+            if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 300 + s)) { ok = false; break; }
+            tc_fence_after();
+            uint8_t* sA = smem + s * C::kStageBytes;
+            uint8_t* sB = sA + TERMS * (RAGGED_K ? C::kABytesC : kABytes);
+            // Ragged K: rows past the group's end arrive as zeros (the per-group
+            // maps end at the group's last row); K=16 steps holding none of the
+            // group's rows are skipped.
+            constexpr int KB = RAGGED_K ? C::kKb : BK;
+            const int rv = t.k_rows - kb * KB;
+            const int nkk = (RAGGED_K && rv < KB) ? (rv + 15) / 16 : KB / 16;
+            if (lane == 0) {
+              const uint32_t b_base = smem_u32(sB);
+    #pragma unroll
+              for (int i = 0; i < TERMS; ++i) {
+                const uint32_t a_base = smem_u32(sA) + i * (RAGGED_K ? C::kABytesC : kABytes);
+                for (int kk = 0; kk < nkk; ++kk) {
+                  const uint64_t ad = A_MN ? smem_desc_sw128(a_base + kk * 2048, KB * 128, 1024)
+                                           : smem_desc_sw128(a_base + kk * 32, 16, 1024);
+                  const uint64_t bd = B_MN ? smem_desc_sw128(b_base + kk * 2048, KB * 128, 1024)
+                                           : smem_desc_sw128(b_base + kk * 32, 16, 1024);
+                  const uint32_t acc = (kb > kb0 || kk > 0 || i > (SPLIT ? 1 : 0)) ? 1u : 0u;
+                  const uint32_t d = d_tmem + (SPLIT && i > 0 ? BN : 0);
+                  if (PAIR) tc_mma_bf16_pair(d, ad, bd, idesc, acc);
+                  else tc_mma_bf16(d, ad, bd, idesc, acc);
+                }
+              }
+              if (PAIR) tc_commit_pair_mc(&empty[s], 3);
+              else tc_commit(&empty[s]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            if (PAIR) tc_commit_pair_mc(&tfull[buf], static_cast<uint16_t>(3u << lead));
+            else if (t.num_kb > 0) tc_commit(&tfull[buf]);
+            else mbar_arrive(&tfull[buf]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
       }
-      if (!ok) break;
+      // every MMA issued by this CTA has completed before TMEM is released
       if (lane == 0) {
-        if (PAIR) tc_commit_pair_mc(&tfull[buf], static_cast<uint16_t>(3u << lead));
-        else if (t.num_kb > 0) tc_commit(&tfull[buf]);
-        else mbar_arrive(&tfull[buf]);
+        if (PAIR) tc_commit_pair_mc(mma_done, static_cast<uint16_t>(1u << lead));
+        else tc_commit(mma_done);
+        mbar_wait_drain(mma_done, 0);
       }
       __syncwarp();
-    }
-    // every MMA issued by this CTA has completed before TMEM is released
-    if (lane == 0) {
-      if (PAIR) tc_commit_pair_mc(mma_done, static_cast<uint16_t>(1u << lead));
-      else tc_commit(mma_done);
-      mbar_wait_drain(mma_done, 0);
-    }
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ scale atoms (MXFP8)
-    // Rearrange the stage's raw scale rows ([block][row]) into the 512-byte
-    // atoms tcgen05.cp expects: for row r, byte j (scale block) of 32-bit word
-    // (r/32)%4 of 16-byte row r%32; one atom per 128 rows of A or of B.
-    // Warp w of the kSfWarps builds the whole of every stage s with
-    // s % kSfWarps == w, so consecutive stages are built at once; lane l
-    // writes 16-byte row l of each atom (rows l, l+32, l+64, l+96).  A warp
-    // owns whole stages and meets each of their fills in order: a parity
-    // wait must never skip a phase of its barrier.
-    if (QUANT) {
-      const int sfw = warp - 10;
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
-        const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-        // A scale rows: ragged M [4][144] from a 16-aligned row; ragged K [4][128]
-        const int a_rem = RAGGED_K ? 0 : (t.row0 & 15);
-        constexpr int AS = RAGGED_K ? 128 : 144;
-        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-          const int s = it % S;
-          if (s % kSfWarps != sfw) continue;
-          const uint32_t ph = (it / S) & 1u;
-          if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 500 + s)) { ok = false; break; }
-          uint8_t* st = smem + s * C::kStageBytes;
-          const uint8_t* ra = st + C::kQARaw;
-          const uint8_t* rb = st + C::kQBRaw;
-          const uint32_t atoms = smem_u32(st + C::kQAtoms);
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = a_rem + lane + 32 * i;
-            w[i] = static_cast<uint32_t>(ra[r]) | (static_cast<uint32_t>(ra[AS + r]) << 8) |
-                   (static_cast<uint32_t>(ra[2 * AS + r]) << 16) | (static_cast<uint32_t>(ra[3 * AS + r]) << 24);
-          }
-          st_shared_v4(atoms + lane * 16, w[0], w[1], w[2], w[3]);
-          // dual N: rows [0, BN/2) from the W1 scale rows, the rest from W3's
-          const int w_ = p.b_dual_n ? BN / 2 : BN;
-#pragma unroll
-          for (int a = 0; a < (BN + 127) / 128; ++a) {
+    } else if (QUANT || W8) {
+      // ------------------------------------------------------------ scale atoms (MXFP8)
+      // Rearrange the stage's raw scale rows ([block][row]) into the 512-byte
+      // atoms tcgen05.cp expects: for row r, byte j (scale block) of 32-bit word
+      // (r/32)%4 of 16-byte row r%32; one atom per 128 rows of A or of B.
+      // Warp w of the kSfWarps builds the whole of every stage s with
+      // s % kSfWarps == w, so consecutive stages are built at once; lane l
+      // writes 16-byte row l of each atom (rows l, l+32, l+64, l+96).  A warp
+      // owns whole stages and meets each of their fills in order: a parity
+      // wait must never skip a phase of its barrier.
+      if (QUANT) {
+        const int sfw = warp - 10;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
+          const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+          // A scale rows: ragged M [4][144] from a 16-aligned row; ragged K [4][128]
+          const int a_rem = RAGGED_K ? 0 : (t.row0 & 15);
+          constexpr int AS = RAGGED_K ? 128 : 144;
+          for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+            const int s = it % S;
+            if (s % kSfWarps != sfw) continue;
+            const uint32_t ph = (it / S) & 1u;
+            if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 500 + s)) { ok = false; break; }
+            uint8_t* st = smem + s * C::kStageBytes;
+            const uint8_t* ra = st + C::kQARaw;
+            const uint8_t* rb = st + C::kQBRaw;
+            const uint32_t atoms = smem_u32(st + C::kQAtoms);
+            uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = 128 * a + lane + 32 * i;
-              const int half = p.b_dual_n ? (r >= BN / 2 ? 1 : 0) : 0;
-              const uint8_t* src = rb + half * 2 * BN + (r - half * (BN / 2));
-              w[i] = r < BN ? (static_cast<uint32_t>(src[0]) | (static_cast<uint32_t>(src[w_]) << 8) |
-                               (static_cast<uint32_t>(src[2 * w_]) << 16) | (static_cast<uint32_t>(src[3 * w_]) << 24))
-                            : 0u;
+              const int r = a_rem + lane + 32 * i;
+              w[i] = static_cast<uint32_t>(ra[r]) | (static_cast<uint32_t>(ra[AS + r]) << 8) |
+                     (static_cast<uint32_t>(ra[2 * AS + r]) << 16) | (static_cast<uint32_t>(ra[3 * AS + r]) << 24);
             }
-            st_shared_v4(atoms + 512 + a * 512 + lane * 16, w[0], w[1], w[2], w[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            // CTA pair: the leader copies both CTAs' atoms; the peer's arrival
-            // releases its atom writes at cluster scope
-            if (PAIR && !leader) mbar_arrive_remote_release(mapa_shared(smem_u32(&sready[s]), lead));
-            else mbar_arrive(&sready[s]);
+            st_shared_v4(atoms + lane * 16, w[0], w[1], w[2], w[3]);
+            // dual N: rows [0, BN/2) from the W1 scale rows, the rest from W3's
+            const int w_ = p.b_dual_n ? BN / 2 : BN;
+#pragma unroll
+            for (int a = 0; a < (BN + 127) / 128; ++a) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = 128 * a + lane + 32 * i;
+                const int half = p.b_dual_n ? (r >= BN / 2 ? 1 : 0) : 0;
+                const uint8_t* src = rb + half * 2 * BN + (r - half * (BN / 2));
+                w[i] = r < BN ? (static_cast<uint32_t>(src[0]) | (static_cast<uint32_t>(src[w_]) << 8) |
+                                 (static_cast<uint32_t>(src[2 * w_]) << 16) | (static_cast<uint32_t>(src[3 * w_]) << 24))
+                              : 0u;
+              }
+              st_shared_v4(atoms + 512 + a * 512 + lane * 16, w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              // CTA pair: the leader copies both CTAs' atoms; the peer's arrival
+              // releases its atom writes at cluster scope
+              if (PAIR && !leader) mbar_arrive_remote_release(mapa_shared(smem_u32(&sready[s]), lead));
+              else mbar_arrive(&sready[s]);
+            }
           }
         }
       }
-    }
-    if (W8) {
-      // ---------------------------------------------------------- converters (FP8 weights)
-      // Each k-block: wait for its code slot and for the stage to be free,
-      // write the bf16 B tile (dequantised value = E4M3 code x its 128 x 128
-      // tile scale, rounded to bf16) in the 128-byte-swizzled layout of the
-      // MMA, release the slot and arrive on the stage.
-      const int ct = threadIdx.x - 10 * 32;   // 0..255
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
-        const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-        for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (it / S) & 1u;
-          const int ws_ = it % C::kW8Slots;
-          if (!mbar_wait_bounded(&wfull[ws_], (it / C::kW8Slots) & 1u, s_abort, p.status, 540 + ws_)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 560 + s)) { ok = false; break; }
-          const int src = (kb < p.kb0) ? 0 : 1;
-          const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
-          const uint8_t* q = smem + C::kW8Off + ws_ * C::kW8SlotBytes;
-          uint8_t* sB = smem + s * C::kStageBytes + kABytes;
-          const int64_t gbase = static_cast<int64_t>(t.g) * p.ws_gstride;
-          // rows / columns past the weight matrix hold zero codes (TMA fill):
-          // clamp their tile index into this matrix's tile grid
-          const int rtiles = static_cast<int>(p.ws_gstride / p.ws_cols);
-          // BN rows (K-major) or 4 MN atoms x 64 k-rows (MN-major), 4 chunks of 16 codes each
-          for (int task = ct; task < BN * 4; task += kConvWarps * 32) {
-            const int j = task & 3;
-            const int row = task >> 2;   // K-major: tile row n; MN-major: atom * 64 + k
-            uint4 codes;
-            float sc;
-            uint8_t* rowp;
-            int sw;
-            if (!B_MN) {
-              codes = *reinterpret_cast<const uint4*>(q + row * 64 + j * 16);
-              const int half = p.b_dual_n ? row / (BN / 2) : 0;
-              const int wrow = p.b_dual_n ? t.nt * (BN / 2) + (row - half * (BN / 2)) : t.nt * BN + row;
-              const float* ss = p.wscale[p.b_dual_n ? half : src];
-              sc = ss[gbase + static_cast<int64_t>(min(wrow / 128, rtiles - 1)) * p.ws_cols + min(k0 / 128, p.ws_cols - 1)];
-              rowp = sB + row * 128;
-              sw = row & 7;
-            } else {
-              const int a = row >> 6, k = row & 63;
-              codes = *reinterpret_cast<const uint4*>(q + a * 4096 + k * 64 + j * 16);
-              const int ncol = t.nt * BN + a * 64 + j * 16;
-              sc = p.wscale[src][gbase + static_cast<int64_t>(min((k0 + k) / 128, rtiles - 1)) * p.ws_cols +
-                                 min(ncol / 128, p.ws_cols - 1)];
-              rowp = sB + a * 8192 + k * 128;
-              sw = k & 7;
+      if (W8) {
+        // ---------------------------------------------------------- converters (FP8 weights)
+        // Each k-block: wait for its code slot and for the stage to be free,
+        // write the bf16 B tile (dequantised value = E4M3 code x its 128 x 128
+        // tile scale, rounded to bf16) in the 128-byte-swizzled layout of the
+        // MMA, release the slot and arrive on the stage.
+        const int ct = threadIdx.x - 10 * 32;   // 0..255
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = unit0; ok && tile < total_tiles; tile += ustride) {
+          const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+          for (int kb = 0; kb < t.num_kb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (it / S) & 1u;
+            const int ws_ = it % C::kW8Slots;
+            if (!mbar_wait_bounded(&wfull[ws_], (it / C::kW8Slots) & 1u, s_abort, p.status, 540 + ws_)) {
+              ok = false;
+              break;
             }
-            uint32_t w[8];
-            dequant16_scaled(codes, sc, w);
-            *reinterpret_cast<uint4*>(rowp + (((2 * j) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(rowp + (((2 * j + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&wempty[ws_]);
-            mbar_arrive(&full[s]);
+            if (!mbar_wait_bounded(&empty[s], ph ^ 1u, s_abort, p.status, 560 + s)) { ok = false; break; }
+            const int src = (kb < p.kb0) ? 0 : 1;
+            const int k0 = (src == 0 ? kb : kb - p.kb0) * BK;
+            const uint8_t* q = smem + C::kW8Off + ws_ * C::kW8SlotBytes;
+            uint8_t* sB = smem + s * C::kStageBytes + kABytes;
+            const int64_t gbase = static_cast<int64_t>(t.g) * p.ws_gstride;
+            // rows / columns past the weight matrix hold zero codes (TMA fill):
+            // clamp their tile index into this matrix's tile grid
+            const int rtiles = static_cast<int>(p.ws_gstride / p.ws_cols);
+            // BN rows (K-major) or 4 MN atoms x 64 k-rows (MN-major), 4 chunks of 16 codes each
+            for (int task = ct; task < BN * 4; task += kConvWarps * 32) {
+              const int j = task & 3;
+              const int row = task >> 2;   // K-major: tile row n; MN-major: atom * 64 + k
+              uint4 codes;
+              float sc;
+              uint8_t* rowp;
+              int sw;
+              if (!B_MN) {
+                codes = *reinterpret_cast<const uint4*>(q + row * 64 + j * 16);
+                const int half = p.b_dual_n ? row / (BN / 2) : 0;
+                const int wrow = p.b_dual_n ? t.nt * (BN / 2) + (row - half * (BN / 2)) : t.nt * BN + row;
+                const float* ss = p.wscale[p.b_dual_n ? half : src];
+                sc = ss[gbase + static_cast<int64_t>(min(wrow / 128, rtiles - 1)) * p.ws_cols + min(k0 / 128, p.ws_cols - 1)];
+                rowp = sB + row * 128;
+                sw = row & 7;
+              } else {
+                const int a = row >> 6, k = row & 63;
+                codes = *reinterpret_cast<const uint4*>(q + a * 4096 + k * 64 + j * 16);
+                const int ncol = t.nt * BN + a * 64 + j * 16;
+                sc = p.wscale[src][gbase + static_cast<int64_t>(min((k0 + k) / 128, rtiles - 1)) * p.ws_cols +
+                                   min(ncol / 128, p.ws_cols - 1)];
+                rowp = sB + a * 8192 + k * 128;
+                sw = k & 7;
+              }
+              uint32_t w[8];
+              dequant16_scaled(codes, sc, w);
+              *reinterpret_cast<uint4*>(rowp + (((2 * j) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(rowp + (((2 * j + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&wempty[ws_]);
+              mbar_arrive(&full[s]);
+            }
           }
         }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    if (CHUNKED && BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int q = warp & 3;           // TMEM lane quarter = tile rows 32q..32q+31
-    const int hf = (warp - 2) >> 2;   // column half of the tile
+    const int hf = (warp - EW) >> 2;   // column half of the tile
     const int r = q * 32 + lane;
     uint32_t tcount = 0;
     uint32_t nstore = 0;   // TMA stores this warp has issued (fp32 staging)
+    uint32_t chunk = 0;   // CHUNKED: chunks so far
     // EPI_BF16_ADD: this warp's 32 rows of the addend come into its own buffer by TMA in boxes of 64
     // columns, those of the next tile as soon as an output has left a buffer again: with one buffer
     // (256-column tiles, the warp's 128 columns) at the tile's end, with two at its start
@@ -1164,11 +1224,45 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
     if (EPI == EPI_BF16_ADD) ask(unit0);
     for (int tile = unit0; tile < total_tiles; tile += ustride, ++tcount) {
       const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
-      const uint32_t buf = tcount & 1u;
-      const uint32_t aph = (tcount >> 1) & 1u;
-      if (!mbar_wait_bounded(&tfull[buf], aph, s_abort, p.status, 400)) break;
-      tc_fence_after();
+      const uint32_t buf = SPLIT ? 0u : tcount & 1u;
+      const uint32_t aph = (SPLIT ? tcount : tcount >> 1) & 1u;
       const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
+      KeptBlock kept;                            // EPI_SWIGLU_BWD_C: the codes of the first 32 columns
+      uint32_t sum[CHUNKED ? BN / 32 : 1][16];   // and this thread's columns of dh, 16 an entry
+      if (CHUNKED) {
+#pragma unroll
+        for (int i = 0; i < (CHUNKED ? BN / 32 : 1); ++i) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[i][j] = 0u;
+        }
+        kept.load(p, r < t.rows_valid, t.row0 + r, t.nt * BN + hf * (BN / 2));
+        bool ok = true;
+        for (int ch = 0; ch < num_chunks(t.num_kb); ++ch, ++chunk) {
+          if (!mbar_wait_bounded(&tfull[chunk & 1u], (chunk >> 1) & 1u, s_abort, p.status, 400)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t at =
+              tmem_base + (chunk & 1u) * BN + (static_cast<uint32_t>(q * 32) << 16) + hf * (BN / 2);
+#pragma unroll
+          for (int i = 0; i < (CHUNKED ? BN / 32 : 1); ++i) {
+            uint32_t u[16];
+            tmem_ld_32x32b_x16(at + 16 * i, u);
+            tmem_wait_ld(u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              sum[i][j] = __float_as_uint(__uint_as_float(sum[i][j]) + __uint_as_float(u[j]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[chunk & 1u]), lead));
+            else mbar_arrive(&tempty[chunk & 1u]);
+          }
+        }
+        if (!ok) break;
+      } else {
+        if (!mbar_wait_bounded(&tfull[buf], aph, s_abort, p.status, 400)) break;
+        tc_fence_after();
+      }
       const bool row_ok = r < t.rows_valid;
       if (EPI == EPI_BF16 || EPI == EPI_F32) {
         int64_t grow;
@@ -1181,6 +1275,19 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         }
         const bool zero = t.num_kb == 0;
         const int c_begin = hf * (BN / 2);
+        auto add_rest = [&](uint32_t at, uint32_t (&lo)[16], uint32_t (&hi)[16]) {   // SPLIT: the other terms' sums
+          if (!SPLIT) return;
+          uint32_t u0[16], u1[16];
+          tmem_ld_32x32b_x16(at + BN, u0);
+          tmem_ld_32x32b_x16(at + BN + 16, u1);
+          tmem_wait_ld(u0);
+          reg_fence(u1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            lo[j] = __float_as_uint(__uint_as_float(lo[j]) + __uint_as_float(u0[j]));
+            hi[j] = __float_as_uint(__uint_as_float(hi[j]) + __uint_as_float(u1[j]));
+          }
+        };
         if (EPI == EPI_F32 && C::kWideStaging && PAIR && p.c_tma && (BN / 2) % 32 == 0) {
           // Weight gradients on CTA pairs: the warp's 32 rows x 32 columns go to a 4 KB
           // shared buffer (one row per lane, 128-byte swizzle: 16-byte chunk j
@@ -1208,6 +1315,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
             tmem_ld_32x32b_x16(tb + c_begin + 16, vb);
             tmem_wait_ld(va);
             reg_fence(vb);
+            add_rest(tb + c_begin, va, vb);
           }
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
@@ -1250,6 +1358,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               if (!zero) {
                 tmem_wait_ld(vc);
                 reg_fence(vd);
+                add_rest(tb + c_begin + 32 * (i + 1), vc, vd);
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -1281,6 +1390,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
             tmem_ld_32x32b_x16(tb + c_begin + 16, vb);
             tmem_wait_ld(va);
             reg_fence(vb);
+            add_rest(tb + c_begin, va, vb);
           }
           const int rr = lane & 15;
 #pragma unroll
@@ -1325,6 +1435,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               if (!zero) {
                 tmem_wait_ld(vc);
                 reg_fence(vd);
+                add_rest(tb + c_begin + 32 * (i + 1), vc, vd);
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -1628,21 +1739,13 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
         const int64_t grow = t.row0 + r;
         float g = 1.0f, dot = 0.0f;
         if (row_ok && p.row_w) g = p.row_w[p.w_map ? p.w_map[grow] : grow];
-        // the codes of the next 32 columns are asked for while these are worked on
-        KeptBlock kb;
-        kb.load(p, row_ok, grow, t.nt * BN + hf * (BN / 2));
 #pragma unroll 1
         for (int c = hf * (BN / 2); c < (hf + 1) * (BN / 2); c += 32) {
-          uint32_t d0[16], d1[16];
-          tmem_ld_32x32b_x16(tb + c, d0);
-          tmem_ld_32x32b_x16(tb + c + 16, d1);
           const int col = t.nt * BN + c;
           const bool ok = row_ok && col < p.n_size;   // n_size is a multiple of 32
           const int64_t off = grow * p.ld_out + col;
-          const KeptBlock cur = kb;
-          if (c + 32 < (hf + 1) * (BN / 2)) kb.load(p, row_ok, grow, col + 32);
-          tmem_wait_ld(d0);
-          reg_fence(d1);
+          const KeptBlock cur = kept;   // the codes of the next 32 columns are asked for while these are worked on
+          if (c + 32 < (hf + 1) * (BN / 2)) kept.load(p, row_ok, grow, col + 32);
           if (ok) {
             const float sa = mx_scale_value(cur.ea), sb = mx_scale_value(cur.eb);
             __nv_bfloat16* q1 = static_cast<__nv_bfloat16*>(p.out0) + off;
@@ -1658,9 +1761,9 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
                 e4m3x4_decode(cur.b[4 * i + k], a3);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const float dh = __uint_as_float(i == 0 ? d0[4 * k + j] : d1[4 * k + j]);
+                  const float dh = __uint_as_float(sum[CHUNKED ? i : 0][4 * k + j]);
                   const float x = a1[j] * sa, y = a3[j] * sb;
-                  const float sg = __fdividef(1.0f, 1.0f + __expf(-x));
+                  const float sg = sigmoid_ftz(x);
                   const float silu = x * sg;
                   const float hv = silu * y;
                   const float gd = g * dh;
@@ -1680,6 +1783,12 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
               st_global_32b(q3 + 16 * i, w3, p.out_wide != 0);
               st_global_32b(qh + 16 * i, wh, p.out_wide != 0);
             }
+          }
+          // the next 32 columns to where these were: the loop stays one body, the registers fixed names
+#pragma unroll
+          for (int i = 0; i + 2 < (CHUNKED ? BN / 32 : 1); ++i) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[i][j] = sum[i + 2][j];
           }
         }
         if (p.row_dot && row_ok) p.row_dot[static_cast<int64_t>(2 * t.nt + hf) * p.dot_ld + grow] = dot;
@@ -1725,7 +1834,7 @@ __global__ void __launch_bounds__(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThread
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && !CHUNKED) {
         if (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[buf]), lead));
         else mbar_arrive(&tempty[buf]);
       }
@@ -1846,6 +1955,12 @@ cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream
     attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(C::smem_bytes(C::kMaxG)));
     max_units = PAIR ? num_sms() / CN : num_sms();
+    if (attr_err == cudaSuccess && EPI == EPI_SWIGLU_BWD_C && !QUANT && !W8 && BN == 256) {
+      // the epilogue waits for registers that only a launch with kRegsLaunch a thread has
+      cudaFuncAttributes fa{};
+      attr_err = cudaFuncGetAttributes(&fa, kern);
+      if (attr_err == cudaSuccess && fa.numRegs < kRegsLaunch) attr_err = cudaErrorInvalidConfiguration;
+    }
     if (attr_err == cudaSuccess && PAIR) {
       cudaLaunchConfig_t cfg{};
       cudaLaunchAttribute at[1];
@@ -1854,7 +1969,7 @@ cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream
       at[0].val.clusterDim.y = 1;
       at[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(CN * max_units);
-      cfg.blockDim = dim3(QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads));
+      cfg.blockDim = dim3(threads_of(EPI, QUANT, W8));
       cfg.dynamicSmemBytes = C::smem_bytes(C::kMaxG);
       cfg.attrs = at;
       cfg.numAttrs = 1;
@@ -1865,7 +1980,7 @@ cudaError_t launch_impl(const KParams& kp, int64_t units_ub, cudaStream_t stream
   });
   if (attr_err != cudaSuccess) return attr_err;
   const int units = static_cast<int>(units_ub < max_units ? units_ub : max_units);
-  const int threads = QUANT ? kThreadsQ : (W8 ? kThreadsW8 : kThreads);
+  const int threads = threads_of(EPI, QUANT, W8);
   if (units_ub > max_units) pdl = false;   // several tiles a CTA: the start is not what counts
   if (!PAIR && !pdl) {
     kern<<<units, threads, smem, stream>>>(kp);
@@ -2241,7 +2356,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.in0 && !make_map(&kp.tmAs[0], o, 64, 32, false)) return cudaErrorInvalidValue;
     kp.c_rows = static_cast<int32_t>(a.max_rows);
   }
-  if (kp.ksplit > 1 && !kp.c_tma) return cudaErrorInvalidValue;   // partials leave through the TMA stores
+  if ((kp.ksplit > 1 || a.a_terms == 3) && !kp.c_tma) return cudaErrorInvalidValue;   // partials leave through the TMA stores
   const int64_t u = tiles_ub;
 
   if (BN == 32) return launch_impl<32, false, false, EPI_F32>(kp, u, stream);

@@ -106,7 +106,8 @@ RouterPlan router_plan(const moe_desc_t& d, size_t scratch) {
   for (int s = 1; s <= kRouterSlices && (s == 1 || (N + s - 1) / s >= 128); ++s) {
     if (s > 1 && router_bytes(d, p.m, s) > scratch) break;
     const double waves = static_cast<double>((units * s + at_once - 1) / at_once);
-    const double t = waves * work / s + s * traffic;
+    // (the terms' accumulators fill tensor memory: a tile's end, about 4, is not hidden behind the next)
+    const double t = waves * (work / s + (p.packed ? 0 : 4)) + s * traffic;
     if (!p.slices || t < best) {
       best = t;
       p.slices = s;

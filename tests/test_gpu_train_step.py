@@ -181,7 +181,7 @@ def _router(dl, x, wg, dxi, dwi, inplace=False, ws=None):
 
 @pytest.mark.parametrize("n,d,e", [(1, 64, 1), (1, 128, 9), (7, 192, 8), (63, 64, 17), (130, 320, 60), (257, 512, 16),
                                    (129, 1088, 64), (512, 256, 65), (1000, 448, 200), (2049, 576, 129), (300, 192, 1024),
-                                   (3000, 704, 256), (4096, 2048, 8)])
+                                   (3000, 704, 256), (4096, 2048, 8), (4096, 1088, 100)])
 def test_router_backward(n, d, e):
     """Three bf16 terms hold the 24 bits of an entry, two lose 2^-17 of it.  The tensor cores add 16 products at a
     time to an fp32 sum, each step off by less than 2^-23 of the magnitudes it has added; the terms' sums, the runs'
@@ -276,8 +276,13 @@ def _offsets(groups, rows, off, seed):
     return off
 
 
-@pytest.mark.parametrize("groups,rows,off", GROUPS)
-@pytest.mark.parametrize("d,f", [(64, 64), (192, 320), (512, 256), (1088, 704)])
+SWIGLU = [(g, r, o, d, f) for g, r, o in GROUPS for d, f in ((64, 64), (192, 320), (512, 256), (1088, 704))] + [
+    # several chunks of the contraction; tiles of 64, 128 and 256 columns and pairs of 256
+    (3, 300, [0, 10, 200, 300], 2624, 192), (2, 1900, None, 2688, 1024), (24, 4000, None, 1728, 1152),
+    (2, 5000, [0, 2100, 4990], 2624, 1088), (1, 2600, [0, 2600], 7168, 2048)]
+
+
+@pytest.mark.parametrize("groups,rows,off,d,f", SWIGLU)
 def test_swiglu_backward(groups, rows, off, d, f):
     """dh is off by (D / 16 + 4) 2^-23 of its magnitudes sum |dy||w2|; the sigmoid's exponential (intrinsic: 2 + 1.2 |a1|
     ulps) and quotient give it 2^-18 for |a1| below 16, s + silu (1 - s) as much of 1 + |a1|; one rounding to
