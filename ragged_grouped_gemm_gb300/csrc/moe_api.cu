@@ -76,7 +76,8 @@ struct RouterPlan {
   bool packed, pair;
   int slices, per;  // runs and the tokens of each but the last (a multiple of 128)
 };
-constexpr int kRouterSlices = 16;
+constexpr int kRouterSlices = 48;
+constexpr int64_t kRouterRun = 896;
 size_t router_terms_bytes(const moe_desc_t& d) {
   return align_up(static_cast<size_t>(d.n_tok) * 3 * moe::router_term_cols(d.n_exp) * 2);
 }
@@ -97,24 +98,30 @@ RouterPlan router_plan(const moe_desc_t& d, size_t scratch) {
   const int64_t N = d.n_tok, D = d.d_model;
   const int64_t units = ((p.m + (p.pair ? 255 : 127)) / (p.pair ? 256 : 128)) * ((D + 255) / 256);
   const int64_t at_once = std::max(1, moe::num_sms() / (p.pair ? 2 : 1));
-  // a wave of whole contractions: 64 tokens take four MMAs of about 0.085 us a term; partial
-  // products are read again at about 5 TB/s (they are written while the MMAs run)
-  const double work = static_cast<double>(N) / 64 * 4 * 0.085 * (p.packed ? 1 : 3);
-  const double traffic = 4.0 * p.m * D / 5e6;
+  // A run of `per` tokens costs its MMAs (64 tokens: four of about 0.085 us a term) and a tile's end of
+  // about 6 us, which the terms' accumulators, filling tensor memory, leave nothing to hide behind;
+  // partial products are written and read again at about 5 TB/s.  Waves that hold tiles of the short
+  // last run alone cost that run.  An accumulator's chain cuts about 1.5e-8 of a sum an addition of 16
+  // tokens, so runs are kept at kRouterRun tokens where the scratch holds that many (4096 x 7168, 256
+  // experts: runs of 512 to 1024 tokens 84, 88, 86, 81 and 83 us, off by 5.0, 6.2, 7.5, 8.7 and 10.3e-7 of
+  // the gradient's norm; one of 2048 74 us and 19e-7).
+  auto cost = [&](int64_t rows) { return static_cast<double>(rows) / 64 * 4 * 0.085 * (p.packed ? 1 : 3) + (p.packed ? 0 : 6); };
   double best = 0;
   p.slices = 0;
-  for (int s = 1; s <= kRouterSlices && (s == 1 || (N + s - 1) / s >= 128); ++s) {
-    if (s > 1 && router_bytes(d, p.m, s) > scratch) break;
-    const double waves = static_cast<double>((units * s + at_once - 1) / at_once);
-    // (the terms' accumulators fill tensor memory: a tile's end, about 4, is not hidden behind the next)
-    const double t = waves * (work / s + (p.packed ? 0 : 4)) + s * traffic;
+  const int64_t first = N > kRouterRun * kRouterSlices ? (N / kRouterSlices + 127) / 128 * 128 : 128;
+  for (int64_t per = first; per <= std::max<int64_t>(kRouterRun, (N + 127) / 128 * 128); per += 128) {
+    const int64_t slices = (N + per - 1) / per;
+    if (slices > kRouterSlices || (slices > 1 && router_bytes(d, p.m, static_cast<int>(slices)) > scratch)) continue;
+    if (p.slices && per > kRouterRun) break;
+    const int64_t full = units * (N / per), waves = (full + at_once - 1) / at_once;
+    const double t = waves * cost(per) + ((units * slices + at_once - 1) / at_once - waves) * cost(N % per) +
+                     slices * (8.0 * p.m * D / 5e6);
     if (!p.slices || t < best) {
       best = t;
-      p.slices = s;
+      p.slices = static_cast<int>(slices);
+      p.per = static_cast<int>(per);
     }
   }
-  p.per = static_cast<int>(((N + p.slices - 1) / p.slices + 127) / 128 * 128);
-  p.slices = static_cast<int>((N + p.per - 1) / p.per);
   return p;
 }
 
@@ -200,8 +207,9 @@ WsLayout layout(const moe_desc_t& d) {
   const size_t norm = align_up(moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
   L.norm = norm <= L.gmaps - L.dl ? L.dl : o;
   if (L.norm == o) o += norm;
-  // the dense router gradient too, over the same scratch where one run of tokens fits
-  const size_t router = router_bytes(d, router_rows(d), 1);
+  // the dense router gradient too, over the same scratch where its runs of tokens fit
+  const size_t router = router_bytes(
+      d, router_rows(d), static_cast<int>(std::clamp<int64_t>((N + kRouterRun - 1) / kRouterRun, 1, kRouterSlices)));
   const bool over = router <= L.gmaps - L.dl;
   L.rterms = over ? L.dl : o;
   if (!over) o += router;
