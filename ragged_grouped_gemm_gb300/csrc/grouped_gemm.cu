@@ -149,8 +149,17 @@ struct KParams {
 };
 
 // The per-group maps of a ragged-K launch: thread g writes group g's copy of
-// the A and B maps, rebased to the group's first row with a row extent of
+// the A and B templates, rebased to the group's first row with a row extent of
 // the group's row count (at least 1; an empty group is never loaded).
+//
+// The templates are encoded for one row.  A map encoded for 128 KB or more has
+// the TMA unit read memory for the rows of a box that lie outside the tensor too
+// (their values are dropped): one row of a 64-row box costs 95 requests to L2 by a
+// map encoded for 152,832 bytes and 24 by one for 127,360, whatever the extents
+// that replaced the encoded ones, and the same at a row pitch of 128 bytes, so
+// these reads stay near the tensor's start.  A whole tensor has its own bytes
+// there; a group of a few rows at an allocation's end has not, and such a launch
+// ended with an illegal address.  One row of 128 KB or more holds those bytes.
 __global__ void build_group_maps_kernel(CUtensorMap* out, const __grid_constant__ CUtensorMap ta,
                                         const __grid_constant__ CUtensorMap tb, const int32_t* __restrict__ offsets,
                                         int G, const char* a_ptr, int64_t a_ld_bytes, const char* b_ptr,
@@ -2306,25 +2315,31 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     kp.tmB[1] = kp.tmB[0];
     if (a.a_terms > 1 && (a.a_terms != 3 || !a.aligned_groups)) return cudaErrorInvalidValue;
     kp.a_term_cols = a.a_term_cols;
+    CUtensorMap ta = kp.tmA[0], tb = kp.tmB[0];   // what the groups' maps are made from: one row
+    if (a.checked || (a.num_groups > 1 && !a.aligned_groups)) {
+      Operand ra = a.a[0], rb = a.b[0];
+      ra.rows = rb.rows = 1;
+      if (!make_map(&ta, ra, 64, kbr, false) || !make_map(&tb, rb, 64, kbr, false)) return cudaErrorInvalidValue;
+    }
     if (a.checked) {
       if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 || a.aligned_groups)
         return cudaErrorInvalidValue;
       CUtensorMap* maps = static_cast<CUtensorMap*>(a.map_ws);
       const cudaError_t e = launch_pdl(checked_group_maps_kernel, 1, (a.num_groups + 31) / 32 * 32, 0, stream, maps,
-                                       kp.tmA[0], kp.tmB[0], a.offsets, a.num_groups, static_cast<int>(a.max_rows),
+                                       ta, tb, a.offsets, a.num_groups, static_cast<int>(a.max_rows),
                                        a.checked, a.status, static_cast<const char*>(a.a[0].ptr), a.a[0].ld * 2,
                                        static_cast<const char*>(a.b[0].ptr), a.b[0].ld * 2);
       if (e != cudaSuccess) return e;
       kp.gmaps = maps;
       kp.offsets = a.checked;
     } else if (a.num_groups > 1 && !a.aligned_groups) {
-      // every group's own maps (copies of these two, rebased), written just before the GEMM
+      // every group's own maps (rebased copies of one map an operand), written just before the GEMM
       if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 ||
           2 * static_cast<size_t>(a.num_groups) * sizeof(CUtensorMap) > kGemmMapScratchBytes)
         return cudaErrorInvalidValue;
       CUtensorMap* maps = static_cast<CUtensorMap*>(a.map_ws);
       build_group_maps_kernel<<<(a.num_groups + 127) / 128, 128, 0, stream>>>(
-          maps, kp.tmA[0], kp.tmB[0], a.offsets, a.num_groups, static_cast<const char*>(a.a[0].ptr), a.a[0].ld * 2,
+          maps, ta, tb, a.offsets, a.num_groups, static_cast<const char*>(a.a[0].ptr), a.a[0].ld * 2,
           static_cast<const char*>(a.b[0].ptr), a.b[0].ld * 2);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;

@@ -373,6 +373,29 @@ def test_wgrad(groups, rows, off, m, k, top_k):
         assert (np.abs(np32(ident) - want) <= steps * 2.0 ** -23 * mag).all()
 
 
+@pytest.mark.parametrize("groups,off", [(5, [0, 0, 9, 22, 23, 24]), (8, [0, 1, 1, 1, 7, 20, 20, 23, 24])])
+@pytest.mark.parametrize("m,k", [(192, 12736), (12736, 192)])
+def test_wgrad_of_few_rows_at_an_allocations_end(groups, off, m, k):
+    """Rows of 128 KB or more in all, in groups of less that end with their allocations."""
+    rows = off[-1]
+    g = torch.Generator().manual_seed(groups + m)
+    torch.cuda.empty_cache()
+    need = api.moe_grouped_wgrad_ckpt_workspace_size(groups, rows, m, k)
+    hold = [torch.empty(20 << 20, dtype=U8, device="cuda") for _ in range(2)]
+    ws = hold[0][(20 << 20) - -(-need // 256) * 256:]
+    api.moe_workspace_init(ws)
+    dy = hold[1][(20 << 20) - 2 * rows * m:].view(BF16).view(rows, m)
+    dy.copy_(torch.randn(rows, m, generator=g))
+    codes, scales = _keep(torch.randn(rows, k, generator=g).to(BF16).cuda())
+    dw = torch.full((groups, m, k), 7.0, device="cuda")
+    api.moe_grouped_wgrad_ckpt(dy, codes, scales, torch.tensor(off, dtype=I32, device="cuda"), None, 1, dw, ws)
+    assert _status(ws) == 0
+    x, dyh = O.kept_values(codes.cpu().numpy(), scales.cpu().numpy()), np32(dy).astype(np.float64)
+    want = O.wgrad_kept(dyh, x, off, np.arange(rows), 1)
+    mag = O.wgrad_kept(np.abs(dyh), np.abs(x), off, np.arange(rows), 1)
+    assert (np.abs(np32(dw) - want) <= (max(np.diff(off)) / 16 + 4) * 2.0 ** -23 * mag).all()
+
+
 def test_kept_products_report_offsets_and_indices():
     groups, rows, d, f = 3, 200, 64, 128
     g = torch.Generator().manual_seed(3)
