@@ -75,14 +75,14 @@ __global__ void __launch_bounds__(256) mx_dequant_rows_kernel(const uint2* __res
 
 // 32 rows a block; its eight warps take every eighth slice, and their sums are added in order.
 __global__ void __launch_bounds__(256) row_dot_sum_kernel(const float* __restrict__ part, int64_t slices, int64_t ld,
-                                                          const int32_t* __restrict__ offsets, int groups,
+                                                          const int32_t* __restrict__ offsets, int groups, int64_t rows,
                                                           float* __restrict__ dg) {
   __shared__ float s_sum[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  const bool in = r >= offsets[0] && r < offsets[groups];
+  const bool in = r >= offsets[0] && r < offsets[groups] && r < rows;
   float s = 0.0f;
   if (in) {
 #pragma unroll 8
@@ -154,7 +154,7 @@ cudaError_t launch_row_dot_sum(const float* part, int64_t slices, int64_t ld, co
                                int64_t rows, float* dg, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   return launch_pdl(row_dot_sum_kernel, static_cast<unsigned>((rows + 31) / 32), 256, 0, st, part, slices, ld, offsets,
-                    groups, dg);
+                    groups, rows, dg);
 }
 
 cudaError_t launch_gate_bwd(int n_tok, int top_k, int gate, const float* dg_row, const int32_t* row_of_copy,
