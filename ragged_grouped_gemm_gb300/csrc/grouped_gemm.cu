@@ -74,7 +74,7 @@ constexpr int kThreadsQ = 448;       // + 4 scale-factor warps (MXFP8 operands)
 constexpr int kThreadsW8 = 576;      // + 8 converter warps (FP8 weights)
 constexpr int kThreadsC = 384;       // CHUNKED: three warpgroups, the epilogue in two of them
 constexpr int kConvWarps = 8;
-constexpr int kChunk = 13;           // k-blocks of 64 elements a chunk, about (CHUNKED)
+constexpr int kChunk = 13;           // k-blocks of 64 elements a chunk (CHUNKED)
 // CHUNKED on 256-column tiles: registers a thread at launch, of the first warpgroup and of the epilogue's
 constexpr int kRegsLaunch = 168, kRegsFirst = 40, kRegsEpi = 232;
 static_assert(128 * kRegsFirst + 256 * kRegsEpi <= kThreadsC * kRegsLaunch, "more registers than the block has");
@@ -480,22 +480,15 @@ struct KeptBlock {
   }
 };
 
+// CHUNKED: the chunks of a contraction of n k-blocks.  What the chains cut is in proportion to their length (13: 8e-7
+// of a sum, 16: 1e-6).  Two longer ones at a tile's start, while the epilogue of the tile before keeps the warps, gave
+// 704 for 717 us in CTA pairs (8192 rows, 14336 x 4096) and took 340 for 332 in single ones (2048 x 7168).
+__device__ __forceinline__ int num_chunks(int n) { return (n + kChunk - 1) / kChunk; }
+
 // GATHER (ragged M, bf16, one contraction source): A rows are gathered from
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
 // instruction, every lane of the producer warp taking four of the tile's
 // 128 rows; no permuted copy of the tokens is read.
-// CHUNKED: the chunks of a contraction of n k-blocks, and the first k-block of chunk ch.  What the chains cut is in
-// proportion to the mean of the chunks' squared lengths over n (8e-7 of a sum where all are 13); the first two
-// are longer where there are several, because they run while the epilogue of the tile before keeps the warps
-// that would empty a third.
-__device__ __forceinline__ int num_chunks(int n) { return (n + kChunk - 1) / kChunk; }
-__device__ __forceinline__ int chunk_start(int ch, int n) {
-  const int nch = num_chunks(n);
-  if (nch < 4) return ch * n / max(nch, 1);
-  constexpr int kLong = kChunk + 5;
-  return ch <= 2 ? ch * kLong : 2 * kLong + (ch - 2) * (n - 2 * kLong) / (nch - 2);
-}
-
 // TERMS (bf16, at most 2 with ragged M): every k-block multiplies that many tiles of A by one of B
 // into the same accumulator.
 template <int BN, bool A_MN, bool B_MN, int EPI, bool QUANT, bool PAIR, bool W8 = false, bool GATHER = false,

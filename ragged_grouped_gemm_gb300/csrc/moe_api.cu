@@ -1444,6 +1444,9 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
     return MOE_OK;
   }
   const WsLayout L = layout(*d);
+  if (E <= moe::kRouterFew)
+    return cuda_status(moe::launch_router_few(dlogits, x, w_gate, dx_in, dx, at<float>(ws, L.rterms), L.rend - L.rterms,
+                                              N, D, E, dw_in, dw_gate, st));
   const RouterPlan plan = router_plan(*d, L.rend - L.rterms);
   const int e8 = plan.e8;
   char* terms = at<char>(ws, L.rterms);

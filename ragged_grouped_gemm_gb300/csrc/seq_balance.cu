@@ -491,6 +491,200 @@ __global__ void __launch_bounds__(256) router_dw_kernel(const V* __restrict__ pa
   dw[o] = acc;
 }
 
+// ---- few experts: the dense router gradient in one pass
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16; lane l holds rows l / 4 and l / 4 + 8 of A and D, column l / 4 of B.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of bf16 across the warp: lane l holds row l / 4, columns 2 (l % 4) and the next.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// The next bf16 term of two numbers, which keep what remains; a number that is not finite is its first term alone.
+__device__ __forceinline__ uint32_t next_term(float2& v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  const float2 r = __bfloat1622float2(h);
+  v.x = isfinite(r.x) ? v.x - r.x : 0.0f;
+  v.y = isfinite(r.y) ? v.y - r.y : 0.0f;
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+//   dx_t = dx_in_t + sum_e dl_te W_e,   dw_e = dw_in_e + sum_t dl_te x_t   for up to 8 * H experts (H 1, 2)
+// tcgen05's tiles of 128 rows would be an eighth full at most, and its two products read x, the addend and dl (as
+// bf16 terms that a third kernel makes) in launches of their own; here each is read once and what bounds it is
+// that traffic (4096 x 4096, 8 experts: 100 MB).  The same on the FMA units took 30 us with 8 experts
+// and 50 with 16, by their instructions.
+//
+// A warp takes 16 tokens x 64 columns a turn: x and the addend come straight into the layout of D, 16 bytes a lane,
+// the columns of the eight 16 x 8 tiles being dealt so that a lane's lie together (column c of the 64 in tile
+// t = c / 32 * 4 + c % 8 / 2, as column c % 32 / 8 * 2 + c % 2); a transpose in registers makes x the
+// B of the second product, and dl's terms their A's.  dx, which bf16 holds to 2^-9, takes two terms of dl (a third: 26 us
+// for 24), dw three; K of the first product is terms and experts, the first term of the second has an accumulator of its
+// own (rows or registers).  W stays in registers.  The block's warps
+// lie cw along the columns, the others take other tokens and are joined at the end.
+// warps of a block and blocks an SM: 128 registers a thread, or 168
+template <int H> constexpr int kFewWarps = H == 1 ? 8 : 4;
+template <int H> constexpr int kFewBlocks = H == 1 ? 2 : 3;
+constexpr int kFewTurns = 56;   // of a warp, about, that one accumulator adds (1.5e-8 of a sum is cut at each)
+template <int H>
+__global__ void __launch_bounds__(kFewWarps<H> * 32, kFewBlocks<H>) router_few_kernel(
+    const float* __restrict__ dl, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wg,
+    const __nv_bfloat16* dx_in, __nv_bfloat16* dx, const float* dw_in, float* dw, int N, int D, int E, int per, int cw) {
+  __shared__ float s_sum[kFewWarps<H>][16][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int tw = kFewWarps<H> / cw, wc = warp % cw, wt = warp / cw;
+  const int col0 = (static_cast<int>(blockIdx.x) * cw + wc) * 64;
+  const bool on = col0 < D;
+  pdl_trigger();
+  pdl_wait();
+  uint32_t wf[8][H];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const int c = col0 + t / 4 * 32 + g / 2 * 8 + t % 4 * 2 + g % 2;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int e = 8 * h + 2 * q;
+      const uint32_t lo = on && e < E ? __ldg(reinterpret_cast<const uint16_t*>(wg) + static_cast<int64_t>(e) * D + c) : 0u;
+      const uint32_t hi = on && e + 1 < E ? __ldg(reinterpret_cast<const uint16_t*>(wg) + static_cast<int64_t>(e + 1) * D + c) : 0u;
+      wf[t][h] = lo | hi << 16;
+    }
+  }
+  float acc[H][8][4];   // H 1: rows 0-7 the first term, 8-15 the others; H 2: [0] the first, [1] the others
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[h][t][i] = 0.0f;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * per;
+  const int64_t t1 = min(static_cast<int64_t>(N), t0 + per);
+  for (int64_t base = t0 + 16 * wt; on && base < t1; base += 16 * tw) {
+    uint4 xv[2][2], av[2][2];   // [rows g, g + 8][columns 8q.., 32 + 8q..]
+    float2 v[2][H];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t t = base + g + 8 * r;
+      const bool in = t < t1;
+      const int64_t o = t * D + col0 + 8 * q;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        xv[r][k] = av[r][k] = make_uint4(0, 0, 0, 0);
+        if (in) xv[r][k] = __ldg(reinterpret_cast<const uint4*>(x + o + 32 * k));
+        if (in && dx_in) av[r][k] = *reinterpret_cast<const uint4*>(dx_in + o + 32 * k);
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int e = 8 * h + 2 * q;
+        v[r][h].x = in && e < E ? __ldg(dl + t * E + e) : 0.0f;
+        v[r][h].y = in && e + 1 < E ? __ldg(dl + t * E + e + 1) : 0.0f;
+      }
+    }
+    uint32_t term[3][2][H];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int h = 0; h < H; ++h) term[i][r][h] = next_term(v[r][h]);
+    // dx: the addend and two terms
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      uint32_t* p0 = reinterpret_cast<uint32_t*>(&av[0][t / 4]) + t % 4;
+      uint32_t* p1 = reinterpret_cast<uint32_t*>(&av[1][t / 4]) + t % 4;
+      float c[4] = {__uint_as_float(*p0 << 16), __uint_as_float(*p0 & 0xffff0000u), __uint_as_float(*p1 << 16),
+                    __uint_as_float(*p1 & 0xffff0000u)};
+      if (H == 1) {
+        const uint32_t a[4] = {term[0][0][0], term[0][1][0], term[1][0][0], term[1][1][0]};
+        mma_16x8x16(c, a, wf[t][0], wf[t][0]);
+      } else {
+#pragma unroll
+        for (int i = 1; i >= 0; --i) {
+          const uint32_t a[4] = {term[i][0][0], term[i][1][0], term[i][0][H - 1], term[i][1][H - 1]};
+          mma_16x8x16(c, a, wf[t][0], wf[t][H - 1]);
+        }
+      }
+      const __nv_bfloat162 r0 = __floats2bfloat162_rn(c[0], c[1]), r1 = __floats2bfloat162_rn(c[2], c[3]);
+      *p0 = *reinterpret_cast<const uint32_t*>(&r0);
+      *p1 = *reinterpret_cast<const uint32_t*>(&r1);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t t = base + g + 8 * r;
+      if (t < t1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(dx + t * D + col0 + 8 * q + 32 * k) = av[r][k];
+      }
+    }
+    // dw: three terms, x and they transposed
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int h = 0; h < H; ++h) term[i][r][h] = transpose8(term[i][r][h]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t b0 = transpose8(reinterpret_cast<const uint32_t*>(&xv[0][t / 4])[t % 4]);
+      const uint32_t b1 = transpose8(reinterpret_cast<const uint32_t*>(&xv[1][t / 4])[t % 4]);
+      if (H == 1) {
+        const uint32_t a[4] = {term[0][0][0], term[1][0][0], term[0][1][0], term[1][1][0]};
+        const uint32_t a2[4] = {0u, term[2][0][0], 0u, term[2][1][0]};
+        mma_16x8x16(acc[0][t], a, b0, b1);
+        mma_16x8x16(acc[0][t], a2, b0, b1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t a[4] = {term[i][0][0], term[i][0][H - 1], term[i][1][0], term[i][1][H - 1]};
+          mma_16x8x16(acc[i > 0 ? H - 1 : 0][t], a, b0, b1);
+        }
+      }
+    }
+  }
+  // eight experts at a time: the terms' sums, then the warps', in order
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        s_sum[warp][2 * t + i][lane] = H == 1 ? acc[0][t][i] + acc[0][t][2 + i] : acc[0][t][2 * h + i] + acc[H - 1][t][2 * h + i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < cw * 512; o += kFewWarps<H> * 32) {
+      const int c = o % 64, e = 8 * h + o / 64 % 8, w = o / 512, col = (static_cast<int>(blockIdx.x) * cw + w) * 64 + c;
+      const int t = c / 32 * 4 + c % 8 / 2;
+      float v = 0.0f;
+      for (int k = 0; k < tw; ++k) v += s_sum[k * cw + w][2 * t + c % 2][e % 8 * 4 + c % 32 / 8];
+      if (e < E && col < D) {
+        const int64_t i = (static_cast<int64_t>(blockIdx.y) * E + e) * D + col;
+        dw[i] = dw_in ? dw_in[i] + v : v;
+      }
+    }
+  }
+}
+
+// dw = dw_in + the runs' partial products: 32 numbers a block, its warps take the runs in turn and are joined in order.
+__global__ void __launch_bounds__(256) router_few_sum_kernel(const float* __restrict__ part, int runs, int64_t n,
+                                                             const float* dw_in, float* dw) {
+  __shared__ float s_sum[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // n is a multiple of 32
+  pdl_trigger();
+  pdl_wait();
+  float s = 0.0f;
+#pragma unroll 4
+  for (int r = warp; r < runs; r += 8) s += __ldcg(part + r * n + o);
+  s_sum[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int k = 1; k < 8; ++k) s += s_sum[k][lane];
+  dw[o] = (dw_in ? dw_in[o] : 0.0f) + s;
+}
+
 }  // namespace
 
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
@@ -557,6 +751,57 @@ cudaError_t launch_router_dw(const float* part, int n_slices, int terms, int n_e
                       n_slices, n / 4, term / 4, reinterpret_cast<const float4*>(dw_in), reinterpret_cast<float4*>(dw));
   return launch_pdl(terms == 3 ? router_dw_kernel<3, float> : router_dw_kernel<1, float>,
                     static_cast<unsigned>((n + 255) / 256), 256, 0, st, part, n_slices, n, term, dw_in, dw);
+}
+
+cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate, const void* dx_in, void* dx,
+                              float* part, size_t part_bytes, int n_tok, int d, int n_exp, const float* dw_in,
+                              float* dw, cudaStream_t st) {
+  if (n_exp > kRouterFew || n_tok < 1 || d % 64) return cudaErrorInvalidValue;
+  // Warps along the columns and runs of tokens: about 2.2 us a turn of all the warps' 16 tokens x 64 columns;
+  // partial products are written and read again by a launch of its own
+  const bool two = n_exp > 8;
+  const int strips64 = d / 64, warps = two ? kFewWarps<2> : kFewWarps<1>;
+  const int at_once = num_sms() * (two ? kFewBlocks<2> : kFewBlocks<1>);
+  const int64_t fit = std::min<int64_t>(kRouterFewRuns, static_cast<int64_t>(part_bytes / (sizeof(float) * n_exp * d)));
+  int cw = 1;
+  int64_t per = n_tok, runs = 1;
+  double best = 0;
+  for (int w = 1; w <= warps; w *= 2) {
+    const int64_t strips = (strips64 + w - 1) / w, tile = 16 * (warps / w);   // tokens of a block's turn
+    const int64_t turns_all = (n_tok + tile - 1) / tile;
+    for (int64_t r = 1; r <= std::max<int64_t>(1, std::min(fit, turns_all)); ++r) {
+      const int64_t turns = (turns_all + r - 1) / r, n = (turns_all + turns - 1) / turns;
+      const int64_t waves = (strips * n + at_once - 1) / at_once;
+      const double t = waves * (2.2 * turns + 1) + (n > 1 ? 3 + n * n_exp * d * 8.0 / 5e6 : 0) +
+                       (turns > kFewTurns ? turns - kFewTurns : 0);
+      if (best == 0 || t < best) {
+        best = t;
+        cw = w;
+        runs = n;
+        per = turns * tile;
+      }
+    }
+  }
+  const int strips = (strips64 + cw - 1) / cw;
+  auto kern = two ? router_few_kernel<2> : router_few_kernel<1>;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(runs));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const auto* xb = static_cast<const __nv_bfloat16*>(x);
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, kern, dl, xb, static_cast<const __nv_bfloat16*>(w_gate), static_cast<const __nv_bfloat16*>(dx_in),
+      static_cast<__nv_bfloat16*>(dx), runs > 1 ? nullptr : dw_in, runs > 1 ? part : dw, n_tok, d, n_exp,
+      static_cast<int>(per), cw);
+  if (e != cudaSuccess || runs == 1) return e;
+  const int64_t n = static_cast<int64_t>(n_exp) * d;
+  return launch_pdl(router_few_sum_kernel, static_cast<unsigned>(n / 32), 256, 0, st, const_cast<const float*>(part),
+                    static_cast<int>(runs), n, dw_in, dw);
 }
 
 }  // namespace moe

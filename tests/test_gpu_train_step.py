@@ -207,6 +207,27 @@ def test_router_backward(n, d, e):
     assert torch.equal(dx, ix) and torch.equal(dw, iw)
 
 
+@pytest.mark.parametrize("n,d,e", [(1, 64, 2), (2, 4096, 3), (5, 192, 5), (33, 1088, 1), (129, 64, 7), (500, 576, 2), (1001, 256, 4),
+                                   (2600, 128, 16), (2047, 1984, 12), (3000, 1024, 8), (7000, 320, 3), (20000, 64, 9)])
+def test_router_backward_of_few_experts(n, d, e):
+    """Three bf16 terms of an entry are the entry but for 2^-24 of it, two (dx) but for 2^-17: a bf16 number is off by
+    2^-9 of what it is made from at most, so what two leave is 2^-18 of it.  The tensor cores add 16 products at a time
+    to an fp32 number, each step off by less than 2^-23 of the magnitudes it has added: two steps for dx, which is
+    rounded to bf16 once; for a weight's gradient two for every 16 tokens, and 64 sums of warps, runs and the addend at most."""
+    g = torch.Generator().manual_seed(n + d + e)
+    dl = (torch.randn(n, e, generator=g) * torch.exp(2 * torch.randn(n, 1, generator=g)) * 1e-2).cuda()
+    x, wg = torch.randn(n, d, generator=g).to(BF16).cuda(), (torch.randn(e, d, generator=g) * 0.1).to(BF16).cuda()
+    dxi, dwi = torch.randn(n, d, generator=g).to(BF16).cuda(), torch.randn(e, d, generator=g).cuda()
+    dl64, x64, w64 = dl.cpu().double().numpy(), np32(x).astype(np.float64), np32(wg).astype(np.float64)
+    dx, dw = _router(dl, x, wg, dxi, dwi)
+    rx, rw = O.router_backward(dl64, x64, w64, np32(dxi).astype(np.float64), np32(dwi).astype(np.float64))
+    mag_x, mag_w = np.abs(dl64) @ np.abs(w64) + np.abs(np32(dxi)), np.abs(dl64).T @ np.abs(x64) + np.abs(np32(dwi))
+    assert (np.abs(np32(dx) - rx) <= 2.0 ** -8 * np.abs(rx) + (2.0 ** -17 + 2 * 2.0 ** -23) * mag_x * (1 + 2.0 ** -8)).all()
+    assert (np.abs(np32(dw).astype(np.float64) - rw) <= (2 * (n / 16 + 1) + 64) * 2.0 ** -23 * mag_w).all()
+    again = _router(dl, x, wg, dxi, dwi, inplace=True)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
 def test_router_backward_not_finite_and_no_tokens():
     n, d, e = 40, 128, 16
     g = torch.Generator().manual_seed(0)
