@@ -652,3 +652,94 @@ def test_gradient_of_the_kept_backward_against_differences():
         num = (at(step) - at(-step)) / (2 * step)
         got = np32(grad).astype(np.float64)
         assert abs(num - (got * v).sum()) <= (2.0 ** -8 * np.abs(got * v)).sum() + step ** 2 * np.abs(v ** 3).sum() * 10
+
+
+class _User:
+    """What one user of the entry points holds: inputs, a workspace for each call, outputs."""
+
+    def __init__(self, seed, n=300, d=192, f=320, e=8, many=40, k=2):
+        g = torch.Generator().manual_seed(seed)
+        r = n * k
+        self.lg, self.idx = _routed(n, e, k, seed)
+        self.off = torch.tensor([0, 100 + seed, n], dtype=I32, device="cuda")
+        self.desc = api.make_desc(MoEConfig("case", n, d, 64, e, k))
+        self.wide = api.make_desc(MoEConfig("case", n, d, 64, many, k))
+        rand = lambda *s: torch.randn(*s, generator=g).to(BF16).cuda()  # noqa: E731
+        self.x, self.wg, self.wgm, self.dx_in, self.dy = rand(n, d), rand(e, d), rand(many, d), rand(n, d), rand(r, d)
+        self.w2, self.dlm = rand(e, d, f), torch.randn(n, many, generator=g).cuda()
+        self.c, self.s = _keep(rand(r, f))
+        self.cx, self.sx = _keep(self.x)
+        self.rmap = torch.randint(0, r, (r,), generator=g).to(I32).cuda()   # rows more than once
+        self.offs = torch.tensor(_offsets(e, r, None, seed), dtype=I32, device="cuda")
+        size = [api.moe_workspace_size(self.desc)[1], api.moe_workspace_size(self.desc)[1], api.moe_workspace_size(self.wide)[1],
+                api.moe_swiglu_backward_ckpt_workspace_size(e, r, d, f), api.moe_grouped_wgrad_ckpt_workspace_size(e, r, d, d)]
+        self.ws = [torch.empty(b, dtype=U8, device="cuda") for b in size]
+        for w in self.ws:
+            api.moe_workspace_init(w)
+        empty = lambda *s, dt=BF16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+        self.out = dict(counts=empty(2, e, dt=I32), loss=empty(2, dt=F32), dl=empty(n, e, dt=F32), dx=empty(n, d),
+                        dwg=empty(e, d, dt=F32), dxm=empty(n, d), dwm=empty(many, d, dt=F32), da1=empty(r, f), da3=empty(r, f),
+                        h=empty(r, f), dg=empty(r, dt=F32), dw=empty(e, d, d, dt=F32), xd=empty(n, d))
+
+    def run(self, stream=None):
+        o = self.out
+        api.moe_balance_loss(self.desc, self.lg, self.idx, self.off, o["counts"], o["loss"], o["dl"], self.ws[0], 0.01, 0.001,
+                             None, stream=stream)
+        api.moe_router_backward(self.desc, o["dl"], self.x, self.wg, self.dx_in, o["dx"], None, o["dwg"], self.ws[1],
+                                stream=stream)
+        api.moe_router_backward(self.wide, self.dlm, self.x, self.wgm, self.dx_in, o["dxm"], None, o["dwm"], self.ws[2],
+                                stream=stream)
+        api.moe_swiglu_backward_ckpt(self.dy, self.offs, self.w2, None, self.c, self.s, self.c, self.s, o["da1"], o["da3"],
+                                     o["h"], o["dg"], self.ws[3], stream=stream)
+        api.moe_grouped_wgrad_ckpt(self.dy, self.cx, self.sx, self.offs, self.rmap, 2, o["dw"], self.ws[4], stream=stream)
+        api.moe_dequantize_mxfp8(self.cx, self.sx, o["xd"], stream=stream)
+
+    def take(self):
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in self.out.items()}
+        for v in self.out.values():
+            v.zero_()
+        torch.cuda.synchronize()
+        return got
+
+
+def test_entry_points_at_once_on_two_streams_and_captured():
+    users = [_User(1), _User(2)]
+    want = []
+    for u in users:
+        u.run()
+        want.append(u.take())
+        x = O.kept_values(u.cx.cpu().numpy(), u.sx.cpu().numpy())
+        off, rmap, dy = u.offs.cpu().numpy(), u.rmap.cpu().numpy(), np32(u.dy).astype(np.float64)
+        ref, mag = O.wgrad_kept(dy, x, off, rmap, 2), O.wgrad_kept(np.abs(dy), np.abs(x), off, rmap, 2)
+        steps = np.diff(off).max() / 16 + 4
+        assert (np.abs(np32(want[-1]["dw"]) - ref) <= steps * 2.0 ** -23 * mag).all()
+    streams = [torch.cuda.Stream() for _ in users]
+    for _ in range(5):
+        for u, s in zip(users, streams):
+            u.run(s)
+    for u, w in zip(users, want):
+        got = u.take()
+        for key in w:
+            assert torch.equal(got[key], w[key]), key
+    graphs = []
+    for u in users:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            u.run()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    for u, w in zip(users, want):
+        got = u.take()
+        for key in w:
+            assert torch.equal(got[key], w[key]), key
+        assert all(_status(ws) == 0 for ws in u.ws)
+
+
+def test_balance_loss_of_an_expert_chosen_twice():
+    lg, _ = _routed(200, 12, 2, 3)
+    idx = torch.full((200, 2), 5, dtype=I32, device="cuda")
+    idx[::3] = 7
+    _check_balance(lg, idx, [0, 90, 200], "softmax", _balance(lg, idx, [0, 90, 200], "softmax"))
