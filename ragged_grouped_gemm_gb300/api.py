@@ -981,12 +981,16 @@ class MoELayer:
             raise ValueError("the balance over sequences is of the dropless layer")
         b, e = self.buf, self.cfg.n_exp
         s = seq_offsets.shape[0] - 1
-        if self.balance is None or self.balance["counts"].shape[0] != s:
-            z = lambda *shape, dt: torch.empty(shape, dtype=dt, device=b["logits"].device)  # noqa: E731
-            self.balance = {"counts": z(s, e, dt=I32), "loss": z(2, dt=F32),
-                            "dlogits": z(self.cfg.n_tok, e, dt=F32)}
+        z = lambda *shape, dt: torch.empty(shape, dtype=dt, device=b["logits"].device)  # noqa: E731
+        if self.balance is None:
+            self.balance = {"loss": z(2, dt=F32), "dlogits": z(self.cfg.n_tok, e, dt=F32)}
+            self._counts = []
             if self.checkpoint:
                 self.balance["x"] = z(self.cfg.n_tok, self.cfg.d_model, dt=BF16)
+        # room for twice as many sequences whenever it grows; captured steps go on writing where they did
+        if not self._counts or self._counts[-1].shape[0] < s:
+            self._counts.append(z(max(s, 2 * self._counts[-1].shape[0]) if self._counts else s, e, dt=I32))
+        self.balance["counts"] = self._counts[-1][:s]
         q = self.balance
         moe_balance_loss(self.desc, b["logits"], b["topk_idx"], seq_offsets, q["counts"], q["loss"], q["dlogits"],
                          self.ws, coef, z_coef, dloss, stream)

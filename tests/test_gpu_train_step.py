@@ -743,3 +743,56 @@ def test_balance_loss_of_an_expert_chosen_twice():
     idx = torch.full((200, 2), 5, dtype=I32, device="cuda")
     idx[::3] = 7
     _check_balance(lg, idx, [0, 90, 200], "softmax", _balance(lg, idx, [0, 90, 200], "softmax"))
+
+
+@pytest.mark.parametrize("precision", ["mxfp8", "fp8w", "fp8b"])
+def test_balance_loss_of_layers_on_other_operands(precision):
+    """The loss's gradient joins dx and dw_gate of a step, and a step of other products follows with the same bits."""
+    cfg = CONFIGS["small_softmax"].replace(precision=precision)
+    p = to_dev(make_layer(cfg, "cpu"))
+    dy = make_dy(cfg, "cpu").cuda()
+    layer = api.MoELayer(cfg, p)
+    layer.forward(p["x"])
+    base = {k: v.clone() for k, v in layer.backward(dy).items()}
+    off = torch.tensor([0, cfg.n_tok // 2, cfg.n_tok - 3], dtype=I32, device="cuda")
+    layer.forward(p["x"])
+    layer.balance_loss(off, 30.0, 10.0)
+    full = layer.backward(dy)
+    rg = O.balance_loss(np32(layer.buf["logits"]), layer.buf["topk_idx"].cpu().numpy(), off.tolist(), cfg.gate, 30.0, 10.0)[2]
+    rx, rw = O.router_backward(rg, np32(p["x"]), np32(p["w_gate"]), np32(base["dx"]), np32(base["dw_gate"]))
+    assert rel(np32(full["dx"]), rx) < 2.0 ** -8 and rel(np32(full["dw_gate"]), rw) < 1e-5
+    layer.forward(p["x"])
+    again = layer.backward(dy)
+    assert all(torch.equal(again[k], v) for k, v in base.items())
+    assert layer.device_status()[0] == 0
+
+
+def test_captured_balance_loss_and_other_numbers_of_sequences():
+    """A captured step goes on writing its own counts after calls with more sequences, and fewer."""
+    cfg = CONFIGS["small_sigmoid"]
+    p = to_dev(make_layer(cfg, "cpu"))
+    n = cfg.n_tok
+    layer = api.MoELayer(cfg, p)
+    layer.forward(p["x"])
+    two = torch.tensor([0, n // 2, n], dtype=I32, device="cuda")
+    layer.balance_loss(two, 1.0, 0.1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(p["x"])
+        layer.balance_loss(two, 1.0, 0.1)
+    counts = layer.balance["counts"]
+    graph.replay()
+    torch.cuda.synchronize()
+    want = counts.clone()
+    many = torch.arange(0, n + 1, 3, dtype=I32, device="cuda")
+    layer.balance_loss(many, 1.0, 0.1)
+    other = layer.balance["counts"]
+    kept = other.clone()
+    assert other.shape[0] == len(many) - 1 and other.data_ptr() != counts.data_ptr()
+    assert other.sum() == cfg.top_k * (many[-1] - many[0])
+    counts.fill_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(counts, want) and torch.equal(other, kept)
+    loss = layer.balance_loss(two, 1.0, 0.1).clone()
+    assert torch.equal(layer.balance["counts"], want) and torch.isfinite(loss).all()
