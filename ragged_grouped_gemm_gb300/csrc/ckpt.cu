@@ -21,24 +21,20 @@ namespace {
 // kTurns turns before it decodes the first.  Bound by the bf16 rows it writes.
 constexpr int kTurns = 8;
 
-__global__ void __launch_bounds__(256) mx_dequant_rows_kernel(const uint2* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales, int64_t src_rows,
-                                                              int n8, int64_t ld, const int32_t* __restrict__ row_map,
-                                                              int row_div, int64_t rows, uint4* __restrict__ out,
-                                                              int32_t* status) {
-  pdl_trigger();
-  pdl_wait();
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (r >= rows) return;
+__device__ __forceinline__ void dequant_rows(const KeptOperand& k, int64_t block, int32_t* status) {
+  const int64_t r = block * blockDim.y + threadIdx.y;
+  if (r >= k.rows) return;
+  const int n8 = k.cols / 8;
+  const auto* codes = reinterpret_cast<const uint2*>(k.codes);
   int64_t src = r;
-  if (row_map) {
-    const int m = __ldg(row_map + r);
-    src = m < 0 ? -1 : m / row_div;
+  if (k.row_map) {
+    const int m = __ldg(k.row_map + r);
+    src = m < 0 ? -1 : m / k.row_div;
   }
-  const bool ok = src >= 0 && src < src_rows;
+  const bool ok = src >= 0 && src < k.src_rows;
   if (!ok && threadIdx.x == 0 && status) atomicOr(status, DEV_BAD_INDEX);
   const uint2* in = codes + src * n8;
-  uint4* dst = out + r * n8;
+  uint4* dst = static_cast<uint4*>(k.out) + r * n8;
   for (int c0 = threadIdx.x; c0 < n8; c0 += kTurns * blockDim.x) {
     uint2 v[kTurns];
     uint32_t e[kTurns];
@@ -49,7 +45,7 @@ __global__ void __launch_bounds__(256) mx_dequant_rows_kernel(const uint2* __res
       e[i] = 0;
       if (ok && c < n8) {
         v[i] = __ldg(in + c);
-        e[i] = __ldg(scales + (c >> 2) * ld + src);
+        e[i] = __ldg(k.scales + (c >> 2) * k.ld + src);
       }
     }
 #pragma unroll
@@ -71,6 +67,44 @@ __global__ void __launch_bounds__(256) mx_dequant_rows_kernel(const uint2* __res
       dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// By the 256 threads of one block.
+__device__ __forceinline__ void group_maps(const GroupMaps& m, int32_t* status) {
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  bool less = false, out = false;
+  for (int g = tid; g < m.groups; g += 256) {
+    const int o0 = m.offsets[g], o1 = m.offsets[g + 1];
+    less |= o1 < o0;
+    out |= o0 < 0 || o0 > m.rows || o1 < 0 || o1 > m.rows;
+  }
+  less = __syncthreads_or(less);
+  out = __syncthreads_or(out);
+  if (tid == 0 && (less || out) && status) atomicOr(status, DEV_BAD_OFFSETS);
+  for (int g = tid; g < m.groups; g += 256) {
+    const int o0 = less ? 0 : min(max(m.offsets[g], 0), m.rows), o1 = less ? 0 : min(max(m.offsets[g + 1], 0), m.rows);
+    m.checked[g] = o0;
+    if (g == m.groups - 1) m.checked[m.groups] = o1;
+    const uint32_t n = static_cast<uint32_t>(max(o1 - o0, 1));   // an empty group is never loaded
+    tensormap_rebase_rows(m.out + g, &m.ta, reinterpret_cast<uint64_t>(m.a + o0 * m.a_ld), n);
+    tensormap_rebase_rows(m.out + m.groups + g, &m.tb, reinterpret_cast<uint64_t>(m.b + o0 * m.b_ld), n);
+  }
+}
+
+__global__ void __launch_bounds__(256) mx_dequant_rows_kernel(const KeptOperand k, int32_t* status) {
+  pdl_trigger();
+  pdl_wait();
+  dequant_rows(k, blockIdx.x, status);
+}
+
+// The first block writes the maps (in a launch of their own 16 groups of 256 x 512 over 3108 rows took 16.8 us
+// where they take 14.6).
+__global__ void __launch_bounds__(256) mx_dequant_rows_maps_kernel(const KeptOperand k, int32_t* status,
+                                                                   const __grid_constant__ GroupMaps m) {
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0) group_maps(m, status);
+  else dequant_rows(k, blockIdx.x - 1, status);
 }
 
 // 32 rows a block; its eight warps take every eighth slice, and their sums are added in order.
@@ -127,13 +161,11 @@ __global__ void __launch_bounds__(256) gate_bwd_kernel(int n_tok, int K, int gat
 
 }  // namespace
 
-cudaError_t launch_mx_dequant_rows(const uint8_t* codes, const uint8_t* scales, int64_t src_rows, int cols, int64_t ld,
-                                   const int32_t* row_map, int row_div, int64_t rows, void* out, int32_t* status,
-                                   cudaStream_t st) {
-  if (rows <= 0) return cudaSuccess;
-  if (cols <= 0 || cols % 32 || row_div < 1) return cudaErrorInvalidValue;
+cudaError_t launch_mx_dequant_rows(const KeptOperand& k, int32_t* status, cudaStream_t st, const GroupMaps* maps) {
+  if (k.rows <= 0 && !maps) return cudaSuccess;
+  if (k.cols <= 0 || k.cols % 32 || k.row_div < 1) return cudaErrorInvalidValue;
   // lanes along a row: as many as it has turns of 8, up to 32
-  const int n8 = cols / 8;
+  const int n8 = k.cols / 8;
   int x = 4;
   while (x < 32 && x < n8) x *= 2;
   const int y = 256 / x;
@@ -141,13 +173,13 @@ cudaError_t launch_mx_dequant_rows(const uint8_t* codes, const uint8_t* scales, 
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + y - 1) / y));
+  cfg.gridDim = dim3(static_cast<unsigned>((k.rows + y - 1) / y + (maps ? 1 : 0)));
   cfg.blockDim = dim3(x, y);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_dequant_rows_kernel, reinterpret_cast<const uint2*>(codes), scales, src_rows, n8,
-                            ld, row_map, row_div, rows, static_cast<uint4*>(out), status);
+  if (maps) return cudaLaunchKernelEx(&cfg, mx_dequant_rows_maps_kernel, k, status, *maps);
+  return cudaLaunchKernelEx(&cfg, mx_dequant_rows_kernel, k, status);
 }
 
 cudaError_t launch_row_dot_sum(const float* part, int64_t slices, int64_t ld, const int32_t* offsets, int groups,

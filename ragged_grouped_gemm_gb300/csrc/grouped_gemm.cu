@@ -53,6 +53,7 @@
 //             descriptor LBO = kb x 128 (next MN atom), SBO = 1024 (next 8
 //             K-rows), advance 2048 B per K=16 step.
 #include "grouped_gemm.cuh"
+#include "ckpt.cuh"
 #include "pdl.cuh"
 #include "sm100_ptx.cuh"
 
@@ -134,7 +135,7 @@ struct KParams {
   int32_t gather_k;
   // Ragged K (bf16), several groups: per-group copies of tmA[0] / tmB[0]
   // whose rows are exactly the group's rows ([0, G) for A, [G, 2G) for B),
-  // written by build_group_maps_kernel before the launch; null with one group
+  // written before the launch; null with one group
   // (the whole-tensor maps end at the group's end already)
   const CUtensorMap* gmaps;
   // TERMS > 1, ragged K: term i of A in its columns from i * a_term_cols (ragged M: behind tmA[i]).
@@ -172,34 +173,6 @@ __global__ void build_group_maps_kernel(CUtensorMap* out, const __grid_constant_
                         rows);
   tensormap_rebase_rows(out + G + g, &tb, reinterpret_cast<uint64_t>(b_ptr + static_cast<int64_t>(r0) * b_ld_bytes),
                         rows);
-}
-
-// The same for offsets from outside the layer, in one block: each is cut to
-// 0 .. rows into `checked`, all of them to zero where they decrease
-// (DEV_BAD_OFFSETS either way).
-__global__ void __launch_bounds__(1024) checked_group_maps_kernel(
-    CUtensorMap* out, const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-    const int32_t* __restrict__ offsets, int G, int rows, int32_t* __restrict__ checked, int32_t* status,
-    const char* a_ptr, int64_t a_ld_bytes, const char* b_ptr, int64_t b_ld_bytes) {
-  const int g = threadIdx.x;
-  pdl_trigger();
-  pdl_wait();
-  int o0 = 0, o1 = 0;
-  if (g < G) {
-    o0 = offsets[g];
-    o1 = offsets[g + 1];
-  }
-  const int out_of = __syncthreads_or(g < G && (o0 < 0 || o0 > rows || o1 < 0 || o1 > rows));
-  const int less = __syncthreads_or(o1 < o0);
-  if (g >= G) return;
-  o0 = less ? 0 : min(max(o0, 0), rows);
-  o1 = less ? 0 : min(max(o1, 0), rows);
-  checked[g] = o0;
-  if (g == G - 1) checked[G] = o1;
-  if (g == 0 && (less || out_of) && status) atomicOr(status, DEV_BAD_OFFSETS);
-  const uint32_t n = static_cast<uint32_t>(max(o1 - o0, 1));   // an empty group is never loaded
-  tensormap_rebase_rows(out + g, &ta, reinterpret_cast<uint64_t>(a_ptr + static_cast<int64_t>(o0) * a_ld_bytes), n);
-  tensormap_rebase_rows(out + G + g, &tb, reinterpret_cast<uint64_t>(b_ptr + static_cast<int64_t>(o0) * b_ld_bytes), n);
 }
 
 // STG: the kernel stages fp32 output blocks for TMA stores (weight gradients)
@@ -2048,8 +2021,8 @@ int num_sms() {
 cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
   if (a.num_groups < 1 || a.num_groups > kMaxGroups || !a.offsets || !a.out0 || a.n_size <= 0)
     return cudaErrorInvalidValue;
-  const bool narrow = (a.block_n == 64 || a.block_n == 128) && !a.quant && !a.w8 && !a.a_gather && a.b_mn && !a.a_mn &&
-                      (a.epi == EPI_SWIGLU_BWD_C || a.epi == EPI_BF16_ADD);
+  const bool narrow_form = a.a_mn ? a.checked && a.epi == EPI_F32 : a.epi == EPI_SWIGLU_BWD_C || a.epi == EPI_BF16_ADD;
+  const bool narrow = (a.block_n == 64 || a.block_n == 128) && !a.quant && !a.w8 && !a.a_gather && a.b_mn && narrow_form;
   if (a.block_n != 256 && !narrow && !(a.block_n == 32 && !a.b_mn && !a.a_mn && a.epi == EPI_F32))
     return cudaErrorInvalidValue;
   // bf16: ragged K comes with MN-major A (the two forms this kernel implements)
@@ -2315,13 +2288,22 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
       if (!make_map(&ta, ra, 64, kbr, false) || !make_map(&tb, rb, 64, kbr, false)) return cudaErrorInvalidValue;
     }
     if (a.checked) {
-      if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 || a.aligned_groups)
+      if (!a.map_ws || (reinterpret_cast<uintptr_t>(a.map_ws) & 127u) != 0 || a.aligned_groups || !a.kept)
         return cudaErrorInvalidValue;
       CUtensorMap* maps = static_cast<CUtensorMap*>(a.map_ws);
-      const cudaError_t e = launch_pdl(checked_group_maps_kernel, 1, (a.num_groups + 31) / 32 * 32, 0, stream, maps,
-                                       ta, tb, a.offsets, a.num_groups, static_cast<int>(a.max_rows),
-                                       a.checked, a.status, static_cast<const char*>(a.a[0].ptr), a.a[0].ld * 2,
-                                       static_cast<const char*>(a.b[0].ptr), a.b[0].ld * 2);
+      GroupMaps gm;
+      gm.ta = ta;
+      gm.tb = tb;
+      gm.out = maps;
+      gm.offsets = a.offsets;
+      gm.checked = a.checked;
+      gm.groups = a.num_groups;
+      gm.rows = static_cast<int32_t>(a.max_rows);
+      gm.a = static_cast<const char*>(a.a[0].ptr);
+      gm.a_ld = a.a[0].ld * 2;
+      gm.b = static_cast<const char*>(a.b[0].ptr);
+      gm.b_ld = a.b[0].ld * 2;
+      const cudaError_t e = launch_mx_dequant_rows(*a.kept, a.status, stream, &gm);
       if (e != cudaSuccess) return e;
       kp.gmaps = maps;
       kp.offsets = a.checked;
@@ -2408,6 +2390,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.a_terms == 3)
       return pair ? launch_impl<256, true, true, EPI_F32, false, true, false, false, 3>(kp, u, stream, a.pdl)
                   : launch_impl<256, true, true, EPI_F32, false, false, false, false, 3>(kp, u, stream, a.pdl);
+    if (BN == 64) return launch_impl<64, true, true, EPI_F32>(kp, u, stream, a.pdl);
+    if (BN == 128) return launch_impl<128, true, true, EPI_F32>(kp, u, stream, a.pdl);
     return pair ? launch_impl<256, true, true, EPI_F32, false, true>(kp, u, stream, a.pdl)
                 : launch_impl<256, true, true, EPI_F32>(kp, u, stream, a.pdl);
   }

@@ -59,11 +59,13 @@ struct Operand {
   int64_t group_stride = 0;  // elements between consecutive matrices
 };
 
+struct KeptOperand;
+
 struct GemmArgs {
   bool a_mn = false;          // A stored MN-major (weight gradients)
   bool b_mn = false;          // B stored MN-major (data gradients)
   bool ragged_k = false;      // contraction over the group's rows
-  int block_n = 256;          // 256, or 32 for narrow N (router logits); EPI_SWIGLU_BWD_C, EPI_BF16_ADD: 64, 128 too
+  int block_n = 256;          // 256, or 32 for narrow N (router logits); EPI_SWIGLU_BWD_C, EPI_BF16_ADD and with `checked`: 64, 128 too
   bool pdl = false;           // bf16: may start while the kernel before it runs (its results are waited for)
   int cta_pair = -1;          // bf16: 0 one SM a tile, 1 a CTA pair, -1 by the rows per group
   int ksplit = 1;             // one group, fp32 out: the contraction in ksplit slices, out0 =
@@ -128,6 +130,7 @@ struct GemmArgs {
   bool check_offsets = false;
   int32_t* range_out = nullptr;
   int32_t* checked = nullptr;
+  const KeptOperand* kept = nullptr;   // with `checked`: what b[0] is decoded from, in the launch that writes the maps
   // Ragged K (bf16) with several groups: global scratch of
   // kGemmMapScratchBytes, 128-byte aligned, for the per-group tensor maps a
   // small kernel writes before the GEMM (same stream)
