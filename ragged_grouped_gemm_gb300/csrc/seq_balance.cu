@@ -15,7 +15,7 @@
 //   d z / d l_tj       = 2 z_coef / T lse_t p_tj
 // with w = q for softmax and s_j (1 - s_j) / sum_i s_i for sigmoid, p the
 // softmax.  So one pass over the logits gives loss and gradient once the counts
-// are known, and those come from the indices alone: two launches.
+// are known, and those come from the indices alone: two launches, or one for a few tokens.
 #include "seq_balance.cuh"
 
 #include <cooperative_groups.h>
@@ -145,6 +145,9 @@ struct RowsParams {
   float4* part;
   int32_t* ticket;
   int32_t* counts_out;
+  const int32_t* idx;   // ALL: the rest
+  int32_t* status;
+  int K;
   float coef, z_coef;
   int n_tok, E, S, per;
 };
@@ -226,21 +229,68 @@ __device__ __forceinline__ void store_row(float* __restrict__ row, int E, int la
   }
 }
 
-template <int NPER, int VEC, int GATE>
+// Few tokens: one cluster counts too, each copy looking up its sequence and adding to counts in global memory
+// (whole numbers, so the order does not matter), which the cluster's barriers zero before and close behind.
+// s_head: sequences that are not empty, their tokens, decreasing offsets.
+constexpr int kAllBlocks = 8;
+__device__ __forceinline__ void count_all(const RowsParams& p, int (&s_head)[3]) {
+  const int N = p.n_tok, tid = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+  if (threadIdx.x < 3) s_head[threadIdx.x] = 0;
+  __syncthreads();
+  int full = 0, used = 0, less = 0, out = 0;
+  for (int i = threadIdx.x; i < p.S; i += kThreads) {
+    const int a = __ldg(p.off + i), b = __ldg(p.off + i + 1);
+    const int len = seq_at(p.off, i + 1, N) - seq_at(p.off, i, N);
+    full += len > 0;
+    used += max(len, 0);
+    less |= b < a;
+    out |= a < 0 || a > N || b < 0 || b > N;
+  }
+  if (full) atomicAdd(&s_head[0], full);
+  if (used) atomicAdd(&s_head[1], used);
+  if (less) atomicOr(&s_head[2], 1);
+  if ((less | out) && blockIdx.x == 0) atomicOr(p.status, DEV_BAD_OFFSETS);
+  const int64_t all = static_cast<int64_t>(p.S) * p.E;
+  for (int64_t i = tid; i < all; i += kAllBlocks * kThreads) p.counts_out[i] = 0;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  if (!s_head[2]) {
+    bool bad = false;
+    for (int i = tid; i < N * p.K; i += kAllBlocks * kThreads) {
+      const int e = __ldg(p.idx + i), t = i / p.K;
+      int lo = -1, hi = p.S;   // start[lo] <= t < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (seq_at(p.off, mid, N) <= t) lo = mid;
+        else hi = mid;
+      }
+      if (lo < 0 || t >= seq_at(p.off, lo + 1, N)) continue;
+      if (e >= 0 && e < p.E) atomicAdd(p.counts_out + static_cast<int64_t>(lo) * p.E + e, 1);
+      else bad = true;
+    }
+    if (bad) atomicOr(p.status, DEV_BAD_INDEX);
+  }
+  cl.sync();
+}
+
+template <int NPER, int VEC, int GATE, bool ALL = false>
 __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(const RowsParams p) {
   __shared__ float4 s_red[kWarps];
   __shared__ int s_last;
+  __shared__ int s_head[3];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.E, N = p.n_tok;
   pdl_wait();
-  const int full = __ldg(p.head), used = __ldg(p.head + 1), wrong = __ldg(p.head + 2);
+  if (ALL) count_all(p, s_head);
+  const int full = ALL ? s_head[0] : __ldg(p.head), used = ALL ? s_head[1] : __ldg(p.head + 1);
+  const int wrong = ALL ? s_head[2] : __ldg(p.head + 2);
   const float up = p.dloss ? __ldg(p.dloss) : 1.0f;
   const float zf = used > 0 ? p.z_coef / static_cast<float>(used) : 0.0f;
   float2 bal = make_float2(0.0f, 0.0f), zz = bal;
   const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.per;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(N), w0));
   const int t1 = static_cast<int>(min(static_cast<int64_t>(N), w0 + p.per));
-  if (wrong) {   // overlapping sequences: no loss, no gradient, no counts
+  if (wrong && !ALL) {   // overlapping sequences: no loss, no gradient, no counts
     const int64_t all = static_cast<int64_t>(p.S) * E;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
@@ -282,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
 #pragma unroll
         for (int j = 0; j < NPER; ++j) {
           const int e = e_of<VEC>(lane, j);
-          f[j] = e < E ? static_cast<float>(__ldg(c + e)) / len : 0.0f;
+          f[j] = e < E ? static_cast<float>(ALL ? __ldcg(c + e) : __ldg(c + e)) / len : 0.0f;
         }
       }
     }
@@ -413,6 +463,10 @@ auto rows_kernel(int n_exp, bool vec) {
          : n_exp <= 256 ? (vec ? seq_rows_kernel<8, 4, GATE> : seq_rows_kernel<8, 1, GATE>)
          : n_exp <= 512 ? (vec ? seq_rows_kernel<16, 4, GATE> : seq_rows_kernel<16, 1, GATE>)
                         : (vec ? seq_rows_kernel<32, 4, GATE> : seq_rows_kernel<32, 1, GATE>);
+}
+template <int GATE>
+auto all_kernel(int n_exp) {   // up to 64 experts
+  return n_exp <= 32 ? seq_rows_kernel<1, 1, GATE, true> : seq_rows_kernel<2, 1, GATE, true>;
 }
 // Blocks of the rows kernel: a warp a token, no more than are resident.
 int rows_grid(int n_tok, int n_exp) {
@@ -689,26 +743,13 @@ __global__ void __launch_bounds__(256) router_few_sum_kernel(const float* __rest
 
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   if (a.n_tok < 1 || a.n_exp < 1 || a.n_exp > 1024 || a.n_seq < 1) return cudaErrorInvalidValue;
-  // One block counts a sequence of up to about 8192 indices in one turn of its 1024 threads; longer
-  // ones, on average, take a cluster of eight (16384 of them: 12 thousand cycles in one block, 9 in eight).
   const int64_t copies = static_cast<int64_t>(a.n_tok) * a.top_k;
-  cudaError_t e;
-  if (copies / a.n_seq > 8192) {
-    e = launch_pdl<8>(seq_counts_kernel<8, 256>, static_cast<unsigned>(a.n_seq + 1) * 8, 256,
-                      8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
-                      a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
-  } else if (copies / a.n_seq > 512 || copies > 32768) {   // lengths may be uneven: one sequence may hold most
-    const int nh = a.n_exp <= 256 ? 32 : 8;
-    e = launch_pdl(seq_counts_kernel<1, 1024>, static_cast<unsigned>(a.n_seq + 1), 1024,
-                   nh * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, nh,
-                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
-  } else {
-    e = launch_pdl(seq_counts_kernel<1, 256>, static_cast<unsigned>(a.n_seq + 1), 256,
-                   8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
-                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
-  }
-  if (e != cudaSuccess) return e;
-  const int grid = rows_grid(a.n_tok, a.n_exp);
+  // Little enough: one launch of one cluster instead of two.  Enqueueing the second costs more than 2 us, and the
+  // kernels' own time is level: 256 x 8, top-2, 1 sequence 7.6 us a call for 9.8 (captured 6.2 for 6.0), 64 x 60 in 8
+  // sequences 7.6 for 9.7 (5.8 for 6.4).  Beyond, eight blocks take longer than a grid: 512 x 8 7.5 us captured
+  // for 6.6, 128 x 64 in 8 sequences 7.6 for 6.2, 128 x 256 13.2 for 7.4
+  const bool one = copies <= 512 && a.n_seq <= 8 && a.n_exp <= 64 && static_cast<int64_t>(a.n_tok) * a.n_exp <= 4096;
+  const int grid = one ? kAllBlocks : rows_grid(a.n_tok, a.n_exp);
   RowsParams p;
   p.logits = a.logits;
   p.counts = a.counts;
@@ -725,8 +766,32 @@ cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st) {
   p.n_tok = a.n_tok;
   p.E = a.n_exp;
   p.S = a.n_seq;
+  p.idx = a.topk_idx;
+  p.status = a.status;
+  p.K = a.top_k;
   p.per = static_cast<int>((static_cast<int64_t>(a.n_tok) + static_cast<int64_t>(grid) * kWarps - 1) /
                            (static_cast<int64_t>(grid) * kWarps));
+  if (one)
+    return launch_pdl<kAllBlocks>(a.gate == 0 ? all_kernel<0>(a.n_exp) : all_kernel<1>(a.n_exp), kAllBlocks, kThreads, 0,
+                                  st, p);
+  // One block counts a sequence of up to about 8192 indices in one turn of its 1024 threads; longer
+  // ones, on average, take a cluster of eight (16384 of them: 12 thousand cycles in one block, 9 in eight).
+  cudaError_t e;
+  if (copies / a.n_seq > 8192) {
+    e = launch_pdl<8>(seq_counts_kernel<8, 256>, static_cast<unsigned>(a.n_seq + 1) * 8, 256,
+                      8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
+                      a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  } else if (copies / a.n_seq > 512 || copies > 32768) {   // lengths may be uneven: one sequence may hold most
+    const int nh = a.n_exp <= 256 ? 32 : 8;
+    e = launch_pdl(seq_counts_kernel<1, 1024>, static_cast<unsigned>(a.n_seq + 1), 1024,
+                   nh * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, nh,
+                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  } else {
+    e = launch_pdl(seq_counts_kernel<1, 256>, static_cast<unsigned>(a.n_seq + 1), 256,
+                   8 * static_cast<size_t>(a.n_exp) * sizeof(int), st, a.n_tok, a.n_exp, a.top_k, a.n_seq, 8,
+                   a.topk_idx, a.seq_offsets, a.counts, a.head, a.status);
+  }
+  if (e != cudaSuccess) return e;
   // 16-byte words above 64 experts (below, lanes would idle), where every row starts on one
   const bool vec = a.n_exp > 64 && a.n_exp % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) |
                                                         reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0;

@@ -77,7 +77,10 @@ def _routed(n, e, k, seed, scale=1.3):
     (1, 1, 1, [0, 1]), (1, 2, 2, [0, 1]), (5, 3, 1, [0, 0, 5, 5]), (33, 31, 4, [0, 7, 33]), (64, 32, 2, [0, 64]),
     (257, 33, 8, [4, 4, 5, 100, 100, 251]), (700, 60, 6, [0, 1, 2, 3, 699]), (2000, 64, 2, [0, 1000, 2000]),
     (1500, 129, 8, [0, 1500]), (3000, 256, 8, [10, 11, 2000, 2950]), (900, 300, 3, [0, 450, 900]),
-    (400, 513, 32, [0, 399]), (350, 1024, 32, [0, 100, 350]), (20000, 8, 2, [0, 19999, 20000])])
+    # one cluster, and the first sizes past it
+    (256, 16, 2, [0, 256]), (64, 64, 8, [0, 10, 10, 40, 64]), (120, 33, 4, [3, 60, 60, 118]), (256, 8, 2, [0, 30, 31, 256]),
+    (512, 8, 1, [0, 1, 2, 3, 4, 5, 6, 7, 512]), (512, 8, 1, [0, 1, 2, 3, 4, 5, 6, 7, 8, 512]), (257, 16, 2, [0, 257]),
+    (63, 65, 8, [0, 63]), (400, 513, 32, [0, 399]), (350, 1024, 32, [0, 100, 350]), (20000, 8, 2, [0, 19999, 20000])])
 def test_balance_loss(n, e, k, off, gate):
     lg, idx = _routed(n, e, k, n + e)
     got = _balance(lg, idx, off, gate)
@@ -135,7 +138,7 @@ def test_balance_loss_masked_experts_and_extreme_logits(gate):
     assert torch.isfinite(bad[2][rest]).all()                        # a row that is not finite keeps to itself
 
 
-@pytest.mark.parametrize("n", [300, 3000])      # one block a sequence, a cluster of eight
+@pytest.mark.parametrize("n", [220, 300, 3000])      # one cluster for all, one block a sequence, a cluster of eight
 def test_balance_loss_reports_offsets_and_indices(n):
     e, k = 16, 2
     lg, idx = _routed(n, e, k, 6)
