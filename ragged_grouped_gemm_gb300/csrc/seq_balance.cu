@@ -847,6 +847,14 @@ cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate
       }
     }
   }
+  // Up to four turns of one run: its launch alone, which writes dw itself.  Enqueueing the second costs 2 us, the turns about
+  // as much as the sums (300 x 7168, 8 experts: 7.8 us a call for 9.8, captured 6.3 for 6.5; 400 x 2048 7.8 for
+  // 9.8, captured 5.6 for 4.8; eight turns, 1000 x 4096, 13.9 for 10.0)
+  if (n_tok <= 4 * 16 * warps && strips64 <= at_once) {
+    cw = 1;
+    runs = 1;
+    per = n_tok;
+  }
   const int strips = (strips64 + cw - 1) / cw;
   auto kern = two ? router_few_kernel<2> : router_few_kernel<1>;
   cudaLaunchConfig_t cfg{};
