@@ -567,6 +567,20 @@ __device__ __forceinline__ uint32_t next_term(float2& v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The B of dlogits W for eight experts from e0 and 64 columns: rows of W, transposed (tile t's columns as below).
+__device__ __forceinline__ void expert_columns(const __nv_bfloat16* __restrict__ wg, int e0, int E, int D, int col0,
+                                               bool on, int lane, uint32_t (&f)[8]) {
+  const int e = e0 + lane / 4;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (on && e < E)
+      v = __ldg(reinterpret_cast<const uint4*>(wg + static_cast<int64_t>(e) * D + col0 + 32 * k + lane % 4 * 8));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[4 * k + i] = transpose8(reinterpret_cast<const uint32_t*>(&v)[i]);
+  }
+}
+
 //   dx_t = dx_in_t + sum_e dl_te W_e,   dw_e = dw_in_e + sum_t dl_te x_t   for up to 8 * H experts (H 1, 2)
 // tcgen05's tiles of 128 rows would be an eighth full at most, and its two products read x, the addend and dl (as
 // bf16 terms that a third kernel makes) in launches of their own; here each is read once and what bounds it is
@@ -584,6 +598,33 @@ __device__ __forceinline__ uint32_t next_term(float2& v) {
 template <int H> constexpr int kFewWarps = H == 1 ? 8 : 4;
 template <int H> constexpr int kFewBlocks = H == 1 ? 2 : 3;
 constexpr int kFewTurns = 56;   // of a warp, about, that one accumulator adds (1.5e-8 of a sum is cut at each)
+// The block's dw of 8 * H experts from e0, eight at a time: the terms' sums, then the warps', in order.
+template <int H, int WARPS>
+__device__ __forceinline__ void few_join(const float (&acc)[H][8][4], float (&s_sum)[WARPS][16][33], int cw, int E, int e0,
+                                         int D, int64_t at, const float* dw_in, float* dw) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tw = WARPS / cw;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        s_sum[warp][2 * t + i][lane] = H == 1 ? acc[0][t][i] + acc[0][t][2 + i] : acc[0][t][2 * h + i] + acc[H - 1][t][2 * h + i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < cw * 512; o += WARPS * 32) {
+      const int c = o % 64, e = e0 + 8 * h + o / 64 % 8, w = o / 512, col = (static_cast<int>(blockIdx.x) * cw + w) * 64 + c;
+      const int t = c / 32 * 4 + c % 8 / 2;
+      float v = 0.0f;
+      for (int k = 0; k < tw; ++k) v += s_sum[k * cw + w][2 * t + c % 2][o / 64 % 8 * 4 + c % 32 / 8];
+      if (e < E && col < D) {
+        const int64_t i = at + static_cast<int64_t>(e) * D + col;
+        dw[i] = dw_in ? dw_in[i] + v : v;
+      }
+    }
+  }
+}
+
 template <int H>
 __global__ void __launch_bounds__(kFewWarps<H> * 32, kFewBlocks<H>) router_few_kernel(
     const float* __restrict__ dl, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wg,
@@ -597,15 +638,11 @@ __global__ void __launch_bounds__(kFewWarps<H> * 32, kFewBlocks<H>) router_few_k
   pdl_wait();
   uint32_t wf[8][H];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    const int c = col0 + t / 4 * 32 + g / 2 * 8 + t % 4 * 2 + g % 2;
+  for (int h = 0; h < H; ++h) {
+    uint32_t f[8];
+    expert_columns(wg, 8 * h, E, D, col0, on, lane, f);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int e = 8 * h + 2 * q;
-      const uint32_t lo = on && e < E ? __ldg(reinterpret_cast<const uint16_t*>(wg) + static_cast<int64_t>(e) * D + c) : 0u;
-      const uint32_t hi = on && e + 1 < E ? __ldg(reinterpret_cast<const uint16_t*>(wg) + static_cast<int64_t>(e + 1) * D + c) : 0u;
-      wf[t][h] = lo | hi << 16;
-    }
+    for (int t = 0; t < 8; ++t) wf[t][h] = f[t];
   }
   float acc[H][8][4];   // H 1: rows 0-7 the first term, 8-15 the others; H 2: [0] the first, [1] the others
 #pragma unroll
@@ -698,27 +735,120 @@ __global__ void __launch_bounds__(kFewWarps<H> * 32, kFewBlocks<H>) router_few_k
       }
     }
   }
-  // eight experts at a time: the terms' sums, then the warps', in order
+  few_join<H, kFewWarps<H>>(acc, s_sum, cw, E, 0, D, static_cast<int64_t>(blockIdx.y) * E * D, dw_in, dw);
+}
+
+// The same for few tokens of more experts, in one launch instead of the tensor cores' four: blocks of z < G =
+// ceil(E / 16) form dw of 16 experts each, 64 columns over all tokens, those behind them dx of 64 tokens each over
+// all experts.  x is read G times and W once for every 64 tokens, from L2, which little work allows.
+constexpr int kShortWarps = 4;
+__global__ void __launch_bounds__(kShortWarps * 32, 3) router_short_kernel(
+    const float* __restrict__ dl, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wg,
+    const __nv_bfloat16* dx_in, __nv_bfloat16* dx, const float* dw_in, float* dw, int N, int D, int E) {
+  __shared__ float s_sum[kShortWarps][16][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int G = (E + 15) / 16, col0 = static_cast<int>(blockIdx.x) * 64;
+  pdl_trigger();
+  pdl_wait();
+  // two (dx) or three terms of dlogits: rows g, g + 8, experts e0 + 2q, e0 + 8 + 2q and the next
+  auto terms_of = [&](int base, int e0, auto& term) {
+    constexpr int T = sizeof(term) / sizeof(term[0]);
 #pragma unroll
-  for (int h = 0; h < H; ++h) {
-    __syncthreads();
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = base + g + 8 * r, e = e0 + 8 * h + 2 * q;
+        const float* p = dl + static_cast<int64_t>(t) * E + e;
+        float2 v = make_float2(t < N && e < E ? __ldg(p) : 0.0f, t < N && e + 1 < E ? __ldg(p + 1) : 0.0f);
+#pragma unroll
+        for (int i = 0; i < T; ++i) term[i][r][h] = next_term(v);
+      }
+  };
+  if (static_cast<int>(blockIdx.z) >= G) {
+    const int base = 16 * ((static_cast<int>(blockIdx.z) - G) * kShortWarps + warp);
+    if (base < N) {
+      float c[8][4];
+      uint4 av[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = base + g + 8 * r;
+          av[r][k] = make_uint4(0, 0, 0, 0);
+          if (t < N && dx_in)
+            av[r][k] = *reinterpret_cast<const uint4*>(dx_in + static_cast<int64_t>(t) * D + col0 + 8 * q + 32 * k);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&av[r][k])[i];
+            c[4 * k + i][2 * r] = __uint_as_float(w << 16);
+            c[4 * k + i][2 * r + 1] = __uint_as_float(w & 0xffff0000u);
+          }
+        }
+      for (int e0 = 0; e0 < E; e0 += 16) {
+        uint32_t w0[8], w1[8], term[2][2][2];
+        terms_of(base, e0, term);
+        expert_columns(wg, e0, E, D, col0, true, lane, w0);
+        expert_columns(wg, e0 + 8, E, D, col0, true, lane, w1);
+#pragma unroll
+        for (int i = 1; i >= 0; --i) {
+          const uint32_t a[4] = {term[i][0][0], term[i][1][0], term[i][0][1], term[i][1][1]};
+#pragma unroll
+          for (int t = 0; t < 8; ++t) mma_16x8x16(c[t], a, w0[t], w1[t]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = base + g + 8 * r;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 o = __floats2bfloat162_rn(c[4 * k + i][2 * r], c[4 * k + i][2 * r + 1]);
+            reinterpret_cast<uint32_t*>(&av[r][k])[i] = *reinterpret_cast<const uint32_t*>(&o);
+          }
+          if (t < N) *reinterpret_cast<uint4*>(dx + static_cast<int64_t>(t) * D + col0 + 8 * q + 32 * k) = av[r][k];
+        }
+    }
+    return;
+  }
+  const int e0 = 16 * static_cast<int>(blockIdx.z);
+  float acc[2][8][4];   // [0] the first term, [1] the others
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        s_sum[warp][2 * t + i][lane] = H == 1 ? acc[0][t][i] + acc[0][t][2 + i] : acc[0][t][2 * h + i] + acc[H - 1][t][2 * h + i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < cw * 512; o += kFewWarps<H> * 32) {
-      const int c = o % 64, e = 8 * h + o / 64 % 8, w = o / 512, col = (static_cast<int>(blockIdx.x) * cw + w) * 64 + c;
-      const int t = c / 32 * 4 + c % 8 / 2;
-      float v = 0.0f;
-      for (int k = 0; k < tw; ++k) v += s_sum[k * cw + w][2 * t + c % 2][e % 8 * 4 + c % 32 / 8];
-      if (e < E && col < D) {
-        const int64_t i = (static_cast<int64_t>(blockIdx.y) * E + e) * D + col;
-        dw[i] = dw_in ? dw_in[i] + v : v;
+      for (int i = 0; i < 4; ++i) acc[h][t][i] = 0.0f;
+  for (int base = 16 * warp; base < N; base += 16 * kShortWarps) {
+    uint4 xv[2][2];
+    uint32_t term[3][2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int t = base + g + 8 * r;
+        xv[r][k] = make_uint4(0, 0, 0, 0);
+        if (t < N) xv[r][k] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * D + col0 + 8 * q + 32 * k));
+      }
+    terms_of(base, e0, term);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) term[i][r][h] = transpose8(term[i][r][h]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t b0 = transpose8(reinterpret_cast<const uint32_t*>(&xv[0][t / 4])[t % 4]);
+      const uint32_t b1 = transpose8(reinterpret_cast<const uint32_t*>(&xv[1][t / 4])[t % 4]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t a[4] = {term[i][0][0], term[i][0][1], term[i][1][0], term[i][1][1]};
+        mma_16x8x16(acc[i > 0 ? 1 : 0][t], a, b0, b1);
       }
     }
   }
+  few_join<2, kShortWarps>(acc, s_sum, 1, E, e0, D, 0, dw_in, dw);
 }
 
 // dw = dw_in + the runs' partial products: 32 numbers a block, its warps take the runs in turn and are joined in order.
@@ -875,6 +1005,24 @@ cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate
   const int64_t n = static_cast<int64_t>(n_exp) * d;
   return launch_pdl(router_few_sum_kernel, static_cast<unsigned>(n / 32), 256, 0, st, const_cast<const float*>(part),
                     static_cast<int>(runs), n, dw_in, dw);
+}
+
+cudaError_t launch_router_short(const float* dl, const void* x, const void* w_gate, const void* dx_in, void* dx, int n_tok,
+                                int d, int n_exp, const float* dw_in, float* dw, cudaStream_t st) {
+  if (n_tok < 1 || d % 64 || !router_short(n_tok, d, n_exp)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(d / 64), 1,
+                     static_cast<unsigned>((n_exp + 15) / 16 + (n_tok + 16 * kShortWarps - 1) / (16 * kShortWarps)));
+  cfg.blockDim = dim3(kShortWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, router_short_kernel, dl, static_cast<const __nv_bfloat16*>(x),
+                            static_cast<const __nv_bfloat16*>(w_gate), static_cast<const __nv_bfloat16*>(dx_in),
+                            static_cast<__nv_bfloat16*>(dx), dw_in, dw, n_tok, d, n_exp);
 }
 
 }  // namespace moe

@@ -183,7 +183,7 @@ def _router(dl, x, wg, dxi, dwi, inplace=False, ws=None):
 
 
 @pytest.mark.parametrize("n,d,e", [(1, 64, 1), (1, 128, 9), (7, 192, 8), (63, 64, 17), (130, 320, 60), (257, 512, 16),
-                                   (129, 1088, 64), (512, 256, 65), (1000, 448, 200), (2049, 576, 129), (300, 192, 1024),
+                                   (129, 1088, 64), (256, 192, 33), (3, 128, 1024), (17, 448, 256), (40, 1024, 100), (70, 7168, 256), (512, 256, 65), (513, 256, 65), (1000, 448, 200), (2049, 576, 129), (300, 192, 1024),
                                    (3000, 704, 256), (4096, 2048, 8), (4096, 1088, 100)])
 def test_router_backward(n, d, e):
     """Three bf16 terms hold the 24 bits of an entry, two lose 2^-17 of it.  The tensor cores add 16 products at a
