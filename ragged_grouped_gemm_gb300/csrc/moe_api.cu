@@ -1444,11 +1444,11 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
     return MOE_OK;
   }
   const WsLayout L = layout(*d);
+  if (moe::router_short(N, D, E))
+    return cuda_status(moe::launch_router_short(dlogits, x, w_gate, dx_in, dx, N, D, E, dw_in, dw_gate, st));
   if (E <= moe::kRouterFew)
     return cuda_status(moe::launch_router_few(dlogits, x, w_gate, dx_in, dx, at<float>(ws, L.rterms), L.rend - L.rterms,
                                               N, D, E, dw_in, dw_gate, st));
-  if (moe::router_short(N, D, E))
-    return cuda_status(moe::launch_router_short(dlogits, x, w_gate, dx_in, dx, N, D, E, dw_in, dw_gate, st));
   const RouterPlan plan = router_plan(*d, L.rend - L.rterms);
   const int e8 = plan.e8;
   char* terms = at<char>(ws, L.rterms);

@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kFewWarps<H> * 32, kFewBlocks<H>) router_few_k
   few_join<H, kFewWarps<H>>(acc, s_sum, cw, E, 0, D, static_cast<int64_t>(blockIdx.y) * E * D, dw_in, dw);
 }
 
-// The same for few tokens of more experts, in one launch instead of the tensor cores' four: blocks of z < G =
+// The same for few tokens of any number of experts, in one launch: blocks of z < G =
 // ceil(E / 16) form dw of 16 experts each, 64 columns over all tokens, those behind them dx of 64 tokens each over
 // all experts.  x is read G times and W once for every 64 tokens, from L2, which little work allows.
 constexpr int kShortWarps = 4;
@@ -976,14 +976,6 @@ cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate
         per = turns * tile;
       }
     }
-  }
-  // Up to four turns of one run: its launch alone, which writes dw itself.  Enqueueing the second costs 2 us, the turns about
-  // as much as the sums (300 x 7168, 8 experts: 7.8 us a call for 9.8, captured 6.3 for 6.5; 400 x 2048 7.8 for
-  // 9.8, captured 5.6 for 4.8; eight turns, 1000 x 4096, 13.9 for 10.0)
-  if (n_tok <= 4 * 16 * warps && strips64 <= at_once) {
-    cw = 1;
-    runs = 1;
-    per = n_tok;
   }
   const int strips = (strips64 + cw - 1) / cw;
   auto kern = two ? router_few_kernel<2> : router_few_kernel<1>;

@@ -44,12 +44,14 @@ cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate
                               float* dw, cudaStream_t st);
 
 // And of any number of experts where there is little to do in all.  What it reads again grows with tokens x columns x
-// experts: 256 x 2048 x 128 9.1 us a call where the tensor cores' four launches take 17.6, 512 x 2048 x 64 11.8 for 18.5,
+// experts: beside the tensor cores' four launches 256 x 2048 x 128 takes 9.1 us a call for 17.6, 512 x 2048 x 64 11.8 for 18.5,
 // 512 x 7168 x 24 9.6 for 20.7, 64 x 256 x 256 7.9 for 16; 64 x 7168 x 256 21.1 for 20.7, 256 x 4096 x 256 24.1 for
-// 22.7.  One run of tokens, so not too many: 768 x 1024 x 64 16.5 for 16.5, 2048 x 512 x 32 24.7 for 16.1.
+// 22.7.  Beside the pass over 16 experts at most and the sums of its runs, 257 x 512 x 16 7.3 for 9.5,
+// 300 x 7168 x 8 7.4 for 7.7, 512 x 4096 x 16 10.5 for 9.8.  One run of tokens, so not too many: 768 x 1024 x 64 16.5 for
+// 16.5, 2048 x 512 x 32 24.7 for 16.1.
 constexpr int kRouterShort = 512;
 inline bool router_short(int n_tok, int d, int n_exp) {
-  return n_tok <= kRouterShort && static_cast<int64_t>(n_tok) * d * n_exp <= 100000000;
+  return n_tok <= kRouterShort && static_cast<int64_t>(n_tok) * d * n_exp <= (n_exp <= kRouterFew ? 30000000 : 100000000);
 }
 cudaError_t launch_router_short(const float* dl, const void* x, const void* w_gate, const void* dx_in, void* dx, int n_tok,
                                 int d, int n_exp, const float* dw_in, float* dw, cudaStream_t st);

@@ -210,7 +210,7 @@ def test_router_backward(n, d, e):
     assert torch.equal(dx, ix) and torch.equal(dw, iw)
 
 
-@pytest.mark.parametrize("n,d,e", [(1, 64, 2), (2, 4096, 3), (5, 192, 5), (33, 1088, 1), (129, 64, 7), (500, 576, 2), (1001, 256, 4),
+@pytest.mark.parametrize("n,d,e", [(1, 64, 2), (2, 4096, 3), (513, 64, 1), (514, 128, 9), (600, 192, 16), (5, 192, 5), (33, 1088, 1), (129, 64, 7), (500, 576, 2), (1001, 256, 4),
                                    (2600, 128, 16), (2047, 1984, 12), (3000, 1024, 8), (7000, 320, 3), (20000, 64, 9)])
 def test_router_backward_of_few_experts(n, d, e):
     """Three bf16 terms of an entry are the entry but for 2^-24 of it, two (dx) but for 2^-17: a bf16 number is off by
