@@ -76,6 +76,7 @@ constexpr int kThreadsW8 = 576;      // + 8 converter warps (FP8 weights)
 constexpr int kThreadsC = 384;       // CHUNKED: three warpgroups, the epilogue in two of them
 constexpr int kConvWarps = 8;
 constexpr int kChunk = 13;           // k-blocks of 64 elements a chunk (CHUNKED)
+constexpr int kRowChunk = 1792;      // rows of a run (ROWCH)
 // CHUNKED on 256-column tiles: registers a thread at launch, of the first warpgroup and of the epilogue's
 constexpr int kRegsLaunch = 168, kRegsFirst = 40, kRegsEpi = 232;
 static_assert(128 * kRegsFirst + 256 * kRegsEpi <= kThreadsC * kRegsLaunch, "more registers than the block has");
@@ -246,7 +247,7 @@ struct Cfg {
 // The configuration of each kernel form: the bf16 ragged-K (weight-gradient)
 // form keeps no group tables and has 4 KB of fp32 staging per epilogue warp.
 template <int BN, bool A_MN, int EPI, bool QUANT, bool PAIR, bool W8, int TERMS = 1>
-using KernelCfg = Cfg<BN, QUANT, PAIR, W8, EPI == EPI_F32, (A_MN && !QUANT && !W8) ? 0 : kMaxGroups, 6,
+using KernelCfg = Cfg<BN, QUANT, PAIR, W8, EPI == EPI_F32 || EPI == EPI_F32_LONG, (A_MN && !QUANT && !W8) ? 0 : kMaxGroups, 6,
                       EPI == EPI_BF16_ADD, TERMS>;
 
 struct Tile {
@@ -458,6 +459,9 @@ struct KeptBlock {
 // 704 for 717 us in CTA pairs (8192 rows, 14336 x 4096) and took 340 for 332 in single ones (2048 x 7168).
 __device__ __forceinline__ int num_chunks(int n) { return (n + kChunk - 1) / kChunk; }
 
+// ROWCH: the runs of a group of `rows` rows (one for none).
+__device__ __forceinline__ int row_runs(int rows) { return max(1, (rows + kRowChunk - 1) / kRowChunk); }
+
 // GATHER (ragged M, bf16, one contraction source): A rows are gathered from
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
 // instruction, every lane of the producer warp taking four of the tile's
@@ -477,6 +481,11 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
   // these 716, one chain 660 with dg off by 4e-6 of its norm; what a chunk costs is its reading from tensor memory).
   constexpr bool CHUNKED = EPI == EPI_SWIGLU_BWD_C && !QUANT && !W8;
   constexpr int EW = CHUNKED ? 4 : 2;   // first epilogue warp
+  // ROWCH: a group of more than kRowChunk rows comes in equal runs of k-blocks, each an accumulator of its own; the
+  // first run's is stored, the others are added to it by the threads, or the TMA unit, that stored it (8192 rows: off by
+  // 4.8e-7 of the gradient's norm, one chain 3.7e-6)
+  constexpr bool ROWCH = EPI == EPI_F32_LONG;
+  constexpr bool F32 = EPI == EPI_F32 || ROWCH;
   // SPLIT: the first term of A has one accumulator, the others, 2^-8 of it or less, the other: adding them to one would
   // cut its last bits three times as often
   constexpr bool SPLIT = TERMS == 3;
@@ -955,7 +964,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * BM : BM, BN, A_MN, B_MN);
       uint32_t it = 0, tcount = 0;
-      uint32_t chunk = 0;   // CHUNKED: chunks so far
+      uint32_t chunk = 0;   // CHUNKED, ROWCH: accumulators so far
       bool ok = true;
       // ragged K: the next tile's group offsets (global memory) are loaded
       // before this tile's k-blocks are issued and used only after them, so
@@ -974,16 +983,18 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
           nx0 = s_off[g];
           nx1 = s_off[g + 1];
         }
-        const int nch = CHUNKED ? num_chunks(t.num_kb) : 1;
+        const int nch = CHUNKED ? num_chunks(t.num_kb) : ROWCH ? row_runs(t.k_rows) : 1;
         for (int ch = 0; ch < nch; ++ch) {
-          const uint32_t use = CHUNKED ? chunk++ : tcount;   // accumulators filled before this one
+          const uint32_t use = CHUNKED || ROWCH ? chunk++ : tcount;   // accumulators filled before this one
           const uint32_t buf = SPLIT ? 0u : use & 1u;
           const uint32_t aph = (SPLIT ? use : use >> 1) & 1u;
           if (!mbar_wait_bounded(&tempty[buf], aph ^ 1u, s_abort, p.status, 200)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
-          const int kb0 = ch * kChunk;
-          for (int kb = kb0; kb < (CHUNKED ? min(t.num_kb, kb0 + kChunk) : t.num_kb); ++kb, ++it) {
+          const bool runs = ROWCH && nch > 1;   // divisions that one run does not pay
+          const int kb0 = runs ? ch * t.num_kb / nch : ch * kChunk;
+          const int kb1 = CHUNKED ? min(t.num_kb, kb0 + kChunk) : runs ? (ch + 1) * t.num_kb / nch : t.num_kb;
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const int s = it % S;
             const uint32_t ph = (it / S) & 1u;
             if (!mbar_wait_bounded(&full[s], ph, s_abort, p.status, 300 + s)) { ok = false; break; }
@@ -1197,8 +1208,15 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
         tma_load_2d(abuf + (AB * i + b) * 4096, &p.tmAs[0], abar + b, box_col(t) + 64 * i, t.row0 + q * 32);
     };
     if (EPI == EPI_BF16_ADD) ask(unit0);
-    for (int tile = unit0; tile < total_tiles; tile += ustride, ++tcount) {
+    int run = 0, runs = 1;   // ROWCH: of the tile at hand
+    auto next = [&](int tile) {
+      if (ROWCH && ++run < runs) return tile;
+      run = 0;
+      return tile + ustride;
+    };
+    for (int tile = unit0; tile < total_tiles; tile = next(tile), ++tcount) {
       const Tile t = decode_tile<RAGGED_K, BN, PAIR>(tile, p, s_off, s_pre, rank);
+      if (ROWCH) runs = row_runs(t.k_rows);
       const uint32_t buf = SPLIT ? 0u : tcount & 1u;
       const uint32_t aph = (SPLIT ? tcount : tcount >> 1) & 1u;
       const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
@@ -1239,14 +1257,14 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
         tc_fence_after();
       }
       const bool row_ok = r < t.rows_valid;
-      if (EPI == EPI_BF16 || EPI == EPI_F32) {
+      if (EPI == EPI_BF16 || F32) {
         int64_t grow;
         char* obase = static_cast<char*>(p.out0);
         if (!RAGGED_K) {
           grow = t.row0 + r;
         } else {
           grow = static_cast<int64_t>(t.m0) + r;
-          obase += static_cast<int64_t>(t.g) * p.group_stride_out * (EPI == EPI_F32 ? 4 : 2);
+          obase += static_cast<int64_t>(t.g) * p.group_stride_out * (F32 ? 4 : 2);
         }
         const bool zero = t.num_kb == 0;
         const int c_begin = hf * (BN / 2);
@@ -1263,7 +1281,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
             hi[j] = __float_as_uint(__uint_as_float(hi[j]) + __uint_as_float(u1[j]));
           }
         };
-        if (EPI == EPI_F32 && C::kWideStaging && PAIR && p.c_tma && (BN / 2) % 32 == 0) {
+        if (F32 && C::kWideStaging && PAIR && p.c_tma && (BN / 2) % 32 == 0) {
           // Weight gradients on CTA pairs: the warp's 32 rows x 32 columns go to a 4 KB
           // shared buffer (one row per lane, 128-byte swizzle: 16-byte chunk j
           // of row r at chunk j ^ (r & 7)) and leave by plain 16-byte stores,
@@ -1311,11 +1329,27 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
                              vb[4 * j + 2], vb[4 * j + 3]);
               __syncwarp();
               const int gc = col + 4 * c8;
+              float4 sum[ROWCH ? 8 : 1];   // what this thread stored of the runs before (n_size is a multiple of 4)
+              if (ROWCH && run > 0) {
+#pragma unroll
+                for (int j = 0; j < (ROWCH ? 8 : 1); ++j) {
+                  const int r2 = (lane >> 3) + 4 * j;
+                  if (row + r2 < rows && gc < p.n_size)
+                    sum[j] = __ldcg(reinterpret_cast<const float4*>(gbase + static_cast<int64_t>(row + r2) * p.ld_out + gc));
+                }
+              }
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const int r2 = (lane >> 3) + 4 * j;
                 uint32_t x0, x1, x2, x3;
                 ld_shared_v4(stg + r2 * 128 + ((c8 ^ (r2 & 7)) << 4), x0, x1, x2, x3);
+                if (ROWCH && run > 0) {
+                  const float4 o = sum[ROWCH ? j : 0];
+                  x0 = __float_as_uint(o.x + __uint_as_float(x0));
+                  x1 = __float_as_uint(o.y + __uint_as_float(x1));
+                  x2 = __float_as_uint(o.z + __uint_as_float(x2));
+                  x3 = __float_as_uint(o.w + __uint_as_float(x3));
+                }
                 if (row + r2 < rows && gc < p.n_size) {
                   float* dst = gbase + static_cast<int64_t>(row + r2) * p.ld_out + gc;
                   if (gc + 4 <= p.n_size) {
@@ -1342,7 +1376,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
               }
             }
           }
-        } else if (EPI == EPI_F32 && p.c_tma && (BN / 2) % 32 == 0) {
+        } else if (F32 && p.c_tma && (BN / 2) % 32 == 0) {
           // Stage this warp's 32 rows x 32 columns as two 16-row halves in a
           // 2 KB shared-memory buffer (128-byte swizzle: 16-byte chunk j of
           // row r at chunk j ^ (r & 7)) and write each half with a TMA tensor
@@ -1357,6 +1391,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
           constexpr int NCH = BN / 64;
           constexpr int NB = C::kWideStaging ? 2 : 1;
           uint8_t* stg0 = smem + C::kEpiOff + (warp - 2) * C::kEpiWarpBytes;
+          if (ROWCH && run > 0 && lane == 0) bulk_wait_group0();   // what the others are added to has landed
           uint32_t va[16], vb[16], vc[16], vd[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) va[j] = vb[j] = vc[j] = vd[j] = 0u;
@@ -1401,7 +1436,8 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                tma_store_3d_hint(&p.tmC, stg, col, row, RAGGED_K ? t.g : t.split, policy_evict_first());
+                if (ROWCH && run > 0) tma_add_3d_hint(&p.tmC, stg, col, row, t.g, policy_evict_first());
+                else tma_store_3d_hint(&p.tmC, stg, col, row, RAGGED_K ? t.g : t.split, policy_evict_first());
                 bulk_commit_group();
               }
               ++nstore;
@@ -1419,7 +1455,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
               }
             }
           }
-        } else if (EPI == EPI_F32 && p.c_tma) {
+        } else if (F32 && p.c_tma) {
           // 16-column form of the above for tiles whose column halves are not
           // a multiple of 32 wide: 32 rows x 16 columns per 2 KB buffer
           // (64-byte swizzle: chunk j of row r at chunk j ^ ((r >> 1) & 3)).
@@ -1472,7 +1508,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
             const int col = t.nt * BN + c;
             if (row_ok && col < p.n_size) {
               const int nvalid = min(16, p.n_size - col);
-              if (EPI == EPI_F32) {
+              if (F32) {
                 float* dst = reinterpret_cast<float*>(obase) + grow * p.ld_out + col;
                 if (nvalid == 16 && (p.ld_out & 3) == 0) {
 #pragma unroll
@@ -1822,7 +1858,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
     // after a wait that ran out: the loads asked for have landed before the block leaves
     if (EPI == EPI_BF16_ADD && p.in0)
       for (; got != asked; ++got) mbar_wait_drain(abar + got % AB, (got / AB) & 1u);
-    if ((EPI == EPI_F32 || EPI == EPI_BF16_ADD) && lane == 0) bulk_wait_group0();   // every TMA store has landed
+    if ((F32 || EPI == EPI_BF16_ADD) && lane == 0) bulk_wait_group0();   // every TMA store has landed
     __syncwarp();
   }
 
@@ -2390,6 +2426,15 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.a_terms == 3)
       return pair ? launch_impl<256, true, true, EPI_F32, false, true, false, false, 3>(kp, u, stream, a.pdl)
                   : launch_impl<256, true, true, EPI_F32, false, false, false, false, 3>(kp, u, stream, a.pdl);
+    // Where a group may be long, and is not so by its skew alone: the form of runs costs 64 groups of 128 rows on
+    // average 3 % (2048 x 7168: 641 us for 622) and 8 of 1024 nothing (14336 x 4096: 652 for 658)
+    if (a.checked && a.max_rows > kRowChunk && a.max_rows >= kRowChunk / 4 * static_cast<int64_t>(a.num_groups)) {
+      if (!kp.c_tma || a.n_size % 4) return cudaErrorInvalidValue;
+      if (BN == 64) return launch_impl<64, true, true, EPI_F32_LONG>(kp, u, stream, a.pdl);
+      if (BN == 128) return launch_impl<128, true, true, EPI_F32_LONG>(kp, u, stream, a.pdl);
+      return pair ? launch_impl<256, true, true, EPI_F32_LONG, false, true>(kp, u, stream, a.pdl)
+                  : launch_impl<256, true, true, EPI_F32_LONG>(kp, u, stream, a.pdl);
+    }
     if (BN == 64) return launch_impl<64, true, true, EPI_F32>(kp, u, stream, a.pdl);
     if (BN == 128) return launch_impl<128, true, true, EPI_F32>(kp, u, stream, a.pdl);
     return pair ? launch_impl<256, true, true, EPI_F32, false, true>(kp, u, stream, a.pdl)

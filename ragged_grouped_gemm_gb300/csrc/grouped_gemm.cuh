@@ -30,6 +30,8 @@ enum EpiKind : int {
                          // weight -> out0 = da1, out1 = da3, out2 = g h (bf16), row_dot = partial sums of dh h
   EPI_BF16_ADD = 7,      // out0[row, col] = bf16(acc + in0[row, col])  (in0 null: zero); one group, n % 64 == 0, two
                          // terms of A
+  EPI_F32_LONG = 8       // EPI_F32 of ragged K in runs of rows, which are added in the output (GemmArgs::checked: chosen
+                         // by the launch where a group may be long)
 };
 
 // Column slices of GemmArgs::row_dot: two per tile of block_n columns.

@@ -420,6 +420,31 @@ def test_wgrad_of_few_rows_at_an_allocations_end(groups, off, m, k):
     assert (np.abs(np32(dw) - want) <= (max(np.diff(off)) / 16 + 4) * 2.0 ** -23 * mag).all()
 
 
+@pytest.mark.parametrize("groups,rows,off,m,k", [
+    (1, 5000, [0, 5000], 192, 256), (1, 4097, [0, 4097], 1024, 2048), (8, 4000, [0, 5, 5, 3000, 3100, 3500, 3500, 3990, 4000], 1664, 1536),
+    (2, 6000, [3, 1795, 5990], 1664, 1536), (3, 8192, [0, 8192, 8192, 8192], 320, 704), (2, 1793, [0, 1793, 1793], 64, 64)])
+def test_wgrad_of_long_groups(groups, rows, off, m, k):
+    """Runs of 1792 rows at most: 112 steps of the tensor cores, each off by less than 2^-23 of the magnitudes it has
+    added, and up to five sums of runs."""
+    g = torch.Generator().manual_seed(rows + m)
+    dy = torch.randn(rows, m, generator=g).to(BF16).cuda()
+    codes, scales = _keep(torch.randn(rows, k, generator=g).to(BF16).cuda())
+    ws = torch.empty(api.moe_grouped_wgrad_ckpt_workspace_size(groups, rows, m, k), dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    dw = torch.full((groups, m, k), 7.0, device="cuda")
+    offs = torch.tensor(off, dtype=I32, device="cuda")
+    api.moe_grouped_wgrad_ckpt(dy, codes, scales, offs, None, 1, dw, ws)
+    assert _status(ws) == 0
+    x, dyh = O.kept_values(codes.cpu().numpy(), scales.cpu().numpy()), np32(dy).astype(np.float64)
+    want = O.wgrad_kept(dyh, x, off, np.arange(rows), 1)
+    mag = O.wgrad_kept(np.abs(dyh), np.abs(x), off, np.arange(rows), 1)
+    assert (np.abs(np32(dw) - want) <= (112 + 8) * 2.0 ** -23 * mag).all()
+    again = torch.empty_like(dw)
+    for _ in range(3):
+        api.moe_grouped_wgrad_ckpt(dy, codes, scales, offs, None, 1, again, ws)
+        assert torch.equal(again, dw)
+
+
 def test_kept_products_report_offsets_and_indices():
     groups, rows, d, f = 3, 200, 64, 128
     g = torch.Generator().manual_seed(3)
