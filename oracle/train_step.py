@@ -17,6 +17,21 @@ def _sigmoid(v):
     return np.where(v >= 0, 1.0 / (1.0 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1.0 + np.exp(-np.abs(v))))
 
 
+def gate_rows(l, gate):
+    """The gate's distribution of every row and its slopes by their own logits.  Normalised sigmoids keep their ratios
+    however low a row lies: their common factor e^m, m the largest logit where that is below zero, is left out."""
+    m = l.max(axis=-1, keepdims=True)
+    m = np.where(np.isfinite(m), m, 0.0)
+    if gate == "softmax":
+        w = s = np.exp(l - m)
+    else:
+        s = np.exp(np.minimum(l, 0.0) - np.minimum(m, 0.0)) * _sigmoid(np.abs(l))
+        w = s * _sigmoid(-l)
+    tot = s.sum(axis=-1, keepdims=True)
+    tot = np.where(tot > 0, tot, 1.0)
+    return s / tot, w / tot
+
+
 def balance_loss(logits, idx, seq_offsets, gate, coef, z_coef, f=None):
     """``coef E / S' sum_s sum_i f_si mean_t q_ti`` and ``z_coef / T sum_t lse_t^2`` over the sequences
     ``[o_s, o_{s+1})``, their gradient [N, E] and the counts [S, E].  ``f`` (optional, [S, E]) holds the fractions
@@ -43,13 +58,7 @@ def balance_loss(logits, idx, seq_offsets, gate, coef, z_coef, f=None):
         tot = np.where(live, ex.sum(axis=1), 1.0)[:, None]
         p = ex / tot
         lse = np.where(live, m[:, 0] + np.log(tot[:, 0]), 0.0)
-        if gate == "softmax":
-            q = dq = p
-        else:
-            sg = _sigmoid(l)
-            ssum = sg.sum(axis=1, keepdims=True)
-            ssum = np.where(ssum > 0, ssum, 1.0)
-            q, dq = sg / ssum, sg * (1.0 - sg) / ssum
+        q, dq = gate_rows(l, gate)
         inner = q @ fs
         balance += coef * e / full * inner.mean()
         square += z_coef / used * (lse ** 2).sum()

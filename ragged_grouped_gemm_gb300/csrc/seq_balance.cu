@@ -387,6 +387,9 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
       m = warp_max(m);
       if (m == -INFINITY) m = 0.0f;   // every expert masked: no probability, no z
       if (__any_sync(0xffffffffu, nan)) m = NAN;
+      // Every logit below zero: the sigmoids without their common factor e^m, which may be below the smallest number,
+      // e^(l - m) / (1 + e^l).  Quotients and slopes over their sum are the same.
+      const bool low = m < 0.0f;
       z = sum = fs = 0.0f;
 #pragma unroll
       for (int j = 0; j < NPER; ++j) {
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
         float d = q[j];
         if (GATE != 0) {
           const float v = expf(-fabsf(l[j]));   // sigmoid(|l|) = 1 / (1 + v), the other side v / (1 + v)
-          const float big = 1.0f / (1.0f + v), small = v * big;
+          const float big = 1.0f / (1.0f + v), small = (low ? q[j] : v) * big;
           d = l[j] > 0.0f ? big : small;
           if (l[j] != l[j]) d = l[j];
           w[j] = big * small;

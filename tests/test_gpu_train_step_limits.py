@@ -1,0 +1,78 @@
+"""GPU limits of the training step's operators: logits far from zero, workspaces of the least size, long groups, and
+how exact the short chains of sums are, against 64-bit numpy, with bounds that count the roundings."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from parity_util import np32
+from ragged_grouped_gemm_gb300 import api
+from ragged_grouped_gemm_gb300.inputs import MoEConfig
+
+pytestmark = pytest.mark.gpu
+BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+U = 2.0 ** -24
+
+
+def _balance(lg, idx, off, gate, coef=0.01, z=0.001, up=None):
+    n, e = lg.shape
+    desc = api.make_desc(MoEConfig("case", n, 64, 64, e, idx.shape[1], gate=gate))
+    ws = torch.empty(api.moe_workspace_size(desc)[0], dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    counts = torch.full((len(off) - 1, e), -7, dtype=I32, device="cuda")
+    loss, dl = torch.full((2,), 9.0, device="cuda"), torch.full((n, e), 5.0, device="cuda")
+    api.moe_balance_loss(desc, lg, idx, torch.tensor(off, dtype=I32, device="cuda"), counts, loss, dl, ws, coef, z,
+                         None if up is None else torch.tensor([up], device="cuda"))
+    return counts, loss, dl
+
+
+def _check_rows(lg, idx, gate, got, coef, z, up=1.0):
+    """One sequence of all rows.  An exponential of l - m carries the rounding of the difference (|l - m| U) and two ulps
+    of its own, a sigmoid two such and its quotient, a sum E / 32 + 5 roundings: a probability is off by
+    r = 2 (E / 32 + 16 + 2 max|l - m|) U of itself, inner by as much, f - inner by r of (f + inner), and the products add
+    eight roundings.  lse is off by r + |lse| U.  Every factor is a normal number, so this holds for each number by
+    itself; what is below 2^-126 in the end is off by a few 2^-149."""
+    lg64 = lg.cpu().double().numpy()
+    n, e = lg64.shape
+    rc, rl, rg = O.balance_loss(lg64, idx.cpu().numpy(), [0, n], gate, coef, z)
+    np.testing.assert_array_equal(got[0].cpu().numpy(), rc)
+    f = rc[0] / n
+    low = np.where(np.isneginf(lg64), np.inf, lg64)
+    m = lg64.max(axis=1, keepdims=True)
+    live = np.isfinite(m[:, 0])
+    m0 = np.where(np.isfinite(m), m, 0.0)
+    span = np.where(live, (m0 - np.where(np.isfinite(low), low, m0)).max(axis=1), 0.0)
+    r = 2 * (e / 32 + 16 + 2 * np.minimum(span, 200.0))[:, None] * U        # beyond 200 a term is zero on both sides
+    p = np.exp(lg64 - m0)
+    lse = np.where(live, m0[:, 0] + np.log(np.where(live, p.sum(1), 1.0)), 0.0)[:, None]
+    p = p / np.where(live, p.sum(1), 1.0)[:, None]
+    q, w = O.train_step.gate_rows(lg64, gate)
+    inner = (q @ f)[:, None]
+    assert abs(got[1][0].item() - rl[0]) <= (r.max() + U) * rl[0]
+    big = np.abs(lse).max()
+    assert abs(got[1][1].item() - rl[1]) <= 2 * z * big * (r.max() + big * U) + U * rl[1]
+    tol = coef * e / n * w * (f + inner) * (2 * r + 8 * U)
+    tol = tol + 2 * z / n * p * (np.abs(lse) * (2 * r + 8 * U) + r + np.abs(lse) * U)
+    assert (np.abs(np32(got[2]).astype(np.float64) - up * rg) <= up * tol + 1e-43).all()
+
+
+def _rows(n, e, k, level, seed):
+    g = torch.Generator().manual_seed(seed)
+    lg = torch.randn(n, e, generator=g) * 1.3 + torch.tensor(level)[torch.arange(n) % len(level)][:, None]
+    return lg.cuda(), lg.topk(k, dim=1).indices.to(I32).cuda()
+
+
+SIZES = [(60, 48, 4), (200, 8, 2), (700, 60, 6), (900, 256, 8), (300, 1021, 3)]   # the first two: one cluster
+
+
+@pytest.mark.parametrize("n,e,k", SIZES)
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_balance_of_logits_far_below_zero(gate, n, e, k):
+    """Where every sigmoid of a row is below the smallest number, their ratios still are the gate's distribution."""
+    lg, idx = _rows(n, e, k, [-29.0, -60.0, -85.0, -90.0, -95.0, -100.0, -103.0, -106.0, -150.0, -1000.0, 0.0, -20.0], n)
+    lg[5, 1:], lg[6, :], lg[7, 1:e // 2] = -float("inf"), -float("inf"), -float("inf")
+    for coef, z in ((0.01, 0.0), (0.01, 0.001)):
+        _check_rows(lg, idx, gate, _balance(lg, idx, [0, n], gate, coef, z), coef, z)
+    lg[8] = torch.finfo(F32).min                                   # log sum beyond 1e19: no z-loss here
+    lg[9, 1:] = torch.finfo(F32).min
+    _check_rows(lg, idx, gate, _balance(lg, idx, [0, n], gate, 0.01, 0.0), 0.01, 0.0)
