@@ -649,7 +649,8 @@ MOE_API moe_status_t moe_dropout_backward(const moe_desc_t* d, const void* dout,
  * and z_coef = 0 give moe_aux_loss.  A logit of -inf (a masked expert) has
  * probability 0; a row of nothing else has no probabilities, no z-loss and a zero
  * gradient, its copies still count.  A NaN or +inf logit makes its row and the
- * losses NaN; a row's log sum beyond 1e19 makes the z-loss infinite.  logits [N,E], topk_idx [N,K] from moe_route.  An entry of
+ * losses NaN (loss[1] stays 0 where z_coef is 0); a row's log sum beyond 1e19
+ * makes the z-loss infinite.  logits [N,E], topk_idx [N,K] from moe_route.  An entry of
  * seq_offsets outside [0, N] is cut to that range and sets MOE_DEV_BAD_OFFSETS;
  * entries that decrease set it too, and every output is zero then.  An index
  * outside [0, E) is not counted (MOE_DEV_BAD_INDEX).  Sums in a fixed order:

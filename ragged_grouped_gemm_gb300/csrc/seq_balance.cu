@@ -378,11 +378,11 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
       inner = fs * invq;
     } else {
       float m = l[0];
-      bool nan = false;   // fmaxf passes a NaN over
+      bool nan = false;   // a NaN, which fmaxf passes over, or +inf
 #pragma unroll
       for (int j = 0; j < NPER; ++j) {
         m = fmaxf(m, l[j]);
-        nan |= l[j] != l[j];
+        nan |= !(l[j] < INFINITY);
       }
       m = warp_max(m);
       if (m == -INFINITY) m = 0.0f;   // every expert masked: no probability, no z
@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
           const float v = expf(-fabsf(l[j]));   // sigmoid(|l|) = 1 / (1 + v), the other side v / (1 + v)
           const float big = 1.0f / (1.0f + v), small = (low ? q[j] : v) * big;
           d = l[j] > 0.0f ? big : small;
-          if (l[j] != l[j]) d = l[j];
           w[j] = big * small;
           if (l[j] == -INFINITY) d = w[j] = 0.0f;
           sum += d;
@@ -410,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
       z = warp_add(z);
       sum = warp_add(sum);
       fs = warp_add(fs);
+      if (m != m) fs = m;   // sigmoids are finite: the row is to be NaN as the softmax makes it
       invz = z != 0.0f ? 1.0f / z : 0.0f;
       lse = z != 0.0f ? m + logf(z) : 0.0f;
       invq = GATE == 0 ? invz : sum != 0.0f ? 1.0f / sum : 0.0f;

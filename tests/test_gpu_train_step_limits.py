@@ -76,3 +76,20 @@ def test_balance_of_logits_far_below_zero(gate, n, e, k):
     lg[8] = torch.finfo(F32).min                                   # log sum beyond 1e19: no z-loss here
     lg[9, 1:] = torch.finfo(F32).min
     _check_rows(lg, idx, gate, _balance(lg, idx, [0, n], gate, 0.01, 0.0), 0.01, 0.0)
+
+
+@pytest.mark.parametrize("n,e,k", SIZES)
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("z", [0.0, 0.001])
+def test_balance_of_a_logit_that_is_no_number(gate, n, e, k, value, z):
+    """Its row and the losses are NaN (the z-loss where there is one), every other row is what it was."""
+    lg, idx = _rows(n, e, k, [0.0, 2.0], n)
+    lg[3, :e // 2] = -float("inf")
+    clean = _balance(lg, idx, [0, n - 2], gate, z=z)
+    lg[3, e - 1] = lg[n - 1, 0] = value                                        # the second in no sequence
+    got = _balance(lg, idx, [0, n - 2], gate, z=z)
+    assert torch.isnan(got[2][3]).all() and torch.isnan(got[1][0])
+    assert torch.isnan(got[1][1]) if z else got[1][1] == 0
+    rest = [i for i in range(n) if i != 3]
+    assert torch.equal(got[2][rest], clean[2][rest]) and torch.equal(got[0], clean[0])
