@@ -368,10 +368,11 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(co
     fs = warp_add(fs);
     if (GATE != 0) sum = warp_add(sum);
     float invz, invq;
-    // Exponentials of the logits as they are, without the largest taken off: right while their sum is neither near the
-    // end of fp32's range (every logit is below 78 then, 1 + v is finite) nor so small that terms that matter were
-    // lost (the largest is above -28 then, what e^l loses below -87 is 1e-25 of it).  Else row by row the long way.
-    if (z < 1e34f && z > 1e-9f) {
+    // Exponentials of the logits as they are, without the largest taken off: right while their sum is not so small that
+    // terms that matter were lost (the largest is above -28 then, what e^l loses below -87 is 1e-25 of it), nor so
+    // large that the gradient's factors, of which 1 / z is one, leave the normal numbers (with coef E / T of 1e-12
+    // there are 1e10 left; up to 1e34 rows near 74 lost 1e-4 of the gradient to 5 %).  Else row by row the long way.
+    if (z < 1e15f && z > 1e-9f) {
       invz = rcp_fast(z);
       lse = logf(z);
       invq = GATE == 0 ? invz : rcp_fast(sum);

@@ -93,3 +93,13 @@ def test_balance_of_a_logit_that_is_no_number(gate, n, e, k, value, z):
     assert torch.isnan(got[1][1]) if z else got[1][1] == 0
     rest = [i for i in range(n) if i != 3]
     assert torch.equal(got[2][rest], clean[2][rest]) and torch.equal(got[0], clean[0])
+
+
+@pytest.mark.parametrize("n,e,k", SIZES + [(20000, 8, 2)])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("up", [1.0, 1024.0])
+def test_balance_of_logits_far_above_zero(gate, n, e, k, up):
+    """A small factor of a row with a large sum of exponentials keeps its bits."""
+    lg, idx = _rows(n, e, k, [20.0, 30.0, 34.0, 36.0, 45.0, 66.0, 68.0, 72.0, 74.0, 76.0, 85.0, 90.0, 0.0, 1000.0], n)
+    for coef, z in ((1e-5, 0.0), (1e-5, 1e-5), (0.0, 1e-7), (1e-8, 0.0)):
+        _check_rows(lg, idx, gate, _balance(lg, idx, [0, n], gate, coef, z, up), coef, z, up)
