@@ -55,6 +55,7 @@
 #include "grouped_gemm.cuh"
 #include "ckpt.cuh"
 #include "pdl.cuh"
+#include "row_runs.h"
 #include "sm100_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -76,7 +77,6 @@ constexpr int kThreadsW8 = 576;      // + 8 converter warps (FP8 weights)
 constexpr int kThreadsC = 384;       // CHUNKED: three warpgroups, the epilogue in two of them
 constexpr int kConvWarps = 8;
 constexpr int kChunk = 13;           // k-blocks of 64 elements a chunk (CHUNKED)
-constexpr int kRowChunk = 1792;      // rows of a run (ROWCH)
 // CHUNKED on 256-column tiles: registers a thread at launch, of the first warpgroup and of the epilogue's
 constexpr int kRegsLaunch = 168, kRegsFirst = 40, kRegsEpi = 232;
 static_assert(128 * kRegsFirst + 256 * kRegsEpi <= kThreadsC * kRegsLaunch, "more registers than the block has");
@@ -458,9 +458,6 @@ struct KeptBlock {
 // of a sum, 16: 1e-6).  Two longer ones at a tile's start, while the epilogue of the tile before keeps the warps, gave
 // 704 for 717 us in CTA pairs (8192 rows, 14336 x 4096) and took 340 for 332 in single ones (2048 x 7168).
 __device__ __forceinline__ int num_chunks(int n) { return (n + kChunk - 1) / kChunk; }
-
-// ROWCH: the runs of a group of `rows` rows (one for none).
-__device__ __forceinline__ int row_runs(int rows) { return max(1, (rows + kRowChunk - 1) / kRowChunk); }
 
 // GATHER (ragged M, bf16, one contraction source): A rows are gathered from
 // the token matrix through p.a_gather by TMA tile::gather4, four rows per
@@ -992,8 +989,8 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
           const bool runs = ROWCH && nch > 1;   // divisions that one run does not pay
-          const int kb0 = runs ? ch * t.num_kb / nch : ch * kChunk;
-          const int kb1 = CHUNKED ? min(t.num_kb, kb0 + kChunk) : runs ? (ch + 1) * t.num_kb / nch : t.num_kb;
+          const int kb0 = runs ? run_begin(ch, nch, t.num_kb) : ch * kChunk;
+          const int kb1 = CHUNKED ? min(t.num_kb, kb0 + kChunk) : runs ? run_begin(ch + 1, nch, t.num_kb) : t.num_kb;
           for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const int s = it % S;
             const uint32_t ph = (it / S) & 1u;

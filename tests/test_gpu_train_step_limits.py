@@ -103,3 +103,24 @@ def test_balance_of_logits_far_above_zero(gate, n, e, k, up):
     lg, idx = _rows(n, e, k, [20.0, 30.0, 34.0, 36.0, 45.0, 66.0, 68.0, 72.0, 74.0, 76.0, 85.0, 90.0, 0.0, 1000.0], n)
     for coef, z in ((1e-5, 0.0), (1e-5, 1e-5), (0.0, 1e-7), (1e-8, 0.0)):
         _check_rows(lg, idx, gate, _balance(lg, idx, [0, n], gate, coef, z, up), coef, z, up)
+
+
+def test_weight_gradient_of_one_group_of_many_million_rows():
+    """The bounds of a group's runs pass 32 bits on the way from 15.7 million rows on.  Small whole numbers: every partial
+    sum is below 2^24, so the gradient is exact."""
+    rows, m, k = (1 << 24) + 77, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    draw = lambda lo, hi: torch.randint(lo, hi, (rows, 64), generator=g, device="cuda", dtype=torch.int8).to(BF16)  # noqa: E731
+    dy, x = draw(-1, 2), draw(-2, 3)
+    codes = torch.empty(rows, k, dtype=U8, device="cuda")
+    scales = torch.empty(k // 32, api.mx_scale_ld(rows), dtype=U8, device="cuda")
+    api.moe_quantize_mxfp8(x, codes, scales)
+    want = torch.zeros(m, k, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 1 << 20):
+        want += dy[i:i + (1 << 20)].double().T @ x[i:i + (1 << 20)].double()
+    ws = torch.empty(api.moe_grouped_wgrad_ckpt_workspace_size(1, rows, m, k), dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    dw = torch.full((1, m, k), 7.0, device="cuda")
+    api.moe_grouped_wgrad_ckpt(dy, codes, scales, torch.tensor([0, rows], dtype=I32, device="cuda"), None, 1, dw, ws)
+    assert api.moe_get_device_status(ws)[0] == 0
+    assert torch.equal(dw[0].double(), want)

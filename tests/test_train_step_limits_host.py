@@ -1,0 +1,34 @@
+"""Limits of the training step's operators that need no GPU: index arithmetic at large sizes, workspace sizes."""
+import subprocess
+
+from ragged_grouped_gemm_gb300 import build
+
+RUNS = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "row_runs.h"
+// Every k-block belongs to one run, in order, and no run is empty or longer than a run and a k-block.
+int main() {
+  const int rows[] = {0, 1, 64, 1791, 1792, 1793, 3584, 3585, 8192, 1000003, 15700000, 16777216, 22300000, 33554433,
+                      1 << 27, (1 << 30) + 1, 2147483647 - 256};
+  for (int r : rows)
+    for (int kb : {64, 128}) {
+      const int runs = moe::row_runs(r), n = (r + kb - 1) / kb;
+      bool ok = runs >= 1 && (runs == 1) == (r <= moe::kRowChunk) && moe::run_begin(0, runs, n) == 0 &&
+                moe::run_begin(runs, runs, n) == n;
+      for (int i = 0; i < runs; ++i) {
+        const int len = moe::run_begin(i + 1, runs, n) - moe::run_begin(i, runs, n);
+        ok = ok && (len > 0 || n == 0) && len <= moe::kRowChunk / kb + 1;
+      }
+      std::printf("%d %d %d\n", r, kb, ok);
+    }
+}
+"""
+
+
+def test_runs_of_rows_cover_a_group(tmp_path):
+    src, exe = tmp_path / "runs.cpp", tmp_path / "runs"
+    src.write_text(RUNS)
+    subprocess.run(["g++", "-O1", "-I", build.CSRC, str(src), "-o", str(exe)], check=True)
+    lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split("\n")[:-1]
+    assert len(lines) == 34 and all(line.endswith(" 1") for line in lines), lines
