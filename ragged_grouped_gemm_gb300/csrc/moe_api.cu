@@ -62,7 +62,6 @@ struct WsLayout {
   size_t t_d0 = 0, t_d0s = 0, t_d1 = 0, t_d1s = 0, t_f0 = 0, t_f0s = 0, t_f1 = 0, t_f1s = 0;
   int64_t rp = 0;   // leading dimension of the transposed code matrices
   size_t norm = 0;  // partial sums of the layer norm's weight gradients (over others' scratch)
-  size_t rterms = 0, rend = 0;  // the dense router gradient's terms and partial products (over others' scratch)
 };
 
 // The dense router gradient's weight product contracts over the tokens, dlogits being three bf16
@@ -78,18 +77,12 @@ struct RouterPlan {
 };
 constexpr int kRouterSlices = 48;
 constexpr int64_t kRouterRun = 896;
-size_t router_terms_bytes(const moe_desc_t& d) {
-  return align_up(static_cast<size_t>(d.n_tok) * 3 * moe::router_term_cols(d.n_exp) * 2);
-}
-// Bytes of scratch: the terms, {0, N} and the runs' starts, the partial products.
-size_t router_bytes(const moe_desc_t& d, int m, int slices) {
-  return router_terms_bytes(d) + kAlign + align_up(static_cast<size_t>(slices) * m * d.d_model * 4);
-}
 int router_rows(const moe_desc_t& d) {
   const int e8 = moe::router_term_cols(d.n_exp);
   return 3 * e8 <= 128 ? 3 * e8 : e8;
 }
-RouterPlan router_plan(const moe_desc_t& d, size_t scratch) {
+// fit: partial products that the scratch holds at a time.
+RouterPlan router_plan(const moe_desc_t& d, int64_t fit) {
   RouterPlan p;
   p.e8 = moe::router_term_cols(d.n_exp);
   p.m = router_rows(d);
@@ -102,16 +95,17 @@ RouterPlan router_plan(const moe_desc_t& d, size_t scratch) {
   // about 6 us, which the terms' accumulators, filling tensor memory, leave nothing to hide behind;
   // partial products are written and read again at about 5 TB/s.  Waves that hold tiles of the short
   // last run alone cost that run.  An accumulator's chain cuts about 1.5e-8 of a sum an addition of 16
-  // tokens, so runs are kept at kRouterRun tokens where the scratch holds that many (4096 x 7168, 256
+  // tokens, so runs are kept at kRouterRun tokens, in several launches where the scratch holds fewer (4096 x 7168, 256
   // experts: runs of 512 to 1024 tokens 84, 88, 86, 81 and 83 us, off by 5.0, 6.2, 7.5, 8.7 and 10.3e-7 of
   // the gradient's norm; one of 2048 74 us and 19e-7).
   auto cost = [&](int64_t rows) { return static_cast<double>(rows) / 64 * 4 * 0.085 * (p.packed ? 1 : 3) + (p.packed ? 0 : 6); };
   double best = 0;
   p.slices = 0;
+  const int64_t most = std::max(fit, std::min<int64_t>((N + kRouterRun - 1) / kRouterRun, kRouterSlices));
   const int64_t first = N > kRouterRun * kRouterSlices ? (N / kRouterSlices + 127) / 128 * 128 : 128;
   for (int64_t per = first; per <= std::max<int64_t>(kRouterRun, (N + 127) / 128 * 128); per += 128) {
     const int64_t slices = (N + per - 1) / per;
-    if (slices > kRouterSlices || (slices > 1 && router_bytes(d, p.m, static_cast<int>(slices)) > scratch)) continue;
+    if (slices > std::min<int64_t>(kRouterSlices, most)) continue;
     if (p.slices && per > kRouterRun) break;
     const int64_t full = units * (N / per), waves = (full + at_once - 1) / at_once;
     const double t = waves * cost(per) + ((units * slices + at_once - 1) / at_once - waves) * cost(N % per) +
@@ -207,13 +201,6 @@ WsLayout layout(const moe_desc_t& d) {
   const size_t norm = align_up(moe::layernorm_bwd_floats(d.n_tok, d.d_model) * 4);
   L.norm = norm <= L.gmaps - L.dl ? L.dl : o;
   if (L.norm == o) o += norm;
-  // the dense router gradient too, over the same scratch where its runs of tokens fit
-  const size_t router = router_bytes(
-      d, router_rows(d), static_cast<int>(std::clamp<int64_t>((N + kRouterRun - 1) / kRouterRun, 1, kRouterSlices)));
-  const bool over = router <= L.gmaps - L.dl;
-  L.rterms = over ? L.dl : o;
-  if (!over) o += router;
-  L.rend = over ? L.gmaps : o;
   L.total = o;
   return L;
 }
@@ -1443,18 +1430,23 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
       MOE_CUDA(cudaMemcpyAsync(dw_gate, dw_in, sizeof(float) * E * D, cudaMemcpyDeviceToDevice, st));
     return MOE_OK;
   }
+  // The scratch lies over the layer's, so a workspace is no larger for it: the terms over the router's logit slices (16
+  // bytes an entry), the runs' starts over the dense offsets, partial products over what the layer's backward
+  // holds in passing (from 512 tokens on one fits, below the path without any serves)
   const WsLayout L = layout(*d);
-  if (moe::router_short(N, D, E))
+  const int e8 = moe::router_term_cols(E);
+  const size_t room = L.gmaps - L.dl, one = sizeof(float) * router_rows(*d) * D;
+  float* part = at<float>(ws, L.dl);
+  if (moe::router_short(N, D, E) || (E > moe::kRouterFew && one > room))
     return cuda_status(moe::launch_router_short(dlogits, x, w_gate, dx_in, dx, N, D, E, dw_in, dw_gate, st));
   if (E <= moe::kRouterFew)
-    return cuda_status(moe::launch_router_few(dlogits, x, w_gate, dx_in, dx, at<float>(ws, L.rterms), L.rend - L.rterms,
-                                              N, D, E, dw_in, dw_gate, st));
-  const RouterPlan plan = router_plan(*d, L.rend - L.rterms);
-  const int e8 = plan.e8;
-  char* terms = at<char>(ws, L.rterms);
-  int32_t* dense = reinterpret_cast<int32_t*>(terms + router_terms_bytes(*d));
+    return cuda_status(moe::launch_router_few(dlogits, x, w_gate, dx_in, dx, part, room, N, D, E, dw_in, dw_gate, st));
+  const int fit = static_cast<int>(std::min<size_t>(room / one, kRouterSlices));
+  const RouterPlan plan = router_plan(*d, fit);
+  static_assert((4 + kRouterSlices + 1) * sizeof(int32_t) <= kAlign, "starts of the runs");
+  char* terms = at<char>(ws, L.gpart);
+  int32_t* dense = at<int32_t>(ws, L.dense_off);
   int32_t* starts = dense + 4;
-  float* part = reinterpret_cast<float*>(terms + router_terms_bytes(*d) + kAlign);
   int32_t* status = at<int32_t>(ws, L.status);
   MOE_CUDA(moe::launch_router_terms(dlogits, N, E, terms, dense, starts, plan.slices, plan.per, st));
   GemmArgs w;
@@ -1463,8 +1455,6 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
   w.cta_pair = plan.pair ? 1 : 0;
   w.pdl = true;
   w.aligned_groups = true;
-  w.offsets = starts;
-  w.num_groups = plan.slices;
   w.max_rows = N;
   w.status = status;
   w.a[0] = act(terms, N, 3 * e8);
@@ -1478,8 +1468,12 @@ moe_status_t moe_router_backward(const moe_desc_t* d, const float* dlogits, cons
   w.out0 = part;
   w.ld_out = D;
   w.group_stride_out = static_cast<int64_t>(plan.m) * D;
-  MOE_CUDA(gemm(moe::TIMING_WGRAD, w, st));
-  MOE_CUDA(moe::launch_router_dw(part, plan.slices, plan.packed ? 3 : 1, E, D, dw_in, dw_gate, st));
+  for (int s = 0; s < plan.slices; s += fit) {
+    w.offsets = starts + s;
+    w.num_groups = std::min(fit, plan.slices - s);
+    MOE_CUDA(gemm(moe::TIMING_WGRAD, w, st));
+    MOE_CUDA(moe::launch_router_dw(part, w.num_groups, plan.packed ? 3 : 1, E, D, s > 0 ? dw_gate : dw_in, dw_gate, st));
+  }
   // dx: the first two terms against W_g
   GemmArgs g;
   g.epi = moe::EPI_BF16_ADD;

@@ -1005,7 +1005,7 @@ cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate
 
 cudaError_t launch_router_short(const float* dl, const void* x, const void* w_gate, const void* dx_in, void* dx, int n_tok,
                                 int d, int n_exp, const float* dw_in, float* dw, cudaStream_t st) {
-  if (n_tok < 1 || d % 64 || !router_short(n_tok, d, n_exp)) return cudaErrorInvalidValue;
+  if (n_tok < 1 || n_tok > kRouterShort || d % 64) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

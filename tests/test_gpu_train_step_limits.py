@@ -124,3 +124,33 @@ def test_weight_gradient_of_one_group_of_many_million_rows():
     api.moe_grouped_wgrad_ckpt(dy, codes, scales, torch.tensor([0, rows], dtype=I32, device="cuda"), None, 1, dw, ws)
     assert api.moe_get_device_status(ws)[0] == 0
     assert torch.equal(dw[0].double(), want)
+
+
+@pytest.mark.parametrize("n,d,e", [(8, 12544, 1001), (100, 65536, 17), (10000, 1024, 1024), (2000, 192, 1020),
+                                   (45000, 128, 520), (1, 1152, 8), (600, 64, 1000)])
+def test_router_backward_in_the_layers_own_scratch(n, d, e):
+    """Workspaces without room for one partial product, or for those of all runs at a time.  Bounds: three bf16 terms hold
+    the 24 bits of an entry, two lose 2^-17 of it; the tensor cores add 16 products at a time to an fp32 sum, each step
+    off by less than 2^-23 of the magnitudes it has added, three chains; the terms', runs' and addend's sums 40 more."""
+    g = torch.Generator().manual_seed(n + d + e)
+    desc = api.make_desc(MoEConfig("case", n, d, 64, e, 1))
+    size = api.moe_workspace_size(desc)[1]
+    ws = torch.full((size + (1 << 20),), 0xab, dtype=U8, device="cuda")
+    api.moe_workspace_init(ws[:size])
+    dl = (torch.randn(n, e, generator=g) * torch.exp(2 * torch.randn(n, 1, generator=g)) * 1e-2).cuda()
+    x, wg = torch.randn(n, d, generator=g).to(BF16).cuda(), (torch.randn(e, d, generator=g) * 0.1).to(BF16).cuda()
+    dxi, dwi = torch.randn(n, d, generator=g).to(BF16).cuda(), torch.randn(e, d, generator=g).cuda()
+    dx, dw = torch.full_like(dxi, 3.0), torch.full_like(dwi, 3.0)
+    api.moe_router_backward(desc, dl, x, wg, dxi, dx, dwi, dw, ws[:size])
+    dl64, x64, w64, dwi64 = dl.double(), x.double(), wg.double(), dwi.double()
+    rx, mx = dxi.double() + dl64 @ w64, dl64.abs() @ w64.abs() + dxi.double().abs()
+    assert ((dx.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + (2.0 ** -17 + (e / 8 + 8) * 2.0 ** -23) * mx
+            * (1 + 2.0 ** -8)).all()
+    rw, mw = dwi64 + dl64.T @ x64, dl64.abs().T @ x64.abs() + dwi64.abs()
+    assert ((dw.double() - rw).abs() <= (3 * (n / 16 + 4) + 40) * 2.0 ** -23 * mw).all()
+    dx2, dw2 = dxi.clone(), dwi.clone()
+    api.moe_router_backward(desc, dl, x, wg, dx2, dx2, dw2, dw2, ws[:size])
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    api.moe_router_backward(desc, dl, x, wg, None, dx2, None, dw2, ws[:size])
+    assert ((dw2.double() - (rw - dwi64)).abs() <= (3 * (n / 16 + 4) + 40) * 2.0 ** -23 * mw).all()
+    assert api.moe_get_device_status(ws)[0] == 0 and (ws[size:] == 0xab).all()

@@ -1,7 +1,10 @@
 """Limits of the training step's operators that need no GPU: index arithmetic at large sizes, workspace sizes."""
 import subprocess
 
-from ragged_grouped_gemm_gb300 import build
+import pytest
+
+from ragged_grouped_gemm_gb300 import api, build
+from ragged_grouped_gemm_gb300.inputs import MoEConfig
 
 RUNS = r"""
 #include <cstdio>
@@ -32,3 +35,12 @@ def test_runs_of_rows_cover_a_group(tmp_path):
     subprocess.run(["g++", "-O1", "-I", build.CSRC, str(src), "-o", str(exe)], check=True)
     lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split("\n")[:-1]
     assert len(lines) == 34 and all(line.endswith(" 1") for line in lines), lines
+
+
+@pytest.mark.parametrize("n,d,f,e,k,most", [
+    (16384, 4096, 512, 512, 1, 317070336), (4096, 1024, 64, 1024, 1, 82879488), (1, 4096, 14336, 8, 2, 1661952),
+    (2, 65536, 64, 1001, 1, 264295680)])
+def test_workspaces_hold_the_layer_alone(n, d, f, e, k, most):
+    """The dense router gradient works in what the layer has: sizes as they were before it came."""
+    build.build()
+    assert api.moe_workspace_size(api.make_desc(MoEConfig("case", n, d, f, e, k)))[1] <= most
