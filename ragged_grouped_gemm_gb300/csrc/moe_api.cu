@@ -136,7 +136,10 @@ WsLayout layout(const moe_desc_t& d) {
   L.blk_counts = o; o = align_up(o + nch * E * 4);
   L.blk_base = o; o = align_up(o + nch * E * 4);
   L.aux = o; o = align_up(o + moe::aux_partial_floats(d.n_tok > 0 ? d.n_tok : 1, d.n_exp) * 4);
-  L.gpart = o; o = align_up(o + static_cast<size_t>(kGateSlices) * N * E * 4);   // router logit slices
+  // router logit slices; the balance loss's partial sums
+  L.gpart = o;
+  o = align_up(o + std::max(static_cast<size_t>(kGateSlices) * N * E * 4,
+                            sizeof(float4) * static_cast<size_t>(moe::seq_balance_parts(d.n_tok))));
   // moe_route_permute's grid-barrier words and per-tile expert histograms (E <= 32)
   L.rp_hist = o;
   o = align_up(o + (E <= 32 ? static_cast<size_t>(moe::route_permute_hist_words(d.n_tok, d.n_exp)) * 4 + 128 : 0));
@@ -1407,7 +1410,7 @@ moe_status_t moe_balance_loss(const moe_desc_t* d, const float* logits, const in
   a.counts = counts;
   a.loss = loss;
   a.dlogits = dlogits;
-  a.part = at<float4>(ws, L.gpart);   // at most N; the region holds 16 N E bytes
+  a.part = at<float4>(ws, L.gpart);
   a.head = at<int32_t>(ws, L.aux);
   a.status = at<int32_t>(ws, L.status);
   a.ticket = a.status + kBalanceTicketWord;

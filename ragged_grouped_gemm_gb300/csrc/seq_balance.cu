@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps == 8, "a block of rows takes 8 tokens at least");
 
 // Sequence offset i, cut to [0, n].
 __device__ __forceinline__ int seq_at(const int32_t* __restrict__ off, int i, int n) {
@@ -232,7 +233,7 @@ __device__ __forceinline__ void store_row(float* __restrict__ row, int E, int la
 // Few tokens: one cluster counts too, each copy looking up its sequence and adding to counts in global memory
 // (whole numbers, so the order does not matter), which the cluster's barriers zero before and close behind.
 // s_head: sequences that are not empty, their tokens, decreasing offsets.
-constexpr int kAllBlocks = 8;
+constexpr int kAllBlocks = kSeqBalanceCluster;
 __device__ __forceinline__ void count_all(const RowsParams& p, int (&s_head)[3]) {
   const int N = p.n_tok, tid = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
   if (threadIdx.x < 3) s_head[threadIdx.x] = 0;

@@ -1,6 +1,7 @@
 // The router's balance loss over ragged sequences, with its z-loss, and the
 // dense router gradient (see seq_balance.cu).
 #pragma once
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -18,11 +19,16 @@ struct SeqBalanceArgs {
   int32_t* counts;             // [S, E]
   float* loss;                 // [2]
   float* dlogits;              // [N, E], nullable
-  float4* part;                // one a block of 8 tokens, 16-byte aligned
+  float4* part;                // one a block of the launch (seq_balance_parts), 16-byte aligned
   int32_t* head;               // 4 int32: sequences that are not empty, their tokens, offsets that decrease
   int32_t* ticket;             // zero before the launch, left zero
   int32_t* status;
 };
+// Blocks of a launch at most: 8 tokens a block, or one cluster for few.
+constexpr int kSeqBalanceCluster = 8;
+inline int64_t seq_balance_parts(int n_tok) {
+  return n_tok > 0 ? std::max<int64_t>(kSeqBalanceCluster, (static_cast<int64_t>(n_tok) + 7) / 8) : 0;
+}
 cudaError_t launch_seq_balance(const SeqBalanceArgs& a, cudaStream_t st);
 
 // dlogits [N, E] fp32 as a sum of three bf16 terms [N, 3 * E8], E8 = E rounded up to 8, term i in the columns
