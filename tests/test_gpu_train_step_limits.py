@@ -154,3 +154,71 @@ def test_router_backward_in_the_layers_own_scratch(n, d, e):
     api.moe_router_backward(desc, dl, x, wg, None, dx2, None, dw2, ws[:size])
     assert ((dw2.double() - (rw - dwi64)).abs() <= (3 * (n / 16 + 4) + 40) * 2.0 ** -23 * mw).all()
     assert api.moe_get_device_status(ws)[0] == 0 and (ws[size:] == 0xab).all()
+
+
+def _rel(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+def _quantised(v):
+    codes = torch.empty(v.shape, dtype=U8, device="cuda")
+    scales = torch.zeros(v.shape[1] // 32, api.mx_scale_ld(v.shape[0]), dtype=U8, device="cuda")
+    api.moe_quantize_mxfp8(v, codes, scales)
+    value = torch.empty_like(v)
+    api.moe_dequantize_mxfp8(codes, scales, value)
+    return codes, scales, value.double()
+
+
+# What an addition to the tensor cores' fp32 accumulators does not hold is cut, about 1.5e-8 of the sum a step of 16
+# elements: 3.7e-6 of the norm of a sum over 8192, in proportion to its length, 8e-6 where terms are few and alike.  Chains
+# are kept short where an fp32 output hangs on them; these bounds lie between what the short chains leave (4.8e-7, 7e-7,
+# 9e-7) and what one chain does.
+@pytest.mark.parametrize("groups,off,m,k", [
+    (1, [0, 8192], 192, 256), (1, [0, 8192], 1024, 2048), (2, [0, 8192, 16384], 1664, 1536),
+    (16, [0, 100] + list(range(7200, 8192, 71)) + [8192], 1664, 1536)])
+def test_weight_gradient_of_long_groups_is_summed_in_runs(groups, off, m, k):
+    rows = off[-1]
+    g = torch.Generator(device="cuda").manual_seed(rows + m)
+    dy = torch.randn(rows, m, generator=g, device="cuda").to(BF16)
+    codes, scales, x = _quantised(torch.randn(rows, k, generator=g, device="cuda").to(BF16))
+    assert len(off) == groups + 1
+    ws = torch.empty(api.moe_grouped_wgrad_ckpt_workspace_size(groups, rows, m, k), dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    dw = torch.full((groups, m, k), 7.0, device="cuda")
+    api.moe_grouped_wgrad_ckpt(dy, codes, scales, torch.tensor(off, dtype=I32, device="cuda"), None, 1, dw, ws)
+    for e in range(groups):
+        r = slice(off[e], off[e + 1])
+        assert _rel(dw[e], dy[r].double().T @ x[r]) <= 1e-6
+
+
+@pytest.mark.parametrize("rows,d,f", [(200, 7168, 512), (1500, 7168, 1024), (4000, 7168, 2048)])
+def test_gradient_of_row_weights_is_summed_in_chunks(rows, d, f):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    dy = torch.randn(rows, d, generator=g, device="cuda").to(BF16)
+    w2 = (torch.randn(1, d, f, generator=g, device="cuda") * 0.02).to(BF16)
+    c1, s1, a1 = _quantised(torch.randn(rows, f, generator=g, device="cuda").to(BF16))
+    c3, s3, a3 = _quantised(torch.randn(rows, f, generator=g, device="cuda").to(BF16))
+    ws = torch.empty(api.moe_swiglu_backward_ckpt_workspace_size(1, rows, d, f), dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    outs = [torch.empty(rows, f, dtype=BF16, device="cuda") for _ in range(3)]
+    dg = torch.empty(rows, device="cuda")
+    api.moe_swiglu_backward_ckpt(dy, torch.tensor([0, rows], dtype=I32, device="cuda"), w2, None, c1, s1, c3, s3, *outs,
+                                 dg, ws)
+    want = (dy.double() @ w2[0].double() * a1 * torch.sigmoid(a1) * a3).sum(1)
+    assert _rel(dg, want) <= 1.5e-6
+
+
+@pytest.mark.parametrize("n,d,e", [(4096, 1024, 256), (4096, 1088, 64), (4096, 704, 33), (4096, 1024, 8),
+                                   (8000, 512, 16), (512, 1024, 64), (10000, 1024, 1024),
+                                   (4096, 7168, 256), (16384, 7168, 8), (30000, 7168, 16)])
+def test_router_weight_gradient_is_summed_in_runs(n, d, e):
+    g = torch.Generator(device="cuda").manual_seed(n + e)
+    desc = api.make_desc(MoEConfig("case", n, d, 64, e, 1))
+    ws = torch.empty(api.moe_workspace_size(desc)[1], dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    dl = torch.randn(n, e, generator=g, device="cuda") * 1e-3
+    x = torch.randn(n, d, generator=g, device="cuda").to(BF16)
+    wg = torch.randn(e, d, generator=g, device="cuda").to(BF16)
+    dx, dw = torch.empty_like(x), torch.empty(e, d, device="cuda")
+    api.moe_router_backward(desc, dl, x, wg, None, dx, None, dw, ws)
+    assert _rel(dw, dl.double().T @ x.double()) <= 1.4e-6
