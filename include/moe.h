@@ -749,7 +749,8 @@ MOE_API moe_status_t moe_swiglu_backward_ckpt(int64_t n_groups, int64_t rows, in
 
 /* Weight gradients from kept rows: for every group e
  *   dw[e] [m,k] (fp32) = sum over the rows r of e of dy[r]^T x[row_map[r] / row_div],
- * zero for an empty group.  dy [rows,m] bf16; x [x_rows,k] kept codes with scales
+ * zero for an empty group.  A group of more than 1792 rows is summed in runs of
+ * about that many, which are added in fp32.  dy [rows,m] bf16; x [x_rows,k] kept codes with scales
  * [k/32][scale_ld], scale_ld >= x_rows and a multiple of 16.  row_map [rows]
  * (copy_of_row with row_div = top_k reads token rows in expert order; NULL: row r,
  * x_rows = rows); an index outside [0, x_rows) stands for a zero row and sets

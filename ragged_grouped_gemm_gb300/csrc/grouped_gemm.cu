@@ -2423,9 +2423,10 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.a_terms == 3)
       return pair ? launch_impl<256, true, true, EPI_F32, false, true, false, false, 3>(kp, u, stream, a.pdl)
                   : launch_impl<256, true, true, EPI_F32, false, false, false, false, 3>(kp, u, stream, a.pdl);
-    // Where a group may be long, and is not so by its skew alone: the form of runs costs 64 groups of 128 rows on
-    // average 3 % (2048 x 7168: 641 us for 622) and 8 of 1024 nothing (14336 x 4096: 652 for 658)
-    if (a.checked && a.max_rows > kRowChunk && a.max_rows >= kRowChunk / 4 * static_cast<int64_t>(a.num_groups)) {
+    // Where a group may be long, whatever the average: one that holds most of the rows is as exact as in a call of its
+    // own.  64 groups of 128 rows pay 2 % for it (2048 x 7168: 633 us for 621), 8 of 1024 nothing (14336 x 4096:
+    // 711 for 710)
+    if (a.checked && a.max_rows > kRowChunk) {
       if (!kp.c_tma || a.n_size % 4) return cudaErrorInvalidValue;
       if (BN == 64) return launch_impl<64, true, true, EPI_F32_LONG>(kp, u, stream, a.pdl);
       if (BN == 128) return launch_impl<128, true, true, EPI_F32_LONG>(kp, u, stream, a.pdl);

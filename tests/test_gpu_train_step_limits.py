@@ -222,3 +222,24 @@ def test_router_weight_gradient_is_summed_in_runs(n, d, e):
     dx, dw = torch.empty_like(x), torch.empty(e, d, device="cuda")
     api.moe_router_backward(desc, dl, x, wg, None, dx, None, dw, ws)
     assert _rel(dw, dl.double().T @ x.double()) <= 1.4e-6
+
+
+@pytest.mark.parametrize("groups,long,rows,m,k", [(64, 8100, 8192, 1664, 1536), (40, 8192, 8192, 64, 64),
+                                                  (100, 8000, 8192, 320, 128)])
+def test_one_long_group_among_many_short_ones(groups, long, rows, m, k):
+    """The same bound where the rows a group are few on average."""
+    short = rows - long
+    off = [short * e // (groups - 1) for e in range(groups)] + [rows]
+    g = torch.Generator(device="cuda").manual_seed(rows + m)
+    dy = torch.randn(rows, m, generator=g, device="cuda").to(BF16)
+    codes, scales, x = _quantised(torch.randn(rows, k, generator=g, device="cuda").to(BF16))
+    ws = torch.empty(api.moe_grouped_wgrad_ckpt_workspace_size(groups, rows, m, k), dtype=U8, device="cuda")
+    api.moe_workspace_init(ws)
+    dw = torch.full((groups, m, k), 7.0, device="cuda")
+    api.moe_grouped_wgrad_ckpt(dy, codes, scales, torch.tensor(off, dtype=I32, device="cuda"), None, 1, dw, ws)
+    for e in range(groups):
+        r = slice(off[e], off[e + 1])
+        if off[e] == off[e + 1]:
+            assert not dw[e].any()
+        else:
+            assert _rel(dw[e], dy[r].double().T @ x[r]) <= 1e-6
