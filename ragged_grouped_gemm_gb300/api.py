@@ -879,6 +879,7 @@ class MoELayer:
             if cfg.n_shared:
                 self.grads.update(dws1=z(fs, d, dt=F32), dws3=z(fs, d, dt=F32), dws2=z(d, fs, dt=F32))
         self.x = None
+        self.kept = False   # checkpoint: what a forward kept is there
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
         self.experts(x, stream)
@@ -935,6 +936,7 @@ class MoELayer:
             moe_quantize_mxfp8(x, self.ckpt["x"], self.ckpt["x_scale"], stream)
             moe_grouped_ffn_ckpt(self.desc, b["x_perm"], b["offsets"], x, p, self.ckpt, b["y_perm"], b["y_shared"],
                                  self.ws, stream)
+            self.kept = True
         elif self.w8:
             saved = {key: b[key] for key in ("a1", "a3", "h", "a1s", "a3s", "hs") if b.get(key) is not None}
             moe_grouped_ffn_fp8w(self.desc, b["x_perm"], b["offsets"], x, self.w8q, saved, b["y_perm"],
@@ -979,6 +981,7 @@ class MoELayer:
             raise ValueError("a layer built with train=False has no backward")
         if self.cap:
             raise ValueError("the balance over sequences is of the dropless layer")
+        self._needs_forward("balance_loss")
         b, e = self.buf, self.cfg.n_exp
         s = seq_offsets.shape[0] - 1
         z = lambda *shape, dt: torch.empty(shape, dtype=dt, device=b["logits"].device)  # noqa: E731
@@ -997,7 +1000,15 @@ class MoELayer:
         q["pending"] = True
         return q["loss"]
 
+    def _needs_forward(self, what: str):
+        # buffers that no forward has written hold any index
+        if self.x is None and not self.kept:
+            raise ValueError(f"{what} needs the forward that it belongs to")
+
     def backward(self, dy: torch.Tensor, stream=None) -> dict:
+        if not self.train:
+            raise ValueError("a layer built with train=False has no backward")
+        self._needs_forward("backward")
         self._backward(dy, stream)
         q, g = self.balance, self.grads
         if q is not None and q.pop("pending", False):

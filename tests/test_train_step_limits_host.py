@@ -2,6 +2,7 @@
 import subprocess
 
 import pytest
+import torch
 
 from ragged_grouped_gemm_gb300 import api, build
 from ragged_grouped_gemm_gb300.inputs import MoEConfig
@@ -44,3 +45,19 @@ def test_workspaces_hold_the_layer_alone(n, d, f, e, k, most):
     """The dense router gradient works in what the layer has: sizes as they were before it came."""
     build.build()
     assert api.moe_workspace_size(api.make_desc(MoEConfig("case", n, d, f, e, k)))[1] <= most
+
+
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_layer_needs_a_forward(monkeypatch, checkpoint):
+    """Buffers that no forward has written hold any index: nothing is enqueued on them."""
+    layer = object.__new__(api.MoELayer)
+    vars(layer).update(train=True, cap=False, checkpoint=checkpoint, x=None, kept=False, balance=None, grads={})
+    for name in ("moe_backward", "moe_backward_ckpt", "moe_balance_loss"):
+        monkeypatch.setattr(api, name, lambda *a, **k: pytest.fail("enqueued"))
+    with pytest.raises(ValueError, match="needs the forward"):
+        layer.backward(None)
+    with pytest.raises(ValueError, match="needs the forward"):
+        layer.balance_loss(torch.zeros(2, dtype=torch.int32), 0.01)
+    layer.train = False
+    with pytest.raises(ValueError, match="train=False"):
+        layer.backward(None)
