@@ -988,8 +988,6 @@ class MoELayer:
         if self.balance is None:
             self.balance = {"loss": z(2, dt=F32), "dlogits": z(self.cfg.n_tok, e, dt=F32)}
             self._counts = []
-            if self.checkpoint:
-                self.balance["x"] = z(self.cfg.n_tok, self.cfg.d_model, dt=BF16)
         # room for twice as many sequences whenever it grows; captured steps go on writing where they did
         if not self._counts or self._counts[-1].shape[0] < s:
             self._counts.append(z(max(s, 2 * self._counts[-1].shape[0]) if self._counts else s, e, dt=I32))
@@ -1013,8 +1011,8 @@ class MoELayer:
         q, g = self.balance, self.grads
         if q is not None and q.pop("pending", False):
             x = self.x
-            if self.checkpoint:
-                x = q["x"]
+            if self.checkpoint:   # decoded where the forward's permuted rows were
+                x = self.buf["x_perm"][:self.cfg.n_tok]
                 moe_dequantize_mxfp8(self.ckpt["x"], self.ckpt["x_scale"], x, stream)
             moe_router_backward(self.desc, q["dlogits"], x, self.p["w_gate"], g["dx"], g["dx"], g["dw_gate"],
                                 g["dw_gate"], self.ws, stream)

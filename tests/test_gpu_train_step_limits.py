@@ -7,7 +7,7 @@ import torch
 import oracle as O
 from parity_util import np32
 from ragged_grouped_gemm_gb300 import api
-from ragged_grouped_gemm_gb300.inputs import MoEConfig
+from ragged_grouped_gemm_gb300.inputs import CONFIGS, MoEConfig, make_dy, make_layer
 
 pytestmark = pytest.mark.gpu
 BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -243,3 +243,22 @@ def test_one_long_group_among_many_short_ones(groups, long, rows, m, k):
             assert not dw[e].any()
         else:
             assert _rel(dw[e], dy[r].double().T @ x[r]) <= 1e-6
+
+
+def test_balance_of_a_checkpointing_layer_keeps_no_rows_of_its_own():
+    """Beside what it writes (gradient of the logits, losses, counts) it holds nothing for the backward."""
+    cfg = CONFIGS["small_softmax"]
+    p = {key: None if v is None else v.cuda() for key, v in make_layer(cfg, "cpu").items()}
+    layer = api.MoELayer(cfg, p, checkpoint=True)
+    layer.forward(p["x"])
+    off = torch.tensor([0, cfg.n_tok], dtype=I32, device="cuda")
+    layer.balance_loss(off, 0.01)
+    held = sum(v.numel() * v.element_size() for v in layer.balance.values() if isinstance(v, torch.Tensor))
+    assert held <= 4 * (cfg.n_tok * cfg.n_exp + 2 + cfg.n_exp)
+    got = layer.backward(make_dy(cfg, "cpu").cuda())
+    x = torch.empty(cfg.n_tok, cfg.d_model, dtype=BF16, device="cuda")
+    api.moe_dequantize_mxfp8(layer.ckpt["x"], layer.ckpt["x_scale"], x)
+    with_loss = got["dw_gate"].clone()
+    plain = layer.backward(make_dy(cfg, "cpu").cuda())["dw_gate"].double()      # the loss was taken back once
+    want = plain + layer.balance["dlogits"].double().T @ x.double()
+    assert _rel(with_loss, want) <= 1e-6
