@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(threads_of(EPI, QUANT, W8), 1)
             const int nkk = (RAGGED_K && rv < KB) ? (rv + 15) / 16 : KB / 16;
             if (lane == 0) {
               const uint32_t b_base = smem_u32(sB);
-    #pragma unroll
+#pragma unroll
               for (int i = 0; i < TERMS; ++i) {
                 const uint32_t a_base = smem_u32(sA) + i * (RAGGED_K ? C::kABytesC : kABytes);
                 for (int kk = 0; kk < nkk; ++kk) {

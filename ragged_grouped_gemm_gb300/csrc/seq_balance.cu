@@ -153,10 +153,6 @@ struct RowsParams {
   int n_tok, E, S, per;
 };
 
-// A warp a token, its experts over the lanes (NPER registers), tokens of a
-// warp consecutive so that a sequence's f stays in registers from one to the
-// next.  Each block's sums leave as two numbers with their rests, and the last
-// block to finish adds them in a fixed order: equal calls give equal bits.
 // acc += v with what the addition lost kept in acc.y: 48 bits from 32-bit additions (64-bit ones, by every warp and
 // then in a tree of the last block, took 9 of 21 us).  An infinite or NaN sum has no rest.
 __device__ __forceinline__ void add_kept(float2& acc, float v, float rest = 0.0f) {
@@ -274,6 +270,12 @@ __device__ __forceinline__ void count_all(const RowsParams& p, int (&s_head)[3])
   cl.sync();
 }
 
+// A warp a token, its experts over the lanes (NPER registers), tokens of a
+// warp consecutive so that a sequence's f stays in registers from one to the
+// next.  Each block's sums leave as two numbers with their rests, and the last
+// block to finish adds them in a fixed order: equal calls give equal bits.
+// Bound by latency: a row is one chain of loads, an exponential, two sums over the warp, a reciprocal and a logarithm, and
+// with a token a warp at a time an SM issues on a third of its cycles (16384 x 256: 17 us alone, DRAM 13 % busy).
 template <int NPER, int VEC, int GATE, bool ALL = false>
 __global__ void __launch_bounds__(kThreads, kRowBlocks<NPER>) seq_rows_kernel(const RowsParams p) {
   __shared__ float4 s_red[kWarps];

@@ -41,8 +41,8 @@ cudaError_t launch_router_terms(const float* dl, int n_tok, int n_exp, void* ter
 cudaError_t launch_router_dw(const float* part, int n_slices, int terms, int n_exp, int d, const float* dw_in,
                              float* dw, cudaStream_t st);
 
-// The whole dense router gradient of up to kRouterFew experts; `part` holds part_bytes, one partial product
-// of E * D floats at least.
+// The whole dense router gradient of up to kRouterFew experts; `part` holds part_bytes: as many runs of tokens as partial
+// products of E * D floats fit, one (which needs none) at least.
 constexpr int kRouterFew = 16;
 constexpr int kRouterFewRuns = 48;
 cudaError_t launch_router_few(const float* dl, const void* x, const void* w_gate, const void* dx_in, void* dx,
